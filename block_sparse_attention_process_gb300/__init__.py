@@ -10,9 +10,18 @@ raises; nothing falls back to another implementation.
     o, lse = fwd(q, k, v, info)                              # bf16 O, fp32 logsumexp
     dkv = mask_compile("causal", S, S, orientation="dkv")
     dq, dk, dv = bwd(q, k, v, o, lse, do, info, dkv)
+
+After a prompt, token by token over a cache held in 4 bits:
+
+    cache = KV4Cache.empty(B, Hkv, capacity, D)
+    kv4_append(cache, k, v, start, weights=key_weights(q, k, lse, dkv))
+    kv4_append(cache, k1, v1, lens)                          # each new token ...
+    o1, lse1 = kv4_fwd(q1, cache, lens + 1, accumulate=True)
+    lens, index = kv4_evict(cache, lens + 1, keep, recent=recent, seen=seen)
 """
 from __future__ import annotations
 
+import contextlib
 import ctypes as C
 import math
 from dataclasses import dataclass
@@ -24,7 +33,7 @@ from . import _abi
 from ._abi import BsaError, check
 
 __all__ = ["mask_compile", "MaskInfo", "fwd", "fwd_partial", "fwd_merge", "bwd", "bwd_noalloc", "bwd_rowsum",
-           "bwd_dkv", "bwd_dq",
+           "bwd_dkv", "bwd_dq", "key_weights", "KV4Cache", "kv4_append", "kv4_fwd", "kv4_evict",
            "get_device_error", "set_wait_limit_ns", "debug_wait_timeout", "debug_selfcheck", "version", "BsaError",
            "library_path"]
 
@@ -304,6 +313,240 @@ def bwd_dq(q, k, v, o, lse, do, dsum, fwd_info: MaskInfo, *, dq=None, softmax_sc
     b = _bwd_args(q, k, v, o, lse, do, dq, None, None, dsum, softmax_scale, grad_fp32)
     check(_abi.lib().bsa_bwd_dq(C.byref(b.args), fwd_info.handle, _stream(stream)), "bsa_bwd_dq")
     return b.dq
+
+
+_INLINE = contextlib.nullcontext()
+
+
+@contextlib.contextmanager
+def _elsewhere(device, stream):
+    with torch.cuda.device(device):
+        if stream is None:
+            yield
+        else:
+            with torch.cuda.stream(stream):
+                yield
+
+
+def _place(device: torch.device, stream):
+    """(context, stream handle) of a call on tensors of `device`: inside the
+    context the device and the stream are current, so that what the call
+    allocates belongs to the stream it is used on."""
+    if not isinstance(stream, (torch.cuda.Stream, type(None))):
+        stream = torch.cuda.ExternalStream(int(stream), device=device) if int(stream) else torch.cuda.default_stream(device)
+    if stream is None:
+        handle = torch.cuda.current_stream(device).cuda_stream
+        return (_INLINE if device.index == torch.cuda.current_device() else _elsewhere(device, None)), handle
+    if stream.device != device:
+        raise ValueError(f"the stream is on {stream.device}, the tensors are on {device}")
+    return _elsewhere(device, stream), stream.cuda_stream
+
+
+def _check_dev(name: str, t: torch.Tensor, dtype: torch.dtype, device, shape=None) -> None:
+    """A contiguous CUDA tensor of a type, on a device, of a shape."""
+    if t.dtype != dtype or not t.is_cuda or not t.is_contiguous():
+        raise ValueError(f"{name} must be a contiguous CUDA {str(dtype)[6:]} tensor")
+    if device is not None and t.device != device:
+        raise ValueError(f"{name} is on {t.device}, the call's other tensors are on {device}")
+    if shape is not None and t.shape != shape:
+        raise ValueError(f"{name} must be {list(shape)}, not {list(t.shape)}")
+
+
+def _rows(name: str, t: torch.Tensor, device):
+    """Strides (batch, head, token) of a 4-D bf16 CUDA tensor whose last axis is contiguous."""
+    if t.dtype != torch.bfloat16 or not t.is_cuda or t.dim() != 4:
+        raise ValueError(f"{name} must be a 4-D CUDA bfloat16 tensor")
+    if device is not None and t.device != device:
+        raise ValueError(f"{name} is on {t.device}, the call's other tensors are on {device}")
+    s = t.stride()
+    # (the stride of an axis of length 1 says nothing)
+    st = [0 if t.shape[i] == 1 else s[i] for i in range(3)]
+    if s[3] != 1 or st[0] % 8 or st[1] % 8 or st[2] % 8 or t.data_ptr() % 16:
+        raise ValueError(f"{name} needs a contiguous last axis, other strides that are multiples of 8 and 16-byte alignment")
+    return (C.c_int64 * 3)(*st)
+
+
+def _lens(name: str, t: Optional[torch.Tensor], B: int, device) -> Optional[int]:
+    if t is None:
+        return None
+    _check_dev(name, t, torch.int32, device, (B,))
+    return t.data_ptr()
+
+
+def _workspace(need: int, device) -> Optional[torch.Tensor]:
+    return torch.empty(need, dtype=torch.uint8, device=device) if need else None
+
+
+def key_weights(q: torch.Tensor, k: torch.Tensor, lse: torch.Tensor, dkv_info: MaskInfo, *,
+                q_lens: Optional[torch.Tensor] = None, out: Optional[torch.Tensor] = None,
+                softmax_scale: Optional[float] = None, logits_soft_cap: Optional[float] = None, stream=None) -> torch.Tensor:
+    """bsa_key_weights: the attention weight each key of a prompt has received.
+    q [B,Hq,S,D], k [B,Hkv,Skv,D] bf16, lse fp32 [B,Hq,S] from ``fwd``, the mask's "dkv" MaskInfo
+    -> fp32 [B,Hkv,Skv].  ``q_lens`` (int32 [B]): queries past it are padding and not counted."""
+    for n, t in (("q", q), ("k", k)):
+        _check_bf16(n, t)
+        if t.dim() != 4:
+            raise ValueError(f"{n} must be 4-D")
+    B, Hq, S, D = q.shape
+    Hkv, Skv = k.shape[1], k.shape[2]
+    if k.shape != (B, Hkv, Skv, D) or k.device != q.device:
+        raise ValueError("k must be [B, Hkv, Skv, D] on q's device")
+    _check_dev("lse", lse, torch.float32, q.device, (B, Hq, S))
+    a = _abi.KeyWeightsArgs(_ptr(q), _ptr(k), _ptr(lse), _lens("q_lens", q_lens, B, q.device), None, None, 0, B, Hq, Hkv,
+                            D, S, Skv, math.nan if softmax_scale is None else softmax_scale, logits_soft_cap or 0.0)
+    ctx, handle = _place(q.device, stream)
+    with ctx:
+        if out is None:
+            out = torch.empty((B, Hkv, Skv), dtype=torch.float32, device=q.device)
+        _check_dev("out", out, torch.float32, q.device, (B, Hkv, Skv))
+        need = C.c_size_t(0)
+        check(_abi.lib().bsa_key_weights_workspace(C.byref(a), dkv_info.handle, C.byref(need)), "bsa_key_weights")
+        ws = _workspace(need.value, q.device)
+        a.weights, a.workspace, a.workspace_bytes = _ptr(out), _ptr(ws), need.value
+        check(_abi.lib().bsa_key_weights(C.byref(a), dkv_info.handle, handle), "bsa_key_weights")
+    return out
+
+
+class KV4Cache:
+    """A key/value cache held in 4 bits (bsa_kv4_cache): the buffers, which the caller owns.
+
+    k_codes, v_codes: uint8 [B, Hkv, capacity, D/2]; k_scales, v_scales: bf16 [B, Hkv, capacity, D/32];
+    weights: fp32 [B, Hkv, capacity] accumulated attention weights, or None; positions: int32
+    [B, Hkv, capacity] the tokens' positions, or None.  capacity is a multiple of 16."""
+
+    __slots__ = ("k_codes", "k_scales", "v_codes", "v_scales", "weights", "positions", "B", "Hkv", "D", "capacity",
+                 "device", "_c")
+
+    def __init__(self, k_codes: torch.Tensor, k_scales: torch.Tensor, v_codes: torch.Tensor, v_scales: torch.Tensor,
+                 weights: Optional[torch.Tensor] = None, positions: Optional[torch.Tensor] = None):
+        if k_codes.dim() != 4:
+            raise ValueError("k_codes must be [B, Hkv, capacity, D/2]")
+        B, H, n, half = k_codes.shape
+        dev = k_codes.device
+        for name, t, dtype, shape in (("k_codes", k_codes, torch.uint8, (B, H, n, half)),
+                                      ("v_codes", v_codes, torch.uint8, (B, H, n, half)),
+                                      ("k_scales", k_scales, torch.bfloat16, (B, H, n, half // 16)),
+                                      ("v_scales", v_scales, torch.bfloat16, (B, H, n, half // 16)),
+                                      ("weights", weights, torch.float32, (B, H, n)),
+                                      ("positions", positions, torch.int32, (B, H, n))):
+            if t is not None:
+                _check_dev(name, t, dtype, dev, shape)
+        self.k_codes, self.k_scales, self.v_codes, self.v_scales = k_codes, k_scales, v_codes, v_scales
+        self.weights, self.positions = weights, positions
+        self.B, self.Hkv, self.D, self.capacity, self.device = B, H, 2 * half, n, dev
+        self._c = _abi.Kv4Cache(_ptr(k_codes), _ptr(k_scales), _ptr(v_codes), _ptr(v_scales), _ptr(weights),
+                                _ptr(positions), B, H, 2 * half, n)
+
+    @classmethod
+    def empty(cls, B: int, Hkv: int, capacity: int, D: int, device="cuda", weights: bool = True) -> "KV4Cache":
+        """A cache without tokens; without ``weights`` it has neither weights nor positions."""
+        def new(shape, dtype):
+            return torch.zeros(shape, dtype=dtype, device=device)
+        codes, scales = (B, Hkv, capacity, D // 2), (B, Hkv, capacity, D // 32)
+        return cls(new(codes, torch.uint8), new(scales, torch.bfloat16), new(codes, torch.uint8),
+                   new(scales, torch.bfloat16), new((B, Hkv, capacity), torch.float32) if weights else None,
+                   new((B, Hkv, capacity), torch.int32) if weights else None)
+
+
+def kv4_append(cache: KV4Cache, k: torch.Tensor, v: torch.Tensor, start: torch.Tensor, *,
+               n_new: Optional[torch.Tensor] = None, positions: Optional[torch.Tensor] = None,
+               weights: Optional[torch.Tensor] = None, values: bool = False, stream=None):
+    """bsa_kv4_append: tokens of k, v (bf16 [B,Hkv,T,D], any strides with a contiguous last axis) into slots
+    start[b] + t (int32 [B] on the device).  ``n_new``: tokens past it are padding; ``positions``: position of token
+    0 (default start); ``weights`` fp32 [B,Hkv,T]: initial accumulated weights (default 0).  With ``values``
+    returns what the cache now holds, (k, v) bf16 [B,Hkv,T,D], 0 for padding."""
+    dev = cache.device
+    B, H, T, D = k.shape if k.dim() == 4 else (0, 0, 0, 0)
+    if (B, H, D) != (cache.B, cache.Hkv, cache.D) or v.shape != k.shape:
+        raise ValueError("k and v must both be [B, Hkv, T, D] with the cache's B, Hkv and D")
+    ks, vs = _rows("k", k, dev), _rows("v", v, dev)
+    if weights is not None:
+        _check_dev("weights", weights, torch.float32, dev, (B, H, T))
+    if start is None:
+        raise ValueError("start is missing")
+    ctx, handle = _place(dev, stream)
+    with ctx:
+        kv = vv = None
+        if values:
+            kv = torch.empty((B, H, T, D), dtype=torch.bfloat16, device=dev)
+            vv = torch.empty((B, H, T, D), dtype=torch.bfloat16, device=dev)
+        a = _abi.Kv4AppendArgs(cache._c, _ptr(k), _ptr(v), ks, vs, T, _lens("start", start, B, dev),
+                               _lens("n_new", n_new, B, dev), _lens("positions", positions, B, dev), _ptr(weights),
+                               _ptr(kv), _ptr(vv))
+        check(_abi.lib().bsa_kv4_append(C.byref(a), handle), "bsa_kv4_append")
+    return (kv, vv) if values else None
+
+
+def kv4_fwd(q: torch.Tensor, cache: KV4Cache, lens: torch.Tensor, *, q_lens: Optional[torch.Tensor] = None,
+            o: Optional[torch.Tensor] = None, lse: Optional[torch.Tensor] = None, softmax_scale: Optional[float] = None,
+            logits_soft_cap: Optional[float] = None, sinks: Optional[torch.Tensor] = None, accumulate: bool = False,
+            stream=None):
+    """bsa_kv4_fwd: attention of T new tokens over the cache.  q bf16 [B,Hq,T,D] (any strides with a contiguous last
+    axis, e.g. a transposed [B,T,Hq,D]), lens int32 [B] on the device: keys held, the new tokens' own included
+    -> (o bf16 [B,Hq,T,D], lse fp32 [B,Hq,T]).  ``q_lens``: new tokens per sequence (default T).  With
+    ``accumulate`` every key's probabilities are added to cache.weights."""
+    dev = cache.device
+    qs = _rows("q", q, dev)
+    B, Hq, T, D = q.shape
+    if (B, D) != (cache.B, cache.D):
+        raise ValueError("q must be [B, Hq, T, D] with the cache's B and D")
+    if lens is None:
+        raise ValueError("lens is missing")
+    sp, sn, skv = _sink_fields(sinks, cache.Hkv)
+    if sinks is not None and sinks.device != dev:
+        raise ValueError(f"sinks is on {sinks.device}, the call's other tensors are on {dev}")
+    ctx, handle = _place(dev, stream)
+    with ctx:
+        if o is None:
+            o = torch.empty((B, Hq, T, D), dtype=torch.bfloat16, device=dev)
+        if o.shape != q.shape:
+            raise ValueError("o must have q's shape")
+        os = _rows("o", o, dev)
+        if lse is None:
+            lse = torch.empty((B, Hq, T), dtype=torch.float32, device=dev)
+        _check_dev("lse", lse, torch.float32, dev, (B, Hq, T))
+        a = _abi.Kv4FwdArgs(cache._c, _ptr(q), _ptr(o), _ptr(lse), qs, os, Hq, T, _lens("lens", lens, B, dev),
+                            _lens("q_lens", q_lens, B, dev), math.nan if softmax_scale is None else softmax_scale,
+                            logits_soft_cap or 0.0, sp, sn, skv, 1 if accumulate else 0, None, 0)
+        need = C.c_size_t(0)
+        L = _abi.lib()
+        check(L.bsa_kv4_fwd_workspace(C.byref(a), C.byref(need)), "bsa_kv4_fwd")
+        ws = _workspace(need.value, dev)
+        a.workspace, a.workspace_bytes = _ptr(ws), need.value
+        check(L.bsa_kv4_fwd(C.byref(a), handle), "bsa_kv4_fwd")
+    return o, lse
+
+
+def kv4_evict(cache: KV4Cache, lens: torch.Tensor, keep: int, *, recent: int = 0, seen: Optional[torch.Tensor] = None,
+              out: Optional[KV4Cache] = None, values: bool = False, stream=None):
+    """bsa_kv4_evict: keep the ``keep`` slots of largest accumulated weight of every sequence and key head, the last
+    ``recent`` positions (of ``seen`` tokens, default lens) before all others.  In place, or into ``out`` (another
+    cache of at least ``keep`` slots).  -> (new lens int32 [B], index int32 [B,Hkv,keep]: the slot each kept token
+    had, -1 past the new length), with ``values`` also (k, v) bf16 [B,Hkv,keep,D] of the kept slots."""
+    dev = cache.device
+    dst = cache if out is None else out
+    if dst.device != dev:
+        raise ValueError(f"out is on {dst.device}, the cache is on {dev}")
+    if lens is None:
+        raise ValueError("lens is missing")
+    B, H, D = cache.B, cache.Hkv, cache.D
+    a = _abi.Kv4EvictArgs(cache._c, dst._c, _lens("lens", lens, B, dev), _lens("seen", seen, B, dev), keep, recent)
+    need = C.c_size_t(0)
+    L = _abi.lib()
+    check(L.bsa_kv4_evict_workspace(C.byref(a), C.byref(need)), "bsa_kv4_evict")
+    ctx, handle = _place(dev, stream)
+    with ctx:
+        new_lens = torch.empty((B,), dtype=torch.int32, device=dev)
+        index = torch.empty((B, H, keep), dtype=torch.int32, device=dev)
+        kv = vv = None
+        if values:
+            kv = torch.empty((B, H, keep, D), dtype=torch.bfloat16, device=dev)
+            vv = torch.empty((B, H, keep, D), dtype=torch.bfloat16, device=dev)
+        ws = _workspace(need.value, dev)
+        a.new_lens, a.index, a.k_values, a.v_values = _ptr(new_lens), _ptr(index), _ptr(kv), _ptr(vv)
+        a.workspace, a.workspace_bytes = _ptr(ws), need.value
+        check(L.bsa_kv4_evict(C.byref(a), handle), "bsa_kv4_evict")
+    return (new_lens, index, kv, vv) if values else (new_lens, index)
 
 
 def get_device_error(stream=None) -> int:

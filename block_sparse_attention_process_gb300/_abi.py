@@ -73,6 +73,42 @@ class BwdArgs(C.Structure):
                 ("sinks_per_kv_head", C.c_int32)]
 
 
+class KeyWeightsArgs(C.Structure):
+    _fields_ = [("q", C.c_void_p), ("k", C.c_void_p), ("lse", C.c_void_p), ("q_lens", C.c_void_p),
+                ("weights", C.c_void_p), ("workspace", C.c_void_p), ("workspace_bytes", C.c_size_t),
+                ("B", C.c_int32), ("Hq", C.c_int32), ("Hkv", C.c_int32), ("D", C.c_int32), ("S_q", C.c_int64),
+                ("S_kv", C.c_int64), ("softmax_scale", C.c_float), ("logits_soft_cap", C.c_float)]
+
+
+class Kv4Cache(C.Structure):
+    _fields_ = [("k_codes", C.c_void_p), ("k_scales", C.c_void_p), ("v_codes", C.c_void_p),
+                ("v_scales", C.c_void_p), ("weights", C.c_void_p), ("positions", C.c_void_p), ("B", C.c_int32),
+                ("Hkv", C.c_int32), ("D", C.c_int32), ("capacity", C.c_int64)]
+
+
+class Kv4AppendArgs(C.Structure):
+    _fields_ = [("cache", Kv4Cache), ("k", C.c_void_p), ("v", C.c_void_p), ("k_stride", C.c_int64 * 3),
+                ("v_stride", C.c_int64 * 3), ("T", C.c_int64), ("start", C.c_void_p), ("n_new", C.c_void_p),
+                ("first_position", C.c_void_p), ("weights0", C.c_void_p), ("k_values", C.c_void_p),
+                ("v_values", C.c_void_p)]
+
+
+class Kv4FwdArgs(C.Structure):
+    _fields_ = [("cache", Kv4Cache), ("q", C.c_void_p), ("o", C.c_void_p), ("lse", C.c_void_p),
+                ("q_stride", C.c_int64 * 3), ("o_stride", C.c_int64 * 3), ("Hq", C.c_int32), ("T", C.c_int64),
+                ("lens", C.c_void_p), ("q_lens", C.c_void_p), ("softmax_scale", C.c_float),
+                ("logits_soft_cap", C.c_float), ("sinks", C.c_void_p), ("num_sinks", C.c_int32),
+                ("sinks_per_kv_head", C.c_int32), ("accumulate", C.c_int32), ("workspace", C.c_void_p),
+                ("workspace_bytes", C.c_size_t)]
+
+
+class Kv4EvictArgs(C.Structure):
+    _fields_ = [("cache", Kv4Cache), ("out", Kv4Cache), ("lens", C.c_void_p), ("seen", C.c_void_p),
+                ("keep", C.c_int64), ("recent", C.c_int64), ("new_lens", C.c_void_p), ("index", C.c_void_p),
+                ("k_values", C.c_void_p), ("v_values", C.c_void_p), ("workspace", C.c_void_p),
+                ("workspace_bytes", C.c_size_t)]
+
+
 # name -> (restype, argtypes); every symbol include/bsa.h declares
 SIGNATURES = {
     "bsa_mask_compile": (C.c_int, [C.POINTER(MaskSpec), C.POINTER(MaskOpts), C.c_void_p, C.POINTER(C.c_void_p)]),
@@ -86,6 +122,13 @@ SIGNATURES = {
     "bsa_bwd_noalloc": (C.c_int, [C.POINTER(BwdArgs), C.c_void_p, C.c_void_p, C.c_void_p]),
     "bsa_bwd_dkv": (C.c_int, [C.POINTER(BwdArgs), C.c_void_p, C.c_void_p]),
     "bsa_bwd_dq": (C.c_int, [C.POINTER(BwdArgs), C.c_void_p, C.c_void_p]),
+    "bsa_key_weights": (C.c_int, [C.POINTER(KeyWeightsArgs), C.c_void_p, C.c_void_p]),
+    "bsa_key_weights_workspace": (C.c_int, [C.POINTER(KeyWeightsArgs), C.c_void_p, C.POINTER(C.c_size_t)]),
+    "bsa_kv4_append": (C.c_int, [C.POINTER(Kv4AppendArgs), C.c_void_p]),
+    "bsa_kv4_fwd": (C.c_int, [C.POINTER(Kv4FwdArgs), C.c_void_p]),
+    "bsa_kv4_fwd_workspace": (C.c_int, [C.POINTER(Kv4FwdArgs), C.POINTER(C.c_size_t)]),
+    "bsa_kv4_evict": (C.c_int, [C.POINTER(Kv4EvictArgs), C.c_void_p]),
+    "bsa_kv4_evict_workspace": (C.c_int, [C.POINTER(Kv4EvictArgs), C.POINTER(C.c_size_t)]),
     "bsa_get_device_error": (C.c_int, [C.c_void_p, C.POINTER(C.c_uint32)]),
     "bsa_set_wait_limit_ns": (C.c_int, [C.c_uint64]),
     "bsa_debug_wait_timeout": (C.c_int, [C.c_void_p]),

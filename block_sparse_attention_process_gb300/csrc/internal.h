@@ -69,6 +69,14 @@ bsa_status dkv_launch(const bsa_bwd_args* a, const bsa_mask_info* info, float sc
                       uint32_t* err = nullptr, bool schedule = true);
 bsa_status dq_launch(const bsa_bwd_args* a, const bsa_mask_info* info, float scale, cudaStream_t stream,
                      uint32_t* err = nullptr, bool schedule = true);
+bsa_status key_weights_launch(const bsa_key_weights_args* a, const bsa_mask_info* info, float scale,
+                              cudaStream_t stream);
+size_t key_weights_workspace_bytes(const bsa_key_weights_args* a, const bsa_mask_info* info);
+bsa_status kv4_append_launch(const bsa_kv4_append_args* a, cudaStream_t stream);
+bsa_status kv4_fwd_launch(const bsa_kv4_fwd_args* a, float scale, cudaStream_t stream);
+size_t kv4_fwd_workspace_bytes(const bsa_kv4_fwd_args* a);
+bsa_status kv4_evict_launch(const bsa_kv4_evict_args* a, cudaStream_t stream);
+size_t kv4_evict_workspace_bytes(const bsa_kv4_evict_args* a);
 bsa_status debug_wait_timeout_launch(cudaStream_t stream);
 bsa_status debug_selfcheck_launch(cudaStream_t stream);
 

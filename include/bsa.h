@@ -316,9 +316,145 @@ BSA_API bsa_status bsa_bwd_dq(const bsa_bwd_args* args, const bsa_mask_info* fwd
 BSA_API bsa_status bsa_bwd_noalloc(const bsa_bwd_args* args, const bsa_mask_info* fwd_info,
                                    const bsa_mask_info* dkv_info, bsa_stream stream);
 
+/* ---------------------------------------------------------------------------
+ * After the prompt: the weights its keys have received, a key/value cache
+ * held in 4 bits, attention of new tokens over it, and its eviction.  A
+ * program runs a prompt through bsa_fwd, appends its keys and values (with
+ * the weights of bsa_key_weights) and then, token by token, appends and
+ * attends, evicting when the cache reaches its budget.  All of these calls
+ * are asynchronous, allocate nothing (workspaces come from the caller), read
+ * every length from device memory and can be captured into a CUDA graph.
+ * ------------------------------------------------------------------------- */
+
+typedef struct {
+  const void* q;           /* bf16 [B, Hq, S_q, D] */
+  const void* k;           /* bf16 [B, Hkv, S_kv, D] */
+  const float* lse;        /* fp32 [B, Hq, S_q]: bsa_fwd's logsumexp (same scale, cap, sinks) */
+  const int32_t* q_lens;   /* device int32 [B], or NULL: queries at or past q_lens[b] are padding and
+                              are not counted (values outside 0..S_q count as the nearer end) */
+  float* weights;          /* fp32 [B, Hkv, S_kv], written */
+  void* workspace;         /* device, 16-byte aligned, bsa_key_weights_workspace bytes */
+  size_t workspace_bytes;
+  int32_t B, Hq, Hkv, D;
+  int64_t S_q, S_kv;
+  float softmax_scale;     /* NaN selects 1/sqrt(D) */
+  float logits_soft_cap;   /* as in bsa_fwd_args */
+} bsa_key_weights_args;
+
+/* The attention weight each key of a prompt has received: weights[b,h,j] =
+ * sum over the q heads of group h and the queries i that see key j of
+ * exp(s_ij - lse_i), s_ij the scaled (and capped) score.  `dkv_info` is the
+ * mask's BSA_ORIENT_DKV MaskInfo.  A row whose lse is -inf (no visible key)
+ * adds nothing.  Sums are fp32 in a fixed order: results repeat bit for bit. */
+BSA_API bsa_status bsa_key_weights(const bsa_key_weights_args* args, const bsa_mask_info* dkv_info,
+                                   bsa_stream stream);
+/* Bytes of workspace the call needs on the current device (0 is possible). */
+BSA_API bsa_status bsa_key_weights_workspace(const bsa_key_weights_args* args, const bsa_mask_info* dkv_info,
+                                             size_t* bytes);
+
+/* A cache of keys and values in 4 bits; all memory is the caller's.  Each row
+ * of D elements holds D/32 groups of 32 consecutive elements with one bf16
+ * scale s = bf16(max|x| / 7) each; an element is the code round(x / s) + 8
+ * (half to even; 1..15, 8 when s is 0) and stands for s * (code - 8).  A group
+ * that holds an infinity or a NaN gets s = NaN and reads as NaN throughout.
+ *
+ * Order of the codes in a row (4 D bits; chosen so that the tensor-core
+ * fragments of bsa_kv4_fwd load without a transpose): element d of a key is
+ * nibble d % 8 of the 32-bit word (d % 32 / 8) * (D / 32) + d / 32; element d
+ * of a value is nibble d % 4 of the 16-bit word (d % 32 / 4) * (D / 32) +
+ * d / 32, and with D = 128 the two 32-byte halves of a value row are exchanged
+ * in slots with bit 1 set. */
+typedef struct {
+  void* k_codes;      /* uint8 [B, Hkv, capacity, D/2], 16-byte aligned */
+  void* k_scales;     /* bf16  [B, Hkv, capacity, D/32], 16-byte aligned */
+  void* v_codes;      /* as k_codes */
+  void* v_scales;     /* as k_scales */
+  float* weights;     /* fp32  [B, Hkv, capacity]: accumulated attention weight of each slot, or NULL */
+  int32_t* positions; /* int32 [B, Hkv, capacity]: the token's position in its sequence, or NULL */
+  int32_t B, Hkv, D;  /* D is 64 or 128 */
+  int64_t capacity;   /* slots per sequence and head, a multiple of 16 */
+} bsa_kv4_cache;
+
+typedef struct {
+  bsa_kv4_cache cache;
+  const void* k;                     /* bf16, element (b, h, t, d) at b*k_stride[0] + h*k_stride[1] + t*k_stride[2] + d */
+  const void* v;                     /* likewise with v_stride; both 16-byte aligned, strides multiples of 8 */
+  int64_t k_stride[3], v_stride[3];
+  int64_t T;                         /* tokens per sequence in k and v */
+  const int32_t* start;              /* device int32 [B]: the slot of token 0 */
+  const int32_t* n_new;              /* device int32 [B], or NULL (= T): tokens at or past n_new[b] are padding */
+  const int32_t* first_position;     /* device int32 [B], or NULL (= start): position of token 0 */
+  const float* weights0;             /* device fp32 [B, Hkv, T], or NULL (= 0): initial accumulated weights */
+  void* k_values;                    /* bf16 [B, Hkv, T, D] or NULL: what the cache now holds (0 for padding) */
+  void* v_values;
+} bsa_kv4_append_args;
+
+/* Writes tokens 0 .. n_new[b] - 1 of every sequence to slots start[b] + t.  A
+ * token whose slot lies outside the cache is not stored and sets the bounds
+ * bit (2) of the device error word.  Slots not written keep their contents. */
+BSA_API bsa_status bsa_kv4_append(const bsa_kv4_append_args* args, bsa_stream stream);
+
+typedef struct {
+  bsa_kv4_cache cache;
+  const void* q;           /* bf16, element (b, h, t, d) at b*q_stride[0] + h*q_stride[1] + t*q_stride[2] + d;
+                              16-byte aligned, strides multiples of 8 */
+  void* o;                 /* bf16, written, addressed likewise through o_stride */
+  float* lse;              /* fp32 [B, Hq, T], written */
+  int64_t q_stride[3], o_stride[3];
+  int32_t Hq;
+  int64_t T;               /* new tokens per sequence (1 in a plain decode step) */
+  const int32_t* lens;     /* device int32 [B]: keys each sequence holds, the new tokens' own included */
+  const int32_t* q_lens;   /* device int32 [B], or NULL (= T): tokens at or past q_lens[b] are padding */
+  float softmax_scale;     /* NaN selects 1/sqrt(D) */
+  float logits_soft_cap;   /* as in bsa_fwd_args */
+  const float* sinks;      /* as in bsa_fwd_args */
+  int32_t num_sinks, sinks_per_kv_head;
+  int32_t accumulate;      /* 1: cache.weights[b,h,j] += sum over the group's rows of their probability of key j */
+  void* workspace;         /* device, 16-byte aligned, bsa_kv4_fwd_workspace bytes */
+  size_t workspace_bytes;
+} bsa_kv4_fwd_args;
+
+/* Attention of T new tokens over the cache.  With n = q_lens[b], token t < n
+ * of sequence b sees slots 0 .. lens[b] - n + t (the new tokens are the last n
+ * slots and causal among themselves).  Rows that see nothing and padding rows
+ * get O = 0 and LSE = -inf (the log-sum of the sinks where there are any).  A
+ * length outside 0..capacity counts as the nearer end and sets the bounds bit
+ * of the device error word.  Slots at or past lens[b] are never used,
+ * whatever they hold. */
+BSA_API bsa_status bsa_kv4_fwd(const bsa_kv4_fwd_args* args, bsa_stream stream);
+BSA_API bsa_status bsa_kv4_fwd_workspace(const bsa_kv4_fwd_args* args, size_t* bytes);
+
+typedef struct {
+  bsa_kv4_cache cache;     /* needs weights */
+  bsa_kv4_cache out;       /* the same buffers (in place) or others, with room for `keep` slots */
+  const int32_t* lens;     /* device int32 [B]: slots each sequence holds */
+  const int32_t* seen;     /* device int32 [B], or NULL (= lens): tokens each sequence has had in all */
+  int64_t keep;            /* slots to keep per sequence and head, >= 1 */
+  int64_t recent;          /* tokens at positions >= seen[b] - recent are kept before all others, 0 <= recent <= keep */
+  int32_t* new_lens;       /* device int32 [B], written: min(lens[b], keep); not the same memory as lens */
+  int32_t* index;          /* device int32 [B, Hkv, keep], written: the slot that the token now in slot r had before,
+                              -1 past new_lens[b] */
+  void* k_values;          /* bf16 [B, Hkv, keep, D] or NULL: what the kept slots hold (0 past new_lens[b]) */
+  void* v_values;
+  void* workspace;         /* device, 16-byte aligned, bsa_kv4_evict_workspace bytes */
+  size_t workspace_bytes;
+} bsa_kv4_evict_args;
+
+/* Keeps, per sequence and key head, the `keep` slots of largest accumulated
+ * weight (recent tokens first; of equal weights the lower slot; a NaN weight
+ * counts as the largest).  Into other buffers the survivors keep their order.
+ * In place the survivors below slot `keep` stay where they are and the others
+ * fill the freed slots in increasing order, so that a step that evicts few
+ * moves few; the order then lives in `positions`, which the cache must have
+ * if recent > 0.  Without positions a slot's position is its index.  Slots of
+ * `out` past new_lens[b] keep their contents. */
+BSA_API bsa_status bsa_kv4_evict(const bsa_kv4_evict_args* args, bsa_stream stream);
+BSA_API bsa_status bsa_kv4_evict_workspace(const bsa_kv4_evict_args* args, size_t* bytes);
+
 /* Synchronises `stream`, returns the device error word of the current
  * device in *word and clears it.  0 = none; otherwise an OR of the flags
- * 1 = a bounded wait ran out, 2 = out-of-range MaskInfo index, 4 =
+ * 1 = a bounded wait ran out, 2 = out-of-range MaskInfo index (or a cache
+ * length or slot), 4 =
  * tensor-memory allocation failure, 8 = a check of the range-checked build
  * (the source line of the first one is then in bits 16-31 of the word),
  * 16 = a kernel found its dynamic shared memory off the 1024-byte boundary

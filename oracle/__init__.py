@@ -31,6 +31,9 @@ What it computes, and the passage each piece follows:
   accumulator, maximum, normaliser) and the merge of shards with the
   flash rescaling and one final divide (Splash page, "What does ring
   attention add on top of the splash kernel?").
+* ``kv4``        -- the 4-bit key/value cache: quantisation, row order,
+  attention over it, accumulated weights, eviction (this library's own
+  definitions; the pages have no counterpart).
 
 Every function is pinned by ``tests/test_oracle_*.py`` against what the
 pages print (block counts, grid widths, partial-block bytes), closed forms,

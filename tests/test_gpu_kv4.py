@@ -1,0 +1,528 @@
+"""The 4-bit key/value cache on the GPU against the fp64 oracle: append (bit
+for bit), attention, accumulated weights, eviction (exactly), a prompt's key
+weights, and a run of them together.
+
+Tolerances (none is a measured one).  A score is an fp32 sum of D exact
+products: off by at most D 2^-24 sum|q k|, twice that where the tensor core
+truncates, so |ds| <= 2^-16 A with A = scale * sum|q k| of the worst seen key;
+the soft cap's tanh adds 2^-19 cap.  exp2 and the conversion to log2 units add
+2^-20 relative, 2^-20 max(1, |lse|) to a logsumexp.
+  LSE:      ds + 2^-20 max(1, |lse|)
+  weights:  relative 2 ds + 2^-19
+  O:        bf16 rounding 2^-8 |o|, plus (2^-10 + 2 ds) sum_j p_j max_d|v_jd|:
+            a probability times its scale is held in fp16, half a step is 2^-11
+            of it or, below 2^-14 of the row's largest, 2^-25 of that, which
+            summed over up to 2^13 keys is at most 2^-11 of the sum
+"""
+import numpy as np
+import pytest
+import torch
+
+from helpers import need_gpu
+from oracle import kv4, masks
+
+pytestmark = pytest.mark.gpu
+
+
+def bsa_():
+    need_gpu()
+    import block_sparse_attention_process_gb300 as bsa
+    return bsa
+
+
+def host(t):
+    return None if t is None else (t.float() if t.dtype == torch.bfloat16 else t).cpu().numpy()
+
+
+def i32(x):
+    return torch.tensor(x, dtype=torch.int32, device="cuda")
+
+
+def rows(shape, seed, scale=1.0):
+    g = torch.Generator().manual_seed(seed)
+    x = torch.randn(shape, generator=g) * scale * torch.exp(0.5 * torch.randn(shape[-1], generator=g))
+    return x.to(torch.bfloat16)
+
+
+def filled(bsa, B, H, cap, D, seed, junk=True, k=None, v=None):
+    """A cache with every slot written (by the oracle's packing) and the values it holds."""
+    k = rows((B, H, cap, D), seed) if k is None else k
+    v = rows((B, H, cap, D), seed + 1) if v is None else v
+    out, val = [], []
+    for name, x in (("k", k), ("v", v)):
+        codes, s = kv4.quantise(x.double().numpy())
+        out += [torch.from_numpy(kv4.pack(codes, name, np.arange(cap))).cuda(),
+                torch.from_numpy(s).to(torch.bfloat16).cuda()]
+        val.append(kv4.values(codes, s))
+    g = torch.Generator().manual_seed(seed + 2)
+    w = torch.rand((B, H, cap), generator=g).cuda()
+    pos = torch.arange(cap, dtype=torch.int32).expand(B, H, cap).contiguous().cuda()
+    return bsa.KV4Cache(*out, w, pos), val[0], val[1]
+
+
+def poison(cache, lens):
+    """Slots at and past the lengths get arbitrary codes and NaN scales."""
+    for b, n in enumerate(lens):
+        for c, s in ((cache.k_codes, cache.k_scales), (cache.v_codes, cache.v_scales)):
+            c[b, :, n:] = 0x5A
+            s[b, :, n:] = float("nan")
+
+
+def within(name, got, want, tol):
+    got, want = np.asarray(got, np.float64), np.asarray(want, np.float64)
+    assert got.shape == want.shape, name
+    assert np.array_equal(np.isfinite(got), np.isfinite(want)), f"{name}: non-finite pattern"
+    f = np.isfinite(want)
+    assert np.array_equal(got[~f & ~np.isnan(want)], want[~f & ~np.isnan(want)]) and np.array_equal(np.isnan(got), np.isnan(want)), name
+    over = (np.abs(got - want) - tol)[f]
+    assert over.size == 0 or over.max() <= 0, f"{name}: {np.abs(got - want)[f].max():.3e}, over the tolerance by {over.max():.3e}"
+
+
+def check_fwd(o, lse, dw, want, cap=0.0):
+    wo, wl, ww, apv, aqk = want
+    ds = 2.0 ** -16 * aqk + 2.0 ** -19 * (cap or 0.0)
+    with np.errstate(invalid="ignore"):
+        fin = np.where(np.isfinite(wl), np.abs(wl), 0)
+    within("lse", host(lse), wl, ds + 2.0 ** -20 * np.maximum(1, fin))
+    within("o", host(o), wo, 2.0 ** -8 * np.abs(wo) + (2.0 ** -10 + 2 * ds[..., None]) * apv)
+    if dw is not None:
+        # (fp32 addition to a weight of at most 1 rounds by 2^-24 of the sum)
+        within("weights", dw, ww, ww * (2 * ds.max() + 2.0 ** -19) + 2.0 ** -23 * (1 + ww))
+
+
+# ------------------------------------------------------------------ append
+
+@pytest.mark.parametrize("B,H,T,D,cap", [(1, 1, 1, 64, 16), (1, 1, 1, 128, 16), (3, 2, 7, 128, 32), (2, 5, 130, 64, 256),
+                                         (2, 3, 33, 128, 48)])
+def test_append_is_bit_exact(B, H, T, D, cap):
+    bsa = bsa_()
+    k, v = rows((B, H, T, D), 1), rows((B, H, T, D), 2)
+    k[0, 0, 0, :32] = 0                                       # a group of zeros
+    v[-1, -1, -1, -32:] = 0
+    k[0, -1, 0, 32:40] = torch.tensor([1, -1, 0.5, 0.25, 3, -7, 7, 3.5]) * 2.0 ** -120
+    k[-1, 0, -1, 0] = 3e38
+    cache = bsa.KV4Cache.empty(B, H, cap, D)
+    for t in (cache.k_codes, cache.v_codes):
+        t.fill_(0x77)
+    cache.weights.fill_(5)
+    start = [(cap - T) * (b + 1) // (B + 1) for b in range(B)]
+    n_new = [max(0, T - 3 * b) for b in range(B)]
+    w0 = torch.rand((B, H, T)).cuda()
+    kv, vv = bsa.kv4_append(cache, k.cuda(), v.cuda(), i32(start), n_new=i32(n_new), positions=i32([100 + b for b in range(B)]),
+                            weights=w0, values=True)
+    assert bsa.get_device_error() == 0
+    for name, x, codes, scales, vals in (("k", k, cache.k_codes, cache.k_scales, kv), ("v", v, cache.v_codes, cache.v_scales, vv)):
+        c, s = kv4.quantise(x.double().numpy())
+        got_c, got_s, val = host(codes), host(scales), host(vals)
+        for b in range(B):
+            n, at = n_new[b], start[b]
+            assert np.array_equal(got_c[b, :, at:at + n], kv4.pack(c[b, :, :n], name, np.arange(at, at + n))), (name, b)
+            assert np.array_equal(got_s[b, :, at:at + n], s[b, :, :n]), (name, b)
+            assert np.array_equal(val[b, :, :n], kv4.bf16(kv4.values(c, s))[b, :, :n]) and (val[b, :, n:] == 0).all()
+            assert (got_c[b, :, :at] == 0x77).all() and (got_c[b, :, at + n:] == 0x77).all()
+            assert (got_s[b, :, :at] == 0).all() and (got_s[b, :, at + n:] == 0).all()
+    w, pos = host(cache.weights), host(cache.positions)
+    for b in range(B):
+        n, at = n_new[b], start[b]
+        assert np.array_equal(w[b, :, at:at + n], host(w0)[b, :, :n]) and (w[b, :, at + n:] == 5).all() and (w[b, :, :at] == 5).all()
+        assert (pos[b, :, at:at + n] == 100 + b + np.arange(n)).all()
+
+
+def test_append_of_infinities_and_nan():
+    bsa = bsa_()
+    k, v = rows((1, 1, 4, 64), 3), rows((1, 1, 4, 64), 4)
+    k[0, 0, 0, 5], k[0, 0, 1, 40], v[0, 0, 2, 0], v[0, 0, 3, 63] = float("inf"), float("nan"), float("-inf"), float("nan")
+    cache = bsa.KV4Cache.empty(1, 1, 16, 64)
+    kv, vv = bsa.kv4_append(cache, k.cuda(), v.cuda(), i32([0]), values=True)
+    for x, s, val in ((k, cache.k_scales, kv), (v, cache.v_scales, vv)):
+        c, want = kv4.quantise(x.double().numpy())
+        assert np.array_equal(host(s)[:, :, :4], want, equal_nan=True)
+        assert np.array_equal(host(val), kv4.bf16(kv4.values(c, want)), equal_nan=True)
+
+
+def test_append_takes_strided_rows_and_every_bf16_magnitude():
+    bsa = bsa_()
+    B, H, T, D = 2, 3, 5, 64
+    wide = rows((B, T, 2 * H, D), 5).cuda()
+    k, v = wide[:, :, :H].transpose(1, 2), wide[:, :, H:].transpose(1, 2)
+    a, b = bsa.KV4Cache.empty(B, H, 16, D), bsa.KV4Cache.empty(B, H, 16, D)
+    bsa.kv4_append(a, k, v, i32([3, 0]))
+    bsa.kv4_append(b, k.contiguous(), v.contiguous(), i32([3, 0]))
+    for n in ("k_codes", "k_scales", "v_codes", "v_scales", "weights", "positions"):
+        assert torch.equal(getattr(a, n), getattr(b, n)), n
+    assert (a.positions[0, :, 3:8].cpu() == torch.arange(3, 8)).all()
+    # all finite bf16 values, ties among them: 65,280 values, 32 a group, sorted by magnitude and shuffled
+    bits = torch.arange(1 << 16, dtype=torch.int32).to(torch.int16).view(torch.bfloat16)
+    x = bits[torch.isfinite(bits.float())].double().numpy()
+    for order in (np.argsort(np.abs(x), kind="stable"), np.random.default_rng(0).permutation(x.size)):
+        y = torch.from_numpy(x[order]).to(torch.bfloat16).reshape(1, 1, -1, 64)
+        n = y.shape[2]
+        c = bsa.KV4Cache.empty(1, 1, (n + 15) // 16 * 16, 64)
+        bsa.kv4_append(c, y.cuda(), y.cuda(), i32([0]))
+        codes, s = kv4.quantise(y.double().numpy())
+        assert np.array_equal(host(c.k_codes)[:, :, :n], kv4.pack(codes, "k", np.arange(n)))
+        assert np.array_equal(host(c.v_codes)[:, :, :n], kv4.pack(codes, "v", np.arange(n)))
+        assert np.array_equal(host(c.k_scales)[:, :, :n], s)
+
+
+def test_append_outside_the_cache_is_dropped_and_reported():
+    bsa = bsa_()
+    k = rows((2, 1, 4, 64), 6).cuda()
+    cache = bsa.KV4Cache.empty(2, 1, 16, 64)
+    bsa.kv4_append(cache, k, k, i32([14, -2]))
+    with pytest.raises(bsa.BsaError):
+        bsa.get_device_error()
+    assert bsa.get_device_error() == 0
+    s = host(cache.k_scales)
+    assert (s[0, 0, :14] == 0).all() and (s[0, 0, 14:] != 0).all()
+    assert (s[1, 0, :2] != 0).all() and (s[1, 0, 2:] == 0).all()
+
+
+# ------------------------------------------------------------------ attention
+
+FWD = [
+    # B, Hq, Hkv, T, D, capacity, lens, q_lens, cap, sinks
+    (1, 1, 1, 1, 64, 16, [1], None, 0, None),
+    (1, 2, 2, 1, 128, 16, [16], None, 0, None),
+    (4, 4, 2, 1, 128, 160, [0, 1, 129, 160], None, 0, None),
+    (4, 4, 2, 1, 64, 160, [0, 15, 17, 159], None, 0, None),
+    (3, 8, 1, 1, 128, 272, [127, 128, 257], None, 0, None),
+    (2, 6, 2, 3, 128, 144, [3, 140], None, 0, None),
+    (3, 6, 2, 3, 64, 144, [2, 0, 137], None, 0, None),              # more new tokens than keys
+    (3, 4, 4, 4, 128, 144, [50, 1, 144], [4, 1, 0], 0, None),       # padded queries
+    (2, 16, 1, 4, 128, 400, [399, 255], None, 30.0, (1, 4)),
+    (2, 9, 3, 1, 64, 208, [200, 3], None, 1.5, (2,)),
+    (2, 4, 4, 2, 128, 64, [0, 1], None, 0, (4, 3)),                 # rows with the sinks alone
+    (1, 40, 1, 1, 128, 144, [130], None, 0, None),                  # a large group
+    (2, 10, 2, 7, 64, 208, [205, 100], None, 0, None),              # 35 rows a key head
+    (1, 8, 2, 1, 128, 2064, [2049], None, 0, None),
+    (1, 32, 8, 1, 128, 1040, [1033], None, 0, None),
+    (8, 2, 1, 1, 64, 1104, [1101, 3, 700, 64, 0, 999, 128, 1], None, 0, None),
+]
+
+
+@pytest.mark.parametrize("case", FWD, ids=lambda c: f"b{c[0]}h{c[1]}-{c[2]}t{c[3]}d{c[4]}n{max(c[6])}")
+def test_fwd_matches_oracle(case):
+    bsa = bsa_()
+    B, Hq, Hkv, T, D, cap, lens, q_lens, softcap, sink_shape = case
+    cache, kv, vv = filled(bsa, B, Hkv, cap, D, 10)
+    poison(cache, lens)
+    q = rows((B, Hq, T, D), 13, 1.5)
+    sinks = None if sink_shape is None else np.random.default_rng(5).standard_normal(
+        (Hkv, sink_shape[1]) if len(sink_shape) == 2 else sink_shape).astype(np.float32)
+    sd = None if sinks is None else torch.from_numpy(sinks).cuda()
+    want = kv4.forward(q.double().numpy(), kv, vv, lens, q_lens, cap=softcap, sinks=sinks)
+    for accumulate in (False, True):
+        before = cache.weights.clone()
+        o, lse = bsa.kv4_fwd(q.cuda(), cache, i32(lens), q_lens=None if q_lens is None else i32(q_lens),
+                             logits_soft_cap=softcap or None, sinks=sd, accumulate=accumulate)
+        assert bsa.get_device_error() == 0
+        dw = cache.weights.double().cpu().numpy() - before.double().cpu().numpy()
+        if not accumulate:
+            assert (dw == 0).all()
+        else:
+            for b, n in enumerate(lens):
+                assert (dw[b, :, n:] == 0).all()
+        check_fwd(o, lse, dw if accumulate else None, want, softcap)
+
+
+def test_fwd_repeats_bit_for_bit_and_takes_strides():
+    bsa = bsa_()
+    B, Hq, Hkv, T, D = 3, 8, 2, 2, 128
+    cache, _, _ = filled(bsa, B, Hkv, 528, D, 20)
+    lens = i32([528, 77, 300])
+    base = rows((B, T, Hq, D), 21).cuda()
+    q = base.transpose(1, 2)
+    w0 = cache.weights.clone()
+    o, lse = bsa.kv4_fwd(q, cache, lens, accumulate=True)
+    w1 = cache.weights.clone()
+    out = torch.full((B, T, Hq, D), float("nan"), dtype=torch.bfloat16, device="cuda").transpose(1, 2)
+    for _ in range(3):
+        cache.weights.copy_(w0)
+        o2, lse2 = bsa.kv4_fwd(q.contiguous(), cache, lens, o=out, accumulate=True)
+        assert o2 is out and torch.equal(o2, o) and torch.equal(lse2, lse) and torch.equal(cache.weights, w1)
+
+
+def test_fwd_with_far_apart_magnitudes():
+    """Values of very different size with weights the other way round, large scores, an explicit scale."""
+    bsa = bsa_()
+    B, H, n, D = 1, 2, 64, 64
+    k, v = rows((B, H, n, D), 30), rows((B, H, n, D), 31)
+    q = rows((B, H, 1, D), 32)
+    k[0, 0, 7] = (q[0, 0, 0].float() * 8).to(torch.bfloat16)      # one key far ahead of the others ...
+    v[0, 0, 7] = (v[0, 0, 7].float() * 2.0 ** -30).to(torch.bfloat16)   # ... of tiny values
+    v[0, 0, 9] = (v[0, 0, 9].float() * 2.0 ** 20).to(torch.bfloat16)
+    v[0, 1, 3] = (v[0, 1, 3].float() * 2.0 ** 100).to(torch.bfloat16)   # huge, of weight ~2^-100
+    k[0, 1, 3] = (q[0, 1, 0].float() * -16).to(torch.bfloat16)
+    cache, kv, vv = filled(bsa, B, H, n, D, 33, k=k, v=v)
+    o, lse = bsa.kv4_fwd(q.cuda(), cache, i32([n]), softmax_scale=0.25)
+    check_fwd(o, lse, None, kv4.forward(q.double().numpy(), kv, vv, [n], scale=0.25))
+    for factor in (2.0 ** -100, 2.0 ** 60):                         # queries of any size
+        q2 = (q.float() * factor).to(torch.bfloat16)
+        o, lse = bsa.kv4_fwd(q2.cuda(), cache, i32([n]), softmax_scale=0.25 / factor)
+        check_fwd(o, lse, None, kv4.forward(q2.double().numpy(), kv, vv, [n], scale=0.25 / factor))
+
+
+def test_fwd_nan_stays_with_its_head():
+    bsa = bsa_()
+    B, H, n, D = 2, 2, 80, 128
+    k, v = rows((B, H, n, D), 40), rows((B, H, n, D), 41)
+    v[0, 1, 11, 3] = float("nan")        # visible to (0, 1) alone
+    k[1, 0, 60, 0] = float("inf")        # behind sequence 1's length
+    cache, kv, vv = filled(bsa, B, H, n, D, 42, k=k, v=v)
+    q = rows((B, 4, 1, D), 43)
+    o, lse = bsa.kv4_fwd(q.cuda(), cache, i32([n, 60]))
+    with np.errstate(invalid="ignore"):
+        want = kv4.forward(q.double().numpy(), np.nan_to_num(kv), np.nan_to_num(vv), [n, 60])
+    o, lse = host(o), host(lse)
+    assert np.isnan(o[0, 2:, :, :32]).all() and np.isfinite(o[0, 2:, :, 32:]).all()   # NaN in its group alone
+    assert np.isfinite(o[0, :2]).all() and np.isfinite(o[1]).all() and np.isfinite(lse).all()
+    within("o", o[1], want[0][1], 2.0 ** -8 * np.abs(want[0][1]) + 2.0 ** -9 * want[3][1])
+
+
+def test_fwd_lengths_outside_the_cache_are_clamped_and_reported():
+    bsa = bsa_()
+    cache, kv, vv = filled(bsa, 2, 1, 32, 64, 50)
+    q = rows((2, 1, 1, 64), 51)
+    o, lse = bsa.kv4_fwd(q.cuda(), cache, i32([1000, -5]))
+    with pytest.raises(bsa.BsaError):
+        bsa.get_device_error()
+    check_fwd(o, lse, None, kv4.forward(q.double().numpy(), kv, vv, [32, 0]))
+
+
+def test_append_and_fwd_in_a_replayed_graph_and_on_another_stream():
+    bsa = bsa_()
+    B, Hq, Hkv, D, cap = 2, 4, 2, 128, 320
+    cache, _, _ = filled(bsa, B, Hkv, cap, D, 60)
+    lens = i32([0, 0])
+    q, k, v = (torch.zeros((B, h, 1, D), dtype=torch.bfloat16, device="cuda") for h in (Hq, Hkv, Hkv))
+
+    def step():
+        bsa.kv4_append(cache, k, v, lens)
+        return bsa.kv4_fwd(q, cache, lens + 1, accumulate=True)
+
+    step()
+    torch.cuda.synchronize()
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph):
+        o, lse = step()
+    side = torch.cuda.Stream()
+    for i, ls in enumerate(([5, 300], [0, 1], [319, 128])):
+        lens.copy_(i32(ls))
+        for t, s in ((q, 61), (k, 62), (v, 63)):
+            t.copy_(rows(t.shape, s + 10 * i))
+        w0 = cache.weights.clone()
+        graph.replay()
+        got = o.clone(), lse.clone(), cache.weights.clone()
+        cache.weights.copy_(w0)
+        side.wait_stream(torch.cuda.current_stream())
+        bsa.kv4_append(cache, k, v, lens, stream=side)
+        lens1 = lens + 1
+        side.wait_stream(torch.cuda.current_stream())
+        o2, lse2 = bsa.kv4_fwd(q, cache, lens1, accumulate=True, stream=side)
+        torch.cuda.current_stream().wait_stream(side)
+        assert torch.equal(o2, got[0]) and torch.equal(lse2, got[1]) and torch.equal(cache.weights, got[2])
+    assert bsa.get_device_error() == 0
+
+
+# ------------------------------------------------------------------ eviction
+
+EVICT = [
+    # B, H, D, capacity, lens, keep, recent
+    (1, 1, 64, 16, [1], 1, 0),
+    (1, 2, 128, 16, [16], 1, 1),
+    (2, 3, 128, 208, [200, 130], 128, 16),
+    (3, 2, 64, 48, [48, 20, 0], 20, 7),
+    (2, 1, 128, 1104, [1100, 1025], 1024, 0),
+    (2, 2, 128, 3088, [3085, 2000], 700, 128),
+    (1, 1, 64, 20016, [20011], 5000, 40),
+]
+
+
+@pytest.mark.parametrize("in_place", [False, True], ids=["into", "in-place"])
+@pytest.mark.parametrize("weights", ["random", "ties", "odd"])
+@pytest.mark.parametrize("case", EVICT, ids=lambda c: f"n{max(c[4])}k{c[5]}")
+def test_evict_is_exact(case, weights, in_place):
+    bsa = bsa_()
+    B, H, D, cap, lens, keep, recent = case
+    rng = np.random.default_rng(7)
+    codes = [torch.from_numpy(rng.integers(0, 256, (B, H, cap, D // 2)).astype(np.uint8)).cuda() for _ in "kv"]
+    scales = [torch.from_numpy(rng.standard_normal((B, H, cap, D // 32)).astype(np.float32)).to(torch.bfloat16).cuda() for _ in "kv"]
+    w = rng.random((B, H, cap)).astype(np.float32) ** 4
+    if weights == "ties":
+        w = rng.integers(0, 3, (B, H, cap)).astype(np.float32)
+    if weights == "odd":
+        w = np.where(rng.random(w.shape) < 0.1, np.float32(-0.0), w)
+        w = np.where(rng.random(w.shape) < 0.1, np.float32(np.nan), w)
+        w = np.where(rng.random(w.shape) < 0.1, np.float32(np.inf), w)
+        w = np.where(rng.random(w.shape) < 0.1, -w, w)
+    pos = np.stack([[rng.permutation(cap) for _ in range(H)] for _ in range(B)]).astype(np.int32)
+    cache = bsa.KV4Cache(codes[0], scales[0], codes[1], scales[1], torch.from_numpy(w).cuda(), torch.from_numpy(pos).cuda())
+    seen = [cap + 3] * B
+    want, new = kv4.evict(w, pos, lens, keep, recent, seen, in_place)
+    src = {n: host(getattr(cache, n)).copy() for n in ("k_codes", "k_scales", "v_codes", "v_scales", "weights", "positions")}
+    src["k_val"] = kv4.values(kv4.unpack(src["k_codes"], "k"), src["k_scales"])
+    src["v_val"] = kv4.values(kv4.unpack(src["v_codes"], "v"), src["v_scales"])
+    out = None
+    if not in_place:
+        out = bsa.KV4Cache.empty(B, H, (keep + 31) // 16 * 16, D)
+        out.weights.fill_(9)
+    new_lens, index, kv, vv = bsa.kv4_evict(cache, i32(lens), keep, recent=recent, seen=i32(seen), out=out, values=True)
+    assert bsa.get_device_error() == 0
+    assert np.array_equal(host(new_lens), new) and np.array_equal(host(index), want)
+    dst = cache if in_place else out
+    got = {n: host(getattr(dst, n)) for n in ("k_codes", "k_scales", "v_codes", "v_scales", "weights", "positions")}
+    got["k_val"] = kv4.values(kv4.unpack(got["k_codes"], "k"), got["k_scales"])
+    got["v_val"] = kv4.values(kv4.unpack(got["v_codes"], "v"), got["v_scales"])
+    for b in range(B):
+        n = int(new[b])
+        for h in range(H):
+            i = want[b, h, :n]
+            for name in ("k_val", "v_val", "weights", "positions", "k_scales", "v_scales"):
+                assert np.array_equal(got[name][b, h, :n], src[name][b, h, i], equal_nan=True), name
+            for vals, name in ((kv, "k_val"), (vv, "v_val")):
+                assert np.array_equal(host(vals)[b, h, :n], kv4.bf16(src[name][b, h, i])) and (host(vals)[b, h, n:] == 0).all()
+        if not in_place:
+            assert (got["weights"][b, :, n:] == 9).all() and (got["k_codes"][b, :, n:] == 0).all()
+
+
+def test_evict_without_positions_and_without_values():
+    bsa = bsa_()
+    c, _, _ = filled(bsa, 2, 2, 64, 64, 80)
+    plain = bsa.KV4Cache(c.k_codes, c.k_scales, c.v_codes, c.v_scales, c.weights)
+    out = bsa.KV4Cache.empty(2, 2, 32, 64)
+    new_lens, index = bsa.kv4_evict(plain, i32([64, 30]), 32, recent=5, out=out)
+    want, new = kv4.evict(host(c.weights), None, [64, 30], 32, 5)
+    assert np.array_equal(host(index), want) and np.array_equal(host(new_lens), new)
+    assert np.array_equal(host(out.positions)[0], want[0])
+    bsa.kv4_evict(plain, i32([200, -1]), 32, out=out)
+    with pytest.raises(bsa.BsaError):
+        bsa.get_device_error()
+
+
+# ------------------------------------------------------------------ key weights
+
+KEYS = [
+    # B, Hq, Hkv, S_q, S_kv, D, mask, kwargs, q_lens, cap
+    (1, 1, 1, 128, 128, 64, "causal", {}, None, 0),
+    (1, 2, 2, 512, 512, 64, "causal", {}, None, 0),
+    (2, 4, 2, 640, 640, 128, "causal", {}, [640, 333], 0),
+    (1, 6, 2, 384, 384, 128, "full", {}, [1], 0),
+    (2, 2, 1, 768, 768, 64, "local", {"local_left": 200, "local_right": 0}, [0, 768], 0),
+    (1, 3, 3, 512, 512, 128, "local", {"local_left": 40, "local_right": 70}, None, 20.0),
+    (1, 8, 1, 1024, 1024, 128, "chunked", {"chunk": 300}, [1000], 0),
+    (1, 4, 2, 256, 512, 128, "dense", {}, None, 0),
+    (2, 2, 2, 512, 256, 64, "dense", {}, [511, 130], 2.0),
+    (1, 4, 2, 384, 384, 64, "perhead", {}, None, 0),
+    (1, 20, 1, 256, 256, 64, "causal", {}, None, 0),
+]
+
+
+@pytest.mark.parametrize("case", KEYS, ids=lambda c: f"{c[6]}-b{c[0]}h{c[1]}-{c[2]}s{c[3]}-{c[4]}d{c[5]}")
+def test_key_weights_match_oracle(case):
+    bsa = bsa_()
+    B, Hq, Hkv, Sq, Skv, D, kind, kw, q_lens, cap = case
+    q, k = rows((B, Hq, Sq, D), 90), rows((B, Hkv, Skv, D), 91)
+    rng = np.random.default_rng(92)
+    heads = Hq if kind == "perhead" else 1
+    if kind in ("dense", "perhead"):
+        dense = (rng.random((heads, Sq, Skv)) < 0.3).astype(np.uint8)
+        dense[:, 5] = 0                                                 # a row that sees nothing
+        dense[:, :128, 128:256] = 0                                     # an empty and a full block
+        dense[:, 128:256, :128] = 1
+        dkv = bsa.mask_compile("dense", Sq, Skv, dense=torch.from_numpy(dense).cuda(), orientation="dkv")
+        allowed = dense != 0
+    else:
+        dkv = bsa.mask_compile(kind, Sq, Skv, orientation="dkv", **kw)
+        allowed = masks.materialise(kind, Sq, Skv, left=kw.get("local_left"), right=kw.get("local_right"), chunk=kw.get("chunk"))[None]
+    qd, kd = q.double().numpy(), k.double().numpy()
+    lse = np.full((B, Hq, Sq), -np.inf, np.float32)
+    want, amax, top = np.zeros((B, Hkv, Skv)), 0.0, 1.0
+    for b in range(B):
+        n = Sq if q_lens is None else q_lens[b]
+        for h in range(Hq):
+            g = h // (Hq // Hkv)
+            s = qd[b, h] @ kd[b, g].T * D ** -0.5
+            amax = max(amax, (np.abs(qd[b, h]) @ np.abs(kd[b, g]).T).max() * D ** -0.5)
+            if cap:
+                s = cap * np.tanh(s / cap)
+            s = np.where(allowed[h if heads > 1 else 0], s, -np.inf)
+            some = np.isfinite(s).any(-1)
+            m = np.where(some, s.max(-1), 0)
+            with np.errstate(divide="ignore"):
+                lse[b, h] = np.where(some, m + np.log(np.exp(s - m[:, None]).sum(-1)), -np.inf)
+            p = np.exp(s - np.where(some, lse[b, h].astype(np.float64), 0)[:, None])
+            want[b, g] += p[:n].sum(0)
+            top = max(top, np.abs(lse[b, h][some]).max())
+    args = (q.cuda(), k.cuda(), torch.from_numpy(lse).cuda(), dkv)
+    kwargs = dict(q_lens=None if q_lens is None else i32(q_lens), logits_soft_cap=cap or None)
+    got = bsa.key_weights(*args, **kwargs)
+    assert bsa.get_device_error() == 0
+    ds = 2.0 ** -16 * amax + 2.0 ** -19 * cap + 2.0 ** -23 * top
+    # (the sum of up to Sq G positive terms: 2^-24 a step, far fewer steps in a row than 2^5)
+    within("key weights", host(got), want, want * (2 * ds + 2.0 ** -18) + 1e-30)
+    assert torch.equal(bsa.key_weights(*args, **kwargs), got)
+
+
+def test_key_weights_of_fwd_sum_to_the_number_of_queries():
+    bsa = bsa_()
+    B, Hq, Hkv, S, D = 1, 8, 2, 2048, 128
+    q, k = rows((B, Hq, S, D), 95).cuda(), rows((B, Hkv, S, D), 96).cuda()
+    info, dkv = bsa.mask_compile("causal", S, S), bsa.mask_compile("causal", S, S, orientation="dkv")
+    _, lse = bsa.fwd(q, k, k, info)
+    side = torch.cuda.Stream()
+    side.wait_stream(torch.cuda.current_stream())
+    w = bsa.key_weights(q, k, lse, dkv, stream=side)
+    torch.cuda.current_stream().wait_stream(side)
+    total = w.double().sum(-1).cpu().numpy()
+    # every query's probabilities sum to 1 up to the errors of its logsumexp (1e-5) and of the scores
+    assert np.abs(total / (Hq // Hkv * S) - 1).max() < 2e-4
+
+
+# ------------------------------------------------------------------ together
+
+def test_prompt_append_decode_evict_together():
+    """A padded batch of prompts, its keys' weights, the cache, and 40 tokens with an eviction whenever the budget
+    is exceeded.  The oracle follows with its own attention on the values the cache holds; what the library
+    evicts must be what the oracle evicts given the library's accumulated weights."""
+    bsa = bsa_()
+    B, Hq, Hkv, D, S = 2, 4, 2, 64, 256
+    prompt, keep, recent, cap = [256, 150], 176, 32, 272
+    q, k, v = rows((B, Hq, S, D), 100), rows((B, Hkv, S, D), 101), rows((B, Hkv, S, D), 102)
+    info, dkv = bsa.mask_compile("causal", S, S), bsa.mask_compile("causal", S, S, orientation="dkv")
+    _, lse = bsa.fwd(q.cuda(), k.cuda(), v.cuda(), info)
+    w = bsa.key_weights(q.cuda(), k.cuda(), lse, dkv, q_lens=i32(prompt))
+    cache = bsa.KV4Cache.empty(B, Hkv, cap, D)
+    bsa.kv4_append(cache, k.cuda(), v.cuda(), i32([0, 0]), n_new=i32(prompt), weights=w)
+
+    def held():
+        return [kv4.values(kv4.unpack(host(c), n), host(s)) for n, c, s in
+                (("k", cache.k_codes, cache.k_scales), ("v", cache.v_codes, cache.v_scales))]
+
+    lens, seen = i32(prompt), i32(prompt)
+    for step in range(40):
+        n_before = host(lens).copy()
+        if (n_before > keep).any() and step % 4 == 0:
+            w0, p0 = host(cache.weights).copy(), host(cache.positions).copy()
+            want, new = kv4.evict(w0, p0, n_before, keep, recent, host(seen), in_place=True)
+            lens, index = bsa.kv4_evict(cache, lens, keep, recent=recent, seen=seen)
+            assert np.array_equal(host(index), want) and np.array_equal(host(lens), new)
+            pos = host(cache.positions)
+            for b in range(B):          # the last `recent` positions are still there
+                for h in range(Hkv):
+                    have = set(pos[b, h, :new[b]].tolist())
+                    assert have >= set(range(int(host(seen)[b]) - recent, int(host(seen)[b]))) and len(have) == new[b]
+        q1, k1, v1 = (rows((B, h, 1, D), 110 + 3 * step + i) for i, h in enumerate((Hq, Hkv, Hkv)))
+        bsa.kv4_append(cache, k1.cuda(), v1.cuda(), lens, positions=seen)
+        lens, seen = lens + 1, seen + 1
+        w0 = cache.weights.double().cpu().numpy()
+        o, l = bsa.kv4_fwd(q1.cuda(), cache, lens, accumulate=True)
+        kk, vv = held()
+        dw = cache.weights.double().cpu().numpy() - w0
+        wo, wl, ww, apv, aqk = kv4.forward(q1.double().numpy(), kk, vv, host(lens))
+        ds = 2.0 ** -16 * aqk
+        within("lse", host(l), wl, ds + 2.0 ** -20 * np.maximum(1, np.abs(wl)))
+        within("o", host(o), wo, 2.0 ** -8 * np.abs(wo) + (2.0 ** -10 + 2 * ds[..., None]) * apv)
+        within("weights", dw, ww, ww * (2 * ds.max() + 2.0 ** -19) + 2.0 ** -23 * (np.abs(w0) + 1))
+    assert bsa.get_device_error() == 0
+    assert (host(lens) <= keep + 4).all()
