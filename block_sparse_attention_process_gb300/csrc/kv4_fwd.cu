@@ -1,11 +1,40 @@
 // Attention of new tokens over the 4-bit cache: o = sum_j p_j v_j, p_j =
 // exp(s_j - lse), s_j = scale q.k_j (capped), over the slots a token sees.
 //
-// One CTA per (sequence, q head, new token): scores into the workspace, the
-// softmax statistics by a block reduction, then one output element per
-// thread.  A second kernel adds the probabilities of a key's rows to its
-// accumulated weight.
+// The rows that read one key head (its group's q heads times the new tokens)
+// are taken kRows at a time as the narrow side of m16n8k16 products:
+//     S^T [16 keys, 8 rows] = K Q^T,     O^T [16 elements, 8 rows] += V^T P^T
+// so the codes are always the 16-row operand, none of it padding.
+//
+// Codes as numbers.  A nibble c at bits 0-3 of a 16-bit half, read as fp16, is
+// the subnormal c 2^-24, at bits 4-7 it is 16 c 2^-24; products with fp16
+// numbers are exact in fp32.  So one AND makes a pair of operands, with no
+// conversion, and q of odd elements carries the factor 1/16 (odd rows of O^T
+// are divided at the end).  The offset 8 leaves K through the accumulators,
+// which start at -8 2^-24 sum(q) of the group, and V by an exact fp16
+// subtraction (a product with a constant operand instead would need
+// accumulators for the sums of p s, registers that are not there).  Each
+// group's scale multiplies S^T in fp32.
+// Roundings: q is exact (bf16 into fp16 after a power of two that brings the
+// row's largest magnitude to [2^14, 2^15); elements 2^-24 times smaller start
+// to lose bits); a probability times its value scale is rounded to fp16.
+//
+// The running reference of a row is R = max(s_j + log2 of the largest value
+// scale of j), so that p s never leaves fp16's range however the scales of the
+// keys differ; l = sum 2^(s_j - R) stays in fp32.  It moves only when it grows
+// by more than 8 (log2 units).
+//
+// Work: all (sequence, head, row tile) pairs' key tiles of 128 form one
+// sequence, cut into equal runs, one per CTA; lengths are read on the device.
+// A run's parts of pairs that other CTAs share go to the workspace as (R, l,
+// O) records; a second kernel joins them in a fixed order and, if asked,
+// turns the stored scores into probabilities and adds them to the weights.
+// Eight warps take 16 keys of a tile each; one lane of warp 0 brings tiles in
+// by bulk copies through a ring of stages (a warp of its own for that would
+// leave 96 registers a thread instead of 128, and spill).
 #include <cmath>
+
+#include <cuda_fp16.h>
 
 #include "internal.h"
 #include "kv4.cuh"
@@ -14,114 +43,813 @@
 namespace bsa {
 namespace {
 
+constexpr int kTileKeys = 128;
+constexpr int kWarps = 8;                  // 16 keys of a tile each
+constexpr int kThreads = 32 * kWarps;
+constexpr float kRescale = 8.0f;
+constexpr float kLog2e = 1.4426950408889634f;
+constexpr float kLn2 = 0.69314718055994530942f;
+
 struct Kv4FwdParams {
   bsa_kv4_cache c;
   const __nv_bfloat16* q;
   __nv_bfloat16* o;
   float* lse;
   int64_t qs[3], os[3];
-  int32_t Hq, T, G;
+  int32_t Hq, T, G, R;      // R = G * T rows per key head
+  int32_t row_tiles;        // ceil(R / kRows)
   const int32_t *lens, *q_lens;
-  float scale, cap;
+  float scale_log2;         // without a cap: scale * log2 e; with one: scale / cap
+  float cap_log2;
   const float* sinks;
   int32_t n_sinks, sinks_kv;
-  int32_t accumulate;
-  float* scores;  // [B, Hq, T, capacity]
+  int32_t n_cta;
+  float* rec_stat;          // [2 * n_cta][2][kRows]: R and l of a CTA's first and last part
+  float* rec_o;             // [2 * n_cta][kRows][D]
+  float* scores;            // [B * Hkv * row_tiles][capacity][score_stride], log2 units, or null
+  int32_t score_stride;
+  int32_t join_rows;        // blocks of the join kernel that merge rows
   uint32_t* err;
+  uint64_t wait_ns;
 };
 
-// Slots that token t of sequence b sees: [0, end).
-__device__ __forceinline__ int32_t visible_end(const Kv4FwdParams& p, int32_t b, int32_t t, uint32_t* err) {
-  const int32_t len = clamp_len(p.lens[b], p.c.capacity, err);
-  const int32_t n = p.q_lens ? min(max(p.q_lens[b], 0), p.T) : p.T;
-  if (t >= n) return 0;
-  return max(0, len - n + t + 1);
+// ------------------------------------------------------------------ walk
+
+// One (sequence, head, row tile) pair's place in the sequence of tiles.
+struct Pair {
+  int32_t b, len, nq;  // keys held; new tokens
+  int32_t tiles;       // key tiles of each of the sequence's Hkv * row_tiles pairs
+};
+
+__device__ __forceinline__ Pair load_pair(const Kv4FwdParams& p, int32_t b, uint32_t* err) {
+  Pair x;
+  x.b = b;
+  x.len = clamp_len(p.lens[b], p.c.capacity, err);
+  x.nq = p.q_lens ? min(max(p.q_lens[b], 0), p.T) : p.T;
+  x.tiles = x.nq > 0 ? (x.len + kTileKeys - 1) / kTileKeys : 0;
+  return x;
 }
 
-template <int D>
-__global__ void __launch_bounds__(256) fwd_rows_kernel(const __grid_constant__ Kv4FwdParams p) {
-  __shared__ float q[D], red[8], part[256];
-  griddep_launch_dependents();
-  griddep_wait();
-  const int32_t row = static_cast<int32_t>(blockIdx.x);
-  const int32_t t = row % p.T, hq = row / p.T % p.Hq, b = row / p.T / p.Hq;
-  const int32_t h = hq / p.G;
-  const int64_t head = (static_cast<int64_t>(b) * p.c.Hkv + h) * p.c.capacity;
-  if (threadIdx.x < D) q[threadIdx.x] = __bfloat162float(p.q[b * p.qs[0] + hq * p.qs[1] + t * p.qs[2] + threadIdx.x]);
-  __syncthreads();
-  const int32_t end = visible_end(p, b, t, threadIdx.x == 0 ? p.err : nullptr);
-  float* x = p.scores + static_cast<int64_t>(row) * p.c.capacity;
-  float m = -INFINITY;
-  for (int32_t j = threadIdx.x; j < end; j += 256) {
-    float s = 0.f;
-    for (int w = 0; w < Kv4<D>::kWords; ++w) {
-      const uint32_t c = static_cast<const uint32_t*>(p.c.k_codes)[(head + j) * Kv4<D>::kWords + w];
-      float dot = 0.f;
-      for (int i = 0; i < 8; ++i)
-        dot = fmaf(static_cast<float>(static_cast<int>((c >> (4 * i)) & 15u) - 8), q[k_word_elem<D>(w) + i], dot);
-      s = fmaf(dot, __bfloat162float(static_cast<const __nv_bfloat16*>(p.c.k_scales)[(head + j) * Kv4<D>::kGroups + w % Kv4<D>::kGroups]), s);
+// Tiles of all sequences; every lane of the calling warp gets the sum.
+__device__ __forceinline__ int64_t total_tiles(const Kv4FwdParams& p) {
+  const int lane = threadIdx.x & 31;
+  const int64_t per = static_cast<int64_t>(p.c.Hkv) * p.row_tiles;
+  int64_t sum = 0;
+  for (int32_t b = lane; b < p.c.B; b += 32) sum += load_pair(p, b, nullptr).tiles * per;
+#pragma unroll
+  for (int o = 16; o > 0; o >>= 1) sum += __shfl_xor_sync(0xffffffffu, sum, o);
+  return sum;
+}
+
+// First tile of sequence b (b uniform over the warp).
+__device__ __forceinline__ int64_t tiles_before(const Kv4FwdParams& p, int32_t b) {
+  const int lane = threadIdx.x & 31;
+  const int64_t per = static_cast<int64_t>(p.c.Hkv) * p.row_tiles;
+  int64_t sum = 0;
+  for (int32_t i = lane; i < b; i += 32) sum += load_pair(p, i, nullptr).tiles * per;
+#pragma unroll
+  for (int o = 16; o > 0; o >>= 1) sum += __shfl_xor_sync(0xffffffffu, sum, o);
+  return sum;
+}
+
+// CTAs that have work (none gets an empty run).  Of n, CTA c has tiles
+// [c * total / n, (c + 1) * total / n); cta_of is the one that has tile t.
+__device__ __forceinline__ int32_t runs(const Kv4FwdParams& p, int64_t total) {
+  return static_cast<int32_t>(min(static_cast<int64_t>(p.n_cta), total));
+}
+__device__ __forceinline__ int64_t first_tile(int64_t c, int64_t total, int32_t n) { return c * total / n; }
+__device__ __forceinline__ int32_t cta_of(int64_t t, int64_t total, int32_t n) {
+  return static_cast<int32_t>(((t + 1) * n - 1) / total);
+}
+
+// Cursor over a CTA's run: parts of pairs, each a range of key tiles.
+struct Run {
+  int64_t at, end;     // tiles of the run still to go
+  int64_t seq0;        // first tile of sequence pair.b
+  Pair pair;
+  int32_t bh, rt;      // b * Hkv + h; row tile
+  int32_t k0, k1;      // the part's key tiles
+  bool whole;          // the part is the whole pair
+  // places the cursor before tile `first` (warp-collective)
+  __device__ __forceinline__ void init(const Kv4FwdParams& p, int64_t first, int64_t last, uint32_t* err) {
+    at = first;
+    end = last;
+    const int lane = threadIdx.x & 31;
+    const int64_t per = static_cast<int64_t>(p.c.Hkv) * p.row_tiles;
+    seq0 = 0;
+    int32_t b = 0;
+    if (at < end) {
+      for (int32_t b0 = 0;; b0 += 32) {
+        const int64_t n = b0 + lane < p.c.B ? load_pair(p, b0 + lane, err).tiles * per : 0;
+        int64_t inc = n;
+#pragma unroll
+        for (int o = 1; o < 32; o *= 2) {
+          const int64_t x = __shfl_up_sync(0xffffffffu, inc, o);
+          if (lane >= o) inc += x;
+        }
+        const uint32_t past = __ballot_sync(0xffffffffu, seq0 + inc > at);
+        if (past || b0 + 32 >= p.c.B) {
+          const int l = past ? __ffs(past) - 1 : 31;
+          b = b0 + l;
+          seq0 += __shfl_sync(0xffffffffu, inc - n, l);
+          break;
+        }
+        seq0 += __shfl_sync(0xffffffffu, inc, 31);
+      }
+      pair = load_pair(p, b, nullptr);
     }
-    s *= p.scale;
-    if (p.cap > 0.f) s = p.cap * tanhf(s / p.cap);
-    x[j] = s;
-    m = fmaxf(m, s);
   }
-  for (int32_t j = threadIdx.x; j < p.n_sinks; j += 256) m = fmaxf(m, p.sinks[(p.sinks_kv ? h * p.n_sinks : 0) + j]);
-  for (int o = 16; o > 0; o >>= 1) m = fmaxf(m, __shfl_xor_sync(0xffffffffu, m, o));
-  if (threadIdx.x % 32 == 0) red[threadIdx.x / 32] = m;
-  __syncthreads();
-  for (int i = 0; i < 8; ++i) m = fmaxf(m, red[i]);
-  __syncthreads();
-  float l = 0.f;
-  for (int32_t j = threadIdx.x; j < end; j += 256) l += expf(x[j] - m);
-  for (int32_t j = threadIdx.x; j < p.n_sinks; j += 256) l += expf(p.sinks[(p.sinks_kv ? h * p.n_sinks : 0) + j] - m);
-  for (int o = 16; o > 0; o >>= 1) l += __shfl_xor_sync(0xffffffffu, l, o);
-  if (threadIdx.x % 32 == 0) red[threadIdx.x / 32] = l;
-  __syncthreads();
-  l = 0.f;
-  for (int i = 0; i < 8; ++i) l += red[i];
-  const float lse = l > 0.f ? m + logf(l) : (m == -INFINITY ? -INFINITY : NAN);
-  if (threadIdx.x == 0) p.lse[row] = lse;
-  // output element d: 256 / D threads share it
-  const int d = threadIdx.x % D;
-  const int g = d / 32, word = (d % 32 / 4) * Kv4<D>::kGroups + g;
-  float acc = 0.f;
-  for (int32_t j = threadIdx.x / D; j < end; j += 256 / D) {
-    const uint32_t c = static_cast<const uint16_t*>(p.c.v_codes)[(head + j) * 2 * Kv4<D>::kWords + (word ^ (2 * v_word_swap<D>(j)))];
-    const float s = __bfloat162float(static_cast<const __nv_bfloat16*>(p.c.v_scales)[(head + j) * Kv4<D>::kGroups + g]);
-    acc = fmaf(expf(x[j] - lse), s * static_cast<float>(static_cast<int>((c >> (4 * (d % 4))) & 15u) - 8), acc);
+  __device__ bool next(const Kv4FwdParams& p) {
+    if (at >= end) return false;
+    const int64_t per = static_cast<int64_t>(p.c.Hkv) * p.row_tiles;
+    while (at >= seq0 + pair.tiles * per) {
+      seq0 += pair.tiles * per;
+      pair = load_pair(p, pair.b + 1, nullptr);
+    }
+    const int64_t i = at - seq0;
+    const int32_t hr = static_cast<int32_t>(i / pair.tiles);
+    bh = pair.b * p.c.Hkv + hr / p.row_tiles;
+    rt = hr % p.row_tiles;
+    k0 = static_cast<int32_t>(i % pair.tiles);
+    k1 = static_cast<int32_t>(min(static_cast<int64_t>(pair.tiles), k0 + (end - at)));
+    whole = k0 == 0 && k1 == pair.tiles;
+    at += k1 - k0;
+    return true;
   }
-  part[threadIdx.x] = acc;
-  __syncthreads();
-  if (threadIdx.x < D) {
-    for (int i = 1; i < 256 / D; ++i) acc += part[threadIdx.x + i * D];
-    p.o[b * p.os[0] + hq * p.os[1] + t * p.os[2] + d] = __float2bfloat16_rn(acc);
+};
+
+template <int D, int NT>
+struct __align__(128) FwdShared {
+  static constexpr int kRows = 8 * NT;
+  static constexpr int kStages = D == 128 ? 5 : 8;
+  // tiles issued ahead of the one being computed: the stage written is the one
+  // released two tiles ago, so the issuing lane hardly ever waits
+  static constexpr int kAhead = kStages - 2;
+  static constexpr int kPad = D + 4;  // floats between rows of the merge buffer (bank spread)
+  uint8_t k[kStages][kTileKeys * Kv4<D>::kRowBytes];
+  uint8_t v[kStages][kTileKeys * Kv4<D>::kRowBytes];
+  uint8_t ks[kStages][kTileKeys * Kv4<D>::kScaleBytes];
+  uint8_t vs[kStages][kTileKeys * Kv4<D>::kScaleBytes];
+  float merge[4][kRows * kPad];
+  float stat[2][kWarps][kRows];
+  uint64_t full[kStages], empty[kStages];
+  Run ahead;          // the loading lane's place in the CTA's run
+  int32_t ahead_tile; // next key tile of that part
+  uint32_t abort_flag;
+};
+
+// ------------------------------------------------------------------ products
+
+__device__ __forceinline__ void mma_f16(float (&c)[4], uint32_t a0, uint32_t a1, uint32_t a2, uint32_t a3, uint32_t b0,
+                                        uint32_t b1) {
+  asm volatile(
+      "mma.sync.aligned.m16n8k16.row.col.f32.f16.f16.f32 {%0,%1,%2,%3}, {%4,%5,%6,%7}, {%8,%9}, {%0,%1,%2,%3};"
+      : "+f"(c[0]), "+f"(c[1]), "+f"(c[2]), "+f"(c[3])
+      : "r"(a0), "r"(a1), "r"(a2), "r"(a3), "r"(b0), "r"(b1));
+}
+
+// The same into fresh accumulators that start at z0 (even column) and z1.
+__device__ __forceinline__ void mma_f16_from(float (&c)[4], uint32_t a0, uint32_t a1, uint32_t a2, uint32_t a3,
+                                             uint32_t b0, uint32_t b1, float z0, float z1) {
+  asm volatile(
+      "mma.sync.aligned.m16n8k16.row.col.f32.f16.f16.f32 {%0,%1,%2,%3}, {%4,%5,%6,%7}, {%8,%9}, {%10,%11,%10,%11};"
+      : "=f"(c[0]), "=f"(c[1]), "=f"(c[2]), "=f"(c[3])
+      : "r"(a0), "r"(a1), "r"(a2), "r"(a3), "r"(b0), "r"(b1), "f"(z0), "f"(z1));
+}
+
+__device__ __forceinline__ uint32_t transpose8x8(uint32_t x) {
+  uint32_t y;
+  asm("movmatrix.sync.aligned.m8n8.trans.b16 %0, %1;" : "=r"(y) : "r"(x));
+  return y;
+}
+
+__device__ __forceinline__ uint32_t pack_f16x2(float lo, float hi) {
+  const __half2 h = __floats2half2_rn(lo, hi);
+  return *reinterpret_cast<const uint32_t*>(&h);
+}
+
+// Two fp16 numbers minus a constant (subnormals all: exact).
+__device__ __forceinline__ uint32_t minus8(uint32_t x, uint32_t c) {
+  uint32_t y;
+  asm("sub.f16x2 %0, %1, %2;" : "=r"(y) : "r"(x), "r"(c));
+  return y;
+}
+
+template <int N>
+__device__ __forceinline__ void lds(uint32_t (&w)[N], const void* p) {
+  if constexpr (N == 4) {
+    const uint4 x = *static_cast<const uint4*>(p);
+    w[0] = x.x;
+    w[1] = x.y;
+    w[2] = x.z;
+    w[3] = x.w;
+  } else if constexpr (N == 2) {
+    const uint2 x = *static_cast<const uint2*>(p);
+    w[0] = x.x;
+    w[1] = x.y;
+  } else {
+    w[0] = *static_cast<const uint32_t*>(p);
   }
 }
 
-__global__ void __launch_bounds__(256) fwd_weights_kernel(const __grid_constant__ Kv4FwdParams p) {
+// log2 of the largest finite scale of a key's groups, rounded down, kept
+// within +-100 (a key without one, all zeros or NaN, counts as the smallest).
+template <int W>
+__device__ __forceinline__ float scale_exponent(const uint32_t (&w)[W]) {
+  uint32_t m = 0;
+#pragma unroll
+  for (int i = 0; i < W; ++i) m = max(m, max(w[i] & 0xFFFFu, w[i] >> 16));
+  if (m >= 0x7F80u) {
+    m = 0;
+#pragma unroll
+    for (int i = 0; i < W; ++i) {
+      if ((w[i] & 0xFFFFu) < 0x7F80u) m = max(m, w[i] & 0xFFFFu);
+      if ((w[i] >> 16) < 0x7F80u) m = max(m, w[i] >> 16);
+    }
+  }
+  const int e = static_cast<int>(m >> 7) - 127;
+  return static_cast<float>(min(max(e, -100), 100));
+}
+
+// ------------------------------------------------------------------ results
+
+// Adds a row's sinks: (R, l) -> its logsumexp in log2 units and the factor of
+// the unnormalised output.
+__device__ __forceinline__ float finish_row(const Kv4FwdParams& p, int32_t h, float R, float l, float& factor) {
+  float lse2 = l == 0.f ? -INFINITY : R + log2f(l);
+  factor = l == 0.f ? 0.f : 1.f / l;
+  if (p.n_sinks > 0) {
+    const float* z = p.sinks + (p.sinks_kv ? h * p.n_sinks : 0);
+    float m = lse2;
+    for (int j = 0; j < p.n_sinks; ++j) m = fmaxf(m, z[j] * kLog2e);
+    float tot = lse2 == -INFINITY ? 0.f : ex2_approx(lse2 - m);
+    for (int j = 0; j < p.n_sinks; ++j) tot += ex2_approx(fmaf(z[j], kLog2e, -m));
+    const float all = m + log2f(tot);
+    if (l != 0.f) factor *= ex2_approx(lse2 - all);
+    lse2 = all;
+  }
+  return lse2;
+}
+
+// Row r (q head r / T of the group, token r % T) of pair bh.
+__device__ __forceinline__ int64_t lse_index(const Kv4FwdParams& p, int32_t bh, int32_t r) {
+  const int32_t b = bh / p.c.Hkv, hq = bh % p.c.Hkv * p.G + r / p.T;
+  return (static_cast<int64_t>(b) * p.Hq + hq) * p.T + r % p.T;
+}
+__device__ __forceinline__ __nv_bfloat16* o_row(const Kv4FwdParams& p, int32_t bh, int32_t r) {
+  const int32_t b = bh / p.c.Hkv, hq = bh % p.c.Hkv * p.G + r / p.T;
+  return p.o + b * p.os[0] + hq * p.os[1] + (r % p.T) * p.os[2];
+}
+
+__device__ __forceinline__ void store_o4(__nv_bfloat16* o, const float4& x, float f) {
+  *reinterpret_cast<uint2*>(o) = make_uint2(pack_bf16x2(x.x * f, x.y * f), pack_bf16x2(x.z * f, x.w * f));
+}
+
+__device__ __forceinline__ void compute_barrier() { asm volatile("bar.sync 1, %0;" ::"n"(32 * kWarps) : "memory"); }
+
+template <int D, int NT, bool kCap>
+__global__ void __launch_bounds__(kThreads, NT == 1 ? 2 : 1) kv4_fwd_kernel(const __grid_constant__ Kv4FwdParams p) {
+  extern __shared__ __align__(128) uint8_t smem_raw[];
+  using Sh = FwdShared<D, NT>;
+  Sh& s = *reinterpret_cast<Sh*>(smem_raw);
+  constexpr int kRows = Sh::kRows, kStages = Sh::kStages, kGroups = Kv4<D>::kGroups;
+  constexpr int kRowBytes = Kv4<D>::kRowBytes, kScaleBytes = Kv4<D>::kScaleBytes;
+  const int warp = warp_id(), lane = threadIdx.x & 31;
+  if (threadIdx.x == 0) {
+    s.abort_flag = 0;
+    for (int i = 0; i < kStages; ++i) {
+      mbar_init(&s.full[i], 1);
+      mbar_init(&s.empty[i], kWarps);
+    }
+    fence_mbar_init();
+  }
+  __syncthreads();
   griddep_launch_dependents();
   griddep_wait();
-  const int32_t bh = static_cast<int32_t>(blockIdx.y), b = bh / p.c.Hkv, h = bh % p.c.Hkv;
-  const int64_t j = static_cast<int64_t>(blockIdx.x) * 256 + threadIdx.x;
-  if (j >= p.c.capacity) return;
-  float w = 0.f;
-  for (int32_t r = 0; r < p.G * p.T; ++r) {
-    const int32_t t = r % p.T, hq = h * p.G + r / p.T;
-    if (j >= visible_end(p, b, t, nullptr)) continue;
-    const int64_t row = (static_cast<int64_t>(b) * p.Hq + hq) * p.T + t;
-    w += expf(p.scores[row * p.c.capacity + j] - p.lse[row]);
+  const WaitCtl wc{p.err, &s.abort_flag, p.wait_ns};
+  const int64_t total = total_tiles(p);
+  const int32_t n_cta = runs(p, total);
+  if (static_cast<int32_t>(blockIdx.x) >= n_cta) return;
+  Run run;
+  run.init(p, first_tile(blockIdx.x, total, n_cta), first_tile(blockIdx.x + 1, total, n_cta), warp == 0 ? p.err : nullptr);
+
+  // lane 0 of warp 0: the next tile of the run into its stage
+  uint32_t issued = 0;
+  auto load_next = [&]() -> bool {
+    if (s.ahead_tile >= s.ahead.k1) {
+      if (!s.ahead.next(p)) return true;
+      s.ahead_tile = s.ahead.k0;
+    }
+    const uint32_t st = issued % kStages;
+    if (issued >= static_cast<uint32_t>(kStages) && !mbar_wait(&s.empty[st], (issued / kStages - 1) & 1u, wc)) return false;
+    const int32_t kt = s.ahead_tile++;
+    const int64_t key = static_cast<int64_t>(s.ahead.bh) * p.c.capacity + static_cast<int64_t>(kt) * kTileKeys;
+    // whole sixteens of keys: the capacity is a multiple of 16
+    const uint32_t keys = static_cast<uint32_t>((min(s.ahead.pair.len - kt * kTileKeys, kTileKeys) + 15) & ~15);
+    mbar_arrive_expect_tx(&s.full[st], keys * 2 * (kRowBytes + kScaleBytes));
+    bulk_load(s.k[st], static_cast<const uint8_t*>(p.c.k_codes) + key * kRowBytes, keys * kRowBytes, &s.full[st]);
+    bulk_load(s.ks[st], static_cast<const uint8_t*>(p.c.k_scales) + key * kScaleBytes, keys * kScaleBytes, &s.full[st]);
+    bulk_load(s.v[st], static_cast<const uint8_t*>(p.c.v_codes) + key * kRowBytes, keys * kRowBytes, &s.full[st]);
+    bulk_load(s.vs[st], static_cast<const uint8_t*>(p.c.v_scales) + key * kScaleBytes, keys * kScaleBytes, &s.full[st]);
+    ++issued;
+    return true;
+  };
+  bool ok = true;
+  if (threadIdx.x == 0) {
+    s.ahead = run;
+    s.ahead.k1 = 0;
+    s.ahead_tile = 0;
+    for (int i = 0; ok && i < Sh::kAhead; ++i) ok = load_next();
   }
-  p.c.weights[bh * p.c.capacity + j] += w;
+  ok = __all_sync(0xffffffffu, ok);
+
+  // -------------------------------------------------- compute warps
+  const int g8 = lane >> 2, t4 = lane & 3;  // fragment row / column pair
+  // V rows of this lane: keys 2 t4, 2 t4 + 1 (+ 8), the one that lies in the
+  // other bank half first in lanes 2 and 3 (kv4.cuh), put right by the byte selectors
+  const int v_first = t4 >> 1;
+  const uint32_t sel_lo = v_first ? 0x1054u : 0x5410u, sel_hi = v_first ? 0x3276u : 0x7632u;
+  uint32_t n = 0;
+  bool first_part = true;
+  while (run.next(p)) {
+    const int32_t h = run.bh % p.c.Hkv;
+    const int64_t head = static_cast<int64_t>(run.bh) * p.row_tiles + run.rt;
+    // Q as fp16 operands, the start of K's accumulators, and per column its factor and last slot
+    uint32_t qb[NT][kGroups][4];
+    float init[NT][kGroups][2], qf[NT][2];
+    int32_t lim[NT][2];
+    int32_t lim_min = INT32_MAX, lim_max = 0;
+#pragma unroll
+    for (int nt = 0; nt < NT; ++nt) {
+      const int32_t r = run.rt * kRows + nt * 8 + g8;  // this lane's row while loading Q
+      const bool in = r < p.R;
+      const int32_t t = in ? r % p.T : 0;
+      uint4 raw[kGroups];
+      uint32_t mx = 0;
+#pragma unroll
+      for (int g = 0; g < kGroups; ++g) {
+        raw[g] = in ? *reinterpret_cast<const uint4*>(p.q + run.pair.b * p.qs[0] + (h * p.G + r / p.T) * p.qs[1] + t * p.qs[2] +
+                                                      32 * g + 8 * t4)
+                    : make_uint4(0, 0, 0, 0);
+        const uint32_t w[4] = {raw[g].x, raw[g].y, raw[g].z, raw[g].w};
+#pragma unroll
+        for (int i = 0; i < 4; ++i) mx = max(mx, max(w[i] & 0x7FFFu, (w[i] >> 16) & 0x7FFFu));
+      }
+      mx = max(mx, __shfl_xor_sync(0xffffffffu, mx, 1));
+      mx = max(mx, __shfl_xor_sync(0xffffffffu, mx, 2));
+      // power of two that brings the row's largest magnitude to [2^14, 2^15)
+      const int e = mx == 0 || mx >= 0x7F80u ? 0 : 14 + 127 - static_cast<int>(max(mx >> 7, 1u));
+      const float up = exp2f(static_cast<float>(e / 2)), up2 = exp2f(static_cast<float>(e - e / 2));
+      float sum[kGroups];
+#pragma unroll
+      for (int g = 0; g < kGroups; ++g) {
+        const uint32_t w[4] = {raw[g].x, raw[g].y, raw[g].z, raw[g].w};
+        float x[8];
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+          x[2 * i] = bf16_lo(w[i]) * up * up2;
+          x[2 * i + 1] = bf16_hi(w[i]) * up * up2 * 0.0625f;
+        }
+        sum[g] = 0.f;
+#pragma unroll
+        for (int st = 0; st < 2; ++st) {  // elements 2 st (+4) and 2 st + 1 (+4): see kv4.cuh
+          const __half2 even = __floats2half2_rn(x[2 * st], x[2 * st + 4]);
+          const __half2 odd = __floats2half2_rn(x[2 * st + 1], x[2 * st + 5]);
+          qb[nt][g][2 * st] = *reinterpret_cast<const uint32_t*>(&even);
+          qb[nt][g][2 * st + 1] = *reinterpret_cast<const uint32_t*>(&odd);
+          const float2 fe = __half22float2(even), fo = __half22float2(odd);
+          sum[g] += fe.x + fe.y + 16.f * (fo.x + fo.y);
+        }
+        sum[g] += __shfl_xor_sync(0xffffffffu, sum[g], 1);
+        sum[g] += __shfl_xor_sync(0xffffffffu, sum[g], 2);
+      }
+      const float f = p.scale_log2 * 16777216.f * exp2f(static_cast<float>(-e));
+      const int32_t last = in && t < run.pair.nq ? max(0, run.pair.len - run.pair.nq + t + 1) : 0;
+#pragma unroll
+      for (int i = 0; i < 2; ++i) {  // this lane's columns are rows 2 t4 and 2 t4 + 1
+        const int from = 4 * (2 * t4 + i);
+#pragma unroll
+        for (int g = 0; g < kGroups; ++g) init[nt][g][i] = __shfl_sync(0xffffffffu, sum[g], from) * (-8.f / 16777216.f);
+        qf[nt][i] = __shfl_sync(0xffffffffu, f, from);
+        lim[nt][i] = __shfl_sync(0xffffffffu, last, from);
+      }
+      const bool real = in;
+      int32_t lo = real ? last : INT32_MAX, hi = last;
+#pragma unroll
+      for (int o = 4; o < 32; o *= 2) {
+        lo = min(lo, __shfl_xor_sync(0xffffffffu, lo, o));
+        hi = max(hi, __shfl_xor_sync(0xffffffffu, hi, o));
+      }
+      lim_min = min(lim_min, lo);
+      lim_max = max(lim_max, hi);
+    }
+
+    float acc[NT][2 * kGroups][4];
+    float R[NT][2], l[NT][2];
+#pragma unroll
+    for (int nt = 0; nt < NT; ++nt) {
+#pragma unroll
+      for (int j = 0; j < 2 * kGroups; ++j)
+#pragma unroll
+        for (int i = 0; i < 4; ++i) acc[nt][j][i] = 0.f;
+      R[nt][0] = R[nt][1] = -INFINITY;
+      l[nt][0] = l[nt][1] = 0.f;
+    }
+
+    for (int32_t kt = run.k0; kt < run.k1; ++kt, ++n) {
+      const uint32_t st = n % kStages;
+      // (after a wait that ran out the loop goes on without waiting, on whatever
+      // the stages hold: the barriers between the warps stay matched)
+      if (threadIdx.x == 0 && ok) ok = load_next();
+      ok = __all_sync(0xffffffffu, ok);
+      if (ok) ok = mbar_wait_warp(&s.full[st], (n / kStages) & 1u, wc);
+      const int32_t key0 = kt * kTileKeys + warp * 16;
+      if (key0 < lim_max) {
+        const bool all_seen = key0 + 16 <= lim_min;
+        // ---- scores
+        uint32_t ka[kGroups], kb[kGroups], sa[kGroups / 2], sb[kGroups / 2];
+        const uint8_t* krow = s.k[st] + (warp * 16 + g8) * kRowBytes + t4 * (kRowBytes / 4);
+        lds(ka, krow);
+        lds(kb, krow + 8 * kRowBytes);
+        const uint8_t* srow = s.ks[st] + (warp * 16 + g8) * kScaleBytes;
+        lds(sa, srow);
+        lds(sb, srow + 8 * kScaleBytes);
+        float x[NT][4];
+#pragma unroll
+        for (int nt = 0; nt < NT; ++nt)
+#pragma unroll
+          for (int i = 0; i < 4; ++i) x[nt][i] = 0.f;
+#pragma unroll
+        for (int g = 0; g < kGroups; ++g) {
+          const float fa = g & 1 ? bf16_hi(sa[g / 2]) : bf16_lo(sa[g / 2]);
+          const float fb = g & 1 ? bf16_hi(sb[g / 2]) : bf16_lo(sb[g / 2]);
+#pragma unroll
+          for (int nt = 0; nt < NT; ++nt) {
+            float c[4];
+            mma_f16_from(c, ka[g] & 0x000F000Fu, kb[g] & 0x000F000Fu, ka[g] & 0x00F000F0u, kb[g] & 0x00F000F0u,
+                         qb[nt][g][0], qb[nt][g][1], init[nt][g][0], init[nt][g][1]);
+            const uint32_t a8 = ka[g] >> 8, b8 = kb[g] >> 8;
+            mma_f16(c, a8 & 0x000F000Fu, b8 & 0x000F000Fu, a8 & 0x00F000F0u, b8 & 0x00F000F0u, qb[nt][g][2], qb[nt][g][3]);
+            x[nt][0] = fmaf(fa, c[0], x[nt][0]);
+            x[nt][1] = fmaf(fa, c[1], x[nt][1]);
+            x[nt][2] = fmaf(fb, c[2], x[nt][2]);
+            x[nt][3] = fmaf(fb, c[3], x[nt][3]);
+          }
+        }
+        // ---- softmax
+        uint32_t va[kGroups / 2], vb[kGroups / 2];
+        const uint8_t* vsrow = s.vs[st] + (warp * 16 + g8) * kScaleBytes;
+        lds(va, vsrow);
+        lds(vb, vsrow + 8 * kScaleBytes);
+        const float ea = scale_exponent(va), eb = scale_exponent(vb);
+        uint32_t pb[NT][kGroups][2];
+#pragma unroll
+        for (int nt = 0; nt < NT; ++nt) {
+#pragma unroll
+          for (int i = 0; i < 4; ++i) {
+            x[nt][i] *= qf[nt][i & 1];
+            if constexpr (kCap) x[nt][i] = p.cap_log2 * tanh_fast(x[nt][i]);
+          }
+          if (!all_seen) {
+#pragma unroll
+            for (int i = 0; i < 4; ++i)
+              if (key0 + g8 + (i >> 1) * 8 >= lim[nt][i & 1]) x[nt][i] = -INFINITY;
+          }
+          if (p.scores) {
+            float* out = p.scores + (head * p.c.capacity + key0 + g8) * p.score_stride + nt * 8 + 2 * t4;
+            if (nt * 8 + 2 * t4 < p.score_stride) {
+              *reinterpret_cast<float2*>(out) = make_float2(x[nt][0], x[nt][1]);
+              *reinterpret_cast<float2*>(out + 8 * p.score_stride) = make_float2(x[nt][2], x[nt][3]);
+            }
+          }
+          float pr[4];
+#pragma unroll
+          for (int i = 0; i < 2; ++i) {
+            float m = fmaxf(x[nt][i] + ea, x[nt][i + 2] + eb);
+#pragma unroll
+            for (int o = 4; o < 32; o *= 2) m = fmaxf(m, __shfl_xor_sync(0xffffffffu, m, o));
+            const bool move = m > R[nt][i] + kRescale;
+            if (__any_sync(0xffffffffu, move)) {
+              // (uniform over the lanes of a column)
+              const float to = move ? m : R[nt][i];
+              const float f = R[nt][i] == -INFINITY ? 0.f : ex2_approx(R[nt][i] - to);
+              R[nt][i] = to;
+              l[nt][i] *= f;
+#pragma unroll
+              for (int j = 0; j < 2 * kGroups; ++j) {
+                acc[nt][j][i] *= f;
+                acc[nt][j][i + 2] *= f;
+              }
+            }
+            const float ref = R[nt][i] == -INFINITY ? 0.f : R[nt][i];
+            pr[i] = ex2_approx(x[nt][i] - ref);
+            pr[i + 2] = ex2_approx(x[nt][i + 2] - ref);
+            l[nt][i] += pr[i] + pr[i + 2];
+          }
+          // probabilities times value scales, transposed into the second product's operand
+#pragma unroll
+          for (int g = 0; g < kGroups; ++g) {
+            const float fa = g & 1 ? bf16_hi(va[g / 2]) : bf16_lo(va[g / 2]);
+            const float fb = g & 1 ? bf16_hi(vb[g / 2]) : bf16_lo(vb[g / 2]);
+            float w[4] = {pr[0] * fa, pr[1] * fa, pr[2] * fb, pr[3] * fb};
+            if (!all_seen) {  // (an unseen slot's scale may be anything)
+#pragma unroll
+              for (int i = 0; i < 4; ++i)
+                if (x[nt][i] == -INFINITY) w[i] = 0.f;
+            }
+            pb[nt][g][0] = transpose8x8(pack_f16x2(w[0], w[1]));
+            pb[nt][g][1] = transpose8x8(pack_f16x2(w[2], w[3]));
+          }
+        }
+        // ---- output
+        uint32_t v0[kGroups / 2], v1[kGroups / 2], v8[kGroups / 2], v9[kGroups / 2];
+        const int piece = D == 128 ? g8 ^ ((t4 & 1) << 2) : g8;
+        const uint8_t* vrow = s.v[st] + (warp * 16 + 2 * t4) * kRowBytes + piece * (kRowBytes / 8);
+        lds(v0, vrow + v_first * kRowBytes);
+        lds(v1, vrow + (v_first ^ 1) * kRowBytes);
+        lds(v8, vrow + (8 + v_first) * kRowBytes);
+        lds(v9, vrow + (8 + (v_first ^ 1)) * kRowBytes);
+#pragma unroll
+        for (int g = 0; g < kGroups; ++g) {
+          const uint32_t sel = g & 1 ? sel_hi : sel_lo;
+          const uint32_t lo = __byte_perm(v0[g / 2], v1[g / 2], sel), hi = __byte_perm(v8[g / 2], v9[g / 2], sel);
+          // elements 4 g8 + 0..3 of the group: rows g8 and (times 16) g8 + 8 of two products
+          const uint32_t a0 = minus8(lo & 0x000F000Fu, 0x00080008u), a1 = minus8(lo & 0x00F000F0u, 0x00800080u);
+          const uint32_t a2 = minus8(hi & 0x000F000Fu, 0x00080008u), a3 = minus8(hi & 0x00F000F0u, 0x00800080u);
+          const uint32_t lo8 = lo >> 8, hi8 = hi >> 8;
+          const uint32_t c0 = minus8(lo8 & 0x000F000Fu, 0x00080008u), c1 = minus8(lo8 & 0x00F000F0u, 0x00800080u);
+          const uint32_t c2 = minus8(hi8 & 0x000F000Fu, 0x00080008u), c3 = minus8(hi8 & 0x00F000F0u, 0x00800080u);
+#pragma unroll
+          for (int nt = 0; nt < NT; ++nt) {
+            mma_f16(acc[nt][2 * g], a0, a1, a2, a3, pb[nt][g][0], pb[nt][g][1]);
+            mma_f16(acc[nt][2 * g + 1], c0, c1, c2, c3, pb[nt][g][0], pb[nt][g][1]);
+          }
+        }
+      }
+      __syncwarp();
+      if (lane == 0) mbar_arrive(&s.empty[st]);
+    }
+
+    // ---- the eight warps' parts into one
+#pragma unroll
+    for (int nt = 0; nt < NT; ++nt)
+#pragma unroll
+      for (int i = 0; i < 2; ++i) {
+#pragma unroll
+        for (int o = 4; o < 32; o *= 2) l[nt][i] += __shfl_xor_sync(0xffffffffu, l[nt][i], o);
+        if (g8 == 0) {
+          s.stat[0][warp][nt * 8 + 2 * t4 + i] = R[nt][i];
+          s.stat[1][warp][nt * 8 + 2 * t4 + i] = l[nt][i];
+        }
+      }
+    compute_barrier();
+    float4 mine[NT][2][kGroups];
+#pragma unroll
+    for (int nt = 0; nt < NT; ++nt)
+#pragma unroll
+      for (int i = 0; i < 2; ++i) {
+        float m = -INFINITY;
+#pragma unroll
+        for (int w = 0; w < kWarps; ++w) m = fmaxf(m, s.stat[0][w][nt * 8 + 2 * t4 + i]);
+        const float f = R[nt][i] == -INFINITY ? (l[nt][i] == 0.f ? 0.f : 1.f) : ex2_approx(R[nt][i] - m);
+        const float f24 = f * 16777216.f;
+#pragma unroll
+        for (int g = 0; g < kGroups; ++g) {
+          mine[nt][i][g] = make_float4(acc[nt][2 * g][i] * f24, acc[nt][2 * g][i + 2] * (f24 * 0.0625f),
+                                       acc[nt][2 * g + 1][i] * f24, acc[nt][2 * g + 1][i + 2] * (f24 * 0.0625f));
+        }
+      }
+    auto slot = [&](int nt, int i, int g) -> float4* {
+      return reinterpret_cast<float4*>(&s.merge[warp & 3][(nt * 8 + 2 * t4 + i) * Sh::kPad + 32 * g + 4 * g8]);
+    };
+    if (warp >= 4) {
+#pragma unroll
+      for (int nt = 0; nt < NT; ++nt)
+#pragma unroll
+        for (int i = 0; i < 2; ++i)
+#pragma unroll
+          for (int g = 0; g < kGroups; ++g) *slot(nt, i, g) = mine[nt][i][g];
+    }
+    compute_barrier();
+    if (warp < 4) {
+#pragma unroll
+      for (int nt = 0; nt < NT; ++nt)
+#pragma unroll
+        for (int i = 0; i < 2; ++i)
+#pragma unroll
+          for (int g = 0; g < kGroups; ++g) {
+            float4* at = slot(nt, i, g);
+            const float4 a = *at, b = mine[nt][i][g];
+            *at = make_float4(a.x + b.x, a.y + b.y, a.z + b.z, a.w + b.w);
+          }
+    }
+    compute_barrier();
+    const int32_t rec = 2 * static_cast<int32_t>(blockIdx.x) + (first_part ? 0 : 1);
+    for (int idx = threadIdx.x; idx < kRows * D / 4; idx += 32 * kWarps) {
+      const int row = idx / (D / 4), d = idx % (D / 4) * 4;
+      float m = -INFINITY, L = 0.f;
+#pragma unroll
+      for (int w = 0; w < kWarps; ++w) m = fmaxf(m, s.stat[0][w][row]);
+#pragma unroll
+      for (int w = 0; w < kWarps; ++w)
+        if (s.stat[1][w][row] != 0.f) L += s.stat[1][w][row] * (m == -INFINITY ? 1.f : ex2_approx(s.stat[0][w][row] - m));
+      float4 x = make_float4(0.f, 0.f, 0.f, 0.f);
+#pragma unroll
+      for (int w = 0; w < 4; ++w) {
+        const float4 y = *reinterpret_cast<const float4*>(&s.merge[w][row * Sh::kPad + d]);
+        x.x += y.x;
+        x.y += y.y;
+        x.z += y.z;
+        x.w += y.w;
+      }
+      if (run.whole) {
+        const int32_t r = run.rt * kRows + row;
+        if (r < p.R) {
+          float f;
+          const float lse2 = finish_row(p, h, m, L, f);
+          store_o4(o_row(p, run.bh, r) + d, x, f);
+          if (d == 0) p.lse[lse_index(p, run.bh, r)] = lse2 * kLn2;
+        }
+      } else {
+        *reinterpret_cast<float4*>(p.rec_o + (static_cast<int64_t>(rec) * kRows + row) * D + d) = x;
+        if (d == 0) {
+          p.rec_stat[rec * 2 * kRows + row] = m;
+          p.rec_stat[rec * 2 * kRows + kRows + row] = L;
+        }
+      }
+    }
+    first_part = false;
+  }
+  if (threadIdx.x == 0 && !ok) {  // let the copies in flight land before the CTA exits
+    uint32_t dummy_abort = 0;
+    WaitCtl dw{nullptr, &dummy_abort, p.wait_ns};
+    for (uint32_t i = issued > kStages ? issued - kStages : 0; i < issued; ++i)
+      (void)mbar_wait(&s.full[i % kStages], (i / kStages) & 1u, dw);
+  }
+}
+
+// The records of pair `hr` (b, h, row tile) of sequence b: those of CTAs c0 ..
+// c1, a CTA's being its first part unless its run began in an earlier pair.
+struct Records {
+  int32_t c0, c1, n;
+  int64_t begin, total;
+  int32_t tiles;
+};
+
+__device__ __forceinline__ Records pair_records(const Kv4FwdParams& p, int32_t bh, int32_t rt) {
+  Records x;
+  const int32_t b = bh / p.c.Hkv, h = bh % p.c.Hkv;
+  x.total = total_tiles(p);
+  x.n = runs(p, x.total);
+  x.tiles = load_pair(p, b, nullptr).tiles;
+  x.begin = tiles_before(p, b) + (static_cast<int64_t>(h) * p.row_tiles + rt) * x.tiles;
+  x.c0 = x.c1 = 0;
+  if (x.tiles > 0) {
+    x.c0 = cta_of(x.begin, x.total, x.n);
+    x.c1 = cta_of(x.begin + x.tiles - 1, x.total, x.n);
+  }
+  return x;
+}
+
+__device__ __forceinline__ int32_t record_of(const Records& x, int32_t c) {
+  return 2 * c + (first_tile(c, x.total, x.n) < x.begin ? 1 : 0);
+}
+
+template <int D, int NT>
+__global__ void __launch_bounds__(256) kv4_join_kernel(const __grid_constant__ Kv4FwdParams p) {
+  constexpr int kRows = 8 * NT;
+  constexpr int kVec = D / 4;           // lanes (float4) of one row
+  constexpr int kSplit = 256 / kVec;    // records read side by side
+  __shared__ float4 part[kSplit][kVec];
+  __shared__ float lse2[kRows];
+  griddep_launch_dependents();
+  griddep_wait();
+  if (static_cast<int32_t>(blockIdx.x) < p.join_rows) {
+    // ---- merge the records of one row
+    const int32_t row = static_cast<int32_t>(blockIdx.x) % kRows;
+    const int32_t hr = static_cast<int32_t>(blockIdx.x) / kRows;
+    const int32_t rt = hr % p.row_tiles, bh = hr / p.row_tiles, r = rt * kRows + row;
+    if (r >= p.R) return;
+    const Records x = pair_records(p, bh, rt);
+    if (x.tiles > 0 && x.c0 == x.c1) return;  // one CTA had all of it
+    const int lane = threadIdx.x % kVec, sub = threadIdx.x / kVec;
+    float m = -INFINITY, L = 0.f;
+    float4 o = make_float4(0.f, 0.f, 0.f, 0.f);
+    if (x.tiles > 0) {
+      for (int32_t c = x.c0; c <= x.c1; ++c) m = fmaxf(m, p.rec_stat[record_of(x, c) * 2 * kRows + row]);
+      for (int32_t c = x.c0; c <= x.c1; ++c) {
+        const float* st = p.rec_stat + record_of(x, c) * 2 * kRows + row;
+        const float w = m == -INFINITY ? 1.f : ex2_approx(st[0] - m);
+        if (st[kRows] != 0.f) L += st[kRows] * w;
+        if ((c - x.c0) % kSplit != sub || st[kRows] == 0.f) continue;
+        const float4 y = *reinterpret_cast<const float4*>(p.rec_o + (static_cast<int64_t>(record_of(x, c)) * kRows + row) * D + 4 * lane);
+        o.x = fmaf(y.x, w, o.x);
+        o.y = fmaf(y.y, w, o.y);
+        o.z = fmaf(y.z, w, o.z);
+        o.w = fmaf(y.w, w, o.w);
+      }
+    }
+    part[sub][lane] = o;
+    __syncthreads();
+    if (sub == 0) {
+      for (int i = 1; i < kSplit; ++i) {
+        const float4 y = part[i][lane];
+        o.x += y.x;
+        o.y += y.y;
+        o.z += y.z;
+        o.w += y.w;
+      }
+      float f;
+      const float all = finish_row(p, bh % p.c.Hkv, m, L, f);
+      store_o4(o_row(p, bh, r) + 4 * lane, o, f);
+      if (lane == 0) p.lse[lse_index(p, bh, r)] = all * kLn2;
+    }
+    return;
+  }
+  // ---- scores into probabilities, added to the keys' weights: 256 slots of one head
+  const int64_t blk = static_cast<int64_t>(blockIdx.x) - p.join_rows;
+  const int32_t chunks = static_cast<int32_t>((p.c.capacity + 255) / 256);
+  const int32_t bh = static_cast<int32_t>(blk / chunks);
+  const int32_t slot = static_cast<int32_t>(blk % chunks) * 256 + static_cast<int32_t>(threadIdx.x);
+  const Pair pair = load_pair(p, bh / p.c.Hkv, nullptr);
+  if (static_cast<int32_t>(blk % chunks) * 256 >= pair.len || pair.nq == 0) return;
+  float w = 0.f;
+  for (int32_t rt = 0; rt < p.row_tiles; ++rt) {
+    const Records x = pair_records(p, bh, rt);
+    __syncthreads();
+    if (threadIdx.x < kRows) {
+      const int32_t r = rt * kRows + threadIdx.x;
+      float R = -INFINITY, L = 0.f, f;
+      if (r < p.R && x.c0 != x.c1) {
+        for (int32_t c = x.c0; c <= x.c1; ++c) R = fmaxf(R, p.rec_stat[record_of(x, c) * 2 * kRows + threadIdx.x]);
+        for (int32_t c = x.c0; c <= x.c1; ++c) {
+          const float* st = p.rec_stat + record_of(x, c) * 2 * kRows + threadIdx.x;
+          if (st[kRows] != 0.f) L += st[kRows] * (R == -INFINITY ? 1.f : ex2_approx(st[0] - R));
+        }
+        lse2[threadIdx.x] = finish_row(p, bh % p.c.Hkv, R, L, f);
+      } else {
+        lse2[threadIdx.x] = r < p.R ? p.lse[lse_index(p, bh, r)] * kLog2e : INFINITY;
+      }
+    }
+    __syncthreads();
+    if (slot < pair.len) {
+      const float* sc = p.scores + ((static_cast<int64_t>(bh) * p.row_tiles + rt) * p.c.capacity + slot) * p.score_stride;
+      const int32_t rows = min(kRows, p.R - rt * kRows);
+      for (int32_t i = 0; i < rows; ++i) {
+        const int32_t t = (rt * kRows + i) % p.T;
+        if (t < pair.nq && slot < pair.len - pair.nq + t + 1) w += ex2_approx(sc[i] - lse2[i]);
+      }
+    }
+  }
+  if (slot < pair.len) p.c.weights[static_cast<int64_t>(bh) * p.c.capacity + slot] += w;
+}
+
+// Sizes of a call that both the workspace query and the launch use.
+struct Plan {
+  int NT, rows, row_tiles, n_cta, stride;
+  size_t stat_bytes, o_bytes, score_bytes;
+};
+
+Plan make_plan(const bsa_kv4_fwd_args* a) {
+  Plan x;
+  const int64_t R = static_cast<int64_t>(a->Hq / a->cache.Hkv) * a->T;
+  x.NT = R <= 8 ? 1 : 2;
+  x.rows = 8 * x.NT;
+  x.row_tiles = static_cast<int>((R + x.rows - 1) / x.rows);
+  const int64_t most = static_cast<int64_t>(a->cache.B) * a->cache.Hkv * x.row_tiles * ((a->cache.capacity + kTileKeys - 1) / kTileKeys);
+  x.n_cta = static_cast<int>(std::min<int64_t>(most, static_cast<int64_t>(num_sms()) * (x.NT == 1 ? 2 : 1)));
+  x.stride = static_cast<int>((std::min<int64_t>(R, x.rows) + 1) & ~int64_t(1));
+  x.stat_bytes = static_cast<size_t>(2 * x.n_cta) * 2 * x.rows * sizeof(float);
+  x.o_bytes = static_cast<size_t>(2 * x.n_cta) * x.rows * a->cache.D * sizeof(float);
+  x.score_bytes = a->accumulate ? static_cast<size_t>(a->cache.B) * a->cache.Hkv * x.row_tiles * a->cache.capacity * x.stride * sizeof(float) : 0;
+  return x;
+}
+
+template <int D, int NT>
+bsa_status launch(const Kv4FwdParams& p, int accumulate, cudaStream_t stream) {
+  auto kern = p.cap_log2 > 0.f ? kv4_fwd_kernel<D, NT, true> : kv4_fwd_kernel<D, NT, false>;
+  const size_t smem = sizeof(FwdShared<D, NT>);
+  const bsa_status st = ensure_smem_attr(reinterpret_cast<const void*>(kern), smem, "set kv4 forward smem size");
+  if (st != BSA_OK) return st;
+  cudaError_t e = launch_kernel(kern, dim3(p.n_cta), dim3(kThreads), smem, stream, p);
+  if (e == cudaSuccess) e = cudaGetLastError();
+  if (e != cudaSuccess) return cuda_fail(e, "kv4 forward launch");
+  const int64_t chunks = accumulate ? (p.c.capacity + 255) / 256 * p.c.B * p.c.Hkv : 0;
+  e = launch_kernel(kv4_join_kernel<D, NT>, dim3(static_cast<unsigned>(p.join_rows + chunks)), dim3(256), 0, stream, p);
+  if (e == cudaSuccess) e = cudaGetLastError();
+  if (e != cudaSuccess) return cuda_fail(e, "kv4 join launch");
+  return BSA_OK;
 }
 
 }  // namespace
 
 size_t kv4_fwd_workspace_bytes(const bsa_kv4_fwd_args* a) {
-  return static_cast<size_t>(a->cache.B) * a->Hq * a->T * a->cache.capacity * sizeof(float);
+  const Plan x = make_plan(a);
+  return x.stat_bytes + x.o_bytes + x.score_bytes;
 }
 
 bsa_status kv4_fwd_launch(const bsa_kv4_fwd_args* a, float scale, cudaStream_t stream) {
+  const Plan x = make_plan(a);
   Kv4FwdParams p{};
   p.c = a->cache;
   p.q = static_cast<const __nv_bfloat16*>(a->q);
@@ -134,29 +862,26 @@ bsa_status kv4_fwd_launch(const bsa_kv4_fwd_args* a, float scale, cudaStream_t s
   p.Hq = a->Hq;
   p.T = static_cast<int32_t>(a->T);
   p.G = a->Hq / a->cache.Hkv;
+  p.R = p.G * p.T;
+  p.row_tiles = x.row_tiles;
   p.lens = a->lens;
   p.q_lens = a->q_lens;
-  p.scale = scale;
-  p.cap = a->logits_soft_cap;
+  p.scale_log2 = a->logits_soft_cap > 0.f ? scale / a->logits_soft_cap : scale * kLog2e;
+  p.cap_log2 = a->logits_soft_cap > 0.f ? a->logits_soft_cap * kLog2e : 0.f;
   p.sinks = a->sinks;
   p.n_sinks = a->num_sinks;
   p.sinks_kv = a->sinks_per_kv_head ? 1 : 0;
-  p.accumulate = a->accumulate;
-  p.scores = static_cast<float*>(a->workspace);
+  p.n_cta = x.n_cta;
+  p.rec_stat = static_cast<float*>(a->workspace);
+  p.rec_o = p.rec_stat + x.stat_bytes / sizeof(float);
+  p.scores = a->accumulate ? p.rec_o + x.o_bytes / sizeof(float) : nullptr;
+  p.score_stride = x.stride;
+  p.join_rows = a->cache.B * a->cache.Hkv * x.row_tiles * x.rows;
   p.err = device_error_word();
+  p.wait_ns = wait_limit_ns();
   if (!p.err) return fail(BSA_ERR_CUDA, "could not allocate the device error word");
-  const unsigned rows = static_cast<unsigned>(a->cache.B) * a->Hq * static_cast<unsigned>(a->T);
-  cudaError_t e = a->cache.D == 128 ? launch_kernel(fwd_rows_kernel<128>, dim3(rows), dim3(256), 0, stream, p)
-                                    : launch_kernel(fwd_rows_kernel<64>, dim3(rows), dim3(256), 0, stream, p);
-  if (e == cudaSuccess) e = cudaGetLastError();
-  if (e != cudaSuccess) return cuda_fail(e, "kv4 forward launch");
-  if (a->accumulate) {
-    e = launch_kernel(fwd_weights_kernel, dim3(static_cast<unsigned>((a->cache.capacity + 255) / 256), a->cache.B * a->cache.Hkv),
-                      dim3(256), 0, stream, p);
-    if (e == cudaSuccess) e = cudaGetLastError();
-    if (e != cudaSuccess) return cuda_fail(e, "kv4 weights launch");
-  }
-  return BSA_OK;
+  if (a->cache.D == 128) return x.NT == 1 ? launch<128, 1>(p, a->accumulate, stream) : launch<128, 2>(p, a->accumulate, stream);
+  return x.NT == 1 ? launch<64, 1>(p, a->accumulate, stream) : launch<64, 2>(p, a->accumulate, stream);
 }
 
 }  // namespace bsa
