@@ -3,24 +3,32 @@
 // The loop is the dK/dV launch's: a tile is a key block of one key head, its
 // items the non-empty query blocks of each q head's row of the dkv MaskInfo.
 //
-// Per item one 128 x 128 x D product and 128^2 exponentials.  Queries are the
-// product's M side (tensor-memory lanes), keys its columns: a row's logsumexp
-// is then one register of a thread, and the sum over the queries stays in 32
-// registers per thread (one per key column) until the tile ends, when the
-// lanes are summed once.
+// Per item one 128 x 128 x D product and 128^2 exponentials.  Keys are the
+// product's M side (tensor-memory lanes), queries its columns, so a thread sums
+// its key's probabilities in registers and a warpgroup can take a whole item:
+// four warpgroups on four items in turn, each at another point of its item,
+// keep the exponential unit busy through one another's waits.  (Queries as the
+// M side leave 64 sums per thread, which forces the warpgroups onto one item
+// together: they then wait, load and compute in step, 283 us on GQA 32/8 causal
+// 8192 against the figure below.)
 //
 // One persistent CTA per SM, warp-specialised:
-//   warp 0      walks MaskInfo; loads K per tile (2 buffers), Q per item (4
-//               stages) and its logsumexp, and publishes the items and the
-//               ends of tiles in a ring
-//   warp 1      tcgen05 issuer: S = Q K^T into one of four tensor-memory buffers
-//   warp 2      adds up the warps' column sums at a tile's end and writes them
-//   warps 4-19  exponentials: warp (part, quarter) takes 32 lanes x 32 columns
+//   warp 0      walks MaskInfo, 32 cells of a row at a time, and publishes the
+//               items in a ring, several at once
+//   warps 1-2   tcgen05 issuers of the even and the odd items: S^T = K Q^T into
+//               one of four tensor-memory buffers (one issuer needs ~1,100
+//               cycles an item, most of it barrier latency)
+//   warp 3      one lane loads K per tile (2 buffers), Q per item (4 stages) and
+//               the item's exponent terms (8)
+//   warps 4-19  exponentials: warpgroup n % 4 takes item n
 // All items of the launch form one sequence, cut into equal runs, one per CTA
 // (the host computes the cuts from MaskInfo's row lengths and passes them as
-// kernel parameters: no schedule to upload).  A tile that two or more CTAs
-// share leaves one partial row per CTA in the workspace, and a second kernel
-// adds these up in CTA order.
+// kernel parameters: no schedule to upload).  A first kernel turns the
+// logsumexp into exponent terms (-lse log2 e, -inf for what is not counted):
+// the producer lane, at ~1,100 cycles an item, set the pace while the terms
+// were made beside it.  Each warpgroup leaves a row of
+// sums per tile and CTA in the workspace, and a second kernel adds these up in
+// order.
 #include <cmath>
 
 #include "internal.h"
@@ -31,34 +39,37 @@
 namespace bsa {
 namespace {
 
-constexpr int kBufs = 4;        // Q stages and score buffers (an item's have the same index)
-constexpr int kRing = 8;        // entries (items and tile ends) between the walker and the others
-constexpr int kParts = 4;       // warpgroups of the exponentials, 32 columns each
-constexpr int kEwWarps = 4 * kParts;
+constexpr int kBufs = 4;        // Q stages, score buffers, warpgroups of the exponentials (item n: n % 4)
+constexpr int kRing = 32;       // items between the walker and the producer
+constexpr int kBatch = 16;      // items published at once
+constexpr int kTerms = 8;       // column terms and descriptions of items between the producer and the exponentials
+constexpr int kEwWarps = 4 * kBufs;
 constexpr int kThreads = 128 + 32 * kEwWarps;
-constexpr uint32_t kRingReaders = 2 + kEwWarps;
 constexpr int kMaxCtas = 160;
+constexpr uint32_t kHidden = 0xFFFFDEADu;  // (a NaN no product gives) mark of an unseen score under a cap
 constexpr float kLog2e = 1.4426950408889634f;
 
-// flags of an entry, beside its column (bits 0-15) and label (16-17)
-constexpr uint32_t kFirst = 1u << 20;    // first item of its part of a tile
-constexpr uint32_t kMask = 1u << 21;     // some pairs of the item are not visible
-constexpr uint32_t kTileEnd = 1u << 22;  // end of a part: y = output row, z = the part had items, w = partial slot + 1 or 0
-constexpr uint32_t kEnd = 1u << 23;
+// flags of an item, beside its column (bits 0-15) and label (16-17)
+constexpr uint32_t kFirst = 1u << 20;  // first item of its part of a tile
+constexpr uint32_t kMask = 1u << 21;   // some pairs of the item are not visible
+constexpr uint32_t kEnd = 1u << 22;    // no item: the run has ended
 
 template <int D>
 struct __align__(1024) KwSmem {
   static constexpr int kTileBytes = 128 * D * 2;
   uint8_t k[2][kTileBytes];
   uint8_t q[kBufs][kTileBytes];
-  float lse[kRing][128];
-  float red[2][4][128];  // [tile parity][quarter][key]
+  float term[kTerms][128];   // minus the logsumexp of the item's queries, log2 units (-inf: not counted)
+  // {column | label << 16 | flags, stack slot, part of the run (tile - first tile), end of the counted queries}
   uint4 entry[kRing];
+  uint2 rows[kRing];         // {Q row, K row}
+  uint4 item[kTerms];        // the entries, handed on
+  uint32_t q_info[kBufs];    // for the issuers: flags, bits 0-7 the K buffer, 8-15 the parity of its load
   uint64_t ring_full[kRing], ring_empty[kRing];
-  uint64_t q_full[kBufs], s_full[kBufs], s_empty[kBufs];  // s_full also frees the Q stage
-  uint64_t k_full[2], k_empty[2];
-  uint64_t red_full[2], red_empty[2];
-  uint64_t drain;
+  uint64_t term_full[kTerms], term_empty[kTerms];
+  uint64_t q_full[kBufs], s_full[kBufs], s_empty[kBufs];  // s_full also frees the Q stage (and, at last, K)
+  uint64_t k_full[2];
+  uint64_t drain[2];
   uint32_t tmem_base, abort_flag;
 };
 static_assert(sizeof(KwSmem<128>) + 1024 <= 232448, "key weights shared memory exceeds 227 KB per CTA");
@@ -75,8 +86,10 @@ struct KwParams {
   float cap_log2;
   const float* lse;
   const int32_t* q_lens;
+  float* terms;    // [B, Hq, Sq]
   float* out;
-  float* partial;  // [n_cta][2][128]
+  float* sums;     // [n_tiles + 2 n_cta][4][128]: a whole tile's sums of each warpgroup, then the first and last parts' of each CTA
+  int32_t n_tiles;
   MaskInfoDev mi;
   int32_t compact;  // rows hold their non-empty blocks first
   int32_t n_cta;
@@ -99,6 +112,111 @@ __device__ __forceinline__ int32_t query_end(const KwParams& p, int32_t b) {
   return p.q_lens ? min(max(p.q_lens[b], 0), static_cast<int32_t>(p.Sq)) : static_cast<int32_t>(p.Sq);
 }
 
+// The row of sums of CTA c's part of tile t: the tile's own if c has all of it.
+__device__ __forceinline__ int32_t sums_row(const KwParams& p, int32_t c, int32_t t) {
+  const Cut a = p.cut[c], b = p.cut[c + 1];
+  const bool whole = !(t == a.tile && a.skip > 0) && !(t == b.tile && b.skip > 0);
+  return whole ? t : p.n_tiles + 2 * c + (t == a.tile ? 0 : 1);
+}
+
+// Whether three barriers' phases are complete (one test's latency, not three).
+__device__ __forceinline__ bool all_complete(uint32_t a, uint32_t pa, uint32_t b, uint32_t pb, uint32_t c, uint32_t pc) {
+  uint32_t ok;
+  asm volatile(
+      "{\n\t.reg .pred p, q, r;\n\t"
+      "mbarrier.test_wait.parity.shared::cta.b64 p, [%1], %2;\n\t"
+      "mbarrier.test_wait.parity.shared::cta.b64 q, [%3], %4;\n\t"
+      "mbarrier.test_wait.parity.shared::cta.b64 r, [%5], %6;\n\t"
+      "and.pred p, p, q;\n\t"
+      "and.pred p, p, r;\n\t"
+      "selp.u32 %0, 1, 0, p;\n\t}"
+      : "=r"(ok)
+      : "r"(a), "r"(pa), "r"(b), "r"(pb), "r"(c), "r"(pc)
+      : "memory");
+  return ok != 0u;
+}
+
+// Exponent terms of all queries: -lse in log2 units; -inf for a query that is
+// padding or sees nothing.
+__global__ void __launch_bounds__(256) key_weights_terms(const __grid_constant__ KwParams p) {
+  griddep_launch_dependents();
+  griddep_wait();
+  const int64_t i = (static_cast<int64_t>(blockIdx.x) * 256 + threadIdx.x) * 4;
+  if (i >= static_cast<int64_t>(p.B) * p.Hq * p.Sq) return;
+  const float4 l = *reinterpret_cast<const float4*>(p.lse + i);
+  const int32_t b = static_cast<int32_t>(i / (p.Hq * p.Sq)), q = static_cast<int32_t>(i % p.Sq);
+  const int32_t end = query_end(p, b);
+  float t[4] = {l.x, l.y, l.z, l.w};
+#pragma unroll
+  for (int k = 0; k < 4; ++k) t[k] = q + k >= end || t[k] == -INFINITY ? -INFINITY : -t[k] * kLog2e;
+  *reinterpret_cast<float4*>(p.terms + i) = make_float4(t[0], t[1], t[2], t[3]);
+}
+
+// Scores of unseen columns become what add_probs turns into an exponent of
+// -infinity: an infinity of the scale's opposite sign, or (cap) a mark.
+template <bool kCap>
+__device__ __forceinline__ void hide(const KwParams& p, uint32_t (&v)[32], uint32_t seen) {
+  const uint32_t gone = kCap ? kHidden : (p.scale_log2 > 0.f ? 0xFF800000u : 0x7F800000u);
+#pragma unroll
+  for (int i = 0; i < 32; ++i)
+    if (!(seen & (1u << i))) v[i] = gone;
+}
+
+// exp2 of one key's scores of 32 queries with the queries' terms, added to four sums.
+template <bool kCap>
+__device__ __forceinline__ void add_probs(const KwParams& p, const uint32_t (&v)[32], const float* term, uint64_t (&acc)[4]) {
+  const uint64_t sc2 = f2_pack(p.scale_log2, p.scale_log2);
+#pragma unroll
+  for (int i = 0; i < 8; ++i) {
+    const float4 t = *reinterpret_cast<const float4*>(term + 4 * i);
+    float e[4];
+    if constexpr (kCap) {
+      const float tt[4] = {t.x, t.y, t.z, t.w};
+#pragma unroll
+      for (int k = 0; k < 4; ++k) {
+        e[k] = fmaf(tanh_fast(__uint_as_float(v[4 * i + k]) * p.scale_log2), p.cap_log2, tt[k]);
+        if (v[4 * i + k] == kHidden) e[k] = -INFINITY;
+      }
+    } else {
+      f2_unpack(f2_fma(f2_pack(__uint_as_float(v[4 * i]), __uint_as_float(v[4 * i + 1])), sc2, f2_pack(t.x, t.y)), e[0], e[1]);
+      f2_unpack(f2_fma(f2_pack(__uint_as_float(v[4 * i + 2]), __uint_as_float(v[4 * i + 3])), sc2, f2_pack(t.z, t.w)), e[2], e[3]);
+    }
+    acc[2 * (i & 1)] = f2_add(acc[2 * (i & 1)], f2_pack(ex2_approx(e[0]), ex2_approx(e[1])));
+    acc[2 * (i & 1) + 1] = f2_add(acc[2 * (i & 1) + 1], f2_pack(ex2_approx(e[2]), ex2_approx(e[3])));
+  }
+}
+
+// Bits of the visible queries [32 c, 32 c + 32) of the item for a key, of a masked item.
+struct Visible {
+  uint32_t w[4];
+};
+__device__ __forceinline__ Visible visible_queries(const KwParams& p, const uint4& x, int64_t key, int r) {
+  Visible m{{~0u, ~0u, ~0u, ~0u}};
+  const int32_t q0 = static_cast<int32_t>(x.x & 0xFFFFu) * 128;
+  int64_t lo = q0, hi = static_cast<int64_t>(x.w) - 1;
+  if (((x.x >> 16) & 3u) == 1u) {
+    if (p.mi.kind == BSA_MASK_DENSE) {
+      const uint4 bits = __ldg(reinterpret_cast<const uint4*>(p.mi.partial_bits) + static_cast<int64_t>(x.y) * 128 + r);
+      m.w[0] = bits.x;
+      m.w[1] = bits.y;
+      m.w[2] = bits.z;
+      m.w[3] = bits.w;
+    } else {
+      int64_t a, b;
+      query_interval(p.mi.kind, p.mi.left, p.mi.right, p.mi.chunk, key, a, b);
+      lo = a > lo ? a : lo;
+      hi = b < hi ? b : hi;
+    }
+  }
+#pragma unroll
+  for (int c = 0; c < 4; ++c) {
+    const int64_t c0 = q0 + 32 * c;
+    const int64_t a = lo > c0 ? lo - c0 : 0, b = hi < c0 + 31 ? hi - c0 : 31;
+    m.w[c] &= b < a ? 0u : (0xFFFFFFFFu >> (31 - (b - a))) << a;
+  }
+  return m;
+}
+
 template <int D, bool kCap>
 __global__ void __launch_bounds__(kThreads, 1)
     key_weights_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constant__ CUtensorMap tm_k,
@@ -107,27 +225,27 @@ __global__ void __launch_bounds__(kThreads, 1)
   using Smem = KwSmem<D>;
   Smem& s = *reinterpret_cast<Smem*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
   constexpr uint32_t kTileBytes = Smem::kTileBytes;
-  constexpr int kChunks = D / 64;
   const int warp = warp_id(), lane = threadIdx.x & 31;
 
   if (threadIdx.x == 0) {
     s.abort_flag = 0;
     for (int i = 0; i < kRing; ++i) {
       mbar_init(&s.ring_full[i], 1);
-      mbar_init(&s.ring_empty[i], kRingReaders);
+      mbar_init(&s.ring_empty[i], 1);
+    }
+    for (int i = 0; i < kTerms; ++i) {
+      mbar_init(&s.term_full[i], 1);
+      mbar_init(&s.term_empty[i], 4);
     }
     for (int i = 0; i < kBufs; ++i) {
       mbar_init(&s.q_full[i], 1);
       mbar_init(&s.s_full[i], 1);
-      mbar_init(&s.s_empty[i], kEwWarps);
+      mbar_init(&s.s_empty[i], 4);
     }
     for (int i = 0; i < 2; ++i) {
       mbar_init(&s.k_full[i], 1);
-      mbar_init(&s.k_empty[i], 1);
-      mbar_init(&s.red_full[i], kEwWarps);
-      mbar_init(&s.red_empty[i], 1);
+      mbar_init(&s.drain[i], 1);
     }
-    mbar_init(&s.drain, 1);
     fence_mbar_init();
   }
   if (warp == 1) {
@@ -141,273 +259,245 @@ __global__ void __launch_bounds__(kThreads, 1)
   const WaitCtl wc{p.err, &s.abort_flag, p.wait_ns};
   griddep_launch_dependents();
   griddep_wait();
+  const Cut c0 = p.cut[blockIdx.x], c1 = p.cut[blockIdx.x + 1];
 
   if (warp == 0) {
-    // ------------------------------------------------ walker and producer
+    // ------------------------------------------------ walker (whole warp)
+    uint32_t e = 0;
+    bool ok = true;
+    // lanes 0 .. m - 1 (in the order of `index`) publish an item each: the one
+    // reader frees slots in order, so a wait for the last slot covers all
+    auto room = [&](uint32_t m) -> bool {
+      const uint32_t last = e + m - 1;
+      return last < static_cast<uint32_t>(kRing) ||
+             mbar_wait_warp(&s.ring_empty[last % kRing], (last / kRing - 1) & 1u, wc);
+    };
+    const int32_t G = p.Hq / p.Hkv;
+    for (int32_t tile = c0.tile; ok && tile <= c1.tile; ++tile) {
+      if (tile == c1.tile && c1.skip == 0) break;
+      const int32_t j = tile % p.mi.rows, bg = tile / p.mi.rows, b = bg / p.Hkv, g = bg % p.Hkv;
+      const int32_t all = tile_items(p, tile);
+      const int32_t begin = tile == c0.tile ? c0.skip : 0;
+      const int32_t stop = tile == c1.tile ? c1.skip : all;
+      const int32_t q_end = query_end(p, b);
+      const uint32_t krow = static_cast<uint32_t>(static_cast<int64_t>(bg) * p.Skv + static_cast<int64_t>(j) * 128);
+      bool first = true;
+      int32_t at = 0;  // items of the tile passed so far
+      for (int32_t gh = 0; ok && gh < G && at < stop; ++gh) {
+        const int32_t hq = g * G + gh, hm = p.mi.heads == 1 ? 0 : hq;
+        const int32_t len = p.mi.row_len[hm * p.mi.rows + j];
+        if (at + len <= begin) {
+          at += len;
+          continue;
+        }
+        const int64_t row_base = (static_cast<int64_t>(hm) * p.mi.rows + j) * p.mi.width;
+        const int64_t head = (static_cast<int64_t>(b) * p.Hq + hq) * p.Sq;
+        const int32_t end = min(at + len, stop);
+        int32_t pos = p.compact && at < begin ? begin - at : 0;
+        at += pos;
+        for (; ok && at < end && pos < p.mi.width; pos += 32) {
+          const RawRef raw = pos + lane < p.mi.width ? load_block(p.mi, row_base, pos + lane) : RawRef{0, 0, 0};
+          const BlockRef br = check_block(p.mi, raw, p.err);
+          // this lane's place among the row's items, and whether it is one to compute
+          const uint32_t cells = __ballot_sync(0xffffffffu, br.label != 0);
+          const int32_t mine = at + __popc(cells & ((1u << lane) - 1u));
+          const bool item = br.label != 0 && mine >= begin && mine < end && br.col * 128 < q_end;  // (not padding only)
+          at = min(at + __popc(cells), end);
+          const uint32_t items = __ballot_sync(0xffffffffu, item);
+          const uint32_t count = __popc(items), index = __popc(items & ((1u << lane) - 1u));
+          for (uint32_t i0 = 0; ok && i0 < count; i0 += kBatch) {
+            const uint32_t m = min(static_cast<uint32_t>(kBatch), count - i0);
+            ok = room(m);
+            if (!ok) break;
+            if (item && index >= i0 && index < i0 + m) {
+              const uint32_t slot = (e + index - i0) % kRing;
+              const bool mask = br.label == 1 || br.col * 128 + 128 > q_end;
+              const int64_t qrow = BSA_RANGE(head + static_cast<int64_t>(br.col) * 128, int64_t(0),
+                                             static_cast<int64_t>(p.B) * p.Hq * p.Sq - 127, p.err);
+              s.entry[slot] = make_uint4(static_cast<uint32_t>(br.col) | static_cast<uint32_t>(br.label) << 16 |
+                                             (first && index == 0 ? kFirst : 0u) | (mask ? kMask : 0u),
+                                         static_cast<uint32_t>(br.slot), static_cast<uint32_t>(tile - c0.tile),
+                                         static_cast<uint32_t>(q_end));
+              s.rows[slot] = make_uint2(static_cast<uint32_t>(qrow), krow);
+              mbar_arrive(&s.ring_full[slot]);
+            }
+            __syncwarp();
+            e += m;
+          }
+          if (count) first = false;
+        }
+        at = end;
+      }
+    }
+    if (ok && room(1) && lane == 0) {
+      s.entry[e % kRing] = make_uint4(kEnd, 0u, 0u, 0u);
+      mbar_arrive(&s.ring_full[e % kRing]);
+    }
+  } else if (warp == 3) {
+    // ------------------------------------------------ producer (one lane)
     if (lane == 0) {
       tma_prefetch_desc(&tm_q);
       tma_prefetch_desc(&tm_k);
       const uint64_t pol = policy_evict_last();
-      uint32_t e = 0, n = 0, k_loads = 0, lse_pending = 0;
+      uint32_t n = 0, k_loads = 0;
+      uint32_t last1 = 0, last2 = 0;  // items passed when the part before the current one, and the one before that, had ended
       bool ok = true;
-      auto slot_free = [&]() -> bool {
-        return e < static_cast<uint32_t>(kRing) || mbar_wait(&s.ring_empty[e % kRing], (e / kRing - 1) & 1u, wc);
+      // item i's scores are computed: its Q stage is free
+      auto done = [&](uint32_t i) -> bool { return mbar_wait(&s.s_full[i % kBufs], (i / kBufs) & 1u, wc); };
+      auto term_free = [&]() -> bool {
+        return n < static_cast<uint32_t>(kTerms) || mbar_wait(&s.term_empty[n % kTerms], (n / kTerms - 1) & 1u, wc);
       };
-      const Cut c0 = p.cut[blockIdx.x], c1 = p.cut[blockIdx.x + 1];
-      const int32_t G = p.Hq / p.Hkv;
-      for (int32_t tile = c0.tile; ok && tile <= c1.tile; ++tile) {
-        if (tile == c1.tile && c1.skip == 0) break;
-        const int32_t j = tile % p.mi.rows, bg = tile / p.mi.rows, b = bg / p.Hkv, g = bg % p.Hkv;
-        const int32_t all = tile_items(p, tile);
-        const int32_t begin = tile == c0.tile ? c0.skip : 0;
-        const int32_t stop = tile == c1.tile ? c1.skip : all;
-        const int32_t q_end = query_end(p, b);
-        const int64_t krow = static_cast<int64_t>(bg) * p.Skv + static_cast<int64_t>(j) * 128;
-        bool first = true;
-        int32_t at = 0;  // items of the tile passed so far
-        for (int32_t gh = 0; ok && gh < G && at < stop; ++gh) {
-          const int32_t hq = g * G + gh, hm = p.mi.heads == 1 ? 0 : hq;
-          const int32_t len = p.mi.row_len[hm * p.mi.rows + j];
-          if (at + len <= begin) {
-            at += len;
-            continue;
-          }
-          const int64_t row_base = (static_cast<int64_t>(hm) * p.mi.rows + j) * p.mi.width;
-          const int32_t end = min(at + len, stop);
-          int32_t pos = p.compact && at < begin ? begin - at : 0;
-          at += pos;
-          RawRef ahead = pos < p.mi.width ? load_block(p.mi, row_base, pos) : RawRef{0, 0, 0};
-          for (; ok && at < end && pos < p.mi.width; ++pos) {
-            const RawRef cur = ahead;
-            if (pos + 1 < p.mi.width) ahead = load_block(p.mi, row_base, pos + 1);
-            const BlockRef br = check_block(p.mi, cur, p.err);
-            if (br.label == 0) continue;
-            if (at++ < begin) continue;
-            if (br.col * 128 >= q_end) continue;  // padding only
-            const uint32_t st = n % kBufs;
-            if (!slot_free()) { ok = false; break; }
-            // the stage's last scores are computed: its Q has been read
-            if (n >= static_cast<uint32_t>(kBufs) && !mbar_wait(&s.s_full[st], (n / kBufs - 1) & 1u, wc)) { ok = false; break; }
-            const int64_t qrow = BSA_RANGE((static_cast<int64_t>(b) * p.Hq + hq) * p.Sq + static_cast<int64_t>(br.col) * 128,
-                                           int64_t(0), static_cast<int64_t>(p.B) * p.Hq * p.Sq - 127, p.err);
-            const bool mask = br.label == 1 || br.col * 128 + 128 > q_end;
-            s.entry[e % kRing] = make_uint4(static_cast<uint32_t>(br.col) | static_cast<uint32_t>(br.label) << 16 |
-                                                (first ? kFirst : 0u) | (mask ? kMask : 0u),
-                                            static_cast<uint32_t>(br.slot), static_cast<uint32_t>(j),
-                                            static_cast<uint32_t>(q_end));
-            mbar_arrive_expect_tx(&s.ring_full[e % kRing], 512);
-            bulk_load(s.lse[e % kRing], p.lse + qrow, 512, &s.ring_full[e % kRing]);
-            lse_pending |= 1u << (e % kRing);
-            ++e;
-            mbar_arrive_expect_tx(&s.q_full[st], kTileBytes);
-            for (int c = 0; c < kChunks; ++c)
-              tma_load_2d(s.q[st] + c * 16384, &tm_q, &s.q_full[st], c * 64, static_cast<int32_t>(qrow), pol);
-            ++n;
-            if (first) {
-              const uint32_t kb = k_loads & 1u;
-              if (k_loads >= 2 && !mbar_wait(&s.k_empty[kb], (k_loads / 2 - 1) & 1u, wc)) { ok = false; break; }
-              mbar_arrive_expect_tx(&s.k_full[kb], kTileBytes);
-              for (int c = 0; c < kChunks; ++c)
-                tma_load_2d(s.k[kb] + c * 16384, &tm_k, &s.k_full[kb], c * 64, static_cast<int32_t>(krow), pol);
-              ++k_loads;
-              first = false;
-            }
-          }
-          at = end;
+      for (uint32_t e = 0; ok; ++e) {
+        const uint32_t slot = e % kRing, st = n % kBufs, ts = n % kTerms;
+        // the three waits' latencies together, when all are long over
+        const bool ready = n >= static_cast<uint32_t>(kTerms) &&
+                           all_complete(smem_u32(&s.ring_full[slot]), (e / kRing) & 1u, smem_u32(&s.s_full[st]),
+                                        (n / kBufs - 1) & 1u, smem_u32(&s.term_empty[ts]), (n / kTerms - 1) & 1u);
+        if (!ready && !mbar_wait(&s.ring_full[slot], (e / kRing) & 1u, wc)) { ok = false; break; }
+        const uint4 x = s.entry[slot];
+        const uint2 rows = s.rows[slot];
+        mbar_arrive(&s.ring_empty[slot]);
+        if (x.x & kEnd) break;
+        if (!ready && ((n >= static_cast<uint32_t>(kBufs) && !done(n - kBufs)) || !term_free())) { ok = false; break; }
+        if (x.x & kFirst) {
+          // the K buffer's part ended with item last2 - 1
+          for (uint32_t i = n >= kBufs ? n - kBufs + 1 : 0; ok && k_loads >= 2 && i < last2; ++i) ok = done(i);
+          if (!ok) break;
+          const uint32_t kb = k_loads & 1u;
+          mbar_arrive_expect_tx(&s.k_full[kb], kTileBytes);
+          tma_load_3d(s.k[kb], &tm_k, &s.k_full[kb], 0, static_cast<int32_t>(rows.y), 0, pol);
+          last2 = last1;
+          ++k_loads;
         }
-        if (!ok || !slot_free()) { ok = false; break; }
-        const bool whole = begin == 0 && stop == all;
-        const uint32_t part = static_cast<uint32_t>(2 * blockIdx.x + (tile == c0.tile ? 0 : 1));
-        s.entry[e % kRing] = make_uint4(kTileEnd, static_cast<uint32_t>(krow), first ? 0u : 1u, whole ? 0u : part + 1u);
-        mbar_arrive(&s.ring_full[e % kRing]);
-        lse_pending &= ~(1u << (e % kRing));
-        ++e;
+        last1 = n + 1;
+        const uint32_t k = k_loads - 1;
+        s.q_info[st] = (k & 1u) | ((k >> 1) & 1u) << 8;
+        mbar_arrive_expect_tx(&s.q_full[st], kTileBytes);
+        tma_load_3d(s.q[st], &tm_q, &s.q_full[st], 0, static_cast<int32_t>(rows.x), 0, pol);
+        s.item[ts] = x;
+        mbar_arrive_expect_tx(&s.term_full[ts], 512);
+        bulk_load(s.term[ts], p.terms + rows.x, 512, &s.term_full[ts]);
+        ++n;
       }
-      if (ok && slot_free()) {
-        s.entry[e % kRing] = make_uint4(kEnd, 0u, 0u, 0u);
-        mbar_arrive(&s.ring_full[e % kRing]);
-        ++e;
-      } else {
+      const uint32_t loads = n;
+      // the end, to both issuers and the four warpgroups
+      for (int i = 0; ok && i < kBufs; ++i, ++n) {
+        if ((n >= static_cast<uint32_t>(kBufs) && n - kBufs < loads && !done(n - kBufs)) || !term_free()) { ok = false; break; }
+        if (i < 2) {
+          s.q_info[n % kBufs] = kEnd;
+          mbar_arrive(&s.q_full[n % kBufs]);
+        }
+        s.item[n % kTerms] = make_uint4(kEnd, 0u, 0u, 0u);
+        mbar_arrive(&s.term_full[n % kTerms]);
+      }
+      if (!ok) {
         // the copies in flight land before the CTA exits
         uint32_t dummy_abort = 0;
         WaitCtl dw{nullptr, &dummy_abort, p.wait_ns};
-        for (uint32_t i = n > kBufs ? n - kBufs : 0; i < n; ++i) (void)mbar_wait(&s.q_full[i % kBufs], (i / kBufs) & 1u, dw);
+        for (uint32_t i = loads > kBufs ? loads - kBufs : 0; i < loads; ++i) (void)mbar_wait(&s.q_full[i % kBufs], (i / kBufs) & 1u, dw);
+        for (uint32_t i = loads > kTerms ? loads - kTerms : 0; i < loads; ++i) (void)mbar_wait(&s.term_full[i % kTerms], (i / kTerms) & 1u, dw);
         for (uint32_t i = k_loads > 2 ? k_loads - 2 : 0; i < k_loads; ++i) (void)mbar_wait(&s.k_full[i & 1u], (i / 2) & 1u, dw);
-        for (uint32_t i = e > kRing ? e - kRing : 0; i < e; ++i)
-          if (lse_pending >> (i % kRing) & 1u) (void)mbar_wait(&s.ring_full[i % kRing], (i / kRing) & 1u, dw);
       }
     }
-  } else if (warp == 1) {
-    // ------------------------------------------------ MMA issuer (whole warp)
+  } else if (warp < 3) {
+    // ------------------------------------------------ MMA issuers (whole warps): items warp - 1, + 2, ...
     constexpr uint32_t idesc = idesc_bf16_f32(128, 128, false, false);
     constexpr uint64_t kTileDesc = kTileBytes >> 4;
     const uint64_t qdesc0 = sdesc_sw128(smem_u32(s.q[0]), 16, 1024);
     const uint64_t kdesc0 = sdesc_sw128(smem_u32(s.k[0]), 16, 1024);
-    uint32_t n = 0, k_uses = 0;
-    for (uint32_t e = 0;; ++e) {
-      const uint32_t slot = e % kRing;
-      if (!mbar_wait_warp(&s.ring_full[slot], (e / kRing) & 1u, wc)) break;
-      const uint4 x = s.entry[slot];
-      __syncwarp();
-      if (lane == 0) mbar_arrive(&s.ring_empty[slot]);
-      if (x.x & kEnd) break;
-      if (x.x & kTileEnd) {
-        if (x.z) {
-          mma_commit_elect(&s.k_empty[k_uses & 1u]);
-          ++k_uses;
-        }
-        continue;
-      }
-      if ((x.x & kFirst) && !mbar_wait_warp(&s.k_full[k_uses & 1u], (k_uses / 2) & 1u, wc)) break;
+    for (uint32_t n = static_cast<uint32_t>(warp) - 1u;; n += 2) {
       const uint32_t b = n % kBufs;
-      if (n >= static_cast<uint32_t>(kBufs) && !mbar_wait_warp(&s.s_empty[b], (n / kBufs - 1) & 1u, wc)) break;
       if (!mbar_wait_warp(&s.q_full[b], (n / kBufs) & 1u, wc)) break;
+      const uint32_t info = __shfl_sync(0xffffffffu, s.q_info[b], 0);
+      if (info & kEnd) break;
+      const uint32_t kb = info & 1u;
+      if (!mbar_wait_warp(&s.k_full[kb], (info >> 8) & 1u, wc)) break;
+      if (n >= static_cast<uint32_t>(kBufs) && !mbar_wait_warp(&s.s_empty[b], (n / kBufs - 1) & 1u, wc)) break;
       tc_fence_after();
-      const uint64_t qd = qdesc0 + b * kTileDesc, kd = kdesc0 + (k_uses & 1u) * kTileDesc;
+      const uint64_t qd = qdesc0 + b * kTileDesc, kd = kdesc0 + kb * kTileDesc;
 #pragma unroll
       for (int kk = 0; kk < D / 16; ++kk) {
         const uint64_t off = static_cast<uint64_t>(((kk >> 2) * 16384 + (kk & 3) * 32) >> 4);
-        mma_ss_elect(BSA_TMEM(tmem + b * 128, 128u, p.err), qd + off, kd + off, idesc, kk > 0 ? 1u : 0u);
+        mma_ss_elect(BSA_TMEM(tmem + b * 128, 128u, p.err), kd + off, qd + off, idesc, kk > 0 ? 1u : 0u);
       }
       mma_commit_elect(&s.s_full[b]);
-      ++n;
     }
-    mma_commit_elect(&s.drain);
+    mma_commit_elect(&s.drain[warp - 1]);
     uint32_t dummy_abort = 0;
     WaitCtl dw{p.err, &dummy_abort, p.wait_ns};
-    (void)mbar_wait(&s.drain, 0, dw);
-  } else if (warp == 2) {
-    // ------------------------------------------------ column sums of finished tiles
-    uint32_t t = 0;
-    for (uint32_t e = 0;; ++e) {
-      const uint32_t slot = e % kRing;
-      if (!mbar_wait_warp(&s.ring_full[slot], (e / kRing) & 1u, wc)) break;
-      const uint4 x = s.entry[slot];
-      __syncwarp();
-      if (lane == 0) mbar_arrive(&s.ring_empty[slot]);
-      if (x.x & kEnd) break;
-      if (!(x.x & kTileEnd)) continue;
-      const uint32_t tp = t & 1u;
-      if (!mbar_wait_warp(&s.red_full[tp], (t / 2) & 1u, wc)) break;
-      float4 v = *reinterpret_cast<const float4*>(&s.red[tp][0][4 * lane]);
+    (void)mbar_wait(&s.drain[warp - 1], 0, dw);
+  } else {
+    // ------------------------------------------------ exponentials: warpgroup w takes items w, w + 4, ...
+    const int w = (warp - 4) >> 2, quarter = (warp - 4) & 3;
+    const int r = quarter * 32 + lane;  // key of the tile == tensor-memory lane
+    const uint32_t taddr = BSA_TMEM(tmem + w * 128 + (static_cast<uint32_t>(quarter * 32) << 16), 128u, p.err);
+    const int32_t parts = c1.tile - c0.tile + (c1.skip > 0 ? 1 : 0);
+    int32_t part = 0;
+    uint64_t acc[4];
 #pragma unroll
-      for (int i = 1; i < 4; ++i) {
-        const float4 y = *reinterpret_cast<const float4*>(&s.red[tp][i][4 * lane]);
-        v = make_float4(v.x + y.x, v.y + y.y, v.z + y.z, v.w + y.w);
+    for (int i = 0; i < 4; ++i) acc[i] = f2_pack(0.f, 0.f);
+    // the finished parts' sums (zeros where this warpgroup had no item)
+    auto flush_to = [&](int32_t to) {
+      for (; part < to; ++part) {
+        float a, b;
+        f2_unpack(f2_add(f2_add(acc[0], acc[1]), f2_add(acc[2], acc[3])), a, b);
+        p.sums[(static_cast<int64_t>(sums_row(p, blockIdx.x, c0.tile + part)) * 4 + w) * 128 + r] = a + b;
+#pragma unroll
+        for (int i = 0; i < 4; ++i) acc[i] = f2_pack(0.f, 0.f);
       }
-      __syncwarp();
-      if (lane == 0) mbar_arrive(&s.red_empty[tp]);
-      const int64_t row = BSA_RANGE(static_cast<int64_t>(x.y), int64_t(0), static_cast<int64_t>(p.B) * p.Hkv * p.Skv - 127, p.err);
-      float* dst = x.w ? p.partial + static_cast<int64_t>(x.w - 1) * 128 : p.out + row;
-      *reinterpret_cast<float4*>(dst + 4 * lane) = v;
-      ++t;
-    }
-  } else if (warp >= 4) {
-    // ------------------------------------------------ exponentials
-    const int part = (warp - 4) >> 2, quarter = (warp - 4) & 3;
-    const int r = quarter * 32 + lane;  // query row of the item == tensor-memory lane
-    const uint32_t taddr = tmem + part * 32 + (static_cast<uint32_t>(quarter * 32) << 16);
-    const uint64_t sc2 = f2_pack(p.scale_log2, p.scale_log2);
-    uint64_t acc[16];
-#pragma unroll
-    for (int i = 0; i < 16; ++i) acc[i] = f2_pack(0.f, 0.f);
-    uint32_t n = 0, t = 0;
-    for (uint32_t e = 0;; ++e) {
-      const uint32_t slot = e % kRing;
-      if (!mbar_wait_warp(&s.ring_full[slot], (e / kRing) & 1u, wc)) break;
-      const uint4 x = s.entry[slot];
-      if (x.x & kEnd) break;
-      if (x.x & kTileEnd) {
-        __syncwarp();
-        if (lane == 0) mbar_arrive(&s.ring_empty[slot]);
-        const uint32_t tp = t & 1u;
-        if (t >= 2 && !mbar_wait_warp(&s.red_empty[tp], (t / 2 - 1) & 1u, wc)) break;
-        // sum over the 32 lanes, column c ending in lane c: halves are exchanged
-        float v[32];
-#pragma unroll
-        for (int i = 0; i < 16; ++i) {
-          f2_unpack(acc[i], v[2 * i], v[2 * i + 1]);
-          acc[i] = f2_pack(0.f, 0.f);
-        }
-#pragma unroll
-        for (int o = 16; o > 0; o >>= 1) {
-          const bool up = lane & o;
-#pragma unroll
-          for (int i = 0; i < o; ++i) {
-            const float keep = up ? v[i + o] : v[i], give = up ? v[i] : v[i + o];
-            v[i] = keep + __shfl_xor_sync(0xffffffffu, give, o);
-          }
-        }
-        s.red[tp][quarter][part * 32 + lane] = v[0];
-        __syncwarp();
-        if (lane == 0) mbar_arrive(&s.red_full[tp]);
-        ++t;
-        continue;
+    };
+    for (uint32_t n = static_cast<uint32_t>(w);; n += kBufs) {
+      const uint32_t ts = n % kTerms;
+      if (!mbar_wait_warp(&s.term_full[ts], (n / kTerms) & 1u, wc)) break;
+      const uint4 x = s.item[ts];
+      if (x.x & kEnd) {
+        flush_to(parts);
+        break;
       }
-      const float l = s.lse[slot][r];
-      const float nl = l == -INFINITY ? -INFINITY : -l * kLog2e;
-      __syncwarp();
-      if (lane == 0) mbar_arrive(&s.ring_empty[slot]);
-      uint32_t seen = 0xFFFFFFFFu;  // visible columns of this row
-      if (x.x & kMask) {
-        const int32_t col = static_cast<int32_t>(x.x & 0xFFFFu);
-        const int64_t q = static_cast<int64_t>(col) * 128 + r;
-        if (((x.x >> 16) & 3u) == 1u) {
-          if (p.mi.kind == BSA_MASK_DENSE) {
-            // word c of the block's rows (keys) part * 32 + c, bit = this query: loaded a row per lane, turned by shuffles
-            const uint32_t word = __ldg(p.mi.partial_bits + (static_cast<int64_t>(x.y) * 128 + part * 32 + lane) * 4 + quarter);
-            seen = 0;
-#pragma unroll
-            for (int c = 0; c < 32; ++c) seen |= ((__shfl_sync(0xffffffffu, word, c) >> lane) & 1u) << c;
-          } else {
-            int64_t lo, hi;
-            key_interval(p.mi.kind, p.mi.left, p.mi.right, p.mi.chunk, q, lo, hi);
-            const int64_t k0 = static_cast<int64_t>(x.z) * 128 + part * 32;
-            const int64_t a = lo > k0 ? lo - k0 : 0, b = hi < k0 + 31 ? hi - k0 : 31;
-            seen = b < a ? 0u : static_cast<uint32_t>((0xFFFFFFFFull >> (31 - (b - a))) << a);
-          }
-        }
-        if (q >= static_cast<int64_t>(x.w)) seen = 0;
-      }
-      const uint32_t b = n % kBufs;
-      if (!mbar_wait_warp(&s.s_full[b], (n / kBufs) & 1u, wc)) break;
+      flush_to(static_cast<int32_t>(x.z));
+      const bool masked = x.x & kMask;
+      Visible m{{~0u, ~0u, ~0u, ~0u}};
+      if (masked) m = visible_queries(p, x, static_cast<int64_t>((c0.tile + part) % p.mi.rows) * 128 + r, r);
+      if (!mbar_wait_warp(&s.s_full[w], (n / kBufs) & 1u, wc)) break;
       tc_fence_after();
-      uint32_t v[32];
-      tmem_ld32(BSA_TMEM(taddr + b * 128, 32u, p.err), v);
-      tmem_wait_ld();
-      reg_fence32(v);
-      tc_fence_before();
-      __syncwarp();
-      if (lane == 0) mbar_arrive(&s.s_empty[b]);
-      ++n;
-      const uint64_t nl2 = f2_pack(nl, nl);
-      if (!(x.x & kMask)) {
-#pragma unroll
-        for (int i = 0; i < 16; ++i) {
-          float e0, e1;
-          if constexpr (kCap) {
-            e0 = fmaf(tanh_fast(__uint_as_float(v[2 * i]) * p.scale_log2), p.cap_log2, nl);
-            e1 = fmaf(tanh_fast(__uint_as_float(v[2 * i + 1]) * p.scale_log2), p.cap_log2, nl);
-          } else {
-            f2_unpack(f2_fma(f2_pack(__uint_as_float(v[2 * i]), __uint_as_float(v[2 * i + 1])), sc2, nl2), e0, e1);
-          }
-          acc[i] = f2_add(acc[i], f2_pack(ex2_approx(e0), ex2_approx(e1)));
-        }
+      const float* term = s.term[ts];
+      uint32_t va[32], vb[32];
+      if (!masked) {
+        // each load runs under the exponentials of the chunk before it (no branch while one is in flight)
+        tmem_ld32(taddr, va);
+        tmem_wait_ld();
+        reg_fence32(va);
+        tmem_ld32(taddr + 32, vb);
+        add_probs<kCap>(p, va, term, acc);
+        tmem_wait_ld();
+        reg_fence32(vb);
+        tmem_ld32(taddr + 64, va);
+        add_probs<kCap>(p, vb, term + 32, acc);
+        tmem_wait_ld();
+        reg_fence32(va);
+        tmem_ld32(taddr + 96, vb);
+        add_probs<kCap>(p, va, term + 64, acc);
+        tmem_wait_ld();
+        reg_fence32(vb);
+        tc_fence_before();
+        __syncwarp();
+        mbar_arrive_cnt_elect(&s.s_empty[w], 1u);
+        add_probs<kCap>(p, vb, term + 96, acc);
       } else {
 #pragma unroll
-        for (int i = 0; i < 16; ++i) {
-          float e0, e1;
-          if constexpr (kCap) {
-            e0 = fmaf(tanh_fast(__uint_as_float(v[2 * i]) * p.scale_log2), p.cap_log2, nl);
-            e1 = fmaf(tanh_fast(__uint_as_float(v[2 * i + 1]) * p.scale_log2), p.cap_log2, nl);
-          } else {
-            f2_unpack(f2_fma(f2_pack(__uint_as_float(v[2 * i]), __uint_as_float(v[2 * i + 1])), sc2, nl2), e0, e1);
-          }
-          const float p0 = (seen >> (2 * i)) & 1u ? ex2_approx(e0) : 0.f;
-          const float p1 = (seen >> (2 * i + 1)) & 1u ? ex2_approx(e1) : 0.f;
-          acc[i] = f2_add(acc[i], f2_pack(p0, p1));
+        for (int c = 0; c < 4; ++c) {
+          tmem_ld32(taddr + 32 * c, va);
+          tmem_wait_ld();
+          reg_fence32(va);
+          hide<kCap>(p, va, m.w[c]);
+          add_probs<kCap>(p, va, term + 32 * c, acc);
         }
+        tc_fence_before();
+        __syncwarp();
+        mbar_arrive_cnt_elect(&s.s_empty[w], 1u);
       }
+      __syncwarp();
+      mbar_arrive_cnt_elect(&s.term_empty[ts], 1u);
     }
   }
 
@@ -419,20 +509,25 @@ __global__ void __launch_bounds__(kThreads, 1)
   }
 }
 
-// Sums the partial rows of the tile that CTA c's run ends in (if it began
-// there, or its run is the tile's first): those of c and the CTAs after it
-// that have items of the same tile.
+// One block per tile: its rows of sums (four of each CTA that had a part of it) added up in order.
 __global__ void __launch_bounds__(128) key_weights_join(const __grid_constant__ KwParams p) {
   griddep_launch_dependents();
   griddep_wait();
-  const int32_t c = static_cast<int32_t>(blockIdx.x);
-  const Cut mine = p.cut[c], next = p.cut[c + 1];
-  if (next.skip == 0 || (mine.tile == next.tile && mine.skip > 0)) return;
-  float v = p.partial[(2 * c + (mine.tile == next.tile ? 0 : 1)) * 128 + threadIdx.x];
-  for (int32_t i = c + 1; i < p.n_cta && p.cut[i].tile == next.tile; ++i)
-    if (p.cut[i].skip > 0) v += p.partial[2 * i * 128 + threadIdx.x];
-  const int32_t bg = next.tile / p.mi.rows, j = next.tile % p.mi.rows;
-  p.out[static_cast<int64_t>(bg) * p.Skv + j * 128 + threadIdx.x] = v;
+  const int32_t t = static_cast<int32_t>(blockIdx.x);
+  // the CTA whose run holds the tile's beginning: the last cut at or before it
+  int32_t lo = 0, hi = p.n_cta;
+  while (hi - lo > 1) {
+    const int32_t mid = (lo + hi) / 2;
+    const Cut c = p.cut[mid];
+    if (c.tile < t || (c.tile == t && c.skip == 0)) lo = mid;
+    else hi = mid;
+  }
+  float v = 0.f;
+  for (int32_t c = lo; c < p.n_cta && (c == lo || (p.cut[c].tile == t && p.cut[c].skip > 0)); ++c) {
+    const float* row = p.sums + static_cast<int64_t>(sums_row(p, c, t)) * 512 + threadIdx.x;
+    v += (row[0] + row[128]) + (row[256] + row[384]);
+  }
+  p.out[static_cast<int64_t>(t / p.mi.rows) * p.Skv + t % p.mi.rows * 128 + threadIdx.x] = v;
 }
 
 // The cuts: n_cta equal runs of the items in tile order.
@@ -473,28 +568,32 @@ void make_cuts(const bsa_key_weights_args* a, const bsa_mask_info* info, KwParam
 template <int D>
 bsa_status launch(const bsa_key_weights_args* a, const KwParams& p, cudaStream_t stream) {
   CUtensorMap tq, tk;
-  if (!make_tmap_bf16_2d(&tq, a->q, static_cast<uint64_t>(a->B) * a->Hq * a->S_q, D, D * 2, 128, 64) ||
-      !make_tmap_bf16_2d(&tk, a->k, static_cast<uint64_t>(a->B) * a->Hkv * a->S_kv, D, D * 2, 128, 64))
+  const int64_t q_rows = static_cast<int64_t>(a->B) * a->Hq * a->S_q;
+  if (!make_tmap_bf16_panels(&tq, a->q, q_rows, D, 128) ||
+      !make_tmap_bf16_panels(&tk, a->k, static_cast<uint64_t>(a->B) * a->Hkv * a->S_kv, D, 128))
     return fail(BSA_ERR_CUDA, "cuTensorMapEncodeTiled rejected a Q/K description");
   auto kern = p.cap_log2 > 0.f ? key_weights_kernel<D, true> : key_weights_kernel<D, false>;
   const size_t smem = sizeof(KwSmem<D>) + 1024;
   const bsa_status st = ensure_smem_attr(reinterpret_cast<const void*>(kern), smem, "set key weights smem size");
   if (st != BSA_OK) return st;
-  cudaError_t e = launch_kernel(kern, dim3(p.n_cta), dim3(kThreads), smem, stream, tq, tk, p);
+  cudaError_t e = launch_kernel(key_weights_terms, dim3(static_cast<unsigned>((q_rows / 4 + 255) / 256)), dim3(256), 0, stream, p);
+  if (e == cudaSuccess) e = cudaGetLastError();
+  if (e != cudaSuccess) return cuda_fail(e, "key weights terms launch");
+  e = launch_kernel(kern, dim3(p.n_cta), dim3(kThreads), smem, stream, tq, tk, p);
   if (e == cudaSuccess) e = cudaGetLastError();
   if (e != cudaSuccess) return cuda_fail(e, "key weights launch");
-  if (p.n_cta > 1) {
-    e = launch_kernel(key_weights_join, dim3(p.n_cta), dim3(128), 0, stream, p);
-    if (e == cudaSuccess) e = cudaGetLastError();
-    if (e != cudaSuccess) return cuda_fail(e, "key weights join launch");
-  }
+  e = launch_kernel(key_weights_join, dim3(p.n_tiles), dim3(128), 0, stream, p);
+  if (e == cudaSuccess) e = cudaGetLastError();
+  if (e != cudaSuccess) return cuda_fail(e, "key weights join launch");
   return BSA_OK;
 }
 
 }  // namespace
 
-size_t key_weights_workspace_bytes(const bsa_key_weights_args*, const bsa_mask_info*) {
-  return static_cast<size_t>(kMaxCtas) * 2 * 128 * sizeof(float);
+size_t key_weights_workspace_bytes(const bsa_key_weights_args* a, const bsa_mask_info* info) {
+  // a row of sums per warpgroup for each tile and each CTA's two shared parts; the exponent terms
+  return ((static_cast<size_t>(a->B) * a->Hkv * info->rows + 2 * kMaxCtas) * 4 * 128 +
+          static_cast<size_t>(a->B) * a->Hq * a->S_q) * sizeof(float);
 }
 
 bsa_status key_weights_launch(const bsa_key_weights_args* a, const bsa_mask_info* info, float scale, cudaStream_t stream) {
@@ -508,11 +607,15 @@ bsa_status key_weights_launch(const bsa_key_weights_args* a, const bsa_mask_info
   p.Sq = a->S_q;
   p.Skv = a->S_kv;
   p.scale_log2 = a->logits_soft_cap > 0.f ? scale / a->logits_soft_cap : scale * kLog2e;
+  // (0 would turn the infinity of an unseen score into a NaN; any score times this is as good as 0)
+  if (p.scale_log2 == 0.f) p.scale_log2 = 1e-30f;
   p.cap_log2 = a->logits_soft_cap > 0.f ? a->logits_soft_cap * kLog2e : 0.f;
   p.lse = a->lse;
   p.q_lens = a->q_lens;
   p.out = a->weights;
-  p.partial = static_cast<float*>(a->workspace);
+  p.sums = static_cast<float*>(a->workspace);
+  p.n_tiles = a->B * a->Hkv * info->rows;
+  p.terms = p.sums + (static_cast<size_t>(p.n_tiles) + 2 * kMaxCtas) * 4 * 128;
   p.mi = mask_info_dev(info);
   p.compact = info->shrink ? 1 : 0;
   make_cuts(a, info, &p);

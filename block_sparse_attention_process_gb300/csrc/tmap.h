@@ -41,6 +41,22 @@ inline bool make_tmap_bf16_2d(CUtensorMap* m, const void* base, uint64_t rows, u
   return r == CUDA_SUCCESS;
 }
 
+// A bf16 matrix [rows, cols], cols a multiple of 64, seen as 64-column panels
+// {64, rows, cols / 64} and copied in boxes of `box_rows` rows of all panels:
+// one copy lays a whole tile out as the panel-major 128-byte-swizzled operand.
+inline bool make_tmap_bf16_panels(CUtensorMap* m, const void* base, uint64_t rows, uint64_t cols, uint32_t box_rows) {
+  auto enc = tmap_encoder();
+  if (!enc) return false;
+  cuuint64_t dims[3] = {64, rows, cols / 64};
+  cuuint64_t strides[2] = {cols * 2, 128};
+  cuuint32_t box[3] = {64, box_rows, static_cast<cuuint32_t>(cols / 64)};
+  cuuint32_t estr[3] = {1, 1, 1};
+  CUresult r = enc(m, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 3, const_cast<void*>(base), dims, strides, box, estr,
+                   CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
+                   CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE);
+  return r == CUDA_SUCCESS;
+}
+
 // The same view copied in boxes of [box_rows, 32] (64-byte rows) with the
 // 64-byte swizzle: 16-byte chunk j of box row r sits at chunk j ^ ((r >> 1) & 3).
 inline bool make_tmap_bf16_2d_sw64(CUtensorMap* m, const void* base, uint64_t rows, uint64_t cols,
