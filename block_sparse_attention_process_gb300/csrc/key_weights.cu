@@ -6,27 +6,33 @@
 // Per item one 128 x 128 x D product and 128^2 exponentials.  Keys are the
 // product's M side (tensor-memory lanes), queries its columns, so a thread sums
 // its key's probabilities in registers and a warpgroup can take a whole item:
-// four warpgroups on four items in turn, each at another point of its item,
+// three warpgroups on three items in turn, each at another point of its item,
 // keep the exponential unit busy through one another's waits.  (Queries as the
 // M side leave 64 sums per thread, which forces the warpgroups onto one item
 // together: they then wait, load and compute in step, 283 us on GQA 32/8 causal
 // 8192 against the figure below.)
 //
+// Shared-memory bandwidth is the other limit: both operands from shared memory
+// take all of its 128 bytes a cycle while a product runs.  K therefore sits in
+// tensor memory as the A operand, and a query's logsumexp enters through one
+// more k-step, a tile of ones times -lse / scale in three bf16 pieces: reading
+// it per column instead costs 256 cycles an item.  (With a soft cap the
+// logsumexp has to be added after the tanh, and is read per column.)
+//
 // One persistent CTA per SM, warp-specialised:
 //   warp 0      walks MaskInfo, 32 cells of a row at a time, and publishes the
 //               items in a ring, several at once
 //   warps 1-2   tcgen05 issuers of the even and the odd items: S^T = K Q^T into
-//               one of four tensor-memory buffers (one issuer needs ~1,100
+//               one of three tensor-memory buffers (one issuer needs ~1,100
 //               cycles an item, most of it barrier latency)
-//   warp 3      one lane loads K per tile (2 buffers), Q per item (4 stages) and
-//               the item's exponent terms (8)
-//   warps 4-19  exponentials: warpgroup n % 4 takes item n
+//   warp 3      one lane loads Q per item and its exponent terms
+//   warps 4-7   bring a tile's K from global into tensor memory (2 buffers)
+//   warps 8-19  exponentials: warpgroup n % 3 takes item n
 // All items of the launch form one sequence, cut into equal runs, one per CTA
 // (the host computes the cuts from MaskInfo's row lengths and passes them as
 // kernel parameters: no schedule to upload).  A first kernel turns the
-// logsumexp into exponent terms (-lse log2 e, -inf for what is not counted):
-// the producer lane, at ~1,100 cycles an item, set the pace while the terms
-// were made beside it.  Each warpgroup leaves a row of
+// logsumexp into exponent terms: the producer lane, at ~1,100 cycles an item,
+// set the pace while they were made beside it.  Each warpgroup leaves a row of
 // sums per tile and CTA in the workspace, and a second kernel adds these up in
 // order.
 #include <cmath>
@@ -39,13 +45,15 @@
 namespace bsa {
 namespace {
 
-constexpr int kBufs = 4;        // Q stages, score buffers, warpgroups of the exponentials (item n: n % 4)
+constexpr int kBufs = 3;        // score buffers, warpgroups of the exponentials (item n: n % 3)
+constexpr int kStages = 5;      // Q and exponent terms
 constexpr int kRing = 32;       // items between the walker and the producer
 constexpr int kBatch = 16;      // items published at once
-constexpr int kTerms = 8;       // column terms and descriptions of items between the producer and the exponentials
+constexpr int kEwWarp0 = 8;
 constexpr int kEwWarps = 4 * kBufs;
-constexpr int kThreads = 128 + 32 * kEwWarps;
+constexpr int kThreads = 32 * (kEwWarp0 + kEwWarps);
 constexpr int kMaxCtas = 160;
+constexpr uint32_t kColK = 128 * kBufs;  // tensor memory: the score buffers, then K (2 buffers of D / 2 columns)
 constexpr uint32_t kHidden = 0xFFFFDEADu;  // (a NaN no product gives) mark of an unseen score under a cap
 constexpr float kLog2e = 1.4426950408889634f;
 
@@ -54,25 +62,36 @@ constexpr uint32_t kFirst = 1u << 20;  // first item of its part of a tile
 constexpr uint32_t kMask = 1u << 21;   // some pairs of the item are not visible
 constexpr uint32_t kEnd = 1u << 22;    // no item: the run has ended
 
+// A block's exponent terms: without a cap a [128 queries, 16] bf16 operand in
+// 8 x 16-byte core matrices (the two k-halves of 8 rows side by side), whose
+// first three columns sum to -lse / scale; with one 128 floats, -lse log2 e.
+template <bool kCap>
+struct Terms {
+  static constexpr int kBytes = kCap ? 512 : 4096;
+};
+
 template <int D>
 struct __align__(1024) KwSmem {
   static constexpr int kTileBytes = 128 * D * 2;
-  uint8_t k[2][kTileBytes];
-  uint8_t q[kBufs][kTileBytes];
-  float term[kTerms][128];   // minus the logsumexp of the item's queries, log2 units (-inf: not counted)
+  uint8_t q[kStages][kTileBytes];
+  uint8_t term[kStages][4096];
+  uint8_t ones[4096];        // [128 keys, 16] bf16, laid out like the terms: 1 in the first three columns
   // {column | label << 16 | flags, stack slot, part of the run (tile - first tile), end of the counted queries}
   uint4 entry[kRing];
   uint2 rows[kRing];         // {Q row, K row}
-  uint4 item[kTerms];        // the entries, handed on
-  uint32_t q_info[kBufs];    // for the issuers: flags, bits 0-7 the K buffer, 8-15 the parity of its load
+  uint4 item[kStages];       // the entries, handed on
+  uint32_t q_info[kStages];  // for the issuers: flags, bits 0-7 the K buffer, 8-15 the parity of its load
+  uint32_t part_row[2];      // K row of the part to load, or ~0: the end
   uint64_t ring_full[kRing], ring_empty[kRing];
-  uint64_t term_full[kTerms], term_empty[kTerms];
-  uint64_t q_full[kBufs], s_full[kBufs], s_empty[kBufs];  // s_full also frees the Q stage (and, at last, K)
-  uint64_t k_full[2];
+  // item n's stage n % kStages: q_full (Q and terms in), stage_empty (its warpgroup is done with it, Q long read)
+  uint64_t q_full[kStages], stage_empty[kStages];
+  uint64_t s_full[kBufs], s_empty[kBufs];
+  uint64_t part_full[2], part_read[2], k_full[2];
   uint64_t drain[2];
   uint32_t tmem_base, abort_flag;
 };
 static_assert(sizeof(KwSmem<128>) + 1024 <= 232448, "key weights shared memory exceeds 227 KB per CTA");
+static_assert(kColK + 2 * 64 <= 512, "tensor memory");
 
 // Where a CTA's run begins: item `skip` of tile (b * Hkv + g) * rows + j.
 struct Cut {
@@ -86,9 +105,11 @@ struct KwParams {
   float cap_log2;
   const float* lse;
   const int32_t* q_lens;
-  float* terms;    // [B, Hq, Sq]
+  const __nv_bfloat16* k;
+  void* terms;     // the blocks of 128 queries' exponent terms, in the order of the queries
+  float term_scale, hidden;  // terms: lse * term_scale, or `hidden` for what is not counted
   float* out;
-  float* sums;     // [n_tiles + 2 n_cta][4][128]: a whole tile's sums of each warpgroup, then the first and last parts' of each CTA
+  float* sums;     // [n_tiles + 2 n_cta][kBufs][128]: a whole tile's sums of each warpgroup, then the first and last parts' of each CTA
   int32_t n_tiles;
   MaskInfoDev mi;
   int32_t compact;  // rows hold their non-empty blocks first
@@ -119,37 +140,46 @@ __device__ __forceinline__ int32_t sums_row(const KwParams& p, int32_t c, int32_
   return whole ? t : p.n_tiles + 2 * c + (t == a.tile ? 0 : 1);
 }
 
-// Whether three barriers' phases are complete (one test's latency, not three).
-__device__ __forceinline__ bool all_complete(uint32_t a, uint32_t pa, uint32_t b, uint32_t pb, uint32_t c, uint32_t pc) {
+// Whether both barriers' phases are complete (one test's latency, not two).
+__device__ __forceinline__ bool both_complete(uint32_t a, uint32_t pa, uint32_t b, uint32_t pb) {
   uint32_t ok;
   asm volatile(
-      "{\n\t.reg .pred p, q, r;\n\t"
+      "{\n\t.reg .pred p, q;\n\t"
       "mbarrier.test_wait.parity.shared::cta.b64 p, [%1], %2;\n\t"
       "mbarrier.test_wait.parity.shared::cta.b64 q, [%3], %4;\n\t"
-      "mbarrier.test_wait.parity.shared::cta.b64 r, [%5], %6;\n\t"
       "and.pred p, p, q;\n\t"
-      "and.pred p, p, r;\n\t"
       "selp.u32 %0, 1, 0, p;\n\t}"
       : "=r"(ok)
-      : "r"(a), "r"(pa), "r"(b), "r"(pb), "r"(c), "r"(pc)
+      : "r"(a), "r"(pa), "r"(b), "r"(pb)
       : "memory");
   return ok != 0u;
 }
 
-// Exponent terms of all queries: -lse in log2 units; -inf for a query that is
-// padding or sees nothing.
+// Exponent terms of all queries, one thread each.
+template <bool kCap>
 __global__ void __launch_bounds__(256) key_weights_terms(const __grid_constant__ KwParams p) {
   griddep_launch_dependents();
   griddep_wait();
-  const int64_t i = (static_cast<int64_t>(blockIdx.x) * 256 + threadIdx.x) * 4;
+  const int64_t i = static_cast<int64_t>(blockIdx.x) * 256 + threadIdx.x;
   if (i >= static_cast<int64_t>(p.B) * p.Hq * p.Sq) return;
-  const float4 l = *reinterpret_cast<const float4*>(p.lse + i);
+  const float l = p.lse[i];
   const int32_t b = static_cast<int32_t>(i / (p.Hq * p.Sq)), q = static_cast<int32_t>(i % p.Sq);
-  const int32_t end = query_end(p, b);
-  float t[4] = {l.x, l.y, l.z, l.w};
-#pragma unroll
-  for (int k = 0; k < 4; ++k) t[k] = q + k >= end || t[k] == -INFINITY ? -INFINITY : -t[k] * kLog2e;
-  *reinterpret_cast<float4*>(p.terms + i) = make_float4(t[0], t[1], t[2], t[3]);
+  const bool gone = q >= query_end(p, b) || l == -INFINITY;
+  const float t = gone ? p.hidden : l * p.term_scale;
+  if constexpr (kCap) {
+    static_cast<float*>(p.terms)[i] = t;
+  } else {
+    // three pieces of 8 bits hold all 24 of the fp32 term (hidden: the first alone)
+    const __nv_bfloat16 hi = __float2bfloat16_rn(t);
+    const float r1 = gone ? 0.f : t - __bfloat162float(hi);
+    const __nv_bfloat16 mid = __float2bfloat16_rn(r1);
+    const __nv_bfloat16 lo = __float2bfloat16_rn(r1 - __bfloat162float(mid));
+    uint8_t* at = static_cast<uint8_t*>(p.terms) + i / 128 * 4096 + (i % 128) / 8 * 256 + (i % 8) * 16;
+    *reinterpret_cast<uint4*>(at) =
+        make_uint4(static_cast<uint32_t>(__bfloat16_as_ushort(hi)) | static_cast<uint32_t>(__bfloat16_as_ushort(mid)) << 16,
+                   __bfloat16_as_ushort(lo), 0u, 0u);
+    *reinterpret_cast<uint4*>(at + 128) = make_uint4(0u, 0u, 0u, 0u);
+  }
 }
 
 // Scores of unseen columns become what add_probs turns into an exponent of
@@ -162,27 +192,22 @@ __device__ __forceinline__ void hide(const KwParams& p, uint32_t (&v)[32], uint3
     if (!(seen & (1u << i))) v[i] = gone;
 }
 
-// exp2 of one key's scores of 32 queries with the queries' terms, added to four sums.
+// exp2 of one key's scores of 32 queries (less the queries' logsumexp, which
+// the scores hold already, or with a cap after the terms), added to four sums.
 template <bool kCap>
 __device__ __forceinline__ void add_probs(const KwParams& p, const uint32_t (&v)[32], const float* term, uint64_t (&acc)[4]) {
   const uint64_t sc2 = f2_pack(p.scale_log2, p.scale_log2);
 #pragma unroll
-  for (int i = 0; i < 8; ++i) {
-    const float4 t = *reinterpret_cast<const float4*>(term + 4 * i);
-    float e[4];
+  for (int i = 0; i < 16; ++i) {
+    float e0, e1;
     if constexpr (kCap) {
-      const float tt[4] = {t.x, t.y, t.z, t.w};
-#pragma unroll
-      for (int k = 0; k < 4; ++k) {
-        e[k] = fmaf(tanh_fast(__uint_as_float(v[4 * i + k]) * p.scale_log2), p.cap_log2, tt[k]);
-        if (v[4 * i + k] == kHidden) e[k] = -INFINITY;
-      }
+      const float2 t = *reinterpret_cast<const float2*>(term + 2 * i);
+      e0 = v[2 * i] == kHidden ? -INFINITY : fmaf(tanh_fast(__uint_as_float(v[2 * i]) * p.scale_log2), p.cap_log2, t.x);
+      e1 = v[2 * i + 1] == kHidden ? -INFINITY : fmaf(tanh_fast(__uint_as_float(v[2 * i + 1]) * p.scale_log2), p.cap_log2, t.y);
     } else {
-      f2_unpack(f2_fma(f2_pack(__uint_as_float(v[4 * i]), __uint_as_float(v[4 * i + 1])), sc2, f2_pack(t.x, t.y)), e[0], e[1]);
-      f2_unpack(f2_fma(f2_pack(__uint_as_float(v[4 * i + 2]), __uint_as_float(v[4 * i + 3])), sc2, f2_pack(t.z, t.w)), e[2], e[3]);
+      f2_unpack(f2_mul(f2_pack(__uint_as_float(v[2 * i]), __uint_as_float(v[2 * i + 1])), sc2), e0, e1);
     }
-    acc[2 * (i & 1)] = f2_add(acc[2 * (i & 1)], f2_pack(ex2_approx(e[0]), ex2_approx(e[1])));
-    acc[2 * (i & 1) + 1] = f2_add(acc[2 * (i & 1) + 1], f2_pack(ex2_approx(e[2]), ex2_approx(e[3])));
+    acc[i & 3] = f2_add(acc[i & 3], f2_pack(ex2_approx(e0), ex2_approx(e1)));
   }
 }
 
@@ -219,8 +244,7 @@ __device__ __forceinline__ Visible visible_queries(const KwParams& p, const uint
 
 template <int D, bool kCap>
 __global__ void __launch_bounds__(kThreads, 1)
-    key_weights_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constant__ CUtensorMap tm_k,
-                       const __grid_constant__ KwParams p) {
+    key_weights_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constant__ KwParams p) {
   extern __shared__ uint8_t smem_raw[];
   using Smem = KwSmem<D>;
   Smem& s = *reinterpret_cast<Smem*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
@@ -233,20 +257,26 @@ __global__ void __launch_bounds__(kThreads, 1)
       mbar_init(&s.ring_full[i], 1);
       mbar_init(&s.ring_empty[i], 1);
     }
-    for (int i = 0; i < kTerms; ++i) {
-      mbar_init(&s.term_full[i], 1);
-      mbar_init(&s.term_empty[i], 4);
+    for (int i = 0; i < kStages; ++i) {
+      mbar_init(&s.q_full[i], 1);
+      mbar_init(&s.stage_empty[i], 4);
     }
     for (int i = 0; i < kBufs; ++i) {
-      mbar_init(&s.q_full[i], 1);
       mbar_init(&s.s_full[i], 1);
       mbar_init(&s.s_empty[i], 4);
     }
     for (int i = 0; i < 2; ++i) {
-      mbar_init(&s.k_full[i], 1);
+      mbar_init(&s.part_full[i], 1);
+      mbar_init(&s.part_read[i], 4);
+      mbar_init(&s.k_full[i], 4);
       mbar_init(&s.drain[i], 1);
     }
     fence_mbar_init();
+  }
+  if (threadIdx.x < 256) {
+    const int i = threadIdx.x;  // 16 bytes of the tile of ones each
+    *reinterpret_cast<uint4*>(s.ones + i * 16) = i / 8 % 2 == 0 ? make_uint4(0x3F803F80u, 0x3F80u, 0u, 0u) : make_uint4(0u, 0u, 0u, 0u);
+    fence_proxy_async_smem();
   }
   if (warp == 1) {
     tmem_alloc(&s.tmem_base, 512);
@@ -337,66 +367,66 @@ __global__ void __launch_bounds__(kThreads, 1)
     // ------------------------------------------------ producer (one lane)
     if (lane == 0) {
       tma_prefetch_desc(&tm_q);
-      tma_prefetch_desc(&tm_k);
       const uint64_t pol = policy_evict_last();
-      uint32_t n = 0, k_loads = 0;
+      uint32_t n = 0, parts = 0;
       uint32_t last1 = 0, last2 = 0;  // items passed when the part before the current one, and the one before that, had ended
       bool ok = true;
-      // item i's scores are computed: its Q stage is free
-      auto done = [&](uint32_t i) -> bool { return mbar_wait(&s.s_full[i % kBufs], (i / kBufs) & 1u, wc); };
-      auto term_free = [&]() -> bool {
-        return n < static_cast<uint32_t>(kTerms) || mbar_wait(&s.term_empty[n % kTerms], (n / kTerms - 1) & 1u, wc);
+      // item i's warpgroup has done with its stage (so its scores are computed); i among the last kStages items
+      auto done = [&](uint32_t i) -> bool { return mbar_wait(&s.stage_empty[i % kStages], (i / kStages) & 1u, wc); };
+      auto stage_free = [&]() -> bool { return n < static_cast<uint32_t>(kStages) || done(n - kStages); };
+      // hands the loaders a K row, or the end
+      auto hand_part = [&](uint32_t row) -> bool {
+        const uint32_t kb = parts & 1u;
+        if (parts >= 2 && !mbar_wait(&s.part_read[kb], (parts / 2 - 1) & 1u, wc)) return false;
+        s.part_row[kb] = row;
+        mbar_arrive(&s.part_full[kb]);
+        ++parts;
+        return true;
       };
       for (uint32_t e = 0; ok; ++e) {
-        const uint32_t slot = e % kRing, st = n % kBufs, ts = n % kTerms;
-        // the three waits' latencies together, when all are long over
-        const bool ready = n >= static_cast<uint32_t>(kTerms) &&
-                           all_complete(smem_u32(&s.ring_full[slot]), (e / kRing) & 1u, smem_u32(&s.s_full[st]),
-                                        (n / kBufs - 1) & 1u, smem_u32(&s.term_empty[ts]), (n / kTerms - 1) & 1u);
+        const uint32_t slot = e % kRing, st = n % kStages;
+        // both waits' latencies together, when both are long over
+        const bool ready = n >= static_cast<uint32_t>(kStages) &&
+                           both_complete(smem_u32(&s.ring_full[slot]), (e / kRing) & 1u, smem_u32(&s.stage_empty[st]),
+                                         (n / kStages - 1) & 1u);
         if (!ready && !mbar_wait(&s.ring_full[slot], (e / kRing) & 1u, wc)) { ok = false; break; }
         const uint4 x = s.entry[slot];
         const uint2 rows = s.rows[slot];
         mbar_arrive(&s.ring_empty[slot]);
         if (x.x & kEnd) break;
-        if (!ready && ((n >= static_cast<uint32_t>(kBufs) && !done(n - kBufs)) || !term_free())) { ok = false; break; }
+        if (!ready && !stage_free()) { ok = false; break; }
         if (x.x & kFirst) {
           // the K buffer's part ended with item last2 - 1
-          for (uint32_t i = n >= kBufs ? n - kBufs + 1 : 0; ok && k_loads >= 2 && i < last2; ++i) ok = done(i);
-          if (!ok) break;
-          const uint32_t kb = k_loads & 1u;
-          mbar_arrive_expect_tx(&s.k_full[kb], kTileBytes);
-          tma_load_3d(s.k[kb], &tm_k, &s.k_full[kb], 0, static_cast<int32_t>(rows.y), 0, pol);
+          for (uint32_t i = n >= kStages ? n - kStages + 1 : 0; ok && parts >= 2 && i < last2; ++i) ok = done(i);
+          if (!ok || !hand_part(rows.y)) { ok = false; break; }
           last2 = last1;
-          ++k_loads;
         }
         last1 = n + 1;
-        const uint32_t k = k_loads - 1;
+        const uint32_t k = parts - 1;
         s.q_info[st] = (k & 1u) | ((k >> 1) & 1u) << 8;
-        mbar_arrive_expect_tx(&s.q_full[st], kTileBytes);
+        s.item[st] = x;
+        mbar_arrive_expect_tx(&s.q_full[st], kTileBytes + Terms<kCap>::kBytes);
         tma_load_3d(s.q[st], &tm_q, &s.q_full[st], 0, static_cast<int32_t>(rows.x), 0, pol);
-        s.item[ts] = x;
-        mbar_arrive_expect_tx(&s.term_full[ts], 512);
-        bulk_load(s.term[ts], p.terms + rows.x, 512, &s.term_full[ts]);
+        bulk_load(s.term[st], static_cast<const uint8_t*>(p.terms) + static_cast<int64_t>(rows.x / 128) * Terms<kCap>::kBytes,
+                  Terms<kCap>::kBytes, &s.q_full[st]);
         ++n;
       }
       const uint32_t loads = n;
-      // the end, to both issuers and the four warpgroups
+      // the end, to the loaders, both issuers and the three warpgroups
+      ok = ok && hand_part(~0u);
       for (int i = 0; ok && i < kBufs; ++i, ++n) {
-        if ((n >= static_cast<uint32_t>(kBufs) && n - kBufs < loads && !done(n - kBufs)) || !term_free()) { ok = false; break; }
-        if (i < 2) {
-          s.q_info[n % kBufs] = kEnd;
-          mbar_arrive(&s.q_full[n % kBufs]);
-        }
-        s.item[n % kTerms] = make_uint4(kEnd, 0u, 0u, 0u);
-        mbar_arrive(&s.term_full[n % kTerms]);
+        ok = stage_free();
+        if (!ok) break;
+        s.q_info[n % kStages] = kEnd;
+        s.item[n % kStages] = make_uint4(kEnd, 0u, 0u, 0u);
+        mbar_arrive(&s.q_full[n % kStages]);
       }
       if (!ok) {
         // the copies in flight land before the CTA exits
         uint32_t dummy_abort = 0;
         WaitCtl dw{nullptr, &dummy_abort, p.wait_ns};
-        for (uint32_t i = loads > kBufs ? loads - kBufs : 0; i < loads; ++i) (void)mbar_wait(&s.q_full[i % kBufs], (i / kBufs) & 1u, dw);
-        for (uint32_t i = loads > kTerms ? loads - kTerms : 0; i < loads; ++i) (void)mbar_wait(&s.term_full[i % kTerms], (i / kTerms) & 1u, dw);
-        for (uint32_t i = k_loads > 2 ? k_loads - 2 : 0; i < k_loads; ++i) (void)mbar_wait(&s.k_full[i & 1u], (i / 2) & 1u, dw);
+        for (uint32_t i = loads > kStages ? loads - kStages : 0; i < loads; ++i)
+          (void)mbar_wait(&s.q_full[i % kStages], (i / kStages) & 1u, dw);
       }
     }
   } else if (warp < 3) {
@@ -404,31 +434,65 @@ __global__ void __launch_bounds__(kThreads, 1)
     constexpr uint32_t idesc = idesc_bf16_f32(128, 128, false, false);
     constexpr uint64_t kTileDesc = kTileBytes >> 4;
     const uint64_t qdesc0 = sdesc_sw128(smem_u32(s.q[0]), 16, 1024);
-    const uint64_t kdesc0 = sdesc_sw128(smem_u32(s.k[0]), 16, 1024);
+    const uint64_t odesc = sdesc_plain(smem_u32(s.ones), 128, 256);
+    const uint64_t tdesc0 = sdesc_plain(smem_u32(s.term[0]), 128, 256);
     for (uint32_t n = static_cast<uint32_t>(warp) - 1u;; n += 2) {
-      const uint32_t b = n % kBufs;
-      if (!mbar_wait_warp(&s.q_full[b], (n / kBufs) & 1u, wc)) break;
-      const uint32_t info = __shfl_sync(0xffffffffu, s.q_info[b], 0);
+      const uint32_t st = n % kStages, b = n % kBufs;
+      if (!mbar_wait_warp(&s.q_full[st], (n / kStages) & 1u, wc)) break;
+      const uint32_t info = __shfl_sync(0xffffffffu, s.q_info[st], 0);
       if (info & kEnd) break;
       const uint32_t kb = info & 1u;
       if (!mbar_wait_warp(&s.k_full[kb], (info >> 8) & 1u, wc)) break;
       if (n >= static_cast<uint32_t>(kBufs) && !mbar_wait_warp(&s.s_empty[b], (n / kBufs - 1) & 1u, wc)) break;
       tc_fence_after();
-      const uint64_t qd = qdesc0 + b * kTileDesc, kd = kdesc0 + kb * kTileDesc;
+      const uint64_t qd = qdesc0 + st * kTileDesc;
+      const uint32_t d = BSA_TMEM(tmem + b * 128, 128u, p.err), ka = BSA_TMEM(tmem + kColK + kb * 64, D / 2u, p.err);
 #pragma unroll
       for (int kk = 0; kk < D / 16; ++kk) {
         const uint64_t off = static_cast<uint64_t>(((kk >> 2) * 16384 + (kk & 3) * 32) >> 4);
-        mma_ss_elect(BSA_TMEM(tmem + b * 128, 128u, p.err), kd + off, qd + off, idesc, kk > 0 ? 1u : 0u);
+        mma_ts_elect(d, ka + kk * 8, qd + off, idesc, kk > 0 ? 1u : 0u);
       }
+      if constexpr (!kCap) mma_ss_elect(d, odesc, tdesc0 + st * (4096 >> 4), idesc, 1u);
       mma_commit_elect(&s.s_full[b]);
     }
     mma_commit_elect(&s.drain[warp - 1]);
     uint32_t dummy_abort = 0;
     WaitCtl dw{p.err, &dummy_abort, p.wait_ns};
     (void)mbar_wait(&s.drain[warp - 1], 0, dw);
+  } else if (warp < kEwWarp0) {
+    // ------------------------------------------------ K into tensor memory: a row per lane
+    const int quarter = warp & 3;
+    for (uint32_t k = 0;; ++k) {
+      const uint32_t kb = k & 1u;
+      if (!mbar_wait_warp(&s.part_full[kb], (k >> 1) & 1u, wc)) break;
+      const uint32_t row = s.part_row[kb];
+      __syncwarp();
+      if (lane == 0) mbar_arrive(&s.part_read[kb]);
+      if (row == ~0u) break;
+      const int64_t r = BSA_RANGE(static_cast<int64_t>(row) + quarter * 32 + lane, int64_t(0),
+                                  static_cast<int64_t>(p.B) * p.Hkv * p.Skv, p.err);
+      const uint4* src = reinterpret_cast<const uint4*>(p.k + r * D);
+      uint32_t v[D / 2];
+#pragma unroll
+      for (int i = 0; i < D / 8; ++i) {
+        const uint4 q = __ldg(src + i);
+        v[4 * i] = q.x;
+        v[4 * i + 1] = q.y;
+        v[4 * i + 2] = q.z;
+        v[4 * i + 3] = q.w;
+      }
+      const uint32_t to = BSA_TMEM(tmem + kColK + kb * 64 + (static_cast<uint32_t>(quarter * 32) << 16), D / 2u, p.err);
+      tc_fence_after();
+#pragma unroll
+      for (int i = 0; i < D / 2; i += 32) tmem_st32(to + i, v + i);
+      tmem_wait_st();
+      tc_fence_before();
+      __syncwarp();
+      if (lane == 0) mbar_arrive(&s.k_full[kb]);
+    }
   } else {
     // ------------------------------------------------ exponentials: warpgroup w takes items w, w + 4, ...
-    const int w = (warp - 4) >> 2, quarter = (warp - 4) & 3;
+    const int w = (warp - kEwWarp0) >> 2, quarter = warp & 3;
     const int r = quarter * 32 + lane;  // key of the tile == tensor-memory lane
     const uint32_t taddr = BSA_TMEM(tmem + w * 128 + (static_cast<uint32_t>(quarter * 32) << 16), 128u, p.err);
     const int32_t parts = c1.tile - c0.tile + (c1.skip > 0 ? 1 : 0);
@@ -441,15 +505,15 @@ __global__ void __launch_bounds__(kThreads, 1)
       for (; part < to; ++part) {
         float a, b;
         f2_unpack(f2_add(f2_add(acc[0], acc[1]), f2_add(acc[2], acc[3])), a, b);
-        p.sums[(static_cast<int64_t>(sums_row(p, blockIdx.x, c0.tile + part)) * 4 + w) * 128 + r] = a + b;
+        p.sums[(static_cast<int64_t>(sums_row(p, blockIdx.x, c0.tile + part)) * kBufs + w) * 128 + r] = a + b;
 #pragma unroll
         for (int i = 0; i < 4; ++i) acc[i] = f2_pack(0.f, 0.f);
       }
     };
     for (uint32_t n = static_cast<uint32_t>(w);; n += kBufs) {
-      const uint32_t ts = n % kTerms;
-      if (!mbar_wait_warp(&s.term_full[ts], (n / kTerms) & 1u, wc)) break;
-      const uint4 x = s.item[ts];
+      const uint32_t st = n % kStages;
+      if (!mbar_wait_warp(&s.q_full[st], (n / kStages) & 1u, wc)) break;
+      const uint4 x = s.item[st];
       if (x.x & kEnd) {
         flush_to(parts);
         break;
@@ -460,7 +524,11 @@ __global__ void __launch_bounds__(kThreads, 1)
       if (masked) m = visible_queries(p, x, static_cast<int64_t>((c0.tile + part) % p.mi.rows) * 128 + r, r);
       if (!mbar_wait_warp(&s.s_full[w], (n / kBufs) & 1u, wc)) break;
       tc_fence_after();
-      const float* term = s.term[ts];
+      const float* term = reinterpret_cast<const float*>(s.term[st]);
+      if constexpr (!kCap) {  // the scores are all that is left of the stage
+        __syncwarp();
+        mbar_arrive_cnt_elect(&s.stage_empty[st], 1u);
+      }
       uint32_t va[32], vb[32];
       if (!masked) {
         // each load runs under the exponentials of the chunk before it (no branch while one is in flight)
@@ -496,8 +564,10 @@ __global__ void __launch_bounds__(kThreads, 1)
         __syncwarp();
         mbar_arrive_cnt_elect(&s.s_empty[w], 1u);
       }
-      __syncwarp();
-      mbar_arrive_cnt_elect(&s.term_empty[ts], 1u);
+      if constexpr (kCap) {
+        __syncwarp();
+        mbar_arrive_cnt_elect(&s.stage_empty[st], 1u);
+      }
     }
   }
 
@@ -509,7 +579,7 @@ __global__ void __launch_bounds__(kThreads, 1)
   }
 }
 
-// One block per tile: its rows of sums (four of each CTA that had a part of it) added up in order.
+// One block per tile: its rows of sums (three of each CTA that had a part of it) added up in order.
 __global__ void __launch_bounds__(128) key_weights_join(const __grid_constant__ KwParams p) {
   griddep_launch_dependents();
   griddep_wait();
@@ -524,8 +594,9 @@ __global__ void __launch_bounds__(128) key_weights_join(const __grid_constant__ 
   }
   float v = 0.f;
   for (int32_t c = lo; c < p.n_cta && (c == lo || (p.cut[c].tile == t && p.cut[c].skip > 0)); ++c) {
-    const float* row = p.sums + static_cast<int64_t>(sums_row(p, c, t)) * 512 + threadIdx.x;
-    v += (row[0] + row[128]) + (row[256] + row[384]);
+    const float* row = p.sums + static_cast<int64_t>(sums_row(p, c, t)) * kBufs * 128 + threadIdx.x;
+#pragma unroll
+    for (int w = 0; w < kBufs; ++w) v += row[w * 128];
   }
   p.out[static_cast<int64_t>(t / p.mi.rows) * p.Skv + t % p.mi.rows * 128 + threadIdx.x] = v;
 }
@@ -565,21 +636,20 @@ void make_cuts(const bsa_key_weights_args* a, const bsa_mask_info* info, KwParam
   }
 }
 
-template <int D>
+template <int D, bool kCap>
 bsa_status launch(const bsa_key_weights_args* a, const KwParams& p, cudaStream_t stream) {
-  CUtensorMap tq, tk;
+  CUtensorMap tq;
   const int64_t q_rows = static_cast<int64_t>(a->B) * a->Hq * a->S_q;
-  if (!make_tmap_bf16_panels(&tq, a->q, q_rows, D, 128) ||
-      !make_tmap_bf16_panels(&tk, a->k, static_cast<uint64_t>(a->B) * a->Hkv * a->S_kv, D, 128))
-    return fail(BSA_ERR_CUDA, "cuTensorMapEncodeTiled rejected a Q/K description");
-  auto kern = p.cap_log2 > 0.f ? key_weights_kernel<D, true> : key_weights_kernel<D, false>;
+  if (!make_tmap_bf16_panels(&tq, a->q, q_rows, D, 128))
+    return fail(BSA_ERR_CUDA, "cuTensorMapEncodeTiled rejected the Q description");
+  auto kern = key_weights_kernel<D, kCap>;
   const size_t smem = sizeof(KwSmem<D>) + 1024;
   const bsa_status st = ensure_smem_attr(reinterpret_cast<const void*>(kern), smem, "set key weights smem size");
   if (st != BSA_OK) return st;
-  cudaError_t e = launch_kernel(key_weights_terms, dim3(static_cast<unsigned>((q_rows / 4 + 255) / 256)), dim3(256), 0, stream, p);
+  cudaError_t e = launch_kernel(key_weights_terms<kCap>, dim3(static_cast<unsigned>((q_rows + 255) / 256)), dim3(256), 0, stream, p);
   if (e == cudaSuccess) e = cudaGetLastError();
   if (e != cudaSuccess) return cuda_fail(e, "key weights terms launch");
-  e = launch_kernel(kern, dim3(p.n_cta), dim3(kThreads), smem, stream, tq, tk, p);
+  e = launch_kernel(kern, dim3(p.n_cta), dim3(kThreads), smem, stream, tq, p);
   if (e == cudaSuccess) e = cudaGetLastError();
   if (e != cudaSuccess) return cuda_fail(e, "key weights launch");
   e = launch_kernel(key_weights_join, dim3(p.n_tiles), dim3(128), 0, stream, p);
@@ -588,12 +658,16 @@ bsa_status launch(const bsa_key_weights_args* a, const KwParams& p, cudaStream_t
   return BSA_OK;
 }
 
+// Floats of the rows of sums: one per warpgroup for each tile and each CTA's two shared parts.
+size_t sums_floats(const bsa_key_weights_args* a, const bsa_mask_info* info) {
+  return (static_cast<size_t>(a->B) * a->Hkv * info->rows + 2 * kMaxCtas) * kBufs * 128;
+}
+
 }  // namespace
 
 size_t key_weights_workspace_bytes(const bsa_key_weights_args* a, const bsa_mask_info* info) {
-  // a row of sums per warpgroup for each tile and each CTA's two shared parts; the exponent terms
-  return ((static_cast<size_t>(a->B) * a->Hkv * info->rows + 2 * kMaxCtas) * 4 * 128 +
-          static_cast<size_t>(a->B) * a->Hq * a->S_q) * sizeof(float);
+  const size_t blocks = static_cast<size_t>(a->B) * a->Hq * (a->S_q / 128);
+  return sums_floats(a, info) * sizeof(float) + blocks * (a->logits_soft_cap > 0.f ? Terms<true>::kBytes : Terms<false>::kBytes);
 }
 
 bsa_status key_weights_launch(const bsa_key_weights_args* a, const bsa_mask_info* info, float scale, cudaStream_t stream) {
@@ -606,23 +680,29 @@ bsa_status key_weights_launch(const bsa_key_weights_args* a, const bsa_mask_info
   p.Hkv = a->Hkv;
   p.Sq = a->S_q;
   p.Skv = a->S_kv;
-  p.scale_log2 = a->logits_soft_cap > 0.f ? scale / a->logits_soft_cap : scale * kLog2e;
-  // (0 would turn the infinity of an unseen score into a NaN; any score times this is as good as 0)
-  if (p.scale_log2 == 0.f) p.scale_log2 = 1e-30f;
+  const bool cap = a->logits_soft_cap > 0.f;
+  p.scale_log2 = cap ? scale / a->logits_soft_cap : scale * kLog2e;
+  // (a scale of 0 would turn what hides a score into a NaN, and the terms are divided by it; products with
+  // anything this small are as good as 0)
+  if (std::fabs(p.scale_log2) < 1e-36f) p.scale_log2 = std::copysign(1e-36f, p.scale_log2);
+  p.term_scale = cap ? -kLog2e : -kLog2e / p.scale_log2;
+  p.hidden = cap ? -INFINITY : std::copysign(3e38f, -p.scale_log2);
   p.cap_log2 = a->logits_soft_cap > 0.f ? a->logits_soft_cap * kLog2e : 0.f;
   p.lse = a->lse;
   p.q_lens = a->q_lens;
   p.out = a->weights;
   p.sums = static_cast<float*>(a->workspace);
   p.n_tiles = a->B * a->Hkv * info->rows;
-  p.terms = p.sums + (static_cast<size_t>(p.n_tiles) + 2 * kMaxCtas) * 4 * 128;
+  p.terms = p.sums + sums_floats(a, info);
+  p.k = static_cast<const __nv_bfloat16*>(a->k);
   p.mi = mask_info_dev(info);
   p.compact = info->shrink ? 1 : 0;
   make_cuts(a, info, &p);
   p.err = device_error_word();
   p.wait_ns = wait_limit_ns();
   if (!p.err) return fail(BSA_ERR_CUDA, "could not allocate the device error word");
-  return a->D == 128 ? launch<128>(a, p, stream) : launch<64>(a, p, stream);
+  if (a->D == 128) return cap ? launch<128, true>(a, p, stream) : launch<128, false>(a, p, stream);
+  return cap ? launch<64, true>(a, p, stream) : launch<64, false>(a, p, stream);
 }
 
 }  // namespace bsa
