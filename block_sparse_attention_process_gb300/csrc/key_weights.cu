@@ -25,7 +25,7 @@
 //   warps 1-2   tcgen05 issuers of the even and the odd items: S^T = K Q^T into
 //               one of three tensor-memory buffers (one issuer needs ~1,100
 //               cycles an item, most of it barrier latency)
-//   warp 3      one lane loads Q per item and its exponent terms
+//   warp 3      loads Q per item and its exponent terms
 //   warps 4-7   bring a tile's K from global into tensor memory (2 buffers)
 //   warps 8-19  exponentials: warpgroup n % 3 takes item n
 // All items of the launch form one sequence, cut into equal runs, one per CTA
@@ -364,70 +364,80 @@ __global__ void __launch_bounds__(kThreads, 1)
       mbar_arrive(&s.ring_full[e % kRing]);
     }
   } else if (warp == 3) {
-    // ------------------------------------------------ producer (one lane)
-    if (lane == 0) {
-      tma_prefetch_desc(&tm_q);
-      const uint64_t pol = policy_evict_last();
-      uint32_t n = 0, parts = 0;
-      uint32_t last1 = 0, last2 = 0;  // items passed when the part before the current one, and the one before that, had ended
-      bool ok = true;
-      // item i's warpgroup has done with its stage (so its scores are computed); i among the last kStages items
-      auto done = [&](uint32_t i) -> bool { return mbar_wait(&s.stage_empty[i % kStages], (i / kStages) & 1u, wc); };
-      auto stage_free = [&]() -> bool { return n < static_cast<uint32_t>(kStages) || done(n - kStages); };
-      // hands the loaders a K row, or the end
-      auto hand_part = [&](uint32_t row) -> bool {
-        const uint32_t kb = parts & 1u;
-        if (parts >= 2 && !mbar_wait(&s.part_read[kb], (parts / 2 - 1) & 1u, wc)) return false;
+    // ------------------------------------------------ producer (whole warp; converged code issues copies faster than one lane's)
+    if (lane == 0) tma_prefetch_desc(&tm_q);
+    __syncwarp();
+    const uint64_t pol = policy_evict_last();
+    uint32_t n = 0, parts = 0;
+    uint32_t last1 = 0, last2 = 0;  // items passed when the part before the current one, and the one before that, had ended
+    bool ok = true;
+    // item i's warpgroup has done with its stage (so its scores are computed); i among the last kStages items
+    auto done = [&](uint32_t i) -> bool { return mbar_wait_warp(&s.stage_empty[i % kStages], (i / kStages) & 1u, wc); };
+    auto stage_free = [&]() -> bool { return n < static_cast<uint32_t>(kStages) || done(n - kStages); };
+    // hands the loaders a K row, or the end
+    auto hand_part = [&](uint32_t row) -> bool {
+      const uint32_t kb = parts & 1u;
+      if (parts >= 2 && !mbar_wait_warp(&s.part_read[kb], (parts / 2 - 1) & 1u, wc)) return false;
+      if (lane == 0) {
         s.part_row[kb] = row;
         mbar_arrive(&s.part_full[kb]);
-        ++parts;
-        return true;
-      };
-      for (uint32_t e = 0; ok; ++e) {
-        const uint32_t slot = e % kRing, st = n % kStages;
-        // both waits' latencies together, when both are long over
-        const bool ready = n >= static_cast<uint32_t>(kStages) &&
-                           both_complete(smem_u32(&s.ring_full[slot]), (e / kRing) & 1u, smem_u32(&s.stage_empty[st]),
-                                         (n / kStages - 1) & 1u);
-        if (!ready && !mbar_wait(&s.ring_full[slot], (e / kRing) & 1u, wc)) { ok = false; break; }
-        const uint4 x = s.entry[slot];
-        const uint2 rows = s.rows[slot];
-        mbar_arrive(&s.ring_empty[slot]);
-        if (x.x & kEnd) break;
-        if (!ready && !stage_free()) { ok = false; break; }
-        if (x.x & kFirst) {
-          // the K buffer's part ended with item last2 - 1
-          for (uint32_t i = n >= kStages ? n - kStages + 1 : 0; ok && parts >= 2 && i < last2; ++i) ok = done(i);
-          if (!ok || !hand_part(rows.y)) { ok = false; break; }
-          last2 = last1;
-        }
-        last1 = n + 1;
-        const uint32_t k = parts - 1;
+      }
+      __syncwarp();
+      ++parts;
+      return true;
+    };
+    for (uint32_t e = 0; ok; ++e) {
+      const uint32_t slot = e % kRing, st = n % kStages;
+      // both waits' latencies together, when both are long over
+      const bool ready =
+          n >= static_cast<uint32_t>(kStages) &&
+          __all_sync(0xffffffffu, both_complete(smem_u32(&s.ring_full[slot]), (e / kRing) & 1u, smem_u32(&s.stage_empty[st]),
+                                                (n / kStages - 1) & 1u));
+      if (!ready && !mbar_wait_warp(&s.ring_full[slot], (e / kRing) & 1u, wc)) { ok = false; break; }
+      const uint4 x = s.entry[slot];
+      const uint32_t qrow = __shfl_sync(0xffffffffu, s.rows[slot].x, 0), krow = s.rows[slot].y;
+      const uint32_t flags = __shfl_sync(0xffffffffu, x.x, 0);
+      mbar_arrive_cnt_elect(&s.ring_empty[slot], 1u);
+      if (flags & kEnd) break;
+      if (!ready && !stage_free()) { ok = false; break; }
+      if (flags & kFirst) {
+        // the K buffer's part ended with item last2 - 1
+        for (uint32_t i = n >= kStages ? n - kStages + 1 : 0; ok && parts >= 2 && i < last2; ++i) ok = done(i);
+        if (!ok || !hand_part(krow)) { ok = false; break; }
+        last2 = last1;
+      }
+      last1 = n + 1;
+      const uint32_t k = parts - 1;
+      if (lane == 0) {
         s.q_info[st] = (k & 1u) | ((k >> 1) & 1u) << 8;
         s.item[st] = x;
-        mbar_arrive_expect_tx(&s.q_full[st], kTileBytes + Terms<kCap>::kBytes);
-        tma_load_3d(s.q[st], &tm_q, &s.q_full[st], 0, static_cast<int32_t>(rows.x), 0, pol);
-        bulk_load(s.term[st], static_cast<const uint8_t*>(p.terms) + static_cast<int64_t>(rows.x / 128) * Terms<kCap>::kBytes,
-                  Terms<kCap>::kBytes, &s.q_full[st]);
-        ++n;
       }
-      const uint32_t loads = n;
-      // the end, to the loaders, both issuers and the three warpgroups
-      ok = ok && hand_part(~0u);
-      for (int i = 0; ok && i < kBufs; ++i, ++n) {
-        ok = stage_free();
-        if (!ok) break;
+      __syncwarp();
+      mbar_arrive_expect_tx_elect(&s.q_full[st], kTileBytes + Terms<kCap>::kBytes);
+      tma_load_3d_elect(s.q[st], &tm_q, &s.q_full[st], 0, static_cast<int32_t>(qrow), 0, pol);
+      bulk_load_elect(s.term[st], static_cast<const uint8_t*>(p.terms) + static_cast<int64_t>(qrow / 128) * Terms<kCap>::kBytes,
+                      Terms<kCap>::kBytes, &s.q_full[st]);
+      ++n;
+    }
+    const uint32_t loads = n;
+    // the end, to the loaders, both issuers and the three warpgroups
+    ok = ok && hand_part(~0u);
+    for (int i = 0; ok && i < kBufs; ++i, ++n) {
+      ok = stage_free();
+      if (!ok) break;
+      if (lane == 0) {
         s.q_info[n % kStages] = kEnd;
         s.item[n % kStages] = make_uint4(kEnd, 0u, 0u, 0u);
         mbar_arrive(&s.q_full[n % kStages]);
       }
-      if (!ok) {
-        // the copies in flight land before the CTA exits
-        uint32_t dummy_abort = 0;
-        WaitCtl dw{nullptr, &dummy_abort, p.wait_ns};
-        for (uint32_t i = loads > kStages ? loads - kStages : 0; i < loads; ++i)
-          (void)mbar_wait(&s.q_full[i % kStages], (i / kStages) & 1u, dw);
-      }
+      __syncwarp();
+    }
+    if (!ok) {
+      // the copies in flight land before the CTA exits
+      uint32_t dummy_abort = 0;
+      WaitCtl dw{nullptr, &dummy_abort, p.wait_ns};
+      for (uint32_t i = loads > kStages ? loads - kStages : 0; i < loads; ++i)
+        (void)mbar_wait(&s.q_full[i % kStages], (i / kStages) & 1u, dw);
     }
   } else if (warp < 3) {
     // ------------------------------------------------ MMA issuers (whole warps): items warp - 1, + 2, ...
@@ -443,7 +453,13 @@ __global__ void __launch_bounds__(kThreads, 1)
       if (info & kEnd) break;
       const uint32_t kb = info & 1u;
       if (!mbar_wait_warp(&s.k_full[kb], (info >> 8) & 1u, wc)) break;
-      if (n >= static_cast<uint32_t>(kBufs) && !mbar_wait_warp(&s.s_empty[b], (n / kBufs - 1) & 1u, wc)) break;
+      // The buffer's last item, n - 3, is the other issuer's.  Its scores are waited for first: without that this
+      // warp could get here while the buffer still holds item n - 6, and take that item's phase of s_empty, two
+      // phases back and of the same parity, for the one it needs.  (Item n - 6's scores are there: the producer
+      // has seen its stage released before it loaded item n - 1.)
+      if (n >= static_cast<uint32_t>(kBufs) && (!mbar_wait_warp(&s.s_full[b], (n / kBufs - 1) & 1u, wc) ||
+                                                !mbar_wait_warp(&s.s_empty[b], (n / kBufs - 1) & 1u, wc)))
+        break;
       tc_fence_after();
       const uint64_t qd = qdesc0 + st * kTileDesc;
       const uint32_t d = BSA_TMEM(tmem + b * 128, 128u, p.err), ka = BSA_TMEM(tmem + kColK + kb * 64, D / 2u, p.err);
