@@ -46,8 +46,8 @@ namespace bsa {
 namespace {
 
 constexpr int kBufs = 3;        // score buffers, warpgroups of the exponentials (item n: n % 3)
-constexpr int kStages = 5;      // Q and exponent terms
-constexpr int kRing = 32;       // items between the walker and the producer
+constexpr int kStages = 6;      // Q and exponent terms
+constexpr int kRing = 32;       // items between the walker and the producer (which reads one per lane)
 constexpr int kBatch = 16;      // items published at once
 constexpr int kEwWarp0 = 8;
 constexpr int kEwWarps = 4 * kBufs;
@@ -138,21 +138,6 @@ __device__ __forceinline__ int32_t sums_row(const KwParams& p, int32_t c, int32_
   const Cut a = p.cut[c], b = p.cut[c + 1];
   const bool whole = !(t == a.tile && a.skip > 0) && !(t == b.tile && b.skip > 0);
   return whole ? t : p.n_tiles + 2 * c + (t == a.tile ? 0 : 1);
-}
-
-// Whether both barriers' phases are complete (one test's latency, not two).
-__device__ __forceinline__ bool both_complete(uint32_t a, uint32_t pa, uint32_t b, uint32_t pb) {
-  uint32_t ok;
-  asm volatile(
-      "{\n\t.reg .pred p, q;\n\t"
-      "mbarrier.test_wait.parity.shared::cta.b64 p, [%1], %2;\n\t"
-      "mbarrier.test_wait.parity.shared::cta.b64 q, [%3], %4;\n\t"
-      "and.pred p, p, q;\n\t"
-      "selp.u32 %0, 1, 0, p;\n\t}"
-      : "=r"(ok)
-      : "r"(a), "r"(pa), "r"(b), "r"(pb)
-      : "memory");
-  return ok != 0u;
 }
 
 // Exponent terms of all queries, one thread each.
@@ -386,20 +371,37 @@ __global__ void __launch_bounds__(kThreads, 1)
       ++parts;
       return true;
     };
-    for (uint32_t e = 0; ok; ++e) {
-      const uint32_t slot = e % kRing, st = n % kStages;
-      // both waits' latencies together, when both are long over
-      const bool ready =
-          n >= static_cast<uint32_t>(kStages) &&
-          __all_sync(0xffffffffu, both_complete(smem_u32(&s.ring_full[slot]), (e / kRing) & 1u, smem_u32(&s.stage_empty[st]),
-                                                (n / kStages - 1) & 1u));
-      if (!ready && !mbar_wait_warp(&s.ring_full[slot], (e / kRing) & 1u, wc)) { ok = false; break; }
-      const uint4 x = s.entry[slot];
-      const uint32_t qrow = __shfl_sync(0xffffffffu, s.rows[slot].x, 0), krow = s.rows[slot].y;
-      const uint32_t flags = __shfl_sync(0xffffffffu, x.x, 0);
-      mbar_arrive_cnt_elect(&s.ring_empty[slot], 1u);
+    // Entries are taken from the ring a batch at a time, one per lane: a wait
+    // per entry, with its two reads, cost more than the copies themselves.
+    uint32_t e = 0, have = 0, next = 0;  // next entry of the ring; entries at hand, and those of them passed
+    uint4 mine = make_uint4(0, 0, 0, 0);
+    uint2 mine_rows = make_uint2(0, 0);
+    while (ok) {
+      if (next == have) {
+        if (!mbar_wait_warp(&s.ring_full[e % kRing], (e / kRing) & 1u, wc)) { ok = false; break; }
+        const uint32_t slot = (e + lane) % kRing;
+        // (kRing lanes: every slot once; a slot whose entry lies a lap ahead shows the phase before it)
+        const uint32_t full = __ballot_sync(0xffffffffu, mbar_test_wait(smem_u32(&s.ring_full[slot]), ((e + lane) / kRing) & 1u));
+        have = full == 0xffffffffu ? 32u : static_cast<uint32_t>(__ffs(~full) - 1);
+        next = 0;
+        if (static_cast<uint32_t>(lane) < have) {
+          mine = s.entry[slot];
+          mine_rows = s.rows[slot];
+          mbar_arrive(&s.ring_empty[slot]);
+        }
+        __syncwarp();
+        e += have;
+        if (have == 0) { ok = false; break; }  // (the wait above has seen entry e)
+      }
+      const uint32_t st = n % kStages;
+      const uint32_t flags = __shfl_sync(0xffffffffu, mine.x, next);
       if (flags & kEnd) break;
-      if (!ready && !stage_free()) { ok = false; break; }
+      const uint32_t qrow = __shfl_sync(0xffffffffu, mine_rows.x, next);
+      const uint4 x = make_uint4(flags, __shfl_sync(0xffffffffu, mine.y, next), __shfl_sync(0xffffffffu, mine.z, next),
+                                 __shfl_sync(0xffffffffu, mine.w, next));
+      const uint32_t krow = __shfl_sync(0xffffffffu, mine_rows.y, next);
+      ++next;
+      if (!stage_free()) { ok = false; break; }
       if (flags & kFirst) {
         // the K buffer's part ended with item last2 - 1
         for (uint32_t i = n >= kStages ? n - kStages + 1 : 0; ok && parts >= 2 && i < last2; ++i) ok = done(i);
@@ -456,7 +458,7 @@ __global__ void __launch_bounds__(kThreads, 1)
       // The buffer's last item, n - 3, is the other issuer's.  Its scores are waited for first: without that this
       // warp could get here while the buffer still holds item n - 6, and take that item's phase of s_empty, two
       // phases back and of the same parity, for the one it needs.  (Item n - 6's scores are there: the producer
-      // has seen its stage released before it loaded item n - 1.)
+      // has seen its stage released before it loaded item n.)
       if (n >= static_cast<uint32_t>(kBufs) && (!mbar_wait_warp(&s.s_full[b], (n / kBufs - 1) & 1u, wc) ||
                                                 !mbar_wait_warp(&s.s_empty[b], (n / kBufs - 1) & 1u, wc)))
         break;
