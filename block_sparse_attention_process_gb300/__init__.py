@@ -328,53 +328,69 @@ def _elsewhere(device, stream):
                 yield
 
 
-def _place(device: torch.device, stream):
+def _place(device: torch.device, index: int, stream):
     """(context, stream handle) of a call on tensors of `device`: inside the
     context the device and the stream are current, so that what the call
     allocates belongs to the stream it is used on."""
-    if not isinstance(stream, (torch.cuda.Stream, type(None))):
-        stream = torch.cuda.ExternalStream(int(stream), device=device) if int(stream) else torch.cuda.default_stream(device)
     if stream is None:
-        handle = torch.cuda.current_stream(device).cuda_stream
-        return (_INLINE if device.index == torch.cuda.current_device() else _elsewhere(device, None)), handle
+        handle = torch._C._cuda_getCurrentRawStream(index)
+        return (_INLINE if index == torch._C._cuda_getDevice() else _elsewhere(device, None)), handle
+    if not isinstance(stream, torch.cuda.Stream):
+        stream = torch.cuda.ExternalStream(int(stream), device=device) if int(stream) else torch.cuda.default_stream(device)
     if stream.device != device:
         raise ValueError(f"the stream is on {stream.device}, the tensors are on {device}")
     return _elsewhere(device, stream), stream.cuda_stream
 
 
-def _check_dev(name: str, t: torch.Tensor, dtype: torch.dtype, device, shape=None) -> None:
-    """A contiguous CUDA tensor of a type, on a device, of a shape."""
-    if t.dtype != dtype or not t.is_cuda or not t.is_contiguous():
-        raise ValueError(f"{name} must be a contiguous CUDA {str(dtype)[6:]} tensor")
-    if device is not None and t.device != device:
-        raise ValueError(f"{name} is on {t.device}, the call's other tensors are on {device}")
-    if shape is not None and t.shape != shape:
+def _need(name: str, t: torch.Tensor, dtype: torch.dtype, index: int, shape) -> int:
+    """The address of a contiguous CUDA tensor of a type and shape on a device."""
+    if t.dtype is not dtype or t.get_device() != index or t.shape != shape or not t.is_contiguous():
+        if t.dtype != dtype or not t.is_cuda or not t.is_contiguous():
+            raise ValueError(f"{name} must be a contiguous CUDA {str(dtype)[6:]} tensor")
+        if t.get_device() != index:
+            raise ValueError(f"{name} is on {t.device}, the call's other tensors are on cuda:{index}")
         raise ValueError(f"{name} must be {list(shape)}, not {list(t.shape)}")
-
-
-def _rows(name: str, t: torch.Tensor, device):
-    """Strides (batch, head, token) of a 4-D bf16 CUDA tensor whose last axis is contiguous."""
-    if t.dtype != torch.bfloat16 or not t.is_cuda or t.dim() != 4:
-        raise ValueError(f"{name} must be a 4-D CUDA bfloat16 tensor")
-    if device is not None and t.device != device:
-        raise ValueError(f"{name} is on {t.device}, the call's other tensors are on {device}")
-    s = t.stride()
-    # (the stride of an axis of length 1 says nothing)
-    st = [0 if t.shape[i] == 1 else s[i] for i in range(3)]
-    if s[3] != 1 or st[0] % 8 or st[1] % 8 or st[2] % 8 or t.data_ptr() % 16:
-        raise ValueError(f"{name} needs a contiguous last axis, other strides that are multiples of 8 and 16-byte alignment")
-    return (C.c_int64 * 3)(*st)
-
-
-def _lens(name: str, t: Optional[torch.Tensor], B: int, device) -> Optional[int]:
-    if t is None:
-        return None
-    _check_dev(name, t, torch.int32, device, (B,))
     return t.data_ptr()
+
+
+def _rows(name: str, t: torch.Tensor, index: int):
+    """Strides (batch, head, token) of a 4-D bf16 CUDA tensor whose last axis is contiguous."""
+    if t.dtype is not torch.bfloat16 or t.get_device() < 0 or t.dim() != 4:
+        raise ValueError(f"{name} must be a 4-D CUDA bfloat16 tensor")
+    if t.get_device() != index:
+        raise ValueError(f"{name} is on {t.device}, the call's other tensors are on cuda:{index}")
+    sb, sh, st, sd = t.stride()
+    if (sb | sh | st) & 7 or sd != 1 or t.data_ptr() & 15:
+        # (the stride of an axis of length 1 says nothing)
+        sb, sh, st, sd = (1 if i == 3 and n == 1 else 0 if n == 1 else s
+                          for i, (n, s) in enumerate(zip(t.shape, (sb, sh, st, sd))))
+        if (sb | sh | st) & 7 or sd != 1 or t.data_ptr() & 15:
+            raise ValueError(f"{name} needs a contiguous last axis, other strides that are multiples of 8 and "
+                             "16-byte alignment")
+    return sb, sh, st
+
+
+def _lens(name: str, t: Optional[torch.Tensor], B: int, index: int) -> int:
+    return 0 if t is None else _need(name, t, torch.int32, index, (B,))
 
 
 def _workspace(need: int, device) -> Optional[torch.Tensor]:
     return torch.empty(need, dtype=torch.uint8, device=device) if need else None
+
+
+# workspace sizes of calls made before, by the shape of the call (host arithmetic, nothing of the data)
+_workspace_sizes: dict = {}
+
+
+def _workspace_size(entry: str, key, args: bytes) -> int:
+    need = _workspace_sizes.get(key)
+    if need is None:
+        n = C.c_size_t(0)
+        check(getattr(_abi.lib(), entry + "_workspace")(args, C.byref(n)), entry)
+        if len(_workspace_sizes) > 4096:
+            _workspace_sizes.clear()
+        need = _workspace_sizes[key] = n.value
+    return need
 
 
 def key_weights(q: torch.Tensor, k: torch.Tensor, lse: torch.Tensor, dkv_info: MaskInfo, *,
@@ -391,18 +407,19 @@ def key_weights(q: torch.Tensor, k: torch.Tensor, lse: torch.Tensor, dkv_info: M
     Hkv, Skv = k.shape[1], k.shape[2]
     if k.shape != (B, Hkv, Skv, D) or k.device != q.device:
         raise ValueError("k must be [B, Hkv, Skv, D] on q's device")
-    _check_dev("lse", lse, torch.float32, q.device, (B, Hq, S))
-    a = _abi.KeyWeightsArgs(_ptr(q), _ptr(k), _ptr(lse), _lens("q_lens", q_lens, B, q.device), None, None, 0, B, Hq, Hkv,
+    index = q.get_device()
+    a = _abi.KeyWeightsArgs(_ptr(q), _ptr(k), _need("lse", lse, torch.float32, index, (B, Hq, S)),
+                            _lens("q_lens", q_lens, B, index) or None, None, None, 0, B, Hq, Hkv,
                             D, S, Skv, math.nan if softmax_scale is None else softmax_scale, logits_soft_cap or 0.0)
-    ctx, handle = _place(q.device, stream)
+    ctx, handle = _place(q.device, index, stream)
     with ctx:
         if out is None:
             out = torch.empty((B, Hkv, Skv), dtype=torch.float32, device=q.device)
-        _check_dev("out", out, torch.float32, q.device, (B, Hkv, Skv))
+        a.weights = _need("out", out, torch.float32, index, (B, Hkv, Skv))
         need = C.c_size_t(0)
         check(_abi.lib().bsa_key_weights_workspace(C.byref(a), dkv_info.handle, C.byref(need)), "bsa_key_weights")
         ws = _workspace(need.value, q.device)
-        a.weights, a.workspace, a.workspace_bytes = _ptr(out), _ptr(ws), need.value
+        a.workspace, a.workspace_bytes = _ptr(ws), need.value
         check(_abi.lib().bsa_key_weights(C.byref(a), dkv_info.handle, handle), "bsa_key_weights")
     return out
 
@@ -415,27 +432,25 @@ class KV4Cache:
     [B, Hkv, capacity] the tokens' positions, or None.  capacity is a multiple of 16."""
 
     __slots__ = ("k_codes", "k_scales", "v_codes", "v_scales", "weights", "positions", "B", "Hkv", "D", "capacity",
-                 "device", "_c")
+                 "device", "index", "_c")
 
     def __init__(self, k_codes: torch.Tensor, k_scales: torch.Tensor, v_codes: torch.Tensor, v_scales: torch.Tensor,
                  weights: Optional[torch.Tensor] = None, positions: Optional[torch.Tensor] = None):
         if k_codes.dim() != 4:
             raise ValueError("k_codes must be [B, Hkv, capacity, D/2]")
-        B, H, n, half = k_codes.shape
-        dev = k_codes.device
-        for name, t, dtype, shape in (("k_codes", k_codes, torch.uint8, (B, H, n, half)),
-                                      ("v_codes", v_codes, torch.uint8, (B, H, n, half)),
-                                      ("k_scales", k_scales, torch.bfloat16, (B, H, n, half // 16)),
-                                      ("v_scales", v_scales, torch.bfloat16, (B, H, n, half // 16)),
-                                      ("weights", weights, torch.float32, (B, H, n)),
-                                      ("positions", positions, torch.int32, (B, H, n))):
-            if t is not None:
-                _check_dev(name, t, dtype, dev, shape)
+        B, H, n, half = shape = k_codes.shape
+        index = k_codes.get_device()
+        if index < 0:
+            raise ValueError("k_codes must be a contiguous CUDA uint8 tensor")
+        scales, slots = (B, H, n, half // 16), (B, H, n)
+        self._c = _abi.KV4_CACHE.pack(
+            _need("k_codes", k_codes, torch.uint8, index, shape), _need("k_scales", k_scales, torch.bfloat16, index, scales),
+            _need("v_codes", v_codes, torch.uint8, index, shape), _need("v_scales", v_scales, torch.bfloat16, index, scales),
+            0 if weights is None else _need("weights", weights, torch.float32, index, slots),
+            0 if positions is None else _need("positions", positions, torch.int32, index, slots), B, H, 2 * half, n)
         self.k_codes, self.k_scales, self.v_codes, self.v_scales = k_codes, k_scales, v_codes, v_scales
         self.weights, self.positions = weights, positions
-        self.B, self.Hkv, self.D, self.capacity, self.device = B, H, 2 * half, n, dev
-        self._c = _abi.Kv4Cache(_ptr(k_codes), _ptr(k_scales), _ptr(v_codes), _ptr(v_scales), _ptr(weights),
-                                _ptr(positions), B, H, 2 * half, n)
+        self.B, self.Hkv, self.D, self.capacity, self.device, self.index = B, H, 2 * half, n, k_codes.device, index
 
     @classmethod
     def empty(cls, B: int, Hkv: int, capacity: int, D: int, device="cuda", weights: bool = True) -> "KV4Cache":
@@ -455,25 +470,24 @@ def kv4_append(cache: KV4Cache, k: torch.Tensor, v: torch.Tensor, start: torch.T
     start[b] + t (int32 [B] on the device).  ``n_new``: tokens past it are padding; ``positions``: position of token
     0 (default start); ``weights`` fp32 [B,Hkv,T]: initial accumulated weights (default 0).  With ``values``
     returns what the cache now holds, (k, v) bf16 [B,Hkv,T,D], 0 for padding."""
-    dev = cache.device
+    dev, index = cache.device, cache.index
     B, H, T, D = k.shape if k.dim() == 4 else (0, 0, 0, 0)
     if (B, H, D) != (cache.B, cache.Hkv, cache.D) or v.shape != k.shape:
         raise ValueError("k and v must both be [B, Hkv, T, D] with the cache's B, Hkv and D")
-    ks, vs = _rows("k", k, dev), _rows("v", v, dev)
-    if weights is not None:
-        _check_dev("weights", weights, torch.float32, dev, (B, H, T))
+    ks, vs = _rows("k", k, index), _rows("v", v, index)
+    w0 = 0 if weights is None else _need("weights", weights, torch.float32, index, (B, H, T))
     if start is None:
         raise ValueError("start is missing")
-    ctx, handle = _place(dev, stream)
+    ctx, handle = _place(dev, index, stream)
     with ctx:
         kv = vv = None
         if values:
             kv = torch.empty((B, H, T, D), dtype=torch.bfloat16, device=dev)
-            vv = torch.empty((B, H, T, D), dtype=torch.bfloat16, device=dev)
-        a = _abi.Kv4AppendArgs(cache._c, _ptr(k), _ptr(v), ks, vs, T, _lens("start", start, B, dev),
-                               _lens("n_new", n_new, B, dev), _lens("positions", positions, B, dev), _ptr(weights),
-                               _ptr(kv), _ptr(vv))
-        check(_abi.lib().bsa_kv4_append(C.byref(a), handle), "bsa_kv4_append")
+            vv = torch.empty_like(kv)
+        args = cache._c + _abi.KV4_APPEND_REST.pack(
+            k.data_ptr(), v.data_ptr(), *ks, *vs, T, _lens("start", start, B, index), _lens("n_new", n_new, B, index),
+            _lens("positions", positions, B, index), w0, kv.data_ptr() if values else 0, vv.data_ptr() if values else 0)
+        check(_abi.lib().bsa_kv4_append(args, handle), "bsa_kv4_append")
     return (kv, vv) if values else None
 
 
@@ -485,35 +499,33 @@ def kv4_fwd(q: torch.Tensor, cache: KV4Cache, lens: torch.Tensor, *, q_lens: Opt
     axis, e.g. a transposed [B,T,Hq,D]), lens int32 [B] on the device: keys held, the new tokens' own included
     -> (o bf16 [B,Hq,T,D], lse fp32 [B,Hq,T]).  ``q_lens``: new tokens per sequence (default T).  With
     ``accumulate`` every key's probabilities are added to cache.weights."""
-    dev = cache.device
-    qs = _rows("q", q, dev)
+    dev, index = cache.device, cache.index
+    qs = _rows("q", q, index)
     B, Hq, T, D = q.shape
-    if (B, D) != (cache.B, cache.D):
+    if B != cache.B or D != cache.D:
         raise ValueError("q must be [B, Hq, T, D] with the cache's B and D")
     if lens is None:
         raise ValueError("lens is missing")
-    sp, sn, skv = _sink_fields(sinks, cache.Hkv)
+    sp, sn, skv = (0, 0, 0) if sinks is None else _sink_fields(sinks, cache.Hkv)
     if sinks is not None and sinks.device != dev:
         raise ValueError(f"sinks is on {sinks.device}, the call's other tensors are on {dev}")
-    ctx, handle = _place(dev, stream)
+    ctx, handle = _place(dev, index, stream)
     with ctx:
         if o is None:
             o = torch.empty((B, Hq, T, D), dtype=torch.bfloat16, device=dev)
-        if o.shape != q.shape:
+        elif o.shape != q.shape:
             raise ValueError("o must have q's shape")
-        os = _rows("o", o, dev)
         if lse is None:
             lse = torch.empty((B, Hq, T), dtype=torch.float32, device=dev)
-        _check_dev("lse", lse, torch.float32, dev, (B, Hq, T))
-        a = _abi.Kv4FwdArgs(cache._c, _ptr(q), _ptr(o), _ptr(lse), qs, os, Hq, T, _lens("lens", lens, B, dev),
-                            _lens("q_lens", q_lens, B, dev), math.nan if softmax_scale is None else softmax_scale,
-                            logits_soft_cap or 0.0, sp, sn, skv, 1 if accumulate else 0, None, 0)
-        need = C.c_size_t(0)
-        L = _abi.lib()
-        check(L.bsa_kv4_fwd_workspace(C.byref(a), C.byref(need)), "bsa_kv4_fwd")
-        ws = _workspace(need.value, dev)
-        a.workspace, a.workspace_bytes = _ptr(ws), need.value
-        check(L.bsa_kv4_fwd(C.byref(a), handle), "bsa_kv4_fwd")
+        head = (q.data_ptr(), o.data_ptr(), _need("lse", lse, torch.float32, index, (B, Hq, T)), *qs, *_rows("o", o, index),
+                Hq, T, _lens("lens", lens, B, index), _lens("q_lens", q_lens, B, index),
+                math.nan if softmax_scale is None else softmax_scale, logits_soft_cap or 0.0, sp, sn, skv,
+                1 if accumulate else 0)
+        pack = _abi.KV4_FWD_REST.pack
+        need = _workspace_size("bsa_kv4_fwd", (index, B, cache.Hkv, D, cache.capacity, Hq, T, accumulate),
+                               cache._c + pack(*head, 0, 0))
+        ws = torch.empty(need, dtype=torch.uint8, device=dev)
+        check(_abi.lib().bsa_kv4_fwd(cache._c + pack(*head, ws.data_ptr(), need), handle), "bsa_kv4_fwd")
     return o, lse
 
 
@@ -523,30 +535,31 @@ def kv4_evict(cache: KV4Cache, lens: torch.Tensor, keep: int, *, recent: int = 0
     ``recent`` positions (of ``seen`` tokens, default lens) before all others.  In place, or into ``out`` (another
     cache of at least ``keep`` slots).  -> (new lens int32 [B], index int32 [B,Hkv,keep]: the slot each kept token
     had, -1 past the new length), with ``values`` also (k, v) bf16 [B,Hkv,keep,D] of the kept slots."""
-    dev = cache.device
+    dev, index = cache.device, cache.index
     dst = cache if out is None else out
-    if dst.device != dev:
+    if dst.index != index:
         raise ValueError(f"out is on {dst.device}, the cache is on {dev}")
     if lens is None:
         raise ValueError("lens is missing")
     B, H, D = cache.B, cache.Hkv, cache.D
-    a = _abi.Kv4EvictArgs(cache._c, dst._c, _lens("lens", lens, B, dev), _lens("seen", seen, B, dev), keep, recent)
-    need = C.c_size_t(0)
+    caches, pack = cache._c + dst._c, _abi.KV4_EVICT_REST.pack
+    head = (_lens("lens", lens, B, index), _lens("seen", seen, B, index), keep, recent)
+    n = C.c_size_t(0)
     L = _abi.lib()
-    check(L.bsa_kv4_evict_workspace(C.byref(a), C.byref(need)), "bsa_kv4_evict")
-    ctx, handle = _place(dev, stream)
+    check(L.bsa_kv4_evict_workspace(caches + pack(*head, 0, 0, 0, 0, 0, 0), C.byref(n)), "bsa_kv4_evict")
+    ctx, handle = _place(dev, index, stream)
     with ctx:
         new_lens = torch.empty((B,), dtype=torch.int32, device=dev)
-        index = torch.empty((B, H, keep), dtype=torch.int32, device=dev)
+        slots = torch.empty((B, H, keep), dtype=torch.int32, device=dev)
         kv = vv = None
         if values:
             kv = torch.empty((B, H, keep, D), dtype=torch.bfloat16, device=dev)
-            vv = torch.empty((B, H, keep, D), dtype=torch.bfloat16, device=dev)
-        ws = _workspace(need.value, dev)
-        a.new_lens, a.index, a.k_values, a.v_values = _ptr(new_lens), _ptr(index), _ptr(kv), _ptr(vv)
-        a.workspace, a.workspace_bytes = _ptr(ws), need.value
-        check(L.bsa_kv4_evict(C.byref(a), handle), "bsa_kv4_evict")
-    return (new_lens, index, kv, vv) if values else (new_lens, index)
+            vv = torch.empty_like(kv)
+        ws = _workspace(n.value, dev)
+        check(L.bsa_kv4_evict(caches + pack(*head, new_lens.data_ptr(), slots.data_ptr(), kv.data_ptr() if values else 0,
+                                            vv.data_ptr() if values else 0, 0 if ws is None else ws.data_ptr(), n.value),
+                              handle), "bsa_kv4_evict")
+    return (new_lens, slots, kv, vv) if values else (new_lens, slots)
 
 
 def get_device_error(stream=None) -> int:

@@ -8,6 +8,7 @@ from __future__ import annotations
 
 import ctypes as C
 import os
+import struct
 
 HERE = os.path.dirname(os.path.abspath(__file__))
 # BSA_LIBRARY_VARIANT=debug loads the range-checked build (see build.py)
@@ -109,6 +110,18 @@ class Kv4EvictArgs(C.Structure):
                 ("workspace_bytes", C.c_size_t)]
 
 
+# The kv4 calls are made once a token, so their arguments are packed with
+# struct (a third of the time a ctypes.Structure of as many fields takes): the
+# cache, which every call begins with, and what follows it.
+KV4_CACHE = struct.Struct("@6P3iq")
+KV4_APPEND_REST = struct.Struct("@2P6qq6P")
+KV4_FWD_REST = struct.Struct("@3P6qiqPPffPiiiPN")
+KV4_EVICT_REST = struct.Struct("@2P2q5PN")
+for _s, _rest in ((Kv4AppendArgs, KV4_APPEND_REST), (Kv4FwdArgs, KV4_FWD_REST)):
+    assert KV4_CACHE.size + _rest.size == C.sizeof(_s)
+assert 2 * KV4_CACHE.size + KV4_EVICT_REST.size == C.sizeof(Kv4EvictArgs)
+
+
 # name -> (restype, argtypes); every symbol include/bsa.h declares
 SIGNATURES = {
     "bsa_mask_compile": (C.c_int, [C.POINTER(MaskSpec), C.POINTER(MaskOpts), C.c_void_p, C.POINTER(C.c_void_p)]),
@@ -124,11 +137,11 @@ SIGNATURES = {
     "bsa_bwd_dq": (C.c_int, [C.POINTER(BwdArgs), C.c_void_p, C.c_void_p]),
     "bsa_key_weights": (C.c_int, [C.POINTER(KeyWeightsArgs), C.c_void_p, C.c_void_p]),
     "bsa_key_weights_workspace": (C.c_int, [C.POINTER(KeyWeightsArgs), C.c_void_p, C.POINTER(C.c_size_t)]),
-    "bsa_kv4_append": (C.c_int, [C.POINTER(Kv4AppendArgs), C.c_void_p]),
-    "bsa_kv4_fwd": (C.c_int, [C.POINTER(Kv4FwdArgs), C.c_void_p]),
-    "bsa_kv4_fwd_workspace": (C.c_int, [C.POINTER(Kv4FwdArgs), C.POINTER(C.c_size_t)]),
-    "bsa_kv4_evict": (C.c_int, [C.POINTER(Kv4EvictArgs), C.c_void_p]),
-    "bsa_kv4_evict_workspace": (C.c_int, [C.POINTER(Kv4EvictArgs), C.POINTER(C.c_size_t)]),
+    "bsa_kv4_append": (C.c_int, [C.c_void_p, C.c_void_p]),
+    "bsa_kv4_fwd": (C.c_int, [C.c_void_p, C.c_void_p]),
+    "bsa_kv4_fwd_workspace": (C.c_int, [C.c_void_p, C.POINTER(C.c_size_t)]),
+    "bsa_kv4_evict": (C.c_int, [C.c_void_p, C.c_void_p]),
+    "bsa_kv4_evict_workspace": (C.c_int, [C.c_void_p, C.POINTER(C.c_size_t)]),
     "bsa_get_device_error": (C.c_int, [C.c_void_p, C.POINTER(C.c_uint32)]),
     "bsa_set_wait_limit_ns": (C.c_int, [C.c_uint64]),
     "bsa_debug_wait_timeout": (C.c_int, [C.c_void_p]),
