@@ -524,8 +524,8 @@ def kv4_fwd(q: torch.Tensor, cache: KV4Cache, lens: torch.Tensor, *, q_lens: Opt
         pack = _abi.KV4_FWD_REST.pack
         need = _workspace_size("bsa_kv4_fwd", (index, B, cache.Hkv, D, cache.capacity, Hq, T, accumulate),
                                cache._c + pack(*head, 0, 0))
-        ws = torch.empty(need, dtype=torch.uint8, device=dev)
-        check(_abi.lib().bsa_kv4_fwd(cache._c + pack(*head, ws.data_ptr(), need), handle), "bsa_kv4_fwd")
+        ws = _workspace(need, dev)
+        check(_abi.lib().bsa_kv4_fwd(cache._c + pack(*head, 0 if ws is None else ws.data_ptr(), need), handle), "bsa_kv4_fwd")
     return o, lse
 
 

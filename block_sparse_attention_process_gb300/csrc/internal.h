@@ -75,6 +75,7 @@ size_t key_weights_workspace_bytes(const bsa_key_weights_args* a, const bsa_mask
 bsa_status kv4_append_launch(const bsa_kv4_append_args* a, cudaStream_t stream);
 bsa_status kv4_fwd_launch(const bsa_kv4_fwd_args* a, float scale, cudaStream_t stream);
 size_t kv4_fwd_workspace_bytes(const bsa_kv4_fwd_args* a);
+bool kv4_fwd_fits(const bsa_kv4_fwd_args* a);  // its grids
 bsa_status kv4_evict_launch(const bsa_kv4_evict_args* a, cudaStream_t stream);
 size_t kv4_evict_workspace_bytes(const bsa_kv4_evict_args* a);
 bsa_status debug_wait_timeout_launch(cudaStream_t stream);

@@ -81,6 +81,7 @@ bsa_status check_fwd(const bsa_kv4_fwd_args* a) {
   if (a->T <= 0) return bad("T must be positive");
   if (static_cast<int64_t>(a->cache.B) * a->Hq > INT32_MAX / a->T)
     return fail(BSA_ERR_UNSUPPORTED, "B*Hq*T must fit in int32");
+  if (!kv4_fwd_fits(a)) return fail(BSA_ERR_UNSUPPORTED, "too many rows or slots for one launch");
   if (a->accumulate != 0 && a->accumulate != 1) return bad("accumulate must be 0 or 1");
   if (a->accumulate && !a->cache.weights) return bad("accumulate needs the cache's weights");
   s = check_cap(a->logits_soft_cap);

@@ -19,19 +19,25 @@
 // row's largest magnitude to [2^14, 2^15); elements 2^-24 times smaller start
 // to lose bits); a probability times its value scale is rounded to fp16.
 //
-// The running reference of a row is R = max(s_j + log2 of the largest value
-// scale of j), so that p s never leaves fp16's range however the scales of the
-// keys differ; l = sum 2^(s_j - R) stays in fp32.  It moves only when it grows
-// by more than 8 (log2 units).
+// p s is kept in fp16's range however the scales differ.  A warp takes the
+// exponent of its first keys' largest value scale as a base, and p s 2^-base
+// is what is rounded; a key whose largest scale is not within a factor of two
+// of the base enters the running reference as R = max(s_j + e_j), e_j its
+// exponent less the base (0 for the others, so that hardly any key pays for
+// it).  l = sum 2^(s_j - R) stays in fp32.  R moves only when it grows by more
+// than 8 (log2 units).
 //
 // Work: all (sequence, head, row tile) pairs' key tiles of 128 form one
 // sequence, cut into equal runs, one per CTA; lengths are read on the device.
 // A run's parts of pairs that other CTAs share go to the workspace as (R, l,
 // O) records; a second kernel joins them in a fixed order and, if asked,
 // turns the stored scores into probabilities and adds them to the weights.
-// Eight warps take 16 keys of a tile each; one lane of warp 0 brings tiles in
-// by bulk copies through a ring of stages (a warp of its own for that would
-// leave 96 registers a thread instead of 128, and spill).
+// Short sequences (a capacity of up to 8 tiles) go a pair to a CTA instead, and
+// nothing is joined.
+// Four warps take 32 keys of a tile each, as two products side by side; the
+// warps take turns in bringing tiles in by bulk copies through a ring of
+// stages.  (Eight warps of 16 keys, one of them loading, needed 453
+// instructions per 16 keys and reached 3.1 TB/s on 64 sequences of 8191 keys.)
 #include <cmath>
 
 #include <cuda_fp16.h>
@@ -44,8 +50,10 @@ namespace bsa {
 namespace {
 
 constexpr int kTileKeys = 128;
-constexpr int kWarps = 8;                  // 16 keys of a tile each
+constexpr int kWarps = 4;                  // 32 keys of a tile each, as two halves of 16
+constexpr int kWholeTiles = 8;             // longest pair, in tiles, that one CTA takes alone
 constexpr int kThreads = 32 * kWarps;
+constexpr int kWeightKeys = 1024;           // keys of one head whose weights a CTA of the join adds to
 constexpr float kRescale = 8.0f;
 constexpr float kLog2e = 1.4426950408889634f;
 constexpr float kLn2 = 0.69314718055994530942f;
@@ -64,6 +72,7 @@ struct Kv4FwdParams {
   const float* sinks;
   int32_t n_sinks, sinks_kv;
   int32_t n_cta;
+  int32_t whole;            // CTA c takes pair c, all of it
   float* rec_stat;          // [2 * n_cta][2][kRows]: R and l of a CTA's first and last part
   float* rec_o;             // [2 * n_cta][kRows][D]
   float* scores;            // [B * Hkv * row_tiles][capacity][score_stride], log2 units, or null
@@ -96,17 +105,6 @@ __device__ __forceinline__ int64_t total_tiles(const Kv4FwdParams& p) {
   const int64_t per = static_cast<int64_t>(p.c.Hkv) * p.row_tiles;
   int64_t sum = 0;
   for (int32_t b = lane; b < p.c.B; b += 32) sum += load_pair(p, b, nullptr).tiles * per;
-#pragma unroll
-  for (int o = 16; o > 0; o >>= 1) sum += __shfl_xor_sync(0xffffffffu, sum, o);
-  return sum;
-}
-
-// First tile of sequence b (b uniform over the warp).
-__device__ __forceinline__ int64_t tiles_before(const Kv4FwdParams& p, int32_t b) {
-  const int lane = threadIdx.x & 31;
-  const int64_t per = static_cast<int64_t>(p.c.Hkv) * p.row_tiles;
-  int64_t sum = 0;
-  for (int32_t i = lane; i < b; i += 32) sum += load_pair(p, i, nullptr).tiles * per;
 #pragma unroll
   for (int o = 16; o > 0; o >>= 1) sum += __shfl_xor_sync(0xffffffffu, sum, o);
   return sum;
@@ -159,7 +157,22 @@ struct Run {
       pair = load_pair(p, b, nullptr);
     }
   }
+  // the whole of pair c (even one without tiles), as a run of one part
+  __device__ __forceinline__ void init_whole(const Kv4FwdParams& p, int32_t c, uint32_t* err) {
+    rt = c % p.row_tiles;
+    bh = c / p.row_tiles;
+    pair = load_pair(p, bh / p.c.Hkv, err);
+    at = -1;
+  }
   __device__ bool next(const Kv4FwdParams& p) {
+    if (p.whole) {
+      if (at == 0) return false;
+      at = 0;
+      k0 = 0;
+      k1 = pair.tiles;
+      whole = true;
+      return true;
+    }
     if (at >= end) return false;
     const int64_t per = static_cast<int64_t>(p.c.Hkv) * p.row_tiles;
     while (at >= seq0 + pair.tiles * per) {
@@ -181,20 +194,20 @@ struct Run {
 template <int D, int NT>
 struct __align__(128) FwdShared {
   static constexpr int kRows = 8 * NT;
-  static constexpr int kStages = D == 128 ? 5 : 8;
-  // tiles issued ahead of the one being computed: the stage written is the one
-  // released two tiles ago, so the issuing lane hardly ever waits
-  static constexpr int kAhead = kStages - 2;
-  static constexpr int kPad = D + 4;  // floats between rows of the merge buffer (bank spread)
+  static constexpr int kStages = D == 128 ? 3 : 4;
+  static constexpr int kAhead = kStages - 1;  // tiles issued before the one being computed
+  static constexpr int kPad = D + 4;          // floats between rows of the merge buffer (bank spread)
   uint8_t k[kStages][kTileKeys * Kv4<D>::kRowBytes];
   uint8_t v[kStages][kTileKeys * Kv4<D>::kRowBytes];
   uint8_t ks[kStages][kTileKeys * Kv4<D>::kScaleBytes];
   uint8_t vs[kStages][kTileKeys * Kv4<D>::kScaleBytes];
-  float merge[4][kRows * kPad];
+  float merge[kWarps / 2][kRows * kPad];
   float stat[2][kWarps][kRows];
+  float lse2[kRows];
   uint64_t full[kStages], empty[kStages];
-  Run ahead;          // the loading lane's place in the CTA's run
-  int32_t ahead_tile; // next key tile of that part
+  Run ahead;            // the loader's place in the CTA's run
+  int32_t ahead_tile;   // next key tile of that part
+  uint32_t issued;      // tiles loaded, or on their way
   uint32_t abort_flag;
 };
 
@@ -252,23 +265,26 @@ __device__ __forceinline__ void lds(uint32_t (&w)[N], const void* p) {
   }
 }
 
-// log2 of the largest finite scale of a key's groups, rounded down, kept
-// within +-100 (a key without one, all zeros or NaN, counts as the smallest).
+// Largest scale of a key's groups, as bf16 bits.
 template <int W>
-__device__ __forceinline__ float scale_exponent(const uint32_t (&w)[W]) {
+__device__ __forceinline__ uint32_t top_scale(const uint32_t (&w)[W]) {
+  uint32_t m = w[0];
+#pragma unroll
+  for (int i = 1; i < W; ++i) m = __vmaxu2(m, w[i]);
+  return max(m & 0xFFFFu, m >> 16);
+}
+
+// A key's exponent against the base: 0 within a factor of two of it, else the
+// exponent of its largest finite scale (a key without one counts as the
+// smallest) less the base, kept within +-100.
+__device__ __noinline__ float far_exponent(uint32_t w0, uint32_t w1, int base) {
+  const uint32_t w[4] = {w0 & 0xFFFFu, w0 >> 16, w1 & 0xFFFFu, w1 >> 16};
   uint32_t m = 0;
 #pragma unroll
-  for (int i = 0; i < W; ++i) m = max(m, max(w[i] & 0xFFFFu, w[i] >> 16));
-  if (m >= 0x7F80u) {
-    m = 0;
-#pragma unroll
-    for (int i = 0; i < W; ++i) {
-      if ((w[i] & 0xFFFFu) < 0x7F80u) m = max(m, w[i] & 0xFFFFu);
-      if ((w[i] >> 16) < 0x7F80u) m = max(m, w[i] >> 16);
-    }
-  }
-  const int e = static_cast<int>(m >> 7) - 127;
-  return static_cast<float>(min(max(e, -100), 100));
+  for (int i = 0; i < 4; ++i)
+    if (w[i] < 0x7F80u) m = max(m, w[i]);
+  const int e = min(max(static_cast<int>(m >> 7) - 127 - base, -100), 100);
+  return e >= -1 && e <= 1 ? 0.f : static_cast<float>(e);
 }
 
 // ------------------------------------------------------------------ results
@@ -305,10 +321,23 @@ __device__ __forceinline__ void store_o4(__nv_bfloat16* o, const float4& x, floa
   *reinterpret_cast<uint2*>(o) = make_uint2(pack_bf16x2(x.x * f, x.y * f), pack_bf16x2(x.z * f, x.w * f));
 }
 
-__device__ __forceinline__ void compute_barrier() { asm volatile("bar.sync 1, %0;" ::"n"(32 * kWarps) : "memory"); }
+// Sum of the probabilities of key j over the rows of a row tile that see it.
+template <int kRows>
+__device__ __forceinline__ float key_probs(const Kv4FwdParams& p, const Pair& pair, int32_t bh, int32_t rt, int32_t j,
+                                           const float* lse2) {
+  const float* sc = p.scores + ((static_cast<int64_t>(bh) * p.row_tiles + rt) * p.c.capacity + j) * p.score_stride;
+  const int32_t rows = min(kRows, p.R - rt * kRows);
+  float w = 0.f;
+  int32_t t = rt * kRows % p.T;
+  for (int32_t i = 0; i < rows; ++i) {
+    if (t < pair.nq && j < pair.len - pair.nq + t + 1) w += ex2_approx(sc[i] - lse2[i]);
+    if (++t == p.T) t = 0;
+  }
+  return w;
+}
 
 template <int D, int NT, bool kCap>
-__global__ void __launch_bounds__(kThreads, NT == 1 ? 2 : 1) kv4_fwd_kernel(const __grid_constant__ Kv4FwdParams p) {
+__global__ void __launch_bounds__(kThreads, NT == 1 ? 3 : 2) kv4_fwd_kernel(const __grid_constant__ Kv4FwdParams p) {
   extern __shared__ __align__(128) uint8_t smem_raw[];
   using Sh = FwdShared<D, NT>;
   Sh& s = *reinterpret_cast<Sh*>(smem_raw);
@@ -327,21 +356,27 @@ __global__ void __launch_bounds__(kThreads, NT == 1 ? 2 : 1) kv4_fwd_kernel(cons
   griddep_launch_dependents();
   griddep_wait();
   const WaitCtl wc{p.err, &s.abort_flag, p.wait_ns};
-  const int64_t total = total_tiles(p);
-  const int32_t n_cta = runs(p, total);
-  if (static_cast<int32_t>(blockIdx.x) >= n_cta) return;
   Run run;
-  run.init(p, first_tile(blockIdx.x, total, n_cta), first_tile(blockIdx.x + 1, total, n_cta), warp == 0 ? p.err : nullptr);
+  if (p.whole) {
+    run.init_whole(p, blockIdx.x, threadIdx.x == 0 ? p.err : nullptr);
+  } else {
+    const int64_t total = total_tiles(p);
+    const int32_t n_cta = runs(p, total);
+    if (static_cast<int32_t>(blockIdx.x) >= n_cta) return;
+    run.init(p, first_tile(blockIdx.x, total, n_cta), first_tile(blockIdx.x + 1, total, n_cta), warp == 0 ? p.err : nullptr);
+  }
 
-  // lane 0 of warp 0: the next tile of the run into its stage
-  uint32_t issued = 0;
-  auto load_next = [&]() -> bool {
+  // One lane: tile `n` of the run into its stage, if there is one; true if that went well.
+  auto load_tile = [&](uint32_t n) -> bool {
+    const uint32_t st = n % kStages;
+    // (also orders this loader after the one before it, which another warp may have been)
+    if (n >= static_cast<uint32_t>(kStages) && !mbar_wait(&s.empty[st], (n / kStages - 1) & 1u, wc)) return false;
     if (s.ahead_tile >= s.ahead.k1) {
-      if (!s.ahead.next(p)) return true;
+      do {
+        if (!s.ahead.next(p)) return true;
+      } while (s.ahead.k0 >= s.ahead.k1);
       s.ahead_tile = s.ahead.k0;
     }
-    const uint32_t st = issued % kStages;
-    if (issued >= static_cast<uint32_t>(kStages) && !mbar_wait(&s.empty[st], (issued / kStages - 1) & 1u, wc)) return false;
     const int32_t kt = s.ahead_tile++;
     const int64_t key = static_cast<int64_t>(s.ahead.bh) * p.c.capacity + static_cast<int64_t>(kt) * kTileKeys;
     // whole sixteens of keys: the capacity is a multiple of 16
@@ -351,7 +386,7 @@ __global__ void __launch_bounds__(kThreads, NT == 1 ? 2 : 1) kv4_fwd_kernel(cons
     bulk_load(s.ks[st], static_cast<const uint8_t*>(p.c.k_scales) + key * kScaleBytes, keys * kScaleBytes, &s.full[st]);
     bulk_load(s.v[st], static_cast<const uint8_t*>(p.c.v_codes) + key * kRowBytes, keys * kRowBytes, &s.full[st]);
     bulk_load(s.vs[st], static_cast<const uint8_t*>(p.c.v_scales) + key * kScaleBytes, keys * kScaleBytes, &s.full[st]);
-    ++issued;
+    s.issued = n + 1;
     return true;
   };
   bool ok = true;
@@ -359,17 +394,21 @@ __global__ void __launch_bounds__(kThreads, NT == 1 ? 2 : 1) kv4_fwd_kernel(cons
     s.ahead = run;
     s.ahead.k1 = 0;
     s.ahead_tile = 0;
-    for (int i = 0; ok && i < Sh::kAhead; ++i) ok = load_next();
+    s.issued = 0;
+    for (int i = 0; ok && i < Sh::kAhead; ++i) ok = load_tile(i);
   }
-  ok = __all_sync(0xffffffffu, ok);
+  ok = __syncthreads_and(ok);
 
-  // -------------------------------------------------- compute warps
   const int g8 = lane >> 2, t4 = lane & 3;  // fragment row / column pair
   // V rows of this lane: keys 2 t4, 2 t4 + 1 (+ 8), the one that lies in the
   // other bank half first in lanes 2 and 3 (kv4.cuh), put right by the byte selectors
   const int v_first = t4 >> 1;
   const uint32_t sel_lo = v_first ? 0x1054u : 0x5410u, sel_hi = v_first ? 0x3276u : 0x7632u;
-  uint32_t n = 0;
+  // this lane's places in a stage
+  const int k_at = (warp * 32 + g8) * kRowBytes + t4 * (kRowBytes / 4), s_at = (warp * 32 + g8) * kScaleBytes;
+  const int v_at = (warp * 32 + 2 * t4 + v_first) * kRowBytes + (D == 128 ? g8 ^ ((t4 & 1) << 2) : g8) * (kRowBytes / 8);
+  const int v_next = v_first ? -kRowBytes : kRowBytes;
+  uint32_t n = 0, st = 0, parity = 0;
   bool first_part = true;
   while (run.next(p)) {
     const int32_t h = run.bh % p.c.Hkv;
@@ -412,11 +451,11 @@ __global__ void __launch_bounds__(kThreads, NT == 1 ? 2 : 1) kv4_fwd_kernel(cons
         }
         sum[g] = 0.f;
 #pragma unroll
-        for (int st = 0; st < 2; ++st) {  // elements 2 st (+4) and 2 st + 1 (+4): see kv4.cuh
-          const __half2 even = __floats2half2_rn(x[2 * st], x[2 * st + 4]);
-          const __half2 odd = __floats2half2_rn(x[2 * st + 1], x[2 * st + 5]);
-          qb[nt][g][2 * st] = *reinterpret_cast<const uint32_t*>(&even);
-          qb[nt][g][2 * st + 1] = *reinterpret_cast<const uint32_t*>(&odd);
+        for (int hf = 0; hf < 2; ++hf) {  // elements 2 hf (+4) and 2 hf + 1 (+4): see kv4.cuh
+          const __half2 even = __floats2half2_rn(x[2 * hf], x[2 * hf + 4]);
+          const __half2 odd = __floats2half2_rn(x[2 * hf + 1], x[2 * hf + 5]);
+          qb[nt][g][2 * hf] = *reinterpret_cast<const uint32_t*>(&even);
+          qb[nt][g][2 * hf + 1] = *reinterpret_cast<const uint32_t*>(&odd);
           const float2 fe = __half22float2(even), fo = __half22float2(odd);
           sum[g] += fe.x + fe.y + 16.f * (fo.x + fo.y);
         }
@@ -433,8 +472,7 @@ __global__ void __launch_bounds__(kThreads, NT == 1 ? 2 : 1) kv4_fwd_kernel(cons
         qf[nt][i] = __shfl_sync(0xffffffffu, f, from);
         lim[nt][i] = __shfl_sync(0xffffffffu, last, from);
       }
-      const bool real = in;
-      int32_t lo = real ? last : INT32_MAX, hi = last;
+      int32_t lo = in ? last : INT32_MAX, hi = last;
 #pragma unroll
       for (int o = 4; o < 32; o *= 2) {
         lo = min(lo, __shfl_xor_sync(0xffffffffu, lo, o));
@@ -455,77 +493,108 @@ __global__ void __launch_bounds__(kThreads, NT == 1 ? 2 : 1) kv4_fwd_kernel(cons
       R[nt][0] = R[nt][1] = -INFINITY;
       l[nt][0] = l[nt][1] = 0.f;
     }
+    int base = INT32_MAX;        // base exponent of the value scales (uniform over the warp; not yet chosen)
+    uint32_t near_lo = 0;        // bf16 bits from here on, for three binades, are near it
+    float down = 1.f, up_back = 1.f;  // 2^-base, 2^base
 
     for (int32_t kt = run.k0; kt < run.k1; ++kt, ++n) {
-      const uint32_t st = n % kStages;
       // (after a wait that ran out the loop goes on without waiting, on whatever
       // the stages hold: the barriers between the warps stay matched)
-      if (threadIdx.x == 0 && ok) ok = load_next();
-      ok = __all_sync(0xffffffffu, ok);
-      if (ok) ok = mbar_wait_warp(&s.full[st], (n / kStages) & 1u, wc);
-      const int32_t key0 = kt * kTileKeys + warp * 16;
+      if (static_cast<int>(n % kWarps) == warp) {
+        if (lane == 0 && ok) ok = load_tile(n + Sh::kAhead);
+        ok = __all_sync(0xffffffffu, ok);
+      }
+      if (ok) ok = mbar_wait_warp(&s.full[st], parity, wc);
+      const int32_t key0 = kt * kTileKeys + warp * 32;
       if (key0 < lim_max) {
-        const bool all_seen = key0 + 16 <= lim_min;
-        // ---- scores
-        uint32_t ka[kGroups], kb[kGroups], sa[kGroups / 2], sb[kGroups / 2];
-        const uint8_t* krow = s.k[st] + (warp * 16 + g8) * kRowBytes + t4 * (kRowBytes / 4);
-        lds(ka, krow);
-        lds(kb, krow + 8 * kRowBytes);
-        const uint8_t* srow = s.ks[st] + (warp * 16 + g8) * kScaleBytes;
-        lds(sa, srow);
-        lds(sb, srow + 8 * kScaleBytes);
-        float x[NT][4];
+        const bool all_seen = key0 + 32 <= lim_min;
+        // ---- scores of both halves
+        float x[2][NT][4];
 #pragma unroll
-        for (int nt = 0; nt < NT; ++nt)
+        for (int u = 0; u < 2; ++u) {
+          uint32_t ka[kGroups], kb[kGroups], sa[kGroups / 2], sb[kGroups / 2];
+          lds(ka, s.k[st] + k_at + u * 16 * kRowBytes);
+          lds(kb, s.k[st] + k_at + (u * 16 + 8) * kRowBytes);
+          lds(sa, s.ks[st] + s_at + u * 16 * kScaleBytes);
+          lds(sb, s.ks[st] + s_at + (u * 16 + 8) * kScaleBytes);
 #pragma unroll
-          for (int i = 0; i < 4; ++i) x[nt][i] = 0.f;
-#pragma unroll
-        for (int g = 0; g < kGroups; ++g) {
-          const float fa = g & 1 ? bf16_hi(sa[g / 2]) : bf16_lo(sa[g / 2]);
-          const float fb = g & 1 ? bf16_hi(sb[g / 2]) : bf16_lo(sb[g / 2]);
-#pragma unroll
-          for (int nt = 0; nt < NT; ++nt) {
-            float c[4];
-            mma_f16_from(c, ka[g] & 0x000F000Fu, kb[g] & 0x000F000Fu, ka[g] & 0x00F000F0u, kb[g] & 0x00F000F0u,
-                         qb[nt][g][0], qb[nt][g][1], init[nt][g][0], init[nt][g][1]);
+          for (int g = 0; g < kGroups; ++g) {
+            const float fa = g & 1 ? bf16_hi(sa[g / 2]) : bf16_lo(sa[g / 2]);
+            const float fb = g & 1 ? bf16_hi(sb[g / 2]) : bf16_lo(sb[g / 2]);
             const uint32_t a8 = ka[g] >> 8, b8 = kb[g] >> 8;
-            mma_f16(c, a8 & 0x000F000Fu, b8 & 0x000F000Fu, a8 & 0x00F000F0u, b8 & 0x00F000F0u, qb[nt][g][2], qb[nt][g][3]);
-            x[nt][0] = fmaf(fa, c[0], x[nt][0]);
-            x[nt][1] = fmaf(fa, c[1], x[nt][1]);
-            x[nt][2] = fmaf(fb, c[2], x[nt][2]);
-            x[nt][3] = fmaf(fb, c[3], x[nt][3]);
+#pragma unroll
+            for (int nt = 0; nt < NT; ++nt) {
+              float c[4];
+              mma_f16_from(c, ka[g] & 0x000F000Fu, kb[g] & 0x000F000Fu, ka[g] & 0x00F000F0u, kb[g] & 0x00F000F0u,
+                           qb[nt][g][0], qb[nt][g][1], init[nt][g][0], init[nt][g][1]);
+              mma_f16(c, a8 & 0x000F000Fu, b8 & 0x000F000Fu, a8 & 0x00F000F0u, b8 & 0x00F000F0u, qb[nt][g][2], qb[nt][g][3]);
+              x[u][nt][0] = g ? fmaf(fa, c[0], x[u][nt][0]) : fa * c[0];
+              x[u][nt][1] = g ? fmaf(fa, c[1], x[u][nt][1]) : fa * c[1];
+              x[u][nt][2] = g ? fmaf(fb, c[2], x[u][nt][2]) : fb * c[2];
+              x[u][nt][3] = g ? fmaf(fb, c[3], x[u][nt][3]) : fb * c[3];
+            }
           }
         }
+        // ---- value scales: are all keys' near the base?
+        uint32_t va[2][kGroups / 2], vb[2][kGroups / 2];
+#pragma unroll
+        for (int u = 0; u < 2; ++u) {
+          lds(va[u], s.vs[st] + s_at + u * 16 * kScaleBytes);
+          lds(vb[u], s.vs[st] + s_at + (u * 16 + 8) * kScaleBytes);
+        }
+        const uint32_t t0 = top_scale(va[0]), t1 = top_scale(vb[0]), t2 = top_scale(va[1]), t3 = top_scale(vb[1]);
+        if (base == INT32_MAX) {
+          // (once a part) the largest finite one of these keys'
+          uint32_t m = 0;
+          const uint32_t tops[4] = {t0, t1, t2, t3};
+#pragma unroll
+          for (int i = 0; i < 4; ++i)
+            if (tops[i] < 0x7F80u && key0 + g8 + 8 * i < run.pair.len) m = max(m, tops[i]);
+#pragma unroll
+          for (int o = 4; o < 32; o *= 2) m = max(m, __shfl_xor_sync(0xffffffffu, m, o));
+          base = min(max(static_cast<int>(m >> 7) - 127, -100), 100);
+          near_lo = static_cast<uint32_t>(base + 126) << 7;
+          down = exp2f(static_cast<float>(-base));
+          up_back = exp2f(static_cast<float>(base));
+        }
+        const bool near = max(max(t0 - near_lo, t1 - near_lo), max(t2 - near_lo, t3 - near_lo)) < (3u << 7);
+        float e[4] = {0.f, 0.f, 0.f, 0.f};
+        if (!__all_sync(0xffffffffu, near)) {
+          e[0] = far_exponent(va[0][0], va[0][kGroups / 2 - 1], base);
+          e[1] = far_exponent(vb[0][0], vb[0][kGroups / 2 - 1], base);
+          e[2] = far_exponent(va[1][0], va[1][kGroups / 2 - 1], base);
+          e[3] = far_exponent(vb[1][0], vb[1][kGroups / 2 - 1], base);
+        }
         // ---- softmax
-        uint32_t va[kGroups / 2], vb[kGroups / 2];
-        const uint8_t* vsrow = s.vs[st] + (warp * 16 + g8) * kScaleBytes;
-        lds(va, vsrow);
-        lds(vb, vsrow + 8 * kScaleBytes);
-        const float ea = scale_exponent(va), eb = scale_exponent(vb);
-        uint32_t pb[NT][kGroups][2];
+        float pr[2][NT][4];
 #pragma unroll
         for (int nt = 0; nt < NT; ++nt) {
 #pragma unroll
-          for (int i = 0; i < 4; ++i) {
-            x[nt][i] *= qf[nt][i & 1];
-            if constexpr (kCap) x[nt][i] = p.cap_log2 * tanh_fast(x[nt][i]);
-          }
+          for (int u = 0; u < 2; ++u)
+#pragma unroll
+            for (int i = 0; i < 4; ++i) {
+              x[u][nt][i] *= qf[nt][i & 1];
+              if constexpr (kCap) x[u][nt][i] = p.cap_log2 * tanh_fast(x[u][nt][i]);
+            }
           if (!all_seen) {
 #pragma unroll
-            for (int i = 0; i < 4; ++i)
-              if (key0 + g8 + (i >> 1) * 8 >= lim[nt][i & 1]) x[nt][i] = -INFINITY;
+            for (int u = 0; u < 2; ++u)
+#pragma unroll
+              for (int i = 0; i < 4; ++i)
+                if (key0 + 16 * u + g8 + (i >> 1) * 8 >= lim[nt][i & 1]) x[u][nt][i] = -INFINITY;
           }
-          if (p.scores) {
-            float* out = p.scores + (head * p.c.capacity + key0 + g8) * p.score_stride + nt * 8 + 2 * t4;
-            if (nt * 8 + 2 * t4 < p.score_stride) {
-              *reinterpret_cast<float2*>(out) = make_float2(x[nt][0], x[nt][1]);
-              *reinterpret_cast<float2*>(out + 8 * p.score_stride) = make_float2(x[nt][2], x[nt][3]);
+          if (p.scores && nt * 8 + 2 * t4 < p.score_stride) {
+#pragma unroll
+            for (int u = 0; u < 2; ++u) {
+              if (key0 + 16 * u >= p.c.capacity) continue;
+              float* out = p.scores + (head * p.c.capacity + key0 + 16 * u + g8) * p.score_stride + nt * 8 + 2 * t4;
+              *reinterpret_cast<float2*>(out) = make_float2(x[u][nt][0], x[u][nt][1]);
+              *reinterpret_cast<float2*>(out + 8 * p.score_stride) = make_float2(x[u][nt][2], x[u][nt][3]);
             }
           }
-          float pr[4];
 #pragma unroll
           for (int i = 0; i < 2; ++i) {
-            float m = fmaxf(x[nt][i] + ea, x[nt][i + 2] + eb);
+            float m = fmaxf(fmaxf(x[0][nt][i] + e[0], x[0][nt][i + 2] + e[1]), fmaxf(x[1][nt][i] + e[2], x[1][nt][i + 2] + e[3]));
 #pragma unroll
             for (int o = 4; o < 32; o *= 2) m = fmaxf(m, __shfl_xor_sync(0xffffffffu, m, o));
             const bool move = m > R[nt][i] + kRescale;
@@ -542,55 +611,65 @@ __global__ void __launch_bounds__(kThreads, NT == 1 ? 2 : 1) kv4_fwd_kernel(cons
               }
             }
             const float ref = R[nt][i] == -INFINITY ? 0.f : R[nt][i];
-            pr[i] = ex2_approx(x[nt][i] - ref);
-            pr[i + 2] = ex2_approx(x[nt][i + 2] - ref);
-            l[nt][i] += pr[i] + pr[i + 2];
-          }
-          // probabilities times value scales, transposed into the second product's operand
 #pragma unroll
-          for (int g = 0; g < kGroups; ++g) {
-            const float fa = g & 1 ? bf16_hi(va[g / 2]) : bf16_lo(va[g / 2]);
-            const float fb = g & 1 ? bf16_hi(vb[g / 2]) : bf16_lo(vb[g / 2]);
-            float w[4] = {pr[0] * fa, pr[1] * fa, pr[2] * fb, pr[3] * fb};
-            if (!all_seen) {  // (an unseen slot's scale may be anything)
-#pragma unroll
-              for (int i = 0; i < 4; ++i)
-                if (x[nt][i] == -INFINITY) w[i] = 0.f;
+            for (int u = 0; u < 2; ++u) {
+              pr[u][nt][i] = ex2_approx(x[u][nt][i] - ref);
+              pr[u][nt][i + 2] = ex2_approx(x[u][nt][i + 2] - ref);
             }
-            pb[nt][g][0] = transpose8x8(pack_f16x2(w[0], w[1]));
-            pb[nt][g][1] = transpose8x8(pack_f16x2(w[2], w[3]));
+            l[nt][i] += (pr[0][nt][i] + pr[0][nt][i + 2]) + (pr[1][nt][i] + pr[1][nt][i + 2]);
           }
         }
-        // ---- output
-        uint32_t v0[kGroups / 2], v1[kGroups / 2], v8[kGroups / 2], v9[kGroups / 2];
-        const int piece = D == 128 ? g8 ^ ((t4 & 1) << 2) : g8;
-        const uint8_t* vrow = s.v[st] + (warp * 16 + 2 * t4) * kRowBytes + piece * (kRowBytes / 8);
-        lds(v0, vrow + v_first * kRowBytes);
-        lds(v1, vrow + (v_first ^ 1) * kRowBytes);
-        lds(v8, vrow + (8 + v_first) * kRowBytes);
-        lds(v9, vrow + (8 + (v_first ^ 1)) * kRowBytes);
+        // ---- output, a half at a time
 #pragma unroll
-        for (int g = 0; g < kGroups; ++g) {
-          const uint32_t sel = g & 1 ? sel_hi : sel_lo;
-          const uint32_t lo = __byte_perm(v0[g / 2], v1[g / 2], sel), hi = __byte_perm(v8[g / 2], v9[g / 2], sel);
-          // elements 4 g8 + 0..3 of the group: rows g8 and (times 16) g8 + 8 of two products
-          const uint32_t a0 = minus8(lo & 0x000F000Fu, 0x00080008u), a1 = minus8(lo & 0x00F000F0u, 0x00800080u);
-          const uint32_t a2 = minus8(hi & 0x000F000Fu, 0x00080008u), a3 = minus8(hi & 0x00F000F0u, 0x00800080u);
-          const uint32_t lo8 = lo >> 8, hi8 = hi >> 8;
-          const uint32_t c0 = minus8(lo8 & 0x000F000Fu, 0x00080008u), c1 = minus8(lo8 & 0x00F000F0u, 0x00800080u);
-          const uint32_t c2 = minus8(hi8 & 0x000F000Fu, 0x00080008u), c3 = minus8(hi8 & 0x00F000F0u, 0x00800080u);
+        for (int u = 0; u < 2; ++u) {
+          uint32_t v0[kGroups / 2], v1[kGroups / 2], v8[kGroups / 2], v9[kGroups / 2];
+          const uint8_t* vrow = s.v[st] + v_at + u * 16 * kRowBytes;
+          lds(v0, vrow);
+          lds(v1, vrow + v_next);
+          lds(v8, vrow + 8 * kRowBytes);
+          lds(v9, vrow + 8 * kRowBytes + v_next);
 #pragma unroll
-          for (int nt = 0; nt < NT; ++nt) {
-            mma_f16(acc[nt][2 * g], a0, a1, a2, a3, pb[nt][g][0], pb[nt][g][1]);
-            mma_f16(acc[nt][2 * g + 1], c0, c1, c2, c3, pb[nt][g][0], pb[nt][g][1]);
+          for (int g = 0; g < kGroups; ++g) {
+            // probabilities times value scales, transposed into the second product's operand
+            const float fa = (g & 1 ? bf16_hi(va[u][g / 2]) : bf16_lo(va[u][g / 2])) * down;
+            const float fb = (g & 1 ? bf16_hi(vb[u][g / 2]) : bf16_lo(vb[u][g / 2])) * down;
+            uint32_t b0[NT], b1[NT];
+#pragma unroll
+            for (int nt = 0; nt < NT; ++nt) {
+              float w[4] = {pr[u][nt][0] * fa, pr[u][nt][1] * fa, pr[u][nt][2] * fb, pr[u][nt][3] * fb};
+              if (!all_seen) {  // (an unseen slot's scale may be anything)
+#pragma unroll
+                for (int i = 0; i < 4; ++i)
+                  if (x[u][nt][i] == -INFINITY) w[i] = 0.f;
+              }
+              b0[nt] = transpose8x8(pack_f16x2(w[0], w[1]));
+              b1[nt] = transpose8x8(pack_f16x2(w[2], w[3]));
+            }
+            const uint32_t sel = g & 1 ? sel_hi : sel_lo;
+            const uint32_t lo = __byte_perm(v0[g / 2], v1[g / 2], sel), hi = __byte_perm(v8[g / 2], v9[g / 2], sel);
+            // elements 4 g8 + 0..3 of the group: rows g8 and (times 16) g8 + 8 of two products
+            const uint32_t a0 = minus8(lo & 0x000F000Fu, 0x00080008u), a1 = minus8(lo & 0x00F000F0u, 0x00800080u);
+            const uint32_t a2 = minus8(hi & 0x000F000Fu, 0x00080008u), a3 = minus8(hi & 0x00F000F0u, 0x00800080u);
+            const uint32_t lo8 = lo >> 8, hi8 = hi >> 8;
+            const uint32_t c0 = minus8(lo8 & 0x000F000Fu, 0x00080008u), c1 = minus8(lo8 & 0x00F000F0u, 0x00800080u);
+            const uint32_t c2 = minus8(hi8 & 0x000F000Fu, 0x00080008u), c3 = minus8(hi8 & 0x00F000F0u, 0x00800080u);
+#pragma unroll
+            for (int nt = 0; nt < NT; ++nt) {
+              mma_f16(acc[nt][2 * g], a0, a1, a2, a3, b0[nt], b1[nt]);
+              mma_f16(acc[nt][2 * g + 1], c0, c1, c2, c3, b0[nt], b1[nt]);
+            }
           }
         }
       }
       __syncwarp();
       if (lane == 0) mbar_arrive(&s.empty[st]);
+      if (++st == kStages) {
+        st = 0;
+        parity ^= 1u;
+      }
     }
 
-    // ---- the eight warps' parts into one
+    // ---- the warps' parts into one
 #pragma unroll
     for (int nt = 0; nt < NT; ++nt)
 #pragma unroll
@@ -602,36 +681,31 @@ __global__ void __launch_bounds__(kThreads, NT == 1 ? 2 : 1) kv4_fwd_kernel(cons
           s.stat[1][warp][nt * 8 + 2 * t4 + i] = l[nt][i];
         }
       }
-    compute_barrier();
-    float4 mine[NT][2][kGroups];
-#pragma unroll
-    for (int nt = 0; nt < NT; ++nt)
-#pragma unroll
-      for (int i = 0; i < 2; ++i) {
-        float m = -INFINITY;
-#pragma unroll
-        for (int w = 0; w < kWarps; ++w) m = fmaxf(m, s.stat[0][w][nt * 8 + 2 * t4 + i]);
-        const float f = R[nt][i] == -INFINITY ? (l[nt][i] == 0.f ? 0.f : 1.f) : ex2_approx(R[nt][i] - m);
-        const float f24 = f * 16777216.f;
-#pragma unroll
-        for (int g = 0; g < kGroups; ++g) {
-          mine[nt][i][g] = make_float4(acc[nt][2 * g][i] * f24, acc[nt][2 * g][i + 2] * (f24 * 0.0625f),
-                                       acc[nt][2 * g + 1][i] * f24, acc[nt][2 * g + 1][i + 2] * (f24 * 0.0625f));
-        }
-      }
+    __syncthreads();
     auto slot = [&](int nt, int i, int g) -> float4* {
-      return reinterpret_cast<float4*>(&s.merge[warp & 3][(nt * 8 + 2 * t4 + i) * Sh::kPad + 32 * g + 4 * g8]);
+      return reinterpret_cast<float4*>(&s.merge[warp % (kWarps / 2)][(nt * 8 + 2 * t4 + i) * Sh::kPad + 32 * g + 4 * g8]);
     };
-    if (warp >= 4) {
+    // this warp's share of a column's output, for the common reference
+    auto share = [&](int nt, int i, int g) -> float4 {
+      float m = -INFINITY;
+#pragma unroll
+      for (int w = 0; w < kWarps; ++w) m = fmaxf(m, s.stat[0][w][nt * 8 + 2 * t4 + i]);
+      const float f = R[nt][i] == -INFINITY ? (l[nt][i] == 0.f ? 0.f : 1.f) : ex2_approx(R[nt][i] - m);
+      const float even = f * 16777216.f, odd = even * 0.0625f;
+      // (2^base by itself: it may be far from 1)
+      return make_float4(acc[nt][2 * g][i] * even * up_back, acc[nt][2 * g][i + 2] * odd * up_back,
+                         acc[nt][2 * g + 1][i] * even * up_back, acc[nt][2 * g + 1][i + 2] * odd * up_back);
+    };
+    if (warp >= kWarps / 2) {
 #pragma unroll
       for (int nt = 0; nt < NT; ++nt)
 #pragma unroll
         for (int i = 0; i < 2; ++i)
 #pragma unroll
-          for (int g = 0; g < kGroups; ++g) *slot(nt, i, g) = mine[nt][i][g];
+          for (int g = 0; g < kGroups; ++g) *slot(nt, i, g) = share(nt, i, g);
     }
-    compute_barrier();
-    if (warp < 4) {
+    __syncthreads();
+    if (warp < kWarps / 2) {
 #pragma unroll
       for (int nt = 0; nt < NT; ++nt)
 #pragma unroll
@@ -639,13 +713,13 @@ __global__ void __launch_bounds__(kThreads, NT == 1 ? 2 : 1) kv4_fwd_kernel(cons
 #pragma unroll
           for (int g = 0; g < kGroups; ++g) {
             float4* at = slot(nt, i, g);
-            const float4 a = *at, b = mine[nt][i][g];
+            const float4 a = *at, b = share(nt, i, g);
             *at = make_float4(a.x + b.x, a.y + b.y, a.z + b.z, a.w + b.w);
           }
     }
-    compute_barrier();
+    __syncthreads();
     const int32_t rec = 2 * static_cast<int32_t>(blockIdx.x) + (first_part ? 0 : 1);
-    for (int idx = threadIdx.x; idx < kRows * D / 4; idx += 32 * kWarps) {
+    for (int idx = threadIdx.x; idx < kRows * D / 4; idx += kThreads) {
       const int row = idx / (D / 4), d = idx % (D / 4) * 4;
       float m = -INFINITY, L = 0.f;
 #pragma unroll
@@ -655,7 +729,7 @@ __global__ void __launch_bounds__(kThreads, NT == 1 ? 2 : 1) kv4_fwd_kernel(cons
         if (s.stat[1][w][row] != 0.f) L += s.stat[1][w][row] * (m == -INFINITY ? 1.f : ex2_approx(s.stat[0][w][row] - m));
       float4 x = make_float4(0.f, 0.f, 0.f, 0.f);
 #pragma unroll
-      for (int w = 0; w < 4; ++w) {
+      for (int w = 0; w < kWarps / 2; ++w) {
         const float4 y = *reinterpret_cast<const float4*>(&s.merge[w][row * Sh::kPad + d]);
         x.x += y.x;
         x.y += y.y;
@@ -668,7 +742,10 @@ __global__ void __launch_bounds__(kThreads, NT == 1 ? 2 : 1) kv4_fwd_kernel(cons
           float f;
           const float lse2 = finish_row(p, h, m, L, f);
           store_o4(o_row(p, run.bh, r) + d, x, f);
-          if (d == 0) p.lse[lse_index(p, run.bh, r)] = lse2 * kLn2;
+          if (d == 0) {
+            s.lse2[row] = lse2;
+            p.lse[lse_index(p, run.bh, r)] = lse2 * kLn2;
+          }
         }
       } else {
         *reinterpret_cast<float4*>(p.rec_o + (static_cast<int64_t>(rec) * kRows + row) * D + d) = x;
@@ -679,70 +756,136 @@ __global__ void __launch_bounds__(kThreads, NT == 1 ? 2 : 1) kv4_fwd_kernel(cons
       }
     }
     first_part = false;
+    if (p.whole && p.scores) {
+      // (one row tile) this CTA's own scores into probabilities
+      __syncthreads();
+      for (int32_t j = threadIdx.x; j < run.pair.len; j += kThreads)
+        p.c.weights[static_cast<int64_t>(run.bh) * p.c.capacity + j] += key_probs<kRows>(p, run.pair, run.bh, 0, j, s.lse2);
+    }
   }
-  if (threadIdx.x == 0 && !ok) {  // let the copies in flight land before the CTA exits
+  if (!__syncthreads_and(ok) && threadIdx.x == 0) {
+    // the copies in flight land before the CTA exits
     uint32_t dummy_abort = 0;
     WaitCtl dw{nullptr, &dummy_abort, p.wait_ns};
-    for (uint32_t i = issued > kStages ? issued - kStages : 0; i < issued; ++i)
+    for (uint32_t i = s.issued > kStages ? s.issued - kStages : 0; i < s.issued; ++i)
       (void)mbar_wait(&s.full[i % kStages], (i / kStages) & 1u, dw);
   }
 }
 
-// The records of pair `hr` (b, h, row tile) of sequence b: those of CTAs c0 ..
-// c1, a CTA's being its first part unless its run began in an earlier pair.
+// The records of a pair: CTAs c0 .. c1, a CTA's being its first part unless its
+// run began in an earlier pair (which only c0's can have).
 struct Records {
-  int32_t c0, c1, n;
-  int64_t begin, total;
+  int32_t c0, c1, first;  // first: c0's record
   int32_t tiles;
+  __device__ __forceinline__ int32_t of(int32_t c) const { return c == c0 ? first : 2 * c; }
 };
 
-__device__ __forceinline__ Records pair_records(const Kv4FwdParams& p, int32_t bh, int32_t rt) {
-  Records x;
+__device__ __forceinline__ Records pair_records(const Kv4FwdParams& p, int32_t bh, int32_t rt, const Pair& pair) {
+  // tiles of all sequences, and of those before this one
+  const int lane = threadIdx.x & 31;
   const int32_t b = bh / p.c.Hkv, h = bh % p.c.Hkv;
-  x.total = total_tiles(p);
-  x.n = runs(p, x.total);
-  x.tiles = load_pair(p, b, nullptr).tiles;
-  x.begin = tiles_before(p, b) + (static_cast<int64_t>(h) * p.row_tiles + rt) * x.tiles;
-  x.c0 = x.c1 = 0;
-  if (x.tiles > 0) {
-    x.c0 = cta_of(x.begin, x.total, x.n);
-    x.c1 = cta_of(x.begin + x.tiles - 1, x.total, x.n);
+  const int64_t per = static_cast<int64_t>(p.c.Hkv) * p.row_tiles;
+  int64_t total = 0, before = 0;
+  for (int32_t i = lane; i < p.c.B; i += 32) {
+    const int64_t t = load_pair(p, i, nullptr).tiles * per;
+    total += t;
+    if (i < b) before += t;
+  }
+#pragma unroll
+  for (int o = 16; o > 0; o >>= 1) {
+    total += __shfl_xor_sync(0xffffffffu, total, o);
+    before += __shfl_xor_sync(0xffffffffu, before, o);
+  }
+  Records x{0, 0, 0, pair.tiles};
+  if (pair.tiles > 0) {
+    const int32_t n = runs(p, total);
+    const int64_t begin = before + (static_cast<int64_t>(h) * p.row_tiles + rt) * pair.tiles;
+    x.c0 = cta_of(begin, total, n);
+    x.c1 = cta_of(begin + pair.tiles - 1, total, n);
+    x.first = 2 * x.c0 + (first_tile(x.c0, total, n) < begin ? 1 : 0);
   }
   return x;
 }
 
-__device__ __forceinline__ int32_t record_of(const Records& x, int32_t c) {
-  return 2 * c + (first_tile(c, x.total, x.n) < x.begin ? 1 : 0);
+constexpr int kJoinThreads = 256;
+
+// Joins records: every row of the pair's reference and sum, by the whole CTA.
+template <int kRows>
+__device__ __forceinline__ void join_stats(const Kv4FwdParams& p, const Records& x, float (*part)[2][kRows], float* R, float* L) {
+  constexpr int kSub = 32 / kRows;  // records side by side in a warp
+  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5, row = lane % kRows;
+  float m = -INFINITY, l = 0.f;
+  for (int32_t c = x.c0 + warp * kSub + lane / kRows; c <= x.c1; c += kJoinThreads / kRows) {
+    const float* st = p.rec_stat + x.of(c) * 2 * kRows + row;
+    const float mc = st[0], lc = st[kRows];
+    const float to = fmaxf(m, mc);
+    l = (l == 0.f ? 0.f : l * (to == -INFINITY ? 1.f : ex2_approx(m - to))) +
+        (lc == 0.f ? 0.f : lc * (to == -INFINITY ? 1.f : ex2_approx(mc - to)));
+    m = to;
+  }
+  auto add = [](float& m, float& l, float mc, float lc) {
+    const float to = fmaxf(m, mc);
+    l = (l == 0.f ? 0.f : l * (to == -INFINITY ? 1.f : ex2_approx(m - to))) +
+        (lc == 0.f ? 0.f : lc * (to == -INFINITY ? 1.f : ex2_approx(mc - to)));
+    m = to;
+  };
+#pragma unroll
+  for (int o = kRows; o < 32; o *= 2) {
+    const float mc = __shfl_xor_sync(0xffffffffu, m, o), lc = __shfl_xor_sync(0xffffffffu, l, o);
+    add(m, l, mc, lc);
+  }
+  __syncthreads();
+  if (lane < kRows) {
+    part[warp][0][row] = m;
+    part[warp][1][row] = l;
+  }
+  __syncthreads();
+  if (threadIdx.x < kRows) {
+    m = part[0][0][threadIdx.x];
+    l = part[0][1][threadIdx.x];
+    for (int w = 1; w < kJoinThreads / 32; ++w) add(m, l, part[w][0][threadIdx.x], part[w][1][threadIdx.x]);
+    R[threadIdx.x] = m;
+    L[threadIdx.x] = l;
+  }
+  __syncthreads();
 }
 
 template <int D, int NT>
-__global__ void __launch_bounds__(256) kv4_join_kernel(const __grid_constant__ Kv4FwdParams p) {
+__global__ void __launch_bounds__(kJoinThreads) kv4_join_kernel(const __grid_constant__ Kv4FwdParams p) {
   constexpr int kRows = 8 * NT;
-  constexpr int kVec = D / 4;           // lanes (float4) of one row
-  constexpr int kSplit = 256 / kVec;    // records read side by side
+  constexpr int kVec = D / 4;                 // lanes (float4) of one row
+  constexpr int kSplit = kJoinThreads / kVec;  // records read side by side
   __shared__ float4 part[kSplit][kVec];
-  __shared__ float lse2[kRows];
+  __shared__ float stats[kJoinThreads / 32][2][kRows], R[kRows], L[kRows];
   griddep_launch_dependents();
   griddep_wait();
   if (static_cast<int32_t>(blockIdx.x) < p.join_rows) {
-    // ---- merge the records of one row
+    // ---- one row's output
     const int32_t row = static_cast<int32_t>(blockIdx.x) % kRows;
     const int32_t hr = static_cast<int32_t>(blockIdx.x) / kRows;
     const int32_t rt = hr % p.row_tiles, bh = hr / p.row_tiles, r = rt * kRows + row;
     if (r >= p.R) return;
-    const Records x = pair_records(p, bh, rt);
+    const Records x = pair_records(p, bh, rt, load_pair(p, bh / p.c.Hkv, nullptr));
     if (x.tiles > 0 && x.c0 == x.c1) return;  // one CTA had all of it
     const int lane = threadIdx.x % kVec, sub = threadIdx.x / kVec;
-    float m = -INFINITY, L = 0.f;
+    if (x.tiles > 0) {
+      join_stats<kRows>(p, x, stats, R, L);
+    } else {
+      if (threadIdx.x == 0) {
+        R[row] = -INFINITY;
+        L[row] = 0.f;
+      }
+      __syncthreads();
+    }
+    const float m = R[row];
     float4 o = make_float4(0.f, 0.f, 0.f, 0.f);
     if (x.tiles > 0) {
-      for (int32_t c = x.c0; c <= x.c1; ++c) m = fmaxf(m, p.rec_stat[record_of(x, c) * 2 * kRows + row]);
-      for (int32_t c = x.c0; c <= x.c1; ++c) {
-        const float* st = p.rec_stat + record_of(x, c) * 2 * kRows + row;
-        const float w = m == -INFINITY ? 1.f : ex2_approx(st[0] - m);
-        if (st[kRows] != 0.f) L += st[kRows] * w;
-        if ((c - x.c0) % kSplit != sub || st[kRows] == 0.f) continue;
-        const float4 y = *reinterpret_cast<const float4*>(p.rec_o + (static_cast<int64_t>(record_of(x, c)) * kRows + row) * D + 4 * lane);
+#pragma unroll 4
+      for (int32_t c = x.c0 + sub; c <= x.c1; c += kSplit) {
+        const int32_t rec = x.of(c);
+        const float* st = p.rec_stat + rec * 2 * kRows + row;
+        const float w = st[kRows] == 0.f ? 0.f : (m == -INFINITY ? 1.f : ex2_approx(st[0] - m));
+        const float4 y = *reinterpret_cast<const float4*>(p.rec_o + (static_cast<int64_t>(rec) * kRows + row) * D + 4 * lane);
         o.x = fmaf(y.x, w, o.x);
         o.y = fmaf(y.y, w, o.y);
         o.z = fmaf(y.z, w, o.z);
@@ -760,53 +903,50 @@ __global__ void __launch_bounds__(256) kv4_join_kernel(const __grid_constant__ K
         o.w += y.w;
       }
       float f;
-      const float all = finish_row(p, bh % p.c.Hkv, m, L, f);
+      const float all = finish_row(p, bh % p.c.Hkv, m, L[row], f);
       store_o4(o_row(p, bh, r) + 4 * lane, o, f);
       if (lane == 0) p.lse[lse_index(p, bh, r)] = all * kLn2;
     }
     return;
   }
-  // ---- scores into probabilities, added to the keys' weights: 256 slots of one head
+  // ---- scores into probabilities, added to the keys' weights: kWeightKeys slots of one head
   const int64_t blk = static_cast<int64_t>(blockIdx.x) - p.join_rows;
-  const int32_t chunks = static_cast<int32_t>((p.c.capacity + 255) / 256);
+  const int32_t chunks = static_cast<int32_t>((p.c.capacity + kWeightKeys - 1) / kWeightKeys);
   const int32_t bh = static_cast<int32_t>(blk / chunks);
-  const int32_t slot = static_cast<int32_t>(blk % chunks) * 256 + static_cast<int32_t>(threadIdx.x);
+  const int32_t j0 = static_cast<int32_t>(blk % chunks) * kWeightKeys;
   const Pair pair = load_pair(p, bh / p.c.Hkv, nullptr);
-  if (static_cast<int32_t>(blk % chunks) * 256 >= pair.len || pair.nq == 0) return;
-  float w = 0.f;
+  if (j0 >= pair.len || pair.nq == 0) return;
+  float w[kWeightKeys / kJoinThreads] = {};
   for (int32_t rt = 0; rt < p.row_tiles; ++rt) {
-    const Records x = pair_records(p, bh, rt);
-    __syncthreads();
+    const Records x = pair_records(p, bh, rt, pair);
+    if (x.c0 != x.c1) join_stats<kRows>(p, x, stats, R, L);
+    else __syncthreads();
     if (threadIdx.x < kRows) {
-      const int32_t r = rt * kRows + threadIdx.x;
-      float R = -INFINITY, L = 0.f, f;
-      if (r < p.R && x.c0 != x.c1) {
-        for (int32_t c = x.c0; c <= x.c1; ++c) R = fmaxf(R, p.rec_stat[record_of(x, c) * 2 * kRows + threadIdx.x]);
-        for (int32_t c = x.c0; c <= x.c1; ++c) {
-          const float* st = p.rec_stat + record_of(x, c) * 2 * kRows + threadIdx.x;
-          if (st[kRows] != 0.f) L += st[kRows] * (R == -INFINITY ? 1.f : ex2_approx(st[0] - R));
-        }
-        lse2[threadIdx.x] = finish_row(p, bh % p.c.Hkv, R, L, f);
-      } else {
-        lse2[threadIdx.x] = r < p.R ? p.lse[lse_index(p, bh, r)] * kLog2e : INFINITY;
-      }
+      const int32_t r = rt * kRows + static_cast<int32_t>(threadIdx.x);
+      float f, v = INFINITY;
+      if (r < p.R) v = x.c0 != x.c1 ? finish_row(p, bh % p.c.Hkv, R[threadIdx.x], L[threadIdx.x], f)
+                                    : p.lse[lse_index(p, bh, r)] * kLog2e;
+      R[threadIdx.x] = v;
     }
     __syncthreads();
-    if (slot < pair.len) {
-      const float* sc = p.scores + ((static_cast<int64_t>(bh) * p.row_tiles + rt) * p.c.capacity + slot) * p.score_stride;
-      const int32_t rows = min(kRows, p.R - rt * kRows);
-      for (int32_t i = 0; i < rows; ++i) {
-        const int32_t t = (rt * kRows + i) % p.T;
-        if (t < pair.nq && slot < pair.len - pair.nq + t + 1) w += ex2_approx(sc[i] - lse2[i]);
-      }
+#pragma unroll
+    for (int i = 0; i < kWeightKeys / kJoinThreads; ++i) {
+      const int32_t j = j0 + i * kJoinThreads + static_cast<int32_t>(threadIdx.x);
+      if (j < pair.len) w[i] += key_probs<kRows>(p, pair, bh, rt, j, R);
     }
+    __syncthreads();
   }
-  if (slot < pair.len) p.c.weights[static_cast<int64_t>(bh) * p.c.capacity + slot] += w;
+#pragma unroll
+  for (int i = 0; i < kWeightKeys / kJoinThreads; ++i) {
+    const int32_t j = j0 + i * kJoinThreads + static_cast<int32_t>(threadIdx.x);
+    if (j < pair.len) p.c.weights[static_cast<int64_t>(bh) * p.c.capacity + j] += w[i];
+  }
 }
 
 // Sizes of a call that both the workspace query and the launch use.
 struct Plan {
   int NT, rows, row_tiles, n_cta, stride;
+  bool whole;
   size_t stat_bytes, o_bytes, score_bytes;
 };
 
@@ -816,12 +956,15 @@ Plan make_plan(const bsa_kv4_fwd_args* a) {
   x.NT = R <= 8 ? 1 : 2;
   x.rows = 8 * x.NT;
   x.row_tiles = static_cast<int>((R + x.rows - 1) / x.rows);
-  const int64_t most = static_cast<int64_t>(a->cache.B) * a->cache.Hkv * x.row_tiles * ((a->cache.capacity + kTileKeys - 1) / kTileKeys);
-  x.n_cta = static_cast<int>(std::min<int64_t>(most, static_cast<int64_t>(num_sms()) * (x.NT == 1 ? 2 : 1)));
+  const int64_t tiles = (a->cache.capacity + kTileKeys - 1) / kTileKeys;
+  const int64_t pairs = static_cast<int64_t>(a->cache.B) * a->cache.Hkv * x.row_tiles;
+  // (a key's weight has one writer: rows in several tiles are added up by the join)
+  x.whole = tiles <= kWholeTiles && !(a->accumulate && x.row_tiles > 1) && pairs <= INT32_MAX;
+  x.n_cta = static_cast<int>(x.whole ? pairs : std::min<int64_t>(pairs * tiles, static_cast<int64_t>(num_sms()) * (x.NT == 1 ? 3 : 2)));
   x.stride = static_cast<int>((std::min<int64_t>(R, x.rows) + 1) & ~int64_t(1));
-  x.stat_bytes = static_cast<size_t>(2 * x.n_cta) * 2 * x.rows * sizeof(float);
-  x.o_bytes = static_cast<size_t>(2 * x.n_cta) * x.rows * a->cache.D * sizeof(float);
-  x.score_bytes = a->accumulate ? static_cast<size_t>(a->cache.B) * a->cache.Hkv * x.row_tiles * a->cache.capacity * x.stride * sizeof(float) : 0;
+  x.stat_bytes = x.whole ? 0 : static_cast<size_t>(2 * x.n_cta) * 2 * x.rows * sizeof(float);
+  x.o_bytes = x.whole ? 0 : static_cast<size_t>(2 * x.n_cta) * x.rows * a->cache.D * sizeof(float);
+  x.score_bytes = a->accumulate ? static_cast<size_t>(pairs) * a->cache.capacity * x.stride * sizeof(float) : 0;
   return x;
 }
 
@@ -834,14 +977,21 @@ bsa_status launch(const Kv4FwdParams& p, int accumulate, cudaStream_t stream) {
   cudaError_t e = launch_kernel(kern, dim3(p.n_cta), dim3(kThreads), smem, stream, p);
   if (e == cudaSuccess) e = cudaGetLastError();
   if (e != cudaSuccess) return cuda_fail(e, "kv4 forward launch");
-  const int64_t chunks = accumulate ? (p.c.capacity + 255) / 256 * p.c.B * p.c.Hkv : 0;
-  e = launch_kernel(kv4_join_kernel<D, NT>, dim3(static_cast<unsigned>(p.join_rows + chunks)), dim3(256), 0, stream, p);
+  if (p.whole) return BSA_OK;
+  const int64_t chunks = accumulate ? (p.c.capacity + kWeightKeys - 1) / kWeightKeys * p.c.B * p.c.Hkv : 0;
+  e = launch_kernel(kv4_join_kernel<D, NT>, dim3(static_cast<unsigned>(p.join_rows + chunks)), dim3(kJoinThreads), 0, stream, p);
   if (e == cudaSuccess) e = cudaGetLastError();
   if (e != cudaSuccess) return cuda_fail(e, "kv4 join launch");
   return BSA_OK;
 }
 
 }  // namespace
+
+bool kv4_fwd_fits(const bsa_kv4_fwd_args* a) {
+  const Plan x = make_plan(a);
+  const int64_t heads = static_cast<int64_t>(a->cache.B) * a->cache.Hkv;
+  return heads * x.row_tiles * x.rows + heads * (a->cache.capacity / kWeightKeys + 1) <= INT32_MAX;
+}
 
 size_t kv4_fwd_workspace_bytes(const bsa_kv4_fwd_args* a) {
   const Plan x = make_plan(a);
@@ -872,6 +1022,7 @@ bsa_status kv4_fwd_launch(const bsa_kv4_fwd_args* a, float scale, cudaStream_t s
   p.n_sinks = a->num_sinks;
   p.sinks_kv = a->sinks_per_kv_head ? 1 : 0;
   p.n_cta = x.n_cta;
+  p.whole = x.whole ? 1 : 0;
   p.rec_stat = static_cast<float*>(a->workspace);
   p.rec_o = p.rec_stat + x.stat_bytes / sizeof(float);
   p.scores = a->accumulate ? p.rec_o + x.o_bytes / sizeof(float) : nullptr;
