@@ -99,14 +99,22 @@ __device__ __forceinline__ Pair load_pair(const Kv4FwdParams& p, int32_t b, uint
   return x;
 }
 
-// Tiles of all sequences; every lane of the calling warp gets the sum.
-__device__ __forceinline__ int64_t total_tiles(const Kv4FwdParams& p) {
+// Tiles of all sequences, and of the first ones up to b; every lane of the calling warp gets both.
+__device__ __forceinline__ int64_t total_tiles(const Kv4FwdParams& p, int32_t b, int64_t* before) {
   const int lane = threadIdx.x & 31;
   const int64_t per = static_cast<int64_t>(p.c.Hkv) * p.row_tiles;
-  int64_t sum = 0;
-  for (int32_t b = lane; b < p.c.B; b += 32) sum += load_pair(p, b, nullptr).tiles * per;
+  int64_t sum = 0, head = 0;
+  for (int32_t i = lane; i < p.c.B; i += 32) {
+    const int64_t n = load_pair(p, i, nullptr).tiles * per;
+    sum += n;
+    if (i < b) head += n;
+  }
 #pragma unroll
-  for (int o = 16; o > 0; o >>= 1) sum += __shfl_xor_sync(0xffffffffu, sum, o);
+  for (int o = 16; o > 0; o >>= 1) {
+    sum += __shfl_xor_sync(0xffffffffu, sum, o);
+    head += __shfl_xor_sync(0xffffffffu, head, o);
+  }
+  *before = head;
   return sum;
 }
 
@@ -115,9 +123,12 @@ __device__ __forceinline__ int64_t total_tiles(const Kv4FwdParams& p) {
 __device__ __forceinline__ int32_t runs(const Kv4FwdParams& p, int64_t total) {
   return static_cast<int32_t>(min(static_cast<int64_t>(p.n_cta), total));
 }
-__device__ __forceinline__ int64_t first_tile(int64_t c, int64_t total, int32_t n) { return c * total / n; }
+__device__ __forceinline__ int64_t quotient(int64_t a, int64_t b) {  // of non-negative numbers, mostly small ones
+  return ((a | b) >> 32) == 0 ? static_cast<int64_t>(static_cast<uint32_t>(a) / static_cast<uint32_t>(b)) : a / b;
+}
+__device__ __forceinline__ int64_t first_tile(int64_t c, int64_t total, int32_t n) { return quotient(c * total, n); }
 __device__ __forceinline__ int32_t cta_of(int64_t t, int64_t total, int32_t n) {
-  return static_cast<int32_t>(((t + 1) * n - 1) / total);
+  return static_cast<int32_t>(quotient((t + 1) * n - 1, total));
 }
 
 // Cursor over a CTA's run: parts of pairs, each a range of key tiles.
@@ -360,7 +371,8 @@ __global__ void __launch_bounds__(kThreads, NT == 1 ? 3 : 2) kv4_fwd_kernel(cons
   if (p.whole) {
     run.init_whole(p, blockIdx.x, threadIdx.x == 0 ? p.err : nullptr);
   } else {
-    const int64_t total = total_tiles(p);
+    int64_t none;
+    const int64_t total = total_tiles(p, 0, &none);
     const int32_t n_cta = runs(p, total);
     if (static_cast<int32_t>(blockIdx.x) >= n_cta) return;
     run.init(p, first_tile(blockIdx.x, total, n_cta), first_tile(blockIdx.x + 1, total, n_cta), warp == 0 ? p.err : nullptr);
@@ -500,14 +512,10 @@ __global__ void __launch_bounds__(kThreads, NT == 1 ? 3 : 2) kv4_fwd_kernel(cons
     for (int32_t kt = run.k0; kt < run.k1; ++kt, ++n) {
       // (after a wait that ran out the loop goes on without waiting, on whatever
       // the stages hold: the barriers between the warps stay matched)
-      if (static_cast<int>(n % kWarps) == warp) {
-        if (lane == 0 && ok) ok = load_tile(n + Sh::kAhead);
-        ok = __all_sync(0xffffffffu, ok);
-      }
       if (ok) ok = mbar_wait_warp(&s.full[st], parity, wc);
       const int32_t key0 = kt * kTileKeys + warp * 32;
       if (key0 < lim_max) {
-        const bool all_seen = key0 + 32 <= lim_min;
+        const bool all_seen = __all_sync(0xffffffffu, key0 + 32 <= lim_min);
         // ---- scores of both halves
         float x[2][NT][4];
 #pragma unroll
@@ -618,6 +626,10 @@ __global__ void __launch_bounds__(kThreads, NT == 1 ? 3 : 2) kv4_fwd_kernel(cons
             }
             l[nt][i] += (pr[0][nt][i] + pr[0][nt][i + 2]) + (pr[1][nt][i] + pr[1][nt][i + 2]);
           }
+#pragma unroll
+          for (int u = 0; u < 2; ++u)
+#pragma unroll
+            for (int i = 0; i < 4; ++i) pr[u][nt][i] *= down;
         }
         // ---- output, a half at a time
 #pragma unroll
@@ -631,8 +643,8 @@ __global__ void __launch_bounds__(kThreads, NT == 1 ? 3 : 2) kv4_fwd_kernel(cons
 #pragma unroll
           for (int g = 0; g < kGroups; ++g) {
             // probabilities times value scales, transposed into the second product's operand
-            const float fa = (g & 1 ? bf16_hi(va[u][g / 2]) : bf16_lo(va[u][g / 2])) * down;
-            const float fb = (g & 1 ? bf16_hi(vb[u][g / 2]) : bf16_lo(vb[u][g / 2])) * down;
+            const float fa = g & 1 ? bf16_hi(va[u][g / 2]) : bf16_lo(va[u][g / 2]);
+            const float fb = g & 1 ? bf16_hi(vb[u][g / 2]) : bf16_lo(vb[u][g / 2]);
             uint32_t b0[NT], b1[NT];
 #pragma unroll
             for (int nt = 0; nt < NT; ++nt) {
@@ -660,6 +672,12 @@ __global__ void __launch_bounds__(kThreads, NT == 1 ? 3 : 2) kv4_fwd_kernel(cons
             }
           }
         }
+      }
+      // (at the end: the stage it goes to, the last tile's, is long released; before this warp's own release, which
+      // hands the loader's place on to the next warp)
+      if (static_cast<int>(n % kWarps) == warp) {
+        if (lane == 0 && ok) ok = load_tile(n + Sh::kAhead);
+        ok = __all_sync(0xffffffffu, ok);
       }
       __syncwarp();
       if (lane == 0) mbar_arrive(&s.empty[st]);
@@ -781,21 +799,9 @@ struct Records {
 };
 
 __device__ __forceinline__ Records pair_records(const Kv4FwdParams& p, int32_t bh, int32_t rt, const Pair& pair) {
-  // tiles of all sequences, and of those before this one
-  const int lane = threadIdx.x & 31;
   const int32_t b = bh / p.c.Hkv, h = bh % p.c.Hkv;
-  const int64_t per = static_cast<int64_t>(p.c.Hkv) * p.row_tiles;
-  int64_t total = 0, before = 0;
-  for (int32_t i = lane; i < p.c.B; i += 32) {
-    const int64_t t = load_pair(p, i, nullptr).tiles * per;
-    total += t;
-    if (i < b) before += t;
-  }
-#pragma unroll
-  for (int o = 16; o > 0; o >>= 1) {
-    total += __shfl_xor_sync(0xffffffffu, total, o);
-    before += __shfl_xor_sync(0xffffffffu, before, o);
-  }
+  int64_t before;
+  const int64_t total = total_tiles(p, b, &before);
   Records x{0, 0, 0, pair.tiles};
   if (pair.tiles > 0) {
     const int32_t n = runs(p, total);
@@ -953,7 +959,7 @@ struct Plan {
 Plan make_plan(const bsa_kv4_fwd_args* a) {
   Plan x;
   const int64_t R = static_cast<int64_t>(a->Hq / a->cache.Hkv) * a->T;
-  x.NT = R <= 8 ? 1 : 2;
+  x.NT = 1;
   x.rows = 8 * x.NT;
   x.row_tiles = static_cast<int>((R + x.rows - 1) / x.rows);
   const int64_t tiles = (a->cache.capacity + kTileKeys - 1) / kTileKeys;
