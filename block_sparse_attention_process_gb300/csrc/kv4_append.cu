@@ -1,14 +1,17 @@
 // Quantisation of new keys and values into the 4-bit cache.
 //
 // Per group of 32 elements: s = bf16(max|x| / 7), c = rint(x / s) + 8.  The
-// fp32 quotient rounds to the same integer as the exact one: x has 8
-// significant bits and s/2 times an odd number at most 12, so a quotient that
-// is not itself a tie is at least 2^-15 (relative) away from one.
+// quotient is taken as x (1/s), off by at most 2^-22: x has 8 significant bits
+// and s/2 times an odd number at most 12, so a quotient that is not itself a
+// tie is at least 2^-15 (relative) away from one and rounds right; a tie shows
+// as a remainder of exactly s/2 and is put to the even side.
 //
-// HBM-bound: 4 D bytes read and D + D/4 codes and scales (+ 4 D values)
+// HBM-bound: 4 D bytes read and D + D/4 of codes and scales (+ 4 D of values)
 // written per token and head.  A row takes D/8 lanes: for K each lane holds
 // 8 consecutive elements, which are one 4-byte word of codes; for V its two
-// quads of elements 32 apart, likewise one word.
+// quads of elements 32 apart, likewise one word.  Four tokens a lane are in
+// flight at once; a true division per element, and one token at a time, took
+// 98 us where this takes APPEND_US (4 x 8 x 8192 rows of 128, values written).
 #include "internal.h"
 #include "kv4.cuh"
 #include "ptx.cuh"
@@ -20,7 +23,7 @@ struct AppendParams {
   bsa_kv4_cache c;
   const __nv_bfloat16 *k, *v;
   int64_t ks[3], vs[3];
-  int64_t T, rows;
+  uint32_t T, rows;
   const int32_t *start, *n_new, *first_position;
   const float* weights0;
   __nv_bfloat16 *k_values, *v_values;
@@ -40,79 +43,127 @@ __device__ __forceinline__ uint32_t scale_bits(uint32_t m) {
   return static_cast<uint32_t>(__bfloat16_as_ushort(s));
 }
 
+// One element: q = rint(x / s); the code q + 8 in the low bits of `bits`.
+__device__ __forceinline__ float quantise(float x, float s, float inv, uint32_t& bits) {
+  constexpr float kMagic = 12582912.f + 8.f;  // 1.5 2^23: the sum's last bits are the rounded integer plus 8
+  const float u = fmaf(x, inv, kMagic);
+  float q = u - kMagic;
+  const float rest = fmaf(-q, s, x);  // exact
+  const bool odd_tie = fabsf(rest) == 0.5f * s && (__float_as_uint(u) & 1u);
+  q += odd_tie ? copysignf(1.f, rest) : 0.f;
+  bits = __float_as_uint(q + kMagic);
+  return q;
+}
+// The same by a true division, for scales that are 0, NaN or so small that
+// their reciprocal might overflow.
+__device__ __forceinline__ float quantise_slow(float x, float s, uint32_t& bits) {
+  // (a subnormal scale is coarse: the largest elements may be 7.5 of it and more)
+  const float q = s > 0.f ? fminf(fmaxf(rintf(x / s), -7.f), 7.f) : 0.f;
+  bits = static_cast<uint32_t>(static_cast<int>(q) + 8);
+  return q;
+}
+
 // Four bf16 elements (two words) -> four codes in the low 16 bits; the values
 // they stand for replace the elements.
-__device__ __forceinline__ uint32_t quantise4(uint32_t& w0, uint32_t& w1, uint32_t sbits) {
-  const float s = __uint_as_float(sbits << 16);
+template <bool kSlow>
+__device__ __forceinline__ uint32_t quantise4(uint32_t& w0, uint32_t& w1, float s, float inv) {
   float x[4] = {bf16_lo(w0), bf16_hi(w0), bf16_lo(w1), bf16_hi(w1)};
   uint32_t c = 0;
 #pragma unroll
   for (int i = 0; i < 4; ++i) {
-    const float q = s > 0.f ? rintf(x[i] / s) : 0.f;
-    c |= static_cast<uint32_t>(static_cast<int>(q) + 8) << (4 * i);
-    x[i] = q * s;
+    uint32_t bits;
+    x[i] = (kSlow ? quantise_slow(x[i], s, bits) : quantise(x[i], s, inv, bits)) * s;
+    c |= (bits & 15u) << (4 * i);
   }
   w0 = pack_bf16x2(x[0], x[1]);
   w1 = pack_bf16x2(x[2], x[3]);
   return c;
 }
 
+// A lane's eight elements of K and two quads of V (bits of their scales): the
+// codes of both, the values in the elements' place.
+template <bool kSlow>
+__device__ __forceinline__ uint2 quantise_lane(uint4& k, uint2& va, uint2& vb, uint32_t sk, uint32_t sa, uint32_t sb) {
+  const float fk = __uint_as_float(sk << 16), fa = __uint_as_float(sa << 16), fb = __uint_as_float(sb << 16);
+  const float ik = kSlow ? 0.f : 1.f / fk, ia = kSlow ? 0.f : 1.f / fa, ib = kSlow ? 0.f : 1.f / fb;
+  uint2 c;
+  c.x = quantise4<kSlow>(k.x, k.y, fk, ik) | quantise4<kSlow>(k.z, k.w, fk, ik) << 16;
+  c.y = quantise4<kSlow>(va.x, va.y, fa, ia) | quantise4<kSlow>(vb.x, vb.y, fb, ib) << 16;
+  return c;
+}
+
+constexpr int kTokens = 4;  // rows that a lane has in flight
+
 template <int D>
 __global__ void __launch_bounds__(256) append_kernel(const __grid_constant__ AppendParams p) {
   constexpr int kLanes = Kv4<D>::kWords;  // lanes of one row
   constexpr int kPiece = Kv4<D>::kPieceWords;
+  constexpr uint32_t kRowsCta = 256 / kLanes;
   griddep_launch_dependents();
   griddep_wait();
-  const int u = threadIdx.x % kLanes;
-  const int64_t step = static_cast<int64_t>(gridDim.x) * (256 / kLanes);
-  // every lane of a warp makes the same number of trips (the shuffles)
-  for (int64_t r0 = static_cast<int64_t>(blockIdx.x) * (256 / kLanes); r0 < p.rows; r0 += step) {
-    const int64_t row = r0 + threadIdx.x / kLanes;
-    const bool in = row < p.rows;
-    const int64_t t = in ? row % p.T : 0, bh = in ? row / p.T : 0;
-    const int64_t b = bh / p.c.Hkv, h = bh % p.c.Hkv;
-    const bool fresh = in && (!p.n_new || t < p.n_new[b]);
-    const int64_t slot = fresh ? static_cast<int64_t>(p.start[b]) + t : 0;
-    const bool fits = slot >= 0 && slot < p.c.capacity;
-    if (fresh && !fits && u == 0 && p.err) atomicOr(p.err, DEV_ERR_BOUNDS);
-    uint4 kw = make_uint4(0, 0, 0, 0);
-    uint2 va = make_uint2(0, 0), vb = make_uint2(0, 0);
-    const int d0 = v_word_elem<D>(u, 0), d1 = v_word_elem<D>(u, 1);
-    if (fresh) {
-      kw = *reinterpret_cast<const uint4*>(p.k + b * p.ks[0] + h * p.ks[1] + t * p.ks[2] + 8 * u);
-      const __nv_bfloat16* vrow = p.v + b * p.vs[0] + h * p.vs[1] + t * p.vs[2];
-      va = *reinterpret_cast<const uint2*>(vrow + d0);
-      vb = *reinterpret_cast<const uint2*>(vrow + d1);
-    }
-    // a K group is 4 neighbouring lanes, a V group every kPiece-th lane of the row
-    uint32_t mk = max_bits(max_bits(max_bits(max_bits(0, kw.x), kw.y), kw.z), kw.w);
-    uint32_t ma = max_bits(max_bits(0, va.x), va.y), mb = max_bits(max_bits(0, vb.x), vb.y);
+  const uint32_t u = threadIdx.x % kLanes, sub = threadIdx.x / kLanes;
+  const int d0 = v_word_elem<D>(u, 0), d1 = v_word_elem<D>(u, 1);
+  const uint32_t step = gridDim.x * kRowsCta;
+  // rows (b, h, t) in order; a lane takes rows r0, r0 + step, ...; a warp's lanes make the same trips (the shuffles)
+  for (uint64_t r0 = blockIdx.x * kRowsCta; r0 < p.rows; r0 += static_cast<uint64_t>(step) * kTokens) {
+    uint4 kw[kTokens];
+    uint2 va[kTokens], vb[kTokens];
+    uint32_t bh[kTokens], tok[kTokens];
+    bool fresh[kTokens];
 #pragma unroll
-    for (int o = 1; o < 4; o *= 2) mk = max(mk, __shfl_xor_sync(0xffffffffu, mk, o));
+    for (int i = 0; i < kTokens; ++i) {
+      const uint64_t row = r0 + sub + static_cast<uint64_t>(i) * step;
+      const bool in = row < p.rows;
+      bh[i] = in ? static_cast<uint32_t>(row) / p.T : 0;
+      tok[i] = in ? static_cast<uint32_t>(row) - bh[i] * p.T : 0;
+      const uint32_t b = bh[i] / static_cast<uint32_t>(p.c.Hkv), h = bh[i] - b * static_cast<uint32_t>(p.c.Hkv);
+      fresh[i] = in && (!p.n_new || static_cast<int32_t>(tok[i]) < p.n_new[b]);
+      const __nv_bfloat16* kr = p.k + b * p.ks[0] + h * p.ks[1] + tok[i] * p.ks[2];
+      const __nv_bfloat16* vr = p.v + b * p.vs[0] + h * p.vs[1] + tok[i] * p.vs[2];
+      kw[i] = fresh[i] ? __ldcs(reinterpret_cast<const uint4*>(kr + 8 * u)) : make_uint4(0, 0, 0, 0);
+      va[i] = fresh[i] ? __ldcs(reinterpret_cast<const uint2*>(vr + d0)) : make_uint2(0, 0);
+      vb[i] = fresh[i] ? __ldcs(reinterpret_cast<const uint2*>(vr + d1)) : make_uint2(0, 0);
+    }
 #pragma unroll
-    for (int o = kPiece; o < 8 * kPiece; o *= 2) {
-      ma = max(ma, __shfl_xor_sync(0xffffffffu, ma, o));
-      mb = max(mb, __shfl_xor_sync(0xffffffffu, mb, o));
-    }
-    const uint32_t sk = scale_bits(mk), sa = scale_bits(ma), sb = scale_bits(mb);
-    const uint32_t ck = quantise4(kw.x, kw.y, sk) | (quantise4(kw.z, kw.w, sk) << 16);
-    const uint32_t cv = quantise4(va.x, va.y, sa) | (quantise4(vb.x, vb.y, sb) << 16);
-    if (fresh && fits) {
-      const int64_t at = (b * p.c.Hkv + h) * p.c.capacity + slot;
-      // elements 8 u + 0..7 of K are group u / 4, piece u % 4
-      static_cast<uint32_t*>(p.c.k_codes)[at * kLanes + (u % 4) * Kv4<D>::kGroups + u / 4] = ck;
-      static_cast<uint32_t*>(p.c.v_codes)[at * kLanes + (u ^ v_word_swap<D>(slot))] = cv;
-      if (u % 4 == 0) static_cast<uint16_t*>(p.c.k_scales)[at * Kv4<D>::kGroups + u / 4] = static_cast<uint16_t>(sk);
-      if (u < kPiece) static_cast<uint32_t*>(p.c.v_scales)[at * kPiece + u] = sa | (sb << 16);
-      if (u == 0 && p.c.weights) p.c.weights[at] = p.weights0 ? p.weights0[row] : 0.f;
-      if (u == 0 && p.c.positions)
-        p.c.positions[at] = (p.first_position ? p.first_position[b] : p.start[b]) + static_cast<int32_t>(t);
-    }
-    // (padding rows: the elements are 0 and so are their values)
-    if (in && p.k_values) *reinterpret_cast<uint4*>(p.k_values + row * D + 8 * u) = kw;
-    if (in && p.v_values) {
-      *reinterpret_cast<uint2*>(p.v_values + row * D + d0) = va;
-      *reinterpret_cast<uint2*>(p.v_values + row * D + d1) = vb;
+    for (int i = 0; i < kTokens; ++i) {
+      const uint64_t row = r0 + sub + static_cast<uint64_t>(i) * step;
+      if (row - sub >= p.rows) break;
+      // a K group is 4 neighbouring lanes, a V group every kPiece-th lane of the row
+      uint32_t mk = max_bits(max_bits(max_bits(max_bits(0, kw[i].x), kw[i].y), kw[i].z), kw[i].w);
+      uint32_t mv = max_bits(max_bits(0, va[i].x), va[i].y) | max_bits(max_bits(0, vb[i].x), vb[i].y) << 16;  // (15 bits each)
+#pragma unroll
+      for (int o = 1; o < 4; o *= 2) mk = max(mk, __shfl_xor_sync(0xffffffffu, mk, o));
+#pragma unroll
+      for (int o = kPiece; o < 8 * kPiece; o *= 2) mv = __vmaxu2(mv, __shfl_xor_sync(0xffffffffu, mv, o));
+      const uint32_t sk = scale_bits(mk), sa = scale_bits(mv & 0xFFFFu), sb = scale_bits(mv >> 16);
+      // 2^-100 <= s, and not NaN
+      constexpr uint32_t kLeast = (127u - 100u) << 7, kSpan = 0x7F80u - kLeast;
+      const bool usual = max(max(sk - kLeast, sa - kLeast), sb - kLeast) < kSpan;
+      const uint2 c = __all_sync(0xffffffffu, usual) ? quantise_lane<false>(kw[i], va[i], vb[i], sk, sa, sb)
+                                                     : quantise_lane<true>(kw[i], va[i], vb[i], sk, sa, sb);
+      if (fresh[i]) {
+        const int32_t b = static_cast<int32_t>(bh[i] / static_cast<uint32_t>(p.c.Hkv));
+        const int64_t slot = static_cast<int64_t>(p.start[b]) + tok[i];
+        if (slot >= 0 && slot < p.c.capacity) {
+          const int64_t at = bh[i] * p.c.capacity + slot;
+          // elements 8 u + 0..7 of K are group u / 4, piece u % 4
+          static_cast<uint32_t*>(p.c.k_codes)[at * kLanes + (u % 4) * Kv4<D>::kGroups + u / 4] = c.x;
+          static_cast<uint32_t*>(p.c.v_codes)[at * kLanes + (u ^ v_word_swap<D>(slot))] = c.y;
+          if (u % 4 == 0) static_cast<uint16_t*>(p.c.k_scales)[at * Kv4<D>::kGroups + u / 4] = static_cast<uint16_t>(sk);
+          if (u < kPiece) static_cast<uint32_t*>(p.c.v_scales)[at * kPiece + u] = sa | (sb << 16);
+          if (u == 0 && p.c.weights) p.c.weights[at] = p.weights0 ? p.weights0[row] : 0.f;
+          if (u == 1 && p.c.positions)
+            p.c.positions[at] = (p.first_position ? p.first_position[b] : p.start[b]) + static_cast<int32_t>(tok[i]);
+        } else if (u == 0 && p.err) {
+          atomicOr(p.err, DEV_ERR_BOUNDS);
+        }
+      }
+      // (padding rows: the elements are 0 and so are their values)
+      if (row < p.rows && p.k_values) __stcs(reinterpret_cast<uint4*>(p.k_values + row * D + 8 * u), kw[i]);
+      if (row < p.rows && p.v_values) {
+        __stcs(reinterpret_cast<uint2*>(p.v_values + row * D + d0), va[i]);
+        __stcs(reinterpret_cast<uint2*>(p.v_values + row * D + d1), vb[i]);
+      }
     }
   }
 }
@@ -128,8 +179,8 @@ bsa_status kv4_append_launch(const bsa_kv4_append_args* a, cudaStream_t stream) 
     p.ks[i] = a->k_stride[i];
     p.vs[i] = a->v_stride[i];
   }
-  p.T = a->T;
-  p.rows = static_cast<int64_t>(a->cache.B) * a->cache.Hkv * a->T;
+  p.T = static_cast<uint32_t>(a->T);
+  p.rows = static_cast<uint32_t>(a->cache.B) * a->cache.Hkv * p.T;
   p.start = a->start;
   p.n_new = a->n_new;
   p.first_position = a->first_position;
@@ -138,8 +189,10 @@ bsa_status kv4_append_launch(const bsa_kv4_append_args* a, cudaStream_t stream) 
   p.v_values = static_cast<__nv_bfloat16*>(a->v_values);
   p.err = device_error_word();
   if (!p.err) return fail(BSA_ERR_CUDA, "could not allocate the device error word");
-  const int per = 256 / (a->cache.D / 8);
-  const int grid = static_cast<int>(std::min<int64_t>((p.rows + per - 1) / per, static_cast<int64_t>(num_sms()) * 16));
+  // one trip of kTokens rows a lane, up to 16 blocks per SM; few rows are spread over the SMs one to a lane
+  const int64_t per = 256 / (a->cache.D / 8);
+  const int64_t blocks = (static_cast<int64_t>(p.rows) + per - 1) / per;
+  const int grid = static_cast<int>(std::min<int64_t>(blocks, std::max<int64_t>(num_sms(), std::min<int64_t>(blocks / kTokens + 1, num_sms() * 16))));
   cudaError_t e = a->cache.D == 128 ? launch_kernel(append_kernel<128>, dim3(grid), dim3(256), 0, stream, p)
                                     : launch_kernel(append_kernel<64>, dim3(grid), dim3(256), 0, stream, p);
   if (e == cudaSuccess) e = cudaGetLastError();

@@ -3,8 +3,15 @@
 // Per (sequence, key head): the `keep` slots of the largest key, key = the
 // weight as an ordered 32-bit integer (recent tokens above everything, NaN
 // above every number), ties to the lower slot.  A radix select of four 8-bit
-// digits finds the smallest kept key; one ordered pass then writes for every
-// kept slot where it goes, and a second kernel moves the rows.
+// digits finds the smallest kept key; every kept slot's place then follows
+// from prefix counts, and a second kernel moves the rows.
+//
+// The selection reads 8 bytes a slot once and is otherwise latency: a cluster
+// of up to 8 CTAs shares a head, each with its slice's keys in shared memory,
+// and adds up its histograms through distributed shared memory.  One CTA a
+// head that read the weights again for every digit took 193 us for 8 heads of
+// 65,536 slots and 25 us for 128 heads of 1088; this takes SELECT_US.  The
+// move is HBM-bound (D + D/4 bytes read, written, and 4 D of values).
 #include "internal.h"
 #include "kv4.cuh"
 #include "ptx.cuh"
@@ -12,7 +19,9 @@
 namespace bsa {
 namespace {
 
-constexpr int kSelThreads = 1024;
+constexpr int kSelThreads = 512;
+constexpr int kCachedKeys = 40 * 1024;  // keys of a slice kept in shared memory (160 KiB); a longer slice reads them again
+constexpr int kMaxCluster = 8;
 
 struct EvictParams {
   bsa_kv4_cache c, o;
@@ -23,6 +32,8 @@ struct EvictParams {
   int32_t* index;
   __nv_bfloat16 *k_values, *v_values;
   int32_t* holes;  // workspace [B, Hkv, keep] (in place only)
+  int32_t cluster;
+  int32_t cached;  // keys a slice may keep in shared memory
   uint32_t* err;
 };
 
@@ -34,34 +45,67 @@ __device__ __forceinline__ uint32_t order_key(float w, bool recent) {
   return (u & 0x80000000u) ? ~u : (u | 0x80000000u);
 }
 
-// Exclusive prefix sum over the CTA of one 0/1 flag per thread, and the total.
-__device__ __forceinline__ int32_t block_rank(bool flag, int32_t* warp_sums, int32_t& total) {
-  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
-  const uint32_t votes = __ballot_sync(0xffffffffu, flag);
-  __syncthreads();  // the sums of the call before have been read
-  if (lane == 0) warp_sums[warp] = __popc(votes);
-  __syncthreads();
-  int32_t before = 0, all = 0;
-  const int32_t mine = lane < kSelThreads / 32 ? warp_sums[lane] : 0;
-  int32_t inc = mine;
-#pragma unroll
-  for (int o = 1; o < 32; o *= 2) {
-    const int32_t x = __shfl_up_sync(0xffffffffu, inc, o);
-    if (lane >= o) inc += x;
-  }
-  before = __shfl_sync(0xffffffffu, inc - mine, warp);
-  all = __shfl_sync(0xffffffffu, inc, 31);
-  total = all;
-  return before + __popc(votes & ((1u << lane) - 1u));
+__device__ __forceinline__ uint32_t cluster_rank() {
+  uint32_t r;
+  asm("mov.u32 %0, %%cluster_ctarank;" : "=r"(r));
+  return r;
+}
+// All threads of the cluster; memory written before is visible after.
+__device__ __forceinline__ void cluster_barrier() {
+  asm volatile("barrier.cluster.arrive.release;\n\tbarrier.cluster.wait.acquire;" ::: "memory");
+}
+// A word of another CTA's shared memory.
+__device__ __forceinline__ uint32_t load_remote(const uint32_t* mine, uint32_t rank) {
+  uint32_t a, v;
+  asm volatile("mapa.shared::cluster.u32 %0, %1, %2;" : "=r"(a) : "r"(smem_u32(mine)), "r"(rank));
+  asm volatile("ld.shared::cluster.u32 %0, [%1];" : "=r"(v) : "r"(a) : "memory");
+  return v;
 }
 
+// Exclusive prefix sums over the CTA's threads of two counts, and their totals.
+__device__ __forceinline__ void block_prefix(int32_t& a, int32_t& b, int32_t (*sums)[2], int32_t& all_a, int32_t& all_b) {
+  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+  int32_t ia = a, ib = b;
+#pragma unroll
+  for (int o = 1; o < 32; o *= 2) {
+    const int32_t xa = __shfl_up_sync(0xffffffffu, ia, o), xb = __shfl_up_sync(0xffffffffu, ib, o);
+    if (lane >= o) {
+      ia += xa;
+      ib += xb;
+    }
+  }
+  if (lane == 31) {
+    sums[warp][0] = ia;
+    sums[warp][1] = ib;
+  }
+  __syncthreads();
+  int32_t before_a = 0, before_b = 0;
+  all_a = all_b = 0;
+#pragma unroll
+  for (int w = 0; w < kSelThreads / 32; ++w) {
+    if (w == warp) {
+      before_a = all_a;
+      before_b = all_b;
+    }
+    all_a += sums[w][0];
+    all_b += sums[w][1];
+  }
+  a = before_a + ia - a;
+  b = before_b + ib - b;
+}
+
+// One head per cluster; CTA r takes the r-th slice of its slots.
 __global__ void __launch_bounds__(kSelThreads) select_kernel(const __grid_constant__ EvictParams p) {
-  __shared__ uint32_t hist[256];
-  __shared__ int32_t warp_sums[32];
+  extern __shared__ uint32_t keys[];  // the slice's, if it is short enough
+  __shared__ uint32_t hist[2][256];   // (two: a CTA may still read one while the next digit's is counted)
+  __shared__ uint32_t totals[256];
   __shared__ uint32_t pick[2];
+  __shared__ uint32_t counts[3];      // slots of the slice above the least kept key, at it, and stays below slot keep
+  __shared__ int32_t sums[kSelThreads / 32][2];
   griddep_launch_dependents();
   griddep_wait();
-  const int64_t bh = blockIdx.x;
+  const uint32_t cta = cluster_rank(), C = static_cast<uint32_t>(p.cluster);
+  const int64_t bh = blockIdx.x / C;
   const int32_t b = static_cast<int32_t>(bh / p.c.Hkv);
   const int32_t n = clamp_len(p.lens[b], p.c.capacity, threadIdx.x == 0 ? p.err : nullptr);
   const int64_t first_recent = static_cast<int64_t>(p.seen ? p.seen[b] : p.lens[b]) - p.recent;
@@ -69,128 +113,217 @@ __global__ void __launch_bounds__(kSelThreads) select_kernel(const __grid_consta
   const int32_t* pos = p.c.positions ? p.c.positions + bh * p.c.capacity : nullptr;
   int32_t* index = p.index + bh * p.keep;
   const int32_t keep = static_cast<int32_t>(p.keep < n ? p.keep : n);
-  if (threadIdx.x == 0 && bh % p.c.Hkv == 0) p.new_lens[b] = keep;
-  auto key_of = [&](int32_t i) {
+  if (threadIdx.x == 0 && cta == 0 && bh % p.c.Hkv == 0) p.new_lens[b] = keep;
+  const int32_t thread = static_cast<int32_t>(cta * kSelThreads + threadIdx.x), threads = static_cast<int32_t>(C * kSelThreads);
+  for (int64_t r = keep + static_cast<int64_t>(thread); r < p.keep; r += threads) index[r] = -1;
+  if (n <= p.keep) {  // (uniform over the cluster) everything stays
+    for (int32_t i = thread; i < n; i += threads) index[i] = i;
+    return;
+  }
+  // this CTA's slice, and this thread's run of it
+  const int32_t chunk = (n + threads - 1) / threads | 1;  // (odd: a warp's runs start in different banks)
+  const int32_t s0 = static_cast<int32_t>(min(static_cast<int64_t>(n), static_cast<int64_t>(cta) * kSelThreads * chunk));
+  const int32_t s1 = static_cast<int32_t>(min(static_cast<int64_t>(n), static_cast<int64_t>(s0) + kSelThreads * chunk));
+  const bool cached = s1 - s0 <= p.cached;
+  auto make_key = [&](int32_t i) {
     const bool recent = p.recent > 0 && (pos ? static_cast<int64_t>(pos[i]) : i) >= first_recent;
     return order_key(w[i], recent);
   };
-
-  uint32_t least = 0;      // smallest kept key
-  int32_t ties = n;        // how many slots with that key are kept
-  if (n > p.keep) {
-    uint32_t prefix = 0, mask = 0;
-    uint32_t want = static_cast<uint32_t>(p.keep);  // rank (1-based, from the top) among keys with this prefix
-    for (int shift = 24; shift >= 0; shift -= 8) {
-      for (int i = threadIdx.x; i < 256; i += kSelThreads) hist[i] = 0;
-      __syncthreads();
-      for (int32_t i = threadIdx.x; i < n; i += kSelThreads) {
-        const uint32_t k = key_of(i);
-        if ((k & mask) == prefix) atomicAdd(&hist[(k >> shift) & 255u], 1u);
-      }
-      __syncthreads();
-      if (threadIdx.x == 0) {
-        uint32_t above = 0;
-        int d = 255;
-        while (d > 0 && above + hist[d] < want) above += hist[d--];
-        pick[0] = static_cast<uint32_t>(d);
-        pick[1] = want - above;
-      }
-      __syncthreads();
-      prefix |= pick[0] << shift;
-      mask |= 255u << shift;
-      want = pick[1];
-      __syncthreads();
-    }
-    least = prefix;
-    ties = static_cast<int32_t>(want);
+  auto key_of = [&](int32_t i) { return cached ? keys[i - s0] : make_key(i); };
+  if (cached) {
+#pragma unroll 4
+    for (int32_t i = s0 + static_cast<int32_t>(threadIdx.x); i < s1; i += kSelThreads) keys[i - s0] = make_key(i);
   }
 
-  // one ordered pass: which slots stay, and where their tokens go
-  int32_t kept_before = 0, ties_before = 0, holes_before = 0;
-  for (int32_t i0 = 0; i0 < n; i0 += kSelThreads) {
-    const int32_t i = i0 + static_cast<int32_t>(threadIdx.x);
-    const uint32_t k = i < n ? key_of(i) : 0u;
-    int32_t total;
-    const bool tie = i < n && k == least && n > p.keep;
-    const int32_t tr = block_rank(tie, warp_sums, total) + ties_before;
-    ties_before += total;
-    const bool stay = i < n && (n <= p.keep || k > least || (tie && tr < ties));
-    if (!p.in_place) {
-      const int32_t r = block_rank(stay, warp_sums, total) + kept_before;
-      kept_before += total;
-      if (stay) index[r] = i;
-    } else {
-      const bool hole = i < n && i < p.keep && !stay;
-      const int32_t hr = block_rank(hole, warp_sums, total) + holes_before;
-      holes_before += total;
-      if (hole) p.holes[bh * p.keep + hr] = i;
-      if (stay && i < p.keep) index[i] = i;
-      const bool mover = stay && i >= p.keep;
-      // (the holes all lie below slot keep, so a mover's hole is already written:
-      // by this trip or an earlier one, and block_rank has barriers in between)
-      const int32_t mr = block_rank(mover, warp_sums, total) + kept_before;
-      kept_before += total;
-      if (mover) index[p.holes[bh * p.keep + mr]] = i;
+  uint32_t prefix = 0, mask = 0;
+  uint32_t want = static_cast<uint32_t>(p.keep);  // rank (1-based, from the top) among keys with this prefix
+  for (int d = 0; d < 4; ++d) {
+    const int shift = 24 - 8 * d;
+    uint32_t* h = hist[d & 1];
+    if (threadIdx.x < 256) h[threadIdx.x] = 0;
+    __syncthreads();
+    // (whole warps go round together: equal digits of a warp are counted at once, most weights share their top ones)
+    for (int32_t i0 = s0; i0 < s1; i0 += kSelThreads) {
+      const int32_t i = i0 + static_cast<int32_t>(threadIdx.x);
+      const uint32_t k = i < s1 ? key_of(i) : 0u;
+      const bool in = i < s1 && (k & mask) == prefix;
+      const uint32_t digit = in ? (k >> shift) & 255u : 256u;
+      const uint32_t same = __match_any_sync(0xffffffffu, digit);
+      if (in && (threadIdx.x & 31) == static_cast<uint32_t>(__ffs(same) - 1)) atomicAdd(&h[digit], static_cast<uint32_t>(__popc(same)));
     }
+    cluster_barrier();
+    if (threadIdx.x < 256) {
+      uint32_t v = 0;
+#pragma unroll
+      for (uint32_t c = 0; c < kMaxCluster; ++c)
+        if (c < C) v += load_remote(&h[threadIdx.x], c);
+      totals[threadIdx.x] = v;
+    }
+    __syncthreads();
+    if (threadIdx.x < 32) {
+      // eight digits a lane, from the top: where does the count reach `want`?
+      uint32_t mine[8], total = 0;
+#pragma unroll
+      for (int i = 0; i < 8; ++i) {
+        mine[i] = totals[255u - (threadIdx.x * 8 + i)];
+        total += mine[i];
+      }
+      uint32_t before = total;
+#pragma unroll
+      for (int o = 1; o < 32; o *= 2) {
+        const uint32_t x = __shfl_up_sync(0xffffffffu, before, o);
+        if (threadIdx.x >= static_cast<uint32_t>(o)) before += x;
+      }
+      before -= total;
+      bool found = before < want && before + total >= want;
+#pragma unroll
+      for (int i = 0; i < 8; ++i) {
+        if (found && before + mine[i] >= want) {
+          pick[0] = 255u - (threadIdx.x * 8 + i);
+          pick[1] = want - before;
+          found = false;
+        }
+        before += mine[i];
+      }
+    }
+    __syncthreads();
+    prefix |= pick[0] << shift;
+    mask |= 255u << shift;
+    want = pick[1];
+    __syncthreads();
   }
-  for (int64_t r = keep + static_cast<int64_t>(threadIdx.x); r < p.keep; r += kSelThreads) index[r] = -1;
+  // `want` slots whose key is `prefix` stay, the lowest ones, and all above it
+
+  const int32_t t0 = static_cast<int32_t>(min(static_cast<int64_t>(s1), s0 + static_cast<int64_t>(threadIdx.x) * chunk));
+  const int32_t t1 = min(s1 - t0, chunk) + t0;
+  int32_t above = 0, ties = 0;
+  for (int32_t i = t0; i < t1; ++i) {
+    const uint32_t k = key_of(i);
+    above += k > prefix;
+    ties += k == prefix;
+  }
+  int32_t all_above, all_ties;
+  block_prefix(above, ties, sums, all_above, all_ties);
+  if (threadIdx.x == 0) {
+    counts[0] = static_cast<uint32_t>(all_above);
+    counts[1] = static_cast<uint32_t>(all_ties);
+    counts[2] = 0;
+  }
+  cluster_barrier();
+  for (uint32_t c = 0; c < cta; ++c) {
+    above += static_cast<int32_t>(load_remote(&counts[0], c));
+    ties += static_cast<int32_t>(load_remote(&counts[1], c));
+  }
+  const int32_t quota = static_cast<int32_t>(want);
+  // stays before slot i: those above the least key, and ties up to the quota
+  if (!p.in_place) {
+    for (int32_t i = t0; i < t1; ++i) {
+      const uint32_t k = key_of(i);
+      const int32_t r = above + min(ties, quota);
+      if (k > prefix || (k == prefix && ties < quota)) index[r] = i;
+      above += k > prefix;
+      ties += k == prefix;
+    }
+    cluster_barrier();  // (no CTA leaves while another reads its counts)
+    return;
+  }
+  // in place: holes (slots below keep that are freed) by rank, then the stays from slot keep on into them
+  int32_t a = above, t = ties;
+  for (int32_t i = t0; i < t1; ++i) {
+    const uint32_t k = key_of(i);
+    const int32_t stays = a + min(t, quota);
+    if (i == keep) counts[2] = static_cast<uint32_t>(stays);  // (one thread of the cluster)
+    if (i < keep) {
+      if (k > prefix || (k == prefix && t < quota)) index[i] = i;
+      else p.holes[bh * p.keep + i - stays] = i;
+    }
+    a += k > prefix;
+    t += k == prefix;
+  }
+  cluster_barrier();  // the holes are written (and n > keep: slot keep has been met)
+  uint32_t below = 0;
+  for (uint32_t c = 0; c < C; ++c) below += load_remote(&counts[2], c);
+  a = above;
+  t = ties;
+  for (int32_t i = t0; i < t1; ++i) {
+    const uint32_t k = key_of(i);
+    const int32_t stays = a + min(t, quota);
+    if (i >= keep && (k > prefix || (k == prefix && t < quota)))
+      index[p.holes[bh * p.keep + stays - static_cast<int32_t>(below)]] = i;
+    a += k > prefix;
+    t += k == prefix;
+  }
+  cluster_barrier();  // (no CTA leaves while another reads its counts)
 }
 
 __device__ __forceinline__ float code_value(uint32_t w, int i, float s) {
   return static_cast<float>(static_cast<int>((w >> (4 * i)) & 15u) - 8) * s;
 }
 
+constexpr int kMoves = 4;  // rows of one head that a lane has in flight
+
 template <int D>
 __global__ void __launch_bounds__(256) move_kernel(const __grid_constant__ EvictParams p) {
   constexpr int kLanes = Kv4<D>::kWords;
   constexpr int kPiece = Kv4<D>::kPieceWords;
   constexpr int kGroups = Kv4<D>::kGroups;
+  constexpr int kRowsCta = 256 / kLanes;
   griddep_launch_dependents();
   griddep_wait();
-  const int u = threadIdx.x % kLanes;
-  const int64_t rows = static_cast<int64_t>(p.c.B) * p.c.Hkv * p.keep;
-  const int64_t step = static_cast<int64_t>(gridDim.x) * (256 / kLanes);
-  for (int64_t row = static_cast<int64_t>(blockIdx.x) * (256 / kLanes) + threadIdx.x / kLanes; row < rows; row += step) {
-    const int64_t bh = row / p.keep, r = row % p.keep;
-    const int32_t src = p.index[row];
-    const bool live = src >= 0;
-    if (!live && !p.k_values && !p.v_values) continue;
-    uint32_t kw = 0x88888888u, vw = 0x88888888u, ks = 0, vs = 0;
-    if (live) {
-      const int64_t from = bh * p.c.capacity + src, to = bh * p.o.capacity + r;
-      kw = static_cast<const uint32_t*>(p.c.k_codes)[from * kLanes + u];
-      vw = static_cast<const uint32_t*>(p.c.v_codes)[from * kLanes + (u ^ v_word_swap<D>(src))];
-      ks = static_cast<const uint16_t*>(p.c.k_scales)[from * kGroups + u % kGroups];
-      vs = static_cast<const uint32_t*>(p.c.v_scales)[from * kPiece + u % kPiece];
-      if (!p.in_place || src != r) {
-        static_cast<uint32_t*>(p.o.k_codes)[to * kLanes + u] = kw;
-        static_cast<uint32_t*>(p.o.v_codes)[to * kLanes + (u ^ v_word_swap<D>(r))] = vw;
-        if (u < kGroups) static_cast<uint16_t*>(p.o.k_scales)[to * kGroups + u] = static_cast<uint16_t>(ks);
-        if (u < kPiece) static_cast<uint32_t*>(p.o.v_scales)[to * kPiece + u] = vs;
-        if (u == 0 && p.o.weights) p.o.weights[to] = p.c.weights[from];
-        if (u == 1 && p.o.positions)
-          p.o.positions[to] = p.c.positions ? p.c.positions[from] : src;
+  const int u = threadIdx.x % kLanes, sub = threadIdx.x / kLanes;
+  const int64_t heads = static_cast<int64_t>(p.c.B) * p.c.Hkv;
+  const int64_t step = static_cast<int64_t>(gridDim.x) * kRowsCta;
+  for (int64_t bh = blockIdx.y; bh < heads; bh += gridDim.y)
+    for (int64_t r0 = static_cast<int64_t>(blockIdx.x) * kRowsCta + sub; r0 < p.keep; r0 += step * kMoves) {
+      int32_t src[kMoves];
+      uint32_t kw[kMoves], vw[kMoves], ks[kMoves], vs[kMoves];
+#pragma unroll
+      for (int i = 0; i < kMoves; ++i) src[i] = r0 + i * step < p.keep ? p.index[bh * p.keep + r0 + i * step] : -1;
+#pragma unroll
+      for (int i = 0; i < kMoves; ++i) {
+        kw[i] = vw[i] = 0x88888888u;
+        ks[i] = vs[i] = 0;
+        if (src[i] < 0) continue;
+        const int64_t from = bh * p.c.capacity + src[i];
+        kw[i] = static_cast<const uint32_t*>(p.c.k_codes)[from * kLanes + u];
+        vw[i] = static_cast<const uint32_t*>(p.c.v_codes)[from * kLanes + (u ^ v_word_swap<D>(src[i]))];
+        ks[i] = static_cast<const uint16_t*>(p.c.k_scales)[from * kGroups + u % kGroups];
+        vs[i] = static_cast<const uint32_t*>(p.c.v_scales)[from * kPiece + u % kPiece];
+      }
+#pragma unroll
+      for (int i = 0; i < kMoves; ++i) {
+        const int64_t r = r0 + i * step;
+        if (r >= p.keep) continue;
+        if (src[i] >= 0 && !(p.in_place && src[i] == r)) {
+          const int64_t from = bh * p.c.capacity + src[i], to = bh * p.o.capacity + r;
+          static_cast<uint32_t*>(p.o.k_codes)[to * kLanes + u] = kw[i];
+          static_cast<uint32_t*>(p.o.v_codes)[to * kLanes + (u ^ v_word_swap<D>(r))] = vw[i];
+          if (u < kGroups) static_cast<uint16_t*>(p.o.k_scales)[to * kGroups + u] = static_cast<uint16_t>(ks[i]);
+          if (u < kPiece) static_cast<uint32_t*>(p.o.v_scales)[to * kPiece + u] = vs[i];
+          if (u == 0 && p.o.weights) p.o.weights[to] = p.c.weights[from];
+          if (u == 1 && p.o.positions) p.o.positions[to] = p.c.positions ? p.c.positions[from] : src[i];
+        }
+        const int64_t row = (bh * p.keep + r) * D;
+        if (p.k_values) {
+          const float s = __uint_as_float(ks[i] << 16);
+          uint4 o;
+          o.x = pack_bf16x2(code_value(kw[i], 0, s), code_value(kw[i], 1, s));
+          o.y = pack_bf16x2(code_value(kw[i], 2, s), code_value(kw[i], 3, s));
+          o.z = pack_bf16x2(code_value(kw[i], 4, s), code_value(kw[i], 5, s));
+          o.w = pack_bf16x2(code_value(kw[i], 6, s), code_value(kw[i], 7, s));
+          __stcs(reinterpret_cast<uint4*>(p.k_values + row + k_word_elem<D>(u)), o);
+        }
+        if (p.v_values) {
+          const float a = bf16_lo(vs[i]), b = bf16_hi(vs[i]);
+          __stcs(reinterpret_cast<uint2*>(p.v_values + row + v_word_elem<D>(u, 0)),
+                 make_uint2(pack_bf16x2(code_value(vw[i], 0, a), code_value(vw[i], 1, a)),
+                            pack_bf16x2(code_value(vw[i], 2, a), code_value(vw[i], 3, a))));
+          __stcs(reinterpret_cast<uint2*>(p.v_values + row + v_word_elem<D>(u, 1)),
+                 make_uint2(pack_bf16x2(code_value(vw[i], 4, b), code_value(vw[i], 5, b)),
+                            pack_bf16x2(code_value(vw[i], 6, b), code_value(vw[i], 7, b))));
+        }
       }
     }
-    if (p.k_values) {
-      const float s = __uint_as_float(ks << 16);
-      uint4 o;
-      o.x = pack_bf16x2(code_value(kw, 0, s), code_value(kw, 1, s));
-      o.y = pack_bf16x2(code_value(kw, 2, s), code_value(kw, 3, s));
-      o.z = pack_bf16x2(code_value(kw, 4, s), code_value(kw, 5, s));
-      o.w = pack_bf16x2(code_value(kw, 6, s), code_value(kw, 7, s));
-      *reinterpret_cast<uint4*>(p.k_values + row * D + k_word_elem<D>(u)) = o;
-    }
-    if (p.v_values) {
-      const float s0 = bf16_lo(vs), s1 = bf16_hi(vs);
-      *reinterpret_cast<uint2*>(p.v_values + row * D + v_word_elem<D>(u, 0)) =
-          make_uint2(pack_bf16x2(code_value(vw, 0, s0), code_value(vw, 1, s0)),
-                     pack_bf16x2(code_value(vw, 2, s0), code_value(vw, 3, s0)));
-      *reinterpret_cast<uint2*>(p.v_values + row * D + v_word_elem<D>(u, 1)) =
-          make_uint2(pack_bf16x2(code_value(vw, 4, s1), code_value(vw, 5, s1)),
-                     pack_bf16x2(code_value(vw, 6, s1), code_value(vw, 7, s1)));
-    }
-  }
 }
 
 }  // namespace
@@ -216,14 +349,37 @@ bsa_status kv4_evict_launch(const bsa_kv4_evict_args* a, cudaStream_t stream) {
   p.holes = static_cast<int32_t*>(a->workspace);
   p.err = device_error_word();
   if (!p.err) return fail(BSA_ERR_CUDA, "could not allocate the device error word");
-  cudaError_t e = launch_kernel(select_kernel, dim3(a->cache.B * a->cache.Hkv), dim3(kSelThreads), 0, stream, p);
+  // CTAs a head: more while SMs are free and a slice has 2048 slots or more
+  const int64_t heads = static_cast<int64_t>(a->cache.B) * a->cache.Hkv;
+  p.cluster = 1;
+  while (p.cluster < kMaxCluster && heads * p.cluster * 2 <= num_sms() && a->cache.capacity / p.cluster >= 4096) p.cluster *= 2;
+  const int64_t slice = ((a->cache.capacity + p.cluster * kSelThreads - 1) / (p.cluster * kSelThreads) | 1) * kSelThreads;
+  p.cached = slice <= kCachedKeys ? static_cast<int32_t>(slice) : 0;
+  const size_t smem = static_cast<size_t>(p.cached) * sizeof(uint32_t);
+  const bsa_status st = ensure_smem_attr(reinterpret_cast<const void*>(select_kernel), kCachedKeys * sizeof(uint32_t), "set selection smem size");
+  if (st != BSA_OK) return st;
+  cudaLaunchConfig_t cfg{};
+  cfg.gridDim = dim3(static_cast<unsigned>(heads * p.cluster));
+  cfg.blockDim = dim3(kSelThreads);
+  cfg.dynamicSmemBytes = smem;
+  cfg.stream = stream;
+  cudaLaunchAttribute attr[2];
+  attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  attr[0].val.programmaticStreamSerializationAllowed = pdl_enabled() ? 1 : 0;
+  attr[1].id = cudaLaunchAttributeClusterDimension;
+  attr[1].val.clusterDim.x = static_cast<unsigned>(p.cluster);
+  attr[1].val.clusterDim.y = 1;
+  attr[1].val.clusterDim.z = 1;
+  cfg.attrs = attr;
+  cfg.numAttrs = 2;
+  cudaError_t e = cudaLaunchKernelEx(&cfg, select_kernel, p);
   if (e == cudaSuccess) e = cudaGetLastError();
   if (e != cudaSuccess) return cuda_fail(e, "kv4 evict selection launch");
-  const int64_t rows = static_cast<int64_t>(a->cache.B) * a->cache.Hkv * a->keep;
-  const int per = 256 / (a->cache.D / 8);
-  const int grid = static_cast<int>(std::min<int64_t>((rows + per - 1) / per, static_cast<int64_t>(num_sms()) * 16));
-  e = a->cache.D == 128 ? launch_kernel(move_kernel<128>, dim3(grid), dim3(256), 0, stream, p)
-                        : launch_kernel(move_kernel<64>, dim3(grid), dim3(256), 0, stream, p);
+  const int64_t per = 256 / (a->cache.D / 8) * kMoves;
+  const unsigned gy = static_cast<unsigned>(std::min<int64_t>(heads, 65535));
+  const unsigned gx = static_cast<unsigned>(std::min<int64_t>((a->keep + per - 1) / per, std::max<int64_t>(1, num_sms() * 16 / gy)));
+  e = a->cache.D == 128 ? launch_kernel(move_kernel<128>, dim3(gx, gy), dim3(256), 0, stream, p)
+                        : launch_kernel(move_kernel<64>, dim3(gx, gy), dim3(256), 0, stream, p);
   if (e == cudaSuccess) e = cudaGetLastError();
   if (e != cudaSuccess) return cuda_fail(e, "kv4 evict move launch");
   return BSA_OK;

@@ -355,7 +355,8 @@ BSA_API bsa_status bsa_key_weights_workspace(const bsa_key_weights_args* args, c
 /* A cache of keys and values in 4 bits; all memory is the caller's.  Each row
  * of D elements holds D/32 groups of 32 consecutive elements with one bf16
  * scale s = bf16(max|x| / 7) each; an element is the code round(x / s) + 8
- * (half to even; 1..15, 8 when s is 0) and stands for s * (code - 8).  A group
+ * (half to even; 8 when s is 0; kept in 1..15, which only a subnormal scale
+ * could leave) and stands for s * (code - 8).  A group
  * that holds an infinity or a NaN gets s = NaN and reads as NaN throughout.
  *
  * Order of the codes in a row (4 D bits; chosen so that the tensor-core

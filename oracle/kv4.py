@@ -2,7 +2,7 @@
 it, accumulated weights and eviction, from their definitions.
 
     a row of D elements is D/32 groups of 32 consecutive ones; per group
-        s = bf16(max|x| / 7),  code = round_half_even(x / s) + 8  (8 if s = 0),
+        s = bf16(max|x| / 7),  code = round_half_even(x / s), kept in -7..7, + 8  (8 if s = 0),
         value = s * (code - 8);  a group with an infinity or a NaN: s = NaN
     K row: element d is nibble d % 8 of 32-bit word (d % 32 // 8) * (D // 32) + d // 32
     V row: element d is nibble d % 4 of 16-bit word (d % 32 // 4) * (D // 32) + d // 32;
@@ -40,7 +40,7 @@ def quantise(x: np.ndarray):
         bad = ~np.isfinite(g).all(-1)
         s = np.where(bad, np.nan, bf16(np.where(bad, 0.0, top) / 7))
         safe = np.where(np.isnan(s) | (s == 0), 1.0, s)[..., None]
-        q = np.where((np.isnan(s) | (s == 0))[..., None], 0.0, np.rint(g / safe))
+        q = np.where((np.isnan(s) | (s == 0))[..., None], 0.0, np.clip(np.rint(g / safe), -7, 7))
     return (q + 8).astype(np.uint8).reshape(x.shape), s
 
 
