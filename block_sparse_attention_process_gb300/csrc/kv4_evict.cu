@@ -19,7 +19,7 @@
 namespace bsa {
 namespace {
 
-constexpr int kSelThreads = 512;
+constexpr int kSelThreads = 1024;
 constexpr int kCachedKeys = 40 * 1024;  // keys of a slice kept in shared memory (160 KiB); a longer slice reads them again
 constexpr int kMaxCluster = 8;
 
@@ -143,10 +143,12 @@ __global__ void __launch_bounds__(kSelThreads) select_kernel(const __grid_consta
     if (threadIdx.x < 256) h[threadIdx.x] = 0;
     __syncthreads();
     // (whole warps go round together: equal digits of a warp are counted at once, most weights share their top ones)
+#pragma unroll 4
     for (int32_t i0 = s0; i0 < s1; i0 += kSelThreads) {
       const int32_t i = i0 + static_cast<int32_t>(threadIdx.x);
       const uint32_t k = i < s1 ? key_of(i) : 0u;
       const bool in = i < s1 && (k & mask) == prefix;
+      if (!__any_sync(0xffffffffu, in)) continue;
       const uint32_t digit = in ? (k >> shift) & 255u : 256u;
       const uint32_t same = __match_any_sync(0xffffffffu, digit);
       if (in && (threadIdx.x & 31) == static_cast<uint32_t>(__ffs(same) - 1)) atomicAdd(&h[digit], static_cast<uint32_t>(__popc(same)));
@@ -260,7 +262,7 @@ __device__ __forceinline__ float code_value(uint32_t w, int i, float s) {
   return static_cast<float>(static_cast<int>((w >> (4 * i)) & 15u) - 8) * s;
 }
 
-constexpr int kMoves = 4;  // rows of one head that a lane has in flight
+constexpr int kMoves = 2;  // rows of one head that a lane has in flight
 
 template <int D>
 __global__ void __launch_bounds__(256) move_kernel(const __grid_constant__ EvictParams p) {
