@@ -143,7 +143,6 @@ __device__ __forceinline__ int32_t sums_row(const KwParams& p, int32_t c, int32_
 // Exponent terms of all queries, one thread each.
 template <bool kCap>
 __global__ void __launch_bounds__(256) key_weights_terms(const __grid_constant__ KwParams p) {
-  griddep_launch_dependents();
   griddep_wait();
   const int64_t i = static_cast<int64_t>(blockIdx.x) * 256 + threadIdx.x;
   if (i >= static_cast<int64_t>(p.B) * p.Hq * p.Sq) return;
@@ -272,7 +271,6 @@ __global__ void __launch_bounds__(kThreads, 1)
   tc_fence_after();
   const uint32_t tmem = __shfl_sync(0xffffffffu, s.tmem_base, 0);
   const WaitCtl wc{p.err, &s.abort_flag, p.wait_ns};
-  griddep_launch_dependents();
   griddep_wait();
   const Cut c0 = p.cut[blockIdx.x], c1 = p.cut[blockIdx.x + 1];
 
@@ -599,7 +597,6 @@ __global__ void __launch_bounds__(kThreads, 1)
 
 // One block per tile: its rows of sums (three of each CTA that had a part of it) added up in order.
 __global__ void __launch_bounds__(128) key_weights_join(const __grid_constant__ KwParams p) {
-  griddep_launch_dependents();
   griddep_wait();
   const int32_t t = static_cast<int32_t>(blockIdx.x);
   // the CTA whose run holds the tile's beginning: the last cut at or before it

@@ -27,17 +27,28 @@
 // it).  l = sum 2^(s_j - R) stays in fp32.  R moves only when it grows by more
 // than 8 (log2 units).
 //
+// Row tiles are of 8, the product's own width.  Tiles of 16 (two products on
+// the same codes) halve the passes over the cache when a head has 9 or more
+// rows, but double the registers of q and O: 41-45 us against 35 us for 16 rows
+// a head (16 sequences, one head of 8192 keys), where the second pass comes out
+// of the second-level cache.
+//
 // Work: all (sequence, head, row tile) pairs' key tiles of 128 form one
 // sequence, cut into equal runs, one per CTA; lengths are read on the device.
 // A run's parts of pairs that other CTAs share go to the workspace as (R, l,
 // O) records; a second kernel joins them in a fixed order and, if asked,
 // turns the stored scores into probabilities and adds them to the weights.
 // Short sequences (a capacity of up to 8 tiles) go a pair to a CTA instead, and
-// nothing is joined.
+// nothing is joined: 128 heads of 512 slots take 13 us so and 19 split, 512 of
+// 1024 32 and 35, 8 of 1024 14 and 12, 8 of 2048 would take 23 for 13.
+//
 // Four warps take 32 keys of a tile each, as two products side by side; the
 // warps take turns in bringing tiles in by bulk copies through a ring of
-// stages.  (Eight warps of 16 keys, one of them loading, needed 453
-// instructions per 16 keys and reached 3.1 TB/s on 64 sequences of 8191 keys.)
+// stages.  What bounds it is the issue of instructions, about 370 per 16 keys
+// and warp, most of them the AND, subtract and pack around the products.
+// 64 sequences of 8191 keys on 8 heads, 32 q heads: 145 us and 8 for the join,
+// 605 MB at 4.2 TB/s (eight warps of 16 keys, one of them loading: 200 us).
+// One sequence of 65,536 keys: 27 us and 10, 75 MB; the join's time is latency.
 #include <cmath>
 
 #include <cuda_fp16.h>
@@ -50,10 +61,11 @@ namespace bsa {
 namespace {
 
 constexpr int kTileKeys = 128;
+constexpr int kRows = 8;                   // rows of a row tile
 constexpr int kWarps = 4;                  // 32 keys of a tile each, as two halves of 16
 constexpr int kWholeTiles = 8;             // longest pair, in tiles, that one CTA takes alone
 constexpr int kThreads = 32 * kWarps;
-constexpr int kWeightKeys = 1024;           // keys of one head whose weights a CTA of the join adds to
+constexpr int kWeightKeys = 1024;          // keys of one head whose weights a CTA of the join adds to
 constexpr float kRescale = 8.0f;
 constexpr float kLog2e = 1.4426950408889634f;
 constexpr float kLn2 = 0.69314718055994530942f;
@@ -77,7 +89,8 @@ struct Kv4FwdParams {
   float* rec_o;             // [2 * n_cta][kRows][D]
   float* scores;            // [B * Hkv * row_tiles][capacity][score_stride], log2 units, or null
   int32_t score_stride;
-  int32_t join_rows;        // blocks of the join kernel that merge rows
+  int32_t join_rows;        // blocks of the join kernel that merge rows ...
+  int32_t rows_per_block;   // ... and how many of a pair's rows each takes (1, or all of a row tile)
   uint32_t* err;
   uint64_t wait_ns;
 };
@@ -202,9 +215,8 @@ struct Run {
   }
 };
 
-template <int D, int NT>
+template <int D>
 struct __align__(128) FwdShared {
-  static constexpr int kRows = 8 * NT;
   static constexpr int kStages = D == 128 ? 3 : 4;
   static constexpr int kAhead = kStages - 1;  // tiles issued before the one being computed
   static constexpr int kPad = D + 4;          // floats between rows of the merge buffer (bank spread)
@@ -333,7 +345,6 @@ __device__ __forceinline__ void store_o4(__nv_bfloat16* o, const float4& x, floa
 }
 
 // Sum of the probabilities of key j over the rows of a row tile that see it.
-template <int kRows>
 __device__ __forceinline__ float key_probs(const Kv4FwdParams& p, const Pair& pair, int32_t bh, int32_t rt, int32_t j,
                                            const float* lse2) {
   const float* sc = p.scores + ((static_cast<int64_t>(bh) * p.row_tiles + rt) * p.c.capacity + j) * p.score_stride;
@@ -347,12 +358,12 @@ __device__ __forceinline__ float key_probs(const Kv4FwdParams& p, const Pair& pa
   return w;
 }
 
-template <int D, int NT, bool kCap>
-__global__ void __launch_bounds__(kThreads, NT == 1 ? 3 : 2) kv4_fwd_kernel(const __grid_constant__ Kv4FwdParams p) {
+template <int D, bool kCap>
+__global__ void __launch_bounds__(kThreads, 3) kv4_fwd_kernel(const __grid_constant__ Kv4FwdParams p) {
   extern __shared__ __align__(128) uint8_t smem_raw[];
-  using Sh = FwdShared<D, NT>;
+  using Sh = FwdShared<D>;
   Sh& s = *reinterpret_cast<Sh*>(smem_raw);
-  constexpr int kRows = Sh::kRows, kStages = Sh::kStages, kGroups = Kv4<D>::kGroups;
+  constexpr int kStages = Sh::kStages, kGroups = Kv4<D>::kGroups;
   constexpr int kRowBytes = Kv4<D>::kRowBytes, kScaleBytes = Kv4<D>::kScaleBytes;
   const int warp = warp_id(), lane = threadIdx.x & 31;
   if (threadIdx.x == 0) {
@@ -364,7 +375,9 @@ __global__ void __launch_bounds__(kThreads, NT == 1 ? 3 : 2) kv4_fwd_kernel(cons
     fence_mbar_init();
   }
   __syncthreads();
-  griddep_launch_dependents();
+  // (not before a join: its early blocks would wait in the place of CTAs of the call after next, which
+  // took 16 sequences of 8192 keys with 16 rows a head from 38 to 54 us a call)
+  if (p.whole) griddep_launch_dependents();
   griddep_wait();
   const WaitCtl wc{p.err, &s.abort_flag, p.wait_ns};
   Run run;
@@ -426,85 +439,79 @@ __global__ void __launch_bounds__(kThreads, NT == 1 ? 3 : 2) kv4_fwd_kernel(cons
     const int32_t h = run.bh % p.c.Hkv;
     const int64_t head = static_cast<int64_t>(run.bh) * p.row_tiles + run.rt;
     // Q as fp16 operands, the start of K's accumulators, and per column its factor and last slot
-    uint32_t qb[NT][kGroups][4];
-    float init[NT][kGroups][2], qf[NT][2];
-    int32_t lim[NT][2];
+    uint32_t qb[kGroups][4];
+    float init[kGroups][2], qf[2];
+    int32_t lim[2];
     int32_t lim_min = INT32_MAX, lim_max = 0;
+    const int32_t r = run.rt * kRows + g8;  // this lane's row while loading Q
+    const bool in = r < p.R;
+    const int32_t t = in ? r % p.T : 0;
+    uint4 raw[kGroups];
+    uint32_t mx = 0;
 #pragma unroll
-    for (int nt = 0; nt < NT; ++nt) {
-      const int32_t r = run.rt * kRows + nt * 8 + g8;  // this lane's row while loading Q
-      const bool in = r < p.R;
-      const int32_t t = in ? r % p.T : 0;
-      uint4 raw[kGroups];
-      uint32_t mx = 0;
+    for (int g = 0; g < kGroups; ++g) {
+      raw[g] = in ? *reinterpret_cast<const uint4*>(p.q + run.pair.b * p.qs[0] + (h * p.G + r / p.T) * p.qs[1] + t * p.qs[2] +
+                                                    32 * g + 8 * t4)
+                  : make_uint4(0, 0, 0, 0);
+      const uint32_t w[4] = {raw[g].x, raw[g].y, raw[g].z, raw[g].w};
 #pragma unroll
-      for (int g = 0; g < kGroups; ++g) {
-        raw[g] = in ? *reinterpret_cast<const uint4*>(p.q + run.pair.b * p.qs[0] + (h * p.G + r / p.T) * p.qs[1] + t * p.qs[2] +
-                                                      32 * g + 8 * t4)
-                    : make_uint4(0, 0, 0, 0);
-        const uint32_t w[4] = {raw[g].x, raw[g].y, raw[g].z, raw[g].w};
-#pragma unroll
-        for (int i = 0; i < 4; ++i) mx = max(mx, max(w[i] & 0x7FFFu, (w[i] >> 16) & 0x7FFFu));
-      }
-      mx = max(mx, __shfl_xor_sync(0xffffffffu, mx, 1));
-      mx = max(mx, __shfl_xor_sync(0xffffffffu, mx, 2));
-      // power of two that brings the row's largest magnitude to [2^14, 2^15)
-      const int e = mx == 0 || mx >= 0x7F80u ? 0 : 14 + 127 - static_cast<int>(max(mx >> 7, 1u));
-      const float up = exp2f(static_cast<float>(e / 2)), up2 = exp2f(static_cast<float>(e - e / 2));
-      float sum[kGroups];
-#pragma unroll
-      for (int g = 0; g < kGroups; ++g) {
-        const uint32_t w[4] = {raw[g].x, raw[g].y, raw[g].z, raw[g].w};
-        float x[8];
-#pragma unroll
-        for (int i = 0; i < 4; ++i) {
-          x[2 * i] = bf16_lo(w[i]) * up * up2;
-          x[2 * i + 1] = bf16_hi(w[i]) * up * up2 * 0.0625f;
-        }
-        sum[g] = 0.f;
-#pragma unroll
-        for (int hf = 0; hf < 2; ++hf) {  // elements 2 hf (+4) and 2 hf + 1 (+4): see kv4.cuh
-          const __half2 even = __floats2half2_rn(x[2 * hf], x[2 * hf + 4]);
-          const __half2 odd = __floats2half2_rn(x[2 * hf + 1], x[2 * hf + 5]);
-          qb[nt][g][2 * hf] = *reinterpret_cast<const uint32_t*>(&even);
-          qb[nt][g][2 * hf + 1] = *reinterpret_cast<const uint32_t*>(&odd);
-          const float2 fe = __half22float2(even), fo = __half22float2(odd);
-          sum[g] += fe.x + fe.y + 16.f * (fo.x + fo.y);
-        }
-        sum[g] += __shfl_xor_sync(0xffffffffu, sum[g], 1);
-        sum[g] += __shfl_xor_sync(0xffffffffu, sum[g], 2);
-      }
-      const float f = p.scale_log2 * 16777216.f * exp2f(static_cast<float>(-e));
-      const int32_t last = in && t < run.pair.nq ? max(0, run.pair.len - run.pair.nq + t + 1) : 0;
-#pragma unroll
-      for (int i = 0; i < 2; ++i) {  // this lane's columns are rows 2 t4 and 2 t4 + 1
-        const int from = 4 * (2 * t4 + i);
-#pragma unroll
-        for (int g = 0; g < kGroups; ++g) init[nt][g][i] = __shfl_sync(0xffffffffu, sum[g], from) * (-8.f / 16777216.f);
-        qf[nt][i] = __shfl_sync(0xffffffffu, f, from);
-        lim[nt][i] = __shfl_sync(0xffffffffu, last, from);
-      }
-      int32_t lo = in ? last : INT32_MAX, hi = last;
-#pragma unroll
-      for (int o = 4; o < 32; o *= 2) {
-        lo = min(lo, __shfl_xor_sync(0xffffffffu, lo, o));
-        hi = max(hi, __shfl_xor_sync(0xffffffffu, hi, o));
-      }
-      lim_min = min(lim_min, lo);
-      lim_max = max(lim_max, hi);
+      for (int i = 0; i < 4; ++i) mx = max(mx, max(w[i] & 0x7FFFu, (w[i] >> 16) & 0x7FFFu));
     }
+    mx = max(mx, __shfl_xor_sync(0xffffffffu, mx, 1));
+    mx = max(mx, __shfl_xor_sync(0xffffffffu, mx, 2));
+    // power of two that brings the row's largest magnitude to [2^14, 2^15)
+    const int e = mx == 0 || mx >= 0x7F80u ? 0 : 14 + 127 - static_cast<int>(max(mx >> 7, 1u));
+    const float up = exp2f(static_cast<float>(e / 2)), up2 = exp2f(static_cast<float>(e - e / 2));
+    float sum[kGroups];
+#pragma unroll
+    for (int g = 0; g < kGroups; ++g) {
+      const uint32_t w[4] = {raw[g].x, raw[g].y, raw[g].z, raw[g].w};
+      float x[8];
+#pragma unroll
+      for (int i = 0; i < 4; ++i) {
+        x[2 * i] = bf16_lo(w[i]) * up * up2;
+        x[2 * i + 1] = bf16_hi(w[i]) * up * up2 * 0.0625f;
+      }
+      sum[g] = 0.f;
+#pragma unroll
+      for (int hf = 0; hf < 2; ++hf) {  // elements 2 hf (+4) and 2 hf + 1 (+4): see kv4.cuh
+        const __half2 even = __floats2half2_rn(x[2 * hf], x[2 * hf + 4]);
+        const __half2 odd = __floats2half2_rn(x[2 * hf + 1], x[2 * hf + 5]);
+        qb[g][2 * hf] = *reinterpret_cast<const uint32_t*>(&even);
+        qb[g][2 * hf + 1] = *reinterpret_cast<const uint32_t*>(&odd);
+        const float2 fe = __half22float2(even), fo = __half22float2(odd);
+        sum[g] += fe.x + fe.y + 16.f * (fo.x + fo.y);
+      }
+      sum[g] += __shfl_xor_sync(0xffffffffu, sum[g], 1);
+      sum[g] += __shfl_xor_sync(0xffffffffu, sum[g], 2);
+    }
+    const float f = p.scale_log2 * 16777216.f * exp2f(static_cast<float>(-e));
+    const int32_t last = in && t < run.pair.nq ? max(0, run.pair.len - run.pair.nq + t + 1) : 0;
+#pragma unroll
+    for (int i = 0; i < 2; ++i) {  // this lane's columns are rows 2 t4 and 2 t4 + 1
+      const int from = 4 * (2 * t4 + i);
+#pragma unroll
+      for (int g = 0; g < kGroups; ++g) init[g][i] = __shfl_sync(0xffffffffu, sum[g], from) * (-8.f / 16777216.f);
+      qf[i] = __shfl_sync(0xffffffffu, f, from);
+      lim[i] = __shfl_sync(0xffffffffu, last, from);
+    }
+    int32_t lo = in ? last : INT32_MAX, hi = last;
+#pragma unroll
+    for (int o = 4; o < 32; o *= 2) {
+      lo = min(lo, __shfl_xor_sync(0xffffffffu, lo, o));
+      hi = max(hi, __shfl_xor_sync(0xffffffffu, hi, o));
+    }
+    lim_min = min(lim_min, lo);
+    lim_max = max(lim_max, hi);
 
-    float acc[NT][2 * kGroups][4];
-    float R[NT][2], l[NT][2];
+    float acc[2 * kGroups][4];
+    float R[2], l[2];
 #pragma unroll
-    for (int nt = 0; nt < NT; ++nt) {
+    for (int j = 0; j < 2 * kGroups; ++j)
 #pragma unroll
-      for (int j = 0; j < 2 * kGroups; ++j)
-#pragma unroll
-        for (int i = 0; i < 4; ++i) acc[nt][j][i] = 0.f;
-      R[nt][0] = R[nt][1] = -INFINITY;
-      l[nt][0] = l[nt][1] = 0.f;
-    }
+      for (int i = 0; i < 4; ++i) acc[j][i] = 0.f;
+    R[0] = R[1] = -INFINITY;
+    l[0] = l[1] = 0.f;
     int base = INT32_MAX;        // base exponent of the value scales (uniform over the warp; not yet chosen)
     uint32_t near_lo = 0;        // bf16 bits from here on, for three binades, are near it
     float down = 1.f, up_back = 1.f;  // 2^-base, 2^base
@@ -517,7 +524,7 @@ __global__ void __launch_bounds__(kThreads, NT == 1 ? 3 : 2) kv4_fwd_kernel(cons
       if (key0 < lim_max) {
         const bool all_seen = __all_sync(0xffffffffu, key0 + 32 <= lim_min);
         // ---- scores of both halves
-        float x[2][NT][4];
+        float x[2][4];
 #pragma unroll
         for (int u = 0; u < 2; ++u) {
           uint32_t ka[kGroups], kb[kGroups], sa[kGroups / 2], sb[kGroups / 2];
@@ -530,17 +537,14 @@ __global__ void __launch_bounds__(kThreads, NT == 1 ? 3 : 2) kv4_fwd_kernel(cons
             const float fa = g & 1 ? bf16_hi(sa[g / 2]) : bf16_lo(sa[g / 2]);
             const float fb = g & 1 ? bf16_hi(sb[g / 2]) : bf16_lo(sb[g / 2]);
             const uint32_t a8 = ka[g] >> 8, b8 = kb[g] >> 8;
-#pragma unroll
-            for (int nt = 0; nt < NT; ++nt) {
-              float c[4];
-              mma_f16_from(c, ka[g] & 0x000F000Fu, kb[g] & 0x000F000Fu, ka[g] & 0x00F000F0u, kb[g] & 0x00F000F0u,
-                           qb[nt][g][0], qb[nt][g][1], init[nt][g][0], init[nt][g][1]);
-              mma_f16(c, a8 & 0x000F000Fu, b8 & 0x000F000Fu, a8 & 0x00F000F0u, b8 & 0x00F000F0u, qb[nt][g][2], qb[nt][g][3]);
-              x[u][nt][0] = g ? fmaf(fa, c[0], x[u][nt][0]) : fa * c[0];
-              x[u][nt][1] = g ? fmaf(fa, c[1], x[u][nt][1]) : fa * c[1];
-              x[u][nt][2] = g ? fmaf(fb, c[2], x[u][nt][2]) : fb * c[2];
-              x[u][nt][3] = g ? fmaf(fb, c[3], x[u][nt][3]) : fb * c[3];
-            }
+            float c[4];
+            mma_f16_from(c, ka[g] & 0x000F000Fu, kb[g] & 0x000F000Fu, ka[g] & 0x00F000F0u, kb[g] & 0x00F000F0u,
+                         qb[g][0], qb[g][1], init[g][0], init[g][1]);
+            mma_f16(c, a8 & 0x000F000Fu, b8 & 0x000F000Fu, a8 & 0x00F000F0u, b8 & 0x00F000F0u, qb[g][2], qb[g][3]);
+            x[u][0] = g ? fmaf(fa, c[0], x[u][0]) : fa * c[0];
+            x[u][1] = g ? fmaf(fa, c[1], x[u][1]) : fa * c[1];
+            x[u][2] = g ? fmaf(fb, c[2], x[u][2]) : fb * c[2];
+            x[u][3] = g ? fmaf(fb, c[3], x[u][3]) : fb * c[3];
           }
         }
         // ---- value scales: are all keys' near the base?
@@ -574,63 +578,60 @@ __global__ void __launch_bounds__(kThreads, NT == 1 ? 3 : 2) kv4_fwd_kernel(cons
           e[3] = far_exponent(vb[1][0], vb[1][kGroups / 2 - 1], base);
         }
         // ---- softmax
-        float pr[2][NT][4];
+        float pr[2][4];
 #pragma unroll
-        for (int nt = 0; nt < NT; ++nt) {
+        for (int u = 0; u < 2; ++u)
+#pragma unroll
+          for (int i = 0; i < 4; ++i) {
+            x[u][i] *= qf[i & 1];
+            if constexpr (kCap) x[u][i] = p.cap_log2 * tanh_fast(x[u][i]);
+          }
+        if (!all_seen) {
 #pragma unroll
           for (int u = 0; u < 2; ++u)
 #pragma unroll
-            for (int i = 0; i < 4; ++i) {
-              x[u][nt][i] *= qf[nt][i & 1];
-              if constexpr (kCap) x[u][nt][i] = p.cap_log2 * tanh_fast(x[u][nt][i]);
-            }
-          if (!all_seen) {
-#pragma unroll
-            for (int u = 0; u < 2; ++u)
-#pragma unroll
-              for (int i = 0; i < 4; ++i)
-                if (key0 + 16 * u + g8 + (i >> 1) * 8 >= lim[nt][i & 1]) x[u][nt][i] = -INFINITY;
-          }
-          if (p.scores && nt * 8 + 2 * t4 < p.score_stride) {
-#pragma unroll
-            for (int u = 0; u < 2; ++u) {
-              if (key0 + 16 * u >= p.c.capacity) continue;
-              float* out = p.scores + (head * p.c.capacity + key0 + 16 * u + g8) * p.score_stride + nt * 8 + 2 * t4;
-              *reinterpret_cast<float2*>(out) = make_float2(x[u][nt][0], x[u][nt][1]);
-              *reinterpret_cast<float2*>(out + 8 * p.score_stride) = make_float2(x[u][nt][2], x[u][nt][3]);
-            }
-          }
-#pragma unroll
-          for (int i = 0; i < 2; ++i) {
-            float m = fmaxf(fmaxf(x[0][nt][i] + e[0], x[0][nt][i + 2] + e[1]), fmaxf(x[1][nt][i] + e[2], x[1][nt][i + 2] + e[3]));
-#pragma unroll
-            for (int o = 4; o < 32; o *= 2) m = fmaxf(m, __shfl_xor_sync(0xffffffffu, m, o));
-            const bool move = m > R[nt][i] + kRescale;
-            if (__any_sync(0xffffffffu, move)) {
-              // (uniform over the lanes of a column)
-              const float to = move ? m : R[nt][i];
-              const float f = R[nt][i] == -INFINITY ? 0.f : ex2_approx(R[nt][i] - to);
-              R[nt][i] = to;
-              l[nt][i] *= f;
-#pragma unroll
-              for (int j = 0; j < 2 * kGroups; ++j) {
-                acc[nt][j][i] *= f;
-                acc[nt][j][i + 2] *= f;
-              }
-            }
-            const float ref = R[nt][i] == -INFINITY ? 0.f : R[nt][i];
-#pragma unroll
-            for (int u = 0; u < 2; ++u) {
-              pr[u][nt][i] = ex2_approx(x[u][nt][i] - ref);
-              pr[u][nt][i + 2] = ex2_approx(x[u][nt][i + 2] - ref);
-            }
-            l[nt][i] += (pr[0][nt][i] + pr[0][nt][i + 2]) + (pr[1][nt][i] + pr[1][nt][i + 2]);
-          }
-#pragma unroll
-          for (int u = 0; u < 2; ++u)
-#pragma unroll
-            for (int i = 0; i < 4; ++i) pr[u][nt][i] *= down;
+            for (int i = 0; i < 4; ++i)
+              if (key0 + 16 * u + g8 + (i >> 1) * 8 >= lim[i & 1]) x[u][i] = -INFINITY;
         }
+        if (p.scores && 2 * t4 < p.score_stride) {
+#pragma unroll
+          for (int u = 0; u < 2; ++u) {
+            if (key0 + 16 * u >= p.c.capacity) continue;
+            float* out = p.scores + (head * p.c.capacity + key0 + 16 * u + g8) * p.score_stride + 2 * t4;
+            *reinterpret_cast<float2*>(out) = make_float2(x[u][0], x[u][1]);
+            *reinterpret_cast<float2*>(out + 8 * p.score_stride) = make_float2(x[u][2], x[u][3]);
+          }
+        }
+#pragma unroll
+        for (int i = 0; i < 2; ++i) {
+          float m = fmaxf(fmaxf(x[0][i] + e[0], x[0][i + 2] + e[1]), fmaxf(x[1][i] + e[2], x[1][i + 2] + e[3]));
+#pragma unroll
+          for (int o = 4; o < 32; o *= 2) m = fmaxf(m, __shfl_xor_sync(0xffffffffu, m, o));
+          const bool move = m > R[i] + kRescale;
+          if (__any_sync(0xffffffffu, move)) {
+            // (uniform over the lanes of a column)
+            const float to = move ? m : R[i];
+            const float f = R[i] == -INFINITY ? 0.f : ex2_approx(R[i] - to);
+            R[i] = to;
+            l[i] *= f;
+#pragma unroll
+            for (int j = 0; j < 2 * kGroups; ++j) {
+              acc[j][i] *= f;
+              acc[j][i + 2] *= f;
+            }
+          }
+          const float ref = R[i] == -INFINITY ? 0.f : R[i];
+#pragma unroll
+          for (int u = 0; u < 2; ++u) {
+            pr[u][i] = ex2_approx(x[u][i] - ref);
+            pr[u][i + 2] = ex2_approx(x[u][i + 2] - ref);
+          }
+          l[i] += (pr[0][i] + pr[0][i + 2]) + (pr[1][i] + pr[1][i + 2]);
+        }
+#pragma unroll
+        for (int u = 0; u < 2; ++u)
+#pragma unroll
+          for (int i = 0; i < 4; ++i) pr[u][i] *= down;
         // ---- output, a half at a time
 #pragma unroll
         for (int u = 0; u < 2; ++u) {
@@ -645,18 +646,15 @@ __global__ void __launch_bounds__(kThreads, NT == 1 ? 3 : 2) kv4_fwd_kernel(cons
             // probabilities times value scales, transposed into the second product's operand
             const float fa = g & 1 ? bf16_hi(va[u][g / 2]) : bf16_lo(va[u][g / 2]);
             const float fb = g & 1 ? bf16_hi(vb[u][g / 2]) : bf16_lo(vb[u][g / 2]);
-            uint32_t b0[NT], b1[NT];
+            uint32_t b0, b1;
+            float w[4] = {pr[u][0] * fa, pr[u][1] * fa, pr[u][2] * fb, pr[u][3] * fb};
+            if (!all_seen) {  // (an unseen slot's scale may be anything)
 #pragma unroll
-            for (int nt = 0; nt < NT; ++nt) {
-              float w[4] = {pr[u][nt][0] * fa, pr[u][nt][1] * fa, pr[u][nt][2] * fb, pr[u][nt][3] * fb};
-              if (!all_seen) {  // (an unseen slot's scale may be anything)
-#pragma unroll
-                for (int i = 0; i < 4; ++i)
-                  if (x[u][nt][i] == -INFINITY) w[i] = 0.f;
-              }
-              b0[nt] = transpose8x8(pack_f16x2(w[0], w[1]));
-              b1[nt] = transpose8x8(pack_f16x2(w[2], w[3]));
+              for (int i = 0; i < 4; ++i)
+                if (x[u][i] == -INFINITY) w[i] = 0.f;
             }
+            b0 = transpose8x8(pack_f16x2(w[0], w[1]));
+            b1 = transpose8x8(pack_f16x2(w[2], w[3]));
             const uint32_t sel = g & 1 ? sel_hi : sel_lo;
             const uint32_t lo = __byte_perm(v0[g / 2], v1[g / 2], sel), hi = __byte_perm(v8[g / 2], v9[g / 2], sel);
             // elements 4 g8 + 0..3 of the group: rows g8 and (times 16) g8 + 8 of two products
@@ -665,11 +663,8 @@ __global__ void __launch_bounds__(kThreads, NT == 1 ? 3 : 2) kv4_fwd_kernel(cons
             const uint32_t lo8 = lo >> 8, hi8 = hi >> 8;
             const uint32_t c0 = minus8(lo8 & 0x000F000Fu, 0x00080008u), c1 = minus8(lo8 & 0x00F000F0u, 0x00800080u);
             const uint32_t c2 = minus8(hi8 & 0x000F000Fu, 0x00080008u), c3 = minus8(hi8 & 0x00F000F0u, 0x00800080u);
-#pragma unroll
-            for (int nt = 0; nt < NT; ++nt) {
-              mma_f16(acc[nt][2 * g], a0, a1, a2, a3, b0[nt], b1[nt]);
-              mma_f16(acc[nt][2 * g + 1], c0, c1, c2, c3, b0[nt], b1[nt]);
-            }
+            mma_f16(acc[2 * g], a0, a1, a2, a3, b0, b1);
+            mma_f16(acc[2 * g + 1], c0, c1, c2, c3, b0, b1);
           }
         }
       }
@@ -689,51 +684,45 @@ __global__ void __launch_bounds__(kThreads, NT == 1 ? 3 : 2) kv4_fwd_kernel(cons
 
     // ---- the warps' parts into one
 #pragma unroll
-    for (int nt = 0; nt < NT; ++nt)
+    for (int i = 0; i < 2; ++i) {
 #pragma unroll
-      for (int i = 0; i < 2; ++i) {
-#pragma unroll
-        for (int o = 4; o < 32; o *= 2) l[nt][i] += __shfl_xor_sync(0xffffffffu, l[nt][i], o);
-        if (g8 == 0) {
-          s.stat[0][warp][nt * 8 + 2 * t4 + i] = R[nt][i];
-          s.stat[1][warp][nt * 8 + 2 * t4 + i] = l[nt][i];
-        }
+      for (int o = 4; o < 32; o *= 2) l[i] += __shfl_xor_sync(0xffffffffu, l[i], o);
+      if (g8 == 0) {
+        s.stat[0][warp][2 * t4 + i] = R[i];
+        s.stat[1][warp][2 * t4 + i] = l[i];
       }
+    }
     __syncthreads();
-    auto slot = [&](int nt, int i, int g) -> float4* {
-      return reinterpret_cast<float4*>(&s.merge[warp % (kWarps / 2)][(nt * 8 + 2 * t4 + i) * Sh::kPad + 32 * g + 4 * g8]);
+    auto slot = [&](int i, int g) -> float4* {
+      return reinterpret_cast<float4*>(&s.merge[warp % (kWarps / 2)][(2 * t4 + i) * Sh::kPad + 32 * g + 4 * g8]);
     };
     // this warp's share of a column's output, for the common reference
-    auto share = [&](int nt, int i, int g) -> float4 {
+    auto share = [&](int i, int g) -> float4 {
       float m = -INFINITY;
 #pragma unroll
-      for (int w = 0; w < kWarps; ++w) m = fmaxf(m, s.stat[0][w][nt * 8 + 2 * t4 + i]);
-      const float f = R[nt][i] == -INFINITY ? (l[nt][i] == 0.f ? 0.f : 1.f) : ex2_approx(R[nt][i] - m);
+      for (int w = 0; w < kWarps; ++w) m = fmaxf(m, s.stat[0][w][2 * t4 + i]);
+      const float f = R[i] == -INFINITY ? (l[i] == 0.f ? 0.f : 1.f) : ex2_approx(R[i] - m);
       const float even = f * 16777216.f, odd = even * 0.0625f;
       // (2^base by itself: it may be far from 1)
-      return make_float4(acc[nt][2 * g][i] * even * up_back, acc[nt][2 * g][i + 2] * odd * up_back,
-                         acc[nt][2 * g + 1][i] * even * up_back, acc[nt][2 * g + 1][i + 2] * odd * up_back);
+      return make_float4(acc[2 * g][i] * even * up_back, acc[2 * g][i + 2] * odd * up_back,
+                         acc[2 * g + 1][i] * even * up_back, acc[2 * g + 1][i + 2] * odd * up_back);
     };
     if (warp >= kWarps / 2) {
 #pragma unroll
-      for (int nt = 0; nt < NT; ++nt)
+      for (int i = 0; i < 2; ++i)
 #pragma unroll
-        for (int i = 0; i < 2; ++i)
-#pragma unroll
-          for (int g = 0; g < kGroups; ++g) *slot(nt, i, g) = share(nt, i, g);
+        for (int g = 0; g < kGroups; ++g) *slot(i, g) = share(i, g);
     }
     __syncthreads();
     if (warp < kWarps / 2) {
 #pragma unroll
-      for (int nt = 0; nt < NT; ++nt)
+      for (int i = 0; i < 2; ++i)
 #pragma unroll
-        for (int i = 0; i < 2; ++i)
-#pragma unroll
-          for (int g = 0; g < kGroups; ++g) {
-            float4* at = slot(nt, i, g);
-            const float4 a = *at, b = share(nt, i, g);
-            *at = make_float4(a.x + b.x, a.y + b.y, a.z + b.z, a.w + b.w);
-          }
+        for (int g = 0; g < kGroups; ++g) {
+          float4* at = slot(i, g);
+          const float4 a = *at, b = share(i, g);
+          *at = make_float4(a.x + b.x, a.y + b.y, a.z + b.z, a.w + b.w);
+        }
     }
     __syncthreads();
     const int32_t rec = 2 * static_cast<int32_t>(blockIdx.x) + (first_part ? 0 : 1);
@@ -778,8 +767,9 @@ __global__ void __launch_bounds__(kThreads, NT == 1 ? 3 : 2) kv4_fwd_kernel(cons
       // (one row tile) this CTA's own scores into probabilities
       __syncthreads();
       for (int32_t j = threadIdx.x; j < run.pair.len; j += kThreads)
-        p.c.weights[static_cast<int64_t>(run.bh) * p.c.capacity + j] += key_probs<kRows>(p, run.pair, run.bh, 0, j, s.lse2);
+        p.c.weights[static_cast<int64_t>(run.bh) * p.c.capacity + j] += key_probs(p, run.pair, run.bh, 0, j, s.lse2);
     }
+    __syncthreads();  // the next part, maybe of few tiles, writes `stat` and `merge` again
   }
   if (!__syncthreads_and(ok) && threadIdx.x == 0) {
     // the copies in flight land before the CTA exits
@@ -816,7 +806,6 @@ __device__ __forceinline__ Records pair_records(const Kv4FwdParams& p, int32_t b
 constexpr int kJoinThreads = 256;
 
 // Joins records: every row of the pair's reference and sum, by the whole CTA.
-template <int kRows>
 __device__ __forceinline__ void join_stats(const Kv4FwdParams& p, const Records& x, float (*part)[2][kRows], float* R, float* L) {
   constexpr int kSub = 32 / kRows;  // records side by side in a warp
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5, row = lane % kRows;
@@ -856,38 +845,37 @@ __device__ __forceinline__ void join_stats(const Kv4FwdParams& p, const Records&
   __syncthreads();
 }
 
-template <int D, int NT>
+template <int D>
 __global__ void __launch_bounds__(kJoinThreads) kv4_join_kernel(const __grid_constant__ Kv4FwdParams p) {
-  constexpr int kRows = 8 * NT;
   constexpr int kVec = D / 4;                 // lanes (float4) of one row
   constexpr int kSplit = kJoinThreads / kVec;  // records read side by side
   __shared__ float4 part[kSplit][kVec];
   __shared__ float stats[kJoinThreads / 32][2][kRows], R[kRows], L[kRows];
-  griddep_launch_dependents();
   griddep_wait();
   if (static_cast<int32_t>(blockIdx.x) < p.join_rows) {
-    // ---- one row's output
-    const int32_t row = static_cast<int32_t>(blockIdx.x) % kRows;
-    const int32_t hr = static_cast<int32_t>(blockIdx.x) / kRows;
-    const int32_t rt = hr % p.row_tiles, bh = hr / p.row_tiles, r = rt * kRows + row;
-    if (r >= p.R) return;
+    // ---- output of one row, or of all rows of a pair side by side
+    const int32_t blocks = p.rows_per_block == 1 ? min(p.R, kRows) : 1;  // per pair (a last, shorter row tile has idle ones)
+    const int32_t hr = static_cast<int32_t>(blockIdx.x) / blocks, rt = hr % p.row_tiles, bh = hr / p.row_tiles;
     const Records x = pair_records(p, bh, rt, load_pair(p, bh / p.c.Hkv, nullptr));
     if (x.tiles > 0 && x.c0 == x.c1) return;  // one CTA had all of it
     const int lane = threadIdx.x % kVec, sub = threadIdx.x / kVec;
+    const int split = kSplit / p.rows_per_block;  // records of a row read side by side
+    const int row = p.rows_per_block == 1 ? static_cast<int32_t>(blockIdx.x) % blocks : sub / split;
+    const int32_t r = rt * kRows + row;
     if (x.tiles > 0) {
-      join_stats<kRows>(p, x, stats, R, L);
+      join_stats(p, x, stats, R, L);
     } else {
-      if (threadIdx.x == 0) {
-        R[row] = -INFINITY;
-        L[row] = 0.f;
+      if (threadIdx.x < kRows) {
+        R[threadIdx.x] = -INFINITY;
+        L[threadIdx.x] = 0.f;
       }
       __syncthreads();
     }
     const float m = R[row];
     float4 o = make_float4(0.f, 0.f, 0.f, 0.f);
-    if (x.tiles > 0) {
+    if (x.tiles > 0 && r < p.R) {
 #pragma unroll 4
-      for (int32_t c = x.c0 + sub; c <= x.c1; c += kSplit) {
+      for (int32_t c = x.c0 + sub % split; c <= x.c1; c += split) {
         const int32_t rec = x.of(c);
         const float* st = p.rec_stat + rec * 2 * kRows + row;
         const float w = st[kRows] == 0.f ? 0.f : (m == -INFINITY ? 1.f : ex2_approx(st[0] - m));
@@ -900,9 +888,9 @@ __global__ void __launch_bounds__(kJoinThreads) kv4_join_kernel(const __grid_con
     }
     part[sub][lane] = o;
     __syncthreads();
-    if (sub == 0) {
-      for (int i = 1; i < kSplit; ++i) {
-        const float4 y = part[i][lane];
+    if (sub % split == 0 && r < p.R) {
+      for (int i = 1; i < split; ++i) {
+        const float4 y = part[sub + i][lane];
         o.x += y.x;
         o.y += y.y;
         o.z += y.z;
@@ -925,7 +913,7 @@ __global__ void __launch_bounds__(kJoinThreads) kv4_join_kernel(const __grid_con
   float w[kWeightKeys / kJoinThreads] = {};
   for (int32_t rt = 0; rt < p.row_tiles; ++rt) {
     const Records x = pair_records(p, bh, rt, pair);
-    if (x.c0 != x.c1) join_stats<kRows>(p, x, stats, R, L);
+    if (x.c0 != x.c1) join_stats(p, x, stats, R, L);
     else __syncthreads();
     if (threadIdx.x < kRows) {
       const int32_t r = rt * kRows + static_cast<int32_t>(threadIdx.x);
@@ -938,7 +926,7 @@ __global__ void __launch_bounds__(kJoinThreads) kv4_join_kernel(const __grid_con
 #pragma unroll
     for (int i = 0; i < kWeightKeys / kJoinThreads; ++i) {
       const int32_t j = j0 + i * kJoinThreads + static_cast<int32_t>(threadIdx.x);
-      if (j < pair.len) w[i] += key_probs<kRows>(p, pair, bh, rt, j, R);
+      if (j < pair.len) w[i] += key_probs(p, pair, bh, rt, j, R);
     }
     __syncthreads();
   }
@@ -951,7 +939,7 @@ __global__ void __launch_bounds__(kJoinThreads) kv4_join_kernel(const __grid_con
 
 // Sizes of a call that both the workspace query and the launch use.
 struct Plan {
-  int NT, rows, row_tiles, n_cta, stride;
+  int row_tiles, n_cta, stride;
   bool whole;
   size_t stat_bytes, o_bytes, score_bytes;
 };
@@ -959,25 +947,23 @@ struct Plan {
 Plan make_plan(const bsa_kv4_fwd_args* a) {
   Plan x;
   const int64_t R = static_cast<int64_t>(a->Hq / a->cache.Hkv) * a->T;
-  x.NT = 1;
-  x.rows = 8 * x.NT;
-  x.row_tiles = static_cast<int>((R + x.rows - 1) / x.rows);
+  x.row_tiles = static_cast<int>((R + kRows - 1) / kRows);
   const int64_t tiles = (a->cache.capacity + kTileKeys - 1) / kTileKeys;
   const int64_t pairs = static_cast<int64_t>(a->cache.B) * a->cache.Hkv * x.row_tiles;
   // (a key's weight has one writer: rows in several tiles are added up by the join)
   x.whole = tiles <= kWholeTiles && !(a->accumulate && x.row_tiles > 1) && pairs <= INT32_MAX;
-  x.n_cta = static_cast<int>(x.whole ? pairs : std::min<int64_t>(pairs * tiles, static_cast<int64_t>(num_sms()) * (x.NT == 1 ? 3 : 2)));
-  x.stride = static_cast<int>((std::min<int64_t>(R, x.rows) + 1) & ~int64_t(1));
-  x.stat_bytes = x.whole ? 0 : static_cast<size_t>(2 * x.n_cta) * 2 * x.rows * sizeof(float);
-  x.o_bytes = x.whole ? 0 : static_cast<size_t>(2 * x.n_cta) * x.rows * a->cache.D * sizeof(float);
+  x.n_cta = static_cast<int>(x.whole ? pairs : std::min<int64_t>(pairs * tiles, static_cast<int64_t>(num_sms()) * 3));
+  x.stride = static_cast<int>((std::min<int64_t>(R, kRows) + 1) & ~int64_t(1));
+  x.stat_bytes = x.whole ? 0 : static_cast<size_t>(2 * x.n_cta) * 2 * kRows * sizeof(float);
+  x.o_bytes = x.whole ? 0 : static_cast<size_t>(2 * x.n_cta) * kRows * a->cache.D * sizeof(float);
   x.score_bytes = a->accumulate ? static_cast<size_t>(pairs) * a->cache.capacity * x.stride * sizeof(float) : 0;
   return x;
 }
 
-template <int D, int NT>
+template <int D>
 bsa_status launch(const Kv4FwdParams& p, int accumulate, cudaStream_t stream) {
-  auto kern = p.cap_log2 > 0.f ? kv4_fwd_kernel<D, NT, true> : kv4_fwd_kernel<D, NT, false>;
-  const size_t smem = sizeof(FwdShared<D, NT>);
+  auto kern = p.cap_log2 > 0.f ? kv4_fwd_kernel<D, true> : kv4_fwd_kernel<D, false>;
+  const size_t smem = sizeof(FwdShared<D>);
   const bsa_status st = ensure_smem_attr(reinterpret_cast<const void*>(kern), smem, "set kv4 forward smem size");
   if (st != BSA_OK) return st;
   cudaError_t e = launch_kernel(kern, dim3(p.n_cta), dim3(kThreads), smem, stream, p);
@@ -985,7 +971,7 @@ bsa_status launch(const Kv4FwdParams& p, int accumulate, cudaStream_t stream) {
   if (e != cudaSuccess) return cuda_fail(e, "kv4 forward launch");
   if (p.whole) return BSA_OK;
   const int64_t chunks = accumulate ? (p.c.capacity + kWeightKeys - 1) / kWeightKeys * p.c.B * p.c.Hkv : 0;
-  e = launch_kernel(kv4_join_kernel<D, NT>, dim3(static_cast<unsigned>(p.join_rows + chunks)), dim3(kJoinThreads), 0, stream, p);
+  e = launch_kernel(kv4_join_kernel<D>, dim3(static_cast<unsigned>(p.join_rows + chunks)), dim3(kJoinThreads), 0, stream, p);
   if (e == cudaSuccess) e = cudaGetLastError();
   if (e != cudaSuccess) return cuda_fail(e, "kv4 join launch");
   return BSA_OK;
@@ -996,7 +982,7 @@ bsa_status launch(const Kv4FwdParams& p, int accumulate, cudaStream_t stream) {
 bool kv4_fwd_fits(const bsa_kv4_fwd_args* a) {
   const Plan x = make_plan(a);
   const int64_t heads = static_cast<int64_t>(a->cache.B) * a->cache.Hkv;
-  return heads * x.row_tiles * x.rows + heads * (a->cache.capacity / kWeightKeys + 1) <= INT32_MAX;
+  return heads * x.row_tiles * kRows + heads * (a->cache.capacity / kWeightKeys + 1) <= INT32_MAX;
 }
 
 size_t kv4_fwd_workspace_bytes(const bsa_kv4_fwd_args* a) {
@@ -1033,12 +1019,16 @@ bsa_status kv4_fwd_launch(const bsa_kv4_fwd_args* a, float scale, cudaStream_t s
   p.rec_o = p.rec_stat + x.stat_bytes / sizeof(float);
   p.scores = a->accumulate ? p.rec_o + x.o_bytes / sizeof(float) : nullptr;
   p.score_stride = x.stride;
-  p.join_rows = a->cache.B * a->cache.Hkv * x.row_tiles * x.rows;
+  // a block a row while these are few (a long pair's records are then read by all of a block), else one a pair:
+  // 4096 rows of 1-2 records take 8 us by the pair and 16 by the row, 32 rows of 57 records 10 us by the row
+  const int64_t pairs = static_cast<int64_t>(a->cache.B) * a->cache.Hkv * x.row_tiles;
+  const int64_t row_blocks = pairs * std::min<int64_t>(p.R, kRows);
+  p.rows_per_block = row_blocks <= 4 * num_sms() ? 1 : kRows;
+  p.join_rows = static_cast<int32_t>(p.rows_per_block == 1 ? row_blocks : pairs);
   p.err = device_error_word();
   p.wait_ns = wait_limit_ns();
   if (!p.err) return fail(BSA_ERR_CUDA, "could not allocate the device error word");
-  if (a->cache.D == 128) return x.NT == 1 ? launch<128, 1>(p, a->accumulate, stream) : launch<128, 2>(p, a->accumulate, stream);
-  return x.NT == 1 ? launch<64, 1>(p, a->accumulate, stream) : launch<64, 2>(p, a->accumulate, stream);
+  return a->cache.D == 128 ? launch<128>(p, a->accumulate, stream) : launch<64>(p, a->accumulate, stream);
 }
 
 }  // namespace bsa
