@@ -50,6 +50,7 @@
 // 605 MB at 4.2 TB/s (eight warps of 16 keys, one of them loading: 200 us).
 // One sequence of 65,536 keys: 27 us and 10, 75 MB; the join's time is latency.
 #include <cmath>
+#include <type_traits>
 
 #include <cuda_fp16.h>
 
@@ -227,6 +228,7 @@ struct __align__(128) FwdShared {
   float merge[kWarps / 2][kRows * kPad];
   float stat[2][kWarps][kRows];
   float lse2[kRows];
+  int32_t lim[kRows];
   uint64_t full[kStages], empty[kStages];
   Run ahead;            // the loader's place in the CTA's run
   int32_t ahead_tile;   // next key tile of that part
@@ -323,7 +325,7 @@ __device__ __forceinline__ float finish_row(const Kv4FwdParams& p, int32_t h, fl
     for (int j = 0; j < p.n_sinks; ++j) m = fmaxf(m, z[j] * kLog2e);
     float tot = lse2 == -INFINITY ? 0.f : ex2_approx(lse2 - m);
     for (int j = 0; j < p.n_sinks; ++j) tot += ex2_approx(fmaf(z[j], kLog2e, -m));
-    const float all = m + log2f(tot);
+    const float all = m == -INFINITY ? -INFINITY : m + log2f(tot);
     if (l != 0.f) factor *= ex2_approx(lse2 - all);
     lse2 = all;
   }
@@ -344,19 +346,37 @@ __device__ __forceinline__ void store_o4(__nv_bfloat16* o, const float4& x, floa
   *reinterpret_cast<uint2*>(o) = make_uint2(pack_bf16x2(x.x * f, x.y * f), pack_bf16x2(x.z * f, x.w * f));
 }
 
-// Sum of the probabilities of key j over the rows of a row tile that see it.
-__device__ __forceinline__ float key_probs(const Kv4FwdParams& p, const Pair& pair, int32_t bh, int32_t rt, int32_t j,
-                                           const float* lse2) {
-  const float* sc = p.scores + ((static_cast<int64_t>(bh) * p.row_tiles + rt) * p.c.capacity + j) * p.score_stride;
-  const int32_t rows = min(kRows, p.R - rt * kRows);
-  float w = 0.f;
-  int32_t t = rt * kRows % p.T;
-  for (int32_t i = 0; i < rows; ++i) {
-    if (t < pair.nq && j < pair.len - pair.nq + t + 1) w += ex2_approx(sc[i] - lse2[i]);
-    if (++t == p.T) t = 0;
-  }
-  return w;
+// Slots that row r of a pair sees: the first `row_limit` ones.
+__device__ __forceinline__ int32_t row_limit(const Kv4FwdParams& p, const Pair& pair, int32_t r) {
+  const int32_t t = r % p.T;
+  return r < p.R && t < pair.nq ? max(0, pair.len - pair.nq + t + 1) : 0;
 }
+
+// The scores of keys j0 + i * step over the rows of a row tile (of pair `head`), and their probabilities, of the rows
+// that see the key, added to w[i].
+template <int N>
+struct KeyScores {
+  float2 v[N][kRows / 2];
+  __device__ __forceinline__ void load(const Kv4FwdParams& p, int64_t head, int32_t j0, int32_t step, int32_t len) {
+#pragma unroll
+    for (int i = 0; i < N; ++i) {
+      const int32_t j = j0 + i * step;
+      const float2* sc = reinterpret_cast<const float2*>(p.scores + (head * p.c.capacity + j) * p.score_stride);
+#pragma unroll
+      for (int r = 0; r < kRows / 2; ++r) v[i][r] = j < len && 2 * r < p.score_stride ? sc[r] : make_float2(0.f, 0.f);
+    }
+  }
+  __device__ __forceinline__ void add(int32_t j0, int32_t step, const float* lse2, const int32_t* lim, float* w) const {
+#pragma unroll
+    for (int r = 0; r < kRows; ++r) {
+      const float l = lse2[r];
+      const int32_t n = lim[r];
+#pragma unroll
+      for (int i = 0; i < N; ++i)
+        if (j0 + i * step < n) w[i] += ex2_approx((r & 1 ? v[i][r / 2].y : v[i][r / 2].x) - l);
+    }
+  }
+};
 
 template <int D, bool kCap>
 __global__ void __launch_bounds__(kThreads, 3) kv4_fwd_kernel(const __grid_constant__ Kv4FwdParams p) {
@@ -516,157 +536,172 @@ __global__ void __launch_bounds__(kThreads, 3) kv4_fwd_kernel(const __grid_const
     uint32_t near_lo = 0;        // bf16 bits from here on, for three binades, are near it
     float down = 1.f, up_back = 1.f;  // 2^-base, 2^base
 
+    // 32 keys; kAll: every row sees all of them
+    auto step = [&](auto all, int key0) __attribute__((always_inline)) {
+      constexpr bool kAll = decltype(all)::value;
+      // ---- scores of both halves
+      float x[2][4];
+#pragma unroll
+      for (int u = 0; u < 2; ++u) {
+        uint32_t ka[kGroups], kb[kGroups], sa[kGroups / 2], sb[kGroups / 2];
+        lds(ka, s.k[st] + k_at + u * 16 * kRowBytes);
+        lds(kb, s.k[st] + k_at + (u * 16 + 8) * kRowBytes);
+        lds(sa, s.ks[st] + s_at + u * 16 * kScaleBytes);
+        lds(sb, s.ks[st] + s_at + (u * 16 + 8) * kScaleBytes);
+#pragma unroll
+        for (int g = 0; g < kGroups; ++g) {
+          const float fa = g & 1 ? bf16_hi(sa[g / 2]) : bf16_lo(sa[g / 2]);
+          const float fb = g & 1 ? bf16_hi(sb[g / 2]) : bf16_lo(sb[g / 2]);
+          const uint32_t a8 = ka[g] >> 8, b8 = kb[g] >> 8;
+          float c[4];
+          mma_f16_from(c, ka[g] & 0x000F000Fu, kb[g] & 0x000F000Fu, ka[g] & 0x00F000F0u, kb[g] & 0x00F000F0u,
+                       qb[g][0], qb[g][1], init[g][0], init[g][1]);
+          mma_f16(c, a8 & 0x000F000Fu, b8 & 0x000F000Fu, a8 & 0x00F000F0u, b8 & 0x00F000F0u, qb[g][2], qb[g][3]);
+          x[u][0] = g ? fmaf(fa, c[0], x[u][0]) : fa * c[0];
+          x[u][1] = g ? fmaf(fa, c[1], x[u][1]) : fa * c[1];
+          x[u][2] = g ? fmaf(fb, c[2], x[u][2]) : fb * c[2];
+          x[u][3] = g ? fmaf(fb, c[3], x[u][3]) : fb * c[3];
+        }
+      }
+      // ---- value scales: are all keys' near the base?
+      uint32_t va[2][kGroups / 2], vb[2][kGroups / 2];
+#pragma unroll
+      for (int u = 0; u < 2; ++u) {
+        lds(va[u], s.vs[st] + s_at + u * 16 * kScaleBytes);
+        lds(vb[u], s.vs[st] + s_at + (u * 16 + 8) * kScaleBytes);
+      }
+      const uint32_t t0 = top_scale(va[0]), t1 = top_scale(vb[0]), t2 = top_scale(va[1]), t3 = top_scale(vb[1]);
+      if (base == INT32_MAX) {
+        // (once a part) the largest finite one of these keys'
+        uint32_t m = 0;
+        const uint32_t tops[4] = {t0, t1, t2, t3};
+#pragma unroll
+        for (int i = 0; i < 4; ++i)
+          if (tops[i] < 0x7F80u && key0 + g8 + 8 * i < run.pair.len) m = max(m, tops[i]);
+#pragma unroll
+        for (int o = 4; o < 32; o *= 2) m = max(m, __shfl_xor_sync(0xffffffffu, m, o));
+        base = min(max(static_cast<int>(m >> 7) - 127, -100), 100);
+        near_lo = static_cast<uint32_t>(base + 126) << 7;
+        down = exp2f(static_cast<float>(-base));
+        up_back = exp2f(static_cast<float>(base));
+      }
+      const bool near = max(max(t0 - near_lo, t1 - near_lo), max(t2 - near_lo, t3 - near_lo)) < (3u << 7);
+      // ---- softmax
+      float pr[2][4];
+#pragma unroll
+      for (int u = 0; u < 2; ++u)
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+          x[u][i] *= qf[i & 1];
+          if constexpr (kCap) x[u][i] = p.cap_log2 * tanh_fast(x[u][i]);
+        }
+      if constexpr (!kAll) {
+#pragma unroll
+        for (int u = 0; u < 2; ++u)
+#pragma unroll
+          for (int i = 0; i < 4; ++i)
+            if (key0 + 16 * u + g8 + (i >> 1) * 8 >= lim[i & 1]) x[u][i] = -INFINITY;
+      }
+      if (p.scores && 2 * t4 < p.score_stride) {
+#pragma unroll
+        for (int u = 0; u < 2; ++u) {
+          if (key0 + 16 * u >= p.c.capacity) continue;
+          float* out = p.scores + (head * p.c.capacity + key0 + 16 * u + g8) * p.score_stride + 2 * t4;
+          *reinterpret_cast<float2*>(out) = make_float2(x[u][0], x[u][1]);
+          *reinterpret_cast<float2*>(out + 8 * p.score_stride) = make_float2(x[u][2], x[u][3]);
+        }
+      }
+      float m[2];
+#pragma unroll
+      for (int i = 0; i < 2; ++i) m[i] = fmaxf(fmaxf(x[0][i], x[0][i + 2]), fmaxf(x[1][i], x[1][i + 2]));
+      if (!__all_sync(0xffffffffu, near)) {
+        const float e[4] = {far_exponent(va[0][0], va[0][kGroups / 2 - 1], base),
+                            far_exponent(vb[0][0], vb[0][kGroups / 2 - 1], base),
+                            far_exponent(va[1][0], va[1][kGroups / 2 - 1], base),
+                            far_exponent(vb[1][0], vb[1][kGroups / 2 - 1], base)};
+#pragma unroll
+        for (int i = 0; i < 2; ++i)
+          m[i] = fmaxf(fmaxf(x[0][i] + e[0], x[0][i + 2] + e[1]), fmaxf(x[1][i] + e[2], x[1][i + 2] + e[3]));
+      }
+#pragma unroll
+      for (int o = 4; o < 32; o *= 2) {
+        m[0] = fmaxf(m[0], __shfl_xor_sync(0xffffffffu, m[0], o));
+        m[1] = fmaxf(m[1], __shfl_xor_sync(0xffffffffu, m[1], o));
+      }
+      if (__any_sync(0xffffffffu, m[0] > R[0] + kRescale || m[1] > R[1] + kRescale)) {
+#pragma unroll
+        for (int i = 0; i < 2; ++i) {
+          // (uniform over the lanes of a column)
+          const float to = m[i] > R[i] + kRescale ? m[i] : R[i];
+          const float f = R[i] == -INFINITY ? 0.f : ex2_approx(R[i] - to);
+          R[i] = to;
+          l[i] *= f;
+#pragma unroll
+          for (int j = 0; j < 2 * kGroups; ++j) {
+            acc[j][i] *= f;
+            acc[j][i + 2] *= f;
+          }
+        }
+      }
+#pragma unroll
+      for (int i = 0; i < 2; ++i) {
+        const float ref = R[i] == -INFINITY ? 0.f : R[i];
+#pragma unroll
+        for (int u = 0; u < 2; ++u) {
+          pr[u][i] = ex2_approx(x[u][i] - ref);
+          pr[u][i + 2] = ex2_approx(x[u][i + 2] - ref);
+        }
+        l[i] += (pr[0][i] + pr[0][i + 2]) + (pr[1][i] + pr[1][i + 2]);
+      }
+#pragma unroll
+      for (int u = 0; u < 2; ++u)
+#pragma unroll
+        for (int i = 0; i < 4; ++i) pr[u][i] *= down;
+      // ---- output, a half at a time
+#pragma unroll
+      for (int u = 0; u < 2; ++u) {
+        uint32_t v0[kGroups / 2], v1[kGroups / 2], v8[kGroups / 2], v9[kGroups / 2];
+        const uint8_t* vrow = s.v[st] + v_at + u * 16 * kRowBytes;
+        lds(v0, vrow);
+        lds(v1, vrow + v_next);
+        lds(v8, vrow + 8 * kRowBytes);
+        lds(v9, vrow + 8 * kRowBytes + v_next);
+#pragma unroll
+        for (int g = 0; g < kGroups; ++g) {
+          // probabilities times value scales, transposed into the second product's operand
+          const float fa = g & 1 ? bf16_hi(va[u][g / 2]) : bf16_lo(va[u][g / 2]);
+          const float fb = g & 1 ? bf16_hi(vb[u][g / 2]) : bf16_lo(vb[u][g / 2]);
+          uint32_t b0, b1;
+          float w[4] = {pr[u][0] * fa, pr[u][1] * fa, pr[u][2] * fb, pr[u][3] * fb};
+          if constexpr (!kAll) {  // (an unseen slot's scale may be anything)
+#pragma unroll
+            for (int i = 0; i < 4; ++i)
+              if (x[u][i] == -INFINITY) w[i] = 0.f;
+          }
+          b0 = transpose8x8(pack_f16x2(w[0], w[1]));
+          b1 = transpose8x8(pack_f16x2(w[2], w[3]));
+          const uint32_t sel = g & 1 ? sel_hi : sel_lo;
+          const uint32_t lo = __byte_perm(v0[g / 2], v1[g / 2], sel), hi = __byte_perm(v8[g / 2], v9[g / 2], sel);
+          // elements 4 g8 + 0..3 of the group: rows g8 and (times 16) g8 + 8 of two products
+          const uint32_t a0 = minus8(lo & 0x000F000Fu, 0x00080008u), a1 = minus8(lo & 0x00F000F0u, 0x00800080u);
+          const uint32_t a2 = minus8(hi & 0x000F000Fu, 0x00080008u), a3 = minus8(hi & 0x00F000F0u, 0x00800080u);
+          const uint32_t lo8 = lo >> 8, hi8 = hi >> 8;
+          const uint32_t c0 = minus8(lo8 & 0x000F000Fu, 0x00080008u), c1 = minus8(lo8 & 0x00F000F0u, 0x00800080u);
+          const uint32_t c2 = minus8(hi8 & 0x000F000Fu, 0x00080008u), c3 = minus8(hi8 & 0x00F000F0u, 0x00800080u);
+          mma_f16(acc[2 * g], a0, a1, a2, a3, b0, b1);
+          mma_f16(acc[2 * g + 1], c0, c1, c2, c3, b0, b1);
+        }
+      }
+    };
+
     for (int32_t kt = run.k0; kt < run.k1; ++kt, ++n) {
       // (after a wait that ran out the loop goes on without waiting, on whatever
       // the stages hold: the barriers between the warps stay matched)
       if (ok) ok = mbar_wait_warp(&s.full[st], parity, wc);
       const int32_t key0 = kt * kTileKeys + warp * 32;
       if (key0 < lim_max) {
-        const bool all_seen = __all_sync(0xffffffffu, key0 + 32 <= lim_min);
-        // ---- scores of both halves
-        float x[2][4];
-#pragma unroll
-        for (int u = 0; u < 2; ++u) {
-          uint32_t ka[kGroups], kb[kGroups], sa[kGroups / 2], sb[kGroups / 2];
-          lds(ka, s.k[st] + k_at + u * 16 * kRowBytes);
-          lds(kb, s.k[st] + k_at + (u * 16 + 8) * kRowBytes);
-          lds(sa, s.ks[st] + s_at + u * 16 * kScaleBytes);
-          lds(sb, s.ks[st] + s_at + (u * 16 + 8) * kScaleBytes);
-#pragma unroll
-          for (int g = 0; g < kGroups; ++g) {
-            const float fa = g & 1 ? bf16_hi(sa[g / 2]) : bf16_lo(sa[g / 2]);
-            const float fb = g & 1 ? bf16_hi(sb[g / 2]) : bf16_lo(sb[g / 2]);
-            const uint32_t a8 = ka[g] >> 8, b8 = kb[g] >> 8;
-            float c[4];
-            mma_f16_from(c, ka[g] & 0x000F000Fu, kb[g] & 0x000F000Fu, ka[g] & 0x00F000F0u, kb[g] & 0x00F000F0u,
-                         qb[g][0], qb[g][1], init[g][0], init[g][1]);
-            mma_f16(c, a8 & 0x000F000Fu, b8 & 0x000F000Fu, a8 & 0x00F000F0u, b8 & 0x00F000F0u, qb[g][2], qb[g][3]);
-            x[u][0] = g ? fmaf(fa, c[0], x[u][0]) : fa * c[0];
-            x[u][1] = g ? fmaf(fa, c[1], x[u][1]) : fa * c[1];
-            x[u][2] = g ? fmaf(fb, c[2], x[u][2]) : fb * c[2];
-            x[u][3] = g ? fmaf(fb, c[3], x[u][3]) : fb * c[3];
-          }
-        }
-        // ---- value scales: are all keys' near the base?
-        uint32_t va[2][kGroups / 2], vb[2][kGroups / 2];
-#pragma unroll
-        for (int u = 0; u < 2; ++u) {
-          lds(va[u], s.vs[st] + s_at + u * 16 * kScaleBytes);
-          lds(vb[u], s.vs[st] + s_at + (u * 16 + 8) * kScaleBytes);
-        }
-        const uint32_t t0 = top_scale(va[0]), t1 = top_scale(vb[0]), t2 = top_scale(va[1]), t3 = top_scale(vb[1]);
-        if (base == INT32_MAX) {
-          // (once a part) the largest finite one of these keys'
-          uint32_t m = 0;
-          const uint32_t tops[4] = {t0, t1, t2, t3};
-#pragma unroll
-          for (int i = 0; i < 4; ++i)
-            if (tops[i] < 0x7F80u && key0 + g8 + 8 * i < run.pair.len) m = max(m, tops[i]);
-#pragma unroll
-          for (int o = 4; o < 32; o *= 2) m = max(m, __shfl_xor_sync(0xffffffffu, m, o));
-          base = min(max(static_cast<int>(m >> 7) - 127, -100), 100);
-          near_lo = static_cast<uint32_t>(base + 126) << 7;
-          down = exp2f(static_cast<float>(-base));
-          up_back = exp2f(static_cast<float>(base));
-        }
-        const bool near = max(max(t0 - near_lo, t1 - near_lo), max(t2 - near_lo, t3 - near_lo)) < (3u << 7);
-        float e[4] = {0.f, 0.f, 0.f, 0.f};
-        if (!__all_sync(0xffffffffu, near)) {
-          e[0] = far_exponent(va[0][0], va[0][kGroups / 2 - 1], base);
-          e[1] = far_exponent(vb[0][0], vb[0][kGroups / 2 - 1], base);
-          e[2] = far_exponent(va[1][0], va[1][kGroups / 2 - 1], base);
-          e[3] = far_exponent(vb[1][0], vb[1][kGroups / 2 - 1], base);
-        }
-        // ---- softmax
-        float pr[2][4];
-#pragma unroll
-        for (int u = 0; u < 2; ++u)
-#pragma unroll
-          for (int i = 0; i < 4; ++i) {
-            x[u][i] *= qf[i & 1];
-            if constexpr (kCap) x[u][i] = p.cap_log2 * tanh_fast(x[u][i]);
-          }
-        if (!all_seen) {
-#pragma unroll
-          for (int u = 0; u < 2; ++u)
-#pragma unroll
-            for (int i = 0; i < 4; ++i)
-              if (key0 + 16 * u + g8 + (i >> 1) * 8 >= lim[i & 1]) x[u][i] = -INFINITY;
-        }
-        if (p.scores && 2 * t4 < p.score_stride) {
-#pragma unroll
-          for (int u = 0; u < 2; ++u) {
-            if (key0 + 16 * u >= p.c.capacity) continue;
-            float* out = p.scores + (head * p.c.capacity + key0 + 16 * u + g8) * p.score_stride + 2 * t4;
-            *reinterpret_cast<float2*>(out) = make_float2(x[u][0], x[u][1]);
-            *reinterpret_cast<float2*>(out + 8 * p.score_stride) = make_float2(x[u][2], x[u][3]);
-          }
-        }
-#pragma unroll
-        for (int i = 0; i < 2; ++i) {
-          float m = fmaxf(fmaxf(x[0][i] + e[0], x[0][i + 2] + e[1]), fmaxf(x[1][i] + e[2], x[1][i + 2] + e[3]));
-#pragma unroll
-          for (int o = 4; o < 32; o *= 2) m = fmaxf(m, __shfl_xor_sync(0xffffffffu, m, o));
-          const bool move = m > R[i] + kRescale;
-          if (__any_sync(0xffffffffu, move)) {
-            // (uniform over the lanes of a column)
-            const float to = move ? m : R[i];
-            const float f = R[i] == -INFINITY ? 0.f : ex2_approx(R[i] - to);
-            R[i] = to;
-            l[i] *= f;
-#pragma unroll
-            for (int j = 0; j < 2 * kGroups; ++j) {
-              acc[j][i] *= f;
-              acc[j][i + 2] *= f;
-            }
-          }
-          const float ref = R[i] == -INFINITY ? 0.f : R[i];
-#pragma unroll
-          for (int u = 0; u < 2; ++u) {
-            pr[u][i] = ex2_approx(x[u][i] - ref);
-            pr[u][i + 2] = ex2_approx(x[u][i + 2] - ref);
-          }
-          l[i] += (pr[0][i] + pr[0][i + 2]) + (pr[1][i] + pr[1][i + 2]);
-        }
-#pragma unroll
-        for (int u = 0; u < 2; ++u)
-#pragma unroll
-          for (int i = 0; i < 4; ++i) pr[u][i] *= down;
-        // ---- output, a half at a time
-#pragma unroll
-        for (int u = 0; u < 2; ++u) {
-          uint32_t v0[kGroups / 2], v1[kGroups / 2], v8[kGroups / 2], v9[kGroups / 2];
-          const uint8_t* vrow = s.v[st] + v_at + u * 16 * kRowBytes;
-          lds(v0, vrow);
-          lds(v1, vrow + v_next);
-          lds(v8, vrow + 8 * kRowBytes);
-          lds(v9, vrow + 8 * kRowBytes + v_next);
-#pragma unroll
-          for (int g = 0; g < kGroups; ++g) {
-            // probabilities times value scales, transposed into the second product's operand
-            const float fa = g & 1 ? bf16_hi(va[u][g / 2]) : bf16_lo(va[u][g / 2]);
-            const float fb = g & 1 ? bf16_hi(vb[u][g / 2]) : bf16_lo(vb[u][g / 2]);
-            uint32_t b0, b1;
-            float w[4] = {pr[u][0] * fa, pr[u][1] * fa, pr[u][2] * fb, pr[u][3] * fb};
-            if (!all_seen) {  // (an unseen slot's scale may be anything)
-#pragma unroll
-              for (int i = 0; i < 4; ++i)
-                if (x[u][i] == -INFINITY) w[i] = 0.f;
-            }
-            b0 = transpose8x8(pack_f16x2(w[0], w[1]));
-            b1 = transpose8x8(pack_f16x2(w[2], w[3]));
-            const uint32_t sel = g & 1 ? sel_hi : sel_lo;
-            const uint32_t lo = __byte_perm(v0[g / 2], v1[g / 2], sel), hi = __byte_perm(v8[g / 2], v9[g / 2], sel);
-            // elements 4 g8 + 0..3 of the group: rows g8 and (times 16) g8 + 8 of two products
-            const uint32_t a0 = minus8(lo & 0x000F000Fu, 0x00080008u), a1 = minus8(lo & 0x00F000F0u, 0x00800080u);
-            const uint32_t a2 = minus8(hi & 0x000F000Fu, 0x00080008u), a3 = minus8(hi & 0x00F000F0u, 0x00800080u);
-            const uint32_t lo8 = lo >> 8, hi8 = hi >> 8;
-            const uint32_t c0 = minus8(lo8 & 0x000F000Fu, 0x00080008u), c1 = minus8(lo8 & 0x00F000F0u, 0x00800080u);
-            const uint32_t c2 = minus8(hi8 & 0x000F000Fu, 0x00080008u), c3 = minus8(hi8 & 0x00F000F0u, 0x00800080u);
-            mma_f16(acc[2 * g], a0, a1, a2, a3, b0, b1);
-            mma_f16(acc[2 * g + 1], c0, c1, c2, c3, b0, b1);
-          }
-        }
+        if (__all_sync(0xffffffffu, key0 + 32 <= lim_min)) step(std::true_type{}, key0);
+        else step(std::false_type{}, key0);
       }
       // (at the end: the stage it goes to, the last tile's, is long released; before this warp's own release, which
       // hands the loader's place on to the next warp)
@@ -765,9 +800,15 @@ __global__ void __launch_bounds__(kThreads, 3) kv4_fwd_kernel(const __grid_const
     first_part = false;
     if (p.whole && p.scores) {
       // (one row tile) this CTA's own scores into probabilities
+      if (threadIdx.x < kRows) s.lim[threadIdx.x] = row_limit(p, run.pair, static_cast<int32_t>(threadIdx.x));
       __syncthreads();
-      for (int32_t j = threadIdx.x; j < run.pair.len; j += kThreads)
-        p.c.weights[static_cast<int64_t>(run.bh) * p.c.capacity + j] += key_probs(p, run.pair, run.bh, 0, j, s.lse2);
+      for (int32_t j = threadIdx.x; j < run.pair.len; j += kThreads) {
+        float w[1] = {};
+        KeyScores<1> x;
+        x.load(p, run.bh, j, 0, run.pair.len);
+        x.add(j, 0, s.lse2, s.lim, w);
+        p.c.weights[static_cast<int64_t>(run.bh) * p.c.capacity + j] += w[0];
+      }
     }
     __syncthreads();  // the next part, maybe of few tiles, writes `stat` and `merge` again
   }
@@ -910,6 +951,7 @@ __global__ void __launch_bounds__(kJoinThreads) kv4_join_kernel(const __grid_con
   const int32_t j0 = static_cast<int32_t>(blk % chunks) * kWeightKeys;
   const Pair pair = load_pair(p, bh / p.c.Hkv, nullptr);
   if (j0 >= pair.len || pair.nq == 0) return;
+  __shared__ int32_t lim[kRows];
   float w[kWeightKeys / kJoinThreads] = {};
   for (int32_t rt = 0; rt < p.row_tiles; ++rt) {
     const Records x = pair_records(p, bh, rt, pair);
@@ -921,12 +963,15 @@ __global__ void __launch_bounds__(kJoinThreads) kv4_join_kernel(const __grid_con
       if (r < p.R) v = x.c0 != x.c1 ? finish_row(p, bh % p.c.Hkv, R[threadIdx.x], L[threadIdx.x], f)
                                     : p.lse[lse_index(p, bh, r)] * kLog2e;
       R[threadIdx.x] = v;
+      lim[threadIdx.x] = row_limit(p, pair, r);
     }
     __syncthreads();
 #pragma unroll
-    for (int i = 0; i < kWeightKeys / kJoinThreads; ++i) {
+    for (int i = 0; i < kWeightKeys / kJoinThreads; i += 2) {  // two at a time: registers, and with them blocks an SM
       const int32_t j = j0 + i * kJoinThreads + static_cast<int32_t>(threadIdx.x);
-      if (j < pair.len) w[i] += key_probs(p, pair, bh, rt, j, R);
+      KeyScores<2> y;
+      y.load(p, static_cast<int64_t>(bh) * p.row_tiles + rt, j, kJoinThreads, pair.len);
+      y.add(j, kJoinThreads, R, lim, w + i);
     }
     __syncthreads();
   }
@@ -1023,7 +1068,7 @@ bsa_status kv4_fwd_launch(const bsa_kv4_fwd_args* a, float scale, cudaStream_t s
   // 4096 rows of 1-2 records take 8 us by the pair and 16 by the row, 32 rows of 57 records 10 us by the row
   const int64_t pairs = static_cast<int64_t>(a->cache.B) * a->cache.Hkv * x.row_tiles;
   const int64_t row_blocks = pairs * std::min<int64_t>(p.R, kRows);
-  p.rows_per_block = row_blocks <= 4 * num_sms() ? 1 : kRows;
+  p.rows_per_block = p.n_cta >= 8 * pairs ? 1 : kRows;
   p.join_rows = static_cast<int32_t>(p.rows_per_block == 1 ? row_blocks : pairs);
   p.err = device_error_word();
   p.wait_ns = wait_limit_ns();
