@@ -33,8 +33,11 @@
 // a head (16 sequences, one head of 8192 keys), where the second pass comes out
 // of the second-level cache.
 //
-// Work: all (sequence, head, row tile) pairs' key tiles of 128 form one
-// sequence, cut into equal runs, one per CTA; lengths are read on the device.
+// Work: all (sequence, head, row tile) pairs' key tiles of 128, and 3 more
+// units for each pair, form one sequence, cut into equal runs, one per CTA;
+// lengths are read on the device.  (A part costs a CTA about as much as 3 tiles,
+// q's way in and the warps' sums: 16 sequences of unequal lengths, 75,000 keys
+// on 8 heads, take 34 us with these units, 51 without.)
 // A run's parts of pairs that other CTAs share go to the workspace as (R, l,
 // O) records; a second kernel joins them in a fixed order and, if asked,
 // turns the stored scores into probabilities and adds them to the weights.
@@ -44,11 +47,12 @@
 //
 // Four warps take 32 keys of a tile each, as two products side by side; the
 // warps take turns in bringing tiles in by bulk copies through a ring of
-// stages.  What bounds it is the issue of instructions, about 370 per 16 keys
-// and warp, most of them the AND, subtract and pack around the products.
-// 64 sequences of 8191 keys on 8 heads, 32 q heads: 145 us and 8 for the join,
-// 605 MB at 4.2 TB/s (eight warps of 16 keys, one of them loading: 200 us).
-// One sequence of 65,536 keys: 27 us and 10, 75 MB; the join's time is latency.
+// stages.  What bounds it is the issue of instructions, most of them the ANDs,
+// subtractions and packs around the products; the step therefore exists twice, and
+// the copy for keys that every row sees has no predicates (145 to 134 us below).
+// 64 sequences of 8191 keys on 8 heads, 32 q heads: 133 us and 8 for the join,
+// 605 MB at 4.5 TB/s (eight warps of 16 keys, one of them loading: 200 us).
+// One sequence of 65,536 keys: 26 us and 10, 75 MB; the join's time is latency.
 #include <cmath>
 #include <type_traits>
 
@@ -65,6 +69,7 @@ constexpr int kTileKeys = 128;
 constexpr int kRows = 8;                   // rows of a row tile
 constexpr int kWarps = 4;                  // 32 keys of a tile each, as two halves of 16
 constexpr int kWholeTiles = 8;             // longest pair, in tiles, that one CTA takes alone
+constexpr int kPartUnits = 3;              // cost of a part beside its tiles', in tiles
 constexpr int kThreads = 32 * kWarps;
 constexpr int kWeightKeys = 1024;          // keys of one head whose weights a CTA of the join adds to
 constexpr float kRescale = 8.0f;
@@ -101,7 +106,8 @@ struct Kv4FwdParams {
 // One (sequence, head, row tile) pair's place in the sequence of tiles.
 struct Pair {
   int32_t b, len, nq;  // keys held; new tokens
-  int32_t tiles;       // key tiles of each of the sequence's Hkv * row_tiles pairs
+  int32_t tiles;       // key tiles of each of the sequence's Hkv * row_tiles pairs ...
+  int32_t units;       // ... and their cost: kPartUnits and one per tile, or 0
 };
 
 __device__ __forceinline__ Pair load_pair(const Kv4FwdParams& p, int32_t b, uint32_t* err) {
@@ -110,16 +116,17 @@ __device__ __forceinline__ Pair load_pair(const Kv4FwdParams& p, int32_t b, uint
   x.len = clamp_len(p.lens[b], p.c.capacity, err);
   x.nq = p.q_lens ? min(max(p.q_lens[b], 0), p.T) : p.T;
   x.tiles = x.nq > 0 ? (x.len + kTileKeys - 1) / kTileKeys : 0;
+  x.units = x.tiles > 0 ? x.tiles + kPartUnits : 0;
   return x;
 }
 
-// Tiles of all sequences, and of the first ones up to b; every lane of the calling warp gets both.
-__device__ __forceinline__ int64_t total_tiles(const Kv4FwdParams& p, int32_t b, int64_t* before) {
+// Units of all sequences, and of the first ones up to b; every lane of the calling warp gets both.
+__device__ __forceinline__ int64_t total_units(const Kv4FwdParams& p, int32_t b, int64_t* before) {
   const int lane = threadIdx.x & 31;
   const int64_t per = static_cast<int64_t>(p.c.Hkv) * p.row_tiles;
   int64_t sum = 0, head = 0;
   for (int32_t i = lane; i < p.c.B; i += 32) {
-    const int64_t n = load_pair(p, i, nullptr).tiles * per;
+    const int64_t n = load_pair(p, i, nullptr).units * per;
     sum += n;
     if (i < b) head += n;
   }
@@ -132,28 +139,29 @@ __device__ __forceinline__ int64_t total_tiles(const Kv4FwdParams& p, int32_t b,
   return sum;
 }
 
-// CTAs that have work (none gets an empty run).  Of n, CTA c has tiles
-// [c * total / n, (c + 1) * total / n); cta_of is the one that has tile t.
+// CTAs that get a run of units (which may be short of a tile).  Of n, CTA c has
+// units [c * total / n, (c + 1) * total / n); cta_of is the one that has unit t.
+// A pair's first kPartUnits units are no tiles.
 __device__ __forceinline__ int32_t runs(const Kv4FwdParams& p, int64_t total) {
   return static_cast<int32_t>(min(static_cast<int64_t>(p.n_cta), total));
 }
 __device__ __forceinline__ int64_t quotient(int64_t a, int64_t b) {  // of non-negative numbers, mostly small ones
   return ((a | b) >> 32) == 0 ? static_cast<int64_t>(static_cast<uint32_t>(a) / static_cast<uint32_t>(b)) : a / b;
 }
-__device__ __forceinline__ int64_t first_tile(int64_t c, int64_t total, int32_t n) { return quotient(c * total, n); }
+__device__ __forceinline__ int64_t first_unit(int64_t c, int64_t total, int32_t n) { return quotient(c * total, n); }
 __device__ __forceinline__ int32_t cta_of(int64_t t, int64_t total, int32_t n) {
   return static_cast<int32_t>(quotient((t + 1) * n - 1, total));
 }
 
 // Cursor over a CTA's run: parts of pairs, each a range of key tiles.
 struct Run {
-  int64_t at, end;     // tiles of the run still to go
-  int64_t seq0;        // first tile of sequence pair.b
+  int64_t at, end;     // units of the run still to go
+  int64_t seq0;        // first unit of sequence pair.b
   Pair pair;
   int32_t bh, rt;      // b * Hkv + h; row tile
   int32_t k0, k1;      // the part's key tiles
   bool whole;          // the part is the whole pair
-  // places the cursor before tile `first` (warp-collective)
+  // places the cursor before unit `first` (warp-collective)
   __device__ __forceinline__ void init(const Kv4FwdParams& p, int64_t first, int64_t last, uint32_t* err) {
     at = first;
     end = last;
@@ -163,7 +171,7 @@ struct Run {
     int32_t b = 0;
     if (at < end) {
       for (int32_t b0 = 0;; b0 += 32) {
-        const int64_t n = b0 + lane < p.c.B ? load_pair(p, b0 + lane, err).tiles * per : 0;
+        const int64_t n = b0 + lane < p.c.B ? load_pair(p, b0 + lane, err).units * per : 0;
         int64_t inc = n;
 #pragma unroll
         for (int o = 1; o < 32; o *= 2) {
@@ -198,20 +206,24 @@ struct Run {
       whole = true;
       return true;
     }
-    if (at >= end) return false;
     const int64_t per = static_cast<int64_t>(p.c.Hkv) * p.row_tiles;
-    while (at >= seq0 + pair.tiles * per) {
-      seq0 += pair.tiles * per;
-      pair = load_pair(p, pair.b + 1, nullptr);
-    }
-    const int64_t i = at - seq0;
-    const int32_t hr = static_cast<int32_t>(i / pair.tiles);
-    bh = pair.b * p.c.Hkv + hr / p.row_tiles;
-    rt = hr % p.row_tiles;
-    k0 = static_cast<int32_t>(i % pair.tiles);
-    k1 = static_cast<int32_t>(min(static_cast<int64_t>(pair.tiles), k0 + (end - at)));
+    do {
+      if (at >= end) return false;
+      while (at >= seq0 + pair.units * per) {
+        seq0 += pair.units * per;
+        pair = load_pair(p, pair.b + 1, nullptr);
+      }
+      const int64_t i = at - seq0;
+      const int32_t hr = static_cast<int32_t>(quotient(i, pair.units));
+      bh = pair.b * p.c.Hkv + hr / p.row_tiles;
+      rt = hr % p.row_tiles;
+      const int32_t u0 = static_cast<int32_t>(i - static_cast<int64_t>(hr) * pair.units);
+      const int32_t u1 = static_cast<int32_t>(min(static_cast<int64_t>(pair.units), u0 + (end - at)));
+      at += u1 - u0;
+      k0 = max(u0 - kPartUnits, 0);
+      k1 = max(u1 - kPartUnits, 0);
+    } while (k0 >= k1);
     whole = k0 == 0 && k1 == pair.tiles;
-    at += k1 - k0;
     return true;
   }
 };
@@ -405,10 +417,10 @@ __global__ void __launch_bounds__(kThreads, 3) kv4_fwd_kernel(const __grid_const
     run.init_whole(p, blockIdx.x, threadIdx.x == 0 ? p.err : nullptr);
   } else {
     int64_t none;
-    const int64_t total = total_tiles(p, 0, &none);
+    const int64_t total = total_units(p, 0, &none);
     const int32_t n_cta = runs(p, total);
     if (static_cast<int32_t>(blockIdx.x) >= n_cta) return;
-    run.init(p, first_tile(blockIdx.x, total, n_cta), first_tile(blockIdx.x + 1, total, n_cta), warp == 0 ? p.err : nullptr);
+    run.init(p, first_unit(blockIdx.x, total, n_cta), first_unit(blockIdx.x + 1, total, n_cta), warp == 0 ? p.err : nullptr);
   }
 
   // One lane: tile `n` of the run into its stage, if there is one; true if that went well.
@@ -832,14 +844,14 @@ struct Records {
 __device__ __forceinline__ Records pair_records(const Kv4FwdParams& p, int32_t bh, int32_t rt, const Pair& pair) {
   const int32_t b = bh / p.c.Hkv, h = bh % p.c.Hkv;
   int64_t before;
-  const int64_t total = total_tiles(p, b, &before);
+  const int64_t total = total_units(p, b, &before);
   Records x{0, 0, 0, pair.tiles};
   if (pair.tiles > 0) {
     const int32_t n = runs(p, total);
-    const int64_t begin = before + (static_cast<int64_t>(h) * p.row_tiles + rt) * pair.tiles;
-    x.c0 = cta_of(begin, total, n);
-    x.c1 = cta_of(begin + pair.tiles - 1, total, n);
-    x.first = 2 * x.c0 + (first_tile(x.c0, total, n) < begin ? 1 : 0);
+    const int64_t begin = before + (static_cast<int64_t>(h) * p.row_tiles + rt) * pair.units;
+    x.c0 = cta_of(begin + kPartUnits, total, n);
+    x.c1 = cta_of(begin + pair.units - 1, total, n);
+    x.first = 2 * x.c0 + (first_unit(x.c0, total, n) < begin ? 1 : 0);
   }
   return x;
 }
@@ -1064,11 +1076,11 @@ bsa_status kv4_fwd_launch(const bsa_kv4_fwd_args* a, float scale, cudaStream_t s
   p.rec_o = p.rec_stat + x.stat_bytes / sizeof(float);
   p.scores = a->accumulate ? p.rec_o + x.o_bytes / sizeof(float) : nullptr;
   p.score_stride = x.stride;
-  // a block a row while these are few (a long pair's records are then read by all of a block), else one a pair:
-  // 4096 rows of 1-2 records take 8 us by the pair and 16 by the row, 32 rows of 57 records 10 us by the row
+  // a block a row where a pair has many records (they are then read by all of a block), else one a pair: 4096 rows
+  // of 1-2 records take 16 us by the row and 8 by the pair, 512 rows of 7 records 8 and 12
   const int64_t pairs = static_cast<int64_t>(a->cache.B) * a->cache.Hkv * x.row_tiles;
   const int64_t row_blocks = pairs * std::min<int64_t>(p.R, kRows);
-  p.rows_per_block = p.n_cta >= 8 * pairs ? 1 : kRows;
+  p.rows_per_block = p.n_cta >= 4 * pairs ? 1 : kRows;
   p.join_rows = static_cast<int32_t>(p.rows_per_block == 1 ? row_blocks : pairs);
   p.err = device_error_word();
   p.wait_ns = wait_limit_ns();
