@@ -20,8 +20,8 @@
 // to lose bits); a probability times its value scale is rounded to fp16.
 //
 // p s is kept in fp16's range however the scales differ.  A warp takes the
-// exponent of its first keys' largest value scale as a base, and p s 2^-base
-// is what is rounded; a key whose largest scale is not within a factor of two
+// exponent of its first keys' largest value scale as a base (the first that are
+// not all 0), and p (s 2^-base) is what is rounded; a key whose largest scale is not within a factor of two
 // of the base enters the running reference as R = max(s_j + e_j), e_j its
 // exponent less the base (0 for the others, so that hardly any key pays for
 // it).  l = sum 2^(s_j - R) stays in fp32.  R moves only when it grows by more
@@ -285,6 +285,13 @@ __device__ __forceinline__ uint32_t minus8(uint32_t x, uint32_t c) {
   return y;
 }
 
+// Two bf16 numbers times a power of two (exact).
+__device__ __forceinline__ uint32_t mul_bf16x2(uint32_t x, uint32_t y) {
+  uint32_t z;
+  asm("mul.rn.bf16x2 %0, %1, %2;" : "=r"(z) : "r"(x), "r"(y));
+  return z;
+}
+
 template <int N>
 __device__ __forceinline__ void lds(uint32_t (&w)[N], const void* p) {
   if constexpr (N == 4) {
@@ -312,14 +319,16 @@ __device__ __forceinline__ uint32_t top_scale(const uint32_t (&w)[W]) {
 }
 
 // A key's exponent against the base: 0 within a factor of two of it, else the
-// exponent of its largest finite scale (a key without one counts as the
-// smallest) less the base, kept within +-100.
+// exponent of its largest finite scale less the base, kept within +-100.
+// A key of no values (no finite scale but 0) has -80: however large its
+// probability, it must not press the others' products out of fp16.
 __device__ __noinline__ float far_exponent(uint32_t w0, uint32_t w1, int base) {
   const uint32_t w[4] = {w0 & 0xFFFFu, w0 >> 16, w1 & 0xFFFFu, w1 >> 16};
   uint32_t m = 0;
 #pragma unroll
   for (int i = 0; i < 4; ++i)
     if (w[i] < 0x7F80u) m = max(m, w[i]);
+  if (m == 0) return -80.f;
   const int e = min(max(static_cast<int>(m >> 7) - 127 - base, -100), 100);
   return e >= -1 && e <= 1 ? 0.f : static_cast<float>(e);
 }
@@ -545,8 +554,9 @@ __global__ void __launch_bounds__(kThreads, 3) kv4_fwd_kernel(const __grid_const
     R[0] = R[1] = -INFINITY;
     l[0] = l[1] = 0.f;
     int base = INT32_MAX;        // base exponent of the value scales (uniform over the warp; not yet chosen)
-    uint32_t near_lo = 0;        // bf16 bits from here on, for three binades, are near it
-    float down = 1.f, up_back = 1.f;  // 2^-base, 2^base
+    uint32_t near_lo = 1u << 7;  // bf16 bits from here on, for three binades, are near it (0 is not)
+    uint32_t down = 0x3F803F80u;  // 2^-base, twice in bf16
+    float up_back = 1.f;          // 2^base
 
     // 32 keys; kAll: every row sees all of them
     auto step = [&](auto all, int key0) __attribute__((always_inline)) {
@@ -584,7 +594,7 @@ __global__ void __launch_bounds__(kThreads, 3) kv4_fwd_kernel(const __grid_const
       }
       const uint32_t t0 = top_scale(va[0]), t1 = top_scale(vb[0]), t2 = top_scale(va[1]), t3 = top_scale(vb[1]);
       if (base == INT32_MAX) {
-        // (once a part) the largest finite one of these keys'
+        // (until there is one) the largest finite one of these keys'; sums of values that are all 0 have no scale yet
         uint32_t m = 0;
         const uint32_t tops[4] = {t0, t1, t2, t3};
 #pragma unroll
@@ -592,10 +602,12 @@ __global__ void __launch_bounds__(kThreads, 3) kv4_fwd_kernel(const __grid_const
           if (tops[i] < 0x7F80u && key0 + g8 + 8 * i < run.pair.len) m = max(m, tops[i]);
 #pragma unroll
         for (int o = 4; o < 32; o *= 2) m = max(m, __shfl_xor_sync(0xffffffffu, m, o));
-        base = min(max(static_cast<int>(m >> 7) - 127, -100), 100);
-        near_lo = static_cast<uint32_t>(base + 126) << 7;
-        down = exp2f(static_cast<float>(-base));
-        up_back = exp2f(static_cast<float>(base));
+        if (m > 0) {
+          base = min(max(static_cast<int>(m >> 7) - 127, -126), 120);  // (2^-base is a bf16 number)
+          near_lo = static_cast<uint32_t>(base + 126) << 7;
+          down = static_cast<uint32_t>(127 - base) * 0x00800080u;
+          up_back = exp2f(static_cast<float>(base));
+        }
       }
       const bool near = max(max(t0 - near_lo, t1 - near_lo), max(t2 - near_lo, t3 - near_lo)) < (3u << 7);
       // ---- softmax
@@ -668,7 +680,10 @@ __global__ void __launch_bounds__(kThreads, 3) kv4_fwd_kernel(const __grid_const
 #pragma unroll
       for (int u = 0; u < 2; ++u)
 #pragma unroll
-        for (int i = 0; i < 4; ++i) pr[u][i] *= down;
+        for (int i = 0; i < kGroups / 2; ++i) {
+          va[u][i] = mul_bf16x2(va[u][i], down);
+          vb[u][i] = mul_bf16x2(vb[u][i], down);
+        }
       // ---- output, a half at a time
 #pragma unroll
       for (int u = 0; u < 2; ++u) {
