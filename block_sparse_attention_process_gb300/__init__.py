@@ -383,6 +383,7 @@ _workspace_sizes: dict = {}
 
 
 def _workspace_size(entry: str, key, args: bytes) -> int:
+    key = (entry, key)
     need = _workspace_sizes.get(key)
     if need is None:
         n = C.c_size_t(0)
@@ -544,9 +545,8 @@ def kv4_evict(cache: KV4Cache, lens: torch.Tensor, keep: int, *, recent: int = 0
     B, H, D = cache.B, cache.Hkv, cache.D
     caches, pack = cache._c + dst._c, _abi.KV4_EVICT_REST.pack
     head = (_lens("lens", lens, B, index), _lens("seen", seen, B, index), keep, recent)
-    n = C.c_size_t(0)
-    L = _abi.lib()
-    check(L.bsa_kv4_evict_workspace(caches + pack(*head, 0, 0, 0, 0, 0, 0), C.byref(n)), "bsa_kv4_evict")
+    need = _workspace_size("bsa_kv4_evict", (index, B, H, D, cache.capacity, dst.capacity, keep, recent, caches[:8] == dst._c[:8]),
+                           caches + pack(*head, 0, 0, 0, 0, 0, 0))
     ctx, handle = _place(dev, index, stream)
     with ctx:
         new_lens = torch.empty((B,), dtype=torch.int32, device=dev)
@@ -555,10 +555,10 @@ def kv4_evict(cache: KV4Cache, lens: torch.Tensor, keep: int, *, recent: int = 0
         if values:
             kv = torch.empty((B, H, keep, D), dtype=torch.bfloat16, device=dev)
             vv = torch.empty_like(kv)
-        ws = _workspace(n.value, dev)
-        check(L.bsa_kv4_evict(caches + pack(*head, new_lens.data_ptr(), slots.data_ptr(), kv.data_ptr() if values else 0,
-                                            vv.data_ptr() if values else 0, 0 if ws is None else ws.data_ptr(), n.value),
-                              handle), "bsa_kv4_evict")
+        ws = _workspace(need, dev)
+        check(_abi.lib().bsa_kv4_evict(
+            caches + pack(*head, new_lens.data_ptr(), slots.data_ptr(), kv.data_ptr() if values else 0,
+                          vv.data_ptr() if values else 0, 0 if ws is None else ws.data_ptr(), need), handle), "bsa_kv4_evict")
     return (new_lens, slots, kv, vv) if values else (new_lens, slots)
 
 

@@ -322,8 +322,11 @@ BSA_API bsa_status bsa_bwd_noalloc(const bsa_bwd_args* args, const bsa_mask_info
  * program runs a prompt through bsa_fwd, appends its keys and values (with
  * the weights of bsa_key_weights) and then, token by token, appends and
  * attends, evicting when the cache reaches its budget.  All of these calls
- * are asynchronous, allocate nothing (workspaces come from the caller), read
- * every length from device memory and can be captured into a CUDA graph.
+ * are asynchronous, allocate nothing (workspaces come from the caller; only
+ * the first library call on a device allocates the error word, so one call
+ * comes before a capture), read every length from device memory and can be
+ * captured into a CUDA graph.  A workspace belongs to one call at a time: two
+ * calls, or two captured graphs, that may overlap need one each.
  * ------------------------------------------------------------------------- */
 
 typedef struct {
@@ -421,7 +424,9 @@ typedef struct {
  * get O = 0 and LSE = -inf (the log-sum of the sinks where there are any).  A
  * length outside 0..capacity counts as the nearer end and sets the bounds bit
  * of the device error word.  Slots at or past lens[b] are never used,
- * whatever they hold. */
+ * whatever they hold.  Products of a probability and a value scale are held in
+ * fp16 beside a power of two chosen per run of keys; the non-zero
+ * scales of the values of one sequence and head may lie up to 2^80 apart. */
 BSA_API bsa_status bsa_kv4_fwd(const bsa_kv4_fwd_args* args, bsa_stream stream);
 BSA_API bsa_status bsa_kv4_fwd_workspace(const bsa_kv4_fwd_args* args, size_t* bytes);
 
