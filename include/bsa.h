@@ -340,7 +340,7 @@ typedef struct {
   size_t workspace_bytes;
   int32_t B, Hq, Hkv, D;
   int64_t S_q, S_kv;
-  float softmax_scale;     /* NaN selects 1/sqrt(D) */
+  float softmax_scale;     /* NaN selects 1/sqrt(D); at least 2^-60 in magnitude without a soft cap */
   float logits_soft_cap;   /* as in bsa_fwd_args */
 } bsa_key_weights_args;
 
@@ -389,7 +389,8 @@ typedef struct {
   const int32_t* n_new;              /* device int32 [B], or NULL (= T): tokens at or past n_new[b] are padding */
   const int32_t* first_position;     /* device int32 [B], or NULL (= start): position of token 0 */
   const float* weights0;             /* device fp32 [B, Hkv, T], or NULL (= 0): initial accumulated weights */
-  void* k_values;                    /* bf16 [B, Hkv, T, D] or NULL: what the cache now holds (0 for padding) */
+  void* k_values;                    /* bf16 [B, Hkv, T, D] or NULL: what the cache now holds (0 for padding; a token
+                                        outside the cache as if stored) */
   void* v_values;
 } bsa_kv4_append_args;
 

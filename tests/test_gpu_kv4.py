@@ -483,6 +483,34 @@ def test_key_weights_of_fwd_sum_to_the_number_of_queries():
     assert np.abs(total / (Hq // Hkv * S) - 1).max() < 2e-4
 
 
+@pytest.mark.parametrize("D,cap", [(64, 0), (128, 0), (128, 10.0)])
+def test_key_weights_keep_nan_and_infinities_where_they_are(D, cap):
+    """Padded queries of NaN change nothing; a NaN query reaches the keys it sees, an infinite key itself alone."""
+    bsa = bsa_()
+    S, n = 384, 300
+    q, k = rows((1, 4, S, D), 97).cuda(), rows((1, 2, S, D), 98).cuda()
+    info, dkv = bsa.mask_compile("causal", S, S), bsa.mask_compile("causal", S, S, orientation="dkv")
+    _, lse = bsa.fwd(q, k, k, info, logits_soft_cap=cap or None)
+    weights = lambda q, k, lse: bsa.key_weights(q, k, lse, dkv, q_lens=i32([n]), logits_soft_cap=cap or None)
+    clean = weights(q, k, lse)
+    assert torch.isfinite(clean).all() and (clean[:, :, n:] == 0).all()
+    q, lse = q.clone(), lse.clone()
+    q[:, :, n:] = float("nan")
+    lse[:, :, n:] = float("nan")
+    lse[:, :, -1] = float("inf")
+    assert torch.equal(weights(q, k, lse), clean)
+    q[0, 1, 131] = float("nan")             # (of the first key head's group)
+    lse[0, 1, 131] = float("nan")
+    got = weights(q, k, lse)
+    assert torch.isnan(got[0, 0, :132]).all() and torch.equal(got[0, 0, 132:], clean[0, 0, 132:]) and torch.equal(got[0, 1], clean[0, 1])
+    k = k.clone()
+    k[0, 1, 70, 3] = float("inf")
+    got = weights(q, k, lse)
+    keep = torch.arange(S, device="cuda") != 70
+    assert not torch.equal(got[0, 1], clean[0, 1]) and torch.equal(got[0, 1, keep], clean[0, 1, keep])
+    assert bsa.get_device_error() == 0
+
+
 # ------------------------------------------------------------------ together
 
 def test_prompt_append_decode_evict_together():
