@@ -1,10 +1,10 @@
 // Quantisation of new keys and values into the 4-bit cache.
 //
 // Per group of 32 elements: s = bf16(max|x| / 7), c = rint(x / s) + 8.  The
-// quotient is taken as x (1/s), off by at most 2^-22: x has 8 significant bits
-// and s/2 times an odd number at most 12, so a quotient that is not itself a
-// tie is at least 2^-15 (relative) away from one and rounds right; a tie shows
-// as a remainder of exactly s/2 and is put to the even side.
+// quotient is x (1/s) and one correction: x has 8 significant bits and s/2 times
+// an odd number at most 12, so a quotient that is not itself a tie is at least
+// 2^-15 (relative) away from one and rounds right, and a tie, a number of few
+// bits, comes out exactly.
 //
 // HBM-bound: 4 D bytes read and D + D/4 of codes and scales (+ 4 D of values)
 // written per token and head.  A row takes D/8 lanes: for K each lane holds
@@ -49,11 +49,8 @@ __device__ __forceinline__ float rcp_approx(float x) {  // off by 2^-23 at most
   return y;
 }
 
-// Largest magnitude as bf16 bits (NaN above infinity above every number).
-__device__ __forceinline__ uint32_t max_bits(uint32_t m, uint32_t w) {
-  m = max(m, w & 0x7FFFu);
-  return max(m, (w >> 16) & 0x7FFFu);
-}
+// Largest magnitudes of the two halves as bf16 bits (NaN above infinity above every number).
+__device__ __forceinline__ uint32_t max_bits(uint32_t m, uint32_t w) { return __vmaxu2(m, w & 0x7FFF7FFFu); }
 
 // The group's scale (bf16 bits) from its largest magnitude.
 __device__ __forceinline__ uint32_t scale_bits(uint32_t m) {
@@ -63,13 +60,12 @@ __device__ __forceinline__ uint32_t scale_bits(uint32_t m) {
   return static_cast<uint32_t>(__bfloat16_as_ushort(s));
 }
 
-// q = rint(x / s), |q| <= 7.
-__device__ __forceinline__ float quantise(float x, float s, float inv, float half) {
-  constexpr float kMagic = 12582912.f;  // 1.5 2^23: the sum's last bits are the rounded integer
-  const float u = fmaf(x, inv, kMagic);
-  const float q = u - kMagic;
-  const float rest = fmaf(-q, s, x);  // exact
-  return fabsf(rest) == half && (__float_as_uint(u) & 1u) ? q + copysignf(1.f, rest) : q;
+// q = rint(x / s), |q| <= 7.  One step of Newton's method: a quotient that is a
+// tie comes out exactly, any other is at least 2^-15 (relative) away from one.
+__device__ __forceinline__ float quantise(float x, float s, float inv) {
+  constexpr float kMagic = 12582912.f;  // 1.5 2^23: the sum is rounded to a whole number, ties to even
+  const float q = x * inv;
+  return fmaf(fmaf(-q, s, x), inv, q) + kMagic - kMagic;
 }
 // The same by a true division, for scales that are 0, NaN or so small that
 // their reciprocal might overflow.
@@ -82,10 +78,9 @@ __device__ __forceinline__ float quantise_slow(float x, float s) {
 // they stand for replace the elements.
 template <bool kSlow>
 __device__ __forceinline__ uint32_t quantise4(uint32_t& w0, uint32_t& w1, float s, float inv) {
-  const float half = 0.5f * s;
   float x[4] = {bf16_lo(w0), bf16_hi(w0), bf16_lo(w1), bf16_hi(w1)}, q[4];
 #pragma unroll
-  for (int i = 0; i < 4; ++i) q[i] = kSlow ? quantise_slow(x[i], s) : quantise(x[i], s, inv, half);
+  for (int i = 0; i < 4; ++i) q[i] = kSlow ? quantise_slow(x[i], s) : quantise(x[i], s, inv);
   w0 = pack_bf16x2(q[0] * s, q[1] * s);
   w1 = pack_bf16x2(q[2] * s, q[3] * s);
   // the four codes as one whole number, exact in fp32, in the last bits of a sum with 2^23
@@ -130,8 +125,10 @@ __global__ void __launch_bounds__(256) append_kernel(const __grid_constant__ App
       vb = __ldcs(reinterpret_cast<const uint2*>(vr + d1));
     }
     // a K group is 4 neighbouring lanes, a V group every kPiece-th lane of the row
-    uint32_t mk = max_bits(max_bits(max_bits(max_bits(0, kw.x), kw.y), kw.z), kw.w);
-    uint32_t mv = max_bits(max_bits(0, va.x), va.y) | max_bits(max_bits(0, vb.x), vb.y) << 16;  // (15 bits each)
+    const uint32_t m2 = max_bits(max_bits(max_bits(kw.x & 0x7FFF7FFFu, kw.y), kw.z), kw.w);
+    const uint32_t ma = max_bits(va.x & 0x7FFF7FFFu, va.y), mb = max_bits(vb.x & 0x7FFF7FFFu, vb.y);
+    uint32_t mk = max(m2 & 0xFFFFu, m2 >> 16);
+    uint32_t mv = __vmaxu2(__byte_perm(ma, mb, 0x5410), __byte_perm(ma, mb, 0x7632));
 #pragma unroll
     for (int o = 1; o < 4; o *= 2) mk = max(mk, __shfl_xor_sync(0xffffffffu, mk, o));
 #pragma unroll

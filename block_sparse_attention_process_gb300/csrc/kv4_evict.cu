@@ -266,8 +266,20 @@ __global__ void __launch_bounds__(kSelThreads) select_kernel(const __grid_consta
   cluster_barrier();  // (no CTA leaves while another reads its counts)
 }
 
-__device__ __forceinline__ float code_value(uint32_t w, int i, float s) {
-  return static_cast<float>(static_cast<int>((w >> (4 * i)) & 15u) - 8) * s;
+// What the nibbles at bits 0-3 and 16-19 of x stand for, as bf16: 128 + c is
+// exact in bf16, so is (128 + c) - 136, and the product is rounded once.
+__device__ __forceinline__ uint32_t code_values(uint32_t x, uint32_t scale2) {
+  uint32_t y, z;
+  asm("sub.rn.bf16x2 %0, %1, %2;" : "=r"(y) : "r"((x & 0x000F000Fu) | 0x43004300u), "r"(0x43084308u));
+  asm("mul.rn.bf16x2 %0, %1, %2;" : "=r"(z) : "r"(y), "r"(scale2));
+  return z;
+}
+// The eight elements of a word in order, under the scales (bf16 bits) of its
+// low and high four.
+__device__ __forceinline__ uint4 word_values(uint32_t w, uint32_t s_lo, uint32_t s_hi) {
+  const uint32_t s = __byte_perm(s_lo, s_hi, 0x5410);  // nibbles i and i + 4 go together
+  const uint32_t a = code_values(w, s), b = code_values(w >> 4, s), c = code_values(w >> 8, s), d = code_values(w >> 12, s);
+  return make_uint4(__byte_perm(a, b, 0x5410), __byte_perm(c, d, 0x5410), __byte_perm(a, b, 0x7632), __byte_perm(c, d, 0x7632));
 }
 
 constexpr int kMoves = 2;  // rows of one head that a lane has in flight
@@ -314,23 +326,11 @@ __global__ void __launch_bounds__(256) move_kernel(const __grid_constant__ Evict
           if (u == 1 && p.o.positions) p.o.positions[to] = p.c.positions ? p.c.positions[from] : src[i];
         }
         const int64_t row = (bh * p.keep + r) * D;
-        if (p.k_values) {
-          const float s = __uint_as_float(ks[i] << 16);
-          uint4 o;
-          o.x = pack_bf16x2(code_value(kw[i], 0, s), code_value(kw[i], 1, s));
-          o.y = pack_bf16x2(code_value(kw[i], 2, s), code_value(kw[i], 3, s));
-          o.z = pack_bf16x2(code_value(kw[i], 4, s), code_value(kw[i], 5, s));
-          o.w = pack_bf16x2(code_value(kw[i], 6, s), code_value(kw[i], 7, s));
-          __stcs(reinterpret_cast<uint4*>(p.k_values + row + k_word_elem<D>(u)), o);
-        }
+        if (p.k_values) __stcs(reinterpret_cast<uint4*>(p.k_values + row + k_word_elem<D>(u)), word_values(kw[i], ks[i], ks[i]));
         if (p.v_values) {
-          const float a = bf16_lo(vs[i]), b = bf16_hi(vs[i]);
-          __stcs(reinterpret_cast<uint2*>(p.v_values + row + v_word_elem<D>(u, 0)),
-                 make_uint2(pack_bf16x2(code_value(vw[i], 0, a), code_value(vw[i], 1, a)),
-                            pack_bf16x2(code_value(vw[i], 2, a), code_value(vw[i], 3, a))));
-          __stcs(reinterpret_cast<uint2*>(p.v_values + row + v_word_elem<D>(u, 1)),
-                 make_uint2(pack_bf16x2(code_value(vw[i], 4, b), code_value(vw[i], 5, b)),
-                            pack_bf16x2(code_value(vw[i], 6, b), code_value(vw[i], 7, b))));
+          const uint4 o = word_values(vw[i], vs[i] & 0xFFFFu, vs[i] >> 16);
+          __stcs(reinterpret_cast<uint2*>(p.v_values + row + v_word_elem<D>(u, 0)), make_uint2(o.x, o.y));
+          __stcs(reinterpret_cast<uint2*>(p.v_values + row + v_word_elem<D>(u, 1)), make_uint2(o.z, o.w));
         }
       }
     }
