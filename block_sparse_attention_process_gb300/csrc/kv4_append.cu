@@ -10,9 +10,10 @@
 // written per token and head.  A row takes D/8 lanes: for K each lane holds
 // 8 consecutive elements, which are one 4-byte word of codes; for V its two
 // quads of elements 32 apart, likewise one word.  4 x 8 x 8192 rows of 128 with
-// their values take 71 us, 64% of the copy bandwidth; the rest is issue slots:
-// with a true division per element 98 us, with two rows a lane in flight 74
-// (fewer warps fit), with four 84.
+// their values take 63 us, 72% of the copy bandwidth; the rest is issue slots:
+// 98 us with a true division per element, 72 with ties found by their remainder
+// and maxima one element at a time.  One row a lane: two in flight measured
+// slower (fewer warps fit).
 #include "internal.h"
 #include "kv4.cuh"
 #include "ptx.cuh"
