@@ -136,9 +136,7 @@ bsa_status check_key_weights(const bsa_key_weights_args* a, const bsa_mask_info*
     return fail(BSA_ERR_UNSUPPORTED, "B*H*S must fit in int32");
   bsa_status s = check_cap(a->logits_soft_cap);
   if (s != BSA_OK) return s;
-  // (a logsumexp enters the scores' product divided by the scale)
-  if (a->logits_soft_cap == 0.f && !(std::fabs(resolve_scale(a->softmax_scale, a->D)) >= 0x1p-60f))
-    return fail(BSA_ERR_UNSUPPORTED, "without a soft cap, softmax_scale must be at least 2^-60 in magnitude");
+  if (a->S_q / kBlock > 65536) return fail(BSA_ERR_UNSUPPORTED, "more than 65536 query blocks are not supported");  // (16 bits of an item)
   if (!info) return bad("dkv MaskInfo is null");
   return BSA_OK;
 }

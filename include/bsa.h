@@ -339,8 +339,8 @@ typedef struct {
   void* workspace;         /* device, 16-byte aligned, bsa_key_weights_workspace bytes */
   size_t workspace_bytes;
   int32_t B, Hq, Hkv, D;
-  int64_t S_q, S_kv;
-  float softmax_scale;     /* NaN selects 1/sqrt(D); at least 2^-60 in magnitude without a soft cap */
+  int64_t S_q, S_kv;       /* S_q up to 2^23 */
+  float softmax_scale;     /* NaN selects 1/sqrt(D) */
   float logits_soft_cap;   /* as in bsa_fwd_args */
 } bsa_key_weights_args;
 

@@ -511,6 +511,23 @@ def test_key_weights_keep_nan_and_infinities_where_they_are(D, cap):
     assert bsa.get_device_error() == 0
 
 
+@pytest.mark.parametrize("scale", [0.0, 1e-30, -0.0, -0.07, 3.0])
+def test_key_weights_of_any_scale(scale):
+    bsa = bsa_()
+    S, D = 256, 64
+    q, k = rows((1, 2, S, D), 99), rows((1, 1, S, D), 100)
+    s = np.where(np.tril(np.ones((S, S), bool)), scale * np.einsum("hid,jd->hij", q.double().numpy()[0], k.double().numpy()[0, 0]), -np.inf)
+    lse = np.log(np.exp(s - s.max(-1, keepdims=True)).sum(-1)) + s.max(-1)
+    l32 = lse.astype(np.float32)
+    want = np.exp(s - l32[..., None].astype(np.float64)).sum((0, 1))
+    dkv = bsa.mask_compile("causal", S, S, orientation="dkv")
+    got = bsa.key_weights(q.cuda(), k.cuda(), torch.from_numpy(l32[None]).cuda(), dkv, softmax_scale=scale)
+    assert bsa.get_device_error() == 0
+    amax = abs(scale) * np.einsum("hid,jd->hij", np.abs(q.double().numpy()[0]), np.abs(k.double().numpy()[0, 0])).max()
+    ds = 2.0 ** -16 * amax + 2.0 ** -23 * max(1.0, np.abs(lse).max())
+    within("key weights", host(got)[0, 0], want, want * (2 * ds + 2.0 ** -18) + 1e-30)
+
+
 # ------------------------------------------------------------------ together
 
 def test_prompt_append_decode_evict_together():

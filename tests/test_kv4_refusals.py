@@ -147,7 +147,7 @@ def test_evict_in_place_needs_positions_and_the_whole_cache():
 @pytest.mark.parametrize("kw,status", [
     ({"B": 0}, "INVALID_ARG"), ({"Hq": 3}, "INVALID_ARG"), ({"S_q": 200}, "INVALID_ARG"), ({"S_kv": 0}, "INVALID_ARG"),
     ({"D": 96}, "UNSUPPORTED"), ({"logits_soft_cap": math.nan}, "INVALID_ARG"), ({"q": None}, "INVALID_ARG"),
-    ({"softmax_scale": 0.0}, "UNSUPPORTED"), ({"softmax_scale": -1e-30}, "UNSUPPORTED"),
+    ({"Hq": 2, "Hkv": 1, "S_q": (1 << 23) + 128}, "UNSUPPORTED"),
     ({"lse": 8}, "INVALID_ARG"), ({"q_lens": 2}, "INVALID_ARG"), ({"weights": None}, "INVALID_ARG"),
     ({"S_q": 1 << 30}, "UNSUPPORTED"),
 ])
