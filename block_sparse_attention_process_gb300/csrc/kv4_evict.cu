@@ -2,15 +2,17 @@
 //
 // Per (sequence, key head): the `keep` slots of the largest key, key = the
 // weight as an ordered 32-bit integer (recent tokens above everything, NaN
-// above every number), ties to the lower slot.  A radix select of four 8-bit
-// digits finds the smallest kept key; every kept slot's place then follows
+// above every number), ties to the lower slot.  A radix select of three digits
+// (11, 11 and 10 bits) finds the smallest kept key; every kept slot's place then follows
 // from prefix counts, and a second kernel moves the rows.
 //
 // The selection reads 8 bytes a slot once and is otherwise latency: a cluster
 // of up to 8 CTAs shares a head, each with its slice's keys in shared memory,
 // and adds up its histograms through distributed shared memory.  One CTA a
 // head that read the weights again for every digit took 193 us for 8 heads of
-// 65,536 slots and 25 us for 128 heads of 1088; this takes 26 and 14 us.  The
+// 65,536 slots and 25 us for 128 heads of 1088; this takes 24 and 12 us
+// (four digits of 8 bits: 26 and 14; the wider first one also spreads the
+// atomics, as most weights share their exponent's top bits).  The
 // move reads and writes D + D / 8 bytes a kept slot (and writes 4 D of values,
 // if asked): 128 heads that keep 1024 of 1088 slots of 128 with their values,
 // 106 MB, 22 us.
@@ -24,6 +26,7 @@ namespace {
 constexpr int kSelThreads = 1024;
 constexpr int kCachedKeys = 40 * 1024;  // keys of a slice kept in shared memory (160 KiB); a longer slice reads them again
 constexpr int kMaxCluster = 8;
+constexpr int kBins = 2048;  // of a digit (64 to each of 32 coarse ones)
 
 struct EvictParams {
   bsa_kv4_cache c, o;
@@ -56,11 +59,12 @@ __device__ __forceinline__ uint32_t cluster_rank() {
 __device__ __forceinline__ void cluster_barrier() {
   asm volatile("barrier.cluster.arrive.release;\n\tbarrier.cluster.wait.acquire;" ::: "memory");
 }
-// A word of another CTA's shared memory.
-__device__ __forceinline__ uint32_t load_remote(const uint32_t* mine, uint32_t rank) {
-  uint32_t a, v;
-  asm volatile("mapa.shared::cluster.u32 %0, %1, %2;" : "=r"(a) : "r"(smem_u32(mine)), "r"(rank));
-  asm volatile("ld.shared::cluster.u32 %0, [%1];" : "=r"(v) : "r"(a) : "memory");
+// Two words of another CTA's shared memory.
+__device__ __forceinline__ uint2 load_remote(const uint32_t* mine, uint32_t rank) {
+  uint32_t a;
+  uint2 v;
+  asm("mapa.shared::cluster.u32 %0, %1, %2;" : "=r"(a) : "r"(smem_u32(mine)), "r"(rank));
+  asm volatile("ld.shared::cluster.v2.u32 {%0, %1}, [%2];" : "=r"(v.x), "=r"(v.y) : "r"(a) : "memory");
   return v;
 }
 
@@ -99,10 +103,10 @@ __device__ __forceinline__ void block_prefix(int32_t& a, int32_t& b, int32_t (*s
 // One head per cluster; CTA r takes the r-th slice of its slots.
 __global__ void __launch_bounds__(kSelThreads) select_kernel(const __grid_constant__ EvictParams p) {
   extern __shared__ uint32_t keys[];  // the slice's, if it is short enough
-  __shared__ uint32_t hist[2][256];   // (two: a CTA may still read one while the next digit's is counted)
-  __shared__ uint32_t totals[256];
+  __shared__ __align__(8) uint32_t hist[2][kBins];  // (two: a CTA may still read one while the next digit's is counted)
+  __shared__ __align__(8) uint32_t coarse[2][32];   // sums of kBins / 32 neighbouring bins
   __shared__ uint32_t pick[2];
-  __shared__ uint32_t counts[3];      // slots of the slice above the least kept key, at it, and stays below slot keep
+  __shared__ __align__(8) uint32_t counts[4];  // slots of the slice above the least kept key, at it, and stays below slot keep
   __shared__ int32_t sums[kSelThreads / 32][2];
   griddep_launch_dependents();
   griddep_wait();
@@ -139,10 +143,11 @@ __global__ void __launch_bounds__(kSelThreads) select_kernel(const __grid_consta
 
   uint32_t prefix = 0, mask = 0;
   uint32_t want = static_cast<uint32_t>(p.keep);  // rank (1-based, from the top) among keys with this prefix
-  for (int d = 0; d < 4; ++d) {
-    const int shift = 24 - 8 * d;
+  for (int d = 0; d < 3; ++d) {  // digits of 11, 11 and 10 bits
+    const int shift = d == 0 ? 21 : d == 1 ? 10 : 0;
+    const uint32_t digits = d == 2 ? 1023u : 2047u;
     uint32_t* h = hist[d & 1];
-    if (threadIdx.x < 256) h[threadIdx.x] = 0;
+    for (int i = static_cast<int>(threadIdx.x); i < kBins; i += kSelThreads) h[i] = 0;
     __syncthreads();
     // (whole warps go round together, and count at once where all their slots have one digit, as weights of 0 do;
     // gathering all equal digits of a warp instead took 2 us more for 8 heads of 65,536 slots)
@@ -152,7 +157,7 @@ __global__ void __launch_bounds__(kSelThreads) select_kernel(const __grid_consta
       const uint32_t k = i < s1 ? key_of(i) : 0u;
       const bool in = i < s1 && (k & mask) == prefix;
       if (!__any_sync(0xffffffffu, in)) continue;
-      const uint32_t digit = in ? (k >> shift) & 255u : 256u;
+      const uint32_t digit = in ? (k >> shift) & digits : kBins;
       int one;  // the whole warp has one digit
       (void)__match_all_sync(0xffffffffu, digit, &one);
       if (one) {
@@ -161,46 +166,64 @@ __global__ void __launch_bounds__(kSelThreads) select_kernel(const __grid_consta
         atomicAdd(&h[digit], 1u);
       }
     }
-    cluster_barrier();
-    if (threadIdx.x < 256) {
-      uint32_t v = 0;
-#pragma unroll
-      for (uint32_t c = 0; c < kMaxCluster; ++c)
-        if (c < C) v += load_remote(&h[threadIdx.x], c);
-      totals[threadIdx.x] = v;
-    }
     __syncthreads();
+    {
+      const uint32_t w = threadIdx.x / 32, l = threadIdx.x % 32;
+      uint32_t v = h[w * (kBins / 32) + l] + h[w * (kBins / 32) + 32 + l];
+      v = __reduce_add_sync(0xffffffffu, v);
+      if (l == 0) coarse[d & 1][w] = v;
+    }
+    if (C > 1) cluster_barrier();
+    else __syncthreads();
     if (threadIdx.x < 32) {
-      // eight digits a lane, from the top: where does the count reach `want`?
-      uint32_t mine[8], total = 0;
+      // from the top: the coarse bin in which the count reaches `want`, then the bin within it
+      const uint32_t lane = threadIdx.x;
+      // two neighbouring counts of all CTAs (loads without branches between them: all on their way at once)
+      auto totals = [&](const uint32_t* at) -> uint2 {
+        if (C == 1) return *reinterpret_cast<const uint2*>(at);
+        uint2 x[kMaxCluster];
 #pragma unroll
-      for (int i = 0; i < 8; ++i) {
-        mine[i] = totals[255u - (threadIdx.x * 8 + i)];
-        total += mine[i];
-      }
-      uint32_t before = total;
+        for (uint32_t c = 0; c < kMaxCluster; ++c) x[c] = load_remote(at, min(c, C - 1));
+        uint2 v = make_uint2(0u, 0u);
 #pragma unroll
-      for (int o = 1; o < 32; o *= 2) {
-        const uint32_t x = __shfl_up_sync(0xffffffffu, before, o);
-        if (threadIdx.x >= static_cast<uint32_t>(o)) before += x;
-      }
-      before -= total;
-      bool found = before < want && before + total >= want;
+        for (uint32_t c = 0; c < kMaxCluster; ++c)
+          if (c < C) {
+            v.x += x[c].x;
+            v.y += x[c].y;
+          }
+        return v;
+      };
+      uint32_t left = want;  // (the same in every lane)
+      auto reach = [&](uint32_t n) -> uint32_t {  // the lane whose n, added to those before it, reaches `left`
+        uint32_t upto = n;
 #pragma unroll
-      for (int i = 0; i < 8; ++i) {
-        if (found && before + mine[i] >= want) {
-          pick[0] = 255u - (threadIdx.x * 8 + i);
-          pick[1] = want - before;
-          found = false;
+        for (int o = 1; o < 32; o *= 2) {
+          const uint32_t x = __shfl_up_sync(0xffffffffu, upto, o);
+          if (lane >= static_cast<uint32_t>(o)) upto += x;
         }
-        before += mine[i];
+        const uint32_t at = static_cast<uint32_t>(__ffs(__ballot_sync(0xffffffffu, upto >= left))) - 1u;
+        left -= __shfl_sync(0xffffffffu, upto - n, at);
+        return at;
+      };
+      const uint2 both = totals(&coarse[d & 1][(31u - lane) & ~1u]);
+      const uint32_t top = 31u - reach(lane & 1 ? both.x : both.y);
+      const uint32_t* bins = h + top * (kBins / 32);
+      const uint2 two = totals(bins + 62u - 2u * lane);  // two neighbours a lane
+      const uint32_t hi = two.y, lo = two.x;
+      const uint32_t pair = reach(hi + lo);
+      const uint32_t first = __shfl_sync(0xffffffffu, hi, pair);
+      const bool second = left > first;
+      if (second) left -= first;
+      if (lane == 0) {
+        pick[0] = top * (kBins / 32) + 63u - 2u * pair - (second ? 1u : 0u);
+        pick[1] = left;
       }
     }
     __syncthreads();
     prefix |= pick[0] << shift;
-    mask |= 255u << shift;
+    mask |= digits << shift;
     want = pick[1];
-    __syncthreads();
+    // (pick is written again only behind the next digit's barriers)
   }
   // `want` slots whose key is `prefix` stay, the lowest ones, and all above it
 
@@ -220,10 +243,18 @@ __global__ void __launch_bounds__(kSelThreads) select_kernel(const __grid_consta
     counts[2] = 0;
   }
   cluster_barrier();
-  for (uint32_t c = 0; c < cta; ++c) {
-    above += static_cast<int32_t>(load_remote(&counts[0], c));
-    ties += static_cast<int32_t>(load_remote(&counts[1], c));
+  if (threadIdx.x < 32) {  // the CTAs before this one, a lane each
+    const uint2 x = threadIdx.x < C ? load_remote(counts, threadIdx.x) : make_uint2(0u, 0u);
+    const uint32_t a = __reduce_add_sync(0xffffffffu, threadIdx.x < cta ? x.x : 0u);
+    const uint32_t t = __reduce_add_sync(0xffffffffu, threadIdx.x < cta ? x.y : 0u);
+    if (threadIdx.x == 0) {
+      pick[0] = a;
+      pick[1] = t;
+    }
   }
+  __syncthreads();
+  above += static_cast<int32_t>(pick[0]);
+  ties += static_cast<int32_t>(pick[1]);
   const int32_t quota = static_cast<int32_t>(want);
   // stays before slot i: those above the least key, and ties up to the quota
   if (!p.in_place) {
@@ -251,8 +282,12 @@ __global__ void __launch_bounds__(kSelThreads) select_kernel(const __grid_consta
     t += k == prefix;
   }
   cluster_barrier();  // the holes are written (and n > keep: slot keep has been met)
-  uint32_t below = 0;
-  for (uint32_t c = 0; c < C; ++c) below += load_remote(&counts[2], c);
+  if (threadIdx.x < 32) {
+    const uint32_t n = __reduce_add_sync(0xffffffffu, threadIdx.x < C ? load_remote(counts + 2, threadIdx.x).x : 0u);
+    if (threadIdx.x == 0) pick[0] = n;
+  }
+  __syncthreads();
+  const uint32_t below = pick[0];
   a = above;
   t = ties;
   for (int32_t i = t0; i < t1; ++i) {
