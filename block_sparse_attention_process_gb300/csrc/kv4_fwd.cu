@@ -320,17 +320,23 @@ __device__ __forceinline__ uint32_t top_scale(const uint32_t (&w)[W]) {
   return max(m & 0xFFFFu, m >> 16);
 }
 
-// A key's exponent against the base: 0 within a factor of two of it, else the
-// exponent of its largest finite scale less the base, kept within +-100.
-// A key of no values (no finite scale but 0) has -80: however large its
-// probability, it must not press the others' products out of fp16.
-__device__ __noinline__ float far_exponent(uint32_t w0, uint32_t w1, int base) {
+// The same of the finite scales alone (a group of NaN or infinities has no size), of a row's first and last word.
+__device__ __forceinline__ uint32_t top_finite(uint32_t w0, uint32_t w1) {
   const uint32_t w[4] = {w0 & 0xFFFFu, w0 >> 16, w1 & 0xFFFFu, w1 >> 16};
   uint32_t m = 0;
 #pragma unroll
   for (int i = 0; i < 4; ++i)
     if (w[i] < 0x7F80u) m = max(m, w[i]);
-  if (m == 0) return -80.f;
+  return m;
+}
+
+// A key's exponent against the base: 0 within a factor of two of it, else the
+// exponent of its largest finite scale less the base, kept within +-100.
+// A key of no values (no finite scale but 0) has -80: however large its
+// probability, it must not press the others' products out of fp16.
+__device__ __noinline__ float far_exponent(uint32_t w0, uint32_t w1, int base) {
+  const uint32_t m = top_finite(w0, w1);
+  if (m == 0 || base == INT32_MAX) return -80.f;  // (without a base no key of the step has values)
   const int e = min(max(static_cast<int>(m >> 7) - 127 - base, -100), 100);
   return e >= -1 && e <= 1 ? 0.f : static_cast<float>(e);
 }
@@ -598,10 +604,11 @@ __global__ void __launch_bounds__(kThreads, ctas_per_sm(D)) kv4_fwd_kernel(const
       if (base == INT32_MAX) {
         // (until there is one) the largest finite one of these keys'; sums of values that are all 0 have no scale yet
         uint32_t m = 0;
-        const uint32_t tops[4] = {t0, t1, t2, t3};
 #pragma unroll
-        for (int i = 0; i < 4; ++i)
-          if (tops[i] < 0x7F80u && key0 + g8 + 8 * i < run.pair.len) m = max(m, tops[i]);
+        for (int i = 0; i < 4; ++i) {
+          const uint32_t(&w)[kGroups / 2] = i & 1 ? vb[i / 2] : va[i / 2];
+          if (key0 + g8 + 8 * i < run.pair.len) m = max(m, top_finite(w[0], w[kGroups / 2 - 1]));
+        }
 #pragma unroll
         for (int o = 4; o < 32; o *= 2) m = max(m, __shfl_xor_sync(0xffffffffu, m, o));
         if (m > 0) {

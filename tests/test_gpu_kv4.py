@@ -796,3 +796,40 @@ def test_range_checked_build_runs_the_cache_and_the_key_weights_clean():
                         "bit_exact or matches_oracle or match_oracle or unequal or together or (is_exact and random)"],
                        env=dict(os.environ, BSA_LIBRARY_VARIANT="debug"), capture_output=True, text=True, timeout=900, cwd=ROOT)
     assert r.returncode == 0 and "passed" in r.stdout, r.stdout[-3000:] + r.stderr[-3000:]
+
+
+# ------------------------------------------------------------------ groups of a value row, each for itself
+
+def check_groups(o, lse, q, kv, vv, lens, bad=(), **kw):
+    """Every 32 channels against the oracle, with a tolerance of their own values' size: beside the rounding of the
+    result, 2^-11 of the sum of p |v| for a product held in fp16 and as much again for the products below 2^-14 of
+    the group's largest (2^-25 of that each, over 2^13 keys or fewer), and what the scores' errors make of p.
+    `bad`: groups that are NaN."""
+    D = q.shape[-1]
+    got = host(o)
+    for g in range(D // 32):
+        part = slice(32 * g, 32 * g + 32)
+        if g in bad:
+            assert np.isnan(got[..., part]).all()
+            continue
+        only = np.zeros_like(vv)
+        only[..., part] = vv[..., part]
+        wo, wl, _, apv, aqk = kv4.forward(q.double().numpy(), kv, only, lens, **kw)
+        ds = 2.0 ** -16 * aqk
+        within(f"o, group {g}", got[..., part], wo[..., part], 2.0 ** -8 * np.abs(wo[..., part]) + (2.0 ** -10 + 2 * ds[..., None]) * apv)
+    within("lse", host(lse), wl, ds + 2.0 ** -20 * np.maximum(1, np.abs(wl)))
+
+
+@pytest.mark.parametrize("size", [2.0 ** -5, 2.0 ** 5])
+@pytest.mark.parametrize("n,cap", [(1, 16), (33, 48), (65, 1024), (97, 112), (1, 2064), (33, 2064), (2049, 2064)])
+@pytest.mark.parametrize("D", [64, 128])
+def test_fwd_nan_group_of_the_only_key_of_a_warp(D, n, cap, size):
+    """The last key, alone among the keys that a warp starts with, has one group of NaN: the others keep their values."""
+    bsa = bsa_()
+    k, v, q = rows((1, 1, cap, D), 150), rows((1, 1, cap, D), 151, size), rows((1, 2, 1, D), 152)
+    v[0, 0, n - 1, 40] = float("nan")
+    cache, kv, vv = filled(bsa, 1, 1, cap, D, 153, k=k, v=v)
+    vv[0, 0, n - 1, 32:64] = 0
+    o, lse = bsa.kv4_fwd(q.cuda(), cache, i32([n]))
+    assert bsa.get_device_error() == 0
+    check_groups(o, lse, q, kv, vv, [n], bad=(1,))
