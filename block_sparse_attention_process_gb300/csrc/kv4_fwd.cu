@@ -19,13 +19,19 @@
 // row's largest magnitude to [2^14, 2^15); elements 2^-24 times smaller start
 // to lose bits); a probability times its value scale is rounded to fp16.
 //
-// p s is kept in fp16's range however the scales differ.  A warp takes the
-// exponent of its first keys' largest value scale as a base (the first that are
-// not all 0), and p (s 2^-base) is what is rounded; a key whose largest scale is not within a factor of two
-// of the base enters the running reference as R = max(s_j + e_j), e_j its
-// exponent less the base (0 for the others, so that hardly any key pays for
-// it).  l = sum 2^(s_j - R) stays in fp32.  R moves only when it grows by more
-// than 8 (log2 units).
+// p s in fp16: 11 bits, where the outputs have 8; more would take two of every second
+// product.  Every group of 32 channels has a base of its own, the exponent of the
+// largest scale among a warp's first keys, and raised by it its scales are good while they
+// lie in [2^-7, 2), 2^-5 to 2^3 of the base's own.  A row's reference R lies 2^10 below the
+// largest score among keys whose scales are all good, and moves when that grows by more than 4 (log2
+// units); l = sum 2^(s_j - R) stays in fp32.  So the largest product of every group is in [2^3, 2^15) and the
+// products below 2^-14, which lose up to 2^-25 each, together lose less than 2^-11 of the
+// sum over up to 2^17 keys of a warp.
+// Other keys (of values 0, NaN, or much smaller or larger) take part in the same products
+// but do not move R, unless a score of theirs is 2^24 above it: then, or where a
+// product would leave fp16, or where a group of zeros gets its first values late, a step
+// (from then on every step of the part, if R had to follow such a key) sorts its
+// products into classes of 28 binades, a matrix product each, added up in fp32.
 //
 // Row tiles are of 8, the product's own width.  Tiles of 16 (two products on
 // the same codes) halve the passes over the cache when a head has 9 or more
@@ -47,12 +53,14 @@
 //
 // Four warps take 32 keys of a tile each, as two products side by side; the
 // warps take turns in bringing tiles in by bulk copies through a ring of
-// stages.  What bounds it is the issue of instructions, most of them the ANDs,
-// subtractions and packs around the products; the step therefore exists twice, and
-// the copy for keys that every row sees has no predicates (145 to 134 us below).
-// 64 sequences of 8191 keys on 8 heads, 32 q heads: 133 us and 8 for the join,
-// 605 MB at 4.5 TB/s (eight warps of 16 keys, one of them loading: 200 us).
-// One sequence of 65,536 keys: 26 us and 10, 75 MB; the join's time is latency.
+// stages.  Most of its instructions are the ANDs, subtractions and packs around
+// the products; the step therefore exists three times, for keys that every row sees (without predicates:
+// 145 to 134 us below), for others, and class by class, in a loop of its own (in the other's loop it
+// took registers: 149 us for 140).
+// 64 sequences of 8191 keys on 8 heads, 32 q heads: 140 us, 605 MB at 4.3 TB/s (eight warps of 16
+// keys, one of them loading: 200 us); 144 if one group of all values is 0, 220 if every 64th
+// value is, 330 class by class.  One sequence of 65,536 keys: 31 us, 75 MB; about 10 of
+// them are the join, whose time is latency.
 #include <cmath>
 #include <type_traits>
 
@@ -74,7 +82,16 @@ constexpr int kThreads = 32 * kWarps;
 constexpr int kWeightKeys = 1024;          // keys of one head whose weights a CTA of the join adds to
 // CTAs an SM, by registers (64 sequences of 8192 keys of 64: 94 us with four, 99 with three)
 constexpr int ctas_per_sm(int D) { return D == 64 ? 4 : 3; }
-constexpr float kRescale = 8.0f;
+constexpr float kRescale = 4.0f;
+constexpr float kHead = 10.0f, kTail = 1.0f / 1024;  // a row's reference lies this far below the score that set it (log2 units)
+constexpr float kAbove = 24.0f;            // how far above that a score of other keys may lie
+// A group's scales are raised so that its base's lie in [2^-2, 2^-1); those good for products in one class are in
+// [2^-7, 2): as bf16 exponent fields 01111xxx, these bits 0 and these 1, in pairs
+constexpr uint32_t kBaseField = 125;
+constexpr uint32_t kScaleZeros = 0xC000C000u, kScaleOnes = 0x3C003C00u;
+constexpr uint32_t kNoBase = 0x7F00u;      // factor of a group whose scales have all been 0 so far: 2^127 leaves no other one small
+constexpr float kTopProduct = 15.0f;       // products in one class stay below 2^15
+constexpr int kClass = 28, kMidClass = 5;  // binades of a class; the class [2^-13, 2^15) among them
 constexpr float kLog2e = 1.4426950408889634f;
 constexpr float kLn2 = 0.69314718055994530942f;
 
@@ -311,34 +328,35 @@ __device__ __forceinline__ void lds(uint32_t (&w)[N], const void* p) {
   }
 }
 
-// Largest scale of a key's groups, as bf16 bits.
+// Finite magnitudes of two bf16 numbers (0 for a NaN or an infinity).
+__device__ __forceinline__ uint32_t finite_bits(uint32_t w) {
+  const uint32_t lo = w & 0x7FFFu, hi = w & 0x7FFF0000u;
+  return (lo < 0x7F80u ? lo : 0u) | (hi < 0x7F800000u ? hi : 0u);
+}
+
+// What raises the scales of a group whose first keys' largest is `top` (bf16 bits, not 0): a power of two, as bf16 bits.
+__device__ __forceinline__ uint32_t raising_bits(uint32_t top) {
+  return min(127u + kBaseField - (top >> 7), 253u) << 7;
+}
+// One over that.
+__device__ __forceinline__ float lowering(uint32_t bits) {
+  const uint32_t e = 254u - (bits >> 7);
+  return __uint_as_float(e ? e << 23 : 0x00400000u);
+}
+
+// Exponent of the power of two above a key's scales.
 template <int W>
-__device__ __forceinline__ uint32_t top_scale(const uint32_t (&w)[W]) {
-  uint32_t m = w[0];
+__device__ __forceinline__ float exponent_above(const uint32_t (&w)[W]) {
+  uint32_t m = w[0] & 0x7FFF7FFFu;
 #pragma unroll
-  for (int i = 1; i < W; ++i) m = __vmaxu2(m, w[i]);
-  return max(m & 0xFFFFu, m >> 16);
+  for (int i = 1; i < W; ++i) m = __vmaxu2(m, w[i] & 0x7FFF7FFFu);
+  return static_cast<float>(static_cast<int>(max(m & 0xFFFFu, m >> 16) >> 7) - 126);
 }
 
-// The same of the finite scales alone (a group of NaN or infinities has no size), of a row's first and last word.
-__device__ __forceinline__ uint32_t top_finite(uint32_t w0, uint32_t w1) {
-  const uint32_t w[4] = {w0 & 0xFFFFu, w0 >> 16, w1 & 0xFFFFu, w1 >> 16};
-  uint32_t m = 0;
-#pragma unroll
-  for (int i = 0; i < 4; ++i)
-    if (w[i] < 0x7F80u) m = max(m, w[i]);
-  return m;
-}
-
-// A key's exponent against the base: 0 within a factor of two of it, else the
-// exponent of its largest finite scale less the base, kept within +-100.
-// A key of no values (no finite scale but 0) has -80: however large its
-// probability, it must not press the others' products out of fp16.
-__device__ __noinline__ float far_exponent(uint32_t w0, uint32_t w1, int base) {
-  const uint32_t m = top_finite(w0, w1);
-  if (m == 0 || base == INT32_MAX) return -80.f;  // (without a base no key of the step has values)
-  const int e = min(max(static_cast<int>(m >> 7) - 127 - base, -100), 100);
-  return e >= -1 && e <= 1 ? 0.f : static_cast<float>(e);
+// Class of a product, 1 to 9, 0 for one too small to count; a NaN or an infinity counts to the middle one.
+__device__ __forceinline__ int class_of(float w) {
+  const uint32_t e = (__float_as_uint(w) >> 23) & 255u;  // (the middle one: 114 to 141)
+  return e == 255u ? kMidClass : min(static_cast<int>((e + 26u) / kClass), 9);
 }
 
 // ------------------------------------------------------------------ results
@@ -561,14 +579,54 @@ __global__ void __launch_bounds__(kThreads, ctas_per_sm(D)) kv4_fwd_kernel(const
       for (int i = 0; i < 4; ++i) acc[j][i] = 0.f;
     R[0] = R[1] = -INFINITY;
     l[0] = l[1] = 0.f;
-    int base = INT32_MAX;        // base exponent of the value scales (uniform over the warp; not yet chosen)
-    uint32_t near_lo = 1u << 7;  // bf16 bits from here on, for three binades, are near it (0 is not)
-    uint32_t down = 0x3F803F80u;  // 2^-base, twice in bf16
-    float up_back = 1.f;          // 2^base
-
-    // 32 keys; kAll: every row sees all of them
-    auto step = [&](auto all, int key0) __attribute__((always_inline)) {
-      constexpr bool kAll = decltype(all)::value;
+    // (uniform over the warp) the factor of each group's scales; is there a group without a base; has there been a
+    // step; are all products to be taken class by class from here on
+    uint32_t down[kGroups / 2];
+#pragma unroll
+    for (int i = 0; i < kGroups / 2; ++i) down[i] = kNoBase * 0x00010001u;
+    bool open = true, begun = false, careful = false;
+    // bits that a good pair of raised scales has none of, and all of (groups without a base: only zeros are good)
+    struct Good {
+      uint32_t zeros, ones;
+    };
+    auto good = [&](int i) __attribute__((always_inline)) -> Good {
+      Good x{kScaleZeros, kScaleOnes};
+      if (open) {
+        const uint32_t none = ((down[i] & 0xFFFFu) == kNoBase ? 0xFFFFu : 0u) | ((down[i] >> 16) == kNoBase ? 0xFFFF0000u : 0u);
+        x.zeros |= none;
+        x.ones &= ~none;
+      }
+      return x;
+    };
+    // before a step while there are groups without a base: bases for those that get values now
+    auto look = [&](int key0) __attribute__((always_inline)) {
+      open = false;
+#pragma unroll
+      for (int i = 0; i < kGroups / 2; ++i) {
+        uint32_t top = 0;
+#pragma unroll
+        for (int u = 0; u < 4; ++u)
+          if (key0 + 8 * u + g8 < run.pair.len)
+            top = __vmaxu2(top, finite_bits(*reinterpret_cast<const uint32_t*>(s.vs[st] + s_at + u * 8 * kScaleBytes + 4 * i)));
+#pragma unroll
+        for (int o = 4; o < 32; o *= 2) top = __vmaxu2(top, __shfl_xor_sync(0xffffffffu, top, o));
+#pragma unroll
+        for (int sh = 0; sh < 32; sh += 16) {
+          if (((down[i] >> sh) & 0xFFFFu) != kNoBase) continue;
+          const uint32_t t = (top >> sh) & 0xFFFFu;
+          if (t) {
+            down[i] = (down[i] & ~(0xFFFFu << sh)) | raising_bits(t) << sh;
+            careful |= begun;  // (the probabilities so far may be far above this group's first)
+          } else {
+            open = true;
+          }
+        }
+      }
+      begun = true;
+    };
+    // 32 keys; kAll: every row sees all of them; kOne: products of one class (false, and nothing done, if they are not)
+    auto step = [&](auto all, auto one, int key0) __attribute__((always_inline)) -> bool {
+      constexpr bool kAll = decltype(all)::value, kOne = decltype(one)::value;
       // ---- scores of both halves
       float x[2][4];
 #pragma unroll
@@ -593,32 +651,34 @@ __global__ void __launch_bounds__(kThreads, ctas_per_sm(D)) kv4_fwd_kernel(const
           x[u][3] = g ? fmaf(fb, c[3], x[u][3]) : fb * c[3];
         }
       }
-      // ---- value scales: are all keys' near the base?
+      // ---- value scales, raised
       uint32_t va[2][kGroups / 2], vb[2][kGroups / 2];
 #pragma unroll
       for (int u = 0; u < 2; ++u) {
         lds(va[u], s.vs[st] + s_at + u * 16 * kScaleBytes);
         lds(vb[u], s.vs[st] + s_at + (u * 16 + 8) * kScaleBytes);
       }
-      const uint32_t t0 = top_scale(va[0]), t1 = top_scale(vb[0]), t2 = top_scale(va[1]), t3 = top_scale(vb[1]);
-      if (base == INT32_MAX) {
-        // (until there is one) the largest finite one of these keys'; sums of values that are all 0 have no scale yet
-        uint32_t m = 0;
+      uint32_t bad_a[2] = {}, bad_b[2] = {}, bad = 0;
 #pragma unroll
-        for (int i = 0; i < 4; ++i) {
-          const uint32_t(&w)[kGroups / 2] = i & 1 ? vb[i / 2] : va[i / 2];
-          if (key0 + g8 + 8 * i < run.pair.len) m = max(m, top_finite(w[0], w[kGroups / 2 - 1]));
-        }
+      for (int i = 0; i < kGroups / 2; ++i) {
+        const Good y = good(i);
 #pragma unroll
-        for (int o = 4; o < 32; o *= 2) m = max(m, __shfl_xor_sync(0xffffffffu, m, o));
-        if (m > 0) {
-          base = min(max(static_cast<int>(m >> 7) - 127, -126), 120);  // (2^-base is a bf16 number)
-          near_lo = static_cast<uint32_t>(base + 126) << 7;
-          down = static_cast<uint32_t>(127 - base) * 0x00800080u;
-          up_back = exp2f(static_cast<float>(base));
+        for (int u = 0; u < 2; ++u) {
+          va[u][i] = mul_bf16x2(va[u][i], down[i]);
+          vb[u][i] = mul_bf16x2(vb[u][i], down[i]);
+          if constexpr (!kAll) {  // (whatever slots past the length hold changes nothing)
+            if (key0 + 16 * u + g8 >= run.pair.len) va[u][i] = y.ones;
+            if (key0 + 16 * u + g8 + 8 >= run.pair.len) vb[u][i] = y.ones;
+          }
+          if constexpr (!kAll) {
+            bad_a[u] |= (va[u][i] & y.zeros) | (~va[u][i] & y.ones);
+            bad_b[u] |= (vb[u][i] & y.zeros) | (~vb[u][i] & y.ones);
+          }
         }
+        bad |= ((va[0][i] | vb[0][i] | va[1][i] | vb[1][i]) & y.zeros) | (~(va[0][i] & vb[0][i] & va[1][i] & vb[1][i]) & y.ones);
       }
-      const bool near = max(max(t0 - near_lo, t1 - near_lo), max(t2 - near_lo, t3 - near_lo)) < (3u << 7);
+      const bool odd = __any_sync(0xffffffffu, bad);
+      if (odd && kOne && (kAll || open)) return false;
       // ---- softmax
       float pr[2][4];
 #pragma unroll
@@ -647,25 +707,48 @@ __global__ void __launch_bounds__(kThreads, ctas_per_sm(D)) kv4_fwd_kernel(const
       float m[2];
 #pragma unroll
       for (int i = 0; i < 2; ++i) m[i] = fmaxf(fmaxf(x[0][i], x[0][i + 2]), fmaxf(x[1][i], x[1][i + 2]));
-      if (!__all_sync(0xffffffffu, near)) {
-        const float e[4] = {far_exponent(va[0][0], va[0][kGroups / 2 - 1], base),
-                            far_exponent(vb[0][0], vb[0][kGroups / 2 - 1], base),
-                            far_exponent(va[1][0], va[1][kGroups / 2 - 1], base),
-                            far_exponent(vb[1][0], vb[1][kGroups / 2 - 1], base)};
+      auto over_keys = [&](float(&y)[2]) __attribute__((always_inline)) {
 #pragma unroll
-        for (int i = 0; i < 2; ++i)
-          m[i] = fmaxf(fmaxf(x[0][i] + e[0], x[0][i + 2] + e[1]), fmaxf(x[1][i] + e[2], x[1][i + 2] + e[3]));
-      }
+        for (int o = 4; o < 32; o *= 2) {
+          y[0] = fmaxf(y[0], __shfl_xor_sync(0xffffffffu, y[0], o));
+          y[1] = fmaxf(y[1], __shfl_xor_sync(0xffffffffu, y[1], o));
+        }
+      };
+      over_keys(m);
+      if (!kAll && odd) {
+        // the reference follows the keys all of whose scales are good, unless another is far above it
+        float near[2] = {-INFINITY, -INFINITY};
 #pragma unroll
-      for (int o = 4; o < 32; o *= 2) {
-        m[0] = fmaxf(m[0], __shfl_xor_sync(0xffffffffu, m[0], o));
-        m[1] = fmaxf(m[1], __shfl_xor_sync(0xffffffffu, m[1], o));
+        for (int u = 0; u < 2; ++u)
+#pragma unroll
+          for (int i = 0; i < 2; ++i) {
+            if (!bad_a[u]) near[i] = fmaxf(near[i], x[u][i]);
+            if (!bad_b[u]) near[i] = fmaxf(near[i], x[u][i + 2]);
+          }
+        over_keys(near);
+        bool far = m[0] > fmaxf(near[0], R[0] + kHead) + kAbove || m[1] > fmaxf(near[1], R[1] + kHead) + kAbove;
+        if constexpr (kOne) {  // nor may a product leave fp16
+#pragma unroll
+          for (int i = 0; i < 2; ++i) {
+            const float top = (near[i] > R[i] + (kHead + kRescale) ? near[i] - kHead : R[i]) + kTopProduct;
+#pragma unroll
+            for (int u = 0; u < 2; ++u)
+              far |= x[u][i] + exponent_above(va[u]) > top || x[u][i + 2] + exponent_above(vb[u]) > top;
+          }
+        }
+        if (__any_sync(0xffffffffu, far)) {
+          if constexpr (kOne) return false;
+          careful = true;
+        } else {
+          m[0] = near[0];
+          m[1] = near[1];
+        }
       }
-      if (__any_sync(0xffffffffu, m[0] > R[0] + kRescale || m[1] > R[1] + kRescale)) {
+      if (__any_sync(0xffffffffu, m[0] > R[0] + (kHead + kRescale) || m[1] > R[1] + (kHead + kRescale))) {
 #pragma unroll
         for (int i = 0; i < 2; ++i) {
           // (uniform over the lanes of a column)
-          const float to = m[i] > R[i] + kRescale ? m[i] : R[i];
+          const float to = m[i] > R[i] + (kHead + kRescale) ? m[i] - kHead : R[i];
           const float f = R[i] == -INFINITY ? 0.f : ex2_approx(R[i] - to);
           R[i] = to;
           l[i] *= f;
@@ -686,13 +769,6 @@ __global__ void __launch_bounds__(kThreads, ctas_per_sm(D)) kv4_fwd_kernel(const
         }
         l[i] += (pr[0][i] + pr[0][i + 2]) + (pr[1][i] + pr[1][i + 2]);
       }
-#pragma unroll
-      for (int u = 0; u < 2; ++u)
-#pragma unroll
-        for (int i = 0; i < kGroups / 2; ++i) {
-          va[u][i] = mul_bf16x2(va[u][i], down);
-          vb[u][i] = mul_bf16x2(vb[u][i], down);
-        }
       // ---- output, a half at a time
 #pragma unroll
       for (int u = 0; u < 2; ++u) {
@@ -707,15 +783,12 @@ __global__ void __launch_bounds__(kThreads, ctas_per_sm(D)) kv4_fwd_kernel(const
           // probabilities times value scales, transposed into the second product's operand
           const float fa = g & 1 ? bf16_hi(va[u][g / 2]) : bf16_lo(va[u][g / 2]);
           const float fb = g & 1 ? bf16_hi(vb[u][g / 2]) : bf16_lo(vb[u][g / 2]);
-          uint32_t b0, b1;
           float w[4] = {pr[u][0] * fa, pr[u][1] * fa, pr[u][2] * fb, pr[u][3] * fb};
           if constexpr (!kAll) {  // (an unseen slot's scale may be anything)
 #pragma unroll
             for (int i = 0; i < 4; ++i)
               if (x[u][i] == -INFINITY) w[i] = 0.f;
           }
-          b0 = transpose8x8(pack_f16x2(w[0], w[1]));
-          b1 = transpose8x8(pack_f16x2(w[2], w[3]));
           const uint32_t sel = g & 1 ? sel_hi : sel_lo;
           const uint32_t lo = __byte_perm(v0[g / 2], v1[g / 2], sel), hi = __byte_perm(v8[g / 2], v9[g / 2], sel);
           // elements 4 g8 + 0..3 of the group: rows g8 and (times 16) g8 + 8 of two products
@@ -724,33 +797,82 @@ __global__ void __launch_bounds__(kThreads, ctas_per_sm(D)) kv4_fwd_kernel(const
           const uint32_t lo8 = lo >> 8, hi8 = hi >> 8;
           const uint32_t c0 = minus8(lo8 & 0x000F000Fu, 0x00080008u), c1 = minus8(lo8 & 0x00F000F0u, 0x00800080u);
           const uint32_t c2 = minus8(hi8 & 0x000F000Fu, 0x00080008u), c3 = minus8(hi8 & 0x00F000F0u, 0x00800080u);
-          mma_f16(acc[2 * g], a0, a1, a2, a3, b0, b1);
-          mma_f16(acc[2 * g + 1], c0, c1, c2, c3, b0, b1);
+          if constexpr (kOne) {
+            const uint32_t b0 = transpose8x8(pack_f16x2(w[0], w[1])), b1 = transpose8x8(pack_f16x2(w[2], w[3]));
+            mma_f16(acc[2 * g], a0, a1, a2, a3, b0, b1);
+            mma_f16(acc[2 * g + 1], c0, c1, c2, c3, b0, b1);
+          } else {
+            int cls[4];
+            uint32_t have = 0;
+#pragma unroll
+            for (int i = 0; i < 4; ++i) {
+              cls[i] = class_of(w[i]);
+              have |= 1u << cls[i];
+            }
+            have = __reduce_or_sync(0xffffffffu, have) & ~1u;
+            while (have) {
+              const int c = __ffs(have) - 1;
+              have &= have - 1;
+              const float into = __uint_as_float(static_cast<uint32_t>(127 + kClass * (kMidClass - c)) << 23);
+              const float back = __uint_as_float(static_cast<uint32_t>(127 - kClass * (kMidClass - c)) << 23);
+              float y[4], x0[4] = {}, x1[4] = {};
+#pragma unroll
+              for (int i = 0; i < 4; ++i) y[i] = cls[i] == c ? w[i] * into : 0.f;
+              const uint32_t b0 = transpose8x8(pack_f16x2(y[0], y[1])), b1 = transpose8x8(pack_f16x2(y[2], y[3]));
+              mma_f16(x0, a0, a1, a2, a3, b0, b1);
+              mma_f16(x1, c0, c1, c2, c3, b0, b1);
+#pragma unroll
+              for (int i = 0; i < 4; ++i) {
+                acc[2 * g][i] = fmaf(x0[i], back, acc[2 * g][i]);
+                acc[2 * g + 1][i] = fmaf(x1[i], back, acc[2 * g + 1][i]);
+              }
+            }
+          }
+        }
+      }
+      return true;
+    };
+
+    int32_t kt = run.k0;
+    auto tiles = [&](auto one) __attribute__((always_inline)) {
+      constexpr bool kOne = decltype(one)::value;
+      for (; kt < run.k1; ++kt, ++n) {
+        // (after a wait that ran out the loop goes on without waiting, on whatever
+        // the stages hold: the barriers between the warps stay matched)
+        if (ok) ok = mbar_wait_warp(&s.full[st], parity, wc);
+        const int32_t key0 = kt * kTileKeys + warp * 32;
+        if (key0 < lim_max) {
+          if constexpr (kOne) {
+            const bool all = __all_sync(0xffffffffu, key0 + 32 <= lim_min);
+            if (!begun) look(key0);
+            if (careful || (!(all && step(std::true_type{}, one, key0)) && !step(std::false_type{}, one, key0))) return;
+          } else {
+            if (open) look(key0);
+            step(std::false_type{}, one, key0);
+          }
+        }
+        // (at the end: the stage it goes to, the last tile's, is long released; before this warp's own release, which
+        // hands the loader's place on to the next warp)
+        if (static_cast<int>(n % kWarps) == warp) {
+          if (lane == 0 && ok) ok = load_tile(n + Sh::kAhead);
+          ok = __all_sync(0xffffffffu, ok);
+        }
+        __syncwarp();
+        if (lane == 0) mbar_arrive(&s.empty[st]);
+        if (++st == kStages) {
+          st = 0;
+          parity ^= 1u;
+        }
+        if (!kOne && !careful) {
+          ++kt;
+          ++n;
+          return;
         }
       }
     };
-
-    for (int32_t kt = run.k0; kt < run.k1; ++kt, ++n) {
-      // (after a wait that ran out the loop goes on without waiting, on whatever
-      // the stages hold: the barriers between the warps stay matched)
-      if (ok) ok = mbar_wait_warp(&s.full[st], parity, wc);
-      const int32_t key0 = kt * kTileKeys + warp * 32;
-      if (key0 < lim_max) {
-        if (__all_sync(0xffffffffu, key0 + 32 <= lim_min)) step(std::true_type{}, key0);
-        else step(std::false_type{}, key0);
-      }
-      // (at the end: the stage it goes to, the last tile's, is long released; before this warp's own release, which
-      // hands the loader's place on to the next warp)
-      if (static_cast<int>(n % kWarps) == warp) {
-        if (lane == 0 && ok) ok = load_tile(n + Sh::kAhead);
-        ok = __all_sync(0xffffffffu, ok);
-      }
-      __syncwarp();
-      if (lane == 0) mbar_arrive(&s.empty[st]);
-      if (++st == kStages) {
-        st = 0;
-        parity ^= 1u;
-      }
+    while (kt < run.k1) {
+      tiles(std::true_type{});
+      tiles(std::false_type{});  // (the tile that is not of one class)
     }
 
     // ---- the warps' parts into one
@@ -759,8 +881,8 @@ __global__ void __launch_bounds__(kThreads, ctas_per_sm(D)) kv4_fwd_kernel(const
 #pragma unroll
       for (int o = 4; o < 32; o *= 2) l[i] += __shfl_xor_sync(0xffffffffu, l[i], o);
       if (g8 == 0) {
-        s.stat[0][warp][2 * t4 + i] = R[i];
-        s.stat[1][warp][2 * t4 + i] = l[i];
+        s.stat[0][warp][2 * t4 + i] = R[i] + kHead;  // (sums as if for the score that set the reference)
+        s.stat[1][warp][2 * t4 + i] = l[i] * kTail;
       }
     }
     __syncthreads();
@@ -772,9 +894,10 @@ __global__ void __launch_bounds__(kThreads, ctas_per_sm(D)) kv4_fwd_kernel(const
       float m = -INFINITY;
 #pragma unroll
       for (int w = 0; w < kWarps; ++w) m = fmaxf(m, s.stat[0][w][2 * t4 + i]);
-      const float f = R[i] == -INFINITY ? (l[i] == 0.f ? 0.f : 1.f) : ex2_approx(R[i] - m);
-      const float even = f * 16777216.f, odd = even * 0.0625f;
-      // (2^base by itself: it may be far from 1)
+      const float f = R[i] == -INFINITY ? (l[i] == 0.f ? 0.f : 1.f) : ex2_approx(R[i] + kHead - m);
+      const float even = f * (kTail * 16777216.f), odd = even * 0.0625f;
+      // (by itself: it may be far from 1)
+      const float up_back = lowering((down[g / 2] >> (g & 1) * 16) & 0xFFFFu);
       return make_float4(acc[2 * g][i] * even * up_back, acc[2 * g][i + 2] * odd * up_back,
                          acc[2 * g + 1][i] * even * up_back, acc[2 * g + 1][i + 2] * odd * up_back);
     };

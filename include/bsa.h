@@ -426,8 +426,9 @@ typedef struct {
  * length outside 0..capacity counts as the nearer end and sets the bounds bit
  * of the device error word.  Slots at or past lens[b] are never used,
  * whatever they hold.  Products of a probability and a value scale are held in
- * fp16 beside a power of two chosen per run of keys; the non-zero
- * scales of the values of one sequence and head may lie up to 2^80 apart. */
+ * fp16 beside a power of two chosen per run of keys and group of 32 channels;
+ * groups may differ in size as they like, the non-zero scales of one group, sequence and
+ * head by up to 2^80. */
 BSA_API bsa_status bsa_kv4_fwd(const bsa_kv4_fwd_args* args, bsa_stream stream);
 BSA_API bsa_status bsa_kv4_fwd_workspace(const bsa_kv4_fwd_args* args, size_t* bytes);
 

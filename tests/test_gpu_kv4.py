@@ -833,3 +833,88 @@ def test_fwd_nan_group_of_the_only_key_of_a_warp(D, n, cap, size):
     o, lse = bsa.kv4_fwd(q.cuda(), cache, i32([n]))
     assert bsa.get_device_error() == 0
     check_groups(o, lse, q, kv, vv, [n], bad=(1,))
+
+
+def group_sized(v, e):
+    """v (bf16 [.., D]) times 2^e, e whole numbers [.., D/32] (broadcast)."""
+    e = np.broadcast_to(np.repeat(np.asarray(e), 32, -1), v.shape)
+    return torch.ldexp(v.double(), torch.from_numpy(e.copy())).to(torch.bfloat16)
+
+
+@pytest.mark.parametrize("n,cap", [(64, 64), (1010, 1024), (2050, 2064)])
+@pytest.mark.parametrize("D,sizes", [(64, (0, -14)), (64, (-20, 3)), (64, (0, -30)), (128, (0, -18, -25, 10)), (128, (-60, 15, 0, -90)),
+                                     (128, (-100, -112, 0, 30))])
+def test_fwd_groups_of_unequal_size(D, sizes, n, cap):
+    bsa = bsa_()
+    k, v, q = rows((1, 2, cap, D), 160), rows((1, 2, cap, D), 161), rows((1, 6, 1, D), 162)
+    cache, kv, vv = filled(bsa, 1, 2, cap, D, 163, k=k, v=group_sized(v, sizes))
+    o, lse = bsa.kv4_fwd(q.cuda(), cache, i32([n]))
+    assert bsa.get_device_error() == 0
+    check_groups(o, lse, q, kv, vv, [n])
+
+
+@pytest.mark.parametrize("n,cap", [(70, 80), (1024, 1024), (2050, 2064)])
+@pytest.mark.parametrize("spread", [4, 12, 40])
+@pytest.mark.parametrize("D", [64, 128])
+def test_fwd_groups_of_sizes_that_change_from_key_to_key(D, spread, n, cap):
+    bsa = bsa_()
+    rng = np.random.default_rng(170)
+    k, v, q = rows((2, 1, cap, D), 171), rows((2, 1, cap, D), 172), rows((2, 3, 2, D), 173)
+    v = group_sized(v, rng.integers(-spread, spread + 1, (2, 1, cap, D // 32)))
+    cache, kv, vv = filled(bsa, 2, 1, cap, D, 174, k=k, v=v)
+    lens = [n, n // 2 + 1]
+    poison(cache, lens)
+    o, lse = bsa.kv4_fwd(q.cuda(), cache, i32(lens))
+    assert bsa.get_device_error() == 0
+    check_groups(o, lse, q, kv, vv, lens)
+
+
+@pytest.mark.parametrize("n,cap", [(100, 112), (2050, 2064)])
+@pytest.mark.parametrize("size", [None, -12, -40, -80])   # None: all zeros
+@pytest.mark.parametrize("ahead", [0.25, 2.0])            # (of all the weight but 2^-7 or so, and but 2^-54 or so)
+@pytest.mark.parametrize("at", [0, 31, 40, 96])
+def test_fwd_key_of_nearly_all_the_weight_has_a_small_group(at, ahead, size, n, cap):
+    """Key `at` takes nearly all the weight of the first row; its second group is far smaller than the others',
+    or 0: what that group gets then comes from keys of little weight."""
+    bsa = bsa_()
+    D = 128
+    k, v, q = rows((1, 1, cap, D), 180), rows((1, 1, cap, D), 181), rows((1, 2, 1, D), 182)
+    k[0, 0, at] = (q[0, 0, 0].float() * ahead).to(torch.bfloat16)
+    v[0, 0, at, 32:64] = 0 if size is None else torch.ldexp(v[0, 0, at, 32:64].double(), torch.tensor(size)).to(torch.bfloat16)
+    cache, kv, vv = filled(bsa, 1, 1, cap, D, 183, k=k, v=v)
+    o, lse = bsa.kv4_fwd(q.cuda(), cache, i32([n]))
+    assert bsa.get_device_error() == 0
+    check_groups(o, lse, q, kv, vv, [n])
+
+
+@pytest.mark.parametrize("n,cap", [(500, 512), (2050, 2064)])
+@pytest.mark.parametrize("zeros", [1, 33, 129, 400, 3000])
+def test_fwd_group_that_begins_with_zeros(zeros, n, cap):
+    """The first keys' last group is 0 (a head of 96 channels padded to 128, where all are), with a key of nearly
+    all the weight among them."""
+    bsa = bsa_()
+    D = 128
+    k, v, q = rows((1, 1, cap, D), 190), rows((1, 1, cap, D), 191), rows((1, 2, 1, D), 192)
+    k[0, 0, 0] = (q[0, 0, 0].float() * 0.75).to(torch.bfloat16)
+    v[0, 0, :zeros, 96:] = 0
+    cache, kv, vv = filled(bsa, 1, 1, cap, D, 193, k=k, v=v)
+    o, lse = bsa.kv4_fwd(q.cuda(), cache, i32([n]))
+    assert bsa.get_device_error() == 0
+    check_groups(o, lse, q, kv, vv, [n])
+
+
+@pytest.mark.parametrize("cap", [256, 2064])
+def test_fwd_does_not_depend_on_what_lies_behind_the_lengths(cap):
+    bsa = bsa_()
+    B, Hq, Hkv, T, D = 3, 4, 2, 2, 128
+    cache, _, _ = filled(bsa, B, Hkv, cap, D, 200)
+    q, lens = rows((B, Hq, T, D), 201).cuda(), [cap - 3, 33, cap // 2 + 1]
+    want = bsa.kv4_fwd(q, cache, i32(lens))
+    for scale in (0.0, float("nan"), 2.0 ** -60, 2.0 ** 60):
+        poison(cache, lens)
+        for b, n in enumerate(lens):
+            cache.k_scales[b, :, n:] = scale
+            cache.v_scales[b, :, n:] = scale
+        got = bsa.kv4_fwd(q, cache, i32(lens))
+        assert torch.equal(got[0], want[0]) and torch.equal(got[1], want[1])
+    assert bsa.get_device_error() == 0
