@@ -193,8 +193,8 @@ __device__ __forceinline__ void add_probs(const KwParams& p, const uint32_t (&v)
     float e0, e1;
     if constexpr (kCap) {
       const float2 t = *reinterpret_cast<const float2*>(term + 2 * i);
-      e0 = v[2 * i] == kHidden ? -INFINITY : fmaf(tanh_fast(__uint_as_float(v[2 * i]) * p.scale_log2), p.cap_log2, t.x);
-      e1 = v[2 * i + 1] == kHidden ? -INFINITY : fmaf(tanh_fast(__uint_as_float(v[2 * i + 1]) * p.scale_log2), p.cap_log2, t.y);
+      e0 = v[2 * i] == kHidden ? -INFINITY : fmaf(tanh_nan(__uint_as_float(v[2 * i]) * p.scale_log2), p.cap_log2, t.x);
+      e1 = v[2 * i + 1] == kHidden ? -INFINITY : fmaf(tanh_nan(__uint_as_float(v[2 * i + 1]) * p.scale_log2), p.cap_log2, t.y);
     } else {
       f2_unpack(f2_mul(f2_pack(__uint_as_float(v[2 * i]), __uint_as_float(v[2 * i + 1])), sc2), e0, e1);
     }

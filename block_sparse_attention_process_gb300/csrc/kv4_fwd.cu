@@ -686,7 +686,7 @@ __global__ void __launch_bounds__(kThreads, ctas_per_sm(D)) kv4_fwd_kernel(const
 #pragma unroll
         for (int i = 0; i < 4; ++i) {
           x[u][i] *= qf[i & 1];
-          if constexpr (kCap) x[u][i] = p.cap_log2 * tanh_fast(x[u][i]);
+          if constexpr (kCap) x[u][i] = p.cap_log2 * tanh_nan(x[u][i]);
         }
       if constexpr (!kAll) {
 #pragma unroll

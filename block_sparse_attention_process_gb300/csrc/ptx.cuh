@@ -560,6 +560,12 @@ __device__ __forceinline__ float tanh_fast(float x) {
   return 1.f - __fdividef(2.f, 1.f + ex2_approx(xc * 2.8853900817779268f));
 }
 
+// The same, with NaN of a NaN (fmin and fmax would drop it).  Nothing needs clamping: exp2 goes to 0 or to infinity,
+// over which 2 is 0.
+__device__ __forceinline__ float tanh_nan(float x) {
+  return 1.f - __fdividef(2.f, 1.f + ex2_approx(x * 2.8853900817779268f));
+}
+
 __device__ __forceinline__ uint32_t elect_one_lane() {
   return (threadIdx.x & 31u) == 0u;
 }

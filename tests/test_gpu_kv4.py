@@ -918,3 +918,74 @@ def test_fwd_does_not_depend_on_what_lies_behind_the_lengths(cap):
         got = bsa.kv4_fwd(q, cache, i32(lens))
         assert torch.equal(got[0], want[0]) and torch.equal(got[1], want[1])
     assert bsa.get_device_error() == 0
+
+
+# ------------------------------------------------------------------ NaN under a soft cap
+
+@pytest.mark.parametrize("softcap", [None, 20.0])
+@pytest.mark.parametrize("n,cap", [(1, 16), (90, 96), (2060, 2064)])
+def test_fwd_nan_scores(n, cap, softcap):
+    """A query of NaN is NaN itself alone; a key that reads as NaN makes its group's rows NaN that see it."""
+    bsa = bsa_()
+    D = 64
+    k, v, q = rows((2, 2, cap, D), 210), rows((2, 2, cap, D), 211), rows((2, 4, 2, D), 212)
+    q[0, 1, 0, 7] = float("nan")             # one row of (0, key head 0)
+    k[1, 1, n - 1, 40] = float("nan")        # seen by the last token of (1, key head 1)
+    cache, kv, vv = filled(bsa, 2, 2, cap, D, 213, k=k, v=v)
+    before = cache.weights.clone()
+    o, lse = bsa.kv4_fwd(q.cuda(), cache, i32([n, n]), logits_soft_cap=softcap, accumulate=True)
+    assert bsa.get_device_error() == 0
+    want = kv4.forward(np.nan_to_num(q.double().numpy()), np.nan_to_num(kv), vv, [n, n], cap=softcap or 0)
+    nan = np.zeros((2, 4, 2), bool)
+    nan[0, 1, 0] = n > 1                     # (of one key the last token alone sees it)
+    nan[1, 2:, 1] = True
+    o, lse, dw = host(o), host(lse), host(cache.weights - before)
+    assert np.array_equal(np.isnan(lse), nan) and np.array_equal(np.isnan(o), np.broadcast_to(nan[..., None], o.shape))
+    ds = (2.0 ** -16 * want[4] + 2.0 ** -19 * (softcap or 0))[~nan]
+    within("lse", lse[~nan], want[1][~nan], ds + 2.0 ** -20 * np.maximum(1, np.nan_to_num(np.abs(want[1][~nan]), posinf=0)))
+    within("o", o[~nan], want[0][~nan], 2.0 ** -8 * np.abs(want[0][~nan]) + (2.0 ** -10 + 2 * ds[:, None]) * want[3][~nan])
+    seen = np.arange(cap) < n
+    assert np.isnan(dw[1, 1, seen]).all() and np.isfinite(dw[0, 1]).all() and np.isfinite(dw[1, 0]).all()
+    assert np.isnan(dw[0, 0, seen & (np.arange(cap) < n - 1)]).all() and (dw[:, :, ~seen] == 0).all()
+
+
+@pytest.mark.parametrize("softcap", [None, 10.0])
+@pytest.mark.parametrize("D", [64, 128])
+def test_key_weights_of_nan_scores(D, softcap):
+    """A NaN query whose logsumexp is finite makes the keys it sees NaN, a NaN key itself."""
+    bsa = bsa_()
+    S = 256
+    q, k = rows((1, 2, S, D), 215).cuda(), rows((1, 2, S, D), 216).cuda()
+    info, dkv = bsa.mask_compile("causal", S, S), bsa.mask_compile("causal", S, S, orientation="dkv")
+    _, lse = bsa.fwd(q, k, k, info, logits_soft_cap=softcap)
+    clean = bsa.key_weights(q, k, lse, dkv, logits_soft_cap=softcap)
+    q, k = q.clone(), k.clone()
+    q[0, 0, 131, 3] = float("nan")
+    k[0, 1, 70, D - 1] = float("nan")
+    got = bsa.key_weights(q, k, lse, dkv, logits_soft_cap=softcap)
+    assert bsa.get_device_error() == 0
+    nan = torch.zeros_like(clean, dtype=torch.bool)
+    nan[0, 0, :132] = True
+    nan[0, 1, 70] = True
+    assert torch.equal(torch.isnan(got), nan) and torch.equal(got[~nan], clean[~nan])
+
+
+def test_fwd_and_key_weights_of_scores_far_above_the_cap():
+    bsa = bsa_()
+    B, Hq, Hkv, S, D, softcap = 1, 2, 1, 128, 64, 3.0
+    q, k, v = rows((B, Hq, S, D), 217, 60.0), rows((B, Hkv, S, D), 218), rows((B, Hkv, S, D), 219)
+    cache, kv, vv = filled(bsa, B, Hkv, S, D, 0, k=k, v=v)
+    want = kv4.forward(q[:, :, :1].double().numpy(), kv, vv, [S], cap=softcap)
+    assert want[4].max() > 64 * softcap                            # (the exponential overflows from 45 of them)
+    o, lse = bsa.kv4_fwd(q[:, :, :1].cuda(), cache, i32([S]), logits_soft_cap=softcap)
+    # (a score's error reaches the capped one at most unchanged; the tanh's own and the rest as above)
+    check_fwd(o, lse, None, want, softcap)
+    dkv = bsa.mask_compile("full", S, S, orientation="dkv")
+    qd, kd = q.double().numpy()[0], k.double().numpy()[0, 0]
+    s = softcap * np.tanh(qd @ kd.T * D ** -0.5 / softcap)
+    lse = np.log(np.exp(s).sum(-1)).astype(np.float32)
+    want = np.exp(s - lse[..., None].astype(np.float64)).sum((0, 1))
+    got = bsa.key_weights(q.cuda(), k.cuda(), torch.from_numpy(lse[None]).cuda(), dkv, logits_soft_cap=softcap)
+    ds = 2.0 ** -16 * (np.abs(qd) @ np.abs(kd).T).max() * D ** -0.5 + 2.0 ** -19 * softcap + 2.0 ** -23 * np.abs(lse).max()
+    within("key weights", host(got)[0, 0], want, want * (2 * ds + 2.0 ** -18) + 1e-30)
+    assert bsa.get_device_error() == 0
