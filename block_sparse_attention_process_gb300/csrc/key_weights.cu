@@ -160,9 +160,9 @@ __global__ void __launch_bounds__(256) key_weights_terms(const __grid_constant__
   if constexpr (kCap) {
     static_cast<float*>(p.terms)[i] = t;
   } else {
-    // three pieces of 8 bits hold all 24 of the fp32 term (hidden: the first alone)
+    // three pieces of 8 bits hold all 24 of the fp32 term (hidden, or an infinity: the first alone)
     const __nv_bfloat16 hi = __float2bfloat16_rn(t);
-    const float r1 = gone ? 0.f : t - __bfloat162float(hi);
+    const float r1 = gone || isinf(__bfloat162float(hi)) ? 0.f : t - __bfloat162float(hi);
     const __nv_bfloat16 mid = __float2bfloat16_rn(r1);
     const __nv_bfloat16 lo = __float2bfloat16_rn(r1 - __bfloat162float(mid));
     uint8_t* at = static_cast<uint8_t*>(p.terms) + i / 128 * 4096 + (i % 128) / 8 * 256 + (i % 8) * 16;

@@ -989,3 +989,28 @@ def test_fwd_and_key_weights_of_scores_far_above_the_cap():
     ds = 2.0 ** -16 * (np.abs(qd) @ np.abs(kd).T).max() * D ** -0.5 + 2.0 ** -19 * softcap + 2.0 ** -23 * np.abs(lse).max()
     within("key weights", host(got)[0, 0], want, want * (2 * ds + 2.0 ** -18) + 1e-30)
     assert bsa.get_device_error() == 0
+
+
+@pytest.mark.parametrize("softcap,scale", [(None, None), (None, -0.05), (None, 0.0), (15.0, None)])
+def test_key_weights_of_infinite_and_huge_logsumexps(softcap, scale):
+    """Queries that count with a logsumexp of infinity, or of 300: their probabilities are 0."""
+    bsa = bsa_()
+    S, D = 256, 64
+    q, k = rows((1, 2, S, D), 220), rows((1, 1, S, D), 221)
+    sc = D ** -0.5 if scale is None else scale
+    s = sc * np.einsum("hid,jd->hij", q.double().numpy()[0], k.double().numpy()[0, 0])
+    if softcap:
+        s = softcap * np.tanh(s / softcap)
+    s = np.where(np.tril(np.ones((S, S), bool)), s, -np.inf)
+    lse = np.log(np.exp(s - s.max(-1, keepdims=True)).sum(-1)) + s.max(-1)
+    lse[0, [0, 100, 255]] = np.inf
+    lse[1, [17, 130]] = 300
+    l32 = lse.astype(np.float32)
+    want = np.exp(s - l32[..., None].astype(np.float64)).sum((0, 1))
+    dkv = bsa.mask_compile("causal", S, S, orientation="dkv")
+    got = bsa.key_weights(q.cuda(), k.cuda(), torch.from_numpy(l32[None]).cuda(), dkv, softmax_scale=scale, logits_soft_cap=softcap)
+    assert bsa.get_device_error() == 0
+    amax = abs(sc) * np.einsum("hid,jd->hij", np.abs(q.double().numpy()[0]), np.abs(k.double().numpy()[0, 0])).max()
+    top = np.abs(lse[np.isfinite(lse) & (lse != 300)]).max()
+    ds = 2.0 ** -16 * amax + 2.0 ** -23 * max(1.0, top) + 2.0 ** -19 * (softcap or 0)
+    within("key weights", host(got)[0, 0], want, want * (2 * ds + 2.0 ** -18) + 1e-30)
