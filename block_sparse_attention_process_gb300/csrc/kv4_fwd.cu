@@ -139,13 +139,14 @@ __device__ __forceinline__ Pair load_pair(const Kv4FwdParams& p, int32_t b, uint
   return x;
 }
 
-// Units of all sequences, and of the first ones up to b; every lane of the calling warp gets both.
-__device__ __forceinline__ int64_t total_units(const Kv4FwdParams& p, int32_t b, int64_t* before) {
+// Units of all sequences, and of the first ones up to b; every lane of the calling warp gets both.  Lengths outside
+// the cache are reported to `err`, if there is one.
+__device__ __forceinline__ int64_t total_units(const Kv4FwdParams& p, int32_t b, int64_t* before, uint32_t* err = nullptr) {
   const int lane = threadIdx.x & 31;
   const int64_t per = static_cast<int64_t>(p.c.Hkv) * p.row_tiles;
   int64_t sum = 0, head = 0;
   for (int32_t i = lane; i < p.c.B; i += 32) {
-    const int64_t n = load_pair(p, i, nullptr).units * per;
+    const int64_t n = load_pair(p, i, err).units * per;
     sum += n;
     if (i < b) head += n;
   }
@@ -181,7 +182,7 @@ struct Run {
   int32_t k0, k1;      // the part's key tiles
   bool whole;          // the part is the whole pair
   // places the cursor before unit `first` (warp-collective)
-  __device__ __forceinline__ void init(const Kv4FwdParams& p, int64_t first, int64_t last, uint32_t* err) {
+  __device__ __forceinline__ void init(const Kv4FwdParams& p, int64_t first, int64_t last) {
     at = first;
     end = last;
     const int lane = threadIdx.x & 31;
@@ -190,7 +191,7 @@ struct Run {
     int32_t b = 0;
     if (at < end) {
       for (int32_t b0 = 0;; b0 += 32) {
-        const int64_t n = b0 + lane < p.c.B ? load_pair(p, b0 + lane, err).units * per : 0;
+        const int64_t n = b0 + lane < p.c.B ? load_pair(p, b0 + lane, nullptr).units * per : 0;
         int64_t inc = n;
 #pragma unroll
         for (int o = 1; o < 32; o *= 2) {
@@ -452,10 +453,11 @@ __global__ void __launch_bounds__(kThreads, ctas_per_sm(D)) kv4_fwd_kernel(const
     run.init_whole(p, blockIdx.x, threadIdx.x == 0 ? p.err : nullptr);
   } else {
     int64_t none;
-    const int64_t total = total_units(p, 0, &none);
+    // (every CTA goes through all sequences; the first one's first warp reports)
+    const int64_t total = total_units(p, 0, &none, blockIdx.x == 0 && warp == 0 ? p.err : nullptr);
     const int32_t n_cta = runs(p, total);
     if (static_cast<int32_t>(blockIdx.x) >= n_cta) return;
-    run.init(p, first_unit(blockIdx.x, total, n_cta), first_unit(blockIdx.x + 1, total, n_cta), warp == 0 ? p.err : nullptr);
+    run.init(p, first_unit(blockIdx.x, total, n_cta), first_unit(blockIdx.x + 1, total, n_cta));
   }
 
   // One lane: tile `n` of the run into its stage, if there is one; true if that went well.

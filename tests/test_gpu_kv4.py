@@ -1014,3 +1014,19 @@ def test_key_weights_of_infinite_and_huge_logsumexps(softcap, scale):
     top = np.abs(lse[np.isfinite(lse) & (lse != 300)]).max()
     ds = 2.0 ** -16 * amax + 2.0 ** -23 * max(1.0, top) + 2.0 ** -19 * (softcap or 0)
     within("key weights", host(got)[0, 0], want, want * (2 * ds + 2.0 ** -18) + 1e-30)
+
+
+@pytest.mark.parametrize("B,cap,T,lens", [(1, 2064, 1, {0: -1}), (2, 2064, 1, {0: -1, 1: -7}), (33, 1040, 1, {32: -1}),
+                                          (70, 1040, 1, {69: -3}), (40, 1040, 1, {35: 1041}), (2, 32, 9, {0: -2, 1: -1})])
+def test_fwd_split_over_ctas_reports_lengths_outside_the_cache(B, cap, T, lens):
+    """Wherever in the batch, and also where no sequence holds a key (T of 9 with weights is split at any capacity)."""
+    bsa = bsa_()
+    D = 64
+    cache, kv, vv = filled(bsa, B, 1, cap, D, 230)
+    q = rows((B, 1, T, D), 231)
+    ls = [lens.get(b, 1 + 7 * b) for b in range(B)]
+    o, lse = bsa.kv4_fwd(q.cuda(), cache, i32(ls), accumulate=T > 8)
+    with pytest.raises(bsa.BsaError):
+        bsa.get_device_error()
+    assert bsa.get_device_error() == 0
+    check_fwd(o, lse, None, kv4.forward(q.double().numpy(), kv, vv, [min(max(n, 0), cap) for n in ls]))
