@@ -15,9 +15,10 @@ After a prompt, token by token over a cache held in 4 bits:
 
     cache = KV4Cache.empty(B, Hkv, capacity, D)
     kv4_append(cache, k, v, start, weights=key_weights(q, k, lse, dkv))
-    kv4_append(cache, k1, v1, lens)                          # each new token ...
-    o1, lse1 = kv4_fwd(q1, cache, lens + 1, accumulate=True)
-    lens, index = kv4_evict(cache, lens + 1, keep, recent=recent, seen=seen)
+    kv4_append(cache, k1, v1, lens, positions=seen)          # each new token: slot lens[b], position seen[b]
+    lens, seen = lens + 1, seen + 1
+    o1, lse1 = kv4_fwd(q1, cache, lens, accumulate=True)
+    lens, index = kv4_evict(cache, lens, keep, recent=recent, seen=seen)
 """
 from __future__ import annotations
 
@@ -469,7 +470,9 @@ def kv4_append(cache: KV4Cache, k: torch.Tensor, v: torch.Tensor, start: torch.T
                weights: Optional[torch.Tensor] = None, values: bool = False, stream=None):
     """bsa_kv4_append: tokens of k, v (bf16 [B,Hkv,T,D], any strides with a contiguous last axis) into slots
     start[b] + t (int32 [B] on the device).  ``n_new``: tokens past it are padding; ``positions``: position of token
-    0 (default start); ``weights`` fp32 [B,Hkv,T]: initial accumulated weights (default 0).  With ``values``
+    0 (default start, which is right until tokens are evicted: from then on a sequence holds fewer tokens than it has
+    had, and eviction's ``recent`` goes by positions); ``weights`` fp32 [B,Hkv,T]: initial accumulated weights
+    (default 0; a cache without weights or positions keeps none).  With ``values``
     returns what the cache now holds, (k, v) bf16 [B,Hkv,T,D], 0 for padding."""
     dev, index = cache.device, cache.index
     B, H, T, D = k.shape if k.dim() == 4 else (0, 0, 0, 0)

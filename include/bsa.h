@@ -387,7 +387,8 @@ typedef struct {
   int64_t T;                         /* tokens per sequence in k and v */
   const int32_t* start;              /* device int32 [B]: the slot of token 0 */
   const int32_t* n_new;              /* device int32 [B], or NULL (= T): tokens at or past n_new[b] are padding */
-  const int32_t* first_position;     /* device int32 [B], or NULL (= start): position of token 0 */
+  const int32_t* first_position;     /* device int32 [B], or NULL (= start, right until tokens are evicted): position
+                                        of token 0 */
   const float* weights0;             /* device fp32 [B, Hkv, T], or NULL (= 0): initial accumulated weights */
   void* k_values;                    /* bf16 [B, Hkv, T, D] or NULL: what the cache now holds (0 for padding; a token
                                         outside the cache as if stored) */

@@ -1030,3 +1030,31 @@ def test_fwd_split_over_ctas_reports_lengths_outside_the_cache(B, cap, T, lens):
         bsa.get_device_error()
     assert bsa.get_device_error() == 0
     check_fwd(o, lse, None, kv4.forward(q.double().numpy(), kv, vv, [min(max(n, 0), cap) for n in ls]))
+
+
+# ------------------------------------------------------------------ the documented loop
+
+def test_the_documented_loop_keeps_the_newest_tokens():
+    """The README's program, line by line; its token lines run again and again, past several evictions."""
+    bsa = bsa_()
+    with open(os.path.join(ROOT, "README.md")) as f:
+        block = [b for b in f.read().split("```python\n")[1:] if "kv4_append" in b][0].split("```")[0]
+    lines = block.splitlines()
+    first = next(i for i, x in enumerate(lines) if x.startswith("bsa.kv4_append(cache, k1"))
+    B, Hq, Hkv, D, S, budget = 2, 4, 2, 64, 256, 272
+    q, k, v = (rows((B, h, S, D), 240 + i).cuda() for i, h in enumerate((Hq, Hkv, Hkv)))
+    dkv = bsa.mask_compile("causal", S, S, orientation="dkv")
+    _, lse = bsa.fwd(q, k, v, bsa.mask_compile("causal", S, S))
+    q1, k1, v1 = (rows((B, h, 1, D), 243 + i).cuda() for i, h in enumerate((Hq, Hkv, Hkv)))
+    ns = dict(bsa=bsa, q=q, k=k, v=v, lse=lse, dkv=dkv, B=B, Hkv=Hkv, D=D, capacity=320, pos=i32([0, 0]), q1=q1, k1=k1, v1=v1,
+              budget=budget, lens=i32([S, S]), seen=i32([S, S]))
+    exec("\n".join(lines[:first]), ns)
+    for step in range(40):
+        exec("\n".join(lines[first:]), ns)
+        assert host(ns["seen"]).tolist() == [S + step + 1] * B and host(ns["lens"]).tolist() == [min(S + step + 1, budget)] * B
+        pos = host(ns["cache"].positions)
+        for b in range(B):
+            for h in range(Hkv):
+                have = pos[b, h, :min(S + step + 1, budget)].tolist()
+                assert len(set(have)) == len(have) and set(have) >= set(range(S + step + 1 - 256, S + step + 1))
+    assert bsa.get_device_error() == 0
