@@ -194,7 +194,8 @@ bsa_status bsa_kv4_evict(const bsa_kv4_evict_args* a, bsa_stream stream) {
     bsa_status s = check_evict(a);
     if (s != BSA_OK) return s;
     if (!a->lens || !a->new_lens || !a->index) return bad("lens, new_lens and index must be non-null");
-    if (a->new_lens == a->lens) return bad("new_lens must not be lens");
+    // (other heads' CTAs still read the lengths)
+    if (a->new_lens == a->lens || a->new_lens == a->seen) return bad("new_lens must be neither lens nor seen");
     if (!aligned4(a->lens) || !aligned4(a->seen) || !aligned4(a->new_lens) || !aligned4(a->index))
       return bad("lens, seen, new_lens and index must be 4-byte aligned");
     if (!aligned16(a->k_values) || !aligned16(a->v_values)) return bad("values must be 16-byte aligned");

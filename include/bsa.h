@@ -440,7 +440,7 @@ typedef struct {
   const int32_t* seen;     /* device int32 [B], or NULL (= lens): tokens each sequence has had in all */
   int64_t keep;            /* slots to keep per sequence and head, >= 1 */
   int64_t recent;          /* tokens at positions >= seen[b] - recent are kept before all others, 0 <= recent <= keep */
-  int32_t* new_lens;       /* device int32 [B], written: min(lens[b], keep); not the same memory as lens */
+  int32_t* new_lens;       /* device int32 [B], written: min(lens[b], keep); not the same memory as lens or seen */
   int32_t* index;          /* device int32 [B, Hkv, keep], written: the slot that the token now in slot r had before,
                               -1 past new_lens[b] */
   void* k_values;          /* bf16 [B, Hkv, keep, D] or NULL: what the kept slots hold (0 past new_lens[b]) */

@@ -174,3 +174,10 @@ def test_the_binding_refuses_tensors_on_the_cpu():
     q = torch.zeros((1, 2, 128, 64), dtype=torch.bfloat16)
     with pytest.raises(ValueError, match="CUDA"):
         bsa.key_weights(q, q, torch.zeros((1, 2, 128)), None)
+
+
+def test_evict_refuses_to_write_the_lengths_over_those_it_reads():
+    abi = _abi()
+    L = abi.lib()
+    a = evict_args(abi, seen=32)             # (where new_lens is)
+    assert L.bsa_kv4_evict(C.byref(a), None) == abi.INVALID_ARG and b"seen" in L.bsa_last_error()
