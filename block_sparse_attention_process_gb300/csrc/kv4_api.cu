@@ -97,7 +97,12 @@ bsa_status check_fwd_tensors(const bsa_kv4_fwd_args* a) {
   if (!aligned16(a->q) || !aligned16(a->o)) return bad("q and o must be 16-byte aligned");
   if (!aligned4(a->lse) || !aligned4(a->lens) || !aligned4(a->q_lens)) return bad("lse, lens and q_lens must be 4-byte aligned");
   bsa_status s = check_strides(a->q_stride);
-  return s != BSA_OK ? s : check_strides(a->o_stride);
+  if (s == BSA_OK) s = check_strides(a->o_stride);
+  if (s != BSA_OK) return s;
+  const int64_t rows[] = {a->cache.B, a->Hq, a->T};
+  for (int i = 0; i < 3; ++i)
+    if (rows[i] > 1 && a->o_stride[i] == 0) return bad("o must not have several rows in one place");
+  return BSA_OK;
 }
 
 bsa_status check_evict(const bsa_kv4_evict_args* a) {

@@ -404,7 +404,7 @@ typedef struct {
   bsa_kv4_cache cache;
   const void* q;           /* bf16, element (b, h, t, d) at b*q_stride[0] + h*q_stride[1] + t*q_stride[2] + d;
                               16-byte aligned, strides multiples of 8 */
-  void* o;                 /* bf16, written, addressed likewise through o_stride */
+  void* o;                 /* bf16, written, addressed likewise through o_stride (no two rows in one place) */
   float* lse;              /* fp32 [B, Hq, T], written */
   int64_t q_stride[3], o_stride[3];
   int32_t Hq;

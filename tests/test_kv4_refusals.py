@@ -181,3 +181,16 @@ def test_evict_refuses_to_write_the_lengths_over_those_it_reads():
     L = abi.lib()
     a = evict_args(abi, seen=32)             # (where new_lens is)
     assert L.bsa_kv4_evict(C.byref(a), None) == abi.INVALID_ARG and b"seen" in L.bsa_last_error()
+
+
+@pytest.mark.parametrize("axis", [0, 1, 2])
+def test_fwd_refuses_outputs_of_several_rows_in_one_place(axis):
+    abi = _abi()
+    L = abi.lib()
+    strides = [512, 128, 128]
+    strides[axis] = 0
+    a = fwd_args(abi, o_stride=(C.c_int64 * 3)(*strides))
+    if axis == 2:
+        a.T = 2
+        a.o_stride[1] = 256
+    assert L.bsa_kv4_fwd(C.byref(a), None) == abi.INVALID_ARG and b"one place" in L.bsa_last_error()
