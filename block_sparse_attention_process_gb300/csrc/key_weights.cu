@@ -37,11 +37,14 @@
 // order.  Neither kernel is started early (a CTA that waits for its predecessor
 // holds the place of one that works: 203 us).
 //
-// GQA 32/8 causal 8192, D = 128: 194 us for 279 GFLOP, 1.44 PFLOP/s; the products
+// GQA 32/8 causal 8192, D = 128: 194 us for 279 GFLOP, 1.44 PFLOP/s, in a run of tens of
+// calls; 217 us at the clocks that hundreds in a row sustain.  The products
 // alone would take 129 us at 512 + 64 cycles an item, the exponentials 115.  What
 // is left is the barriers between the roles, ~800 cycles of issuer per two items
 // and ~1,590 of warpgroup per three.  Two prompts of 4096 with a local
 // window of 1024, 16 heads, D = 64: 36 us, of which 11 are the two small kernels.
+// With a soft cap 1342 and 204 us: three special functions a score in place of one, the
+// logsumexps read per column, and registers that spill (96 a thread).
 #include <cmath>
 
 #include "internal.h"
@@ -514,7 +517,7 @@ __global__ void __launch_bounds__(kThreads, 1)
       if (lane == 0) mbar_arrive(&s.k_full[kb]);
     }
   } else {
-    // ------------------------------------------------ exponentials: warpgroup w takes items w, w + 4, ...
+    // ------------------------------------------------ exponentials: warpgroup w takes items w, w + 3, ...
     const int w = (warp - kEwWarp0) >> 2, quarter = warp & 3;
     const int r = quarter * 32 + lane;  // key of the tile == tensor-memory lane
     const uint32_t taddr = BSA_TMEM(tmem + w * 128 + (static_cast<uint32_t>(quarter * 32) << 16), 128u, p.err);

@@ -6,11 +6,12 @@
 // 2^-15 (relative) away from one and rounds right, and a tie, a number of few
 // bits, comes out exactly.
 //
-// HBM-bound: 4 D bytes read and D + D/4 of codes and scales (+ 4 D of values)
+// HBM-bound: 4 D bytes read and D + D/8 of codes and scales (+ 4 D of values)
 // written per token and head.  A row takes D/8 lanes: for K each lane holds
 // 8 consecutive elements, which are one 4-byte word of codes; for V its two
 // quads of elements 32 apart, likewise one word.  4 x 8 x 8192 rows of 128 with
-// their values take 63 us, 72% of the copy bandwidth; the rest is issue slots:
+// their values take 63 us, 72% of the copy bandwidth, and 58 without values, 44% of
+// it.  The rest is instructions (68% of the issue slots) and latency:
 // 98 us with a true division per element, 72 with ties found by their remainder
 // and maxima one element at a time.  One row a lane: two in flight measured
 // slower (fewer warps fit).

@@ -19,19 +19,21 @@
 // row's largest magnitude to [2^14, 2^15); elements 2^-24 times smaller start
 // to lose bits); a probability times its value scale is rounded to fp16.
 //
-// p s in fp16: 11 bits, where the outputs have 8; more would take two of every second
-// product.  Every group of 32 channels has a base of its own, the exponent of the
-// largest scale among a warp's first keys, and raised by it its scales are good while they
-// lie in [2^-7, 2), 2^-5 to 2^3 of the base's own.  A row's reference R lies 2^10 below the
-// largest score among keys whose scales are all good, and moves when that grows by more than 4 (log2
-// units); l = sum 2^(s_j - R) stays in fp32.  So the largest product of every group is in [2^3, 2^15) and the
-// products below 2^-14, which lose up to 2^-25 each, together lose less than 2^-11 of the
-// sum over up to 2^17 keys of a warp.
-// Other keys (of values 0, NaN, or much smaller or larger) take part in the same products
-// but do not move R, unless a score of theirs is 2^24 above it: then, or where a
-// product would leave fp16, or where a group of zeros gets its first values late, a step
-// (from then on every step of the part, if R had to follow such a key) sorts its
-// products into classes of 28 binades, a matrix product each, added up in fp32.
+// p s in fp16: 11 bits, where the outputs have 8; more would take two of every
+// second product.  Every group of 32 channels has a base of its own, the exponent
+// of the largest scale among a warp's first keys; raised by it, its scales are
+// good while they lie in [2^-7, 2), 2^-5 to 2^3 of the base's own.  A row's
+// reference R lies 2^10 below the largest score among keys whose scales are all
+// good, and moves when that grows by more than 4 (log2 units); l = sum 2^(s_j - R)
+// stays in fp32.  So the largest product of every group is in [2^3, 2^15), and the
+// products below 2^-14, which lose up to 2^-25 each, together lose less than 2^-11
+// of the sum over up to 2^17 keys of a warp.
+// Other keys (of values 0, NaN, or much smaller or larger) take part in the same
+// products but do not move R, unless a score of theirs is 2^24 above it: then, or
+// where a product would leave fp16, or where a group of zeros gets its first
+// values late, a step (from then on every step of the part, if R had to follow
+// such a key) sorts its products into classes of 28 binades, a matrix product
+// each, added up in fp32.
 //
 // Row tiles are of 8, the product's own width.  Tiles of 16 (two products on
 // the same codes) halve the passes over the cache when a head has 9 or more
@@ -53,14 +55,16 @@
 //
 // Four warps take 32 keys of a tile each, as two products side by side; the
 // warps take turns in bringing tiles in by bulk copies through a ring of
-// stages.  Most of its instructions are the ANDs, subtractions and packs around
-// the products; the step therefore exists three times, for keys that every row sees (without predicates:
-// 145 to 134 us below), for others, and class by class, in a loop of its own (in the other's loop it
-// took registers: 149 us for 140).
-// 64 sequences of 8191 keys on 8 heads, 32 q heads: 140 us, 605 MB at 4.3 TB/s (eight warps of 16
-// keys, one of them loading: 200 us); 144 if one group of all values is 0, 220 if every 64th
-// value is, 330 class by class.  One sequence of 65,536 keys: 31 us, 75 MB; about 10 of
-// them are the join, whose time is latency.
+// stages.  At three warps a scheduler what bounds it is the latency between
+// their instructions (60% of the issue slots are taken, 53% of the ALU's).  Most
+// of these are the ANDs, subtractions and packs around the products; the step
+// therefore exists three times: for keys that every row sees (without predicates:
+// 145 to 134 us below), for others, and class by class, in a loop of its own (in
+// the others' loop it took registers: 149 us for 140).
+// 64 sequences of 8191 keys on 8 heads, 32 q heads: 140 us, 605 MB at 4.3 TB/s
+// (eight warps of 16 keys, one of them loading: 200 us); 144 if one group of all
+// values is 0, 220 if every 64th value is, 330 class by class.  One sequence of
+// 65,536 keys: 31 us, 75 MB; about 10 of them are the join, whose time is latency.
 #include <cmath>
 #include <type_traits>
 

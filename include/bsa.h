@@ -411,7 +411,7 @@ typedef struct {
   int64_t T;               /* new tokens per sequence (1 in a plain decode step) */
   const int32_t* lens;     /* device int32 [B]: keys each sequence holds, the new tokens' own included */
   const int32_t* q_lens;   /* device int32 [B], or NULL (= T): tokens at or past q_lens[b] are padding */
-  float softmax_scale;     /* NaN selects 1/sqrt(D) */
+  float softmax_scale;     /* NaN selects 1/sqrt(D); over the cap, if any, and times any |q| it stays below 2^110 */
   float logits_soft_cap;   /* as in bsa_fwd_args */
   const float* sinks;      /* as in bsa_fwd_args */
   int32_t num_sinks, sinks_per_kv_head;
