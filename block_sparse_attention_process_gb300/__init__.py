@@ -19,6 +19,16 @@ After a prompt, token by token over a cache held in 4 bits:
     lens, seen = lens + 1, seen + 1
     o1, lse1 = kv4_fwd(q1, cache, lens, accumulate=True)
     lens, index = kv4_evict(cache, lens, keep, recent=recent, seen=seen)
+
+Or over a cache in pages, which sequences take and give back as they grow and end, attending to all of it
+or to the pages that promise the largest scores:
+
+    cache = PagedCache.empty(pages, Hkv, page, D)
+    table, free, used = paged_table(pages, B, M)
+    lens, used, slots = paged_resize(table, free, used, lens, new_lens, page, T)
+    paged_append(cache, k, v, slots)                         # k, v [B,Hkv,T,D]
+    o, lse = paged_fwd(q, cache, table, lens)
+    o, lse = paged_fwd(q, cache, table, lens, select=paged_select(q, cache, table, lens, keep))
 """
 from __future__ import annotations
 
@@ -35,6 +45,7 @@ from ._abi import BsaError, check
 
 __all__ = ["mask_compile", "MaskInfo", "fwd", "fwd_partial", "fwd_merge", "bwd", "bwd_noalloc", "bwd_rowsum",
            "bwd_dkv", "bwd_dq", "key_weights", "KV4Cache", "kv4_append", "kv4_fwd", "kv4_evict",
+           "PagedCache", "paged_table", "paged_resize", "paged_append", "paged_select", "paged_fwd",
            "get_device_error", "set_wait_limit_ns", "debug_wait_timeout", "debug_selfcheck", "version", "BsaError",
            "library_path"]
 
@@ -563,6 +574,172 @@ def kv4_evict(cache: KV4Cache, lens: torch.Tensor, keep: int, *, recent: int = 0
             caches + pack(*head, new_lens.data_ptr(), slots.data_ptr(), kv.data_ptr() if values else 0,
                           vv.data_ptr() if values else 0, 0 if ws is None else ws.data_ptr(), need), handle), "bsa_kv4_evict")
     return (new_lens, slots, kv, vv) if values else (new_lens, slots)
+
+
+def _pages(name: str, t: torch.Tensor, index: int):
+    """Strides (page, head, token) of a cache tensor [pages, Hkv, page, D]."""
+    strides = _rows(name, t, index)
+    if min(strides) < 0 or any(n > 1 and s == 0 for n, s in zip(t.shape, strides)):
+        raise ValueError(f"{name} must not have several rows in one place")
+    return strides
+
+
+class PagedCache:
+    """A key/value cache in pages (bsa_paged_cache): the buffers, which the caller owns.
+
+    k, v: bf16 [pages, Hkv, page, D], any strides with a contiguous last axis (e.g. [pages, page, Hkv, D]
+    transposed); bounds: bf16 [pages, Hkv, 2, D], an upper and a lower bound of each channel of a page's keys, which
+    ``paged_append`` keeps and ``paged_select`` reads, or None.  page is 16, 32, 64, 128 or 256."""
+
+    __slots__ = ("k", "v", "bounds", "pages", "Hkv", "page", "D", "device", "index", "_c")
+
+    def __init__(self, k: torch.Tensor, v: torch.Tensor, bounds: Optional[torch.Tensor] = None):
+        index = k.get_device()
+        if index < 0 or k.dim() != 4:
+            raise ValueError("k must be a CUDA bfloat16 tensor [pages, Hkv, page, D]")
+        if v.shape != k.shape:
+            raise ValueError("v must have k's shape")
+        P, H, page, D = k.shape
+        self._c = _abi.PAGED_CACHE.pack(
+            k.data_ptr(), v.data_ptr(), *_pages("k", k, index), *_pages("v", v, index),
+            0 if bounds is None else _need("bounds", bounds, torch.bfloat16, index, (P, H, 2, D)), P, H, D, page)
+        self.k, self.v, self.bounds = k, v, bounds
+        self.pages, self.Hkv, self.page, self.D, self.device, self.index = P, H, page, D, k.device, index
+
+    @classmethod
+    def empty(cls, pages: int, Hkv: int, page: int, D: int, device="cuda", bounds: bool = True) -> "PagedCache":
+        """A cache without tokens; without ``bounds`` it keeps none."""
+        def new(*shape):
+            return torch.zeros(shape, dtype=torch.bfloat16, device=device)
+        return cls(new(pages, Hkv, page, D), new(pages, Hkv, page, D), new(pages, Hkv, 2, D) if bounds else None)
+
+
+def paged_table(pages: int, B: int, M: int, device="cuda"):
+    """(table int32 [B, M], free int32 [pages], used int32 [1]) of a cache of `pages` pages that holds no sequence yet."""
+    return (torch.full((B, M), -1, dtype=torch.int32, device=device), torch.arange(pages, dtype=torch.int32, device=device),
+            torch.zeros((1,), dtype=torch.int32, device=device))
+
+
+def _table(table: torch.Tensor, B: int, index: int) -> int:
+    if table.dim() != 2:
+        raise ValueError("table must be [B, M]")
+    return _need("table", table, torch.int32, index, (B, table.shape[1]))
+
+
+def paged_resize(table: torch.Tensor, free: torch.Tensor, used: torch.Tensor, lens: torch.Tensor, new_lens: torch.Tensor,
+                 page: int, T: int, *, stream=None):
+    """bsa_paged_resize: sequences of ``lens`` tokens get ``new_lens`` (int32 [B], 0 for one that has ended); pages go back
+    to the free stack and from it into the rows of ``table`` (int32 [B, M]) and ``free`` (int32 [pages], entries used[0] ..
+    are free), both in place.  -> (lens int32 [B] that they now have, used int32 [1], slots int32 [B, T]: where the tokens
+    lens[b] + i go, -1 behind the last).  Where the pages do not suffice a sequence, and every later one that needs
+    any, keeps its length."""
+    index = table.get_device()
+    if index < 0:
+        raise ValueError("table must be a contiguous CUDA int32 tensor")
+    B = table.shape[0]
+    head = (_table(table, B, index), _need("free", free, torch.int32, index, (free.numel(),)),
+            _need("used", used, torch.int32, index, (1,)), _lens("lens", lens, B, index), _lens("new_lens", new_lens, B, index))
+    ctx, handle = _place(table.device, index, stream)
+    with ctx:
+        out = torch.empty((B,), dtype=torch.int32, device=table.device)
+        used_out = torch.empty((1,), dtype=torch.int32, device=table.device)
+        slots = torch.empty((B, max(T, 0)), dtype=torch.int32, device=table.device)
+        check(_abi.lib().bsa_paged_resize(
+            _abi.PAGED_RESIZE.pack(*head, out.data_ptr(), used_out.data_ptr(), slots.data_ptr(), B, table.shape[1], T, free.numel(),
+                                   page), handle), "bsa_paged_resize")
+    return out, used_out, slots
+
+
+def paged_append(cache: PagedCache, k: torch.Tensor, v: torch.Tensor, slots: torch.Tensor, *, stream=None) -> None:
+    """bsa_paged_append: tokens of k, v (bf16 [B,Hkv,T,D], any strides with a contiguous last axis) into ``slots`` (int32
+    [B, T] on the device, negative: padding), as ``paged_resize`` gives them; the bounds of their pages are
+    renewed if the cache has any.  Without bounds the slots may come in any order."""
+    index = cache.index
+    B, H, T, D = k.shape if k.dim() == 4 else (0, 0, 0, 0)
+    if (H, D) != (cache.Hkv, cache.D) or v.shape != k.shape:
+        raise ValueError("k and v must both be [B, Hkv, T, D] with the cache's Hkv and D")
+    ks, vs = _rows("k", k, index), _rows("v", v, index)
+    args = cache._c + _abi.PAGED_APPEND_REST.pack(k.data_ptr(), v.data_ptr(), *ks, *vs,
+                                                  _need("slots", slots, torch.int32, index, (B, T)), B, T)
+    ctx, handle = _place(cache.device, index, stream)
+    with ctx:
+        check(_abi.lib().bsa_paged_append(args, handle), "bsa_paged_append")
+
+
+def paged_select(q: torch.Tensor, cache: PagedCache, table: torch.Tensor, lens: torch.Tensor, keep: int, *, first: int = 1,
+                 recent: int = 1, q_lens: Optional[torch.Tensor] = None, stream=None) -> torch.Tensor:
+    """bsa_paged_select: for every new token and key head the ``keep`` pages with the largest bound on q.k, the ``first``
+    and the last ``recent`` ones that it sees among them.  q bf16 [B,Hq,T,D] (any strides with a contiguous last axis),
+    lens int32 [B] with the new tokens' own keys included -> int32 [B,Hkv,T,keep], numbers of the
+    sequence's pages in increasing order, -1 behind the last; for ``paged_fwd``'s ``select``."""
+    dev, index = cache.device, cache.index
+    qs = _rows("q", q, index)
+    B, Hq, T, D = q.shape
+    if D != cache.D:
+        raise ValueError("q must be [B, Hq, T, D] with the cache's D")
+    if lens is None:
+        raise ValueError("lens is missing")
+    head = (q.data_ptr(), *qs, _table(table, B, index), _lens("lens", lens, B, index), _lens("q_lens", q_lens, B, index))
+    M, pack = table.shape[1], _abi.PAGED_SELECT_REST.pack
+    tail = (B, Hq, M, T, keep, first, recent)
+    need = _workspace_size("bsa_paged_select", (index, cache.Hkv, D, cache.page, cache.pages, cache.bounds is None, *tail),
+                           cache._c + pack(*head, 0, *tail, 0, 0))
+    ctx, handle = _place(dev, index, stream)
+    with ctx:
+        out = torch.empty((B, cache.Hkv, T, keep), dtype=torch.int32, device=dev)
+        ws = _workspace(need, dev)
+        check(_abi.lib().bsa_paged_select(cache._c + pack(*head, out.data_ptr(), *tail, 0 if ws is None else ws.data_ptr(), need),
+                                          handle), "bsa_paged_select")
+    return out
+
+
+def paged_fwd(q: torch.Tensor, cache: PagedCache, table: torch.Tensor, lens: torch.Tensor, *,
+              q_lens: Optional[torch.Tensor] = None, select: Optional[torch.Tensor] = None, local_left: Optional[int] = None,
+              chunk: Optional[int] = None, o: Optional[torch.Tensor] = None, lse: Optional[torch.Tensor] = None,
+              softmax_scale: Optional[float] = None, logits_soft_cap: Optional[float] = None,
+              sinks: Optional[torch.Tensor] = None, stream=None):
+    """bsa_paged_fwd: attention of T new tokens over their sequences' pages.  q bf16 [B,Hq,T,D] (any strides with a
+    contiguous last axis), table int32 [B, M], lens int32 [B] on the device: keys held, the new tokens' own included
+    -> (o bf16 [B,Hq,T,D], lse fp32 [B,Hq,T]).  ``q_lens``: new tokens per sequence (default T).  ``local_left`` or
+    ``chunk``: the local or chunked causal mask instead of the causal one.  ``select`` (int32 [B,Hkv,T,keep] from
+    ``paged_select``): only the pages listed for each query."""
+    dev, index = cache.device, cache.index
+    qs = _rows("q", q, index)
+    B, Hq, T, D = q.shape
+    if D != cache.D:
+        raise ValueError("q must be [B, Hq, T, D] with the cache's D")
+    if lens is None:
+        raise ValueError("lens is missing")
+    if local_left is not None and chunk is not None:
+        raise ValueError("local_left and chunk exclude each other")
+    kind = _abi.MASK_LOCAL if local_left is not None else _abi.MASK_CHUNKED_CAUSAL if chunk is not None else _abi.MASK_CAUSAL
+    keep = 0
+    if select is not None:
+        if select.dim() != 4 or select.shape[3] < 1:
+            raise ValueError("select must be [B, Hkv, T, keep]")
+        keep = select.shape[3]
+    sp, sn, skv = (0, 0, 0) if sinks is None else _sink_fields(sinks, cache.Hkv)
+    if sinks is not None and sinks.device != dev:
+        raise ValueError(f"sinks is on {sinks.device}, the call's other tensors are on {dev}")
+    M = _table(table, B, index) and table.shape[1]
+    ctx, handle = _place(dev, index, stream)
+    with ctx:
+        if o is None:
+            o = torch.empty((B, Hq, T, D), dtype=torch.bfloat16, device=dev)
+        elif o.shape != q.shape:
+            raise ValueError("o must have q's shape")
+        if lse is None:
+            lse = torch.empty((B, Hq, T), dtype=torch.float32, device=dev)
+        head = (q.data_ptr(), o.data_ptr(), _need("lse", lse, torch.float32, index, (B, Hq, T)), *qs, *_rows("o", o, index),
+                table.data_ptr(), _lens("lens", lens, B, index), _lens("q_lens", q_lens, B, index),
+                0 if select is None else _need("select", select, torch.int32, index, (B, cache.Hkv, T, keep)), B, Hq, M, T, keep,
+                kind, -1 if local_left is None else local_left, chunk or 0, math.nan if softmax_scale is None else softmax_scale,
+                logits_soft_cap or 0.0, sp, sn, skv)
+        pack = _abi.PAGED_FWD_REST.pack
+        need = _workspace_size("bsa_paged_fwd", (index, B, cache.Hkv, D, cache.page, Hq, M, T, keep), cache._c + pack(*head, 0, 0))
+        ws = _workspace(need, dev)
+        check(_abi.lib().bsa_paged_fwd(cache._c + pack(*head, 0 if ws is None else ws.data_ptr(), need), handle), "bsa_paged_fwd")
+    return o, lse
 
 
 def get_device_error(stream=None) -> int:

@@ -110,7 +110,39 @@ class Kv4EvictArgs(C.Structure):
                 ("workspace_bytes", C.c_size_t)]
 
 
-# The kv4 calls are made once a token, so their arguments are packed with
+class PagedCache(C.Structure):
+    _fields_ = [("k", C.c_void_p), ("v", C.c_void_p), ("k_stride", C.c_int64 * 3), ("v_stride", C.c_int64 * 3),
+                ("bounds", C.c_void_p), ("pages", C.c_int64), ("Hkv", C.c_int32), ("D", C.c_int32), ("page", C.c_int32)]
+
+
+class PagedResizeArgs(C.Structure):
+    _fields_ = [("table", C.c_void_p), ("free_pages", C.c_void_p), ("used", C.c_void_p), ("lens", C.c_void_p),
+                ("new_lens", C.c_void_p), ("lens_out", C.c_void_p), ("used_out", C.c_void_p), ("slots", C.c_void_p),
+                ("B", C.c_int32), ("M", C.c_int64), ("T", C.c_int64), ("pages", C.c_int64), ("page", C.c_int32)]
+
+
+class PagedAppendArgs(C.Structure):
+    _fields_ = [("cache", PagedCache), ("k", C.c_void_p), ("v", C.c_void_p), ("src_k_stride", C.c_int64 * 3),
+                ("src_v_stride", C.c_int64 * 3), ("slots", C.c_void_p), ("B", C.c_int32), ("T", C.c_int64)]
+
+
+class PagedSelectArgs(C.Structure):
+    _fields_ = [("cache", PagedCache), ("q", C.c_void_p), ("q_stride", C.c_int64 * 3), ("table", C.c_void_p),
+                ("lens", C.c_void_p), ("q_lens", C.c_void_p), ("index", C.c_void_p), ("B", C.c_int32), ("Hq", C.c_int32),
+                ("M", C.c_int64), ("T", C.c_int64), ("keep", C.c_int64), ("first", C.c_int64), ("recent", C.c_int64),
+                ("workspace", C.c_void_p), ("workspace_bytes", C.c_size_t)]
+
+
+class PagedFwdArgs(C.Structure):
+    _fields_ = [("cache", PagedCache), ("q", C.c_void_p), ("o", C.c_void_p), ("lse", C.c_void_p),
+                ("q_stride", C.c_int64 * 3), ("o_stride", C.c_int64 * 3), ("table", C.c_void_p), ("lens", C.c_void_p),
+                ("q_lens", C.c_void_p), ("select", C.c_void_p), ("B", C.c_int32), ("Hq", C.c_int32), ("M", C.c_int64),
+                ("T", C.c_int64), ("keep", C.c_int64), ("kind", C.c_int32), ("local_left", C.c_int64), ("chunk", C.c_int64),
+                ("softmax_scale", C.c_float), ("logits_soft_cap", C.c_float), ("sinks", C.c_void_p), ("num_sinks", C.c_int32),
+                ("sinks_per_kv_head", C.c_int32), ("workspace", C.c_void_p), ("workspace_bytes", C.c_size_t)]
+
+
+# The kv4 and paged calls are made once a token, so their arguments are packed with
 # struct (a third of the time a ctypes.Structure of as many fields takes): the
 # cache, which every call begins with, and what follows it.
 KV4_CACHE = struct.Struct("@6P3iq")
@@ -119,6 +151,14 @@ KV4_FWD_REST = struct.Struct("@3P6qiqPPffPiiiPN")
 KV4_EVICT_REST = struct.Struct("@2P2q5PN")
 for _s, _rest in ((Kv4AppendArgs, KV4_APPEND_REST), (Kv4FwdArgs, KV4_FWD_REST)):
     assert KV4_CACHE.size + _rest.size == C.sizeof(_s)
+PAGED_CACHE = struct.Struct("@2P6qPq3i0q")
+PAGED_RESIZE = struct.Struct("@8Pi3qi0q")
+PAGED_APPEND_REST = struct.Struct("@2P6qPiq")
+PAGED_SELECT_REST = struct.Struct("@P3q4P2i5qPN")
+PAGED_FWD_REST = struct.Struct("@3P6q4P2i3qi2q2fP2iPN")
+assert PAGED_RESIZE.size == C.sizeof(PagedResizeArgs)
+for _s, _rest in ((PagedAppendArgs, PAGED_APPEND_REST), (PagedSelectArgs, PAGED_SELECT_REST), (PagedFwdArgs, PAGED_FWD_REST)):
+    assert PAGED_CACHE.size + _rest.size == C.sizeof(_s)
 assert 2 * KV4_CACHE.size + KV4_EVICT_REST.size == C.sizeof(Kv4EvictArgs)
 
 
@@ -142,6 +182,12 @@ SIGNATURES = {
     "bsa_kv4_fwd_workspace": (C.c_int, [C.c_void_p, C.POINTER(C.c_size_t)]),
     "bsa_kv4_evict": (C.c_int, [C.c_void_p, C.c_void_p]),
     "bsa_kv4_evict_workspace": (C.c_int, [C.c_void_p, C.POINTER(C.c_size_t)]),
+    "bsa_paged_resize": (C.c_int, [C.c_void_p, C.c_void_p]),
+    "bsa_paged_append": (C.c_int, [C.c_void_p, C.c_void_p]),
+    "bsa_paged_select": (C.c_int, [C.c_void_p, C.c_void_p]),
+    "bsa_paged_select_workspace": (C.c_int, [C.c_void_p, C.POINTER(C.c_size_t)]),
+    "bsa_paged_fwd": (C.c_int, [C.c_void_p, C.c_void_p]),
+    "bsa_paged_fwd_workspace": (C.c_int, [C.c_void_p, C.POINTER(C.c_size_t)]),
     "bsa_get_device_error": (C.c_int, [C.c_void_p, C.POINTER(C.c_uint32)]),
     "bsa_set_wait_limit_ns": (C.c_int, [C.c_uint64]),
     "bsa_debug_wait_timeout": (C.c_int, [C.c_void_p]),

@@ -1,0 +1,35 @@
+// The cache in pages: what its kernels share.
+#pragma once
+#include <cstdint>
+
+#include "bsa.h"
+#include "internal.h"
+#include "ptx.cuh"
+
+namespace bsa {
+
+// A device-side length brought into [0, hi]; one outside sets the bounds bit.
+__device__ __forceinline__ int32_t paged_len(int32_t n, int64_t hi, uint32_t* err) {
+  if (n < 0 || n > hi) {
+    if (err) atomicOr(err, DEV_ERR_BOUNDS);
+    return n < 0 ? 0 : static_cast<int32_t>(hi);
+  }
+  return n;
+}
+
+// 2^max(floor(log2 top) - bits, -100) and its inverse, of 0 <= top < 2^100; both are normal numbers.
+__device__ __forceinline__ void unit_of(float top, int bits, float& unit, float& inverse) {
+  const int e = max(static_cast<int>(__float_as_uint(top) >> 23) - 127 - bits, -100);
+  unit = __uint_as_float(static_cast<uint32_t>(127 + e) << 23);
+  inverse = __uint_as_float(static_cast<uint32_t>(127 - e) << 23);
+}
+constexpr float kUsualTop = 0x1p100f;  // keys (or queries) below this have bounds (or codes)
+
+// log2 of a page size (16 .. 256)
+inline int page_shift(int32_t page) {
+  int s = 0;
+  while ((1 << s) < page) ++s;
+  return s;
+}
+
+}  // namespace bsa

@@ -1,0 +1,222 @@
+// Keys and values into the slots of the cache in pages, and the bounds of the pages' keys.
+//
+// Without bounds a row (one token and head) is D/8 lanes of 16 bytes, wherever its slot is.
+//
+// With bounds a CTA takes the tokens of one sequence and head that go into one page: the slots of a sequence's
+// tokens follow each other, so token t lies at place (o + t) % page, o being the place of token 0, and
+// unit u holds tokens u * page - o .. (u + 1) * page - o - 1.  It writes them, reads the keys that the page held before them, and
+// has every key of the page in registers then: maxima and minima are exact in any order, so the bounds need no
+// atomics, no second pass over the new keys, and come out the same each time.
+#include <algorithm>
+
+#include "paged.cuh"
+
+namespace bsa {
+namespace {
+
+constexpr int kThreads = 256;
+
+struct AppendParams {
+  bsa_paged_cache c;
+  const __nv_bfloat16 *k, *v;
+  int64_t ks[3], vs[3];
+  const int32_t* slots;
+  int32_t B, shift;
+  int64_t T;
+  int64_t units;  // of one sequence and head
+  uint32_t* err;
+};
+
+__device__ __forceinline__ int64_t page_at(const int64_t (&stride)[3], int32_t slot, int32_t shift, int32_t h) {
+  return (slot >> shift) * stride[0] + h * stride[1] + (slot & ((1 << shift) - 1)) * stride[2];
+}
+
+template <int D>
+__global__ void __launch_bounds__(kThreads) append_rows_kernel(const __grid_constant__ AppendParams p) {
+  constexpr int kLanes = D / 8;
+  griddep_launch_dependents();
+  griddep_wait();
+  const int u = threadIdx.x % kLanes, sub = threadIdx.x / kLanes;
+  const int64_t rows = p.B * p.T * p.c.Hkv, limit = p.c.pages << p.shift;
+  // rows in order of (b, h, t)
+  for (int64_t r = static_cast<int64_t>(blockIdx.x) * (kThreads / kLanes) + sub; r < rows;
+       r += static_cast<int64_t>(gridDim.x) * (kThreads / kLanes)) {
+    const int64_t bh = r / p.T, t = r - bh * p.T;
+    const int32_t b = static_cast<int32_t>(bh / p.c.Hkv), h = static_cast<int32_t>(bh - static_cast<int64_t>(b) * p.c.Hkv);
+    const int32_t slot = p.slots[b * p.T + t];
+    if (slot < 0) continue;
+    if (slot >= limit) {
+      if (u == 0 && p.err) atomicOr(p.err, DEV_ERR_BOUNDS);
+      continue;
+    }
+    const uint4 k = __ldcs(reinterpret_cast<const uint4*>(p.k + b * p.ks[0] + h * p.ks[1] + t * p.ks[2] + 8 * u));
+    const uint4 v = __ldcs(reinterpret_cast<const uint4*>(p.v + b * p.vs[0] + h * p.vs[1] + t * p.vs[2] + 8 * u));
+    *reinterpret_cast<uint4*>(static_cast<__nv_bfloat16*>(p.c.k) + page_at(p.c.k_stride, slot, p.shift, h) + 8 * u) = k;
+    *reinterpret_cast<uint4*>(static_cast<__nv_bfloat16*>(p.c.v) + page_at(p.c.v_stride, slot, p.shift, h) + 8 * u) = v;
+  }
+}
+
+__device__ __forceinline__ float lo_f(uint32_t w) { return __uint_as_float(w << 16); }
+__device__ __forceinline__ float hi_f(uint32_t w) { return __uint_as_float(w & 0xFFFF0000u); }
+
+// Running maximum and minimum of 8 channels, and the largest magnitude as bf16 bits (NaN is above every number there).
+struct Range {
+  float hi[8], lo[8];
+  uint32_t top;
+  __device__ __forceinline__ void clear() {
+#pragma unroll
+    for (int i = 0; i < 8; ++i) {
+      hi[i] = -INFINITY;
+      lo[i] = INFINITY;
+    }
+    top = 0;
+  }
+  __device__ __forceinline__ void add(const uint4& x) {
+    const uint32_t w[4] = {x.x, x.y, x.z, x.w};
+    uint32_t m = 0;
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+      hi[2 * i] = fmaxf(hi[2 * i], lo_f(w[i]));
+      hi[2 * i + 1] = fmaxf(hi[2 * i + 1], hi_f(w[i]));
+      lo[2 * i] = fminf(lo[2 * i], lo_f(w[i]));
+      lo[2 * i + 1] = fminf(lo[2 * i + 1], hi_f(w[i]));
+      m = __vmaxu2(m, w[i] & 0x7FFF7FFFu);
+    }
+    top = max(top, max(m & 0xFFFFu, m >> 16));
+  }
+};
+
+template <int D>
+__global__ void __launch_bounds__(kThreads) append_bounds_kernel(const __grid_constant__ AppendParams p) {
+  constexpr int kLanes = D / 8, kSubs = kThreads / kLanes, kWarps = kThreads / 32;
+  __shared__ float hi[kWarps][D], lo[kWarps][D];
+  __shared__ uint32_t top[kWarps];
+  griddep_launch_dependents();
+  griddep_wait();
+  const int u = threadIdx.x % kLanes, sub = threadIdx.x / kLanes, lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+  const int32_t page = 1 << p.shift;
+  const int64_t limit = p.c.pages << p.shift;
+  const int64_t bh = blockIdx.x / p.units, unit = blockIdx.x - bh * p.units;
+  const int32_t b = static_cast<int32_t>(bh / p.c.Hkv), h = static_cast<int32_t>(bh - static_cast<int64_t>(b) * p.c.Hkv);
+  const int32_t* slots = p.slots + b * p.T;
+  const int32_t s0 = slots[0];
+  const int32_t o = s0 < 0 ? 0 : s0 & (page - 1);
+  const int64_t t0 = unit * page - o;  // token of the page's place 0
+  if (t0 >= p.T) return;
+  // the page is that of the unit's first token
+  const int32_t first = slots[max(t0, static_cast<int64_t>(0))];
+  const int32_t begin = t0 < 0 ? o : 0;  // its place
+  const int32_t page0 = first < 0 || first >= limit ? -1 : first - begin;  // slot of place 0 (another place: nothing fits)
+  const bool good = page0 >= 0 && (page0 & (page - 1)) == 0;
+  Range r;
+  r.clear();
+  int32_t last = -1;
+  bool wrong = false;
+  const __nv_bfloat16* src_k = p.k + b * p.ks[0] + h * p.ks[1] + 8 * u;
+  const __nv_bfloat16* src_v = p.v + b * p.vs[0] + h * p.vs[1] + 8 * u;
+  __nv_bfloat16* dst_k = static_cast<__nv_bfloat16*>(p.c.k) + 8 * u;
+  __nv_bfloat16* dst_v = static_cast<__nv_bfloat16*>(p.c.v) + 8 * u;
+  for (int32_t i = begin + sub; i < page && t0 + i < p.T; i += kSubs) {
+    const int64_t t = t0 + i;
+    const int32_t slot = slots[t];
+    if (slot < 0) continue;
+    if (!good || slot != page0 + i) {
+      wrong = true;
+      continue;
+    }
+    const uint4 k = __ldcs(reinterpret_cast<const uint4*>(src_k + t * p.ks[2]));
+    const uint4 v = __ldcs(reinterpret_cast<const uint4*>(src_v + t * p.vs[2]));
+    *reinterpret_cast<uint4*>(dst_k + page_at(p.c.k_stride, slot, p.shift, h)) = k;
+    *reinterpret_cast<uint4*>(dst_v + page_at(p.c.v_stride, slot, p.shift, h)) = v;
+    r.add(k);
+    last = i;
+  }
+  if (wrong && u == 0 && p.err) atomicOr(p.err, DEV_ERR_BOUNDS);
+  if (!__syncthreads_or(last >= 0)) return;  // nothing stored
+  // keys that the page held (places before the first new one)
+  for (int32_t i = sub; i < begin; i += kSubs) r.add(*reinterpret_cast<const uint4*>(dst_k + page_at(p.c.k_stride, page0 + i, p.shift, h)));
+  // ---- over the warp's rows, then over the warps
+#pragma unroll
+  for (int s = kLanes; s < 32; s *= 2) {
+#pragma unroll
+    for (int i = 0; i < 8; ++i) {
+      r.hi[i] = fmaxf(r.hi[i], __shfl_xor_sync(0xffffffffu, r.hi[i], s));
+      r.lo[i] = fminf(r.lo[i], __shfl_xor_sync(0xffffffffu, r.lo[i], s));
+    }
+  }
+  r.top = __reduce_max_sync(0xffffffffu, r.top);
+  if (lane < kLanes) {
+#pragma unroll
+    for (int i = 0; i < 8; ++i) {
+      hi[warp][8 * u + i] = r.hi[i];
+      lo[warp][8 * u + i] = r.lo[i];
+    }
+  }
+  if (lane == 0) top[warp] = r.top;
+  __syncthreads();
+  if (threadIdx.x < D) {
+    const int d = threadIdx.x;
+    float a = hi[0][d], c = lo[0][d];
+    uint32_t m = top[0];
+#pragma unroll
+    for (int w = 1; w < kWarps; ++w) {
+      a = fmaxf(a, hi[w][d]);
+      c = fminf(c, lo[w][d]);
+      m = max(m, top[w]);
+    }
+    const float largest = __uint_as_float(m << 16);
+    if (largest < kUsualTop) {
+      float s, inv;
+      unit_of(largest, 7, s, inv);
+      const float up = ceilf(a * inv) * s, down = floorf(c * inv) * s;
+      a = up < a ? s : up;  // (a product that underflowed to 0)
+      c = down > c ? -s : down;
+    } else {
+      a = INFINITY;
+      c = -INFINITY;
+    }
+    __nv_bfloat16* out = static_cast<__nv_bfloat16*>(p.c.bounds) + ((static_cast<int64_t>(page0 >> p.shift) * p.c.Hkv + h) * 2) * D + d;
+    out[0] = __float2bfloat16_rn(a);
+    out[D] = __float2bfloat16_rn(c);
+  }
+}
+
+}  // namespace
+
+int64_t paged_append_units(const bsa_paged_append_args* a) {
+  return (a->T + 2 * a->cache.page - 2) / a->cache.page;  // (pages that T tokens in a row can lie in)
+}
+
+bsa_status paged_append_launch(const bsa_paged_append_args* a, cudaStream_t stream) {
+  AppendParams p{};
+  p.c = a->cache;
+  p.k = static_cast<const __nv_bfloat16*>(a->k);
+  p.v = static_cast<const __nv_bfloat16*>(a->v);
+  for (int i = 0; i < 3; ++i) {
+    p.ks[i] = a->src_k_stride[i];
+    p.vs[i] = a->src_v_stride[i];
+  }
+  p.slots = a->slots;
+  p.B = a->B;
+  p.shift = page_shift(a->cache.page);
+  p.T = a->T;
+  p.units = paged_append_units(a);
+  p.err = device_error_word();
+  if (!p.err) return fail(BSA_ERR_CUDA, "could not allocate the device error word");
+  cudaError_t e;
+  if (a->cache.bounds) {
+    const dim3 grid(static_cast<unsigned>(p.units * a->B * a->cache.Hkv));
+    e = a->cache.D == 128 ? launch_kernel(append_bounds_kernel<128>, grid, dim3(kThreads), 0, stream, p)
+                          : launch_kernel(append_bounds_kernel<64>, grid, dim3(kThreads), 0, stream, p);
+  } else {
+    const int64_t per = kThreads / (a->cache.D / 8), rows = a->T * a->B * a->cache.Hkv;
+    const dim3 grid(static_cast<unsigned>(std::min<int64_t>((rows + per - 1) / per, static_cast<int64_t>(num_sms()) * 16)));
+    e = a->cache.D == 128 ? launch_kernel(append_rows_kernel<128>, grid, dim3(kThreads), 0, stream, p)
+                          : launch_kernel(append_rows_kernel<64>, grid, dim3(kThreads), 0, stream, p);
+  }
+  if (e == cudaSuccess) e = cudaGetLastError();
+  if (e != cudaSuccess) return cuda_fail(e, "paged append launch");
+  return BSA_OK;
+}
+
+}  // namespace bsa

@@ -1,0 +1,760 @@
+// Attention of new tokens over a cache in pages: o = sum_j p_j v_j, p_j = exp(s_j - lse), s_j = scale q.k_j
+// (capped), over the keys a token sees, or over those of them in the pages of its list.
+//
+// The rows that read one key head (its group's q heads times the new tokens; with lists, the group's q heads of
+// one token) are the 16-row side of m16n8k16 products, keys and channels the narrow one:
+//     S [16 rows, 8 keys] = Q K^T,     O [16 rows, 8 channels] += P V
+// The accumulators of S are, packed to bf16, the operand P of the second product.  Few rows against a long cache: 4 G
+// operations for 4 bytes of a key's channel, G rows a head; the memory bounds it by far, and the products only have to stay out
+// of its way (rows that are padding cost nothing that is short).
+//
+// A unit of loading is 16 keys (K and V), which lie in one page.  They go by 16-byte asynchronous copies, which
+// take any stride between tokens, heads and pages, into a ring of stages that belongs to the RT warps that
+// share these keys: RT row tiles of 16, a warp each (RT = 1: a warp has its keys for itself, and no barrier).  A CTA has four warps, 4 / RT such groups,
+// which take 16 keys in turn.  A group's page numbers come 32 units at a time, one a lane, a batch ahead.
+//
+// Work: all pairs (sequence, head, row tiles; with lists also token) and their tiles of 64 keys, and kPartUnits more units for
+// each pair, form one sequence, cut into equal runs, one per CTA; lengths are read on the device.  A run's parts
+// of pairs that other CTAs share go to the workspace as (m, l, O) records, which a second kernel joins in a fixed order.
+#include <cmath>
+
+#include "internal.h"
+#include "paged.cuh"
+
+namespace bsa {
+namespace {
+
+constexpr int kUnit = 16;       // keys of one load
+constexpr int kTileKeys = 64;
+constexpr int kWarps = 4;
+constexpr int kThreads = 32 * kWarps;
+constexpr int kRowTile = 16;
+constexpr int kPartUnits = 3;   // cost of a part beside its tiles', in tiles
+constexpr int kWholeTiles = 8;  // longest pair, in tiles, that one CTA takes alone
+constexpr int kCtas = 2;        // CTAs an SM
+constexpr int kRingBytes = 96 * 1024;
+constexpr float kLog2e = 1.4426950408889634f;
+constexpr float kLn2 = 0.69314718055994530942f;
+
+struct FwdParams {
+  bsa_paged_cache c;
+  const __nv_bfloat16* q;
+  __nv_bfloat16* o;
+  float* lse;
+  int64_t qs[3], os[3];
+  const int32_t *table, *lens, *q_lens, *select;
+  int32_t B, Hq, Hkv, T, G, shift, pages;
+  int64_t M;
+  int32_t keep;
+  int32_t queries;    // query sets of a sequence that have keys of their own: T with lists, else 1
+  int32_t R;          // rows of a pair: G * T, with lists G
+  int32_t row_tiles;  // pairs of a query set and head
+  int32_t kind;
+  int64_t left, chunk;
+  float scale_log2;   // without a cap: scale * log2 e; with one: scale / cap
+  float cap_log2;
+  const float* sinks;
+  int32_t n_sinks, sinks_kv;
+  int32_t n_cta;
+  int32_t whole;      // CTA c takes pair c, all of it
+  float* rec_stat;    // [2 * n_cta][2][16 RT]: m and l of a CTA's first and last part
+  float* rec_o;       // [2 * n_cta][16 RT][D]
+  uint32_t* err;
+};
+
+// ------------------------------------------------------------------ walk
+
+// A query set: what its pairs (one per head and row tile) have in common.
+struct Pair {
+  int32_t s;           // query set: sequence s / queries, its token s % queries (with lists)
+  int32_t len, nq;     // keys held; new tokens
+  int32_t lo, hi;      // keys lo .. hi - 1 are seen by some row (with lists: places in the list's pages)
+  int32_t first_tile;
+  int32_t tiles, units;
+};
+
+__device__ __forceinline__ int32_t first_key(const FwdParams& p, int32_t pos) {
+  if (p.kind == BSA_MASK_LOCAL) return p.left < 0 || p.left >= pos ? 0 : pos - static_cast<int32_t>(p.left);
+  if (p.kind == BSA_MASK_CHUNKED_CAUSAL) return p.chunk > pos ? 0 : pos - pos % static_cast<int32_t>(p.chunk);
+  return 0;
+}
+
+__device__ __forceinline__ Pair load_pair(const FwdParams& p, int32_t s, uint32_t* err) {
+  Pair x;
+  x.s = s;
+  const int32_t b = s / p.queries;
+  x.len = paged_len(p.lens[b], p.M << p.shift, err);
+  x.nq = p.q_lens ? min(max(p.q_lens[b], 0), p.T) : p.T;
+  x.lo = 0;
+  x.hi = 0;
+  if (p.select) {
+    const int32_t t = s % p.queries;
+    const int32_t seen = t < x.nq ? max(x.len - x.nq + t + 1, 0) : 0;
+    x.hi = min(p.keep, static_cast<int32_t>((static_cast<int64_t>(seen) + (1 << p.shift) - 1) >> p.shift)) << p.shift;
+  } else if (x.nq > 0 && x.len > 0) {
+    x.lo = first_key(p, max(x.len - x.nq, 0));
+    x.hi = x.len;
+  }
+  x.first_tile = x.lo / kTileKeys;
+  x.tiles = (x.hi + kTileKeys - 1) / kTileKeys - x.first_tile;
+  if (x.hi == 0) x.tiles = 0;
+  x.units = x.tiles > 0 ? x.tiles + kPartUnits : 0;
+  return x;
+}
+
+// Units of all query sets, and of the first ones up to s; every lane of the calling warp gets both.
+__device__ __forceinline__ int64_t total_units(const FwdParams& p, int32_t s, int64_t* before, uint32_t* err = nullptr) {
+  const int lane = threadIdx.x & 31;
+  const int64_t per = static_cast<int64_t>(p.Hkv) * p.row_tiles;
+  int64_t sum = 0, head = 0;
+  for (int32_t i = lane; i < p.B * p.queries; i += 32) {
+    const int64_t n = load_pair(p, i, err).units * per;
+    sum += n;
+    if (i < s) head += n;
+  }
+#pragma unroll
+  for (int o = 16; o > 0; o >>= 1) {
+    sum += __shfl_xor_sync(0xffffffffu, sum, o);
+    head += __shfl_xor_sync(0xffffffffu, head, o);
+  }
+  *before = head;
+  return sum;
+}
+
+// Of n runs, CTA c has units [c * total / n, (c + 1) * total / n); cta_of is the one that has unit t.
+// A pair's first kPartUnits units are no tiles.
+__device__ __forceinline__ int32_t runs(const FwdParams& p, int64_t total) {
+  return static_cast<int32_t>(min(static_cast<int64_t>(p.n_cta), total));
+}
+__device__ __forceinline__ int64_t quotient(int64_t a, int64_t b) {  // of non-negative numbers, mostly small ones
+  return ((a | b) >> 32) == 0 ? static_cast<int64_t>(static_cast<uint32_t>(a) / static_cast<uint32_t>(b)) : a / b;
+}
+__device__ __forceinline__ int64_t first_unit(int64_t c, int64_t total, int32_t n) { return quotient(c * total, n); }
+__device__ __forceinline__ int32_t cta_of(int64_t t, int64_t total, int32_t n) {
+  return static_cast<int32_t>(quotient((t + 1) * n - 1, total));
+}
+
+// Cursor over a CTA's run: parts of pairs, each a range of key tiles.
+struct Run {
+  int64_t at, end;     // units of the run still to go
+  int64_t seq0;        // first unit of query set pair.s
+  Pair pair;
+  int32_t h, rt;
+  int32_t k0, k1;      // the part's key tiles
+  bool whole;          // the part is the whole pair
+  __device__ __forceinline__ void init(const FwdParams& p, int64_t first, int64_t last) {  // (warp-collective)
+    at = first;
+    end = last;
+    const int lane = threadIdx.x & 31;
+    const int64_t per = static_cast<int64_t>(p.Hkv) * p.row_tiles;
+    seq0 = 0;
+    if (at >= end) return;
+    int32_t s = 0;
+    const int32_t n_sets = p.B * p.queries;
+    for (int32_t s0 = 0;; s0 += 32) {
+      const int64_t n = s0 + lane < n_sets ? load_pair(p, s0 + lane, nullptr).units * per : 0;
+      int64_t inc = n;
+#pragma unroll
+      for (int o = 1; o < 32; o *= 2) {
+        const int64_t x = __shfl_up_sync(0xffffffffu, inc, o);
+        if (lane >= o) inc += x;
+      }
+      const uint32_t past = __ballot_sync(0xffffffffu, seq0 + inc > at);
+      if (past || s0 + 32 >= n_sets) {
+        const int l = past ? __ffs(past) - 1 : 31;
+        s = min(s0 + l, n_sets - 1);
+        seq0 += __shfl_sync(0xffffffffu, inc - n, l);
+        break;
+      }
+      seq0 += __shfl_sync(0xffffffffu, inc, 31);
+    }
+    pair = load_pair(p, s, nullptr);
+  }
+  __device__ __forceinline__ void init_whole(const FwdParams& p, int32_t c, uint32_t* err) {
+    rt = c % p.row_tiles;
+    h = c / p.row_tiles % p.Hkv;
+    pair = load_pair(p, c / p.row_tiles / p.Hkv, err);
+    at = -1;
+  }
+  __device__ bool next(const FwdParams& p) {
+    if (p.whole) {
+      if (at == 0) return false;
+      at = 0;
+      k0 = pair.first_tile;
+      k1 = k0 + pair.tiles;
+      whole = true;
+      return true;
+    }
+    const int64_t per = static_cast<int64_t>(p.Hkv) * p.row_tiles;
+    do {
+      if (at >= end) return false;
+      while (at >= seq0 + pair.units * per) {
+        seq0 += pair.units * per;
+        pair = load_pair(p, pair.s + 1, nullptr);
+      }
+      const int64_t i = at - seq0;
+      const int32_t hr = static_cast<int32_t>(quotient(i, pair.units));
+      h = hr / p.row_tiles;
+      rt = hr % p.row_tiles;
+      const int32_t u0 = static_cast<int32_t>(i - static_cast<int64_t>(hr) * pair.units);
+      const int32_t u1 = static_cast<int32_t>(min(static_cast<int64_t>(pair.units), u0 + (end - at)));
+      at += u1 - u0;
+      k0 = max(u0 - kPartUnits, 0);
+      k1 = max(u1 - kPartUnits, 0);
+    } while (k0 >= k1);
+    whole = k0 == 0 && k1 == pair.tiles;
+    k0 += pair.first_tile;
+    k1 += pair.first_tile;
+    return true;
+  }
+};
+
+// Row r of a pair: q head and token.
+__device__ __forceinline__ int32_t row_head(const FwdParams& p, int32_t h, int32_t r) { return h * p.G + (p.select ? r : r / p.T); }
+__device__ __forceinline__ int32_t row_token(const FwdParams& p, int32_t s, int32_t r) { return p.select ? s % p.queries : r % p.T; }
+
+// ------------------------------------------------------------------ loads and products
+
+__device__ __forceinline__ void copy16(uint32_t dst, const void* src, bool valid) {
+  asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(dst), "l"(src), "r"(valid ? 16 : 0) : "memory");
+}
+__device__ __forceinline__ void copy_commit() { asm volatile("cp.async.commit_group;" ::: "memory"); }
+template <int N>
+__device__ __forceinline__ void copy_wait() {
+  asm volatile("cp.async.wait_group %0;" ::"n"(N) : "memory");
+}
+__device__ __forceinline__ void ldsm4(uint32_t (&r)[4], uint32_t a) {
+  asm volatile("ldmatrix.sync.aligned.m8n8.x4.shared.b16 {%0,%1,%2,%3}, [%4];"
+               : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3])
+               : "r"(a)
+               : "memory");
+}
+__device__ __forceinline__ void ldsm4t(uint32_t (&r)[4], uint32_t a) {
+  asm volatile("ldmatrix.sync.aligned.m8n8.x4.trans.shared.b16 {%0,%1,%2,%3}, [%4];"
+               : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3])
+               : "r"(a)
+               : "memory");
+}
+__device__ __forceinline__ void mma_bf16(float (&c)[4], const uint32_t (&a)[4], uint32_t b0, uint32_t b1) {
+  asm volatile(
+      "mma.sync.aligned.m16n8k16.row.col.f32.bf16.bf16.f32 {%0,%1,%2,%3}, {%4,%5,%6,%7}, {%8,%9}, {%0,%1,%2,%3};"
+      : "+f"(c[0]), "+f"(c[1]), "+f"(c[2]), "+f"(c[3])
+      : "r"(a[0]), "r"(a[1]), "r"(a[2]), "r"(a[3]), "r"(b0), "r"(b1));
+}
+
+// The RT warps that share keys.
+template <int RT>
+__device__ __forceinline__ void group_sync(int group) {
+  if constexpr (RT == 1) __syncwarp();
+  else asm volatile("bar.sync %0, %1;" ::"r"(group + 1), "n"(RT * 32) : "memory");
+}
+
+template <int D, int RT>
+struct FwdShared {
+  static constexpr int kGroups = kWarps / RT;
+  static constexpr int kStageBytes = kUnit * D * 2 * 2;  // K, then V
+  static constexpr int kStages = kRingBytes / kGroups / kStageBytes;
+  static constexpr int kPad = D + 4;  // floats between rows of the merge buffer
+  static_assert(kGroups * RT * kRowTile * kPad * 4 <= kRingBytes, "the merge buffer is the ring's memory");
+};
+
+// Adds a row's sinks: (m, l) -> its logsumexp in log2 units and the factor of the unnormalised output.
+__device__ __forceinline__ float finish_row(const FwdParams& p, int32_t h, float m, float l, float& factor) {
+  float lse2 = l == 0.f ? -INFINITY : m + log2f(l);
+  factor = l == 0.f ? 0.f : 1.f / l;
+  if (p.n_sinks > 0) {
+    const float* z = p.sinks + (p.sinks_kv ? h * p.n_sinks : 0);
+    float top = lse2;
+    for (int j = 0; j < p.n_sinks; ++j) top = fmaxf(top, z[j] * kLog2e);
+    float sum = lse2 == -INFINITY ? 0.f : ex2_approx(lse2 - top);
+    for (int j = 0; j < p.n_sinks; ++j) sum += ex2_approx(fmaf(z[j], kLog2e, -top));
+    const float all = top == -INFINITY ? -INFINITY : top + log2f(sum);
+    if (l != 0.f) factor *= ex2_approx(lse2 - all);
+    lse2 = all;
+  }
+  return lse2;
+}
+
+__device__ __forceinline__ void store_row4(const FwdParams& p, int32_t s, int32_t h, int32_t r, int d, const float4& x, float m, float l) {
+  const int32_t b = s / p.queries, hq = row_head(p, h, r), t = row_token(p, s, r);
+  float f;
+  const float lse2 = finish_row(p, h, m, l, f);
+  // (a row without keys has O = 0, whatever the keys that others see)
+  const float4 y = l == 0.f ? make_float4(0.f, 0.f, 0.f, 0.f) : make_float4(x.x * f, x.y * f, x.z * f, x.w * f);
+  *reinterpret_cast<uint2*>(p.o + b * p.os[0] + hq * p.os[1] + t * p.os[2] + d) = make_uint2(pack_bf16x2(y.x, y.y), pack_bf16x2(y.z, y.w));
+  if (d == 0) p.lse[(static_cast<int64_t>(b) * p.Hq + hq) * p.T + t] = lse2 * kLn2;
+}
+
+template <int D, int RT, bool kCap>
+__global__ void __launch_bounds__(kThreads, kCtas) paged_fwd_kernel(const __grid_constant__ FwdParams p) {
+  using Sh = FwdShared<D, RT>;
+  constexpr int kStages = Sh::kStages, kGroups = Sh::kGroups, kK = D / 16, kRows = kRowTile * RT;
+  extern __shared__ __align__(128) uint8_t ring[];
+  __shared__ float stat_m[kGroups][kRows], stat_l[kGroups][kRows];
+  __shared__ int32_t place[kGroups][kStages];  // position of a stage's first key, -1: no keys
+  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5, tile = warp % RT, group = warp / RT;
+  const int g = lane >> 2, t4 = lane & 3;
+  const uint32_t ring0 = smem_u32(ring) + group * kStages * Sh::kStageBytes;
+  griddep_launch_dependents();
+  griddep_wait();
+  Run run;
+  if (p.whole) {
+    run.init_whole(p, static_cast<int32_t>(blockIdx.x), threadIdx.x == 0 ? p.err : nullptr);
+  } else {
+    int64_t none;
+    const int64_t total = total_units(p, 0, &none, blockIdx.x == 0 && warp == 0 ? p.err : nullptr);
+    const int32_t n = runs(p, total), c = static_cast<int32_t>(blockIdx.x);
+    run.init(p, c < n ? first_unit(c, total, n) : 0, c < n ? first_unit(c + 1, total, n) : 0);
+  }
+  const int page_units = p.shift - 4;  // log2 of the units in a page
+  int part = 0;
+  for (; run.next(p); ++part) {
+    const Pair& pair = run.pair;
+    const int32_t b = pair.s / p.queries, h = run.h;
+    const int32_t* table = p.table + b * p.M;
+    const int32_t* list = p.select ? p.select + ((static_cast<int64_t>(b) * p.Hkv + h) * p.T + pair.s % p.queries) * p.keep : nullptr;
+    // ---- this thread's two rows: the keys they see, and q as operand
+    int32_t lo[2], hi[2];
+    bool real[2];  // (others' sums are not used)
+    uint32_t qa[kK][4];
+    int32_t all_lo = 0, all_hi = INT32_MAX;  // keys that every row of the tile sees
+#pragma unroll
+    for (int i = 0; i < 2; ++i) {
+      const int32_t r = run.rt * kRows + tile * kRowTile + g + 8 * i, t = row_token(p, pair.s, r);
+      const int32_t pos = pair.len - pair.nq + t;
+      real[i] = r < p.R && t < pair.nq && pos >= 0;
+      hi[i] = real[i] ? pos : -1;
+      lo[i] = real[i] ? first_key(p, pos) : 0;
+      if (real[i]) {
+        all_lo = max(all_lo, lo[i]);
+        all_hi = min(all_hi, hi[i]);
+      }
+      const uint32_t* src = reinterpret_cast<const uint32_t*>(p.q + b * p.qs[0] + row_head(p, h, min(r, p.R - 1)) * p.qs[1] + t * p.qs[2]);
+#pragma unroll
+      for (int k = 0; k < kK; ++k) {
+        qa[k][i] = r < p.R ? src[8 * k + t4] : 0u;
+        qa[k][i + 2] = r < p.R ? src[8 * k + t4 + 4] : 0u;
+      }
+    }
+    all_lo = __reduce_max_sync(0xffffffffu, all_lo);
+    all_hi = __reduce_min_sync(0xffffffffu, all_hi);
+    // ---- units of this group: numbers u0 + i * kGroups
+    const int32_t u0 = run.k0 * (kTileKeys / kUnit) + group;
+    const int32_t u1 = min(run.k1 * (kTileKeys / kUnit), (pair.hi + kUnit - 1) / kUnit);
+    const int32_t n = u1 > u0 ? (u1 - u0 + kGroups - 1) / kGroups : 0;
+    // pages of units i0 .. i0 + 31, one a lane: its number in the cache (-1: none), and in the sequence
+    auto look_up = [&](int32_t i0, int32_t& page, int32_t& own) {
+      page = -1;
+      own = 0;
+      const int32_t i = i0 + lane;
+      if (i >= n) return;
+      own = (u0 + i * kGroups) >> page_units;
+      if (list) {
+        own = list[own];
+        const int32_t last = pair.len - pair.nq + pair.s % p.queries;  // (the query's position)
+        if (own < 0 || own > last >> p.shift) {
+          if (p.err) atomicOr(p.err, DEV_ERR_BOUNDS);
+          own = 0;
+          return;
+        }
+      }
+      page = table[own];
+      if (page < 0 || page >= p.pages) {
+        if (p.err) atomicOr(p.err, DEV_ERR_BOUNDS);
+        page = -1;
+      }
+    };
+    int32_t page_now, own_now, page_next, own_next;
+    look_up(0, page_now, own_now);
+    look_up(32, page_next, own_next);
+    const __nv_bfloat16* base_k = static_cast<const __nv_bfloat16*>(p.c.k) + h * p.c.k_stride[1];
+    const __nv_bfloat16* base_v = static_cast<const __nv_bfloat16*>(p.c.v) + h * p.c.v_stride[1];
+    // keys of a sequence that some row sees; with lists those up to the query
+    const int32_t load_lo = p.select ? 0 : pair.lo, load_hi = p.select ? pair.len - pair.nq + pair.s % p.queries + 1 : pair.hi;
+    auto issue = [&](int32_t i) {
+      if (i < n) {
+        const int32_t page = __shfl_sync(0xffffffffu, page_now, i & 31), own = __shfl_sync(0xffffffffu, own_now, i & 31);
+        const int32_t in_page = ((u0 + i * kGroups) << 4) & ((1 << p.shift) - 1);
+        const int32_t pos = (own << p.shift) + in_page;
+        const int stage = i % kStages;
+        if (lane == 0 && tile == 0) place[group][stage] = page < 0 ? -1 : pos;
+        const uint32_t dst = ring0 + stage * Sh::kStageBytes;
+        const __nv_bfloat16* k = base_k + (page < 0 ? 0 : page) * p.c.k_stride[0] + in_page * p.c.k_stride[2];
+        const __nv_bfloat16* v = base_v + (page < 0 ? 0 : page) * p.c.v_stride[0] + in_page * p.c.v_stride[2];
+        constexpr int kLanes = D / 8, kStep = 32 / kLanes * RT;
+        const int u = lane % kLanes;
+#pragma unroll
+        for (int x = 0; x < kUnit / kStep; ++x) {
+          const int row = x * kStep + tile * (32 / kLanes) + lane / kLanes;
+          const bool valid = page >= 0 && pos + row >= load_lo && pos + row < load_hi;
+          const uint32_t at = dst + row * D * 2 + ((u ^ (row & 7)) << 4);
+          copy16(at, k + row * p.c.k_stride[2] + u * 8, valid);
+          copy16(at + kUnit * D * 2, v + row * p.c.v_stride[2] + u * 8, valid);
+        }
+        if ((i & 31) == 31) {
+          page_now = page_next;
+          own_now = own_next;
+          look_up(i + 33, page_next, own_next);
+        }
+      }
+      copy_commit();
+    };
+    float m[2] = {-INFINITY, -INFINITY}, l[2] = {0.f, 0.f};
+    float acc[D / 8][4];
+#pragma unroll
+    for (int i = 0; i < D / 8; ++i) acc[i][0] = acc[i][1] = acc[i][2] = acc[i][3] = 0.f;
+    for (int i = 0; i < kStages - 1; ++i) issue(i);
+    for (int32_t i = 0; i < n; ++i) {
+      copy_wait<kStages - 2>();
+      group_sync<RT>(group);
+      issue(i + kStages - 1);
+      const int stage = i % kStages;
+      const uint32_t ks = ring0 + stage * Sh::kStageBytes, vs = ks + kUnit * D * 2;
+      const int32_t pos = place[group][stage];
+      if (pos < 0) continue;  // (uniform over the group)
+      // ---- scores of 16 keys: element (row g + 8 (e / 2), key 8 c + 2 t4 + e % 2) is s[c][e]
+      float s[2][4] = {};
+#pragma unroll
+      for (int k = 0; k < kK; ++k) {
+        uint32_t kb[4];
+        const int row = (lane & 7) + ((lane >> 4) << 3), u = 2 * k + (lane >> 3 & 1);
+        ldsm4(kb, ks + row * D * 2 + ((u ^ (row & 7)) << 4));
+        mma_bf16(s[0], qa[k], kb[0], kb[1]);
+        mma_bf16(s[1], qa[k], kb[2], kb[3]);
+      }
+#pragma unroll
+      for (int c = 0; c < 2; ++c)
+#pragma unroll
+        for (int e = 0; e < 4; ++e) {
+          s[c][e] *= p.scale_log2;
+          if constexpr (kCap) s[c][e] = p.cap_log2 * tanh_nan(s[c][e]);
+        }
+      const bool masked = pos < all_lo || pos + kUnit - 1 > all_hi;
+      if (masked) {
+#pragma unroll
+        for (int c = 0; c < 2; ++c)
+#pragma unroll
+          for (int e = 0; e < 4; ++e) {
+            const int32_t j = pos + 8 * c + 2 * t4 + (e & 1);
+            if (j < lo[e >> 1] || j > hi[e >> 1]) s[c][e] = -INFINITY;
+          }
+      }
+      // ---- running maximum and sum
+      float top[2], from[2];
+      bool moved = false;
+#pragma unroll
+      for (int r = 0; r < 2; ++r) {
+        top[r] = fmaxf(fmaxf(s[0][2 * r], s[0][2 * r + 1]), fmaxf(s[1][2 * r], s[1][2 * r + 1]));
+        top[r] = fmaxf(top[r], __shfl_xor_sync(0xffffffffu, top[r], 1));
+        top[r] = fmaxf(m[r], fmaxf(top[r], __shfl_xor_sync(0xffffffffu, top[r], 2)));
+        moved |= top[r] > m[r];
+        from[r] = top[r] == -INFINITY ? 0.f : top[r];
+      }
+      if (__any_sync(0xffffffffu, moved)) {
+#pragma unroll
+        for (int r = 0; r < 2; ++r) {
+          const float f = ex2_approx(m[r] - from[r]);  // (0 of a row's first keys)
+          l[r] *= f;
+          m[r] = top[r];
+#pragma unroll
+          for (int c = 0; c < D / 8; ++c) {
+            acc[c][2 * r] *= f;
+            acc[c][2 * r + 1] *= f;
+          }
+        }
+      }
+      uint32_t pa[4];
+#pragma unroll
+      for (int c = 0; c < 2; ++c)
+#pragma unroll
+        for (int r = 0; r < 2; ++r) {
+          const float x = ex2_approx(s[c][2 * r] - from[r]), y = ex2_approx(s[c][2 * r + 1] - from[r]);
+          l[r] += x + y;
+          pa[2 * c + r] = pack_bf16x2(x, y);
+        }
+      // ---- a key that only some rows see must not reach the others, even with values that are not numbers (0 times
+      // them is not 0): such keys leave the product and are added row by row
+      uint32_t keep_keys[2] = {0xFFFFFFFFu, 0xFFFFFFFFu};
+      if (masked && p.T > 1 && !p.select) {
+        bool odd = false;
+        const int row = lane & 15;
+#pragma unroll
+        for (int x = 0; x < D / 16; ++x) {
+          const int u = x + (lane >> 4) * (D / 16);
+          uint32_t w[4];
+          asm volatile("ld.shared.v4.u32 {%0,%1,%2,%3}, [%4];"
+                       : "=r"(w[0]), "=r"(w[1]), "=r"(w[2]), "=r"(w[3])
+                       : "r"(vs + row * D * 2 + ((u ^ (row & 7)) << 4)));
+#pragma unroll
+          for (int y = 0; y < 4; ++y) odd |= (w[y] & 0x7F80u) == 0x7F80u || (w[y] & 0x7F800000u) == 0x7F800000u;
+        }
+        uint32_t keys = __ballot_sync(0xffffffffu, odd);
+        keys = (keys | keys >> 16) & 0xFFFFu;
+        if (keys) {
+          keep_keys[0] = (keys >> (2 * t4) & 1u ? 0u : 0xFFFFu) | (keys >> (2 * t4 + 1) & 1u ? 0u : 0xFFFF0000u);
+          keep_keys[1] = (keys >> (8 + 2 * t4) & 1u ? 0u : 0xFFFFu) | (keys >> (9 + 2 * t4) & 1u ? 0u : 0xFFFF0000u);
+          for (uint32_t left = keys; left; left &= left - 1) {
+            const int j = __ffs(left) - 1, from_lane = (lane & 28) | ((j & 7) >> 1);
+#pragma unroll
+            for (int r = 0; r < 2; ++r) {
+              const uint32_t w0 = __shfl_sync(0xffffffffu, pa[r], from_lane), w1 = __shfl_sync(0xffffffffu, pa[2 + r], from_lane);
+              const uint32_t w = j < 8 ? w0 : w1;
+              const float x = __uint_as_float(j & 1 ? w & 0xFFFF0000u : w << 16);
+              if (pos + j < lo[r] || pos + j > hi[r]) continue;
+#pragma unroll
+              for (int c = 0; c < D / 8; ++c) {
+                uint32_t v;
+                asm volatile("ld.shared.u32 %0, [%1];" : "=r"(v) : "r"(vs + j * D * 2 + ((c ^ (j & 7)) << 4) + t4 * 4));
+                acc[c][2 * r] = fmaf(x, __uint_as_float(v << 16), acc[c][2 * r]);
+                acc[c][2 * r + 1] = fmaf(x, __uint_as_float(v & 0xFFFF0000u), acc[c][2 * r + 1]);
+              }
+            }
+          }
+        }
+      }
+#pragma unroll
+      for (int c = 0; c < D / 16; ++c) {
+        uint32_t vb[4];
+        const int row = lane & 15, u = 2 * c + (lane >> 4);
+        ldsm4t(vb, vs + row * D * 2 + ((u ^ (row & 7)) << 4));
+        mma_bf16(acc[2 * c], pa, vb[0] & keep_keys[0], vb[1] & keep_keys[1]);
+        mma_bf16(acc[2 * c + 1], pa, vb[2] & keep_keys[0], vb[3] & keep_keys[1]);
+      }
+    }
+    copy_wait<0>();
+    // ---- the groups' sums together
+#pragma unroll
+    for (int r = 0; r < 2; ++r) {
+      l[r] += __shfl_xor_sync(0xffffffffu, l[r], 1);
+      l[r] += __shfl_xor_sync(0xffffffffu, l[r], 2);
+      if (t4 == 0) {
+        stat_m[group][tile * kRowTile + g + 8 * r] = real[r] ? m[r] : -INFINITY;
+        stat_l[group][tile * kRowTile + g + 8 * r] = real[r] ? l[r] : 0.f;
+      }
+    }
+    __syncthreads();  // (and every warp is done with the ring)
+    float* merge = reinterpret_cast<float*>(ring);
+#pragma unroll
+    for (int r = 0; r < 2; ++r) {
+      const int row = tile * kRowTile + g + 8 * r;
+      float top = -INFINITY;
+#pragma unroll
+      for (int w = 0; w < kGroups; ++w) top = fmaxf(top, stat_m[w][row]);
+      const float f = m[r] == -INFINITY ? (l[r] == 0.f ? 0.f : 1.f) : ex2_approx(m[r] - top);
+#pragma unroll
+      for (int c = 0; c < D / 8; ++c)
+        *reinterpret_cast<float2*>(&merge[(group * kRows + row) * Sh::kPad + 8 * c + 2 * t4]) = make_float2(acc[c][2 * r] * f, acc[c][2 * r + 1] * f);
+    }
+    __syncthreads();
+    const int64_t rec = 2 * static_cast<int64_t>(blockIdx.x) + (part > 0 ? 1 : 0);
+    const int32_t live = min(kRows, p.R - run.rt * kRows);
+    for (int i = threadIdx.x; i < live * (D / 4); i += kThreads) {
+      const int row = i / (D / 4), d = i % (D / 4) * 4;
+      float top = -INFINITY, sum = 0.f;
+#pragma unroll
+      for (int w = 0; w < kGroups; ++w) top = fmaxf(top, stat_m[w][row]);
+      float4 x = make_float4(0.f, 0.f, 0.f, 0.f);
+#pragma unroll
+      for (int w = 0; w < kGroups; ++w) {
+        const float lw = stat_l[w][row];
+        if (lw == 0.f) continue;  // (no keys)
+        sum += lw * (stat_m[w][row] == -INFINITY ? 1.f : ex2_approx(stat_m[w][row] - top));
+        const float4 y = *reinterpret_cast<const float4*>(&merge[(w * kRows + row) * Sh::kPad + d]);
+        x.x += y.x;
+        x.y += y.y;
+        x.z += y.z;
+        x.w += y.w;
+      }
+      if (run.whole) {
+        store_row4(p, pair.s, h, run.rt * kRows + row, d, x, top, sum);
+      } else {
+        *reinterpret_cast<float4*>(p.rec_o + (rec * kRows + row) * D + d) = x;
+        if (d == 0) {
+          p.rec_stat[rec * 2 * kRows + row] = top;
+          p.rec_stat[rec * 2 * kRows + kRows + row] = sum;
+        }
+      }
+    }
+    __syncthreads();  // the next part writes the ring and `stat` again
+  }
+}
+
+// ------------------------------------------------------------------ join
+
+// One row of a pair a CTA: the records of CTAs c0 .. c1, a CTA's being its first part unless its run began in an
+// earlier pair (which only c0's can have).
+template <int D, int RT>
+__global__ void __launch_bounds__(kThreads) paged_join_kernel(const __grid_constant__ FwdParams p) {
+  constexpr int kRows = kRowTile * RT, kVec = D / 4, kSplit = kThreads / kVec;
+  __shared__ float4 part[kSplit][kVec];
+  __shared__ float sums[2][kWarps];
+  griddep_launch_dependents();
+  griddep_wait();
+  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+  const int32_t rows = min(p.R, kRows);  // (a last, shorter tile's blocks past its rows leave)
+  const int32_t row = static_cast<int32_t>(blockIdx.x) % rows;
+  const int32_t hr = static_cast<int32_t>(blockIdx.x) / rows, rt = hr % p.row_tiles, h = hr / p.row_tiles % p.Hkv, s = hr / p.row_tiles / p.Hkv;
+  const int32_t r = rt * kRows + row;
+  if (r >= p.R) return;
+  const Pair pair = load_pair(p, s, nullptr);
+  int32_t c0 = 0, c1 = -1, first = 0;
+  if (pair.tiles > 0) {
+    int64_t before;
+    const int64_t total = total_units(p, s, &before);
+    const int32_t n = runs(p, total);
+    const int64_t begin = before + (static_cast<int64_t>(h) * p.row_tiles + rt) * pair.units;
+    c0 = cta_of(begin + kPartUnits, total, n);
+    c1 = cta_of(begin + pair.units - 1, total, n);
+    if (c0 == c1) return;  // one CTA had all of it
+    // (a run that begins in an earlier pair has had a part of it, unless only units without tiles)
+    first = 2 * c0 + (first_unit(c0, total, n) < begin ? 1 : 0);
+  }
+  auto record = [&](int32_t c) { return static_cast<int64_t>(c == c0 ? first : 2 * c); };
+  float m = -INFINITY, l = 0.f;
+  for (int32_t c = c0 + static_cast<int32_t>(threadIdx.x); c <= c1; c += kThreads) m = fmaxf(m, p.rec_stat[record(c) * 2 * kRows + row]);
+#pragma unroll
+  for (int o = 16; o > 0; o >>= 1) m = fmaxf(m, __shfl_xor_sync(0xffffffffu, m, o));
+  if (lane == 0) sums[0][warp] = m;
+  __syncthreads();
+#pragma unroll
+  for (int w = 0; w < kWarps; ++w) m = fmaxf(m, sums[0][w]);
+  for (int32_t c = c0 + static_cast<int32_t>(threadIdx.x); c <= c1; c += kThreads) {
+    const float* st = p.rec_stat + record(c) * 2 * kRows + row;
+    if (st[kRows] != 0.f) l += st[kRows] * (st[0] == -INFINITY ? 1.f : ex2_approx(st[0] - m));
+  }
+#pragma unroll
+  for (int o = 16; o > 0; o >>= 1) l += __shfl_xor_sync(0xffffffffu, l, o);
+  if (lane == 0) sums[1][warp] = l;
+  const int vec = threadIdx.x % kVec, sub = threadIdx.x / kVec;
+  float4 x = make_float4(0.f, 0.f, 0.f, 0.f);
+#pragma unroll 4
+  for (int32_t c = c0 + sub; c <= c1; c += kSplit) {
+    const float* st = p.rec_stat + record(c) * 2 * kRows + row;
+    const float w = st[kRows] == 0.f ? 0.f : (st[0] == -INFINITY ? 1.f : ex2_approx(st[0] - m));
+    const float4 y = *reinterpret_cast<const float4*>(p.rec_o + (record(c) * kRows + row) * D + 4 * vec);
+    if (st[kRows] != 0.f) {
+      x.x = fmaf(y.x, w, x.x);
+      x.y = fmaf(y.y, w, x.y);
+      x.z = fmaf(y.z, w, x.z);
+      x.w = fmaf(y.w, w, x.w);
+    }
+  }
+  part[sub][vec] = x;
+  __syncthreads();
+  if (sub > 0) return;
+  l = 0.f;
+#pragma unroll
+  for (int w = 0; w < kWarps; ++w) l += sums[1][w];
+  for (int i = 1; i < kSplit; ++i) {
+    const float4 y = part[i][vec];
+    x.x += y.x;
+    x.y += y.y;
+    x.z += y.z;
+    x.w += y.w;
+  }
+  store_row4(p, s, h, r, 4 * vec, x, m, l);
+}
+
+// Sizes of a call that both the workspace query and the launch use.
+struct Plan {
+  int rt;         // row tiles of a CTA
+  int64_t row_tiles, pairs;
+  int32_t R, n_cta;
+  bool whole;
+  size_t stat_bytes, o_bytes;
+};
+
+Plan make_plan(const bsa_paged_fwd_args* a) {
+  Plan x;
+  const int64_t G = a->Hq / a->cache.Hkv;
+  x.R = static_cast<int32_t>(a->select ? G : G * a->T);
+  x.rt = x.R <= kRowTile ? 1 : x.R <= 2 * kRowTile ? 2 : 4;
+  const int64_t rows = kRowTile * x.rt;
+  x.row_tiles = (x.R + rows - 1) / rows;
+  x.pairs = static_cast<int64_t>(a->B) * (a->select ? a->T : 1) * a->cache.Hkv * x.row_tiles;
+  const int64_t longest = (a->select ? std::min(a->keep, a->M) : a->M) * a->cache.page, tiles = (longest + kTileKeys - 1) / kTileKeys;
+  x.whole = tiles <= kWholeTiles && x.pairs <= INT32_MAX;
+  x.n_cta = static_cast<int32_t>(x.whole ? x.pairs : std::min<int64_t>(x.pairs * tiles, static_cast<int64_t>(num_sms()) * kCtas));
+  x.stat_bytes = x.whole ? 0 : static_cast<size_t>(2 * x.n_cta) * 2 * rows * sizeof(float);
+  x.o_bytes = x.whole ? 0 : static_cast<size_t>(2 * x.n_cta) * rows * a->cache.D * sizeof(float);
+  return x;
+}
+
+template <int D, int RT>
+bsa_status launch(const FwdParams& p, const Plan& x, cudaStream_t stream) {
+  auto kern = p.cap_log2 > 0.f ? paged_fwd_kernel<D, RT, true> : paged_fwd_kernel<D, RT, false>;
+  const bsa_status st = ensure_smem_attr(reinterpret_cast<const void*>(kern), kRingBytes, "set paged forward smem size");
+  if (st != BSA_OK) return st;
+  cudaError_t e = launch_kernel(kern, dim3(p.n_cta), dim3(kThreads), kRingBytes, stream, p);
+  if (e == cudaSuccess) e = cudaGetLastError();
+  if (e != cudaSuccess) return cuda_fail(e, "paged forward launch");
+  if (p.whole) return BSA_OK;
+  const int64_t rows = x.pairs * std::min<int64_t>(p.R, kRowTile * RT);
+  e = launch_kernel(paged_join_kernel<D, RT>, dim3(static_cast<unsigned>(rows)), dim3(kThreads), 0, stream, p);
+  if (e == cudaSuccess) e = cudaGetLastError();
+  if (e != cudaSuccess) return cuda_fail(e, "paged join launch");
+  return BSA_OK;
+}
+
+template <int D>
+bsa_status launch_rows(const FwdParams& p, const Plan& x, cudaStream_t stream) {
+  return x.rt == 1 ? launch<D, 1>(p, x, stream) : x.rt == 2 ? launch<D, 2>(p, x, stream) : launch<D, 4>(p, x, stream);
+}
+
+}  // namespace
+
+bool paged_fwd_fits(const bsa_paged_fwd_args* a) {
+  const Plan x = make_plan(a);
+  return x.pairs <= INT32_MAX / (kRowTile * x.rt);
+}
+
+size_t paged_fwd_workspace_bytes(const bsa_paged_fwd_args* a) {
+  const Plan x = make_plan(a);
+  return x.stat_bytes + x.o_bytes;
+}
+
+bsa_status paged_fwd_launch(const bsa_paged_fwd_args* a, float scale, cudaStream_t stream) {
+  const Plan x = make_plan(a);
+  FwdParams p{};
+  p.c = a->cache;
+  p.q = static_cast<const __nv_bfloat16*>(a->q);
+  p.o = static_cast<__nv_bfloat16*>(a->o);
+  p.lse = a->lse;
+  for (int i = 0; i < 3; ++i) {
+    p.qs[i] = a->q_stride[i];
+    p.os[i] = a->o_stride[i];
+  }
+  p.table = a->table;
+  p.lens = a->lens;
+  p.q_lens = a->q_lens;
+  p.select = a->select;
+  p.B = a->B;
+  p.Hq = a->Hq;
+  p.Hkv = a->cache.Hkv;
+  p.T = static_cast<int32_t>(a->T);
+  p.G = a->Hq / a->cache.Hkv;
+  p.shift = page_shift(a->cache.page);
+  p.pages = static_cast<int32_t>(a->cache.pages);
+  p.M = a->M;
+  p.keep = a->select ? static_cast<int32_t>(a->keep) : 0;
+  p.queries = a->select ? p.T : 1;
+  p.R = x.R;
+  p.row_tiles = static_cast<int32_t>(x.row_tiles);
+  p.kind = a->kind;
+  p.left = a->local_left;
+  p.chunk = a->chunk;
+  p.scale_log2 = a->logits_soft_cap > 0.f ? scale / a->logits_soft_cap : scale * kLog2e;
+  p.cap_log2 = a->logits_soft_cap > 0.f ? a->logits_soft_cap * kLog2e : 0.f;
+  p.sinks = a->sinks;
+  p.n_sinks = a->num_sinks;
+  p.sinks_kv = a->sinks_per_kv_head ? 1 : 0;
+  p.n_cta = x.n_cta;
+  p.whole = x.whole ? 1 : 0;
+  p.rec_stat = static_cast<float*>(a->workspace);
+  p.rec_o = p.rec_stat + x.stat_bytes / sizeof(float);
+  p.err = device_error_word();
+  if (!p.err) return fail(BSA_ERR_CUDA, "could not allocate the device error word");
+  return a->cache.D == 128 ? launch_rows<128>(p, x, stream) : launch_rows<64>(p, x, stream);
+}
+
+}  // namespace bsa

@@ -460,6 +460,161 @@ typedef struct {
 BSA_API bsa_status bsa_kv4_evict(const bsa_kv4_evict_args* args, bsa_stream stream);
 BSA_API bsa_status bsa_kv4_evict_workspace(const bsa_kv4_evict_args* args, size_t* bytes);
 
+/* ---------------------------------------------------------------------------
+ * A cache in pages: keys and values of many sequences in pages of `page`
+ * tokens that belong to whichever sequence needs them.  bsa_paged_resize keeps
+ * the tables (pages of each sequence) and gives every new token its slot,
+ * bsa_paged_append writes keys and values there, bsa_paged_fwd attends, and
+ * bsa_paged_select chooses for each query the pages worth attending to, for
+ * block-sparse attention while answering.  As above: asynchronous, nothing
+ * allocated, lengths read from device memory, capturable; a workspace belongs
+ * to one call at a time.
+ * ------------------------------------------------------------------------- */
+
+/* All memory is the caller's.  Key i of page p and head h is at k + p*k_stride[0]
+ * + h*k_stride[1] + i*k_stride[2] (elements), so that [pages, Hkv, page, D],
+ * [pages, page, Hkv, D] and keys beside values in one buffer all are caches. */
+typedef struct {
+  void* k;               /* bf16, 16-byte aligned */
+  void* v;               /* likewise, through v_stride */
+  int64_t k_stride[3];   /* page, head, token; non-negative multiples of 8, not 0 along an axis longer than 1; D elements lie together */
+  int64_t v_stride[3];
+  void* bounds;          /* bf16 [pages, Hkv, 2, D], 16-byte aligned, or NULL: per page and head an upper bound and a
+                            lower bound of each channel of its keys (see bsa_paged_append) */
+  int64_t pages;         /* pages * page below 2^31 */
+  int32_t Hkv, D;        /* D is 64 or 128 */
+  int32_t page;          /* tokens of a page: 16, 32, 64, 128 or 256 */
+} bsa_paged_cache;
+
+typedef struct {
+  int32_t* table;          /* device int32 [B, M], read and written: the pages of each sequence, in order */
+  int32_t* free_pages;     /* device int32 [pages], read and written: entries used .. pages - 1 are the pages of no sequence */
+  const int32_t* used;     /* device int32 [1] */
+  const int32_t* lens;     /* device int32 [B]: tokens of each sequence */
+  const int32_t* new_lens; /* device int32 [B]: tokens it is to have */
+  int32_t* lens_out;       /* device int32 [B], written: tokens it now has */
+  int32_t* used_out;       /* device int32 [1], written */
+  int32_t* slots;          /* device int32 [B, T], written: slots[b, i] = page * (page size) + place of token lens[b] + i,
+                              -1 behind the last new one */
+  int32_t B;               /* 1..4096 */
+  int64_t M;               /* longest sequence, in pages */
+  int64_t T;               /* tokens a sequence can grow by in one call */
+  int64_t pages;           /* pages * page below 2^31 */
+  int32_t page;
+} bsa_paged_resize_args;
+
+/* Lengthens and shortens sequences (one that has finished gets 0 tokens).  A
+ * sequence of n tokens has the first ceil(n / page) entries of its row of the
+ * table.  First the pages that are no longer needed go back: those of sequence
+ * 0, then 1, .., in the order of its row, to entries used - (their number) ..
+ * used - 1 of free_pages.  Then pages are taken from there upwards in order of
+ * the sequences.  A sequence that does not get all pages it needs keeps its
+ * length, and so does every later one that needs any: lens_out tells.  Table
+ * entries past a sequence's pages are neither read nor changed.  No output may be
+ * the memory of an input (lens_out is not lens): a call repeated with the same inputs gives the same
+ * results.  A sequence with a length outside 0..M*page, or more than T new
+ * tokens, keeps its length and sets the bounds bit (2) of the device error
+ * word, and so does a page number outside the cache (it is moved like the
+ * others; its tokens' slots are -1).  If `used` is outside 0..pages or less
+ * than the pages given back, nothing changes and the bit is set. */
+BSA_API bsa_status bsa_paged_resize(const bsa_paged_resize_args* args, bsa_stream stream);
+
+typedef struct {
+  bsa_paged_cache cache;
+  const void* k;            /* bf16, element (b, h, t, d) at b*src_k_stride[0] + h*src_k_stride[1] + t*src_k_stride[2] + d */
+  const void* v;            /* likewise; both 16-byte aligned, strides multiples of 8 */
+  int64_t src_k_stride[3], src_v_stride[3];
+  const int32_t* slots;     /* device int32 [B, T]: the slot of each token, negative: padding, not stored */
+  int32_t B;
+  int64_t T;
+} bsa_paged_append_args;
+
+/* Writes keys and values to their slots; no two tokens of a call share one.  A
+ * token whose slot lies outside the cache is not stored and sets the bounds
+ * bit of the device error word.  Slots not written keep their contents.
+ *
+ * A cache without bounds takes tokens in any order.  With bounds, the slots are
+ * those of bsa_paged_resize: each sequence's tokens fill its pages in order, from
+ * wherever the first one is, padding behind the last, and no two sequences of a call have tokens in one
+ * page; a token out of that order is not stored and sets the bounds bit.  The
+ * bounds of every page that takes tokens are then renewed, over its slots 0
+ * .. last new one: with m the largest magnitude of the head's keys there and e =
+ * max(floor(log2 m) - 7, -100), each channel's largest and smallest key
+ * rounded up and down to a multiple of 2^e (exact in bf16); plus and minus
+ * infinity throughout where m is not below 2^100 or a key is NaN. */
+BSA_API bsa_status bsa_paged_append(const bsa_paged_append_args* args, bsa_stream stream);
+
+typedef struct {
+  bsa_paged_cache cache;   /* needs bounds; k and v are not read and may be NULL */
+  const void* q;           /* bf16, as in bsa_paged_fwd_args */
+  int64_t q_stride[3];
+  const int32_t* table;    /* device int32 [B, M] */
+  const int32_t* lens;     /* device int32 [B]: keys each sequence holds, the new tokens' own included */
+  const int32_t* q_lens;   /* device int32 [B], or NULL (= T) */
+  int32_t* index;          /* device int32 [B, Hkv, T, keep], written */
+  int32_t B, Hq;
+  int64_t M, T;
+  int64_t keep;            /* pages to choose, >= 1, >= first + recent */
+  int64_t first, recent;   /* the first and the last pages that a query sees are always chosen, this many */
+  void* workspace;         /* device, 16-byte aligned, bsa_paged_select_workspace bytes */
+  size_t workspace_bytes;
+} bsa_paged_select_args;
+
+/* For every query (new token and key head, its group of q heads together) the
+ * `keep` pages it sees with the largest bound on q.k, in increasing order, -1
+ * behind the last one if it sees fewer.  With qc = round_half_even(q / 2^f), f =
+ * max(floor(log2 max|q|) - 6, -100) over the group (qc = 0 where max|q| is not
+ * below 2^100 or is NaN), a page's score is the largest over the group's heads of sum_d
+ * max(qc_d upper_d, qc_d lower_d), infinite where that is not finite; of equal scores the lower page
+ * is chosen.  Whole numbers of at most 23 bits times a power of two: sums are exact in fp32 in any
+ * order, so the choice does not depend on how the work is split.  Token t of
+ * n = q_lens[b] stands at position lens[b] - n + t and sees the pages up to
+ * its own.  Rows of padding, or of tokens before position 0, are -1.  Lengths
+ * outside 0..M*page count as the nearer end, page numbers outside the cache
+ * as a score of minus infinity; both set the bounds bit of the device error
+ * word. */
+BSA_API bsa_status bsa_paged_select(const bsa_paged_select_args* args, bsa_stream stream);
+BSA_API bsa_status bsa_paged_select_workspace(const bsa_paged_select_args* args, size_t* bytes);
+
+typedef struct {
+  bsa_paged_cache cache;   /* (bounds are not used) */
+  const void* q;           /* bf16, element (b, h, t, d) at b*q_stride[0] + h*q_stride[1] + t*q_stride[2] + d;
+                              16-byte aligned, strides multiples of 8 */
+  void* o;                 /* bf16, written, addressed likewise through o_stride (no two rows in one place) */
+  float* lse;              /* fp32 [B, Hq, T], written */
+  int64_t q_stride[3], o_stride[3];
+  const int32_t* table;    /* device int32 [B, M] */
+  const int32_t* lens;     /* device int32 [B]: keys each sequence holds, the new tokens' own included */
+  const int32_t* q_lens;   /* device int32 [B], or NULL (= T): tokens at or past q_lens[b] are padding */
+  const int32_t* select;   /* device int32 [B, Hkv, T, keep], or NULL: see below */
+  int32_t B, Hq;
+  int64_t M, T;            /* T: new tokens per sequence (1 in a plain decode step) */
+  int64_t keep;
+  int32_t kind;            /* BSA_MASK_CAUSAL, BSA_MASK_LOCAL or BSA_MASK_CHUNKED_CAUSAL (with select: causal) */
+  int64_t local_left;      /* LOCAL: keys back to position - local_left; -1 = unbounded */
+  int64_t chunk;           /* CHUNKED_CAUSAL: chunk length (> 0) */
+  float softmax_scale;     /* NaN selects 1/sqrt(D) */
+  float logits_soft_cap;   /* as in bsa_fwd_args */
+  const float* sinks;      /* as in bsa_fwd_args */
+  int32_t num_sinks, sinks_per_kv_head;
+  void* workspace;         /* device, 16-byte aligned, bsa_paged_fwd_workspace bytes */
+  size_t workspace_bytes;
+} bsa_paged_fwd_args;
+
+/* Attention of T new tokens over their sequences' pages.  With n = q_lens[b],
+ * token t < n of sequence b stands at position lens[b] - n + t and sees the
+ * keys up to it that the mask leaves.  With `select`, a query (b, key head, t) that
+ * sees p pages attends to the keys in the first min(keep, p) pages of its
+ * list only (numbers of the sequence's own pages, in any order, none twice).  Rows that
+ * see nothing and padding rows get O = 0 and LSE = -inf (the log-sum of the
+ * sinks where there are any).  Slots that no row of a call sees are never used,
+ * whatever they hold, and one that some row sees changes no row that does not.
+ * A length outside 0..M*page counts as the nearer end, a page number outside
+ * the cache, or in a list outside the pages a query sees, as a page without
+ * keys; both set the bounds bit of the device error word. */
+BSA_API bsa_status bsa_paged_fwd(const bsa_paged_fwd_args* args, bsa_stream stream);
+BSA_API bsa_status bsa_paged_fwd_workspace(const bsa_paged_fwd_args* args, size_t* bytes);
+
 /* Synchronises `stream`, returns the device error word of the current
  * device in *word and clears it.  0 = none; otherwise an OR of the flags
  * 1 = a bounded wait ran out, 2 = out-of-range MaskInfo index (or a cache
