@@ -116,20 +116,34 @@ __global__ void __launch_bounds__(kThreads) append_bounds_kernel(const __grid_co
   const __nv_bfloat16* src_v = p.v + b * p.vs[0] + h * p.vs[1] + 8 * u;
   __nv_bfloat16* dst_k = static_cast<__nv_bfloat16*>(p.c.k) + 8 * u;
   __nv_bfloat16* dst_v = static_cast<__nv_bfloat16*>(p.c.v) + 8 * u;
-  for (int32_t i = begin + sub; i < page && t0 + i < p.T; i += kSubs) {
-    const int64_t t = t0 + i;
-    const int32_t slot = slots[t];
-    if (slot < 0) continue;
-    if (!good || slot != page0 + i) {
-      wrong = true;
-      continue;
+  constexpr int kBatch = 4;  // rows a thread has on their way at a time
+  for (int32_t i0 = begin + sub; i0 < page && t0 + i0 < p.T; i0 += kBatch * kSubs) {
+    int32_t slot[kBatch];
+    uint4 k[kBatch], v[kBatch];
+#pragma unroll
+    for (int x = 0; x < kBatch; ++x) {
+      const int32_t i = i0 + x * kSubs;
+      const bool in = i < page && t0 + i < p.T;
+      slot[x] = in ? slots[t0 + i] : -1;
+      // (read before the slot is known: it is the call's own memory)
+      if (in) {
+        k[x] = __ldcs(reinterpret_cast<const uint4*>(src_k + (t0 + i) * p.ks[2]));
+        v[x] = __ldcs(reinterpret_cast<const uint4*>(src_v + (t0 + i) * p.vs[2]));
+      }
     }
-    const uint4 k = __ldcs(reinterpret_cast<const uint4*>(src_k + t * p.ks[2]));
-    const uint4 v = __ldcs(reinterpret_cast<const uint4*>(src_v + t * p.vs[2]));
-    *reinterpret_cast<uint4*>(dst_k + page_at(p.c.k_stride, slot, p.shift, h)) = k;
-    *reinterpret_cast<uint4*>(dst_v + page_at(p.c.v_stride, slot, p.shift, h)) = v;
-    r.add(k);
-    last = i;
+#pragma unroll
+    for (int x = 0; x < kBatch; ++x) {
+      const int32_t i = i0 + x * kSubs;
+      if (slot[x] < 0) continue;
+      if (!good || slot[x] != page0 + i) {
+        wrong = true;
+        continue;
+      }
+      *reinterpret_cast<uint4*>(dst_k + page_at(p.c.k_stride, slot[x], p.shift, h)) = k[x];
+      *reinterpret_cast<uint4*>(dst_v + page_at(p.c.v_stride, slot[x], p.shift, h)) = v[x];
+      r.add(k[x]);
+      last = i;
+    }
   }
   if (wrong && u == 0 && p.err) atomicOr(p.err, DEV_ERR_BOUNDS);
   if (!__syncthreads_or(last >= 0)) return;  // nothing stored

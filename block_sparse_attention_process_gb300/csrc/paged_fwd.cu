@@ -57,6 +57,7 @@ struct FwdParams {
   int32_t n_sinks, sinks_kv;
   int32_t n_cta;
   int32_t whole;      // CTA c takes pair c, all of it
+  int32_t join_warps; // that join a row: 1 or all of a CTA
   float* rec_stat;    // [2 * n_cta][2][16 RT]: m and l of a CTA's first and last part
   float* rec_o;       // [2 * n_cta][16 RT][D]
   uint32_t* err;
@@ -83,8 +84,8 @@ __device__ __forceinline__ Pair load_pair(const FwdParams& p, int32_t s, uint32_
   Pair x;
   x.s = s;
   const int32_t b = s / p.queries;
-  x.len = paged_len(p.lens[b], p.M << p.shift, err);
-  x.nq = p.q_lens ? min(max(p.q_lens[b], 0), p.T) : p.T;
+  x.len = paged_len(__ldcg(p.lens + b), p.M << p.shift, err);
+  x.nq = p.q_lens ? min(max(__ldcg(p.q_lens + b), 0), p.T) : p.T;
   x.lo = 0;
   x.hi = 0;
   if (p.select) {
@@ -295,8 +296,8 @@ __global__ void __launch_bounds__(kThreads, kCtas) paged_fwd_kernel(const __grid
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5, tile = warp % RT, group = warp / RT;
   const int g = lane >> 2, t4 = lane & 3;
   const uint32_t ring0 = smem_u32(ring) + group * kStages * Sh::kStageBytes;
-  griddep_launch_dependents();
   griddep_wait();
+  griddep_launch_dependents();  // (after the wait: the join's CTAs read the lengths at once)
   Run run;
   if (p.whole) {
     run.init_whole(p, static_cast<int32_t>(blockIdx.x), threadIdx.x == 0 ? p.err : nullptr);
@@ -581,78 +582,89 @@ __global__ void __launch_bounds__(kThreads, kCtas) paged_fwd_kernel(const __grid
 
 // ------------------------------------------------------------------ join
 
-// One row of a pair a CTA: the records of CTAs c0 .. c1, a CTA's being its first part unless its run began in an
-// earlier pair (which only c0's can have).
+constexpr int kJoinThreads = 256, kJoinWarps = kJoinThreads / 32;
+
+// One row of a pair, by a warp or by all of a CTA: the records of CTAs c0 .. c1, a CTA's being its first part unless its
+// run began in an earlier pair (which only c0's can have).  Each warp joins some with a running maximum.
 template <int D, int RT>
-__global__ void __launch_bounds__(kThreads) paged_join_kernel(const __grid_constant__ FwdParams p) {
-  constexpr int kRows = kRowTile * RT, kVec = D / 4, kSplit = kThreads / kVec;
-  __shared__ float4 part[kSplit][kVec];
-  __shared__ float sums[2][kWarps];
-  griddep_launch_dependents();
-  griddep_wait();
+__global__ void __launch_bounds__(kJoinThreads) paged_join_kernel(const __grid_constant__ FwdParams p) {
+  constexpr int kRows = kRowTile * RT, kVec = D / 4, kSide = 32 / kVec;  // records side by side in a warp
+  __shared__ float4 part[kJoinWarps][kVec];
+  __shared__ float stats[kJoinWarps][2];
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
-  const int32_t rows = min(p.R, kRows);  // (a last, shorter tile's blocks past its rows leave)
-  const int32_t row = static_cast<int32_t>(blockIdx.x) % rows;
-  const int32_t hr = static_cast<int32_t>(blockIdx.x) / rows, rt = hr % p.row_tiles, h = hr / p.row_tiles % p.Hkv, s = hr / p.row_tiles / p.Hkv;
+  const int32_t rows = min(p.R, kRows);  // (a last, shorter tile has rows past its end)
+  const bool wide = p.join_warps > 1;
+  const int64_t at = wide ? static_cast<int64_t>(blockIdx.x) : static_cast<int64_t>(blockIdx.x) * kJoinWarps + warp;
+  const int32_t hr = static_cast<int32_t>(at / rows), row = static_cast<int32_t>(at - static_cast<int64_t>(hr) * rows);
+  const int32_t rt = hr % p.row_tiles, h = hr / p.row_tiles % p.Hkv, s = hr / p.row_tiles / p.Hkv;
   const int32_t r = rt * kRows + row;
-  if (r >= p.R) return;
-  const Pair pair = load_pair(p, s, nullptr);
+  // Where the records are: known from the lengths, before the first kernel ends (it lets this one start once its own
+  // wait is over, so what wrote the lengths has ended).
+  bool mine = s < p.B * p.queries && r < p.R;  // (uniform over the warp)
   int32_t c0 = 0, c1 = -1, first = 0;
-  if (pair.tiles > 0) {
-    int64_t before;
-    const int64_t total = total_units(p, s, &before);
-    const int32_t n = runs(p, total);
-    const int64_t begin = before + (static_cast<int64_t>(h) * p.row_tiles + rt) * pair.units;
-    c0 = cta_of(begin + kPartUnits, total, n);
-    c1 = cta_of(begin + pair.units - 1, total, n);
-    if (c0 == c1) return;  // one CTA had all of it
-    // (a run that begins in an earlier pair has had a part of it, unless only units without tiles)
-    first = 2 * c0 + (first_unit(c0, total, n) < begin ? 1 : 0);
-  }
-  auto record = [&](int32_t c) { return static_cast<int64_t>(c == c0 ? first : 2 * c); };
-  float m = -INFINITY, l = 0.f;
-  for (int32_t c = c0 + static_cast<int32_t>(threadIdx.x); c <= c1; c += kThreads) m = fmaxf(m, p.rec_stat[record(c) * 2 * kRows + row]);
-#pragma unroll
-  for (int o = 16; o > 0; o >>= 1) m = fmaxf(m, __shfl_xor_sync(0xffffffffu, m, o));
-  if (lane == 0) sums[0][warp] = m;
-  __syncthreads();
-#pragma unroll
-  for (int w = 0; w < kWarps; ++w) m = fmaxf(m, sums[0][w]);
-  for (int32_t c = c0 + static_cast<int32_t>(threadIdx.x); c <= c1; c += kThreads) {
-    const float* st = p.rec_stat + record(c) * 2 * kRows + row;
-    if (st[kRows] != 0.f) l += st[kRows] * (st[0] == -INFINITY ? 1.f : ex2_approx(st[0] - m));
-  }
-#pragma unroll
-  for (int o = 16; o > 0; o >>= 1) l += __shfl_xor_sync(0xffffffffu, l, o);
-  if (lane == 0) sums[1][warp] = l;
-  const int vec = threadIdx.x % kVec, sub = threadIdx.x / kVec;
-  float4 x = make_float4(0.f, 0.f, 0.f, 0.f);
-#pragma unroll 4
-  for (int32_t c = c0 + sub; c <= c1; c += kSplit) {
-    const float* st = p.rec_stat + record(c) * 2 * kRows + row;
-    const float w = st[kRows] == 0.f ? 0.f : (st[0] == -INFINITY ? 1.f : ex2_approx(st[0] - m));
-    const float4 y = *reinterpret_cast<const float4*>(p.rec_o + (record(c) * kRows + row) * D + 4 * vec);
-    if (st[kRows] != 0.f) {
-      x.x = fmaf(y.x, w, x.x);
-      x.y = fmaf(y.y, w, x.y);
-      x.z = fmaf(y.z, w, x.z);
-      x.w = fmaf(y.w, w, x.w);
+  if (mine) {
+    const Pair pair = load_pair(p, s, nullptr);
+    if (pair.tiles > 0) {
+      int64_t before;
+      const int64_t total = total_units(p, s, &before);
+      const int32_t n = runs(p, total);
+      const int64_t begin = before + (static_cast<int64_t>(h) * p.row_tiles + rt) * pair.units;
+      c0 = cta_of(begin + kPartUnits, total, n);
+      c1 = cta_of(begin + pair.units - 1, total, n);
+      first = 2 * c0 + (first_unit(c0, total, n) < begin ? 1 : 0);
+      mine = c0 != c1;  // else one CTA had all of it
     }
   }
-  part[sub][vec] = x;
-  __syncthreads();
-  if (sub > 0) return;
-  l = 0.f;
+  griddep_launch_dependents();
+  griddep_wait();
+  if (!mine) return;  // (where the CTA has one row: all of it)
+  const int vec = lane % kVec;
+  float m = -INFINITY, l = 0.f;
+  float4 x = make_float4(0.f, 0.f, 0.f, 0.f);
+  auto add = [&](float mc, float lc, const float4& y) {
+    if (lc == 0.f) return;  // (no keys)
+    const float to = fmaxf(m, mc), from = to == -INFINITY ? 0.f : to;
+    const float f = l == 0.f ? 0.f : m == -INFINITY ? 1.f : ex2_approx(m - from), fc = mc == -INFINITY ? 1.f : ex2_approx(mc - from);
+    l = l * f + lc * fc;
+    x.x = x.x * f + y.x * fc;
+    x.y = x.y * f + y.y * fc;
+    x.z = x.z * f + y.z * fc;
+    x.w = x.w * f + y.w * fc;
+    m = to;
+  };
+  const int32_t step = kSide * (wide ? kJoinWarps : 1);
+  for (int32_t c = c0 + (wide ? warp * kSide : 0) + lane / kVec; c <= c1; c += 4 * step) {
+    float mc[4], lc[4];
+    float4 y[4];
 #pragma unroll
-  for (int w = 0; w < kWarps; ++w) l += sums[1][w];
-  for (int i = 1; i < kSplit; ++i) {
-    const float4 y = part[i][vec];
-    x.x += y.x;
-    x.y += y.y;
-    x.z += y.z;
-    x.w += y.w;
+    for (int i = 0; i < 4; ++i) {
+      const bool in = c + i * step <= c1;
+      const int64_t rec = !in ? first : c + i * step == c0 ? first : 2 * (c + i * step);
+      mc[i] = p.rec_stat[rec * 2 * kRows + row];
+      lc[i] = in ? p.rec_stat[rec * 2 * kRows + kRows + row] : 0.f;
+      y[i] = *reinterpret_cast<const float4*>(p.rec_o + (rec * kRows + row) * D + 4 * vec);
+    }
+#pragma unroll
+    for (int i = 0; i < 4; ++i) add(mc[i], lc[i], y[i]);
   }
-  store_row4(p, s, h, r, 4 * vec, x, m, l);
+#pragma unroll
+  for (int o = kVec; o < 32; o *= 2) {
+    const float mc = __shfl_xor_sync(0xffffffffu, m, o), lc = __shfl_xor_sync(0xffffffffu, l, o);
+    const float4 y = make_float4(__shfl_xor_sync(0xffffffffu, x.x, o), __shfl_xor_sync(0xffffffffu, x.y, o),
+                                 __shfl_xor_sync(0xffffffffu, x.z, o), __shfl_xor_sync(0xffffffffu, x.w, o));
+    add(mc, lc, y);
+  }
+  if (wide) {
+    if (lane < kVec) part[warp][vec] = x;
+    if (lane == 0) {
+      stats[warp][0] = m;
+      stats[warp][1] = l;
+    }
+    __syncthreads();
+    if (warp > 0) return;
+    for (int w = 1; w < kJoinWarps; ++w) add(stats[w][0], stats[w][1], part[w][vec]);
+  }
+  if (lane < kVec) store_row4(p, s, h, r, 4 * vec, x, m, l);
 }
 
 // Sizes of a call that both the workspace query and the launch use.
@@ -689,8 +701,8 @@ bsa_status launch(const FwdParams& p, const Plan& x, cudaStream_t stream) {
   if (e == cudaSuccess) e = cudaGetLastError();
   if (e != cudaSuccess) return cuda_fail(e, "paged forward launch");
   if (p.whole) return BSA_OK;
-  const int64_t rows = x.pairs * std::min<int64_t>(p.R, kRowTile * RT);
-  e = launch_kernel(paged_join_kernel<D, RT>, dim3(static_cast<unsigned>(rows)), dim3(kThreads), 0, stream, p);
+  const int64_t rows = x.pairs * std::min<int64_t>(p.R, kRowTile * RT), per = kJoinWarps / p.join_warps;
+  e = launch_kernel(paged_join_kernel<D, RT>, dim3(static_cast<unsigned>((rows + per - 1) / per)), dim3(kJoinThreads), 0, stream, p);
   if (e == cudaSuccess) e = cudaGetLastError();
   if (e != cudaSuccess) return cuda_fail(e, "paged join launch");
   return BSA_OK;
@@ -750,6 +762,7 @@ bsa_status paged_fwd_launch(const bsa_paged_fwd_args* a, float scale, cudaStream
   p.sinks_kv = a->sinks_per_kv_head ? 1 : 0;
   p.n_cta = x.n_cta;
   p.whole = x.whole ? 1 : 0;
+  p.join_warps = x.n_cta >= 4 * x.pairs ? kJoinWarps : 1;  // (records of a pair: some n_cta / pairs)
   p.rec_stat = static_cast<float*>(a->workspace);
   p.rec_o = p.rec_stat + x.stat_bytes / sizeof(float);
   p.err = device_error_word();

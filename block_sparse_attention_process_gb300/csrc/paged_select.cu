@@ -12,8 +12,9 @@
 // the 16-row side.  The channels of a product's k axis are taken in an order that makes a thread's share of 8 pages 16-byte loads
 // straight from memory (thread t of a quad: channels 8 t .. 8 t + 7 of every 32), the four of a quad 64 bytes
 // side by side; nothing goes through shared memory but q.
-// Second kernel: one CTA a query.  Scores as ordered 32-bit keys; three digits' counts give the least key that is
-// kept and how many pages of it; then the kept pages in order, by prefix sums.
+// Second kernel: one CTA a query.  Scores as ordered 32-bit keys, less the smallest; counts of their digits, from the
+// highest one on, give the least key that is kept and how many pages of it; then the kept pages in order, by
+// prefix sums.
 #include <algorithm>
 
 #include "paged.cuh"
@@ -22,9 +23,10 @@ namespace bsa {
 namespace {
 
 constexpr int kScoreThreads = 128;
-constexpr int kScorePages = 128;  // pages of one CTA
+constexpr int kScorePages = kScoreThreads / 4;  // pages of one CTA: 8 a warp
 constexpr int kPickThreads = 512;
 constexpr int kBins = 2048;
+constexpr int kHeld = 8;  // keys a thread keeps in registers
 
 struct SelectParams {
   const __nv_bfloat16* bounds;
@@ -56,7 +58,7 @@ __device__ __forceinline__ void mma_bf16(float (&c)[4], uint32_t a0, uint32_t a1
       : "r"(a0), "r"(a1), "r"(a2), "r"(a3), "r"(b0), "r"(b1));
 }
 
-// Order of scores as order of unsigned numbers; above every score: all ones.
+// Order of scores as order of unsigned numbers.
 __device__ __forceinline__ uint32_t ordered(float s) {
   const uint32_t x = __float_as_uint(s + 0.f);  // (-0 is 0)
   return (x >> 31) ? ~x : x | 0x80000000u;
@@ -67,27 +69,33 @@ __global__ void __launch_bounds__(kScoreThreads) score_kernel(const __grid_const
   constexpr int kRow = 2 * D + 32;  // bf16 elements between rows of q (64 bytes of padding: two rows of a load in different banks)
   constexpr int kChunks = 2 * D / 32;
   __shared__ __align__(16) __nv_bfloat16 qc[16 * kRow];
-  __shared__ float score[kScorePages];
   __shared__ uint32_t tops[kScoreThreads / 32];
   griddep_launch_dependents();
   griddep_wait();
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5, g = lane >> 2, t4 = lane & 3;
   const int32_t row = static_cast<int32_t>(blockIdx.x) / p.chunks, chunk = static_cast<int32_t>(blockIdx.x) % p.chunks;
   const int32_t t = row % p.T, bh = row / p.T, b = bh / p.Hkv, h = bh % p.Hkv;
-  const int32_t n = pages_seen(p, b, t, chunk == 0 && threadIdx.x == 0 && h == 0 ? p.err : nullptr);
-  const int32_t j0 = chunk * kScorePages;
-  if (j0 >= n || n <= p.keep) return;  // (all are kept: nothing to score)
+  const int32_t j0 = chunk * kScorePages + warp * 8, j = j0 + g;  // this warp's pages, this quad's
+  // (the table's entry and q are on their way before the length is known)
+  const int32_t page = j < p.M ? p.table[b * p.M + j] : -1;
   const __nv_bfloat16* q = p.q + b * p.qs[0] + static_cast<int64_t>(h) * p.G * p.qs[1] + t * p.qs[2];
-  // ---- the group's unit
   uint32_t top = 0;
   for (int i = threadIdx.x; i < p.G * (D / 8); i += kScoreThreads) {
     const uint4 x = *reinterpret_cast<const uint4*>(q + (i / (D / 8)) * p.qs[1] + i % (D / 8) * 8);
     const uint32_t m = __vmaxu2(__vmaxu2(x.x & 0x7FFF7FFFu, x.y & 0x7FFF7FFFu), __vmaxu2(x.z & 0x7FFF7FFFu, x.w & 0x7FFF7FFFu));
     top = max(top, max(m & 0xFFFFu, m >> 16));
   }
+  const int32_t n = pages_seen(p, b, t, chunk == 0 && threadIdx.x == 0 && h == 0 ? p.err : nullptr);
+  if (chunk * kScorePages >= n || n <= p.keep) return;  // (all are kept: nothing to score)
+  const bool known = j < n && page >= 0 && page < p.pages;
+  if (j < n && !known && t4 == 0 && p.err) atomicOr(p.err, DEV_ERR_BOUNDS);
+  const uint4* src = reinterpret_cast<const uint4*>(p.bounds + (static_cast<int64_t>(known ? page : 0) * p.Hkv + h) * 2 * D) + t4;
+  uint4 x[kChunks];
+#pragma unroll
+  for (int c = 0; c < kChunks; ++c) x[c] = known ? src[c * 4] : make_uint4(0, 0, 0, 0);
+  // ---- the group's unit
   top = __reduce_max_sync(0xffffffffu, top);
   if (lane == 0) tops[warp] = top;
-  for (int i = threadIdx.x; i < kScorePages; i += kScoreThreads) score[i] = -INFINITY;
   __syncthreads();
 #pragma unroll
   for (int w = 0; w < kScoreThreads / 32; ++w) top = max(top, tops[w]);
@@ -95,13 +103,14 @@ __global__ void __launch_bounds__(kScoreThreads) score_kernel(const __grid_const
   float unit = 0.f, inv = 0.f;  // (codes are 0 then)
   const bool usual = largest < kUsualTop;
   if (usual) unit_of(largest, 6, unit, inv);
+  float best[2] = {-INFINITY, -INFINITY};  // pages 2 t4 and 2 t4 + 1 of the warp's
   for (int32_t r0 = 0; r0 < p.G; r0 += 16) {
     // ---- codes of 16 q heads (a head once more in rows past the last one)
     if (r0 > 0) __syncthreads();
     for (int i = threadIdx.x; i < 16 * (D / 8); i += kScoreThreads) {
       const int r = i / (D / 8), d = i % (D / 8) * 8;
-      const uint4 x = *reinterpret_cast<const uint4*>(q + min(r0 + r, p.G - 1) * p.qs[1] + d);
-      const uint32_t w[4] = {x.x, x.y, x.z, x.w};
+      const uint4 y = *reinterpret_cast<const uint4*>(q + min(r0 + r, p.G - 1) * p.qs[1] + d);
+      const uint32_t w[4] = {y.x, y.y, y.z, y.w};
       uint32_t up[4], down[4];
 #pragma unroll
       for (int k = 0; k < 4; ++k) {
@@ -113,45 +122,29 @@ __global__ void __launch_bounds__(kScoreThreads) score_kernel(const __grid_const
       *reinterpret_cast<uint4*>(&qc[r * kRow + D + d]) = make_uint4(down[0], down[1], down[2], down[3]);
     }
     __syncthreads();
-    for (int32_t i = warp * 8; i < kScorePages && j0 + i < n; i += kScoreThreads / 32 * 8) {
-      const int32_t j = j0 + i + g;
-      const int32_t page = j < n ? p.table[b * p.M + j] : -1;
-      const bool known = page >= 0 && page < p.pages;
-      if (j < n && !known && t4 == 0 && p.err) atomicOr(p.err, DEV_ERR_BOUNDS);
-      const uint4* src = reinterpret_cast<const uint4*>(p.bounds + (static_cast<int64_t>(known ? page : 0) * p.Hkv + h) * 2 * D) + t4;
-      uint4 x[kChunks];
+    float acc[2][4] = {};
 #pragma unroll
-      for (int c = 0; c < kChunks; ++c) x[c] = known ? __ldg(src + c * 4) : make_uint4(0, 0, 0, 0);
-      float acc[2][4] = {};
+    for (int c = 0; c < kChunks; ++c) {
+      const uint4 lo = *reinterpret_cast<const uint4*>(&qc[g * kRow + c * 32 + t4 * 8]);
+      const uint4 hi = *reinterpret_cast<const uint4*>(&qc[(g + 8) * kRow + c * 32 + t4 * 8]);
+      mma_bf16(acc[0], lo.x, hi.x, lo.y, hi.y, x[c].x, x[c].y);
+      mma_bf16(acc[1], lo.z, hi.z, lo.w, hi.w, x[c].z, x[c].w);
+    }
+    // heads g and g + 8
 #pragma unroll
-      for (int c = 0; c < kChunks; ++c) {
-        const uint4 lo = *reinterpret_cast<const uint4*>(&qc[g * kRow + c * 32 + t4 * 8]);
-        const uint4 hi = *reinterpret_cast<const uint4*>(&qc[(g + 8) * kRow + c * 32 + t4 * 8]);
-        mma_bf16(acc[0], lo.x, hi.x, lo.y, hi.y, x[c].x, x[c].y);
-        mma_bf16(acc[1], lo.z, hi.z, lo.w, hi.w, x[c].z, x[c].w);
-      }
-      // pages 2 t4 and 2 t4 + 1, heads g and g + 8
-      float best[2];
-#pragma unroll
-      for (int k = 0; k < 2; ++k) {
-        const float s0 = acc[0][k] + acc[1][k], s1 = acc[0][k + 2] + acc[1][k + 2];
-        best[k] = fmaxf(fabsf(s0) < INFINITY ? s0 : INFINITY, fabsf(s1) < INFINITY ? s1 : INFINITY);
-#pragma unroll
-        for (int o = 4; o < 32; o *= 2) best[k] = fmaxf(best[k], __shfl_xor_sync(0xffffffffu, best[k], o));
-      }
-      const uint32_t ok = __ballot_sync(0xffffffffu, known);  // lane 4 g stands for page g
-      if (g == 0) {
-#pragma unroll
-        for (int k = 0; k < 2; ++k)
-          if (ok >> (4 * (2 * t4 + k)) & 1u) score[i + 2 * t4 + k] = fmaxf(score[i + 2 * t4 + k], best[k]);
-      }
+    for (int k = 0; k < 2; ++k) {
+      const float s0 = acc[0][k] + acc[1][k], s1 = acc[0][k + 2] + acc[1][k + 2];
+      best[k] = fmaxf(best[k], fmaxf(fabsf(s0) < INFINITY ? s0 : INFINITY, fabsf(s1) < INFINITY ? s1 : INFINITY));
     }
   }
-  __syncthreads();
+  const uint32_t ok = __ballot_sync(0xffffffffu, known);  // lane 4 g stands for page g
   uint32_t* keys = p.keys + static_cast<int64_t>(row) * p.M;
-  for (int32_t i = threadIdx.x; i < kScorePages && j0 + i < n; i += kScoreThreads) {
-    const int32_t j = j0 + i;
-    keys[j] = j < p.first || j >= n - p.recent ? ~0u : ordered(score[i]);
+#pragma unroll
+  for (int k = 0; k < 2; ++k) {
+#pragma unroll
+    for (int o = 4; o < 32; o *= 2) best[k] = fmaxf(best[k], __shfl_xor_sync(0xffffffffu, best[k], o));
+    const int32_t i = 2 * t4 + k;
+    if (g == 0 && j0 + i < n) keys[j0 + i] = ordered(ok >> (4 * i) & 1u ? best[k] : -INFINITY);
   }
 }
 
@@ -181,11 +174,30 @@ __device__ __forceinline__ void block_prefix(int32_t& a, int32_t& b, int32_t (*s
   b = before_b + ib - b;
 }
 
+// Keys of a thread's run of pages, i0 .. i1 - 1: in registers where the run is short.
+struct Held {
+  const uint32_t* keys;
+  int32_t i0, i1;
+  bool held;
+  uint32_t k[kHeld];
+  template <typename F>
+  __device__ __forceinline__ void each(F&& f) const {
+    if (held) {
+#pragma unroll
+      for (int i = 0; i < kHeld; ++i)
+        if (i0 + i < i1) f(i0 + i, k[i]);
+    } else {
+      for (int32_t i = i0; i < i1; ++i) f(i, keys[i]);
+    }
+  }
+};
+
 __global__ void __launch_bounds__(kPickThreads) pick_kernel(const __grid_constant__ SelectParams p) {
+  constexpr int kWarps = kPickThreads / 32, kPer = kBins / kPickThreads;
   __shared__ uint32_t hist[kBins];
-  __shared__ uint32_t warp_sum[kPickThreads / 32];
-  __shared__ uint32_t pick[2];
-  __shared__ int32_t sums[kPickThreads / 32][2];
+  __shared__ uint32_t least[kWarps], most[kWarps], warp_sum[kWarps];
+  __shared__ uint32_t pick[3];
+  __shared__ int32_t sums[kWarps][2];
   griddep_launch_dependents();
   griddep_wait();
   const int64_t row = blockIdx.x;
@@ -197,29 +209,65 @@ __global__ void __launch_bounds__(kPickThreads) pick_kernel(const __grid_constan
     for (int32_t i = threadIdx.x; i < n; i += kPickThreads) index[i] = i;
     return;
   }
-  const uint32_t* keys = p.keys + row * p.M;
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
-  // ---- the least kept key, from its highest digit on
-  uint32_t prefix = 0, mask = 0;
-  uint32_t want = kept;  // of the keys that share the prefix, this many largest ones are kept
-  constexpr int kShift[3] = {21, 10, 0};
+  // (n is above keep, which is at least first + recent: pages m0 .. m1 - 1 are chosen by their keys)
+  const int32_t m0 = p.first, m1 = n - p.recent;
+  uint32_t want = static_cast<uint32_t>(p.keep - p.first - p.recent);
+  Held mine;
+  const int32_t per = (m1 - m0 + kPickThreads - 1) / kPickThreads;
+  mine.keys = p.keys + row * p.M;
+  mine.i0 = m0 + static_cast<int32_t>(threadIdx.x) * per;
+  mine.i1 = min(mine.i0 + per, m1);
+  mine.held = per <= kHeld;
+  if (mine.held) {
 #pragma unroll
-  for (int digit = 0; digit < 3; ++digit) {
-    const int bits = digit == 2 ? 10 : 11, shift = kShift[digit];
-    for (int i = threadIdx.x; i < kBins; i += kPickThreads) hist[i] = 0;
+    for (int i = 0; i < kHeld; ++i) mine.k[i] = mine.i0 + i < mine.i1 ? mine.keys[mine.i0 + i] : 0u;
+  }
+  for (int32_t i = threadIdx.x; i < p.first; i += kPickThreads) index[i] = i;
+  for (int32_t i = threadIdx.x; i < p.recent; i += kPickThreads) index[p.keep - p.recent + i] = m1 + i;
+  if (want == 0) return;
+  // ---- the range of the keys: its digits, not the floats', spread them over the bins
+  uint32_t lo = ~0u, hi = 0u;
+  mine.each([&](int32_t, uint32_t k) {
+    lo = min(lo, k);
+    hi = max(hi, k);
+  });
+  lo = __reduce_min_sync(0xffffffffu, lo);
+  hi = __reduce_max_sync(0xffffffffu, hi);
+  if (lane == 0) {
+    least[warp] = lo;
+    most[warp] = hi;
+  }
+#pragma unroll
+  for (int i = 0; i < kPer; ++i) hist[i * kPickThreads + threadIdx.x] = 0;
+  __syncthreads();
+#pragma unroll
+  for (int w = 0; w < kWarps; ++w) {
+    lo = min(lo, least[w]);
+    hi = max(hi, most[w]);
+  }
+  // ---- the least kept key, from its highest digit on: of key - lo, the bits above `shift` are `digits`, and of the pages
+  // that share them `want` are kept
+  int shift = 32 - __clz(hi - lo);
+  uint32_t digits = 0;
+  bool all = shift == 0;  // (equal keys)
+  while (!all) {
+    const int bits = min(shift, 11);
+    shift -= bits;
+    mine.each([&](int32_t, uint32_t k) {
+      const uint32_t x = (k - lo) >> shift;
+      if (x >> bits == digits) atomicAdd(&hist[x & ((1u << bits) - 1)], 1u);
+    });
     __syncthreads();
-    for (int32_t i = threadIdx.x; i < n; i += kPickThreads) {
-      const uint32_t k = keys[i];
-      if ((k & mask) == prefix) atomicAdd(&hist[k >> shift & ((1u << bits) - 1)], 1u);
-    }
-    __syncthreads();
-    // suffix sums: thread i has bins 4 i .. 4 i + 3, counted from the top
-    constexpr int kPer = kBins / kPickThreads;
+    // suffix sums: thread i has kPer bins, counted from the top
     const int top = kBins - 1 - kPer * static_cast<int>(threadIdx.x);
-    uint32_t c[kPer], mine = 0;
+    uint32_t c[kPer], sum = 0;
 #pragma unroll
-    for (int i = 0; i < kPer; ++i) mine += c[i] = hist[top - i];
-    uint32_t inc = mine;
+    for (int i = 0; i < kPer; ++i) {
+      sum += c[i] = hist[top - i];
+      hist[top - i] = 0;
+    }
+    uint32_t inc = sum;
 #pragma unroll
     for (int o = 1; o < 32; o *= 2) {
       const uint32_t x = __shfl_up_sync(0xffffffffu, inc, o);
@@ -227,40 +275,40 @@ __global__ void __launch_bounds__(kPickThreads) pick_kernel(const __grid_constan
     }
     if (lane == 31) warp_sum[warp] = inc;
     __syncthreads();
-    uint32_t above = inc - mine;
+    uint32_t above = inc - sum;
     for (int w = 0; w < warp; ++w) above += warp_sum[w];
 #pragma unroll
     for (int i = 0; i < kPer; ++i) {
       if (above < want && want <= above + c[i]) {
         pick[0] = top - i;
         pick[1] = want - above;
+        pick[2] = c[i];
       }
       above += c[i];
     }
     __syncthreads();
-    prefix |= pick[0] << shift;
-    mask |= ((1u << bits) - 1) << shift;
+    digits = digits << bits | pick[0];
     want = pick[1];
-    __syncthreads();
+    all = shift == 0 || pick[2] == want;
   }
-  // ---- kept pages in order: those above the least key, and the first `want` ones at it; a run of pages a thread
-  const int32_t per = (n + kPickThreads - 1) / kPickThreads, i0 = static_cast<int32_t>(threadIdx.x) * per, i1 = min(i0 + per, n);
+  // ---- kept pages in order: those above the least digits, and the first `want` ones at them
   int32_t more = 0, same = 0;
-  for (int32_t i = i0; i < i1; ++i) {
-    const uint32_t k = keys[i];
-    more += k > prefix;
-    same += k == prefix;
-  }
+  mine.each([&](int32_t, uint32_t k) {
+    const uint32_t x = (k - lo) >> shift;
+    more += x > digits;
+    same += x == digits;
+  });
   block_prefix(more, same, sums);
-  for (int32_t i = i0; i < i1; ++i) {
-    const uint32_t k = keys[i];
-    if (k > prefix) {
+  index += p.first;
+  mine.each([&](int32_t i, uint32_t k) {
+    const uint32_t x = (k - lo) >> shift;
+    if (x > digits) {
       index[more++ + min(same, static_cast<int32_t>(want))] = i;
-    } else if (k == prefix) {
+    } else if (x == digits) {
       if (same < static_cast<int32_t>(want)) index[more + same] = i;
       ++same;
     }
-  }
+  });
 }
 
 }  // namespace
