@@ -394,10 +394,11 @@ def _workspace(need: int, device) -> Optional[torch.Tensor]:
 _workspace_sizes: dict = {}
 
 
-def _workspace_size(entry: str, key, args: bytes) -> int:
+def _workspace_size(entry: str, key, args) -> int:
     key = (entry, key)
     need = _workspace_sizes.get(key)
     if need is None:
+        args = args if isinstance(args, bytes) else args()
         n = C.c_size_t(0)
         check(getattr(_abi.lib(), entry + "_workspace")(args, C.byref(n)), entry)
         if len(_workspace_sizes) > 4096:
@@ -578,8 +579,8 @@ def kv4_evict(cache: KV4Cache, lens: torch.Tensor, keep: int, *, recent: int = 0
 
 def _pages(name: str, t: torch.Tensor, index: int):
     """Strides (page, head, token) of a cache tensor [pages, Hkv, page, D]."""
-    strides = _rows(name, t, index)
-    if min(strides) < 0 or any(n > 1 and s == 0 for n, s in zip(t.shape, strides)):
+    strides = sp, sh, st = _rows(name, t, index)
+    if (sp <= 0 or sh <= 0 or st <= 0) and (min(strides) < 0 or any(n > 1 and s == 0 for n, s in zip(t.shape, strides))):
         raise ValueError(f"{name} must not have several rows in one place")
     return strides
 
@@ -683,7 +684,7 @@ def paged_select(q: torch.Tensor, cache: PagedCache, table: torch.Tensor, lens: 
     M, pack = table.shape[1], _abi.PAGED_SELECT_REST.pack
     tail = (B, Hq, M, T, keep, first, recent)
     need = _workspace_size("bsa_paged_select", (index, cache.Hkv, D, cache.page, cache.pages, cache.bounds is None, *tail),
-                           cache._c + pack(*head, 0, *tail, 0, 0))
+                           lambda: cache._c + pack(*head, 0, *tail, 0, 0))
     ctx, handle = _place(dev, index, stream)
     with ctx:
         out = torch.empty((B, cache.Hkv, T, keep), dtype=torch.int32, device=dev)
@@ -721,22 +722,26 @@ def paged_fwd(q: torch.Tensor, cache: PagedCache, table: torch.Tensor, lens: tor
     sp, sn, skv = (0, 0, 0) if sinks is None else _sink_fields(sinks, cache.Hkv)
     if sinks is not None and sinks.device != dev:
         raise ValueError(f"sinks is on {sinks.device}, the call's other tensors are on {dev}")
-    M = _table(table, B, index) and table.shape[1]
+    tp, M = _table(table, B, index), table.shape[1]
     ctx, handle = _place(dev, index, stream)
     with ctx:
         if o is None:
             o = torch.empty((B, Hq, T, D), dtype=torch.bfloat16, device=dev)
+            os = (Hq * T * D, T * D, D)
         elif o.shape != q.shape:
             raise ValueError("o must have q's shape")
+        else:
+            os = _rows("o", o, index)
         if lse is None:
             lse = torch.empty((B, Hq, T), dtype=torch.float32, device=dev)
-        head = (q.data_ptr(), o.data_ptr(), _need("lse", lse, torch.float32, index, (B, Hq, T)), *qs, *_rows("o", o, index),
-                table.data_ptr(), _lens("lens", lens, B, index), _lens("q_lens", q_lens, B, index),
+        else:
+            _need("lse", lse, torch.float32, index, (B, Hq, T))
+        head = (q.data_ptr(), o.data_ptr(), lse.data_ptr(), *qs, *os, tp, _lens("lens", lens, B, index), _lens("q_lens", q_lens, B, index),
                 0 if select is None else _need("select", select, torch.int32, index, (B, cache.Hkv, T, keep)), B, Hq, M, T, keep,
                 kind, -1 if local_left is None else local_left, chunk or 0, math.nan if softmax_scale is None else softmax_scale,
                 logits_soft_cap or 0.0, sp, sn, skv)
         pack = _abi.PAGED_FWD_REST.pack
-        need = _workspace_size("bsa_paged_fwd", (index, B, cache.Hkv, D, cache.page, Hq, M, T, keep), cache._c + pack(*head, 0, 0))
+        need = _workspace_size("bsa_paged_fwd", (index, B, cache.Hkv, D, cache.page, Hq, M, T, keep), lambda: cache._c + pack(*head, 0, 0))
         ws = _workspace(need, dev)
         check(_abi.lib().bsa_paged_fwd(cache._c + pack(*head, 0 if ws is None else ws.data_ptr(), need), handle), "bsa_paged_fwd")
     return o, lse

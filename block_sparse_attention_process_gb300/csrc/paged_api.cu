@@ -44,6 +44,7 @@ bsa_status check_cache(const bsa_paged_cache& c, bool need_kv) {
   for (const int64_t* st : {c.k_stride, c.v_stride})
     for (int i = 0; i < 3; ++i) {
       if (st[i] < 0 || st[i] % 8) return bad("the cache's strides must be non-negative multiples of 8 elements");
+      if (st[i] >= (int64_t(1) << 35)) return unsupported("the cache's strides must be below 2^35 elements");  // (in 16 bytes: 32 bits)
       if (n[i] > 1 && st[i] == 0) return bad("the cache must not have several rows in one place");
     }
   return BSA_OK;

@@ -33,6 +33,9 @@ constexpr int kPartUnits = 3;   // cost of a part beside its tiles', in tiles
 constexpr int kWholeTiles = 8;  // longest pair, in tiles, that one CTA takes alone
 constexpr int kCtas = 2;        // CTAs an SM
 constexpr int kRingBytes = 96 * 1024;
+constexpr int kSmemBytes = kRingBytes + 256;
+constexpr int32_t kNoKeys = -4096;  // place of a unit without keys: before every key a row sees
+constexpr float kLag = 8.0f;        // log2 units
 constexpr float kLog2e = 1.4426950408889634f;
 constexpr float kLn2 = 0.69314718055994530942f;
 
@@ -42,6 +45,7 @@ struct FwdParams {
   __nv_bfloat16* o;
   float* lse;
   int64_t qs[3], os[3];
+  uint32_t k8[3], v8[3];  // the cache's strides, in 16 bytes
   const int32_t *table, *lens, *q_lens, *select;
   int32_t B, Hq, Hkv, T, G, shift, pages;
   int64_t M;
@@ -253,7 +257,9 @@ __device__ __forceinline__ void group_sync(int group) {
 template <int D, int RT>
 struct FwdShared {
   static constexpr int kGroups = kWarps / RT;
-  static constexpr int kStageBytes = kUnit * D * 2 * 2;  // K, then V
+  static constexpr int kPer = RT == 1 ? 1 : 2;           // units of a step (two where the ring has room for them)
+  static constexpr int kUnitBytes = kUnit * D * 2 * 2;   // K, then V
+  static constexpr int kStageBytes = kPer * kUnitBytes;
   static constexpr int kStages = kRingBytes / kGroups / kStageBytes;
   static constexpr int kPad = D + 4;  // floats between rows of the merge buffer
   static_assert(kGroups * RT * kRowTile * kPad * 4 <= kRingBytes, "the merge buffer is the ring's memory");
@@ -286,13 +292,58 @@ __device__ __forceinline__ void store_row4(const FwdParams& p, int32_t s, int32_
   if (d == 0) p.lse[(static_cast<int64_t>(b) * p.Hq + hq) * p.T + t] = lse2 * kLn2;
 }
 
+// Which of 16 value rows hold an infinity or a NaN, as bits.
+template <int D>
+__device__ __forceinline__ uint32_t odd_keys(uint32_t v, int lane) {
+  bool odd = false;
+  const int row = lane & 15;
+#pragma unroll
+  for (int x = 0; x < D / 16; ++x) {
+    const int u = x + (lane >> 4) * (D / 16);
+    uint32_t w[4];
+    asm volatile("ld.shared.v4.u32 {%0,%1,%2,%3}, [%4];"
+                 : "=r"(w[0]), "=r"(w[1]), "=r"(w[2]), "=r"(w[3])
+                 : "r"(v + row * D * 2 + ((u ^ (row & 7)) << 4))
+                 : "memory");
+#pragma unroll
+    for (int y = 0; y < 4; ++y) odd |= (w[y] & 0x7F80u) == 0x7F80u || (w[y] & 0x7F800000u) == 0x7F800000u;
+  }
+  const uint32_t keys = __ballot_sync(0xffffffffu, odd);
+  return (keys | keys >> 16) & 0xFFFFu;
+}
+
+// O += p v of the marked keys, for the rows that see them (probabilities as the product's operand).
+template <int D>
+__device__ __forceinline__ void add_odd_keys(float (&acc)[D / 8][4], const uint32_t (&pa)[4], uint32_t keys, uint32_t v, int lane, int32_t pos,
+                                          const int32_t (&lo)[2], const int32_t (&hi)[2]) {
+  const int t4 = lane & 3;
+  for (; keys; keys &= keys - 1) {
+    const int j = __ffs(keys) - 1, from = (lane & 28) | ((j & 7) >> 1);
+#pragma unroll
+    for (int r = 0; r < 2; ++r) {
+      const uint32_t w0 = __shfl_sync(0xffffffffu, pa[r], from), w1 = __shfl_sync(0xffffffffu, pa[2 + r], from);
+      const uint32_t w = j < 8 ? w0 : w1;
+      const float x = __uint_as_float(j & 1 ? w & 0xFFFF0000u : w << 16);
+      if (pos + j < lo[r] || pos + j > hi[r]) continue;
+#pragma unroll
+      for (int c = 0; c < D / 8; ++c) {
+        uint32_t y;
+        asm volatile("ld.shared.u32 %0, [%1];" : "=r"(y) : "r"(v + j * D * 2 + ((c ^ (j & 7)) << 4) + t4 * 4) : "memory");
+        acc[c][2 * r] = fmaf(x, __uint_as_float(y << 16), acc[c][2 * r]);
+        acc[c][2 * r + 1] = fmaf(x, __uint_as_float(y & 0xFFFF0000u), acc[c][2 * r + 1]);
+      }
+    }
+  }
+}
+
 template <int D, int RT, bool kCap>
 __global__ void __launch_bounds__(kThreads, kCtas) paged_fwd_kernel(const __grid_constant__ FwdParams p) {
   using Sh = FwdShared<D, RT>;
-  constexpr int kStages = Sh::kStages, kGroups = Sh::kGroups, kK = D / 16, kRows = kRowTile * RT;
-  extern __shared__ __align__(128) uint8_t ring[];
+  constexpr int kStages = Sh::kStages, kGroups = Sh::kGroups, kPer = Sh::kPer, kK = D / 16, kRows = kRowTile * RT;
+  extern __shared__ uint8_t raw[];
+  uint8_t* const ring = raw + (-smem_u32(raw) & 255u);  // (addresses in it are XORed below bit 8)
   __shared__ float stat_m[kGroups][kRows], stat_l[kGroups][kRows];
-  __shared__ int32_t place[kGroups][kStages];  // position of a stage's first key, -1: no keys
+  __shared__ int32_t place[kGroups][kStages][kPer];  // position of a unit's first key, or kNoKeys
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5, tile = warp % RT, group = warp / RT;
   const int g = lane >> 2, t4 = lane & 3;
   const uint32_t ring0 = smem_u32(ring) + group * kStages * Sh::kStageBytes;
@@ -368,34 +419,54 @@ __global__ void __launch_bounds__(kThreads, kCtas) paged_fwd_kernel(const __grid
     int32_t page_now, own_now, page_next, own_next;
     look_up(0, page_now, own_now);
     look_up(32, page_next, own_next);
-    const __nv_bfloat16* base_k = static_cast<const __nv_bfloat16*>(p.c.k) + h * p.c.k_stride[1];
-    const __nv_bfloat16* base_v = static_cast<const __nv_bfloat16*>(p.c.v) + h * p.c.v_stride[1];
     // keys of a sequence that some row sees; with lists those up to the query
     const int32_t load_lo = p.select ? 0 : pair.lo, load_hi = p.select ? pair.len - pair.nq + pair.s % p.queries + 1 : pair.hi;
-    auto issue = [&](int32_t i) {
-      if (i < n) {
-        const int32_t page = __shfl_sync(0xffffffffu, page_now, i & 31), own = __shfl_sync(0xffffffffu, own_now, i & 31);
-        const int32_t in_page = ((u0 + i * kGroups) << 4) & ((1 << p.shift) - 1);
-        const int32_t pos = (own << p.shift) + in_page;
-        const int stage = i % kStages;
-        if (lane == 0 && tile == 0) place[group][stage] = page < 0 ? -1 : pos;
-        const uint32_t dst = ring0 + stage * Sh::kStageBytes;
-        const __nv_bfloat16* k = base_k + (page < 0 ? 0 : page) * p.c.k_stride[0] + in_page * p.c.k_stride[2];
-        const __nv_bfloat16* v = base_v + (page < 0 ? 0 : page) * p.c.v_stride[0] + in_page * p.c.v_stride[2];
-        constexpr int kLanes = D / 8, kStep = 32 / kLanes * RT;
-        const int u = lane % kLanes;
+    // ---- copies: a lane has 16 bytes of every kStep-th row, from row0 on; the chunks of a row are XORed with its number
+    constexpr int kLanes = D / 8, kStep = 32 / kLanes * RT;
+    const int row0 = tile * (32 / kLanes) + lane / kLanes;
+    const uint4* lane_k = static_cast<const uint4*>(p.c.k) + h * static_cast<int64_t>(p.k8[1]) + row0 * static_cast<int64_t>(p.k8[2]) + lane % kLanes;
+    const uint4* lane_v = static_cast<const uint4*>(p.c.v) + h * static_cast<int64_t>(p.v8[1]) + row0 * static_cast<int64_t>(p.v8[2]) + lane % kLanes;
+    const uint32_t lane_dst = ring0 + row0 * D * 2 + ((lane % kLanes ^ (row0 & 7)) << 4);
+    const int32_t steps = (n + kPer - 1) / kPer;
+    auto issue = [&](int32_t step, int stage) {
+      if (step < steps) {
 #pragma unroll
-        for (int x = 0; x < kUnit / kStep; ++x) {
-          const int row = x * kStep + tile * (32 / kLanes) + lane / kLanes;
-          const bool valid = page >= 0 && pos + row >= load_lo && pos + row < load_hi;
-          const uint32_t at = dst + row * D * 2 + ((u ^ (row & 7)) << 4);
-          copy16(at, k + row * p.c.k_stride[2] + u * 8, valid);
-          copy16(at + kUnit * D * 2, v + row * p.c.v_stride[2] + u * 8, valid);
-        }
-        if ((i & 31) == 31) {
-          page_now = page_next;
-          own_now = own_next;
-          look_up(i + 33, page_next, own_next);
+        for (int y = 0; y < kPer; ++y) {
+          const int32_t i = step * kPer + y;  // (one past the last: no page)
+          const int32_t page = __shfl_sync(0xffffffffu, page_now, i & 31), own = __shfl_sync(0xffffffffu, own_now, i & 31);
+          const int32_t in_page = ((u0 + i * kGroups) << 4) & ((1 << p.shift) - 1);
+          const int32_t pos = (own << p.shift) + in_page;
+          if (lane == 0 && tile == 0) place[group][stage][y] = page < 0 ? kNoKeys : pos;
+          const uint32_t dst = lane_dst + stage * Sh::kStageBytes + y * Sh::kUnitBytes;
+          const uint32_t some = page < 0 ? 0 : page;
+          const uint4* k = lane_k + (static_cast<uint64_t>(some) * p.k8[0] + static_cast<uint64_t>(in_page) * p.k8[2]);
+          const uint4* v = lane_v + (static_cast<uint64_t>(some) * p.v8[0] + static_cast<uint64_t>(in_page) * p.v8[2]);
+          if (page >= 0 && pos >= load_lo && pos + kUnit <= load_hi) {
+#pragma unroll
+            for (int x = 0; x < kUnit / kStep; ++x) {
+              const uint32_t at = (dst ^ ((x * kStep & 7) << 4)) + x * kStep * D * 2;
+              copy16(at, k, true);
+              copy16(at + kUnit * D * 2, v, true);
+              k += static_cast<uint64_t>(p.k8[2]) * kStep;
+              v += static_cast<uint64_t>(p.v8[2]) * kStep;
+            }
+          } else {
+#pragma unroll
+            for (int x = 0; x < kUnit / kStep; ++x) {
+              const uint32_t at = (dst ^ ((x * kStep & 7) << 4)) + x * kStep * D * 2;
+              const int32_t j = pos + x * kStep + row0;
+              const bool valid = page >= 0 && j >= load_lo && j < load_hi;
+              copy16(at, k, valid);
+              copy16(at + kUnit * D * 2, v, valid);
+              k += static_cast<uint64_t>(p.k8[2]) * kStep;
+              v += static_cast<uint64_t>(p.v8[2]) * kStep;
+            }
+          }
+          if ((i & 31) == 31) {
+            page_now = page_next;
+            own_now = own_next;
+            look_up(i + 33, page_next, own_next);
+          }
         }
       }
       copy_commit();
@@ -404,57 +475,75 @@ __global__ void __launch_bounds__(kThreads, kCtas) paged_fwd_kernel(const __grid
     float acc[D / 8][4];
 #pragma unroll
     for (int i = 0; i < D / 8; ++i) acc[i][0] = acc[i][1] = acc[i][2] = acc[i][3] = 0.f;
-    for (int i = 0; i < kStages - 1; ++i) issue(i);
-    for (int32_t i = 0; i < n; ++i) {
+    for (int i = 0; i < kStages - 1; ++i) issue(i, i);
+    // fragments: row lane & 7 (+ 8) of a matrix, its 16-byte chunks 2 k (+ 1), as XOR of the lane's first address
+    const uint32_t lane_kf = ring0 + ((lane & 7) + (lane >> 4) * 8) * D * 2 + (((lane >> 3 & 1) ^ (lane & 7)) << 4);
+    const uint32_t lane_vf = ring0 + kUnit * D * 2 + (lane & 15) * D * 2 + (((lane >> 4) ^ (lane & 7)) << 4);
+    int stage = 0, stage_in = kStages - 1;
+    for (int32_t i = 0; i < steps; ++i) {
       copy_wait<kStages - 2>();
       group_sync<RT>(group);
-      issue(i + kStages - 1);
-      const int stage = i % kStages;
-      const uint32_t ks = ring0 + stage * Sh::kStageBytes, vs = ks + kUnit * D * 2;
-      const int32_t pos = place[group][stage];
-      if (pos < 0) continue;  // (uniform over the group)
-      // ---- scores of 16 keys: element (row g + 8 (e / 2), key 8 c + 2 t4 + e % 2) is s[c][e]
-      float s[2][4] = {};
+      issue(i + kStages - 1, stage_in);
+      const uint32_t at = stage * Sh::kStageBytes;
+      int32_t pos[kPer];
+      bool any = false, masked = false;
 #pragma unroll
-      for (int k = 0; k < kK; ++k) {
-        uint32_t kb[4];
-        const int row = (lane & 7) + ((lane >> 4) << 3), u = 2 * k + (lane >> 3 & 1);
-        ldsm4(kb, ks + row * D * 2 + ((u ^ (row & 7)) << 4));
-        mma_bf16(s[0], qa[k], kb[0], kb[1]);
-        mma_bf16(s[1], qa[k], kb[2], kb[3]);
+      for (int y = 0; y < kPer; ++y) {
+        pos[y] = place[group][stage][y];
+        any |= pos[y] != kNoKeys;
+        masked |= pos[y] < all_lo || pos[y] + kUnit - 1 > all_hi;
       }
+      stage_in = stage;
+      stage = stage + 1 == kStages ? 0 : stage + 1;
+      if (!any) continue;  // (uniform over the group)
+      // ---- scores of 16 keys: element (row g + 8 (e / 2), key 8 c + 2 t4 + e % 2) is s[.][c][e]
+      float s[kPer][2][4] = {};
 #pragma unroll
-      for (int c = 0; c < 2; ++c)
+      for (int k = 0; k < kK; ++k)
 #pragma unroll
-        for (int e = 0; e < 4; ++e) {
-          s[c][e] *= p.scale_log2;
-          if constexpr (kCap) s[c][e] = p.cap_log2 * tanh_nan(s[c][e]);
+        for (int y = 0; y < kPer; ++y) {
+          uint32_t kb[4];
+          ldsm4(kb, (lane_kf + at + y * Sh::kUnitBytes) ^ (k << 5));
+          mma_bf16(s[y][0], qa[k], kb[0], kb[1]);
+          mma_bf16(s[y][1], qa[k], kb[2], kb[3]);
         }
-      const bool masked = pos < all_lo || pos + kUnit - 1 > all_hi;
-      if (masked) {
+#pragma unroll
+      for (int y = 0; y < kPer; ++y)
 #pragma unroll
         for (int c = 0; c < 2; ++c)
 #pragma unroll
           for (int e = 0; e < 4; ++e) {
-            const int32_t j = pos + 8 * c + 2 * t4 + (e & 1);
-            if (j < lo[e >> 1] || j > hi[e >> 1]) s[c][e] = -INFINITY;
+            s[y][c][e] *= p.scale_log2;
+            if constexpr (kCap) s[y][c][e] = p.cap_log2 * tanh_nan(s[y][c][e]);
           }
+      if (masked) {
+#pragma unroll
+        for (int y = 0; y < kPer; ++y)
+#pragma unroll
+          for (int c = 0; c < 2; ++c)
+#pragma unroll
+            for (int e = 0; e < 4; ++e) {
+              const int32_t j = pos[y] + 8 * c + 2 * t4 + (e & 1);
+              if (j < lo[e >> 1] || j > hi[e >> 1]) s[y][c][e] = -INFINITY;
+            }
       }
-      // ---- running maximum and sum
-      float top[2], from[2];
+      // ---- running maximum and sum; the reference m follows the maximum once that is 2^kLag above it (a probability is
+      // rounded to 8 bits wherever it lies, so the lag costs no accuracy and saves the scaling of O)
+      float top[2];
       bool moved = false;
 #pragma unroll
       for (int r = 0; r < 2; ++r) {
-        top[r] = fmaxf(fmaxf(s[0][2 * r], s[0][2 * r + 1]), fmaxf(s[1][2 * r], s[1][2 * r + 1]));
-        top[r] = fmaxf(top[r], __shfl_xor_sync(0xffffffffu, top[r], 1));
-        top[r] = fmaxf(m[r], fmaxf(top[r], __shfl_xor_sync(0xffffffffu, top[r], 2)));
-        moved |= top[r] > m[r];
-        from[r] = top[r] == -INFINITY ? 0.f : top[r];
+        float x = fmaxf(fmaxf(s[0][0][2 * r], s[0][0][2 * r + 1]), fmaxf(s[0][1][2 * r], s[0][1][2 * r + 1]));
+        if constexpr (kPer == 2) x = fmaxf(x, fmaxf(fmaxf(s[1][0][2 * r], s[1][0][2 * r + 1]), fmaxf(s[1][1][2 * r], s[1][1][2 * r + 1])));
+        x = fmaxf(x, __shfl_xor_sync(0xffffffffu, x, 1));
+        top[r] = fmaxf(m[r], fmaxf(x, __shfl_xor_sync(0xffffffffu, x, 2)));
+        if (top[r] > m[r] + kLag) moved = true;
+        else top[r] = m[r];  // (each row by itself: no row's bits depend on what others see)
       }
       if (__any_sync(0xffffffffu, moved)) {
 #pragma unroll
         for (int r = 0; r < 2; ++r) {
-          const float f = ex2_approx(m[r] - from[r]);  // (0 of a row's first keys)
+          const float f = ex2_approx(m[r] - (top[r] == -INFINITY ? 0.f : top[r]));  // (0 of a row's first keys)
           l[r] *= f;
           m[r] = top[r];
 #pragma unroll
@@ -464,62 +553,44 @@ __global__ void __launch_bounds__(kThreads, kCtas) paged_fwd_kernel(const __grid
           }
         }
       }
-      uint32_t pa[4];
+      const float from[2] = {m[0] == -INFINITY ? 0.f : m[0], m[1] == -INFINITY ? 0.f : m[1]};
 #pragma unroll
-      for (int c = 0; c < 2; ++c)
+      for (int y = 0; y < kPer; ++y) {
+        uint32_t pa[4];
 #pragma unroll
-        for (int r = 0; r < 2; ++r) {
-          const float x = ex2_approx(s[c][2 * r] - from[r]), y = ex2_approx(s[c][2 * r + 1] - from[r]);
-          l[r] += x + y;
-          pa[2 * c + r] = pack_bf16x2(x, y);
-        }
-      // ---- a key that only some rows see must not reach the others, even with values that are not numbers (0 times
-      // them is not 0): such keys leave the product and are added row by row
-      uint32_t keep_keys[2] = {0xFFFFFFFFu, 0xFFFFFFFFu};
-      if (masked && p.T > 1 && !p.select) {
-        bool odd = false;
-        const int row = lane & 15;
+        for (int c = 0; c < 2; ++c)
 #pragma unroll
-        for (int x = 0; x < D / 16; ++x) {
-          const int u = x + (lane >> 4) * (D / 16);
-          uint32_t w[4];
-          asm volatile("ld.shared.v4.u32 {%0,%1,%2,%3}, [%4];"
-                       : "=r"(w[0]), "=r"(w[1]), "=r"(w[2]), "=r"(w[3])
-                       : "r"(vs + row * D * 2 + ((u ^ (row & 7)) << 4)));
+          for (int r = 0; r < 2; ++r) {
+            const float a = ex2_approx(s[y][c][2 * r] - from[r]), b = ex2_approx(s[y][c][2 * r + 1] - from[r]);
+            l[r] += a + b;
+            pa[2 * c + r] = pack_bf16x2(a, b);
+          }
+        const uint32_t vs = lane_vf + at + y * Sh::kUnitBytes;
+        if (masked && p.T > 1 && !p.select) {
+          // a key that only some rows see must not reach the others, even with values that are not numbers (0 times
+          // them is not 0): such keys leave the product and are added row by row
+          const uint32_t keys = odd_keys<D>(ring0 + at + y * Sh::kUnitBytes + kUnit * D * 2, lane);
+          if (keys) {
+            add_odd_keys<D>(acc, pa, keys, ring0 + at + y * Sh::kUnitBytes + kUnit * D * 2, lane, pos[y], lo, hi);
+            const uint32_t keep[2] = {(keys >> (2 * t4) & 1u ? 0u : 0xFFFFu) | (keys >> (2 * t4 + 1) & 1u ? 0u : 0xFFFF0000u),
+                                      (keys >> (8 + 2 * t4) & 1u ? 0u : 0xFFFFu) | (keys >> (9 + 2 * t4) & 1u ? 0u : 0xFFFF0000u)};
 #pragma unroll
-          for (int y = 0; y < 4; ++y) odd |= (w[y] & 0x7F80u) == 0x7F80u || (w[y] & 0x7F800000u) == 0x7F800000u;
-        }
-        uint32_t keys = __ballot_sync(0xffffffffu, odd);
-        keys = (keys | keys >> 16) & 0xFFFFu;
-        if (keys) {
-          keep_keys[0] = (keys >> (2 * t4) & 1u ? 0u : 0xFFFFu) | (keys >> (2 * t4 + 1) & 1u ? 0u : 0xFFFF0000u);
-          keep_keys[1] = (keys >> (8 + 2 * t4) & 1u ? 0u : 0xFFFFu) | (keys >> (9 + 2 * t4) & 1u ? 0u : 0xFFFF0000u);
-          for (uint32_t left = keys; left; left &= left - 1) {
-            const int j = __ffs(left) - 1, from_lane = (lane & 28) | ((j & 7) >> 1);
-#pragma unroll
-            for (int r = 0; r < 2; ++r) {
-              const uint32_t w0 = __shfl_sync(0xffffffffu, pa[r], from_lane), w1 = __shfl_sync(0xffffffffu, pa[2 + r], from_lane);
-              const uint32_t w = j < 8 ? w0 : w1;
-              const float x = __uint_as_float(j & 1 ? w & 0xFFFF0000u : w << 16);
-              if (pos + j < lo[r] || pos + j > hi[r]) continue;
-#pragma unroll
-              for (int c = 0; c < D / 8; ++c) {
-                uint32_t v;
-                asm volatile("ld.shared.u32 %0, [%1];" : "=r"(v) : "r"(vs + j * D * 2 + ((c ^ (j & 7)) << 4) + t4 * 4));
-                acc[c][2 * r] = fmaf(x, __uint_as_float(v << 16), acc[c][2 * r]);
-                acc[c][2 * r + 1] = fmaf(x, __uint_as_float(v & 0xFFFF0000u), acc[c][2 * r + 1]);
-              }
+            for (int c = 0; c < D / 16; ++c) {
+              uint32_t vb[4];
+              ldsm4t(vb, vs ^ (c << 5));
+              mma_bf16(acc[2 * c], pa, vb[0] & keep[0], vb[1] & keep[1]);
+              mma_bf16(acc[2 * c + 1], pa, vb[2] & keep[0], vb[3] & keep[1]);
             }
+            continue;
           }
         }
-      }
 #pragma unroll
-      for (int c = 0; c < D / 16; ++c) {
-        uint32_t vb[4];
-        const int row = lane & 15, u = 2 * c + (lane >> 4);
-        ldsm4t(vb, vs + row * D * 2 + ((u ^ (row & 7)) << 4));
-        mma_bf16(acc[2 * c], pa, vb[0] & keep_keys[0], vb[1] & keep_keys[1]);
-        mma_bf16(acc[2 * c + 1], pa, vb[2] & keep_keys[0], vb[3] & keep_keys[1]);
+        for (int c = 0; c < D / 16; ++c) {
+          uint32_t vb[4];
+          ldsm4t(vb, vs ^ (c << 5));
+          mma_bf16(acc[2 * c], pa, vb[0], vb[1]);
+          mma_bf16(acc[2 * c + 1], pa, vb[2], vb[3]);
+        }
       }
     }
     copy_wait<0>();
@@ -695,9 +766,9 @@ Plan make_plan(const bsa_paged_fwd_args* a) {
 template <int D, int RT>
 bsa_status launch(const FwdParams& p, const Plan& x, cudaStream_t stream) {
   auto kern = p.cap_log2 > 0.f ? paged_fwd_kernel<D, RT, true> : paged_fwd_kernel<D, RT, false>;
-  const bsa_status st = ensure_smem_attr(reinterpret_cast<const void*>(kern), kRingBytes, "set paged forward smem size");
+  const bsa_status st = ensure_smem_attr(reinterpret_cast<const void*>(kern), kSmemBytes, "set paged forward smem size");
   if (st != BSA_OK) return st;
-  cudaError_t e = launch_kernel(kern, dim3(p.n_cta), dim3(kThreads), kRingBytes, stream, p);
+  cudaError_t e = launch_kernel(kern, dim3(p.n_cta), dim3(kThreads), kSmemBytes, stream, p);
   if (e == cudaSuccess) e = cudaGetLastError();
   if (e != cudaSuccess) return cuda_fail(e, "paged forward launch");
   if (p.whole) return BSA_OK;
@@ -735,6 +806,10 @@ bsa_status paged_fwd_launch(const bsa_paged_fwd_args* a, float scale, cudaStream
   for (int i = 0; i < 3; ++i) {
     p.qs[i] = a->q_stride[i];
     p.os[i] = a->o_stride[i];
+  }
+  for (int i = 0; i < 3; ++i) {
+    p.k8[i] = static_cast<uint32_t>(a->cache.k_stride[i] / 8);
+    p.v8[i] = static_cast<uint32_t>(a->cache.v_stride[i] / 8);
   }
   p.table = a->table;
   p.lens = a->lens;
