@@ -108,12 +108,12 @@ __device__ __forceinline__ Pair load_pair(const FwdParams& p, int32_t s, uint32_
 }
 
 // Units of all query sets, and of the first ones up to s; every lane of the calling warp gets both.
-__device__ __forceinline__ int64_t total_units(const FwdParams& p, int32_t s, int64_t* before, uint32_t* err = nullptr) {
+__device__ __forceinline__ int64_t total_units(const FwdParams& p, int32_t s, int64_t* before) {
   const int lane = threadIdx.x & 31;
   const int64_t per = static_cast<int64_t>(p.Hkv) * p.row_tiles;
   int64_t sum = 0, head = 0;
   for (int32_t i = lane; i < p.B * p.queries; i += 32) {
-    const int64_t n = load_pair(p, i, err).units * per;
+    const int64_t n = load_pair(p, i, nullptr).units * per;
     sum += n;
     if (i < s) head += n;
   }
@@ -139,6 +139,16 @@ __device__ __forceinline__ int32_t cta_of(int64_t t, int64_t total, int32_t n) {
   return static_cast<int32_t>(quotient((t + 1) * n - 1, total));
 }
 
+// Inclusive prefix sum over the warp.
+__device__ __forceinline__ int64_t scan(int64_t x) {
+#pragma unroll
+  for (int o = 1; o < 32; o *= 2) {
+    const int64_t y = __shfl_up_sync(0xffffffffu, x, o);
+    if ((threadIdx.x & 31) >= o) x += y;
+  }
+  return x;
+}
+
 // Cursor over a CTA's run: parts of pairs, each a range of key tiles.
 struct Run {
   int64_t at, end;     // units of the run still to go
@@ -147,33 +157,49 @@ struct Run {
   int32_t h, rt;
   int32_t k0, k1;      // the part's key tiles
   bool whole;          // the part is the whole pair
-  __device__ __forceinline__ void init(const FwdParams& p, int64_t first, int64_t last) {  // (warp-collective)
-    at = first;
-    end = last;
+  // run c of those that the query sets' units are cut into (warp-collective)
+  __device__ __forceinline__ void init(const FwdParams& p, int32_t c, uint32_t* err) {
     const int lane = threadIdx.x & 31;
     const int64_t per = static_cast<int64_t>(p.Hkv) * p.row_tiles;
+    const int32_t n_sets = p.B * p.queries;
+    Pair x{};
+    int64_t total = 0, inc = 0, own = 0;
+    // up to 32 sets: a lane holds its own from here on
+    for (int32_t s0 = 0; s0 < n_sets; s0 += 32) {
+      x.units = 0;
+      if (s0 + lane < n_sets) x = load_pair(p, s0 + lane, err);
+      own = x.units * per;
+      inc = scan(own);
+      total += __shfl_sync(0xffffffffu, inc, 31);
+    }
+    const int32_t n = runs(p, total);
+    at = c < n ? first_unit(c, total, n) : 0;
+    end = c < n ? first_unit(c + 1, total, n) : 0;
     seq0 = 0;
     if (at >= end) return;
-    int32_t s = 0;
-    const int32_t n_sets = p.B * p.queries;
     for (int32_t s0 = 0;; s0 += 32) {
-      const int64_t n = s0 + lane < n_sets ? load_pair(p, s0 + lane, nullptr).units * per : 0;
-      int64_t inc = n;
-#pragma unroll
-      for (int o = 1; o < 32; o *= 2) {
-        const int64_t x = __shfl_up_sync(0xffffffffu, inc, o);
-        if (lane >= o) inc += x;
+      if (n_sets > 32) {
+        x.units = 0;
+        if (s0 + lane < n_sets) x = load_pair(p, s0 + lane, nullptr);
+        own = x.units * per;
+        inc = scan(own);
       }
       const uint32_t past = __ballot_sync(0xffffffffu, seq0 + inc > at);
       if (past || s0 + 32 >= n_sets) {
         const int l = past ? __ffs(past) - 1 : 31;
-        s = min(s0 + l, n_sets - 1);
-        seq0 += __shfl_sync(0xffffffffu, inc - n, l);
-        break;
+        seq0 += __shfl_sync(0xffffffffu, inc - own, l);
+        pair.s = __shfl_sync(0xffffffffu, x.s, l);
+        pair.len = __shfl_sync(0xffffffffu, x.len, l);
+        pair.nq = __shfl_sync(0xffffffffu, x.nq, l);
+        pair.lo = __shfl_sync(0xffffffffu, x.lo, l);
+        pair.hi = __shfl_sync(0xffffffffu, x.hi, l);
+        pair.first_tile = __shfl_sync(0xffffffffu, x.first_tile, l);
+        pair.tiles = __shfl_sync(0xffffffffu, x.tiles, l);
+        pair.units = __shfl_sync(0xffffffffu, x.units, l);
+        return;
       }
       seq0 += __shfl_sync(0xffffffffu, inc, 31);
     }
-    pair = load_pair(p, s, nullptr);
   }
   __device__ __forceinline__ void init_whole(const FwdParams& p, int32_t c, uint32_t* err) {
     rt = c % p.row_tiles;
@@ -353,10 +379,7 @@ __global__ void __launch_bounds__(kThreads, kCtas) paged_fwd_kernel(const __grid
   if (p.whole) {
     run.init_whole(p, static_cast<int32_t>(blockIdx.x), threadIdx.x == 0 ? p.err : nullptr);
   } else {
-    int64_t none;
-    const int64_t total = total_units(p, 0, &none, blockIdx.x == 0 && warp == 0 ? p.err : nullptr);
-    const int32_t n = runs(p, total), c = static_cast<int32_t>(blockIdx.x);
-    run.init(p, c < n ? first_unit(c, total, n) : 0, c < n ? first_unit(c + 1, total, n) : 0);
+    run.init(p, static_cast<int32_t>(blockIdx.x), blockIdx.x == 0 && warp == 0 ? p.err : nullptr);
   }
   const int page_units = p.shift - 4;  // log2 of the units in a page
   int part = 0;
@@ -365,31 +388,6 @@ __global__ void __launch_bounds__(kThreads, kCtas) paged_fwd_kernel(const __grid
     const int32_t b = pair.s / p.queries, h = run.h;
     const int32_t* table = p.table + b * p.M;
     const int32_t* list = p.select ? p.select + ((static_cast<int64_t>(b) * p.Hkv + h) * p.T + pair.s % p.queries) * p.keep : nullptr;
-    // ---- this thread's two rows: the keys they see, and q as operand
-    int32_t lo[2], hi[2];
-    bool real[2];  // (others' sums are not used)
-    uint32_t qa[kK][4];
-    int32_t all_lo = 0, all_hi = INT32_MAX;  // keys that every row of the tile sees
-#pragma unroll
-    for (int i = 0; i < 2; ++i) {
-      const int32_t r = run.rt * kRows + tile * kRowTile + g + 8 * i, t = row_token(p, pair.s, r);
-      const int32_t pos = pair.len - pair.nq + t;
-      real[i] = r < p.R && t < pair.nq && pos >= 0;
-      hi[i] = real[i] ? pos : -1;
-      lo[i] = real[i] ? first_key(p, pos) : 0;
-      if (real[i]) {
-        all_lo = max(all_lo, lo[i]);
-        all_hi = min(all_hi, hi[i]);
-      }
-      const uint32_t* src = reinterpret_cast<const uint32_t*>(p.q + b * p.qs[0] + row_head(p, h, min(r, p.R - 1)) * p.qs[1] + t * p.qs[2]);
-#pragma unroll
-      for (int k = 0; k < kK; ++k) {
-        qa[k][i] = r < p.R ? src[8 * k + t4] : 0u;
-        qa[k][i + 2] = r < p.R ? src[8 * k + t4 + 4] : 0u;
-      }
-    }
-    all_lo = __reduce_max_sync(0xffffffffu, all_lo);
-    all_hi = __reduce_min_sync(0xffffffffu, all_hi);
     // ---- units of this group: numbers u0 + i * kGroups
     const int32_t u0 = run.k0 * (kTileKeys / kUnit) + group;
     const int32_t u1 = min(run.k1 * (kTileKeys / kUnit), (pair.hi + kUnit - 1) / kUnit);
@@ -475,7 +473,43 @@ __global__ void __launch_bounds__(kThreads, kCtas) paged_fwd_kernel(const __grid
     float acc[D / 8][4];
 #pragma unroll
     for (int i = 0; i < D / 8; ++i) acc[i][0] = acc[i][1] = acc[i][2] = acc[i][3] = 0.f;
+    // ---- q by way of the ring's last stage (free until the first step), then the first stages
+    const uint32_t q_at = ring0 + (kStages - 1) * Sh::kStageBytes + tile * kRowTile * D * 2;
+#pragma unroll
+    for (int x = 0; x < kRowTile * kLanes / 32; ++x) {
+      const int row = x * (32 / kLanes) + lane / kLanes;
+      const int32_t r = run.rt * kRows + tile * kRowTile + row, rr = min(r, p.R - 1);
+      const __nv_bfloat16* src = p.q + b * p.qs[0] + row_head(p, h, rr) * p.qs[1] + row_token(p, pair.s, rr) * p.qs[2] + lane % kLanes * 8;
+      copy16(q_at + row * D * 2 + ((lane % kLanes ^ (row & 7)) << 4), src, r < p.R);
+    }
+    copy_commit();
     for (int i = 0; i < kStages - 1; ++i) issue(i, i);
+    // ---- this thread's two rows: the keys they see
+    int32_t lo[2], hi[2];
+    bool real[2];  // (others' sums are not used)
+    int32_t all_lo = 0, all_hi = INT32_MAX;  // keys that every row of the tile sees
+#pragma unroll
+    for (int i = 0; i < 2; ++i) {
+      const int32_t r = run.rt * kRows + tile * kRowTile + g + 8 * i, t = row_token(p, pair.s, r);
+      const int32_t pos = pair.len - pair.nq + t;
+      real[i] = r < p.R && t < pair.nq && pos >= 0;
+      hi[i] = real[i] ? pos : -1;
+      lo[i] = real[i] ? first_key(p, pos) : 0;
+      if (real[i]) {
+        all_lo = max(all_lo, lo[i]);
+        all_hi = min(all_hi, hi[i]);
+      }
+    }
+    all_lo = __reduce_max_sync(0xffffffffu, all_lo);
+    all_hi = __reduce_min_sync(0xffffffffu, all_hi);
+    copy_wait<kStages - 1>();
+    __syncwarp();
+    uint32_t qa[kK][4];
+#pragma unroll
+    for (int k = 0; k < kK; ++k) {
+      const uint32_t at = q_at + (lane & 15) * D * 2;
+      ldsm4(qa[k], at + ((2 * k + (lane >> 4) ^ (lane & 7)) << 4));
+    }
     // fragments: row lane & 7 (+ 8) of a matrix, its 16-byte chunks 2 k (+ 1), as XOR of the lane's first address
     const uint32_t lane_kf = ring0 + ((lane & 7) + (lane >> 4) * 8) * D * 2 + (((lane >> 3 & 1) ^ (lane & 7)) << 4);
     const uint32_t lane_vf = ring0 + kUnit * D * 2 + (lane & 15) * D * 2 + (((lane >> 4) ^ (lane & 7)) << 4);
