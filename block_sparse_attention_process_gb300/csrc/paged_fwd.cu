@@ -26,14 +26,12 @@ namespace {
 
 constexpr int kUnit = 16;       // keys of one load
 constexpr int kTileKeys = 64;
-constexpr int kWarps = 4;
-constexpr int kThreads = 32 * kWarps;
 constexpr int kRowTile = 16;
 constexpr int kPartUnits = 3;   // cost of a part beside its tiles', in tiles
 constexpr int kWholeTiles = 8;  // longest pair, in tiles, that one CTA takes alone
-constexpr int kCtas = 2;        // CTAs an SM
-constexpr int kRingBytes = 96 * 1024;
-constexpr int kSmemBytes = kRingBytes + 256;
+constexpr int kSmWarps = 8;      // warps an SM: a CTA of all of them for runs, two of four where a pair is whole to a CTA
+constexpr int kWarpRing = 24 * 1024;
+constexpr int smem_bytes(int warps) { return warps * kWarpRing + 256; }
 constexpr int32_t kNoKeys = -4096;  // place of a unit without keys: before every key a row sees
 constexpr float kLag = 8.0f;        // log2 units
 constexpr float kLog2e = 1.4426950408889634f;
@@ -280,15 +278,15 @@ __device__ __forceinline__ void group_sync(int group) {
   else asm volatile("bar.sync %0, %1;" ::"r"(group + 1), "n"(RT * 32) : "memory");
 }
 
-template <int D, int RT>
+template <int D, int RT, int W>
 struct FwdShared {
-  static constexpr int kGroups = kWarps / RT;
+  static constexpr int kGroups = W / RT;
   static constexpr int kPer = RT == 1 ? 1 : 2;           // units of a step (two where the ring has room for them)
   static constexpr int kUnitBytes = kUnit * D * 2 * 2;   // K, then V
   static constexpr int kStageBytes = kPer * kUnitBytes;
-  static constexpr int kStages = kRingBytes / kGroups / kStageBytes;
+  static constexpr int kStages = RT * kWarpRing / kStageBytes;
   static constexpr int kPad = D + 4;  // floats between rows of the merge buffer
-  static_assert(kGroups * RT * kRowTile * kPad * 4 <= kRingBytes, "the merge buffer is the ring's memory");
+  static_assert(W * kRowTile * kPad * 4 <= W * kWarpRing, "the merge buffer is the ring's memory");
 };
 
 // Adds a row's sinks: (m, l) -> its logsumexp in log2 units and the factor of the unnormalised output.
@@ -362,9 +360,9 @@ __device__ __forceinline__ void add_odd_keys(float (&acc)[D / 8][4], const uint3
   }
 }
 
-template <int D, int RT, bool kCap>
-__global__ void __launch_bounds__(kThreads, kCtas) paged_fwd_kernel(const __grid_constant__ FwdParams p) {
-  using Sh = FwdShared<D, RT>;
+template <int D, int RT, int W, bool kCap>
+__global__ void __launch_bounds__(32 * W, kSmWarps / W) paged_fwd_kernel(const __grid_constant__ FwdParams p) {
+  using Sh = FwdShared<D, RT, W>;
   constexpr int kStages = Sh::kStages, kGroups = Sh::kGroups, kPer = Sh::kPer, kK = D / 16, kRows = kRowTile * RT;
   extern __shared__ uint8_t raw[];
   uint8_t* const ring = raw + (-smem_u32(raw) & 255u);  // (addresses in it are XORed below bit 8)
@@ -654,7 +652,7 @@ __global__ void __launch_bounds__(kThreads, kCtas) paged_fwd_kernel(const __grid
     __syncthreads();
     const int64_t rec = 2 * static_cast<int64_t>(blockIdx.x) + (part > 0 ? 1 : 0);
     const int32_t live = min(kRows, p.R - run.rt * kRows);
-    for (int i = threadIdx.x; i < live * (D / 4); i += kThreads) {
+    for (int i = threadIdx.x; i < live * (D / 4); i += 32 * W) {
       const int row = i / (D / 4), d = i % (D / 4) * 4;
       float top = -INFINITY, sum = 0.f;
 #pragma unroll
@@ -791,7 +789,7 @@ Plan make_plan(const bsa_paged_fwd_args* a) {
   x.pairs = static_cast<int64_t>(a->B) * (a->select ? a->T : 1) * a->cache.Hkv * x.row_tiles;
   const int64_t longest = (a->select ? std::min(a->keep, a->M) : a->M) * a->cache.page, tiles = (longest + kTileKeys - 1) / kTileKeys;
   x.whole = tiles <= kWholeTiles && x.pairs <= INT32_MAX;
-  x.n_cta = static_cast<int32_t>(x.whole ? x.pairs : std::min<int64_t>(x.pairs * tiles, static_cast<int64_t>(num_sms()) * kCtas));
+  x.n_cta = static_cast<int32_t>(x.whole ? x.pairs : std::min<int64_t>(x.pairs * tiles, static_cast<int64_t>(num_sms())));
   x.stat_bytes = x.whole ? 0 : static_cast<size_t>(2 * x.n_cta) * 2 * rows * sizeof(float);
   x.o_bytes = x.whole ? 0 : static_cast<size_t>(2 * x.n_cta) * rows * a->cache.D * sizeof(float);
   return x;
@@ -799,10 +797,12 @@ Plan make_plan(const bsa_paged_fwd_args* a) {
 
 template <int D, int RT>
 bsa_status launch(const FwdParams& p, const Plan& x, cudaStream_t stream) {
-  auto kern = p.cap_log2 > 0.f ? paged_fwd_kernel<D, RT, true> : paged_fwd_kernel<D, RT, false>;
-  const bsa_status st = ensure_smem_attr(reinterpret_cast<const void*>(kern), kSmemBytes, "set paged forward smem size");
+  auto kern = p.whole ? (p.cap_log2 > 0.f ? paged_fwd_kernel<D, RT, kSmWarps / 2, true> : paged_fwd_kernel<D, RT, kSmWarps / 2, false>)
+                      : (p.cap_log2 > 0.f ? paged_fwd_kernel<D, RT, kSmWarps, true> : paged_fwd_kernel<D, RT, kSmWarps, false>);
+  const int warps = p.whole ? kSmWarps / 2 : kSmWarps;
+  const bsa_status st = ensure_smem_attr(reinterpret_cast<const void*>(kern), smem_bytes(warps), "set paged forward smem size");
   if (st != BSA_OK) return st;
-  cudaError_t e = launch_kernel(kern, dim3(p.n_cta), dim3(kThreads), kSmemBytes, stream, p);
+  cudaError_t e = launch_kernel(kern, dim3(p.n_cta), dim3(32 * warps), smem_bytes(warps), stream, p);
   if (e == cudaSuccess) e = cudaGetLastError();
   if (e != cudaSuccess) return cuda_fail(e, "paged forward launch");
   if (p.whole) return BSA_OK;
