@@ -386,6 +386,11 @@ def _lens(name: str, t: Optional[torch.Tensor], B: int, index: int) -> int:
     return 0 if t is None else _need(name, t, torch.int32, index, (B,))
 
 
+# a workspace for one call, on the stream that the call uses (an allocation by way of a tensor costs three times as much
+# beside a launch)
+_raw_alloc, _raw_free = torch._C._cuda_cudaCachingAllocator_raw_alloc, torch._C._cuda_cudaCachingAllocator_raw_delete
+
+
 def _workspace(need: int, device) -> Optional[torch.Tensor]:
     return torch.empty(need, dtype=torch.uint8, device=device) if need else None
 
@@ -681,16 +686,11 @@ def paged_select(q: torch.Tensor, cache: PagedCache, table: torch.Tensor, lens: 
     if lens is None:
         raise ValueError("lens is missing")
     head = (q.data_ptr(), *qs, _table(table, B, index), _lens("lens", lens, B, index), _lens("q_lens", q_lens, B, index))
-    M, pack = table.shape[1], _abi.PAGED_SELECT_REST.pack
-    tail = (B, Hq, M, T, keep, first, recent)
-    need = _workspace_size("bsa_paged_select", (index, cache.Hkv, D, cache.page, cache.pages, cache.bounds is None, *tail),
-                           lambda: cache._c + pack(*head, 0, *tail, 0, 0))
     ctx, handle = _place(dev, index, stream)
     with ctx:
-        out = torch.empty((B, cache.Hkv, T, keep), dtype=torch.int32, device=dev)
-        ws = _workspace(need, dev)
-        check(_abi.lib().bsa_paged_select(cache._c + pack(*head, out.data_ptr(), *tail, 0 if ws is None else ws.data_ptr(), need),
-                                          handle), "bsa_paged_select")
+        out = torch.empty((B, cache.Hkv, T, max(keep, 0)), dtype=torch.int32, device=dev)
+        args = cache._c + _abi.PAGED_SELECT_REST.pack(*head, out.data_ptr(), B, Hq, table.shape[1], T, keep, first, recent)
+        check(_abi.lib().bsa_paged_select(args, handle), "bsa_paged_select")
     return out
 
 
@@ -742,8 +742,12 @@ def paged_fwd(q: torch.Tensor, cache: PagedCache, table: torch.Tensor, lens: tor
                 logits_soft_cap or 0.0, sp, sn, skv)
         pack = _abi.PAGED_FWD_REST.pack
         need = _workspace_size("bsa_paged_fwd", (index, B, cache.Hkv, D, cache.page, Hq, M, T, keep), lambda: cache._c + pack(*head, 0, 0))
-        ws = _workspace(need, dev)
-        check(_abi.lib().bsa_paged_fwd(cache._c + pack(*head, 0 if ws is None else ws.data_ptr(), need), handle), "bsa_paged_fwd")
+        ws = _raw_alloc(need, handle) if need else 0
+        try:
+            check(_abi.lib().bsa_paged_fwd(cache._c + pack(*head, ws, need), handle), "bsa_paged_fwd")
+        finally:
+            if ws:
+                _raw_free(ws)
     return o, lse
 
 

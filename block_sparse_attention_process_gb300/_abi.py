@@ -129,8 +129,7 @@ class PagedAppendArgs(C.Structure):
 class PagedSelectArgs(C.Structure):
     _fields_ = [("cache", PagedCache), ("q", C.c_void_p), ("q_stride", C.c_int64 * 3), ("table", C.c_void_p),
                 ("lens", C.c_void_p), ("q_lens", C.c_void_p), ("index", C.c_void_p), ("B", C.c_int32), ("Hq", C.c_int32),
-                ("M", C.c_int64), ("T", C.c_int64), ("keep", C.c_int64), ("first", C.c_int64), ("recent", C.c_int64),
-                ("workspace", C.c_void_p), ("workspace_bytes", C.c_size_t)]
+                ("M", C.c_int64), ("T", C.c_int64), ("keep", C.c_int64), ("first", C.c_int64), ("recent", C.c_int64)]
 
 
 class PagedFwdArgs(C.Structure):
@@ -154,7 +153,7 @@ for _s, _rest in ((Kv4AppendArgs, KV4_APPEND_REST), (Kv4FwdArgs, KV4_FWD_REST)):
 PAGED_CACHE = struct.Struct("@2P6qPq3i0q")
 PAGED_RESIZE = struct.Struct("@8Pi3qi0q")
 PAGED_APPEND_REST = struct.Struct("@2P6qPiq")
-PAGED_SELECT_REST = struct.Struct("@P3q4P2i5qPN")
+PAGED_SELECT_REST = struct.Struct("@P3q4P2i5q")
 PAGED_FWD_REST = struct.Struct("@3P6q4P2i3qi2q2fP2iPN")
 assert PAGED_RESIZE.size == C.sizeof(PagedResizeArgs)
 for _s, _rest in ((PagedAppendArgs, PAGED_APPEND_REST), (PagedSelectArgs, PAGED_SELECT_REST), (PagedFwdArgs, PAGED_FWD_REST)):
@@ -185,7 +184,6 @@ SIGNATURES = {
     "bsa_paged_resize": (C.c_int, [C.c_void_p, C.c_void_p]),
     "bsa_paged_append": (C.c_int, [C.c_void_p, C.c_void_p]),
     "bsa_paged_select": (C.c_int, [C.c_void_p, C.c_void_p]),
-    "bsa_paged_select_workspace": (C.c_int, [C.c_void_p, C.POINTER(C.c_size_t)]),
     "bsa_paged_fwd": (C.c_int, [C.c_void_p, C.c_void_p]),
     "bsa_paged_fwd_workspace": (C.c_int, [C.c_void_p, C.POINTER(C.c_size_t)]),
     "bsa_get_device_error": (C.c_int, [C.c_void_p, C.POINTER(C.c_uint32)]),

@@ -82,8 +82,7 @@ bsa_status paged_resize_launch(const bsa_paged_resize_args* a, cudaStream_t stre
 bsa_status paged_append_launch(const bsa_paged_append_args* a, cudaStream_t stream);
 int64_t paged_append_units(const bsa_paged_append_args* a);  // CTAs of a sequence and head, with bounds
 bsa_status paged_select_launch(const bsa_paged_select_args* a, cudaStream_t stream);
-size_t paged_select_workspace_bytes(const bsa_paged_select_args* a);
-bool paged_select_fits(const bsa_paged_select_args* a);  // its grids
+bool paged_select_fits(const bsa_paged_select_args* a);  // its grid and shared memory
 bsa_status paged_fwd_launch(const bsa_paged_fwd_args* a, float scale, cudaStream_t stream);
 size_t paged_fwd_workspace_bytes(const bsa_paged_fwd_args* a);
 bool paged_fwd_fits(const bsa_paged_fwd_args* a);  // its grids

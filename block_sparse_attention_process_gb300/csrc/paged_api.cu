@@ -130,7 +130,7 @@ bsa_status check_select(const bsa_paged_select_args* a) {
   if (a->keep < 1) return bad("keep must be at least 1");
   if (a->first > a->keep || a->recent > a->keep - a->first) return bad("keep must be at least first + recent");
   if (a->keep > INT32_MAX / (static_cast<int64_t>(a->B) * a->cache.Hkv * a->T)) return unsupported("B*Hkv*T*keep must fit in int32");
-  if (!paged_select_fits(a)) return unsupported("too many pages for one launch");
+  if (!paged_select_fits(a)) return unsupported("more than 49152 pages a sequence, or too many queries for one launch");
   return BSA_OK;
 }
 
@@ -194,15 +194,6 @@ bsa_status bsa_paged_append(const bsa_paged_append_args* a, bsa_stream stream) {
   });
 }
 
-bsa_status bsa_paged_select_workspace(const bsa_paged_select_args* a, size_t* bytes) {
-  return guarded([&] {
-    if (!bytes) return bad("bytes is null");
-    const bsa_status s = check_select(a);
-    if (s == BSA_OK) *bytes = paged_select_workspace_bytes(a);
-    return s;
-  });
-}
-
 bsa_status bsa_paged_select(const bsa_paged_select_args* a, bsa_stream stream) {
   return guarded([&] {
     bsa_status s = check_select(a);
@@ -212,7 +203,6 @@ bsa_status bsa_paged_select(const bsa_paged_select_args* a, bsa_stream stream) {
     if (!aligned4(a->table) || !aligned4(a->lens) || !aligned4(a->q_lens) || !aligned4(a->index))
       return bad("table, lens, q_lens and index must be 4-byte aligned");
     s = check_strides(a->q_stride);
-    if (s == BSA_OK) s = check_workspace(a->workspace, a->workspace_bytes, paged_select_workspace_bytes(a));
     return s != BSA_OK ? s : paged_select_launch(a, static_cast<cudaStream_t>(stream));
   });
 }

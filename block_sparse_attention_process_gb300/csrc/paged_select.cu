@@ -8,13 +8,13 @@
 // one is 0) at most 2^22: multiples of 2^e that fp32 accumulators hold exactly, whatever the order.  2^f is the same for all of a
 // query's pages and is left out.  So the choice is one and the same for every way to split the work, and ties are real ties.
 //
-// First kernel: a warp scores 8 pages at a time as the narrow side of m16n8k16 products, the group's q heads being
-// the 16-row side.  The channels of a product's k axis are taken in an order that makes a thread's share of 8 pages 16-byte loads
-// straight from memory (thread t of a quad: channels 8 t .. 8 t + 7 of every 32), the four of a quad 64 bytes
-// side by side; nothing goes through shared memory but q.
-// Second kernel: one CTA a query.  Scores as ordered 32-bit keys, less the smallest; counts of their digits, from the
-// highest one on, give the least key that is kept and how many pages of it; then the kept pages in order, by
-// prefix sums.
+// One launch, a cluster a query.  A warp scores 8 pages at a time as the narrow side of m16n8k16 products, the group's q
+// heads being the 16-row side.  The channels of a product's k axis are taken in an order that makes a thread's share of 8
+// pages 16-byte loads straight from memory (thread t of a quad: channels 8 t .. 8 t + 7 of every 32), the four of a
+// quad 64 bytes side by side; nothing goes through shared memory but q.  The CTAs of the cluster take the pages in turn and write
+// the scores, as ordered 32-bit keys, to the first one's shared memory.  That one chooses: keys less the smallest; counts of
+// their digits, from the highest one on, give the least key that is kept and how many pages of it; then the
+// kept pages in order, by prefix sums.
 #include <algorithm>
 
 #include "paged.cuh"
@@ -22,10 +22,13 @@
 namespace bsa {
 namespace {
 
-constexpr int kScoreThreads = 128;
-constexpr int kScorePages = kScoreThreads / 4;  // pages of one CTA: 8 a warp
-constexpr int kPickThreads = 512;
+constexpr int kThreads = 512;
+constexpr int kWarps = kThreads / 32;
+constexpr int kSide = 2;               // groups of 8 pages that a warp has on their way at a time
+constexpr int kPassPages = kWarps * 8 * kSide;
+constexpr int kMaxCluster = 8;
 constexpr int kBins = 2048;
+constexpr int kMaxPages = 49152;        // keys that the first CTA's shared memory holds
 constexpr int kHeld = 8;  // keys a thread keeps in registers
 
 struct SelectParams {
@@ -34,11 +37,10 @@ struct SelectParams {
   int64_t qs[3];
   const int32_t *table, *lens, *q_lens;
   int32_t* index;
-  uint32_t* keys;  // [B, Hkv, T, M]
   int32_t B, Hkv, G, T, shift, pages;
   int64_t M;
   int32_t keep, first, recent;
-  int32_t chunks;  // CTAs that score a query's pages
+  int32_t cluster;
   uint32_t* err;
 };
 
@@ -62,90 +64,6 @@ __device__ __forceinline__ void mma_bf16(float (&c)[4], uint32_t a0, uint32_t a1
 __device__ __forceinline__ uint32_t ordered(float s) {
   const uint32_t x = __float_as_uint(s + 0.f);  // (-0 is 0)
   return (x >> 31) ? ~x : x | 0x80000000u;
-}
-
-template <int D>
-__global__ void __launch_bounds__(kScoreThreads) score_kernel(const __grid_constant__ SelectParams p) {
-  constexpr int kRow = 2 * D + 32;  // bf16 elements between rows of q (64 bytes of padding: two rows of a load in different banks)
-  constexpr int kChunks = 2 * D / 32;
-  __shared__ __align__(16) __nv_bfloat16 qc[16 * kRow];
-  __shared__ uint32_t tops[kScoreThreads / 32];
-  griddep_launch_dependents();
-  griddep_wait();
-  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5, g = lane >> 2, t4 = lane & 3;
-  const int32_t row = static_cast<int32_t>(blockIdx.x) / p.chunks, chunk = static_cast<int32_t>(blockIdx.x) % p.chunks;
-  const int32_t t = row % p.T, bh = row / p.T, b = bh / p.Hkv, h = bh % p.Hkv;
-  const int32_t j0 = chunk * kScorePages + warp * 8, j = j0 + g;  // this warp's pages, this quad's
-  // (the table's entry and q are on their way before the length is known)
-  const int32_t page = j < p.M ? p.table[b * p.M + j] : -1;
-  const __nv_bfloat16* q = p.q + b * p.qs[0] + static_cast<int64_t>(h) * p.G * p.qs[1] + t * p.qs[2];
-  uint32_t top = 0;
-  for (int i = threadIdx.x; i < p.G * (D / 8); i += kScoreThreads) {
-    const uint4 x = *reinterpret_cast<const uint4*>(q + (i / (D / 8)) * p.qs[1] + i % (D / 8) * 8);
-    const uint32_t m = __vmaxu2(__vmaxu2(x.x & 0x7FFF7FFFu, x.y & 0x7FFF7FFFu), __vmaxu2(x.z & 0x7FFF7FFFu, x.w & 0x7FFF7FFFu));
-    top = max(top, max(m & 0xFFFFu, m >> 16));
-  }
-  const int32_t n = pages_seen(p, b, t, chunk == 0 && threadIdx.x == 0 && h == 0 ? p.err : nullptr);
-  if (chunk * kScorePages >= n || n <= p.keep) return;  // (all are kept: nothing to score)
-  const bool known = j < n && page >= 0 && page < p.pages;
-  if (j < n && !known && t4 == 0 && p.err) atomicOr(p.err, DEV_ERR_BOUNDS);
-  const uint4* src = reinterpret_cast<const uint4*>(p.bounds + (static_cast<int64_t>(known ? page : 0) * p.Hkv + h) * 2 * D) + t4;
-  uint4 x[kChunks];
-#pragma unroll
-  for (int c = 0; c < kChunks; ++c) x[c] = known ? src[c * 4] : make_uint4(0, 0, 0, 0);
-  // ---- the group's unit
-  top = __reduce_max_sync(0xffffffffu, top);
-  if (lane == 0) tops[warp] = top;
-  __syncthreads();
-#pragma unroll
-  for (int w = 0; w < kScoreThreads / 32; ++w) top = max(top, tops[w]);
-  const float largest = __uint_as_float(top << 16);
-  float unit = 0.f, inv = 0.f;  // (codes are 0 then)
-  const bool usual = largest < kUsualTop;
-  if (usual) unit_of(largest, 6, unit, inv);
-  float best[2] = {-INFINITY, -INFINITY};  // pages 2 t4 and 2 t4 + 1 of the warp's
-  for (int32_t r0 = 0; r0 < p.G; r0 += 16) {
-    // ---- codes of 16 q heads (a head once more in rows past the last one)
-    if (r0 > 0) __syncthreads();
-    for (int i = threadIdx.x; i < 16 * (D / 8); i += kScoreThreads) {
-      const int r = i / (D / 8), d = i % (D / 8) * 8;
-      const uint4 y = *reinterpret_cast<const uint4*>(q + min(r0 + r, p.G - 1) * p.qs[1] + d);
-      const uint32_t w[4] = {y.x, y.y, y.z, y.w};
-      uint32_t up[4], down[4];
-#pragma unroll
-      for (int k = 0; k < 4; ++k) {
-        const float a = usual ? rintf(__uint_as_float(w[k] << 16) * inv) : 0.f, c = usual ? rintf(__uint_as_float(w[k] & 0xFFFF0000u) * inv) : 0.f;
-        up[k] = pack_bf16x2(fmaxf(a, 0.f), fmaxf(c, 0.f));
-        down[k] = pack_bf16x2(fminf(a, 0.f), fminf(c, 0.f));
-      }
-      *reinterpret_cast<uint4*>(&qc[r * kRow + d]) = make_uint4(up[0], up[1], up[2], up[3]);
-      *reinterpret_cast<uint4*>(&qc[r * kRow + D + d]) = make_uint4(down[0], down[1], down[2], down[3]);
-    }
-    __syncthreads();
-    float acc[2][4] = {};
-#pragma unroll
-    for (int c = 0; c < kChunks; ++c) {
-      const uint4 lo = *reinterpret_cast<const uint4*>(&qc[g * kRow + c * 32 + t4 * 8]);
-      const uint4 hi = *reinterpret_cast<const uint4*>(&qc[(g + 8) * kRow + c * 32 + t4 * 8]);
-      mma_bf16(acc[0], lo.x, hi.x, lo.y, hi.y, x[c].x, x[c].y);
-      mma_bf16(acc[1], lo.z, hi.z, lo.w, hi.w, x[c].z, x[c].w);
-    }
-    // heads g and g + 8
-#pragma unroll
-    for (int k = 0; k < 2; ++k) {
-      const float s0 = acc[0][k] + acc[1][k], s1 = acc[0][k + 2] + acc[1][k + 2];
-      best[k] = fmaxf(best[k], fmaxf(fabsf(s0) < INFINITY ? s0 : INFINITY, fabsf(s1) < INFINITY ? s1 : INFINITY));
-    }
-  }
-  const uint32_t ok = __ballot_sync(0xffffffffu, known);  // lane 4 g stands for page g
-  uint32_t* keys = p.keys + static_cast<int64_t>(row) * p.M;
-#pragma unroll
-  for (int k = 0; k < 2; ++k) {
-#pragma unroll
-    for (int o = 4; o < 32; o *= 2) best[k] = fmaxf(best[k], __shfl_xor_sync(0xffffffffu, best[k], o));
-    const int32_t i = 2 * t4 + k;
-    if (g == 0 && j0 + i < n) keys[j0 + i] = ordered(ok >> (4 * i) & 1u ? best[k] : -INFINITY);
-  }
 }
 
 // Exclusive prefix sums of two counts over the CTA.
@@ -192,41 +110,167 @@ struct Held {
   }
 };
 
-__global__ void __launch_bounds__(kPickThreads) pick_kernel(const __grid_constant__ SelectParams p) {
-  constexpr int kWarps = kPickThreads / 32, kPer = kBins / kPickThreads;
+__device__ __forceinline__ uint32_t cluster_rank() {
+  uint32_t r;
+  asm("mov.u32 %0, %%cluster_ctarank;" : "=r"(r));
+  return r;
+}
+__device__ __forceinline__ void cluster_arrive() { asm volatile("barrier.cluster.arrive.release;" ::: "memory"); }
+__device__ __forceinline__ void cluster_wait() { asm volatile("barrier.cluster.wait.acquire;" ::: "memory"); }
+
+template <int D>
+__global__ void __launch_bounds__(kThreads) select_kernel(const __grid_constant__ SelectParams p) {
+  constexpr int kRow = 2 * D + 32;  // bf16 elements between rows of q (64 bytes of padding: two rows of a load in different banks)
+  constexpr int kChunks = 2 * D / 32, kPer = kBins / kThreads;
+  extern __shared__ uint32_t keys[];  // of all pages, in the cluster's first CTA
+  __shared__ __align__(16) __nv_bfloat16 qc[16 * kRow];
   __shared__ uint32_t hist[kBins];
   __shared__ uint32_t least[kWarps], most[kWarps], warp_sum[kWarps];
   __shared__ uint32_t pick[3];
   __shared__ int32_t sums[kWarps][2];
   griddep_launch_dependents();
   griddep_wait();
-  const int64_t row = blockIdx.x;
-  const int32_t t = static_cast<int32_t>(row % p.T), b = static_cast<int32_t>(row / p.T / p.Hkv);
-  const int32_t n = pages_seen(p, b, t, nullptr), kept = min(n, p.keep);
-  int32_t* index = p.index + row * p.keep;
-  for (int32_t i = kept + threadIdx.x; i < p.keep; i += kPickThreads) index[i] = -1;
-  if (n <= p.keep) {
-    for (int32_t i = threadIdx.x; i < n; i += kPickThreads) index[i] = i;
+  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5, g = lane >> 2, t4 = lane & 3;
+  const int32_t cta = static_cast<int32_t>(cluster_rank()), row = static_cast<int32_t>(blockIdx.x) / p.cluster;
+  const int32_t t = row % p.T, bh = row / p.T, b = bh / p.Hkv, h = bh % p.Hkv;
+  int32_t j0 = cta * kPassPages + warp * 8 * kSide;  // this warp's pages; the quad's are j0 + g, j0 + 8 + g
+  // (the table's entries and q are on their way before the length is known)
+  const int32_t* table = p.table + b * p.M;
+  int32_t page[kSide];
+#pragma unroll
+  for (int y = 0; y < kSide; ++y) page[y] = j0 + 8 * y + g < p.M ? table[j0 + 8 * y + g] : -1;
+  const __nv_bfloat16* q = p.q + b * p.qs[0] + static_cast<int64_t>(h) * p.G * p.qs[1] + t * p.qs[2];
+  uint32_t top = 0;
+  for (int i = threadIdx.x; i < p.G * (D / 8); i += kThreads) {
+    const uint4 x = *reinterpret_cast<const uint4*>(q + (i / (D / 8)) * p.qs[1] + i % (D / 8) * 8);
+    const uint32_t m = __vmaxu2(__vmaxu2(x.x & 0x7FFF7FFFu, x.y & 0x7FFF7FFFu), __vmaxu2(x.z & 0x7FFF7FFFu, x.w & 0x7FFF7FFFu));
+    top = max(top, max(m & 0xFFFFu, m >> 16));
+  }
+  const int32_t n = pages_seen(p, b, t, cta == 0 && threadIdx.x == 0 && h == 0 ? p.err : nullptr);
+  int32_t* index = p.index + static_cast<int64_t>(row) * p.keep;
+  if (cta == 0)
+    for (int32_t i = min(n, p.keep) + threadIdx.x; i < p.keep; i += kThreads) index[i] = -1;
+  if (n <= p.keep) {  // (uniform over the cluster) all are kept: nothing to score
+    if (cta == 0)
+      for (int32_t i = threadIdx.x; i < n; i += kThreads) index[i] = i;
     return;
   }
-  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
-  // (n is above keep, which is at least first + recent: pages m0 .. m1 - 1 are chosen by their keys)
+  if (p.cluster > 1) cluster_arrive();  // (a CTA's shared memory is written once it is known to run)
+  // ---- the group's unit
+  top = __reduce_max_sync(0xffffffffu, top);
+  if (lane == 0) warp_sum[warp] = top;
+  __syncthreads();
+#pragma unroll
+  for (int w = 0; w < kWarps; ++w) top = max(top, warp_sum[w]);
+  const float largest = __uint_as_float(top << 16);
+  float unit = 0.f, inv = 0.f;  // (codes are 0 then)
+  const bool usual = largest < kUsualTop;
+  if (usual) unit_of(largest, 6, unit, inv);
+  // codes of 16 q heads (a head once more in rows past the last one)
+  auto code = [&](int32_t r0) {
+    for (int i = threadIdx.x; i < 16 * (D / 8); i += kThreads) {
+      const int r = i / (D / 8), d = i % (D / 8) * 8;
+      const uint4 y = *reinterpret_cast<const uint4*>(q + min(r0 + r, p.G - 1) * p.qs[1] + d);
+      const uint32_t w[4] = {y.x, y.y, y.z, y.w};
+      uint32_t up[4], down[4];
+#pragma unroll
+      for (int k = 0; k < 4; ++k) {
+        const float a = usual ? rintf(__uint_as_float(w[k] << 16) * inv) : 0.f, c = usual ? rintf(__uint_as_float(w[k] & 0xFFFF0000u) * inv) : 0.f;
+        up[k] = pack_bf16x2(fmaxf(a, 0.f), fmaxf(c, 0.f));
+        down[k] = pack_bf16x2(fminf(a, 0.f), fminf(c, 0.f));
+      }
+      *reinterpret_cast<uint4*>(&qc[r * kRow + d]) = make_uint4(up[0], up[1], up[2], up[3]);
+      *reinterpret_cast<uint4*>(&qc[r * kRow + D + d]) = make_uint4(down[0], down[1], down[2], down[3]);
+    }
+    __syncthreads();
+  };
+  uint32_t first_keys;  // the first CTA's `keys`
+  asm("mapa.shared::cluster.u32 %0, %1, %2;" : "=r"(first_keys) : "r"(smem_u32(keys)), "r"(0));
+  bool started = p.cluster == 1;
+  for (int32_t pass = 0; pass * p.cluster * kPassPages < n; ++pass) {  // (as many for every CTA of the cluster)
+    bool known[kSide];
+    uint4 x[kSide][kChunks];
+#pragma unroll
+    for (int y = 0; y < kSide; ++y) {
+      const int32_t j = j0 + 8 * y + g;
+      known[y] = j < n && page[y] >= 0 && page[y] < p.pages;
+      if (j < n && !known[y] && t4 == 0 && p.err) atomicOr(p.err, DEV_ERR_BOUNDS);
+      const uint4* src = reinterpret_cast<const uint4*>(p.bounds + (static_cast<int64_t>(known[y] ? page[y] : 0) * p.Hkv + h) * 2 * D) + t4;
+#pragma unroll
+      for (int c = 0; c < kChunks; ++c) x[y][c] = known[y] ? src[c * 4] : make_uint4(0, 0, 0, 0);
+      const int32_t next = j + p.cluster * kPassPages;
+      page[y] = next < n ? table[next] : -1;
+    }
+    float best[kSide][2];  // pages 2 t4 and 2 t4 + 1 of a group
+#pragma unroll
+    for (int y = 0; y < kSide; ++y) best[y][0] = best[y][1] = -INFINITY;
+    for (int32_t r0 = 0; r0 < p.G; r0 += 16) {
+      if (pass == 0 || p.G > 16) {
+        if (pass + r0 > 0) __syncthreads();
+        code(r0);
+      }
+      float acc[kSide][4] = {};
+#pragma unroll
+      for (int c = 0; c < kChunks; ++c) {
+        const uint4 lo = *reinterpret_cast<const uint4*>(&qc[g * kRow + c * 32 + t4 * 8]);
+        const uint4 hi = *reinterpret_cast<const uint4*>(&qc[(g + 8) * kRow + c * 32 + t4 * 8]);
+#pragma unroll
+        for (int y = 0; y < kSide; ++y) {
+          mma_bf16(acc[y], lo.x, hi.x, lo.y, hi.y, x[y][c].x, x[y][c].y);
+          mma_bf16(acc[y], lo.z, hi.z, lo.w, hi.w, x[y][c].z, x[y][c].w);
+        }
+      }
+      // heads g and g + 8
+#pragma unroll
+      for (int y = 0; y < kSide; ++y)
+#pragma unroll
+        for (int k = 0; k < 2; ++k) {
+          const float s0 = acc[y][k], s1 = acc[y][k + 2];
+          best[y][k] = fmaxf(best[y][k], fmaxf(fabsf(s0) < INFINITY ? s0 : INFINITY, fabsf(s1) < INFINITY ? s1 : INFINITY));
+        }
+    }
+    if (!started) cluster_wait();
+    started = true;
+#pragma unroll
+    for (int y = 0; y < kSide; ++y) {
+      const uint32_t ok = __ballot_sync(0xffffffffu, known[y]);  // lane 4 g stands for page g
+#pragma unroll
+      for (int k = 0; k < 2; ++k) {
+#pragma unroll
+        for (int o = 4; o < 32; o *= 2) best[y][k] = fmaxf(best[y][k], __shfl_xor_sync(0xffffffffu, best[y][k], o));
+        const int32_t i = 2 * t4 + k, j = j0 + 8 * y + i;
+        if (g == 0 && j < n)
+          asm volatile("st.shared::cluster.u32 [%0], %1;" ::"r"(first_keys + 4 * j), "r"(ordered(ok >> (4 * i) & 1u ? best[y][k] : -INFINITY)) : "memory");
+      }
+    }
+    j0 += p.cluster * kPassPages;
+  }
+  if (p.cluster > 1) {
+    cluster_arrive();
+    cluster_wait();
+  }
+  if (cta > 0) return;
+  // ---- the choice (n is above keep, which is at least first + recent: pages m0 .. m1 - 1 are chosen by their keys)
   const int32_t m0 = p.first, m1 = n - p.recent;
   uint32_t want = static_cast<uint32_t>(p.keep - p.first - p.recent);
+  for (int32_t i = threadIdx.x; i < p.first; i += kThreads) index[i] = i;
+  for (int32_t i = threadIdx.x; i < p.recent; i += kThreads) index[p.keep - p.recent + i] = m1 + i;
+  if (want == 0) return;
+#pragma unroll
+  for (int i = 0; i < kPer; ++i) hist[i * kThreads + threadIdx.x] = 0;
+  __syncthreads();  // (a lone CTA's own keys)
+  // a run of pages a thread (odd: a warp's runs start in different banks)
+  const int32_t per = (m1 - m0 + kThreads - 1) / kThreads | 1;
   Held mine;
-  const int32_t per = (m1 - m0 + kPickThreads - 1) / kPickThreads;
-  mine.keys = p.keys + row * p.M;
+  mine.keys = keys;
   mine.i0 = m0 + static_cast<int32_t>(threadIdx.x) * per;
   mine.i1 = min(mine.i0 + per, m1);
   mine.held = per <= kHeld;
   if (mine.held) {
 #pragma unroll
-    for (int i = 0; i < kHeld; ++i) mine.k[i] = mine.i0 + i < mine.i1 ? mine.keys[mine.i0 + i] : 0u;
+    for (int i = 0; i < kHeld; ++i) mine.k[i] = mine.i0 + i < mine.i1 ? keys[mine.i0 + i] : 0u;
   }
-  for (int32_t i = threadIdx.x; i < p.first; i += kPickThreads) index[i] = i;
-  for (int32_t i = threadIdx.x; i < p.recent; i += kPickThreads) index[p.keep - p.recent + i] = m1 + i;
-  if (want == 0) return;
-  // ---- the range of the keys: its digits, not the floats', spread them over the bins
+  // the range of the keys: its digits, not the floats', spread them over the bins
   uint32_t lo = ~0u, hi = 0u;
   mine.each([&](int32_t, uint32_t k) {
     lo = min(lo, k);
@@ -238,16 +282,14 @@ __global__ void __launch_bounds__(kPickThreads) pick_kernel(const __grid_constan
     least[warp] = lo;
     most[warp] = hi;
   }
-#pragma unroll
-  for (int i = 0; i < kPer; ++i) hist[i * kPickThreads + threadIdx.x] = 0;
   __syncthreads();
 #pragma unroll
   for (int w = 0; w < kWarps; ++w) {
     lo = min(lo, least[w]);
     hi = max(hi, most[w]);
   }
-  // ---- the least kept key, from its highest digit on: of key - lo, the bits above `shift` are `digits`, and of the pages
-  // that share them `want` are kept
+  // the least kept key, from its highest digit on: of key - lo, the bits above `shift` are `digits`, and of the pages that
+  // share them `want` are kept
   int shift = 32 - __clz(hi - lo);
   uint32_t digits = 0;
   bool all = shift == 0;  // (equal keys)
@@ -255,23 +297,23 @@ __global__ void __launch_bounds__(kPickThreads) pick_kernel(const __grid_constan
     const int bits = min(shift, 11);
     shift -= bits;
     mine.each([&](int32_t, uint32_t k) {
-      const uint32_t x = (k - lo) >> shift;
-      if (x >> bits == digits) atomicAdd(&hist[x & ((1u << bits) - 1)], 1u);
+      const uint32_t y = (k - lo) >> shift;
+      if (y >> bits == digits) atomicAdd(&hist[y & ((1u << bits) - 1)], 1u);
     });
     __syncthreads();
     // suffix sums: thread i has kPer bins, counted from the top
-    const int top = kBins - 1 - kPer * static_cast<int>(threadIdx.x);
+    const int first_bin = kBins - 1 - kPer * static_cast<int>(threadIdx.x);
     uint32_t c[kPer], sum = 0;
 #pragma unroll
     for (int i = 0; i < kPer; ++i) {
-      sum += c[i] = hist[top - i];
-      hist[top - i] = 0;
+      sum += c[i] = hist[first_bin - i];
+      hist[first_bin - i] = 0;
     }
     uint32_t inc = sum;
 #pragma unroll
     for (int o = 1; o < 32; o *= 2) {
-      const uint32_t x = __shfl_up_sync(0xffffffffu, inc, o);
-      if (lane >= o) inc += x;
+      const uint32_t y = __shfl_up_sync(0xffffffffu, inc, o);
+      if (lane >= o) inc += y;
     }
     if (lane == 31) warp_sum[warp] = inc;
     __syncthreads();
@@ -280,7 +322,7 @@ __global__ void __launch_bounds__(kPickThreads) pick_kernel(const __grid_constan
 #pragma unroll
     for (int i = 0; i < kPer; ++i) {
       if (above < want && want <= above + c[i]) {
-        pick[0] = top - i;
+        pick[0] = first_bin - i;
         pick[1] = want - above;
         pick[2] = c[i];
       }
@@ -291,36 +333,54 @@ __global__ void __launch_bounds__(kPickThreads) pick_kernel(const __grid_constan
     want = pick[1];
     all = shift == 0 || pick[2] == want;
   }
-  // ---- kept pages in order: those above the least digits, and the first `want` ones at them
+  // kept pages in order: those above the least digits, and the first `want` ones at them
   int32_t more = 0, same = 0;
   mine.each([&](int32_t, uint32_t k) {
-    const uint32_t x = (k - lo) >> shift;
-    more += x > digits;
-    same += x == digits;
+    const uint32_t y = (k - lo) >> shift;
+    more += y > digits;
+    same += y == digits;
   });
   block_prefix(more, same, sums);
   index += p.first;
   mine.each([&](int32_t i, uint32_t k) {
-    const uint32_t x = (k - lo) >> shift;
-    if (x > digits) {
+    const uint32_t y = (k - lo) >> shift;
+    if (y > digits) {
       index[more++ + min(same, static_cast<int32_t>(want))] = i;
-    } else if (x == digits) {
+    } else if (y == digits) {
       if (same < static_cast<int32_t>(want)) index[more + same] = i;
       ++same;
     }
   });
 }
 
-}  // namespace
-
-static int64_t score_chunks(const bsa_paged_select_args* a) { return (a->M + kScorePages - 1) / kScorePages; }
-
-bool paged_select_fits(const bsa_paged_select_args* a) {
-  return score_chunks(a) <= INT32_MAX / (static_cast<int64_t>(a->B) * a->cache.Hkv * a->T);
+template <int D>
+bsa_status launch(const SelectParams& p, cudaStream_t stream) {
+  const bsa_status st = ensure_smem_attr(reinterpret_cast<const void*>(select_kernel<D>), kMaxPages * sizeof(uint32_t), "set page selection smem size");
+  if (st != BSA_OK) return st;
+  cudaLaunchConfig_t cfg{};
+  cfg.gridDim = dim3(static_cast<unsigned>(static_cast<int64_t>(p.B) * p.Hkv * p.T * p.cluster));
+  cfg.blockDim = dim3(kThreads);
+  cfg.dynamicSmemBytes = static_cast<size_t>(p.M) * sizeof(uint32_t);
+  cfg.stream = stream;
+  cudaLaunchAttribute attr[2];
+  attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  attr[0].val.programmaticStreamSerializationAllowed = pdl_enabled() ? 1 : 0;
+  attr[1].id = cudaLaunchAttributeClusterDimension;
+  attr[1].val.clusterDim.x = static_cast<unsigned>(p.cluster);
+  attr[1].val.clusterDim.y = 1;
+  attr[1].val.clusterDim.z = 1;
+  cfg.attrs = attr;
+  cfg.numAttrs = 2;
+  cudaError_t e = cudaLaunchKernelEx(&cfg, select_kernel<D>, p);
+  if (e == cudaSuccess) e = cudaGetLastError();
+  if (e != cudaSuccess) return cuda_fail(e, "paged select launch");
+  return BSA_OK;
 }
 
-size_t paged_select_workspace_bytes(const bsa_paged_select_args* a) {
-  return static_cast<size_t>(a->B) * a->cache.Hkv * a->T * a->M * sizeof(uint32_t);
+}  // namespace
+
+bool paged_select_fits(const bsa_paged_select_args* a) {
+  return a->M <= kMaxPages && static_cast<int64_t>(a->B) * a->cache.Hkv <= INT32_MAX / kMaxCluster / a->T;
 }
 
 bsa_status paged_select_launch(const bsa_paged_select_args* a, cudaStream_t stream) {
@@ -332,7 +392,6 @@ bsa_status paged_select_launch(const bsa_paged_select_args* a, cudaStream_t stre
   p.lens = a->lens;
   p.q_lens = a->q_lens;
   p.index = a->index;
-  p.keys = static_cast<uint32_t*>(a->workspace);
   p.B = a->B;
   p.Hkv = a->cache.Hkv;
   p.G = a->Hq / a->cache.Hkv;
@@ -345,17 +404,11 @@ bsa_status paged_select_launch(const bsa_paged_select_args* a, cudaStream_t stre
   p.recent = static_cast<int32_t>(a->recent);
   p.err = device_error_word();
   if (!p.err) return fail(BSA_ERR_CUDA, "could not allocate the device error word");
-  cudaError_t e;
-  p.chunks = static_cast<int32_t>(score_chunks(a));
-  const dim3 grid(static_cast<unsigned>(p.chunks * a->B * a->cache.Hkv * a->T));
-  e = a->cache.D == 128 ? launch_kernel(score_kernel<128>, grid, dim3(kScoreThreads), 0, stream, p)
-                        : launch_kernel(score_kernel<64>, grid, dim3(kScoreThreads), 0, stream, p);
-  if (e == cudaSuccess) e = cudaGetLastError();
-  if (e != cudaSuccess) return cuda_fail(e, "paged score launch");
-  e = launch_kernel(pick_kernel, dim3(static_cast<unsigned>(a->B * a->cache.Hkv * a->T)), dim3(kPickThreads), 0, stream, p);
-  if (e == cudaSuccess) e = cudaGetLastError();
-  if (e != cudaSuccess) return cuda_fail(e, "paged select launch");
-  return BSA_OK;
+  // CTAs a query: more while all of them have room at once and a pass of pages each
+  const int64_t queries = static_cast<int64_t>(p.B) * p.Hkv * p.T;
+  p.cluster = 1;
+  while (p.cluster < kMaxCluster && queries * p.cluster * 2 <= num_sms() && p.cluster * kPassPages < p.M) p.cluster *= 2;
+  return a->cache.D == 128 ? launch<128>(p, stream) : launch<64>(p, stream);
 }
 
 }  // namespace bsa

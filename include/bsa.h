@@ -553,11 +553,9 @@ typedef struct {
   const int32_t* q_lens;   /* device int32 [B], or NULL (= T) */
   int32_t* index;          /* device int32 [B, Hkv, T, keep], written */
   int32_t B, Hq;
-  int64_t M, T;
+  int64_t M, T;            /* M up to 49152 */
   int64_t keep;            /* pages to choose, >= 1, >= first + recent */
   int64_t first, recent;   /* the first and the last pages that a query sees are always chosen, this many */
-  void* workspace;         /* device, 16-byte aligned, bsa_paged_select_workspace bytes */
-  size_t workspace_bytes;
 } bsa_paged_select_args;
 
 /* For every query (new token and key head, its group of q heads together) the
@@ -574,7 +572,6 @@ typedef struct {
  * as a score of minus infinity; both set the bounds bit of the device error
  * word. */
 BSA_API bsa_status bsa_paged_select(const bsa_paged_select_args* args, bsa_stream stream);
-BSA_API bsa_status bsa_paged_select_workspace(const bsa_paged_select_args* args, size_t* bytes);
 
 typedef struct {
   bsa_paged_cache cache;   /* (bounds are not used) */

@@ -362,6 +362,30 @@ def test_select_sums_stay_exact():
         assert np.array_equal(got.cpu().numpy(), want_select(cache, table, q, [n * 16], keep, 0, 0))
 
 
+@pytest.mark.parametrize("n,queries,keep", [(49152, 1, 500), (20000, 1, 2049), (9000, 24, 33), (300, 600, 17)])
+def test_select_of_many_pages(n, queries, keep):
+    """Up to the most pages a sequence can have; many queries to a launch."""
+    bsa = bsa_()
+    D, P = 64, n + 1
+    g = torch.Generator(device="cuda").manual_seed(n)
+    k = torch.zeros((P, 1, 16, D), dtype=torch.bfloat16, device="cuda")
+    code = torch.randint(-256, 257, (P, 1, 2, D), generator=g, device="cuda")
+    bounds = (torch.sort(code, dim=2, descending=True).values * 2.0 ** torch.randint(-9, -6, (P, 1, 1, 1), generator=g, device="cuda")).to(torch.bfloat16)
+    cache = bsa.PagedCache(k, k, bounds)
+    table = torch.randperm(P, generator=g, device="cuda")[:n].to(torch.int32).expand(queries, n).contiguous()
+    q = torch.randn((queries, 2, 1, D), generator=g, device="cuda").to(torch.bfloat16)
+    got = bsa.paged_select(q, cache, table, i32([n * 16] * queries), keep, first=2, recent=1)
+    qc = q.double() / 2.0 ** (torch.floor(torch.log2(q.double().abs().amax((1, 2, 3), keepdim=True))) - 6)
+    qc = torch.round(qc)[:, :, 0].flatten(0, 1)
+    b = bounds[table[0].long(), 0].double()
+    s = (qc.clamp(min=0) @ b[:, 0].T + qc.clamp(max=0) @ b[:, 1].T).view(queries, 2, n).amax(1)
+    s[:, :2], s[:, -1] = float("inf"), float("inf")
+    want = torch.sort(torch.sort(s, dim=-1, descending=True, stable=True).indices[:, :keep], dim=-1).values
+    assert torch.equal(got.view(queries, keep).long(), want)
+    with pytest.raises(bsa.BsaError):
+        bsa.paged_select(q[:1], cache, torch.zeros((1, 49153), dtype=torch.int32, device="cuda"), i32([16]), 4)
+
+
 def test_select_reports_bad_tables_and_lengths():
     bsa = bsa_()
     cache, table, _, _ = paged_batch(bsa, 1, 1, 64, 16, [160], 9)

@@ -39,8 +39,7 @@ def append_args(abi, cache_kw=None, **kw):
 
 
 def select_args(abi, cache_kw=None, **kw):
-    return made(abi.PagedSelectArgs(cache(abi, **(cache_kw or {})), 16, I3(512, 128, 128), 32, 48, None, 64, 2, 4, 4, 1, 2, 1, 1,
-                                    80, 1 << 40), kw)
+    return made(abi.PagedSelectArgs(cache(abi, **(cache_kw or {})), 16, I3(512, 128, 128), 32, 48, None, 64, 2, 4, 4, 1, 2, 1, 1), kw)
 
 
 def fwd_args(abi, cache_kw=None, **kw):
@@ -104,21 +103,16 @@ def test_append_refuses(kw, status):
     ({"T": 0}, "INVALID_ARG"), ({"T": 1 << 30}, "UNSUPPORTED"), ({"M": 0}, "INVALID_ARG"), ({"M": 1 << 27}, "UNSUPPORTED"),
     ({"keep": 0, "first": 0, "recent": 0}, "INVALID_ARG"), ({"keep": 1}, "INVALID_ARG"), ({"first": -1}, "INVALID_ARG"),
     ({"recent": -1}, "INVALID_ARG"), ({"recent": 1 << 62}, "INVALID_ARG"), ({"keep": 1 << 40}, "UNSUPPORTED"),
-    ({"q_stride": I3(512, 12, 128)}, "INVALID_ARG"), ({"workspace": None}, "INVALID_ARG"), ({"workspace": 8}, "INVALID_ARG"),
-    ({"workspace_bytes": 4}, "INVALID_ARG"),
+    ({"q_stride": I3(512, 12, 128)}, "INVALID_ARG"), ({"M": 49153}, "UNSUPPORTED"),
 ])
 def test_select_refuses(kw, status):
     abi = _abi()
     refused(abi, "bsa_paged_select", select_args(abi, **kw), status)
 
 
-def test_select_needs_bounds_and_no_rows():
+def test_select_needs_bounds():
     abi = _abi()
     refused(abi, "bsa_paged_select", select_args(abi, cache_kw={"bounds": None}), "INVALID_ARG")
-    need = C.c_size_t(0)
-    a = select_args(abi, cache_kw={"k": None, "v": None})
-    assert abi.lib().bsa_paged_select_workspace(C.byref(a), C.byref(need)) == abi.OK and need.value > 0
-    assert abi.lib().bsa_paged_select_workspace(C.byref(a), None) == abi.INVALID_ARG
 
 
 @pytest.mark.parametrize("kw,status", [
