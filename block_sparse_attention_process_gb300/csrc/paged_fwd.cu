@@ -129,8 +129,10 @@ __device__ __forceinline__ int64_t total_units(const FwdParams& p, int32_t s, in
 __device__ __forceinline__ int32_t runs(const FwdParams& p, int64_t total) {
   return static_cast<int32_t>(min(static_cast<int64_t>(p.n_cta), total));
 }
-__device__ __forceinline__ int64_t quotient(int64_t a, int64_t b) {  // of non-negative numbers, mostly small ones
-  return ((a | b) >> 32) == 0 ? static_cast<int64_t>(static_cast<uint32_t>(a) / static_cast<uint32_t>(b)) : a / b;
+// Of non-negative numbers, mostly small ones.  (Out of line: a kernel's first instructions come out of a cold cache.)
+__device__ __noinline__ int64_t quotient64(int64_t a, int64_t b) { return a / b; }
+__device__ __forceinline__ int64_t quotient(int64_t a, int64_t b) {
+  return ((a | b) >> 32) == 0 ? static_cast<int64_t>(static_cast<uint32_t>(a) / static_cast<uint32_t>(b)) : quotient64(a, b);
 }
 __device__ __forceinline__ int64_t first_unit(int64_t c, int64_t total, int32_t n) { return quotient(c * total, n); }
 __device__ __forceinline__ int32_t cta_of(int64_t t, int64_t total, int32_t n) {
@@ -239,8 +241,8 @@ struct Run {
 };
 
 // Row r of a pair: q head and token.
-__device__ __forceinline__ int32_t row_head(const FwdParams& p, int32_t h, int32_t r) { return h * p.G + (p.select ? r : r / p.T); }
-__device__ __forceinline__ int32_t row_token(const FwdParams& p, int32_t s, int32_t r) { return p.select ? s % p.queries : r % p.T; }
+__device__ __forceinline__ int32_t row_head(const FwdParams& p, int32_t h, int32_t r) { return h * p.G + (p.select || p.T == 1 ? r : r / p.T); }
+__device__ __forceinline__ int32_t row_token(const FwdParams& p, int32_t s, int32_t r) { return p.T == 1 ? 0 : p.select ? s % p.queries : r % p.T; }
 
 // ------------------------------------------------------------------ loads and products
 
@@ -473,7 +475,7 @@ __global__ void __launch_bounds__(32 * W, kSmWarps / W) paged_fwd_kernel(const _
     for (int i = 0; i < D / 8; ++i) acc[i][0] = acc[i][1] = acc[i][2] = acc[i][3] = 0.f;
     // ---- q by way of the ring's last stage (free until the first step), then the first stages
     const uint32_t q_at = ring0 + (kStages - 1) * Sh::kStageBytes + tile * kRowTile * D * 2;
-#pragma unroll
+#pragma unroll 1
     for (int x = 0; x < kRowTile * kLanes / 32; ++x) {
       const int row = x * (32 / kLanes) + lane / kLanes;
       const int32_t r = run.rt * kRows + tile * kRowTile + row, rr = min(r, p.R - 1);
@@ -481,41 +483,44 @@ __global__ void __launch_bounds__(32 * W, kSmWarps / W) paged_fwd_kernel(const _
       copy16(q_at + row * D * 2 + ((lane % kLanes ^ (row & 7)) << 4), src, r < p.R);
     }
     copy_commit();
-    for (int i = 0; i < kStages - 1; ++i) issue(i, i);
-    // ---- this thread's two rows: the keys they see
+    // this thread's two rows: the keys they see
     int32_t lo[2], hi[2];
-    bool real[2];  // (others' sums are not used)
+    bool real[2] = {false, false};  // (others' sums are not used)
     int32_t all_lo = 0, all_hi = INT32_MAX;  // keys that every row of the tile sees
-#pragma unroll
-    for (int i = 0; i < 2; ++i) {
-      const int32_t r = run.rt * kRows + tile * kRowTile + g + 8 * i, t = row_token(p, pair.s, r);
-      const int32_t pos = pair.len - pair.nq + t;
-      real[i] = r < p.R && t < pair.nq && pos >= 0;
-      hi[i] = real[i] ? pos : -1;
-      lo[i] = real[i] ? first_key(p, pos) : 0;
-      if (real[i]) {
-        all_lo = max(all_lo, lo[i]);
-        all_hi = min(all_hi, hi[i]);
-      }
-    }
-    all_lo = __reduce_max_sync(0xffffffffu, all_lo);
-    all_hi = __reduce_min_sync(0xffffffffu, all_hi);
-    copy_wait<kStages - 1>();
-    __syncwarp();
     uint32_t qa[kK][4];
-#pragma unroll
-    for (int k = 0; k < kK; ++k) {
-      const uint32_t at = q_at + (lane & 15) * D * 2;
-      ldsm4(qa[k], at + ((2 * k + (lane >> 4) ^ (lane & 7)) << 4));
-    }
     // fragments: row lane & 7 (+ 8) of a matrix, its 16-byte chunks 2 k (+ 1), as XOR of the lane's first address
     const uint32_t lane_kf = ring0 + ((lane & 7) + (lane >> 4) * 8) * D * 2 + (((lane >> 3 & 1) ^ (lane & 7)) << 4);
     const uint32_t lane_vf = ring0 + kUnit * D * 2 + (lane & 15) * D * 2 + (((lane >> 4) ^ (lane & 7)) << 4);
-    int stage = 0, stage_in = kStages - 1;
-    for (int32_t i = 0; i < steps; ++i) {
-      copy_wait<kStages - 2>();
-      group_sync<RT>(group);
+    int stage = 0, stage_in = 0;
+    // (the first kStages - 1 turns only load: one copy of the loading code, out of a cold instruction cache)
+#pragma unroll 1
+    for (int32_t i = 1 - kStages; i < steps; ++i) {
+      if (i >= 0) {
+        copy_wait<kStages - 2>();
+        if (i == 0) {
+          __syncwarp();
+#pragma unroll
+          for (int k = 0; k < kK; ++k) ldsm4(qa[k], q_at + (lane & 15) * D * 2 + ((2 * k + (lane >> 4) ^ (lane & 7)) << 4));
+#pragma unroll
+          for (int r = 0; r < 2; ++r) {
+            const int32_t rr = run.rt * kRows + tile * kRowTile + g + 8 * r, t = row_token(p, pair.s, rr);
+            const int32_t at = pair.len - pair.nq + t;
+            real[r] = rr < p.R && t < pair.nq && at >= 0;
+            hi[r] = real[r] ? at : -1;
+            lo[r] = real[r] ? first_key(p, at) : 0;
+            if (real[r]) {
+              all_lo = max(all_lo, lo[r]);
+              all_hi = min(all_hi, hi[r]);
+            }
+          }
+          all_lo = __reduce_max_sync(0xffffffffu, all_lo);
+          all_hi = __reduce_min_sync(0xffffffffu, all_hi);
+        }
+        group_sync<RT>(group);
+      }
       issue(i + kStages - 1, stage_in);
+      stage_in = stage_in + 1 == kStages ? 0 : stage_in + 1;
+      if (i < 0) continue;
       const uint32_t at = stage * Sh::kStageBytes;
       int32_t pos[kPer];
       bool any = false, masked = false;
@@ -525,7 +530,6 @@ __global__ void __launch_bounds__(32 * W, kSmWarps / W) paged_fwd_kernel(const _
         any |= pos[y] != kNoKeys;
         masked |= pos[y] < all_lo || pos[y] + kUnit - 1 > all_hi;
       }
-      stage_in = stage;
       stage = stage + 1 == kStages ? 0 : stage + 1;
       if (!any) continue;  // (uniform over the group)
       // ---- scores of 16 keys: element (row g + 8 (e / 2), key 8 c + 2 t4 + e % 2) is s[.][c][e]
