@@ -647,8 +647,7 @@ def paged_resize(table: torch.Tensor, free: torch.Tensor, used: torch.Tensor, le
             _need("used", used, torch.int32, index, (1,)), _lens("lens", lens, B, index), _lens("new_lens", new_lens, B, index))
     ctx, handle = _place(table.device, index, stream)
     with ctx:
-        out = torch.empty((B,), dtype=torch.int32, device=table.device)
-        used_out = torch.empty((1,), dtype=torch.int32, device=table.device)
+        out, used_out = torch.empty_like(lens), torch.empty_like(used)
         slots = torch.empty((B, max(T, 0)), dtype=torch.int32, device=table.device)
         check(_abi.lib().bsa_paged_resize(
             _abi.PAGED_RESIZE.pack(*head, out.data_ptr(), used_out.data_ptr(), slots.data_ptr(), B, table.shape[1], T, free.numel(),
@@ -726,7 +725,7 @@ def paged_fwd(q: torch.Tensor, cache: PagedCache, table: torch.Tensor, lens: tor
     ctx, handle = _place(dev, index, stream)
     with ctx:
         if o is None:
-            o = torch.empty((B, Hq, T, D), dtype=torch.bfloat16, device=dev)
+            o = torch.empty_like(q) if q.is_contiguous() else torch.empty((B, Hq, T, D), dtype=torch.bfloat16, device=dev)
             os = (Hq * T * D, T * D, D)
         elif o.shape != q.shape:
             raise ValueError("o must have q's shape")

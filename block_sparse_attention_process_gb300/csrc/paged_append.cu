@@ -14,7 +14,8 @@
 namespace bsa {
 namespace {
 
-constexpr int kThreads = 256;
+constexpr int kThreads = 128;  // (256: 54 us for 4 x 8 x 8191 tokens, 128: 44)
+constexpr int kBatch = 4;      // rows that a thread has on their way at a time
 
 struct AppendParams {
   bsa_paged_cache c;
@@ -36,23 +37,36 @@ __global__ void __launch_bounds__(kThreads) append_rows_kernel(const __grid_cons
   constexpr int kLanes = D / 8;
   griddep_launch_dependents();
   griddep_wait();
-  const int u = threadIdx.x % kLanes, sub = threadIdx.x / kLanes;
-  const int64_t rows = p.B * p.T * p.c.Hkv, limit = p.c.pages << p.shift;
-  // rows in order of (b, h, t)
-  for (int64_t r = static_cast<int64_t>(blockIdx.x) * (kThreads / kLanes) + sub; r < rows;
-       r += static_cast<int64_t>(gridDim.x) * (kThreads / kLanes)) {
-    const int64_t bh = r / p.T, t = r - bh * p.T;
-    const int32_t b = static_cast<int32_t>(bh / p.c.Hkv), h = static_cast<int32_t>(bh - static_cast<int64_t>(b) * p.c.Hkv);
-    const int32_t slot = p.slots[b * p.T + t];
-    if (slot < 0) continue;
-    if (slot >= limit) {
-      if (u == 0 && p.err) atomicOr(p.err, DEV_ERR_BOUNDS);
-      continue;
+  constexpr uint32_t kSubs = kThreads / kLanes;
+  const int u = threadIdx.x % kLanes;
+  const uint32_t T = static_cast<uint32_t>(p.T), rows = static_cast<uint32_t>(p.B) * p.c.Hkv * T;  // (below 2^31)
+  const int64_t limit = p.c.pages << p.shift;
+  // rows in order of (b, h, t), kBatch at a time
+  for (uint32_t r0 = blockIdx.x * kBatch * kSubs + threadIdx.x / kLanes; r0 < rows; r0 += gridDim.x * kBatch * kSubs) {
+    int32_t slot[kBatch], h[kBatch];
+    uint4 k[kBatch], v[kBatch];
+#pragma unroll
+    for (int x = 0; x < kBatch; ++x) {
+      const uint32_t r = r0 + x * kSubs;
+      slot[x] = -1;
+      if (r >= rows) continue;
+      const uint32_t bh = r / T, t = r - bh * T, b = bh / p.c.Hkv;
+      h[x] = static_cast<int32_t>(bh - b * p.c.Hkv);
+      slot[x] = p.slots[b * T + t];
+      // (read before the slot is known: it is the call's own memory)
+      k[x] = __ldcs(reinterpret_cast<const uint4*>(p.k + b * p.ks[0] + h[x] * p.ks[1] + t * p.ks[2] + 8 * u));
+      v[x] = __ldcs(reinterpret_cast<const uint4*>(p.v + b * p.vs[0] + h[x] * p.vs[1] + t * p.vs[2] + 8 * u));
     }
-    const uint4 k = __ldcs(reinterpret_cast<const uint4*>(p.k + b * p.ks[0] + h * p.ks[1] + t * p.ks[2] + 8 * u));
-    const uint4 v = __ldcs(reinterpret_cast<const uint4*>(p.v + b * p.vs[0] + h * p.vs[1] + t * p.vs[2] + 8 * u));
-    *reinterpret_cast<uint4*>(static_cast<__nv_bfloat16*>(p.c.k) + page_at(p.c.k_stride, slot, p.shift, h) + 8 * u) = k;
-    *reinterpret_cast<uint4*>(static_cast<__nv_bfloat16*>(p.c.v) + page_at(p.c.v_stride, slot, p.shift, h) + 8 * u) = v;
+#pragma unroll
+    for (int x = 0; x < kBatch; ++x) {
+      if (slot[x] < 0) continue;
+      if (slot[x] >= limit) {
+        if (u == 0 && p.err) atomicOr(p.err, DEV_ERR_BOUNDS);
+        continue;
+      }
+      *reinterpret_cast<uint4*>(static_cast<__nv_bfloat16*>(p.c.k) + page_at(p.c.k_stride, slot[x], p.shift, h[x]) + 8 * u) = k[x];
+      *reinterpret_cast<uint4*>(static_cast<__nv_bfloat16*>(p.c.v) + page_at(p.c.v_stride, slot[x], p.shift, h[x]) + 8 * u) = v[x];
+    }
   }
 }
 
@@ -116,7 +130,6 @@ __global__ void __launch_bounds__(kThreads) append_bounds_kernel(const __grid_co
   const __nv_bfloat16* src_v = p.v + b * p.vs[0] + h * p.vs[1] + 8 * u;
   __nv_bfloat16* dst_k = static_cast<__nv_bfloat16*>(p.c.k) + 8 * u;
   __nv_bfloat16* dst_v = static_cast<__nv_bfloat16*>(p.c.v) + 8 * u;
-  constexpr int kBatch = 4;  // rows a thread has on their way at a time
   for (int32_t i0 = begin + sub; i0 < page && t0 + i0 < p.T; i0 += kBatch * kSubs) {
     int32_t slot[kBatch];
     uint4 k[kBatch], v[kBatch];
@@ -223,7 +236,7 @@ bsa_status paged_append_launch(const bsa_paged_append_args* a, cudaStream_t stre
     e = a->cache.D == 128 ? launch_kernel(append_bounds_kernel<128>, grid, dim3(kThreads), 0, stream, p)
                           : launch_kernel(append_bounds_kernel<64>, grid, dim3(kThreads), 0, stream, p);
   } else {
-    const int64_t per = kThreads / (a->cache.D / 8), rows = a->T * a->B * a->cache.Hkv;
+    const int64_t per = kBatch * (kThreads / (a->cache.D / 8)), rows = a->T * a->B * a->cache.Hkv;
     const dim3 grid(static_cast<unsigned>(std::min<int64_t>((rows + per - 1) / per, static_cast<int64_t>(num_sms()) * 16)));
     e = a->cache.D == 128 ? launch_kernel(append_rows_kernel<128>, grid, dim3(kThreads), 0, stream, p)
                           : launch_kernel(append_rows_kernel<64>, grid, dim3(kThreads), 0, stream, p);
