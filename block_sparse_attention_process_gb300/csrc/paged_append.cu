@@ -2,7 +2,7 @@
 //
 // Without bounds a row (one token and head) is D/8 lanes of 16 bytes, wherever its slot is.
 //
-// With bounds a CTA takes the tokens of one sequence and head that go into one page: the slots of a sequence's
+// With bounds a warp, or two or four, takes the tokens of one sequence and head that go into one page: the slots of a sequence's
 // tokens follow each other, so token t lies at place (o + t) % page, o being the place of token 0, and
 // unit u holds tokens u * page - o .. (u + 1) * page - o - 1.  It writes them, reads the keys that the page held before them, and
 // has every key of the page in registers then: maxima and minima are exact in any order, so the bounds need no
@@ -25,6 +25,7 @@ struct AppendParams {
   int32_t B, shift;
   int64_t T;
   int64_t units;  // of one sequence and head
+  int32_t warps;  // of a page
   uint32_t* err;
 };
 
@@ -100,22 +101,45 @@ struct Range {
   }
 };
 
+// The warps that share a page (1, 2 or 4).
+__device__ __forceinline__ void group_sync(int group, int warps) {
+  if (warps == 1) __syncwarp();
+  else asm volatile("bar.sync %0, %1;" ::"r"(group + 1), "r"(warps * 32) : "memory");
+}
+__device__ __forceinline__ bool group_any(int group, int warps, bool x) {
+  if (warps == 1) return __any_sync(0xffffffffu, x);
+  uint32_t any;
+  asm volatile(
+      "{\n\t.reg .pred p, q;\n\t"
+      "setp.ne.u32 p, %1, 0;\n\t"
+      "barrier.cta.red.or.pred q, %2, %3, p;\n\t"
+      "selp.u32 %0, 1, 0, q;\n\t}"
+      : "=r"(any)
+      : "r"(static_cast<uint32_t>(x)), "r"(group + 1), "r"(warps * 32)
+      : "memory");
+  return any != 0u;
+}
+
 template <int D>
 __global__ void __launch_bounds__(kThreads) append_bounds_kernel(const __grid_constant__ AppendParams p) {
-  constexpr int kLanes = D / 8, kSubs = kThreads / kLanes, kWarps = kThreads / 32;
+  constexpr int kLanes = D / 8, kWarps = kThreads / 32;
   __shared__ float hi[kWarps][D], lo[kWarps][D];
   __shared__ uint32_t top[kWarps];
   griddep_launch_dependents();
   griddep_wait();
-  const int u = threadIdx.x % kLanes, sub = threadIdx.x / kLanes, lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+  const int warps = p.warps, group = warp / warps, first_warp = group * warps;
+  const int kSubs = warps * (32 / kLanes), u = lane % kLanes, sub = (warp - first_warp) * (32 / kLanes) + lane / kLanes;
   const int32_t page = 1 << p.shift;
   const int64_t limit = p.c.pages << p.shift;
-  const int64_t bh = blockIdx.x / p.units, unit = blockIdx.x - bh * p.units;
-  const int32_t b = static_cast<int32_t>(bh / p.c.Hkv), h = static_cast<int32_t>(bh - static_cast<int64_t>(b) * p.c.Hkv);
+  const uint32_t at = blockIdx.x * (kWarps / warps) + group;  // (below 2^31)
+  if (at >= static_cast<uint32_t>(p.units) * p.B * p.c.Hkv) return;
+  const uint32_t bh = at / static_cast<uint32_t>(p.units), unit = at - bh * static_cast<uint32_t>(p.units);
+  const int32_t b = static_cast<int32_t>(bh / p.c.Hkv), h = static_cast<int32_t>(bh) - b * p.c.Hkv;
   const int32_t* slots = p.slots + b * p.T;
   const int32_t s0 = slots[0];
   const int32_t o = s0 < 0 ? 0 : s0 & (page - 1);
-  const int64_t t0 = unit * page - o;  // token of the page's place 0
+  const int64_t t0 = static_cast<int64_t>(unit) * page - o;  // token of the page's place 0
   if (t0 >= p.T) return;
   // the page is that of the unit's first token
   const int32_t first = slots[max(t0, static_cast<int64_t>(0))];
@@ -159,7 +183,7 @@ __global__ void __launch_bounds__(kThreads) append_bounds_kernel(const __grid_co
     }
   }
   if (wrong && u == 0 && p.err) atomicOr(p.err, DEV_ERR_BOUNDS);
-  if (!__syncthreads_or(last >= 0)) return;  // nothing stored
+  if (!group_any(group, warps, last >= 0)) return;  // nothing stored
   // keys that the page held (places before the first new one)
   for (int32_t i = sub; i < begin; i += kSubs) r.add(*reinterpret_cast<const uint4*>(dst_k + page_at(p.c.k_stride, page0 + i, p.shift, h)));
   // ---- over the warp's rows, then over the warps
@@ -180,13 +204,11 @@ __global__ void __launch_bounds__(kThreads) append_bounds_kernel(const __grid_co
     }
   }
   if (lane == 0) top[warp] = r.top;
-  __syncthreads();
-  if (threadIdx.x < D) {
-    const int d = threadIdx.x;
-    float a = hi[0][d], c = lo[0][d];
-    uint32_t m = top[0];
-#pragma unroll
-    for (int w = 1; w < kWarps; ++w) {
+  group_sync(group, warps);
+  for (int d = threadIdx.x - first_warp * 32; d < D; d += warps * 32) {
+    float a = hi[first_warp][d], c = lo[first_warp][d];
+    uint32_t m = top[first_warp];
+    for (int w = first_warp + 1; w < first_warp + warps; ++w) {
       a = fmaxf(a, hi[w][d]);
       c = fminf(c, lo[w][d]);
       m = max(m, top[w]);
@@ -232,7 +254,10 @@ bsa_status paged_append_launch(const bsa_paged_append_args* a, cudaStream_t stre
   if (!p.err) return fail(BSA_ERR_CUDA, "could not allocate the device error word");
   cudaError_t e;
   if (a->cache.bounds) {
-    const dim3 grid(static_cast<unsigned>(p.units * a->B * a->cache.Hkv));
+    // a warp for every 16 places of a page, up to a CTA
+    p.warps = std::min(a->cache.page / 16, kThreads / 32);
+    const int64_t units = p.units * a->B * a->cache.Hkv, per = kThreads / 32 / p.warps;
+    const dim3 grid(static_cast<unsigned>((units + per - 1) / per));
     e = a->cache.D == 128 ? launch_kernel(append_bounds_kernel<128>, grid, dim3(kThreads), 0, stream, p)
                           : launch_kernel(append_bounds_kernel<64>, grid, dim3(kThreads), 0, stream, p);
   } else {
