@@ -15,6 +15,7 @@ namespace bsa {
 namespace {
 
 constexpr int kThreads = 128;  // (256: 54 us for 4 x 8 x 8191 tokens, 128: 44)
+constexpr int kWarpPlaces = 16;
 constexpr int kBatch = 4;      // rows that a thread has on their way at a time
 
 struct AppendParams {
@@ -25,7 +26,6 @@ struct AppendParams {
   int32_t B, shift;
   int64_t T;
   int64_t units;  // of one sequence and head
-  int32_t warps;  // of a page
   uint32_t* err;
 };
 
@@ -120,7 +120,7 @@ __device__ __forceinline__ bool group_any(int group, int warps, bool x) {
   return any != 0u;
 }
 
-template <int D>
+template <int D, int warps>
 __global__ void __launch_bounds__(kThreads) append_bounds_kernel(const __grid_constant__ AppendParams p) {
   constexpr int kLanes = D / 8, kWarps = kThreads / 32;
   __shared__ float hi[kWarps][D], lo[kWarps][D];
@@ -128,8 +128,9 @@ __global__ void __launch_bounds__(kThreads) append_bounds_kernel(const __grid_co
   griddep_launch_dependents();
   griddep_wait();
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
-  const int warps = p.warps, group = warp / warps, first_warp = group * warps;
-  const int kSubs = warps * (32 / kLanes), u = lane % kLanes, sub = (warp - first_warp) * (32 / kLanes) + lane / kLanes;
+  constexpr int kSubs = warps * (32 / kLanes);
+  const int group = warp / warps, first_warp = group * warps;
+  const int u = lane % kLanes, sub = (warp - first_warp) * (32 / kLanes) + lane / kLanes;
   const int32_t page = 1 << p.shift;
   const int64_t limit = p.c.pages << p.shift;
   const uint32_t at = blockIdx.x * (kWarps / warps) + group;  // (below 2^31)
@@ -254,12 +255,13 @@ bsa_status paged_append_launch(const bsa_paged_append_args* a, cudaStream_t stre
   if (!p.err) return fail(BSA_ERR_CUDA, "could not allocate the device error word");
   cudaError_t e;
   if (a->cache.bounds) {
-    // a warp for every 16 places of a page, up to a CTA
-    p.warps = std::min(a->cache.page / 16, kThreads / 32);
-    const int64_t units = p.units * a->B * a->cache.Hkv, per = kThreads / 32 / p.warps;
+    // a warp for every kWarpPlaces places of a page, up to a CTA
+    const int warps = std::min(a->cache.page / kWarpPlaces, kThreads / 32);
+    const int64_t units = p.units * a->B * a->cache.Hkv, per = kThreads / 32 / warps;
     const dim3 grid(static_cast<unsigned>((units + per - 1) / per));
-    e = a->cache.D == 128 ? launch_kernel(append_bounds_kernel<128>, grid, dim3(kThreads), 0, stream, p)
-                          : launch_kernel(append_bounds_kernel<64>, grid, dim3(kThreads), 0, stream, p);
+    auto kern = a->cache.D == 128 ? (warps >= 4 ? append_bounds_kernel<128, 4> : warps == 2 ? append_bounds_kernel<128, 2> : append_bounds_kernel<128, 1>)
+                                  : (warps >= 4 ? append_bounds_kernel<64, 4> : warps == 2 ? append_bounds_kernel<64, 2> : append_bounds_kernel<64, 1>);
+    e = launch_kernel(kern, grid, dim3(kThreads), 0, stream, p);
   } else {
     const int64_t per = kBatch * (kThreads / (a->cache.D / 8)), rows = a->T * a->B * a->cache.Hkv;
     const dim3 grid(static_cast<unsigned>(std::min<int64_t>((rows + per - 1) / per, static_cast<int64_t>(num_sms()) * 16)));
