@@ -25,6 +25,20 @@ __device__ __forceinline__ void unit_of(float top, int bits, float& unit, float&
 }
 constexpr float kUsualTop = 0x1p100f;  // keys (or queries) below this have bounds (or codes)
 
+// Division of 0 <= n < 2^31 by a number known on the host, as a product: with l = ceil(log2 d) and m = floor(2^32 (2^l - d) / d) + 1,
+// n / d = (n m / 2^32 + n) / 2^l, rounded down both times.
+struct Divisor {
+  uint32_t m = 1, l = 0;
+  Divisor() = default;
+  explicit Divisor(uint32_t d) {
+    while (l < 31 && (uint32_t(1) << l) < d) ++l;
+    m = static_cast<uint32_t>((((uint64_t(1) << l) - d) << 32) / d) + 1;
+  }
+  __device__ __forceinline__ int32_t of(int32_t n) const {
+    return static_cast<int32_t>((__umulhi(static_cast<uint32_t>(n), m) + static_cast<uint32_t>(n)) >> l);
+  }
+};
+
 // log2 of a page size (16 .. 256)
 inline int page_shift(int32_t page) {
   int s = 0;

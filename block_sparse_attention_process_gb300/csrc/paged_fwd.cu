@@ -29,7 +29,7 @@ constexpr int kTileKeys = 64;
 constexpr int kRowTile = 16;
 constexpr int kPartUnits = 3;   // cost of a part beside its tiles', in tiles
 constexpr int kWholeTiles = 8;  // longest pair, in tiles, that one CTA takes alone
-constexpr int kSmWarps = 8;      // warps an SM: a CTA of all of them for runs, two of four where a pair is whole to a CTA
+constexpr int kSmWarps = 8;      // warps an SM: a CTA of all of them, or two of four where pairs are whole to a CTA and more than SMs
 constexpr int kWarpRing = 24 * 1024;
 constexpr int smem_bytes(int warps) { return warps * kWarpRing + 256; }
 constexpr int32_t kNoKeys = -4096;  // place of a unit without keys: before every key a row sees
@@ -51,9 +51,10 @@ struct FwdParams {
   int32_t queries;    // query sets of a sequence that have keys of their own: T with lists, else 1
   int32_t R;          // rows of a pair: G * T, with lists G
   int32_t row_tiles;  // pairs of a query set and head
+  Divisor by_t;       // of T
   int32_t kind;
   int64_t left, chunk;
-  float scale_log2;   // without a cap: scale * log2 e; with one: scale / cap
+  float scale_log2;   // without a cap: scale * log2 e; with one: 2 log2 e * scale / cap
   float cap_log2;
   const float* sinks;
   int32_t n_sinks, sinks_kv;
@@ -241,8 +242,8 @@ struct Run {
 };
 
 // Row r of a pair: q head and token.
-__device__ __forceinline__ int32_t row_head(const FwdParams& p, int32_t h, int32_t r) { return h * p.G + (p.select || p.T == 1 ? r : r / p.T); }
-__device__ __forceinline__ int32_t row_token(const FwdParams& p, int32_t s, int32_t r) { return p.T == 1 ? 0 : p.select ? s % p.queries : r % p.T; }
+__device__ __forceinline__ int32_t row_head(const FwdParams& p, int32_t h, int32_t r) { return h * p.G + (p.select ? r : p.by_t.of(r)); }
+__device__ __forceinline__ int32_t row_token(const FwdParams& p, int32_t s, int32_t r) { return p.select ? s % p.queries : r - p.by_t.of(r) * p.T; }
 
 // ------------------------------------------------------------------ loads and products
 
@@ -290,6 +291,12 @@ struct FwdShared {
   static constexpr int kPad = D + 4;  // floats between rows of the merge buffer
   static_assert(W * kRowTile * kPad * 4 <= W * kWarpRing, "the merge buffer is the ring's memory");
 };
+
+__device__ __forceinline__ float rcp_approx(float x) {
+  float y;
+  asm("rcp.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
+  return y;
+}
 
 // Adds a row's sinks: (m, l) -> its logsumexp in log2 units and the factor of the unnormalised output.
 __device__ __forceinline__ float finish_row(const FwdParams& p, int32_t h, float m, float l, float& factor) {
@@ -550,7 +557,8 @@ __global__ void __launch_bounds__(32 * W, kSmWarps / W) paged_fwd_kernel(const _
 #pragma unroll
           for (int e = 0; e < 4; ++e) {
             s[y][c][e] *= p.scale_log2;
-            if constexpr (kCap) s[y][c][e] = p.cap_log2 * tanh_nan(s[y][c][e]);
+            // cap tanh(x) = cap - 2 cap / (1 + e^2x); the exponential goes to 0 or to infinity, NaN stays
+            if constexpr (kCap) s[y][c][e] = fmaf(-2.f * p.cap_log2, rcp_approx(1.f + ex2_approx(s[y][c][e])), p.cap_log2);
           }
       if (masked) {
 #pragma unroll
@@ -801,9 +809,9 @@ Plan make_plan(const bsa_paged_fwd_args* a) {
 
 template <int D, int RT>
 bsa_status launch(const FwdParams& p, const Plan& x, cudaStream_t stream) {
-  auto kern = p.whole ? (p.cap_log2 > 0.f ? paged_fwd_kernel<D, RT, kSmWarps / 2, true> : paged_fwd_kernel<D, RT, kSmWarps / 2, false>)
+  const int warps = p.whole && p.n_cta > num_sms() ? kSmWarps / 2 : kSmWarps;
+  auto kern = warps < kSmWarps ? (p.cap_log2 > 0.f ? paged_fwd_kernel<D, RT, kSmWarps / 2, true> : paged_fwd_kernel<D, RT, kSmWarps / 2, false>)
                       : (p.cap_log2 > 0.f ? paged_fwd_kernel<D, RT, kSmWarps, true> : paged_fwd_kernel<D, RT, kSmWarps, false>);
-  const int warps = p.whole ? kSmWarps / 2 : kSmWarps;
   const bsa_status st = ensure_smem_attr(reinterpret_cast<const void*>(kern), smem_bytes(warps), "set paged forward smem size");
   if (st != BSA_OK) return st;
   cudaError_t e = launch_kernel(kern, dim3(p.n_cta), dim3(32 * warps), smem_bytes(warps), stream, p);
@@ -865,10 +873,11 @@ bsa_status paged_fwd_launch(const bsa_paged_fwd_args* a, float scale, cudaStream
   p.queries = a->select ? p.T : 1;
   p.R = x.R;
   p.row_tiles = static_cast<int32_t>(x.row_tiles);
+  p.by_t = Divisor(static_cast<uint32_t>(p.T));
   p.kind = a->kind;
   p.left = a->local_left;
   p.chunk = a->chunk;
-  p.scale_log2 = a->logits_soft_cap > 0.f ? scale / a->logits_soft_cap : scale * kLog2e;
+  p.scale_log2 = a->logits_soft_cap > 0.f ? scale / a->logits_soft_cap * (2.f * kLog2e) : scale * kLog2e;
   p.cap_log2 = a->logits_soft_cap > 0.f ? a->logits_soft_cap * kLog2e : 0.f;
   p.sinks = a->sinks;
   p.n_sinks = a->num_sinks;
