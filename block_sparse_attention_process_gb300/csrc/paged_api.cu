@@ -63,10 +63,11 @@ bsa_status check_workspace(const void* ws, size_t have, size_t need) {
   return BSA_OK;
 }
 
-// A table's rows cover at most 2^31 - 1 tokens.
+constexpr int64_t kMostTokens = int64_t(1) << 30;  // of a sequence
+
 bsa_status check_table(int64_t M, int32_t page) {
   if (M <= 0) return bad("M must be positive");
-  if (M > INT32_MAX / page) return unsupported("M pages must hold fewer than 2^31 tokens");
+  if (M > kMostTokens / page) return unsupported("M pages must hold at most 2^30 tokens");
   return BSA_OK;
 }
 
@@ -148,7 +149,7 @@ bsa_status check_fwd(const bsa_paged_fwd_args* a) {
   if (a->select) {
     if (a->kind != BSA_MASK_CAUSAL) return unsupported("lists of pages go with the causal kind");
     if (a->keep < 1) return bad("keep must be at least 1");
-    if (a->keep > INT32_MAX / a->cache.page) return unsupported("keep pages must hold fewer than 2^31 tokens");
+    if (a->keep > kMostTokens / a->cache.page) return unsupported("keep pages must hold at most 2^30 tokens");
     if (!aligned4(a->select)) return bad("select must be 4-byte aligned");
   }
   if (!paged_fwd_fits(a)) return unsupported("too many rows for one launch");

@@ -497,7 +497,7 @@ typedef struct {
   int32_t* slots;          /* device int32 [B, T], written: slots[b, i] = page * (page size) + place of token lens[b] + i,
                               -1 behind the last new one */
   int32_t B;               /* 1..4096 */
-  int64_t M;               /* longest sequence, in pages */
+  int64_t M;               /* longest sequence, in pages (at most 2^30 tokens) */
   int64_t T;               /* tokens a sequence can grow by in one call */
   int64_t pages;           /* pages * page below 2^31 */
   int32_t page;
@@ -577,10 +577,11 @@ typedef struct {
   bsa_paged_cache cache;   /* (bounds are not used) */
   const void* q;           /* bf16, element (b, h, t, d) at b*q_stride[0] + h*q_stride[1] + t*q_stride[2] + d;
                               16-byte aligned, strides multiples of 8 */
-  void* o;                 /* bf16, written, addressed likewise through o_stride (no two rows in one place) */
+  void* o;                 /* bf16, written, addressed likewise through o_stride (no two rows in one place; q's own memory
+                              only row for row) */
   float* lse;              /* fp32 [B, Hq, T], written */
   int64_t q_stride[3], o_stride[3];
-  const int32_t* table;    /* device int32 [B, M] */
+  const int32_t* table;    /* device int32 [B, M], M pages of at most 2^30 tokens; rows may share pages */
   const int32_t* lens;     /* device int32 [B]: keys each sequence holds, the new tokens' own included */
   const int32_t* q_lens;   /* device int32 [B], or NULL (= T): tokens at or past q_lens[b] are padding */
   const int32_t* select;   /* device int32 [B, Hkv, T, keep], or NULL: see below */
