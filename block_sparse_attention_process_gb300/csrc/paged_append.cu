@@ -177,6 +177,7 @@ __global__ void __launch_bounds__(kThreads) append_bounds_kernel(const __grid_co
         wrong = true;
         continue;
       }
+      slot[x] = BSA_RANGE(slot[x], 0, static_cast<int32_t>(limit), p.err);
       *reinterpret_cast<uint4*>(dst_k + page_at(p.c.k_stride, slot[x], p.shift, h)) = k[x];
       *reinterpret_cast<uint4*>(dst_v + page_at(p.c.v_stride, slot[x], p.shift, h)) = v[x];
       r.add(k[x]);

@@ -443,7 +443,7 @@ __global__ void __launch_bounds__(32 * W, kSmWarps / W) paged_fwd_kernel(const _
           const int32_t pos = (own << p.shift) + in_page;
           if (lane == 0 && tile == 0) place[group][stage][y] = page < 0 ? kNoKeys : pos;
           const uint32_t dst = lane_dst + stage * Sh::kStageBytes + y * Sh::kUnitBytes;
-          const uint32_t some = page < 0 ? 0 : page;
+          const uint32_t some = BSA_RANGE(page < 0 ? 0 : page, 0, p.pages, p.err);
           const uint4* k = lane_k + (static_cast<uint64_t>(some) * p.k8[0] + static_cast<uint64_t>(in_page) * p.k8[2]);
           const uint4* v = lane_v + (static_cast<uint64_t>(some) * p.v8[0] + static_cast<uint64_t>(in_page) * p.v8[2]);
           if (page >= 0 && pos >= load_lo && pos + kUnit <= load_hi) {
@@ -662,7 +662,7 @@ __global__ void __launch_bounds__(32 * W, kSmWarps / W) paged_fwd_kernel(const _
         *reinterpret_cast<float2*>(&merge[(group * kRows + row) * Sh::kPad + 8 * c + 2 * t4]) = make_float2(acc[c][2 * r] * f, acc[c][2 * r + 1] * f);
     }
     __syncthreads();
-    const int64_t rec = 2 * static_cast<int64_t>(blockIdx.x) + (part > 0 ? 1 : 0);
+    const int64_t rec = 2 * static_cast<int64_t>(BSA_RANGE(static_cast<int32_t>(blockIdx.x), 0, p.n_cta, p.err)) + (part > 0 ? 1 : 0);
     const int32_t live = min(kRows, p.R - run.rt * kRows);
     for (int i = threadIdx.x; i < live * (D / 4); i += 32 * W) {
       const int row = i / (D / 4), d = i % (D / 4) * 4;
@@ -754,7 +754,7 @@ __global__ void __launch_bounds__(kJoinThreads) paged_join_kernel(const __grid_c
 #pragma unroll
     for (int i = 0; i < 4; ++i) {
       const bool in = c + i * step <= c1;
-      const int64_t rec = !in ? first : c + i * step == c0 ? first : 2 * (c + i * step);
+      const int64_t rec = BSA_RANGE(!in ? first : c + i * step == c0 ? first : 2 * (c + i * step), 0, 2 * p.n_cta, p.err);
       mc[i] = p.rec_stat[rec * 2 * kRows + row];
       lc[i] = in ? p.rec_stat[rec * 2 * kRows + kRows + row] : 0.f;
       y[i] = *reinterpret_cast<const float4*>(p.rec_o + (rec * kRows + row) * D + 4 * vec);

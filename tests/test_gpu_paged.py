@@ -11,11 +11,15 @@ the soft cap's tanh adds 2^-19 cap.  exp2 and the conversion to log2 units add
   O:    bf16 rounding 2^-8 |o|, plus (2^-8 + 2 ds + 2^-19) sum_j p_j |v_jd|: a
         probability is rounded to bf16 before it meets the value
 """
+import os
+import subprocess
+import sys
+
 import numpy as np
 import pytest
 import torch
 
-from helpers import need_gpu
+from helpers import ROOT, need_gpu
 from oracle import paged
 
 pytestmark = pytest.mark.gpu
@@ -721,3 +725,54 @@ def test_wrong_tensors_are_refused():
         with pytest.raises((ValueError, bsa.BsaError)):
             call()
     assert bsa.get_device_error() == 0
+
+
+def test_output_over_the_queries():
+    bsa = bsa_()
+    lens = [3000, 40]
+    cache, table, k, v = paged_batch(bsa, 2, 2, 64, 16, lens, 3)
+    q = rows((2, 8, 3, 64), 1).cuda()
+    want, lse = check_fwd(bsa, cache, table, k, v, q, lens)
+    mine = q.clone()
+    got, lse2 = bsa.paged_fwd(mine, cache, table, i32(lens), o=mine)
+    assert got is mine and torch.equal(got, want) and torch.equal(lse, lse2)
+
+
+def test_sequences_that_share_pages():
+    bsa = bsa_()
+    n = 1000
+    cache, table, k, v = paged_batch(bsa, 1, 2, 64, 16, [n], 3)
+    B, lens = 70, [n - 13 * b for b in range(70)]
+    shared = table.expand(B, -1).contiguous()
+    q = rows((B, 4, 1, 64), 1).cuda()
+    index = bsa.paged_select(q, cache, shared, i32(lens), 9)
+    assert np.array_equal(index.cpu().numpy(), want_select(cache, shared, q, lens, 9, 1, 1))
+    kk, vv = k.expand(B, -1, -1, -1), v.expand(B, -1, -1, -1)
+    check_fwd(bsa, cache, shared, kk, vv, q, lens)
+    check_fwd(bsa, cache, shared, kk, vv, q, lens, select=index.cpu().numpy())
+
+
+def test_the_same_results_again():
+    """Sums run in a fixed order: results repeat bit for bit."""
+    bsa = bsa_()
+    lens = [5000, 17, 900, 2222]
+    cache, table, _, _ = paged_batch(bsa, 4, 2, 128, 32, lens, 3)
+    q = rows((4, 8, 2, 128), 1).cuda()
+    want = bsa.paged_fwd(q, cache, table, i32(lens))
+    for _ in range(10):
+        got = bsa.paged_fwd(q, cache, table, i32(lens))
+        assert torch.equal(got[0], want[0]) and torch.equal(got[1], want[1])
+
+
+def test_range_checked_build():
+    """The same kernels in the build that checks pages, slots and records on the device: right, and nothing found."""
+    if os.environ.get("BSA_LIBRARY_VARIANT") == "debug":
+        pytest.skip("already in it")
+    need_gpu()
+    from block_sparse_attention_process_gb300 import build as b
+    if not os.path.exists(b.LIB_DEBUG):
+        b.build(debug=True)
+    r = subprocess.run([sys.executable, "-m", "pytest", "-x", "-q", "-m", "gpu", os.path.abspath(__file__), "-k",
+                        "test_fwd or test_append or test_select_with or test_sequences or selected"],
+                       env=dict(os.environ, BSA_LIBRARY_VARIANT="debug"), capture_output=True, text=True, timeout=900, cwd=ROOT)
+    assert r.returncode == 0, r.stdout[-3000:] + r.stderr[-2000:]
