@@ -24,8 +24,7 @@ namespace {
 
 constexpr int kThreads = 512;
 constexpr int kWarps = kThreads / 32;
-constexpr int kSide = 2;               // groups of 8 pages that a warp has on their way at a time
-constexpr int kPassPages = kWarps * 8 * kSide;
+constexpr int kPassPages = kWarps * 8;  // pages that a CTA scores side by side
 constexpr int kMaxCluster = 8;
 constexpr int kBins = 2048;
 constexpr int kMaxPages = 49152;        // keys that the first CTA's shared memory holds
@@ -133,12 +132,11 @@ __global__ void __launch_bounds__(kThreads) select_kernel(const __grid_constant_
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5, g = lane >> 2, t4 = lane & 3;
   const int32_t cta = static_cast<int32_t>(cluster_rank()), row = static_cast<int32_t>(blockIdx.x) / p.cluster;
   const int32_t t = row % p.T, bh = row / p.T, b = bh / p.Hkv, h = bh % p.Hkv;
-  int32_t j0 = cta * kPassPages + warp * 8 * kSide;  // this warp's pages; the quad's are j0 + g, j0 + 8 + g
+  int32_t j0 = cta * kPassPages + warp * 8;  // this warp's pages; the quad's is j0 + g
+  const int32_t step = p.cluster * kPassPages;
   // (the table's entries and q are on their way before the length is known)
   const int32_t* table = p.table + b * p.M;
-  int32_t page[kSide];
-#pragma unroll
-  for (int y = 0; y < kSide; ++y) page[y] = j0 + 8 * y + g < p.M ? table[j0 + 8 * y + g] : -1;
+  int32_t page = j0 + g < p.M ? table[j0 + g] : -1;
   const __nv_bfloat16* q = p.q + b * p.qs[0] + static_cast<int64_t>(h) * p.G * p.qs[1] + t * p.qs[2];
   uint32_t top = 0;
   for (int i = threadIdx.x; i < p.G * (D / 8); i += kThreads) {
@@ -156,6 +154,19 @@ __global__ void __launch_bounds__(kThreads) select_kernel(const __grid_constant_
     return;
   }
   if (p.cluster > 1) cluster_arrive();  // (a CTA's shared memory is written once it is known to run)
+  // ---- bounds: a pass of pages is on its way while the one before is scored
+  uint4 x[kChunks];
+  bool known;
+  auto load = [&](int32_t j, uint4 (&y)[kChunks]) {  // the quad's page j, whose number is `page`; then the next number
+    const bool in = j < n && page >= 0 && page < p.pages;
+    if (j < n && !in && t4 == 0 && p.err) atomicOr(p.err, DEV_ERR_BOUNDS);
+    const uint4* src = reinterpret_cast<const uint4*>(p.bounds + (static_cast<int64_t>(in ? page : 0) * p.Hkv + h) * 2 * D) + t4;
+#pragma unroll
+    for (int c = 0; c < kChunks; ++c) y[c] = in ? src[c * 4] : make_uint4(0, 0, 0, 0);
+    page = j + step < n ? table[j + step] : -1;
+    return in;
+  };
+  known = load(j0 + g, x);
   // ---- the group's unit
   top = __reduce_max_sync(0xffffffffu, top);
   if (lane == 0) warp_sum[warp] = top;
@@ -187,63 +198,45 @@ __global__ void __launch_bounds__(kThreads) select_kernel(const __grid_constant_
   uint32_t first_keys;  // the first CTA's `keys`
   asm("mapa.shared::cluster.u32 %0, %1, %2;" : "=r"(first_keys) : "r"(smem_u32(keys)), "r"(0));
   bool started = p.cluster == 1;
-  for (int32_t pass = 0; pass * p.cluster * kPassPages < n; ++pass) {  // (as many for every CTA of the cluster)
-    bool known[kSide];
-    uint4 x[kSide][kChunks];
-#pragma unroll
-    for (int y = 0; y < kSide; ++y) {
-      const int32_t j = j0 + 8 * y + g;
-      known[y] = j < n && page[y] >= 0 && page[y] < p.pages;
-      if (j < n && !known[y] && t4 == 0 && p.err) atomicOr(p.err, DEV_ERR_BOUNDS);
-      const uint4* src = reinterpret_cast<const uint4*>(p.bounds + (static_cast<int64_t>(known[y] ? page[y] : 0) * p.Hkv + h) * 2 * D) + t4;
-#pragma unroll
-      for (int c = 0; c < kChunks; ++c) x[y][c] = known[y] ? src[c * 4] : make_uint4(0, 0, 0, 0);
-      const int32_t next = j + p.cluster * kPassPages;
-      page[y] = next < n ? table[next] : -1;
-    }
-    float best[kSide][2];  // pages 2 t4 and 2 t4 + 1 of a group
-#pragma unroll
-    for (int y = 0; y < kSide; ++y) best[y][0] = best[y][1] = -INFINITY;
+  for (int32_t pass = 0; pass * step < n; ++pass) {  // (as many for every CTA of the cluster)
+    uint4 ahead[kChunks];
+    const bool known_ahead = load(j0 + step + g, ahead);
+    float best[2] = {-INFINITY, -INFINITY};  // pages 2 t4 and 2 t4 + 1 of the warp's
     for (int32_t r0 = 0; r0 < p.G; r0 += 16) {
       if (pass == 0 || p.G > 16) {
         if (pass + r0 > 0) __syncthreads();
         code(r0);
       }
-      float acc[kSide][4] = {};
+      float acc[2][4] = {};
 #pragma unroll
       for (int c = 0; c < kChunks; ++c) {
         const uint4 lo = *reinterpret_cast<const uint4*>(&qc[g * kRow + c * 32 + t4 * 8]);
         const uint4 hi = *reinterpret_cast<const uint4*>(&qc[(g + 8) * kRow + c * 32 + t4 * 8]);
-#pragma unroll
-        for (int y = 0; y < kSide; ++y) {
-          mma_bf16(acc[y], lo.x, hi.x, lo.y, hi.y, x[y][c].x, x[y][c].y);
-          mma_bf16(acc[y], lo.z, hi.z, lo.w, hi.w, x[y][c].z, x[y][c].w);
-        }
+        mma_bf16(acc[0], lo.x, hi.x, lo.y, hi.y, x[c].x, x[c].y);
+        mma_bf16(acc[1], lo.z, hi.z, lo.w, hi.w, x[c].z, x[c].w);
       }
       // heads g and g + 8
 #pragma unroll
-      for (int y = 0; y < kSide; ++y)
-#pragma unroll
-        for (int k = 0; k < 2; ++k) {
-          const float s0 = acc[y][k], s1 = acc[y][k + 2];
-          best[y][k] = fmaxf(best[y][k], fmaxf(fabsf(s0) < INFINITY ? s0 : INFINITY, fabsf(s1) < INFINITY ? s1 : INFINITY));
-        }
+      for (int k = 0; k < 2; ++k) {
+        const float s0 = acc[0][k] + acc[1][k], s1 = acc[0][k + 2] + acc[1][k + 2];
+        best[k] = fmaxf(best[k], fmaxf(fabsf(s0) < INFINITY ? s0 : INFINITY, fabsf(s1) < INFINITY ? s1 : INFINITY));
+      }
     }
     if (!started) cluster_wait();
     started = true;
+    const uint32_t ok = __ballot_sync(0xffffffffu, known);  // lane 4 g stands for page g
 #pragma unroll
-    for (int y = 0; y < kSide; ++y) {
-      const uint32_t ok = __ballot_sync(0xffffffffu, known[y]);  // lane 4 g stands for page g
+    for (int k = 0; k < 2; ++k) {
 #pragma unroll
-      for (int k = 0; k < 2; ++k) {
-#pragma unroll
-        for (int o = 4; o < 32; o *= 2) best[y][k] = fmaxf(best[y][k], __shfl_xor_sync(0xffffffffu, best[y][k], o));
-        const int32_t i = 2 * t4 + k, j = j0 + 8 * y + i;
-        if (g == 0 && j < n)
-          asm volatile("st.shared::cluster.u32 [%0], %1;" ::"r"(first_keys + 4 * j), "r"(ordered(ok >> (4 * i) & 1u ? best[y][k] : -INFINITY)) : "memory");
-      }
+      for (int o = 4; o < 32; o *= 2) best[k] = fmaxf(best[k], __shfl_xor_sync(0xffffffffu, best[k], o));
+      const int32_t i = 2 * t4 + k;
+      if (g == 0 && j0 + i < n)
+        asm volatile("st.shared::cluster.u32 [%0], %1;" ::"r"(first_keys + 4 * (j0 + i)), "r"(ordered(ok >> (4 * i) & 1u ? best[k] : -INFINITY)) : "memory");
     }
-    j0 += p.cluster * kPassPages;
+#pragma unroll
+    for (int c = 0; c < kChunks; ++c) x[c] = ahead[c];
+    known = known_ahead;
+    j0 += step;
   }
   if (p.cluster > 1) {
     cluster_arrive();
