@@ -740,7 +740,7 @@ def paged_fwd(q: torch.Tensor, cache: PagedCache, table: torch.Tensor, lens: tor
                 kind, -1 if local_left is None else local_left, chunk or 0, math.nan if softmax_scale is None else softmax_scale,
                 logits_soft_cap or 0.0, sp, sn, skv)
         pack = _abi.PAGED_FWD_REST.pack
-        need = _workspace_size("bsa_paged_fwd", (index, B, cache.Hkv, D, cache.page, Hq, M, T, keep), lambda: cache._c + pack(*head, 0, 0))
+        need = _workspace_size("bsa_paged_fwd", (index, B, cache.Hkv, D, cache.page, Hq, M, T, keep, kind, local_left, chunk), lambda: cache._c + pack(*head, 0, 0))
         ws = _raw_alloc(need, handle) if need else 0
         try:
             check(_abi.lib().bsa_paged_fwd(cache._c + pack(*head, ws, need), handle), "bsa_paged_fwd")

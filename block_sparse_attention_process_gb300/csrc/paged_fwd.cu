@@ -28,7 +28,13 @@ constexpr int kUnit = 16;       // keys of one load
 constexpr int kTileKeys = 64;
 constexpr int kRowTile = 16;
 constexpr int kPartUnits = 3;   // cost of a part beside its tiles', in tiles
-constexpr int kWholeTiles = 8;  // longest pair, in tiles, that one CTA takes alone
+// Pairs that one CTA takes alone (no records, no join), by the longest that one can be, in tiles: 8; up to 32 while there
+// are pairs enough, tiles x SMs up to 96 x pairs (with several row tiles: pairs for three quarters of the SMs); and lists and windows, whose lengths differ less, of up to 64 where
+// there are pairs for half of the SMs.  Keys on 8 heads, whole and cut (us): 16 x 2048 24.7 and 29.0, 64 x 128 to 1024 31 and 43,
+// 6 x 1024 11.8 and 15.8, 6 x 2048 18.2 and 18.5, 1 x 1024 11.2 and 9.0; on one head of 64 rows 128 x 2048 48.6 and 58.8,
+// 64 x 1024 28.4 and 24.9; 64 pages of 64 for 16 queries 56.7 and 60.3 with their selection.  One sequence of 4096
+// among 15 short ones would take 31 whole and takes 17.
+constexpr int kWholeTiles = 8, kManyTiles = 32, kEvenTiles = 64;
 constexpr int kSmWarps = 8;      // warps an SM: a CTA of all of them, or two of four where pairs are whole to a CTA and more than SMs
 constexpr int kWarpRing = 24 * 1024;
 constexpr int smem_bytes(int warps) { return warps * kWarpRing + 256; }
@@ -806,8 +812,15 @@ Plan make_plan(const bsa_paged_fwd_args* a) {
   const int64_t rows = kRowTile * x.rt;
   x.row_tiles = (x.R + rows - 1) / rows;
   x.pairs = static_cast<int64_t>(a->B) * (a->select ? a->T : 1) * a->cache.Hkv * x.row_tiles;
-  const int64_t longest = (a->select ? std::min(a->keep, a->M) : a->M) * a->cache.page, tiles = (longest + kTileKeys - 1) / kTileKeys;
-  x.whole = tiles <= kWholeTiles && x.pairs <= INT32_MAX;
+  // the longest a pair can be: what the table, a list or a window holds
+  const int64_t room = a->M * a->cache.page;
+  int64_t longest = a->select ? std::min(a->keep * a->cache.page, room) : room;
+  if (a->kind == BSA_MASK_LOCAL && a->local_left >= 0) longest = std::min(longest, std::min(a->local_left, room) + a->T + kTileKeys);
+  if (a->kind == BSA_MASK_CHUNKED_CAUSAL) longest = std::min(longest, std::min(a->chunk, room) + a->T + kTileKeys);
+  const int64_t tiles = (longest + kTileKeys - 1) / kTileKeys;
+  const bool many = tiles <= kManyTiles && (x.rt == 1 ? tiles * num_sms() <= 96 * x.pairs : 4 * x.pairs >= 3 * num_sms());
+  const bool even = x.rt == 1 && 2 * x.pairs >= num_sms() && tiles <= kEvenTiles && longest < room;
+  x.whole = (tiles <= kWholeTiles || many || even) && x.pairs <= INT32_MAX;
   x.n_cta = static_cast<int32_t>(x.whole ? x.pairs : std::min<int64_t>(x.pairs * tiles, static_cast<int64_t>(num_sms())));
   x.stat_bytes = x.whole ? 0 : static_cast<size_t>(2 * x.n_cta) * 2 * rows * sizeof(float);
   x.o_bytes = x.whole ? 0 : static_cast<size_t>(2 * x.n_cta) * rows * a->cache.D * sizeof(float);
