@@ -442,7 +442,8 @@ def check_fwd(bsa, cache, table, k, v, q, lens, *, q_lens=None, scale=None, cap=
     (1, 2, 8, 128, 64, 1, [3000], "both"), (2, 1, 16, 64, 16, 1, [1025, 1], "phtd"), (1, 1, 17, 128, 16, 1, [700], "pthd"),
     (2, 1, 5, 64, 128, 3, [520, 130], "phtd"), (1, 1, 16, 128, 32, 4, [2000], "phtd"), (2, 2, 10, 64, 16, 7, [90, 700], "both"),
     (1, 1, 100, 64, 256, 1, [600], "phtd"), (1, 1, 3, 128, 256, 40, [1111], "pthd"), (16, 2, 4, 64, 16, 1, list(range(1, 1600, 100)), "phtd"),
-    (1, 1, 2, 128, 16, 1, [20000], "phtd"), (40, 1, 1, 64, 16, 1, [5 + 37 * i % 900 for i in range(40)], "phtd"),
+    (1, 1, 2, 128, 16, 1, [20000], "phtd"), (90, 2, 2, 64, 16, 1, [1 + 29 * i % 600 for i in range(90)], "pthd"),
+    (80, 2, 20, 64, 16, 1, [1 + 7 * i % 90 for i in range(80)], "phtd"), (9, 1, 9, 64, 32, 5, [300 * i for i in range(9)], "phtd"), (40, 1, 1, 64, 16, 1, [5 + 37 * i % 900 for i in range(40)], "phtd"),
 ])
 def test_fwd(B, H, G, D, page, T, lens, kind):
     bsa = bsa_()
