@@ -224,6 +224,8 @@ bsa_status bsa_paged_fwd(const bsa_paged_fwd_args* a, bsa_stream stream) {
     if (s == BSA_OK) s = check_workspace(a->workspace, a->workspace_bytes, paged_fwd_workspace_bytes(a));
     if (s != BSA_OK) return s;
     const float scale = std::isnan(a->softmax_scale) ? 1.0f / std::sqrt(static_cast<float>(a->cache.D)) : a->softmax_scale;
+    if (!std::isfinite(4.0f * scale) || (a->logits_soft_cap > 0.f && !std::isfinite(4.0f * (scale / a->logits_soft_cap))))
+      return bad("softmax_scale, and softmax_scale over the cap, must be finite");  // (times 2 log2 e)
     return paged_fwd_launch(a, scale, static_cast<cudaStream_t>(stream));
   });
 }

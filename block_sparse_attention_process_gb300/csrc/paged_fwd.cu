@@ -4,18 +4,24 @@
 // The rows that read one key head (its group's q heads times the new tokens; with lists, the group's q heads of
 // one token) are the 16-row side of m16n8k16 products, keys and channels the narrow one:
 //     S [16 rows, 8 keys] = Q K^T,     O [16 rows, 8 channels] += P V
-// The accumulators of S are, packed to bf16, the operand P of the second product.  Few rows against a long cache: 4 G
-// operations for 4 bytes of a key's channel, G rows a head; the memory bounds it by far, and the products only have to stay out
-// of its way (rows that are padding cost nothing that is short).
+// The accumulators of S are, rounded to bf16, the operand P of the second product: both operands have one type, and V
+// comes as bf16.  That takes 8 bits of every probability, as the output's own rounding does of O; l sums them unrounded.
+// The memory bounds it by far (G rows a head: 4 G operations for 4 bytes of a key's channel); at 4 rows a head the
+// products, 8 cycles each of a sub-partition, take a fifth of the time that the keys take to come.
 //
 // A unit of loading is 16 keys (K and V), which lie in one page.  They go by 16-byte asynchronous copies, which
-// take any stride between tokens, heads and pages, into a ring of stages that belongs to the RT warps that
-// share these keys: RT row tiles of 16, a warp each (RT = 1: a warp has its keys for itself, and no barrier).  A CTA has four warps, 4 / RT such groups,
-// which take 16 keys in turn.  A group's page numbers come 32 units at a time, one a lane, a batch ahead.
+// take any stride between tokens, heads and pages and can bring zeros for keys that no row sees, into a ring of stages that
+// belongs to the RT warps that share these keys: RT row tiles of 16, a warp each (RT = 1: a warp has its keys for itself, and
+// no barrier).  A CTA's groups of RT warps take 16 keys in turn.  A group's page numbers come 32 units at a
+// time, one a lane, a batch ahead.
 //
 // Work: all pairs (sequence, head, row tiles; with lists also token) and their tiles of 64 keys, and kPartUnits more units for
 // each pair, form one sequence, cut into equal runs, one per CTA; lengths are read on the device.  A run's parts
 // of pairs that other CTAs share go to the workspace as (m, l, O) records, which a second kernel joins in a fixed order.
+// Where there are pairs enough, a pair goes whole to a CTA instead, and nothing is joined.
+//
+// 64 sequences of 8191 keys on 8 heads, 32 q heads: 314 us, 2.1 GB at 6.8 TB/s, what a copy reaches.  One sequence of 65,536 keys:
+// 47 us (5.7 TB/s); 5 of them until the first keys are there (lengths, table, keys: a chain of loads), 5 the join.
 #include <cmath>
 
 #include "internal.h"
@@ -28,12 +34,13 @@ constexpr int kUnit = 16;       // keys of one load
 constexpr int kTileKeys = 64;
 constexpr int kRowTile = 16;
 constexpr int kPartUnits = 3;   // cost of a part beside its tiles', in tiles
-// Pairs that one CTA takes alone (no records, no join), by the longest that one can be, in tiles: 8; up to 32 while there
-// are pairs enough, tiles x SMs up to 96 x pairs (with several row tiles: pairs for three quarters of the SMs); and lists and windows, whose lengths differ less, of up to 64 where
-// there are pairs for half of the SMs.  Keys on 8 heads, whole and cut (us): 16 x 2048 24.7 and 29.0, 64 x 128 to 1024 31 and 43,
-// 6 x 1024 11.8 and 15.8, 6 x 2048 18.2 and 18.5, 1 x 1024 11.2 and 9.0; on one head of 64 rows 128 x 2048 48.6 and 58.8,
-// 64 x 1024 28.4 and 24.9; 64 pages of 64 for 16 queries 56.7 and 60.3 with their selection.  One sequence of 4096
-// among 15 short ones would take 31 whole and takes 17.
+// Pairs that one CTA takes alone (no records, no join), by the longest that one can be, in tiles: up to 8; up to 32 where
+// there are pairs enough (tiles x SMs up to 96 x pairs; with several row tiles pairs for three quarters of the SMs); and
+// lists and windows, whose lengths differ less, of up to 64 where there are pairs for half of the SMs.
+// Sequences of keys on 8 heads, whole and cut (us): 16 of 2048 24.7 and 29.0, 64 of 128 to 1024 31 and 43, 6 of 1024 11.8 and
+// 15.8, 6 of 2048 18.2 and 18.5, 1 of 1024 11.2 and 9.0; on one head of 64 rows 128 of 2048 48.6 and 58.8, 64 of 1024
+// 28.4 and 24.9; 64 pages of 64 for 16 queries, with their selection, 56.7 and 60.3.  (One sequence of 4096 among 15 short
+// ones would take 31 whole and takes 17.)
 constexpr int kWholeTiles = 8, kManyTiles = 32, kEvenTiles = 64;
 constexpr int kSmWarps = 8;      // warps an SM: a CTA of all of them, or two of four where pairs are whole to a CTA and more than SMs
 constexpr int kWarpRing = 24 * 1024;

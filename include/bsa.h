@@ -558,7 +558,7 @@ typedef struct {
   int64_t first, recent;   /* the first and the last pages that a query sees are always chosen, this many */
 } bsa_paged_select_args;
 
-/* For every query (new token and key head, its group of q heads together) the
+/* For every query (new token and key head, its group of q heads together; scores with a positive scale) the
  * `keep` pages it sees with the largest bound on q.k, in increasing order, -1
  * behind the last one if it sees fewer.  With qc = round_half_even(q / 2^f), f =
  * max(floor(log2 max|q|) - 6, -100) over the group (qc = 0 where max|q| is not
@@ -591,7 +591,7 @@ typedef struct {
   int32_t kind;            /* BSA_MASK_CAUSAL, BSA_MASK_LOCAL or BSA_MASK_CHUNKED_CAUSAL (with select: causal) */
   int64_t local_left;      /* LOCAL: keys back to position - local_left; -1 = unbounded */
   int64_t chunk;           /* CHUNKED_CAUSAL: chunk length (> 0) */
-  float softmax_scale;     /* NaN selects 1/sqrt(D) */
+  float softmax_scale;     /* NaN selects 1/sqrt(D); finite, and over the cap too, if any (below 2^126) */
   float logits_soft_cap;   /* as in bsa_fwd_args */
   const float* sinks;      /* as in bsa_fwd_args */
   int32_t num_sinks, sinks_per_kv_head;

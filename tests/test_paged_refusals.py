@@ -124,7 +124,8 @@ def test_select_needs_bounds():
     ({"select": 112, "keep": 0}, "INVALID_ARG"), ({"select": 114, "keep": 2}, "INVALID_ARG"),
     ({"select": 112, "keep": 2, "kind": 2}, "UNSUPPORTED"), ({"select": 112, "keep": 1 << 28}, "UNSUPPORTED"),
     ({"q_stride": I3(512, 128, 4)}, "INVALID_ARG"), ({"o_stride": I3(512, 0, 128)}, "INVALID_ARG"),
-    ({"logits_soft_cap": -1.0}, "INVALID_ARG"), ({"logits_soft_cap": math.inf}, "INVALID_ARG"),
+    ({"logits_soft_cap": -1.0}, "INVALID_ARG"), ({"logits_soft_cap": math.inf}, "INVALID_ARG"), ({"softmax_scale": math.inf}, "INVALID_ARG"),
+    ({"logits_soft_cap": 1e-30, "softmax_scale": 1e9}, "INVALID_ARG"), ({"logits_soft_cap": math.nan}, "INVALID_ARG"),
     ({"num_sinks": 65, "sinks": 96}, "UNSUPPORTED"), ({"num_sinks": 2}, "INVALID_ARG"), ({"num_sinks": 2, "sinks": 98}, "INVALID_ARG"),
     ({"workspace": None}, "INVALID_ARG"), ({"workspace": 8}, "INVALID_ARG"), ({"workspace_bytes": 64}, "INVALID_ARG"),
 ])
