@@ -127,7 +127,8 @@ def test_select_needs_bounds():
     ({"logits_soft_cap": -1.0}, "INVALID_ARG"), ({"logits_soft_cap": math.inf}, "INVALID_ARG"), ({"softmax_scale": math.inf}, "INVALID_ARG"),
     ({"logits_soft_cap": 1e-30, "softmax_scale": 1e9}, "INVALID_ARG"), ({"logits_soft_cap": math.nan}, "INVALID_ARG"),
     ({"num_sinks": 65, "sinks": 96}, "UNSUPPORTED"), ({"num_sinks": 2}, "INVALID_ARG"), ({"num_sinks": 2, "sinks": 98}, "INVALID_ARG"),
-    ({"workspace": None}, "INVALID_ARG"), ({"workspace": 8}, "INVALID_ARG"), ({"workspace_bytes": 64}, "INVALID_ARG"),
+    ({"M": 4096, "workspace": None}, "INVALID_ARG"), ({"M": 4096, "workspace": 8}, "INVALID_ARG"),
+    ({"M": 4096, "workspace_bytes": 64}, "INVALID_ARG"),  # (sequences that long are cut into runs)
 ])
 def test_fwd_refuses(kw, status):
     abi = _abi()
