@@ -7,6 +7,8 @@
 // unit u holds tokens u * page - o .. (u + 1) * page - o - 1.  It writes them, reads the keys that the page held before them, and
 // has every key of the page in registers then: maxima and minima are exact in any order, so the bounds need no
 // atomics, no second pass over the new keys, and come out the same each time.
+// 4 x 8 heads x 8191 tokens: 43.8 us with bounds (pages of 64; 44.5 with pages of 16, 47.9 of 256), 42.6 without: 91 to 93% of a
+// copy's bandwidth.  64 x 8 heads x 1 token: 3.5 and 2.1 us, latency.
 #include <algorithm>
 
 #include "paged.cuh"

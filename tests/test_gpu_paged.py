@@ -379,7 +379,7 @@ def test_select_of_many_pages(n, queries, keep):
     table = torch.randperm(P, generator=g, device="cuda")[:n].to(torch.int32).expand(queries, n).contiguous()
     q = torch.randn((queries, 2, 1, D), generator=g, device="cuda").to(torch.bfloat16)
     got = bsa.paged_select(q, cache, table, i32([n * 16] * queries), keep, first=2, recent=1)
-    qc = q.double() / 2.0 ** (torch.floor(torch.log2(q.double().abs().amax((1, 2, 3), keepdim=True))) - 6)
+    qc = torch.ldexp(q.float(), 7 - torch.frexp(q.float().abs().amax((1, 2, 3), keepdim=True)).exponent).double()
     qc = torch.round(qc)[:, :, 0].flatten(0, 1)
     b = bounds[table[0].long(), 0].double()
     s = (qc.clamp(min=0) @ b[:, 0].T + qc.clamp(max=0) @ b[:, 1].T).view(queries, 2, n).amax(1)
