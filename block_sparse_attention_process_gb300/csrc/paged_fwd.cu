@@ -49,7 +49,6 @@ constexpr int kSmWarps = 8;      // warps an SM: a CTA of all of them, or two of
 constexpr int kWarpRing = 24 * 1024;
 constexpr int smem_bytes(int warps) { return warps * kWarpRing + 256; }
 constexpr int32_t kNoKeys = -4096;  // place of a unit without keys: before every key a row sees
-constexpr float kLag = 8.0f;        // log2 units
 constexpr float kLog2e = 1.4426950408889634f;
 constexpr float kLn2 = 0.69314718055994530942f;
 
@@ -594,8 +593,9 @@ __global__ void __launch_bounds__(32 * W, kSmWarps / W) paged_fwd_kernel(const _
               if (j < lo[e >> 1] || j > hi[e >> 1]) s[y][c][e] = -INFINITY;
             }
       }
-      // ---- running maximum and sum; the reference m follows the maximum once that is 2^kLag above it (a probability is
-      // rounded to 8 bits wherever it lies, so the lag costs no accuracy and saves the scaling of O)
+      // ---- running maximum and sum.  (A reference that lags by up to 2^8 saves the scaling of O, 1% of the time; but the largest
+      // probability, now 1 exactly, is then rounded too, and where it counts for much the error of O grows from
+      // 2.0e-3 to 2.4e-3 of its norm.)
       float top[2];
       bool moved = false;
 #pragma unroll
@@ -604,13 +604,13 @@ __global__ void __launch_bounds__(32 * W, kSmWarps / W) paged_fwd_kernel(const _
         if constexpr (kPer == 2) x = fmaxf(x, fmaxf(fmaxf(s[1][0][2 * r], s[1][0][2 * r + 1]), fmaxf(s[1][1][2 * r], s[1][1][2 * r + 1])));
         x = fmaxf(x, __shfl_xor_sync(0xffffffffu, x, 1));
         top[r] = fmaxf(m[r], fmaxf(x, __shfl_xor_sync(0xffffffffu, x, 2)));
-        if (top[r] > m[r] + kLag) moved = true;
-        else top[r] = m[r];  // (each row by itself: no row's bits depend on what others see)
+        moved |= top[r] > m[r];
       }
       if (__any_sync(0xffffffffu, moved)) {
 #pragma unroll
         for (int r = 0; r < 2; ++r) {
-          const float f = ex2_approx(m[r] - (top[r] == -INFINITY ? 0.f : top[r]));  // (0 of a row's first keys)
+          // (0 of a row's first keys; 1 for a row that has not moved: no row's bits depend on what others see)
+          const float f = ex2_approx(m[r] - (top[r] == -INFINITY ? 0.f : top[r]));
           l[r] *= f;
           m[r] = top[r];
 #pragma unroll
