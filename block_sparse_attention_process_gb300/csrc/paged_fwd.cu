@@ -20,8 +20,8 @@
 // of pairs that other CTAs share go to the workspace as (m, l, O) records, which a second kernel joins in a fixed order.
 // Where there are pairs enough, a pair goes whole to a CTA instead, and nothing is joined.
 //
-// 64 sequences of 8191 keys on 8 heads, 32 q heads: 309 us, 2.1 GB at 6.9 TB/s, what a copy reaches.  One sequence of 65,536 keys:
-// 46 us (5.8 TB/s); 5 of them until the first keys are there (lengths, table, keys: a chain of loads), 5 the join.
+// 64 sequences of 8191 keys on 8 heads, 32 q heads: 312 us, 2.1 GB at 6.9 TB/s, what a copy reaches.  One sequence of 65,536 keys:
+// 47 us (5.7 TB/s); 5 of them until the first keys are there (lengths, table, keys: a chain of loads), 5 the join.
 #include <cmath>
 
 #include "internal.h"
