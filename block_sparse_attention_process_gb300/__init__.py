@@ -388,7 +388,7 @@ def _lens(name: str, t: Optional[torch.Tensor], B: int, index: int) -> int:
 
 # a workspace for one call, on the stream that the call uses (an allocation by way of a tensor costs three times as much
 # beside a launch)
-_raw_alloc, _raw_free = torch._C._cuda_cudaCachingAllocator_raw_alloc, torch._C._cuda_cudaCachingAllocator_raw_delete
+_raw_alloc, _raw_free = (getattr(torch._C, "_cuda_cudaCachingAllocator_raw_" + x, None) for x in ("alloc", "delete"))
 
 
 def _workspace(need: int, device) -> Optional[torch.Tensor]:
@@ -642,6 +642,8 @@ def paged_resize(table: torch.Tensor, free: torch.Tensor, used: torch.Tensor, le
     index = table.get_device()
     if index < 0:
         raise ValueError("table must be a contiguous CUDA int32 tensor")
+    if lens is None or new_lens is None:
+        raise ValueError("lens and new_lens are missing")
     B = table.shape[0]
     head = (_table(table, B, index), _need("free", free, torch.int32, index, (free.numel(),)),
             _need("used", used, torch.int32, index, (1,)), _lens("lens", lens, B, index), _lens("new_lens", new_lens, B, index))

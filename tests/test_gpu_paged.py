@@ -716,7 +716,7 @@ def test_wrong_tensors_are_refused():
         lambda: bsa.paged_select(q, cache, table, n, 0, first=0, recent=0), lambda: bsa.paged_select(q[:, :3], cache, table, n, 3),
         lambda: bsa.paged_append(cache, k, k, n), lambda: bsa.paged_append(cache, k, k[:1], i32([[0], [16]])),
         lambda: bsa.paged_append(cache, k[..., :32], k[..., :32], i32([[0], [16]])),
-        lambda: bsa.paged_resize(table, n, n[:1], n, n, 24, 1), lambda: bsa.paged_resize(table, n, n[:1], n, n, 16, 0),
+        lambda: bsa.paged_resize(table, n, n[:1], None, n, 16, 1), lambda: bsa.paged_resize(table, n, n[:1], n, n, 24, 1), lambda: bsa.paged_resize(table, n, n[:1], n, n, 16, 0),
         lambda: bsa.paged_resize(table, n, n, n, n, 16, 1), lambda: bsa.PagedCache(cache.k, cache.v[:1]),
         lambda: bsa.PagedCache(cache.k, cache.v, cache.bounds[:1]), lambda: bsa.PagedCache(cache.k[:, :, :8], cache.v[:, :, :8]) and bsa.paged_append(
             bsa.PagedCache(cache.k[:, :, :8], cache.v[:, :, :8]), k, k, i32([[0], [16]])),
