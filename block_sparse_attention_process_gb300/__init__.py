@@ -340,13 +340,16 @@ def _elsewhere(device, stream):
                 yield
 
 
+_raw_stream, _current_device = (getattr(torch._C, "_cuda_" + x, None) for x in ("getCurrentRawStream", "getDevice"))
+
+
 def _place(device: torch.device, index: int, stream):
     """(context, stream handle) of a call on tensors of `device`: inside the
     context the device and the stream are current, so that what the call
     allocates belongs to the stream it is used on."""
     if stream is None:
-        handle = torch._C._cuda_getCurrentRawStream(index)
-        return (_INLINE if index == torch._C._cuda_getDevice() else _elsewhere(device, None)), handle
+        handle = _raw_stream(index)
+        return (_INLINE if index == _current_device() else _elsewhere(device, None)), handle
     if not isinstance(stream, torch.cuda.Stream):
         stream = torch.cuda.ExternalStream(int(stream), device=device) if int(stream) else torch.cuda.default_stream(device)
     if stream.device != device:
@@ -600,12 +603,12 @@ class PagedCache:
     __slots__ = ("k", "v", "bounds", "pages", "Hkv", "page", "D", "device", "index", "_c")
 
     def __init__(self, k: torch.Tensor, v: torch.Tensor, bounds: Optional[torch.Tensor] = None):
-        index = k.get_device()
-        if index < 0 or k.dim() != 4:
+        index, shape = k.get_device(), k.shape
+        if index < 0 or len(shape) != 4:
             raise ValueError("k must be a CUDA bfloat16 tensor [pages, Hkv, page, D]")
-        if v.shape != k.shape:
+        if v.shape != shape:
             raise ValueError("v must have k's shape")
-        P, H, page, D = k.shape
+        P, H, page, D = shape
         self._c = _abi.PAGED_CACHE.pack(
             k.data_ptr(), v.data_ptr(), *_pages("k", k, index), *_pages("v", v, index),
             0 if bounds is None else _need("bounds", bounds, torch.bfloat16, index, (P, H, 2, D)), P, H, D, page)
