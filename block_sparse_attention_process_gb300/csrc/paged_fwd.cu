@@ -673,9 +673,11 @@ __global__ void __launch_bounds__(32 * W, kSmWarps / W) paged_fwd_kernel(const _
     }
     __syncthreads();  // (and every warp is done with the ring)
     float* merge = reinterpret_cast<float*>(ring);
+    const int32_t live = min(kRows, p.R - run.rt * kRows);
 #pragma unroll
     for (int r = 0; r < 2; ++r) {
       const int row = tile * kRowTile + g + 8 * r;
+      if (row >= live) continue;
       float top = -INFINITY;
 #pragma unroll
       for (int w = 0; w < kGroups; ++w) top = fmaxf(top, stat_m[w][row]);
@@ -686,7 +688,6 @@ __global__ void __launch_bounds__(32 * W, kSmWarps / W) paged_fwd_kernel(const _
     }
     __syncthreads();
     const int64_t rec = 2 * static_cast<int64_t>(BSA_RANGE(static_cast<int32_t>(blockIdx.x), 0, p.n_cta, p.err)) + (part > 0 ? 1 : 0);
-    const int32_t live = min(kRows, p.R - run.rt * kRows);
     for (int i = threadIdx.x; i < live * (D / 4); i += 32 * W) {
       const int row = i / (D / 4), d = i % (D / 4) * 4;
       float top = -INFINITY, sum = 0.f;
