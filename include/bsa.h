@@ -568,9 +568,10 @@ typedef struct {
  * order, so the choice does not depend on how the work is split.  Token t of
  * n = q_lens[b] stands at position lens[b] - n + t and sees the pages up to
  * its own.  Rows of padding, or of tokens before position 0, are -1.  Lengths
- * outside 0..M*page count as the nearer end, page numbers outside the cache
- * as a score of minus infinity; both set the bounds bit of the device error
- * word. */
+ * outside 0..M*page count as the nearer end; a page number outside the cache
+ * counts as a score of minus infinity where pages are scored (a query that
+ * sees `keep` pages or fewer has them all).  Both set the bounds bit of the
+ * device error word. */
 BSA_API bsa_status bsa_paged_select(const bsa_paged_select_args* args, bsa_stream stream);
 
 typedef struct {
