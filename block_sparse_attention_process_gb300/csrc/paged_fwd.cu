@@ -417,8 +417,9 @@ __global__ void __launch_bounds__(32 * W, kSmWarps / W) paged_fwd_kernel(const _
     const int32_t b = pair.s / p.queries, h = run.h;
     const int32_t* table = p.table + b * p.M;
     const int32_t* list = p.select ? p.select + ((static_cast<int64_t>(b) * p.Hkv + h) * p.T + pair.s % p.queries) * p.keep : nullptr;
-    // ---- units of this group: numbers u0 + i * kGroups
-    const int32_t u0 = run.k0 * (kTileKeys / kUnit) + group;
+    // ---- units of this group: numbers u0 + i * kGroups, none of them before the first key that is seen or past the last
+    // (the table's entries there need not be pages)
+    const int32_t u0 = max(run.k0 * (kTileKeys / kUnit), pair.lo / kUnit) + group;
     const int32_t u1 = min(run.k1 * (kTileKeys / kUnit), (pair.hi + kUnit - 1) / kUnit);
     const int32_t n = u1 > u0 ? (u1 - u0 + kGroups - 1) / kGroups : 0;
     // pages of units i0 .. i0 + 31, one a lane: its number in the cache (-1: none), and in the sequence

@@ -610,7 +610,9 @@ typedef struct {
  * whatever they hold, and one that some row sees changes no row that does not.
  * A length outside 0..M*page counts as the nearer end, a page number outside
  * the cache, or in a list outside the pages a query sees, as a page without
- * keys; both set the bounds bit of the device error word. */
+ * keys; both set the bounds bit of the device error word.  Entries of pages that no
+ * row sees (behind a local or chunked mask, past the last key) are not
+ * looked at. */
 BSA_API bsa_status bsa_paged_fwd(const bsa_paged_fwd_args* args, bsa_stream stream);
 BSA_API bsa_status bsa_paged_fwd_workspace(const bsa_paged_fwd_args* args, size_t* bytes);
 
