@@ -103,7 +103,7 @@ __device__ __forceinline__ Pair load_pair(const FwdParams& p, int32_t s, uint32_
   x.s = s;
   const int32_t b = s / p.queries;
   x.len = paged_len(__ldcg(p.lens + b), p.M << p.shift, err);
-  x.nq = p.q_lens ? min(max(__ldcg(p.q_lens + b), 0), p.T) : p.T;
+  x.nq = p.q_lens ? paged_len(__ldcg(p.q_lens + b), p.T, err) : p.T;
   x.lo = 0;
   x.hi = 0;
   if (p.select) {

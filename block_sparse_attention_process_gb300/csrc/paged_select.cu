@@ -49,7 +49,7 @@ struct SelectParams {
 // Pages that token t of sequence b sees (0: padding).
 __device__ __forceinline__ int32_t pages_seen(const SelectParams& p, int32_t b, int32_t t, uint32_t* err) {
   const int32_t len = paged_len(p.lens[b], p.M << p.shift, err);
-  const int32_t nq = p.q_lens ? min(max(p.q_lens[b], 0), p.T) : p.T;
+  const int32_t nq = p.q_lens ? paged_len(p.q_lens[b], p.T, err) : p.T;
   if (t >= nq) return 0;
   const int64_t end = static_cast<int64_t>(len) - nq + t + 1;  // keys
   return end <= 0 ? 0 : static_cast<int32_t>((end + (1 << p.shift) - 1) >> p.shift);

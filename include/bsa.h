@@ -568,9 +568,9 @@ typedef struct {
  * order, so the choice does not depend on how the work is split.  Token t of
  * n = q_lens[b] stands at position lens[b] - n + t and sees the pages up to
  * its own.  Rows of padding, or of tokens before position 0, are -1.  Lengths
- * outside 0..M*page count as the nearer end; a page number outside the cache
+ * outside 0..M*page, and q_lens outside 0..T, count as the nearer end; a page number outside the cache
  * counts as a score of minus infinity where pages are scored (a query that
- * sees `keep` pages or fewer has them all).  Both set the bounds bit of the
+ * sees `keep` pages or fewer has them all).  All of them set the bounds bit of the
  * device error word. */
 BSA_API bsa_status bsa_paged_select(const bsa_paged_select_args* args, bsa_stream stream);
 
@@ -608,9 +608,9 @@ typedef struct {
  * see nothing and padding rows get O = 0 and LSE = -inf (the log-sum of the
  * sinks where there are any).  Slots that no row of a call sees are never used,
  * whatever they hold, and one that some row sees changes no row that does not.
- * A length outside 0..M*page counts as the nearer end, a page number outside
+ * A length outside 0..M*page, or a q_lens[b] outside 0..T, counts as the nearer end, a page number outside
  * the cache, or in a list outside the pages a query sees, as a page without
- * keys; both set the bounds bit of the device error word.  Entries of pages that no
+ * keys; all of them set the bounds bit of the device error word.  Entries of pages that no
  * row sees (behind a local or chunked mask, past the last key) are not
  * looked at. */
 BSA_API bsa_status bsa_paged_fwd(const bsa_paged_fwd_args* args, bsa_stream stream);
