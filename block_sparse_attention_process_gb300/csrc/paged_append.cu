@@ -6,7 +6,8 @@
 // tokens follow each other, so token t lies at place (o + t) % page, o being the place of token 0, and
 // unit u holds tokens u * page - o .. (u + 1) * page - o - 1.  It writes them, reads the keys that the page held before them, and
 // has every key of the page in registers then: maxima and minima are exact in any order, so the bounds need no
-// atomics, no second pass over the new keys, and come out the same each time.
+// atomics, no second pass over the new keys, and come out the same each time.  Where a place among the new tokens' was left out
+// (padding, or a slot elsewhere) the page holds a key there that no register does: its bounds are infinite then.
 // 4 x 8 heads x 8191 tokens: 43.8 us with bounds (pages of 64; 44.5 with pages of 16, 47.9 of 256), 42.6 without: 91 to 93% of a
 // copy's bandwidth.  64 x 8 heads x 1 token: 3.5 and 2.1 us, latency.
 #include <algorithm>
@@ -127,6 +128,7 @@ __global__ void __launch_bounds__(kThreads) append_bounds_kernel(const __grid_co
   constexpr int kLanes = D / 8, kWarps = kThreads / 32;
   __shared__ float hi[kWarps][D], lo[kWarps][D];
   __shared__ uint32_t top[kWarps];
+  __shared__ int32_t left_out[kWarps], stored[kWarps];  // the first place left out, the last one stored
   griddep_launch_dependents();
   griddep_wait();
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
@@ -151,7 +153,7 @@ __global__ void __launch_bounds__(kThreads) append_bounds_kernel(const __grid_co
   const bool good = page0 >= 0 && (page0 & (page - 1)) == 0;
   Range r;
   r.clear();
-  int32_t last = -1;
+  int32_t last = -1, gap = INT32_MAX;
   bool wrong = false;
   const __nv_bfloat16* src_k = p.k + b * p.ks[0] + h * p.ks[1] + 8 * u;
   const __nv_bfloat16* src_v = p.v + b * p.vs[0] + h * p.vs[1] + 8 * u;
@@ -174,9 +176,9 @@ __global__ void __launch_bounds__(kThreads) append_bounds_kernel(const __grid_co
 #pragma unroll
     for (int x = 0; x < kBatch; ++x) {
       const int32_t i = i0 + x * kSubs;
-      if (slot[x] < 0) continue;
-      if (!good || slot[x] != page0 + i) {
-        wrong = true;
+      if (slot[x] < 0 || !good || slot[x] != page0 + i) {
+        wrong |= slot[x] >= 0;
+        gap = min(gap, i);
         continue;
       }
       slot[x] = BSA_RANGE(slot[x], 0, static_cast<int32_t>(limit), p.err);
@@ -200,6 +202,8 @@ __global__ void __launch_bounds__(kThreads) append_bounds_kernel(const __grid_co
     }
   }
   r.top = __reduce_max_sync(0xffffffffu, r.top);
+  last = __reduce_max_sync(0xffffffffu, last);
+  gap = __reduce_min_sync(0xffffffffu, gap);
   if (lane < kLanes) {
 #pragma unroll
     for (int i = 0; i < 8; ++i) {
@@ -207,18 +211,28 @@ __global__ void __launch_bounds__(kThreads) append_bounds_kernel(const __grid_co
       lo[warp][8 * u + i] = r.lo[i];
     }
   }
-  if (lane == 0) top[warp] = r.top;
+  if (lane == 0) {
+    top[warp] = r.top;
+    left_out[warp] = gap;
+    stored[warp] = last;
+  }
   group_sync(group, warps);
   for (int d = threadIdx.x - first_warp * 32; d < D; d += warps * 32) {
     float a = hi[first_warp][d], c = lo[first_warp][d];
     uint32_t m = top[first_warp];
+    gap = left_out[first_warp];
+    last = stored[first_warp];
     for (int w = first_warp + 1; w < first_warp + warps; ++w) {
       a = fmaxf(a, hi[w][d]);
       c = fminf(c, lo[w][d]);
       m = max(m, top[w]);
+      gap = min(gap, left_out[w]);
+      last = max(last, stored[w]);
     }
+    const bool whole = last < gap;
+    if (!whole && d == 0 && p.err) atomicOr(p.err, DEV_ERR_BOUNDS);
     const float largest = __uint_as_float(m << 16);
-    if (largest < kUsualTop) {
+    if (largest < kUsualTop && whole) {
       float s, inv;
       unit_of(largest, 7, s, inv);
       const float up = ceilf(a * inv) * s, down = floorf(c * inv) * s;

@@ -536,9 +536,11 @@ typedef struct {
  * A cache without bounds takes tokens in any order.  With bounds, the slots are
  * those of bsa_paged_resize: each sequence's tokens fill its pages in order, from
  * wherever the first one is, padding behind the last, and no two sequences of a call have tokens in one
- * page; a token out of that order is not stored and sets the bounds bit.  The
- * bounds of every page that takes tokens are then renewed, over its slots 0
- * .. last new one: with m the largest magnitude of the head's keys there and e =
+ * page.  A token in another place than its page's first new one gives (padding
+ * gives none) is not stored and sets the bounds bit; so does padding between
+ * two tokens of a page (those are stored).  The bounds of every page that takes
+ * tokens are then renewed, over its slots 0 .. last new one (infinite if a place
+ * among the new tokens' was left out): with m the largest magnitude of the head's keys there and e =
  * max(floor(log2 m) - 7, -100), each channel's largest and smallest key
  * rounded up and down to a multiple of 2^e (exact in bf16); plus and minus
  * infinity throughout where m is not below 2^100 or a key is NaN. */
