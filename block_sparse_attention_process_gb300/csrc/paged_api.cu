@@ -153,7 +153,7 @@ bsa_status check_fwd(const bsa_paged_fwd_args* a) {
     if (!aligned4(a->select)) return bad("select must be 4-byte aligned");
   }
   if (!paged_fwd_fits(a)) return unsupported("too many rows for one launch");
-  if (!(a->logits_soft_cap >= 0.f) || std::isinf(a->logits_soft_cap)) return bad("logits_soft_cap must be finite and >= 0");
+  if (!(a->logits_soft_cap >= 0.f) || std::isinf(4.0f * a->logits_soft_cap)) return bad("logits_soft_cap must be >= 0 and below 2^126");
   if (a->num_sinks < 0 || a->num_sinks > 64) return unsupported("num_sinks must be in 0..64");
   if (a->num_sinks > 0 && !a->sinks) return bad("sinks is null");
   if (!aligned4(a->sinks)) return bad("sinks must be 4-byte aligned");

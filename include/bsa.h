@@ -157,7 +157,10 @@ typedef struct {
   float softmax_scale; /* NaN selects 1/sqrt(D) */
   /* Optional score transforms (the logits_soft_cap and softmax_aux arguments
    * of the EasyDeL blocksparse_attention operator; zero-initialised = off):
-   * logits_soft_cap c > 0 maps each visible scaled score s to c*tanh(s/c);
+   * logits_soft_cap c > 0 maps each visible scaled score s to c*tanh(s/c)
+   * (tanh is formed to 2^-20, so a score is off by up to 2^-20 c: caps of tens
+   * or hundreds are what this is for, and only bsa_paged_fwd is exact to a
+   * score's own last bits for larger ones);
    * sinks are num_sinks extra logits per row that enter the normaliser (and
    * the maximum) but carry no value, fp32 on the device, [Hkv, num_sinks]
    * (q head h uses row h / (Hq/Hkv)) when sinks_per_kv_head is 1, else
@@ -595,7 +598,7 @@ typedef struct {
   int64_t local_left;      /* LOCAL: keys back to position - local_left; -1 = unbounded */
   int64_t chunk;           /* CHUNKED_CAUSAL: chunk length (> 0) */
   float softmax_scale;     /* NaN selects 1/sqrt(D); finite, and over the cap too, if any (below 2^126) */
-  float logits_soft_cap;   /* as in bsa_fwd_args */
+  float logits_soft_cap;   /* as in bsa_fwd_args, below 2^126; however large, it costs a score no more than its own last bits */
   const float* sinks;      /* as in bsa_fwd_args */
   int32_t num_sinks, sinks_per_kv_head;
   void* workspace;         /* device, 16-byte aligned, bsa_paged_fwd_workspace bytes */

@@ -114,3 +114,64 @@ def test_tokens_out_of_order_leave_no_bound_too_small():
     held = f64(cache.k)[0, 0, :12]
     assert held[6].tolist() == [100.0] * 64 and held[7].tolist() == f64(k)[0, 0, 3].tolist()
     assert (f64(cache.bounds)[0, 0, 0] >= held.max(0)).all() and (f64(cache.bounds)[0, 0, 1] <= held.min(0)).all()
+
+
+# ------------------------------------------------------------------ scores and sums
+
+def reference(cache, table, k, v, q, lens, *, q_lens=None, cap=0.0, scale=None):
+    """O, LSE, sum p |v| and A of every row, fp64."""
+    B, Hq, T, D = q.shape
+    want, wl, mass, a = np.zeros((B, Hq, T, D)), np.zeros((B, Hq, T)), np.zeros((B, Hq, T, D)), np.zeros((B, Hq, T))
+    qh, kh, vh = f64(q), f64(k), f64(v)
+    for b in range(B):
+        nq = T if q_lens is None else q_lens[b]
+        for h in range(Hq):
+            for t in range(T):
+                n = max(lens[b] - nq + t + 1, 0) if t < nq else 0
+                g = h // (Hq // cache.Hkv)
+                want[b, h, t], wl[b, h, t], mass[b, h, t], a[b, h, t] = paged.attend(
+                    qh[b, h, t], kh[b, g, :n], vh[b, g, :n], D ** -0.5 if scale is None else scale, cap)
+    return want, wl, mass, a
+
+
+@pytest.mark.parametrize("cap", [1.0, 5.0, 30.0, 1e3, 1e4, 1e6, 1e12, 1e30, 8e37])
+@pytest.mark.parametrize("D,G,T", [(64, 4, 1), (128, 4, 1), (128, 16, 2)])
+def test_a_cap_of_any_size(cap, D, G, T):
+    """A capped score is no further off than its own size allows, however large the cap.
+
+    tanh x as 1 - 2 / (1 + e^2x): e off by 2^-22 (exp2) + 2 |x| 2^-23 (its argument) relative, 1 + e by 2^-24, the reciprocal
+    by 2^-23, the difference by 2^-24: 2^-20.8 absolute, of tanh x from 1/4 on 2^-18.8 relative.  Below 1/4 a polynomial, 2^-22
+    relative.  |capped| <= A: ds = (2^-16 + 2^-18) A.  Four units in the last place of an exponential 2^-20, of a logarithm and its
+    conversion 2^-20 max(1, |lse|)."""
+    bsa = bsa_()
+    lens = [700, 40]
+    cache, table, k, v = paged_batch(bsa, 2, 2, D, 16, lens, 9, scale=2.0)
+    q = rows((2, 2 * G, T, D), 10, 2.0).cuda()
+    want, wl, mass, a = reference(cache, table, k, v, q, lens, cap=cap)
+    ds = (2.0 ** -16 + 2.0 ** -18) * a
+    for M in (None, 256):
+        wide = table if M is None else torch.cat((table, table.new_full((2, M - table.shape[1]), -1)), 1).contiguous()
+        o, lse = bsa.paged_fwd(q, cache, wide, i32(lens), logits_soft_cap=cap)
+        within("lse", f64(lse), wl, ds + 2.0 ** -20 * np.maximum(1, np.abs(wl)))
+        within("o", f64(o), want, 2.0 ** -8 * np.abs(want) + (2.0 ** -8 + 2 * ds[..., None] + 2.0 ** -19) * mass)
+    assert bsa.get_device_error() == 0
+
+
+def test_caps_and_infinities():
+    """A NaN score stays one, an infinite one is the cap itself."""
+    bsa = bsa_()
+    n = 40
+    cache, table, k, v = paged_batch(bsa, 1, 1, 64, 16, [n], 9)
+    q = torch.ones((1, 4, 1, 64), dtype=torch.bfloat16, device="cuda")
+    for bad, limit in ((float("inf"), 20.0), (-float("inf"), -20.0)):
+        k[0, 0, 5] = bad
+        cache.k[table[0, 0].long(), 0, 5] = bad
+        s = 20.0 * np.tanh((f64(k)[0, 0, :n].sum(1) / 8) / 20.0)
+        assert s[5] == limit
+        want = np.log(np.exp(s).sum())
+        _, lse = bsa.paged_fwd(q, cache, table, i32([n]), logits_soft_cap=20.0)
+        a = np.delete(np.abs(f64(k)[0, 0, :n]).sum(1) / 8, 5).max()
+        within("lse", f64(lse), np.full((1, 4, 1), want), (2.0 ** -16 + 2.0 ** -18) * max(a, 20.0) + 2.0 ** -20 * max(1, abs(want)))
+    cache.k[table[0, 0].long(), 0, 5] = float("nan")
+    o, lse = bsa.paged_fwd(q, cache, table, i32([n]), logits_soft_cap=20.0)
+    assert torch.isnan(lse).all() and torch.isnan(o.float()).all()
