@@ -4,8 +4,11 @@
 // The rows that read one key head (its group's q heads times the new tokens; with lists, the group's q heads of
 // one token) are the 16-row side of m16n8k16 products, keys and channels the narrow one:
 //     S [16 rows, 8 keys] = Q K^T,     O [16 rows, 8 channels] += P V
-// The accumulators of S are, rounded to bf16, the operand P of the second product: both operands have one type, and V
-// comes as bf16.  That takes 8 bits of every probability, as the output's own rounding does of O; l sums them unrounded.
+// The accumulators of S are the operand P of the second product, as a sum of two bf16 numbers and so in two products: both
+// operands have one type, V comes as bf16, and 8 bits of a probability alone would cost O as much as its own rounding does (error
+// against 64 bits 2.0e-3 of the norm, with two terms 1.7e-3, which is the output's rounding).  One term and two: 64 x 8191
+// keys 309.5 and 309.7 us, 16 ragged sequences 54.3 and 55.2, 64 of 128 to 1024 31.3 and 33.1, 64 rows of 16,384 keys 23.9 and 25.9, 128
+// rows 52.2 and 58.9.
 // The memory bounds it by far (G rows a head: 4 G operations for 4 bytes of a key's channel); at 4 rows a head the
 // products, 8 cycles each of a sub-partition, take a fifth of the time that the keys take to come.
 //
@@ -379,18 +382,30 @@ __device__ __forceinline__ uint32_t odd_keys(uint32_t v, int lane) {
   return (keys | keys >> 16) & 0xFFFFu;
 }
 
-// O += p v of the marked keys, for the rows that see them (probabilities as the product's operand).
+// Probabilities a and b as sums of two bf16 numbers, the operands of two products: the first is a (1 - 2^-8) cut to 8 bits, the second the
+// rest, rounded, so 2^-14 of a are lost.  Neither is 0 where a is not (an infinite value stays one).
+__device__ __forceinline__ void two_terms(float a, float b, uint32_t& first, uint32_t& rest) {
+  const uint32_t x = __float_as_uint(a * (1.f - 0x1p-8f)), y = __float_as_uint(b * (1.f - 0x1p-8f));
+  first = __byte_perm(x, y, 0x7632);
+  rest = pack_bf16x2(a - __uint_as_float(x & 0xFFFF0000u), b - __uint_as_float(y & 0xFFFF0000u));
+}
+
+// O += p v of the marked keys, for the rows that see them (probabilities as the products' operands).
 template <int D>
-__device__ __forceinline__ void add_odd_keys(float (&acc)[D / 8][4], const uint32_t (&pa)[4], uint32_t keys, uint32_t v, int lane, int32_t pos,
+__device__ __forceinline__ void add_odd_keys(float (&acc)[D / 8][4], const uint32_t (&pa)[4], const uint32_t (&pb)[4], uint32_t keys, uint32_t v, int lane, int32_t pos,
                                           const int32_t (&lo)[2], const int32_t (&hi)[2]) {
   const int t4 = lane & 3;
   for (; keys; keys &= keys - 1) {
     const int j = __ffs(keys) - 1, from = (lane & 28) | ((j & 7) >> 1);
 #pragma unroll
     for (int r = 0; r < 2; ++r) {
-      const uint32_t w0 = __shfl_sync(0xffffffffu, pa[r], from), w1 = __shfl_sync(0xffffffffu, pa[2 + r], from);
-      const uint32_t w = j < 8 ? w0 : w1;
-      const float x = __uint_as_float(j & 1 ? w & 0xFFFF0000u : w << 16);
+      float x = 0.f;
+#pragma unroll
+      for (int i = 0; i < 2; ++i) {
+        const uint32_t w0 = __shfl_sync(0xffffffffu, i ? pb[r] : pa[r], from), w1 = __shfl_sync(0xffffffffu, i ? pb[2 + r] : pa[2 + r], from);
+        const uint32_t w = j < 8 ? w0 : w1;
+        x += __uint_as_float(j & 1 ? w & 0xFFFF0000u : w << 16);
+      }
       if (pos + j < lo[r] || pos + j > hi[r]) continue;
 #pragma unroll
       for (int c = 0; c < D / 8; ++c) {
@@ -622,9 +637,8 @@ __global__ void __launch_bounds__(32 * W, kSmWarps / W) paged_fwd_kernel(const _
               if (j < lo[e >> 1] || j > hi[e >> 1]) s[y][c][e] = -INFINITY;
             }
       }
-      // ---- running maximum and sum.  (A reference that lags by up to 2^8 saves the scaling of O, 1% of the time; but the largest
-      // probability, now 1 exactly, is then rounded too, and where it counts for much the error of O grows from
-      // 2.0e-3 to 2.4e-3 of its norm.)
+      // ---- running maximum and sum.  (A reference that lags by up to 2^8 saved the scaling of O, 1% of the time, while a
+      // probability was one bf16 term, whose error it raised from 2.0e-3 to 2.4e-3 of the norm of O; with two it was not measured.)
       float top[2];
       bool moved = false;
 #pragma unroll
@@ -652,14 +666,14 @@ __global__ void __launch_bounds__(32 * W, kSmWarps / W) paged_fwd_kernel(const _
       const float from[2] = {m[0] == -INFINITY ? 0.f : m[0], m[1] == -INFINITY ? 0.f : m[1]};
 #pragma unroll
       for (int y = 0; y < kPer; ++y) {
-        uint32_t pa[4];
+        uint32_t pa[4], pb[4];
 #pragma unroll
         for (int c = 0; c < 2; ++c)
 #pragma unroll
           for (int r = 0; r < 2; ++r) {
             const float a = ex2_approx(s[y][c][2 * r] - from[r]), b = ex2_approx(s[y][c][2 * r + 1] - from[r]);
             l[r] += a + b;
-            pa[2 * c + r] = pack_bf16x2(a, b);
+            two_terms(a, b, pa[2 * c + r], pb[2 * c + r]);
           }
         const uint32_t vs = lane_vf + at + y * Sh::kUnitBytes;
         if (masked && p.T > 1 && !p.select) {
@@ -667,15 +681,19 @@ __global__ void __launch_bounds__(32 * W, kSmWarps / W) paged_fwd_kernel(const _
           // them is not 0): such keys leave the product and are added row by row
           const uint32_t keys = odd_keys<D>(ring0 + at + y * Sh::kUnitBytes + kUnit * D * 2, lane);
           if (keys) {
-            add_odd_keys<D>(acc, pa, keys, ring0 + at + y * Sh::kUnitBytes + kUnit * D * 2, lane, pos[y], lo, hi);
+            add_odd_keys<D>(acc, pa, pb, keys, ring0 + at + y * Sh::kUnitBytes + kUnit * D * 2, lane, pos[y], lo, hi);
             const uint32_t keep[2] = {(keys >> (2 * t4) & 1u ? 0u : 0xFFFFu) | (keys >> (2 * t4 + 1) & 1u ? 0u : 0xFFFF0000u),
                                       (keys >> (8 + 2 * t4) & 1u ? 0u : 0xFFFFu) | (keys >> (9 + 2 * t4) & 1u ? 0u : 0xFFFF0000u)};
 #pragma unroll
             for (int c = 0; c < D / 16; ++c) {
               uint32_t vb[4];
               ldsm4t(vb, vs ^ (c << 5));
-              mma_bf16(acc[2 * c], pa, vb[0] & keep[0], vb[1] & keep[1]);
-              mma_bf16(acc[2 * c + 1], pa, vb[2] & keep[0], vb[3] & keep[1]);
+#pragma unroll
+              for (int x = 0; x < 4; ++x) vb[x] &= keep[x & 1];
+              mma_bf16(acc[2 * c], pa, vb[0], vb[1]);
+              mma_bf16(acc[2 * c + 1], pa, vb[2], vb[3]);
+              mma_bf16(acc[2 * c], pb, vb[0], vb[1]);
+              mma_bf16(acc[2 * c + 1], pb, vb[2], vb[3]);
             }
             continue;
           }
@@ -686,6 +704,8 @@ __global__ void __launch_bounds__(32 * W, kSmWarps / W) paged_fwd_kernel(const _
           ldsm4t(vb, vs ^ (c << 5));
           mma_bf16(acc[2 * c], pa, vb[0], vb[1]);
           mma_bf16(acc[2 * c + 1], pa, vb[2], vb[3]);
+          mma_bf16(acc[2 * c], pb, vb[0], vb[1]);
+          mma_bf16(acc[2 * c + 1], pb, vb[2], vb[3]);
         }
       }
     }

@@ -175,3 +175,64 @@ def test_caps_and_infinities():
     cache.k[table[0, 0].long(), 0, 5] = float("nan")
     o, lse = bsa.paged_fwd(q, cache, table, i32([n]), logits_soft_cap=20.0)
     assert torch.isnan(lse).all() and torch.isnan(o.float()).all()
+
+
+def nearly_cancelling(D, G, seed):
+    """q, k, v of two keys: with a_h the probability of key 1 relative to key 0's in head h, v0 is minus a_d rounded to bf16 in
+    channel d and v1 is 1, so that O[h, h] is what rounding a_h to bf16 takes off."""
+    g = torch.Generator().manual_seed(seed)
+    q, k, v = torch.zeros((G, D)), torch.zeros((2, D)), torch.ones((2, D))
+    q[:, 0] = -(0.2 + torch.rand(G, generator=g))
+    q = q.to(torch.bfloat16)
+    k[1, 0] = 1.0
+    a = torch.exp(q[:, 0].double())
+    v[0, :] = -0.5
+    v[0, :min(G, D)] = -a[:D].to(torch.bfloat16).float()
+    return q, k.to(torch.bfloat16), v.to(torch.bfloat16)
+
+
+@pytest.mark.parametrize("D,G", [(64, 3), (64, 16), (128, 16), (64, 32), (128, 31), (64, 64), (128, 64)])
+@pytest.mark.parametrize("cut,T", [(False, 1), (True, 1), (False, 2)])
+def test_probabilities_are_not_rounded_to_a_value_s_eight_bits(D, G, cut, T):
+    """A probability meets its value as two bf16 terms: the first at most 2^-8 + 2^-7 of it away, the second rounded, so
+    3 2^-16 off, and the sums of few products 2^-23 each: with ds and an exponential's 2^-19 O is off by bf16's rounding and
+    (2^-13 + 2 ds) sum p |v|."""
+    bsa = bsa_()
+    q, k, v = nearly_cancelling(D, G, G + D)
+    page, keys = 16, T + 1
+    cache = bsa.PagedCache.empty(3, 1, page, D)
+    # key 1 is the last new token's own; with T = 2 the first one does not see it, and one of its values is a NaN
+    kk, vv = torch.zeros((1, 1, keys, D), dtype=torch.bfloat16), torch.zeros((1, 1, keys, D), dtype=torch.bfloat16)
+    kk[0, 0, 0], kk[0, 0, -1], vv[0, 0, 0], vv[0, 0, -1] = k[0], k[1], v[0], v[1]
+    if T == 2:
+        kk[0, 0, 1, 0] = 60.0             # between them one far below (q is negative)
+    cache.k[1, 0, :keys], cache.v[1, 0, :keys] = kk[0, 0].cuda(), vv[0, 0].cuda()
+    if T == 2:
+        cache.v[1, 0, 2, D - 1] = float("nan")
+    table = i32([[1] + [-1] * (255 if cut else 0)])
+    qq = q.view(1, G, 1, D).expand(1, G, T, D).contiguous().cuda()
+    o, _ = bsa.paged_fwd(qq, cache, table, i32([keys]), softmax_scale=1.0)
+    want, _, mass, a = reference(cache, table, kk, vv, qq, [keys], scale=1.0)
+    a = np.minimum(a, 2.0)                # (the key between has no weight: its own error counts for nothing)
+    ds = 2.0 ** -16 * a
+    c = slice(0, D - 1) if T == 2 else slice(0, D)
+    within("o", f64(o)[..., c], want[..., c], (2.0 ** -8 * np.abs(want) + (2.0 ** -13 + 2 * ds[..., None]) * mass)[..., c])
+    if T == 2:
+        assert torch.isnan(o[:, :, 1, D - 1].float()).all() and torch.isfinite(o[:, :, 0].float()).all()
+
+
+@pytest.mark.parametrize("bad", [float("inf"), -float("inf")])
+@pytest.mark.parametrize("D,G", [(64, 4), (128, 4), (128, 20), (64, 40)])
+def test_infinite_values_of_keys_that_all_rows_see(bad, D, G):
+    bsa = bsa_()
+    n = 300
+    cache, table, k, v = paged_batch(bsa, 1, 1, D, 16, [n], 13)
+    for key in (0, 17, 298, 299):
+        p, i = int(table[0, key // 16]), key % 16
+        old = cache.v[p, 0, i, 3].clone()
+        cache.v[p, 0, i, 3] = bad
+        o, lse = bsa.paged_fwd(rows((1, G, 1, D), 14).cuda(), cache, table, i32([n]))
+        assert bool((o[..., 3] == bad).all())
+        rest = torch.cat((o[..., :3], o[..., 4:]), -1)
+        assert torch.isfinite(rest.float()).all() and torch.isfinite(lse).all()
+        cache.v[p, 0, i, 3] = old
