@@ -236,3 +236,149 @@ def test_infinite_values_of_keys_that_all_rows_see(bad, D, G):
         rest = torch.cat((o[..., :3], o[..., 4:]), -1)
         assert torch.isfinite(rest.float()).all() and torch.isfinite(lse).all()
         cache.v[p, 0, i, 3] = old
+
+
+# ------------------------------------------------------------------ joins, walks, warps
+
+def workspace(bsa, cache, q, M, keep=0):
+    """Bytes that the call needs: none where no pair is cut."""
+    import ctypes as C
+    a, (B, Hq, T, D) = bsa._abi, q.shape
+    I3 = C.c_int64 * 3
+    st = I3(Hq * T * D, T * D, D)
+    kv = a.PagedCache(cache.k.data_ptr(), cache.v.data_ptr(), I3(*cache.k.stride()[:3]), I3(*cache.v.stride()[:3]), None, cache.pages,
+                      cache.Hkv, D, cache.page)
+    x = a.PagedFwdArgs(kv, 16, 32, 48, st, st, 64, 80, None, 96 if keep else None, B, Hq, M, T, keep, a.MASK_CAUSAL, -1, 0, float("nan"),
+                       0.0, None, 0, 0, None, 0)
+    n = C.c_size_t(0)
+    assert a.lib().bsa_paged_fwd_workspace(C.byref(x), C.byref(n)) == 0
+    return n.value
+
+
+def sms():
+    return torch.cuda.get_device_properties(0).multi_processor_count
+
+
+@pytest.mark.parametrize("B,H,G,D,T", [
+    (45, 1, 2, 64, 1), (70, 1, 3, 128, 1), (45, 2, 20, 64, 1), (70, 1, 9, 128, 2), (40, 1, 70, 64, 1), (39, 1, 40, 128, 1), (33, 3, 5, 64, 5),
+    (100, 1, 1, 128, 1), (20, 8, 4, 128, 1),
+])
+def test_many_sequences_cut_into_runs(B, H, G, D, T):
+    """More pairs than a quarter of the SMs (a warp joins a row) and more than 32 sequences (a walk over several lanes' worth), some empty."""
+    bsa = bsa_()
+    page, M = 16, 256
+    lens = [0 if b % 7 == 3 else 1 + 97 * b * b % 700 for b in range(B)]
+    q_lens = None if T == 1 else [b % (T + 1) for b in range(B)]
+    cache, table, k, v = paged_batch(bsa, B, H, D, page, lens, 17)
+    table = torch.cat((table, table.new_full((B, M - table.shape[1]), -1)), 1).contiguous()
+    q = rows((B, T, H * G, D), 18).transpose(1, 2).cuda()
+    R = G * T
+    pairs = B * H * -(-R // (16 if R <= 16 else 32 if R <= 32 else 64))
+    assert workspace(bsa, cache, q, M) > 0 and 4 * pairs > sms()
+    check_fwd(bsa, cache, table, k, v, q, lens, q_lens=q_lens)
+    check_fwd(bsa, cache, table, k, v, q, lens, q_lens=q_lens, cap=25.0, sinks=torch.linspace(-1, 1, H).cuda().view(H, 1))
+    assert bsa.get_device_error() == 0
+
+
+@pytest.mark.parametrize("B,H,G,D,T", [(14, 2, 3, 64, 3), (50, 1, 4, 128, 1), (9, 1, 20, 64, 5), (13, 1, 40, 128, 3)])
+def test_many_lists_cut_into_runs(B, H, G, D, T):
+    bsa = bsa_()
+    page, keep = 64, 70
+    lens = [0 if b % 6 == 5 else 1 + 1931 * b % 5000 for b in range(B)]
+    cache, table, k, v = paged_batch(bsa, B, H, D, page, lens, 19, M=90)
+    q = rows((B, H * G, T, D), 20).cuda()
+    assert workspace(bsa, cache, q, 90, keep) > 0 and 4 * B * T * H > sms() and B * T > 32
+    select = want_select(cache, table, q, lens, keep, 1, 1)
+    got = bsa.paged_select(q, cache, table, i32(lens), keep)
+    assert np.array_equal(got.cpu().numpy(), select)
+    check_fwd(bsa, cache, table, k, v, q, lens, select=select)
+    assert bsa.get_device_error() == 0
+
+
+@pytest.mark.parametrize("D", [64, 128])
+@pytest.mark.parametrize("G", [2, 20, 40])
+@pytest.mark.parametrize("cap", [0.0, 25.0])
+def test_more_whole_pairs_than_sms(D, G, cap):
+    """Pairs that go whole to a CTA of four warps."""
+    bsa = bsa_()
+    B = sms() + 9
+    lens = [1 + 37 * b % 130 for b in range(B)]
+    cache, table, k, v = paged_batch(bsa, B, 1, D, 16, lens, 21)
+    q = rows((B, G, 1, D), 22).cuda()
+    assert workspace(bsa, cache, q, table.shape[1]) == 0
+    check_fwd(bsa, cache, table, k, v, q, lens, cap=cap)
+    assert bsa.get_device_error() == 0
+
+
+@pytest.mark.parametrize("bad", [float("nan"), float("inf"), -float("inf")])
+@pytest.mark.parametrize("where", ["k", "v"])
+@pytest.mark.parametrize("D,H,G,T", [(128, 2, 4, 4), (128, 2, 4, 5), (128, 1, 16, 4), (64, 1, 3, 5)])
+def test_what_a_row_does_not_see_does_not_reach_it_in_any_tile(bad, where, D, H, G, T):
+    bsa = bsa_()
+    n = 600
+    for left, key in ((None, n - 2), (None, n - T + 1), (50, n - T - 50), (50, n - T - 48)):
+        cache, table, k, v = paged_batch(bsa, 1, H, D, 16, [n], 13)
+        c = cache.k if where == "k" else cache.v
+        page = table[0, key // 16].long()
+        c[page, :, key % 16, 3] = bad
+        q = rows((1, H * G, T, D), 14).cuda()
+        o, lse = bsa.paged_fwd(q, cache, table, i32([n]), local_left=left)
+        sees = [key <= n - T + t and (left is None or key >= n - T + t - left) for t in range(T)]
+        assert any(sees) and not all(sees)
+        (k if where == "k" else v)[0, :, key, 3] = 1.0
+        c[page, :, key % 16, 3] = 1.0
+        want_o, want_lse = check_fwd(bsa, cache, table, k, v, q, [n], left=left)
+        for t in range(T):
+            if not sees[t]:
+                assert torch.equal(o[:, :, t], want_o[:, :, t]) and torch.equal(lse[:, :, t], want_lse[:, :, t])
+            elif where == "v":
+                x = o[0, :, t, 3].float()
+                assert bool((torch.isnan(x) if bad != bad else x == bad).all())
+                assert torch.isfinite(torch.cat((o[0, :, t, :3], o[0, :, t, 4:]), -1).float()).all() and torch.equal(lse[:, :, t], want_lse[:, :, t])
+            elif bad != bad:
+                assert torch.isnan(lse[0, :, t]).all() and torch.isnan(o[0, :, t].float()).all()
+
+
+@pytest.mark.parametrize("B,M", [(3, 300), (45, 256)])    # joined by a CTA a row, and by a warp
+def test_replayed_with_a_workspace_and_a_join(B, M):
+    """One captured step whose lengths change from replay to replay, two such graphs, other calls between them."""
+    bsa = bsa_()
+    H, G, D, page = 2, 2, 64, 16
+    longest = 900
+    cache, table, k, v = paged_batch(bsa, B, H, D, page, [longest] * B, 23, junk=False)
+    table = torch.cat((table, table.new_full((B, M - table.shape[1]), -1)), 1).contiguous()
+    q = [rows((B, H * G, 1, D), s).cuda() for s in (24, 25)]
+    lens = [i32([1] * B) for _ in range(2)]
+    assert workspace(bsa, cache, q[0], M) > 0
+    graphs, outs = [], []
+    for x, n in zip(q, lens):
+        g = torch.cuda.CUDAGraph()
+        with torch.cuda.graph(g):
+            outs.append(bsa.paged_fwd(x, cache, table, n))
+        graphs.append(g)
+    for step in range(4):
+        now = [[(311 * b + 97 * step + 450 * i) % (longest + 1) for b in range(B)] for i in range(2)]
+        for i in range(2):
+            lens[i].copy_(i32(now[i]))
+        for g in graphs:
+            g.replay()
+        other = bsa.paged_fwd(q[0], cache, table, i32([longest] * B))
+        for i in range(2):
+            want = check_fwd(bsa, cache, table, k, v, q[i], now[i])
+            assert torch.equal(outs[i][0], want[0]) and torch.equal(outs[i][1], want[1])
+        del other
+    assert bsa.get_device_error() == 0
+
+
+def test_paths_in_the_range_checked_build():
+    """The same calls in the build that checks pages, slots and records on the device: right, and nothing found."""
+    if os.environ.get("BSA_LIBRARY_VARIANT") == "debug":
+        pytest.skip("already in it")
+    need_gpu()
+    from block_sparse_attention_process_gb300 import build as b
+    if not os.path.exists(b.LIB_DEBUG):
+        b.build(debug=True)
+    r = subprocess.run([sys.executable, "-m", "pytest", "-x", "-q", "-m", "gpu", os.path.abspath(__file__), "-k",
+                        "window or outside or padding_between or runs or whole or replayed"],
+                       env=dict(os.environ, BSA_LIBRARY_VARIANT="debug"), capture_output=True, text=True, timeout=900, cwd=ROOT)
+    assert r.returncode == 0, r.stdout[-3000:] + r.stderr[-2000:]
