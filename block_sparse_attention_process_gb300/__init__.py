@@ -389,8 +389,8 @@ def _lens(name: str, t: Optional[torch.Tensor], B: int, index: int) -> int:
     return 0 if t is None else _need(name, t, torch.int32, index, (B,))
 
 
-# a workspace for one call, on the stream that the call uses (an allocation by way of a tensor costs three times as much
-# beside a launch)
+# a workspace for one call, on the stream that the call uses (an allocation by way of a tensor, which serves where torch
+# does not offer these, costs three times as much beside a launch)
 _raw_alloc, _raw_free = (getattr(torch._C, "_cuda_cudaCachingAllocator_raw_" + x, None) for x in ("alloc", "delete"))
 
 
@@ -746,12 +746,13 @@ def paged_fwd(q: torch.Tensor, cache: PagedCache, table: torch.Tensor, lens: tor
                 logits_soft_cap or 0.0, sp, sn, skv)
         pack = _abi.PAGED_FWD_REST.pack
         need = _workspace_size("bsa_paged_fwd", (index, B, cache.Hkv, D, cache.page, Hq, M, T, keep, kind, local_left, chunk), lambda: cache._c + pack(*head, 0, 0))
-        ws = _raw_alloc(need, handle) if need else 0
+        own = _raw_alloc(need, handle) if need and _raw_alloc and _raw_free else 0
+        held = _workspace(0 if own else need, dev)
         try:
-            check(_abi.lib().bsa_paged_fwd(cache._c + pack(*head, ws, need), handle), "bsa_paged_fwd")
+            check(_abi.lib().bsa_paged_fwd(cache._c + pack(*head, own or _ptr(held) or 0, need), handle), "bsa_paged_fwd")
         finally:
-            if ws:
-                _raw_free(ws)
+            if own:
+                _raw_free(own)
     return o, lse
 
 

@@ -382,3 +382,17 @@ def test_paths_in_the_range_checked_build():
                         "window or outside or padding_between or runs or whole or replayed"],
                        env=dict(os.environ, BSA_LIBRARY_VARIANT="debug"), capture_output=True, text=True, timeout=900, cwd=ROOT)
     assert r.returncode == 0, r.stdout[-3000:] + r.stderr[-2000:]
+
+
+def test_without_the_allocator_s_own_call(monkeypatch):
+    """Where torch does not offer it, the workspace is a tensor."""
+    bsa = bsa_()
+    lens = [5000, 17]
+    cache, table, _, _ = paged_batch(bsa, 2, 2, 64, 16, lens, 3)
+    q = rows((2, 4, 1, 64), 1).cuda()
+    assert workspace(bsa, cache, q, table.shape[1]) > 0
+    want = bsa.paged_fwd(q, cache, table, i32(lens))
+    monkeypatch.setattr(bsa, "_raw_alloc", None)
+    monkeypatch.setattr(bsa, "_raw_free", None)
+    got = bsa.paged_fwd(q, cache, table, i32(lens))
+    assert torch.equal(got[0], want[0]) and torch.equal(got[1], want[1])
