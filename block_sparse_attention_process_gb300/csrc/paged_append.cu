@@ -8,8 +8,8 @@
 // has every key of the page in registers then: maxima and minima are exact in any order, so the bounds need no
 // atomics, no second pass over the new keys, and come out the same each time.  Where a place among the new tokens' was left out
 // (padding, or a slot elsewhere) the page holds a key there that no register does: its bounds are infinite then.
-// 4 x 8 heads x 8191 tokens: 43.8 us with bounds (pages of 64; 44.5 with pages of 16, 47.9 of 256), 42.6 without: 91 to 93% of a
-// copy's bandwidth.  64 x 8 heads x 1 token: 3.5 and 2.1 us, latency.
+// 4 x 8 heads x 8191 tokens: 44.0 us with bounds (pages of 64; 44.8 with pages of 16, 48.1 of 256), 42.8 without: 90 to 92% of a
+// copy's bandwidth.  64 x 8 heads x 1 token: 3.6 and 2.1 us, latency.
 #include <algorithm>
 
 #include "paged.cuh"

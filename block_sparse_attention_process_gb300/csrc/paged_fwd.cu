@@ -10,7 +10,9 @@
 // keys 309.5 and 309.7 us, 16 ragged sequences 54.3 and 55.2, 64 of 128 to 1024 31.3 and 33.1, 64 rows of 16,384 keys 23.9 and 25.9, 128
 // rows 52.2 and 58.9.
 // The memory bounds it by far (G rows a head: 4 G operations for 4 bytes of a key's channel); at 4 rows a head the
-// products, 8 cycles each of a sub-partition, take a fifth of the time that the keys take to come.
+// products, 8 cycles each of a sub-partition, take a quarter of the time that the keys take to come.  Many rows a head (a prompt's
+// tokens behind a cached prefix) read the keys again for every 64 rows and are bound by the products and the softmax between them:
+// 512 tokens of 32 q heads behind 8192 keys on 8 heads 378 us, 188 TFLOP/s.
 //
 // A unit of loading is 16 keys (K and V), which lie in one page.  They go by 16-byte asynchronous copies, which
 // take any stride between tokens, heads and pages and can bring zeros for keys that no row sees, into a ring of stages that
@@ -23,7 +25,7 @@
 // of pairs that other CTAs share go to the workspace as (m, l, O) records, which a second kernel joins in a fixed order.
 // Where there are pairs enough, a pair goes whole to a CTA instead, and nothing is joined.
 //
-// 64 sequences of 8191 keys on 8 heads, 32 q heads: 312 us, 2.1 GB at 6.9 TB/s, what a copy reaches.  One sequence of 65,536 keys:
+// 64 sequences of 8191 keys on 8 heads, 32 q heads: 309 us, 2.1 GB at 6.9 TB/s, what a copy reaches.  One sequence of 65,536 keys:
 // 47 us (5.7 TB/s); 5 of them until the first keys are there (lengths, table, keys: a chain of loads), 5 the join.
 #include <cmath>
 
@@ -37,16 +39,20 @@ constexpr int kUnit = 16;       // keys of one load
 constexpr int kTileKeys = 64;
 constexpr int kRowTile = 16;
 // Cost of a part beside its tiles', in tiles: lookups, the first keys' way in, the sums' way out.  3, 11 and 15 of them: 16 ragged
-// sequences of up to 8192 keys on 8 heads 56.9, 54.8 and 55.6 us, 20 of them 68.9, 66.5 and 67.6, 4 of 8192 29.2, 28.3 and 27.8;
-// 8 of 16,384 with 128 rows a head 49.8, 50.9 and 51.2.
+// sequences of up to 8192 keys on 8 heads 56.2, 54.8 and 56.5 us, 20 of them 67.6, 66.8 and 67.3, 4 of 8192 28.1, 27.1 and 27.0;
+// 8 of 16,384 with 128 rows a head 57.9, 58.9 and 59.4.
 constexpr int kPartUnits = 11;
 // Pairs that one CTA takes alone (no records, no join), by the longest that one can be, in tiles: up to 8; up to 32 where
 // there are pairs enough (tiles x SMs up to 96 x pairs; with several row tiles pairs for three quarters of the SMs); and
 // lists and windows, whose lengths differ less, of up to 64 where there are pairs for half of the SMs.
-// Sequences of keys on 8 heads, whole and cut (us): 16 of 2048 24.7 and 29.0, 64 of 128 to 1024 31 and 43, 6 of 1024 11.8 and
-// 15.8, 6 of 2048 18.2 and 18.5, 1 of 1024 11.2 and 9.0; on one head of 64 rows 128 of 2048 48.6 and 58.8, 64 of 1024
-// 28.4 and 24.9; 64 pages of 64 for 16 queries, with their selection, 56.7 and 60.3.  (One sequence of 4096 among 15 short
-// ones would take 31 whole and takes 17.)
+// Sequences of keys on 8 heads, whole and cut (us): 16 of 2048 24.5 and 28.7, 64 of 128 to 1024 33.2 and 38.4, 6 of 1024 12.7 and
+// 14.1, 6 of 2048 19.9 and 17.3, 1 of 1024 11.8 and 8.9; on one head of 64 rows 128 of 2048 57.9 and 70.3, 64 of 1024
+// 33.7 and 30.1.  (One sequence of 4096 among 15 short ones would take 34 whole and takes 17.)
+// Lists of 64 pages of 64, with their selection, for 64, 80, 96 and 128 pairs: 44.1 and 39.3, 47.1 and 46.9, 47.5 and 51.3, 56.5 and
+// 60.6; of 40 pages, 80 and 128 pairs, 36.2 and 37.8, 42.3 and 46.6.  Windows of 2500 keys, 64, 80 and 128 pairs: 23.7 and 21.9, 23.8 and
+// 24.8, 28.7 and 32.9; of 4000 34.0 and 28.4, 34.1 and 33.0, 42.4 and 46.6.
+// What a pair can be is known from the table's width, not from the lengths: in a table of 8192 tokens the 16 of 2048 keys take 28.7 us
+// and the 64 short ones 39.9 instead of 35.2, in one of their own width.
 constexpr int kWholeTiles = 8, kManyTiles = 32, kEvenTiles = 64;
 constexpr int kSmWarps = 8;      // warps an SM: a CTA of all of them, or two of four where pairs are whole to a CTA and more than SMs
 constexpr int kWarpRing = 24 * 1024;
@@ -868,8 +874,9 @@ Plan make_plan(const bsa_paged_fwd_args* a) {
   Plan x;
   const int64_t G = a->Hq / a->cache.Hkv;
   x.R = static_cast<int32_t>(a->select ? G : G * a->T);
-  // (16 rows a head as one, two or four tiles 57, 58 and 95 us, 24 rows 26, 22 and 28, 32 rows 20.5, 20.3 and 22, 64 rows 27, 25 and
-  // 23, 128 rows 60, 52 and 50: tiles that share keys read them once, and wait for each other)
+  // (8 sequences of 16,384 keys on one head, as one, two or four tiles: 16 rows 21.1, 22.9 and 31.8 us, 24 rows 27.0, 23.6 and 32.4, 32
+  // rows 27.7, 24.2 and 32.7, 64 rows 40.2, 34.7 and 34.5, 128 rows 64.3, 58.8 and 58.6: tiles that share keys read them once, and
+  // wait for each other)
   x.rt = x.R <= kRowTile ? 1 : x.R <= 2 * kRowTile ? 2 : 4;
   const int64_t rows = kRowTile * x.rt;
   x.row_tiles = (x.R + rows - 1) / rows;
@@ -967,7 +974,7 @@ bsa_status paged_fwd_launch(const bsa_paged_fwd_args* a, float scale, cudaStream
   p.sinks_kv = a->sinks_per_kv_head ? 1 : 0;
   p.n_cta = x.n_cta;
   p.whole = x.whole ? 1 : 0;
-  // (records of a pair: some n_cta / pairs.  One sequence of 65,536 keys by one warp a row 50.9 us, by eight 46.9; 64 of 4096 162 and 172)
+  // (records of a pair: some n_cta / pairs.  One sequence of 65,536 keys by one warp a row 51.1 us, by eight 47.0; 64 of 4096 163 and 171)
   p.join_warps = x.n_cta >= 4 * x.pairs ? kJoinWarps : 1;
   p.rec_stat = static_cast<float*>(a->workspace);
   p.rec_o = p.rec_stat + x.stat_bytes / sizeof(float);

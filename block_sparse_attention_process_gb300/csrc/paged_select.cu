@@ -1,4 +1,4 @@
-// The pages worth attending to, for each query: those with the largest bound on q.k.
+// The pages worth attending to, for each query: those with the largest bound on q.k, q rounded to 8 bits.
 //
 // A page's keys lie between its bounds, so sum_d max(q_d hi_d, q_d lo_d) bounds q.k over the page.  With q+ =
 // max(q, 0) and q- = min(q, 0) that is q+ hi + q- lo: one matrix product of length 2 D, [q+ | q-] [hi | lo]^T.

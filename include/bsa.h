@@ -519,7 +519,12 @@ typedef struct {
  * tokens, keeps its length and sets the bounds bit (2) of the device error
  * word, and so does a page number outside the cache (it is moved like the
  * others; its tokens' slots are -1).  If `used` is outside 0..pages or less
- * than the pages given back, nothing changes and the bit is set. */
+ * than the pages given back, nothing changes and the bit is set.
+ *
+ * References are not counted: a page that rows share (bsa_paged_fwd allows it) is
+ * given back by every row that drops it, and would be handed out as often.  Of rows that
+ * share their first pages all but the last shrink to those pages' tokens only, and the
+ * program sets their lens to 0 itself. */
 BSA_API bsa_status bsa_paged_resize(const bsa_paged_resize_args* args, bsa_stream stream);
 
 typedef struct {
@@ -564,7 +569,8 @@ typedef struct {
 } bsa_paged_select_args;
 
 /* For every query (new token and key head, its group of q heads together; scores with a positive scale) the
- * `keep` pages it sees with the largest bound on q.k, in increasing order, -1
+ * `keep` pages it sees with the largest bound on qc.k (q rounded to whole numbers of 8
+ * bits; q.k itself can be above it by what rounding takes), in increasing order, -1
  * behind the last one if it sees fewer.  With qc = round_half_even(q / 2^f), f =
  * max(floor(log2 max|q|) - 6, -100) over the group (qc = 0 where max|q| is not
  * below 2^100 or is NaN), a page's score is the largest over the group's heads of sum_d
