@@ -639,9 +639,9 @@ def paged_resize(table: torch.Tensor, free: torch.Tensor, used: torch.Tensor, le
                  page: int, T: int, *, stream=None):
     """bsa_paged_resize: sequences of ``lens`` tokens get ``new_lens`` (int32 [B], 0 for one that has ended); pages go back
     to the free stack and from it into the rows of ``table`` (int32 [B, M]) and ``free`` (int32 [pages], entries used[0] ..
-    are free), both in place; a page that rows share is given back by each of them (nothing counts references).  -> (lens int32 [B] that they now have, used int32 [1], slots int32 [B, T]: where the tokens
-    lens[b] + i go, -1 behind the last).  Where the pages do not suffice a sequence, and every later one that needs
-    any, keeps its length."""
+    are free), both in place; a page that rows share is given back by each of them (nothing counts references).  -> (lens
+    int32 [B] that they now have, used int32 [1], slots int32 [B, T]: where the tokens lens[b] + i go, -1 behind the last).
+    Where the pages do not suffice a sequence, and every later one that needs any, keeps its length."""
     index = table.get_device()
     if index < 0:
         raise ValueError("table must be a contiguous CUDA int32 tensor")
@@ -678,9 +678,9 @@ def paged_append(cache: PagedCache, k: torch.Tensor, v: torch.Tensor, slots: tor
 
 def paged_select(q: torch.Tensor, cache: PagedCache, table: torch.Tensor, lens: torch.Tensor, keep: int, *, first: int = 1,
                  recent: int = 1, q_lens: Optional[torch.Tensor] = None, stream=None) -> torch.Tensor:
-    """bsa_paged_select: for every new token and key head the ``keep`` pages with the largest bound on q.k (q rounded to 8
-    bits), the ``first`` and the last ``recent`` ones that it sees among them.  q bf16 [B,Hq,T,D] (any strides with a contiguous last axis),
-    lens int32 [B] with the new tokens' own keys included -> int32 [B,Hkv,T,keep], numbers of the
+    """bsa_paged_select: for every new token and key head the ``keep`` pages with the largest bound on q.k (q rounded to
+    8 bits), the ``first`` and the last ``recent`` ones that it sees among them.  q bf16 [B,Hq,T,D] (any strides with a
+    contiguous last axis), lens int32 [B] with the new tokens' own keys included -> int32 [B,Hkv,T,keep], numbers of the
     sequence's pages in increasing order, -1 behind the last; for ``paged_fwd``'s ``select``."""
     dev, index = cache.device, cache.index
     qs = _rows("q", q, index)

@@ -389,7 +389,7 @@ __device__ __forceinline__ uint32_t odd_keys(uint32_t v, int lane) {
 }
 
 // Probabilities a and b as sums of two bf16 numbers, the operands of two products: the first is a (1 - 2^-8) cut to 8 bits, the second the
-// rest, rounded, so 2^-14 of a are lost.  Neither is 0 where a is not (an infinite value stays one).
+// rest, rounded, so 2^-14 of a are lost.  Neither is 0 where a is above 2^-125 (an infinite value stays one).
 __device__ __forceinline__ void two_terms(float a, float b, uint32_t& first, uint32_t& rest) {
   const uint32_t x = __float_as_uint(a * (1.f - 0x1p-8f)), y = __float_as_uint(b * (1.f - 0x1p-8f));
   first = __byte_perm(x, y, 0x7632);
